@@ -345,10 +345,138 @@ tg_status tg_attention_fwd(const void* Q, const void* K, const void* V, void* O,
  */
 tg_status tg_softmax_rows(const void* X, void* Y, int64_t M, int64_t N, tg_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions, and a paged key/value cache held in 8 bits: writing it,
+ * reading it back, and attention over it.
+ *
+ * 16-bit tensors of (tokens, heads, dim) are TG_FP16 or TG_BF16, dim
+ * contiguous, token and head strides in elements (so slices of one packed
+ * projection output need no copy). DEVICE pointers throughout.
+ *
+ * The cache. A page holds `page` consecutive tokens of one sequence (16, 32,
+ * 64 or 128), for every kv head:
+ *
+ *   k_cache, v_cache   pages x kv_heads x page x dim codes of one byte,
+ *                      16-byte aligned; dim 64 or 128
+ *   k_scale, v_scale   pages x kv_heads fp32
+ *
+ * A code q of page p, head h stands for value(q) * scale[p][h], value() being
+ * e4m3 (TG_KV_E4M3, largest 448) or two's complement (TG_KV_INT8, -127..127).
+ *
+ * The batch. Sequence i's pages are table[i * table_width + 0, 1, ..], in
+ * order. Packed tensors hold the sequences' new tokens one after another,
+ * sequence i's in rows cu[i] .. cu[i + 1] - 1 (batch + 1 int32 offsets; with
+ * cu NULL every sequence has one row); no sequence has more than max_new.
+ * No page is shared by sequences that are written in one call.
+ *
+ * These arrays live on the device, so the kernels check them: an offset,
+ * length or page number out of range is not followed, the sequence (append),
+ * the row (read) or the page's keys (attention) are left out, and the next
+ * tg_device_status answers TG_ERR_BOUNDS. Table entries past a sequence's last
+ * page are never read.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { TG_FP16 = 0, TG_BF16 = 1 } tg_dtype;
+typedef enum { TG_KV_E4M3 = 0, TG_KV_INT8 = 1 } tg_kv_format;
+typedef enum {
+    TG_ROPE_HALF = 0,        /* pairs (j, j + rotary / 2) */
+    TG_ROPE_INTERLEAVED = 1  /* pairs (2 j, 2 j + 1) */
+} tg_rope_layout;
+
+/*
+ * Rotary positions: the first `rotary` values (even, at most dim) of every
+ * head, in pairs (a, b) by `layout`, are turned by t = positions[token] *
+ * inv_freq[pair],
+ *
+ *     y_a = amplitude (x_a cos t - x_b sin t),  y_b = amplitude (x_b cos t + x_a sin t),
+ *
+ * the others are copied. inv_freq: rotary / 2 float64 radians per position (a
+ * scaling for long contexts is a choice of these and of amplitude). backward =
+ * 1 applies the transposed map: with dY for X it gives dX. Angles are exact to
+ * 2^-31 of a half turn for every int32 position; products are fp32, rounded once. Y
+ * may be X itself (same strides) but must not otherwise overlap it.
+ * Stream-ordered; allocates nothing.
+ */
+tg_status tg_rope(const void* X, int64_t x_token_stride, int64_t x_head_stride, void* Y, int64_t y_token_stride,
+                  int64_t y_head_stride, const int32_t* positions, int64_t tokens, int64_t heads, int64_t dim,
+                  const double* inv_freq, int64_t rotary, double amplitude, int layout, int backward, int dtype,
+                  tg_stream_t stream);
+
+/*
+ * Writes new keys and values (total rows of kv_heads x dim) into the cache at
+ * positions lens[i], lens[i] + 1, .. of their sequences (lens: tokens held
+ * before the call; the caller adds the new ones afterwards), quantised on the
+ * way. For each page and head that is written to, in fp32:
+ *
+ *     s     = max(s of the page's held tokens, max |new| * (1 / qmax), 2^-60)
+ *     held  = round(held * (s_old * (1 / s)))                               where s grew
+ *     new   = round(x * (1 / s))                                            to nearest, ties to even
+ *
+ * max |new| is over the finite values; infinities become the largest of them,
+ * a NaN stays one in e4m3 and becomes 0 in int8. A page whose first token is
+ * written takes over nothing of what it held. With rotary > 0 the keys are
+ * rotated first, in fp32 and not rounded between, by their position (see
+ * tg_rope), and with heads > 0 the queries Q too, into Q_out (Q itself, with
+ * the same strides, is allowed). Results do not depend on timing.
+ * Stream-ordered; allocates nothing.
+ */
+tg_status tg_kv_append(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int64_t pages, int64_t kv_heads,
+                       int64_t page, int64_t dim, int format, const void* K, int64_t k_token_stride,
+                       int64_t k_head_stride, const void* V, int64_t v_token_stride, int64_t v_head_stride,
+                       const int32_t* table, int64_t table_width, const int32_t* lens, const int32_t* cu,
+                       int64_t batch, int64_t total, int64_t max_new, const double* inv_freq, int64_t rotary,
+                       double amplitude, int layout, const void* Q, int64_t q_token_stride, int64_t q_head_stride,
+                       void* Q_out, int64_t qo_token_stride, int64_t qo_head_stride, int64_t heads, int dtype,
+                       tg_stream_t stream);
+
+/*
+ * Reads positions first[i] .. first[i] + (cu[i + 1] - cu[i]) - 1 of every
+ * sequence back into K and V (total x kv_heads x dim, contiguous, 16-byte
+ * aligned): code * scale in fp32, rounded once. Stream-ordered; allocates
+ * nothing.
+ */
+tg_status tg_kv_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                     int64_t pages, int64_t kv_heads, int64_t page, int64_t dim, int format, const int32_t* table,
+                     int64_t table_width, const int32_t* first, const int32_t* cu, int64_t batch, int64_t total,
+                     void* K, void* V, int dtype, tg_stream_t stream);
+
+/*
+ * Attention over the cache: for every new token and query head h, with kv head
+ * g = h / (heads / kv_heads),
+ *
+ *     o = sum_j p_j v_j,  p = softmax over the visible j of (scale * q . k_j).
+ *
+ * lens[i] is sequence i's length with its new tokens, which are its last ones:
+ * row r of the n new ones is at position lens[i] - n + r. causal 1: it sees
+ * positions up to its own, with window > 0 only the last `window` of them;
+ * causal 0: all lens[i]. A row that sees nothing (lens[i] 0, say) gives zeros.
+ * lse (NULL, or total x heads fp32) receives the natural log of the sum of
+ * exp(scale * q . k_j), -inf for such a row. max_len bounds lens (longer
+ * sequences are reported and give zeros).
+ *
+ * Scores, softmax and sums are fp32, codes enter the products exactly, O
+ * (total x heads x dim, contiguous, 16-byte aligned) is rounded once. Results
+ * are bit-identical from run to run. The caller gives `workspace` (16-byte
+ * aligned) of at least the bytes that tg_attention_kv_workspace answers for
+ * the same sizes; its contents need not be kept between calls. Stream-ordered;
+ * allocates nothing, so it can be captured into a graph.
+ */
+tg_status tg_attention_kv_workspace(int64_t kv_heads, int64_t page, int64_t dim, int format, int64_t heads,
+                                    int64_t batch, int64_t total, int64_t max_new, int64_t max_len, int64_t window,
+                                    int dtype, int64_t* bytes);
+tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int64_t q_head_stride, void* O, float* lse,
+                          const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                          int64_t pages, int64_t kv_heads, int64_t page, int64_t dim, int format,
+                          const int32_t* table, int64_t table_width, const int32_t* lens, const int32_t* cu,
+                          int64_t batch, int64_t total, int64_t heads, int64_t max_new, int64_t max_len, int causal,
+                          int64_t window, double scale, int dtype, void* workspace, int64_t workspace_bytes,
+                          tg_stream_t stream);
+
 /*
  * Synchronises `stream`, then reports (and clears) the device-side status word
  * that kernels set when one of their bounded waits expires: TG_OK or
- * TG_ERR_TIMEOUT (or, in debug builds, TG_ERR_BOUNDS for a failed bounds check). `*where` (if not NULL) receives the code of the wait that
+ * TG_ERR_TIMEOUT (or TG_ERR_BOUNDS: a cache call's device arrays were out of
+ * range, or in debug builds a bounds check failed). `*where` (if not NULL) receives the code of the wait that
  * expired first (0 if none). Every wait inside the kernels gives up after the
  * watchdog limit (tg_set_watchdog_ns) instead of spinning forever; the kernel
  * then drains its in-flight copies, frees its tensor memory and exits, leaving

@@ -14,6 +14,7 @@ CPU path: if the library has not been built, importing this package raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -25,12 +26,16 @@ NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024  # TG_NOALLOC_SCRATCH_BYTES
 KERNEL_AUTO, KERNEL_TILED_TMA, KERNEL_TILED_LSU, KERNEL_SPLITK, KERNEL_TILED_PAIR = 0, 1, 2, 3, 4
 W4_INT4, W4_FP4_E2M1 = 0, 1
 W4_KERNEL_AUTO, W4_KERNEL_TMEM, W4_KERNEL_REG = 0, 1, 2
+FP16, BF16 = 0, 1
+KV_E4M3, KV_INT8 = 0, 1
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED_DEVICE, ERR_CUDA, ERR_TIMEOUT, ERR_NO_MEMORY, ERR_BOUNDS = range(7)
 
 # every symbol include/tg_gemm.h declares
 EXPORTS = ("tg_gemm", "tg_gemm_ex", "tg_gemm_plan", "tg_gemm_staged", "tg_gemm_splitk_noalloc", "tg_gemm_w4", "tg_gemm_w4_ex",
            "tg_gemm_w4_kernel", "tg_attention_fwd",
            "tg_softmax_rows", "tg_bias_gelu",
+           "tg_rope", "tg_kv_append", "tg_kv_read", "tg_attention_kv_workspace", "tg_attention_kv",
            "tg_device_status", "tg_debug_status",
            "tg_set_watchdog_ns",
            "tg_debug_skip_first_arrive", "tg_debug_bounds_limit", "tg_debug_build", "tg_status_string",
@@ -42,6 +47,7 @@ if not os.path.exists(LIB_PATH):
                       "(or python tiled_tensor_core_tcgen05_gb300/build.py); there is no fallback path")
 
 _vp, _i64, _int, _u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64
+_dbl = ctypes.c_double
 
 
 def bind(path: str) -> ctypes.CDLL:
@@ -60,6 +66,16 @@ def bind(path: str) -> ctypes.CDLL:
     lib.tg_attention_fwd.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp]
     lib.tg_softmax_rows.argtypes = [_vp, _vp, _i64, _i64, _vp]
     lib.tg_bias_gelu.argtypes = [_vp, _vp, _i64, _i64, _int, _vp]
+    cache = [_vp] * 4 + [_i64] * 4 + [_int]   # codes, scales, pages, kv_heads, page, dim, format
+    strided = [_vp, _i64, _i64]               # pointer, token stride, head stride
+    batch = [_vp, _i64, _vp, _vp, _i64, _i64]  # table, its width, lens, cu, batch, total
+    lib.tg_rope.argtypes = strided + strided + [_vp, _i64, _i64, _i64, _vp, _i64, _dbl, _int, _int, _int, _vp]
+    lib.tg_kv_append.argtypes = (cache + strided + strided + batch + [_i64, _vp, _i64, _dbl, _int] + strided + strided
+                                 + [_i64, _int, _vp])
+    lib.tg_kv_read.argtypes = cache + batch + [_vp, _vp, _int, _vp]
+    lib.tg_attention_kv_workspace.argtypes = [_i64, _i64, _i64, _int] + [_i64] * 6 + [_int, ctypes.POINTER(_i64)]
+    lib.tg_attention_kv.argtypes = (strided + [_vp, _vp] + cache + batch + [_i64, _i64, _i64, _int, _i64, _dbl, _int,
+                                                                            _vp, _i64, _vp])
     lib.tg_device_status.argtypes = [_vp, ctypes.POINTER(_int)]
     lib.tg_debug_status.argtypes = [_vp]
     lib.tg_set_watchdog_ns.argtypes = [_u64]
@@ -76,7 +92,8 @@ def bind(path: str) -> ctypes.CDLL:
     lib.tg_shutdown.argtypes = []
     lib.tg_shutdown.restype = None
     for name in ("tg_gemm", "tg_gemm_ex", "tg_gemm_plan", "tg_gemm_staged", "tg_gemm_splitk_noalloc", "tg_gemm_w4", "tg_gemm_w4_ex",
-                 "tg_gemm_w4_kernel", "tg_attention_fwd", "tg_softmax_rows", "tg_bias_gelu", "tg_device_status", "tg_debug_status",
+                 "tg_gemm_w4_kernel", "tg_attention_fwd", "tg_softmax_rows", "tg_bias_gelu", "tg_rope", "tg_kv_append", "tg_kv_read", "tg_attention_kv_workspace",
+                 "tg_attention_kv", "tg_device_status", "tg_debug_status",
                  "tg_set_watchdog_ns", "tg_debug_skip_first_arrive", "tg_debug_bounds_limit", "tg_debug_build",
                  "tg_version"):
         getattr(lib, name).restype = _int
@@ -201,6 +218,37 @@ def bias_gelu_(C, bias=None, gelu: bool = True, stream=None):
     return C
 
 
+def tg_rope(X: int, x_token_stride: int, x_head_stride: int, Y: int, y_token_stride: int, y_head_stride: int,
+            positions: int, tokens: int, heads: int, dim: int, inv_freq: int | None, rotary: int, amplitude: float,
+            layout: int, backward: bool, dtype: int, stream: int | None) -> None:
+    _check(_lib.tg_rope(X, x_token_stride, x_head_stride, Y, y_token_stride, y_head_stride, positions, tokens, heads,
+                        dim, inv_freq, rotary, amplitude, layout, int(backward), dtype, stream))
+
+
+def tg_kv_append(*args) -> None:
+    """The C entry point's arguments in its order (include/tg_gemm.h)."""
+    _check(_lib.tg_kv_append(*args))
+
+
+def tg_kv_read(*args) -> None:
+    """The C entry point's arguments in its order (include/tg_gemm.h)."""
+    _check(_lib.tg_kv_read(*args))
+
+
+def tg_attention_kv_workspace(kv_heads: int, page: int, dim: int, fmt: int, heads: int, batch: int, total: int,
+                              max_new: int, max_len: int, window: int, dtype: int) -> int:
+    """Bytes of workspace that tg_attention_kv needs for these sizes."""
+    n = _i64()
+    _check(_lib.tg_attention_kv_workspace(kv_heads, page, dim, fmt, heads, batch, total, max_new, max_len, window,
+                                          dtype, ctypes.byref(n)))
+    return n.value
+
+
+def tg_attention_kv(*args) -> None:
+    """The C entry point's arguments in its order (include/tg_gemm.h)."""
+    _check(_lib.tg_attention_kv(*args))
+
+
 def tg_device_status(stream: int | None) -> tuple[int, int]:
     where = _int(0)
     st = _lib.tg_device_status(stream, ctypes.byref(where))
@@ -257,6 +305,17 @@ def _stream_handle(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _on(stream):
+    """The torch context in which tensors are allocated for work on ``stream``."""
+    if stream is None:
+        return _NO_CONTEXT
+    import torch
+    return torch.cuda.stream(stream)
 
 
 def _dev_fp16(t, name):
@@ -346,3 +405,255 @@ def ring_bytes(block_M: int, block_N: int, block_K: int, num_stages: int, elem_b
     ("TileLang: you write the dataflow, the compiler owns the schedule",
     section "What a tile costs, exactly")."""
     return num_stages * (block_M * block_K + block_K * block_N) * elem_bytes
+
+
+# ---------------------------------------------------------------- rotary positions and the 8-bit cache
+
+def _dtype_code(dtype, name):
+    import torch
+    if dtype is torch.float16:
+        return FP16
+    if dtype is torch.bfloat16:
+        return BF16
+    raise TypeError(f"{name} must be float16 or bfloat16, got {dtype}")
+
+
+def _rows(t, name, dtype=None):
+    """(pointer, token stride, head stride) of a (tokens, heads, dim) CUDA tensor with contiguous dim."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have shape (tokens, heads, dim), got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    token, head, unit = t.stride()
+    if unit != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    return t.data_ptr(), token, head
+
+
+def _ints(t, name, shape):
+    import torch
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be int32, got {t.dtype}")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _frequencies(inv_freq):
+    import torch
+    if inv_freq.dtype is not torch.float64 or not inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous CUDA float64 vector (radians per position of each pair)")
+    return inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+
+
+def rope_frequencies(rotary: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     trained: int = 4096, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """(inv_freq, amplitude) for ``rope`` and ``kv_append``: base ** (-2 j / rotary) radians per
+    position for pair j, in float64, scaled for contexts beyond the ``trained`` length:
+
+    "none"    as they are;
+    "linear"  every frequency divided by ``factor`` (positions interpolated);
+    "ntk"     the base raised to base * factor ** (rotary / (rotary - 2)), which divides the
+              slowest frequency by ``factor`` and leaves the fastest;
+    "yarn"    pairs that turn more than ``fast`` times within ``trained`` positions kept, those
+              that turn less than ``slow`` times divided by ``factor``, a linear ramp over the
+              pair index between, and the amplitude 0.1 ln(factor) + 1.
+    """
+    import math
+
+    import torch
+    if rotary < 2 or rotary % 2:
+        raise ValueError(f"rotary must be even and at least 2, got {rotary}")
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError(f"scaling must be none, linear, ntk or yarn, got {scaling!r}")
+    if not factor >= 1.0 or not base > 1.0 or trained < 1:
+        raise ValueError("factor must be at least 1, base above 1 and trained at least 1")
+    if scaling == "ntk":
+        if rotary < 4:
+            raise ValueError("ntk scaling needs rotary of at least 4")
+        base = base * factor ** (rotary / (rotary - 2))
+    freq = base ** (-torch.arange(0, rotary, 2, dtype=torch.float64) / rotary)
+    amplitude = 1.0
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "yarn":
+        def pair(turns):  # the pair that turns so often within the trained length
+            return rotary * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))
+        low, high = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rotary - 1)
+        keep = 1 - ((torch.arange(rotary // 2, dtype=torch.float64) - low) / max(high - low, 0.001)).clamp(0, 1)
+        freq = freq * keep + freq / factor * (1 - keep)
+        amplitude = 0.1 * math.log(factor) + 1.0
+    return freq.to(device), amplitude
+
+
+def rope(X, positions, inv_freq, amplitude: float = 1.0, layout: int = ROPE_HALF, backward: bool = False, out=None,
+         stream=None):
+    """Rotary positions on X (tokens, heads, dim), float16 or bfloat16: the first 2 * len(inv_freq)
+    values of each head turned in pairs by positions[token] * inv_freq[pair] and multiplied by
+    ``amplitude``, the others copied. ``positions`` int32, ``inv_freq`` float64 (see
+    ``rope_frequencies``). ``backward``: the transposed map, which takes the output's gradient to
+    the input's. ``out`` may be X. X and out may be slices (contiguous in dim)."""
+    import torch
+    x, xt, xh = _rows(X, "X")
+    dtype = _dtype_code(X.dtype, "X")
+    T, H, D = X.shape
+    freq, rotary = _frequencies(inv_freq)
+    pos = _ints(positions, "positions", (T,))
+    if out is None:
+        with _on(stream):
+            out = torch.empty((T, H, D), dtype=X.dtype, device=X.device)
+    elif out.shape != X.shape:
+        raise ValueError("out has the wrong shape")
+    y, yt, yh = _rows(out, "out", X.dtype)
+    tg_rope(x, xt, xh, y, yt, yh, pos, T, H, D, freq, rotary, amplitude, layout, backward, dtype,
+            _stream_handle(stream))
+    return out
+
+
+class KvCache:
+    """A paged key/value cache held in 8 bits: codes k, v (pages, kv_heads, page, dim), float8_e4m3fn
+    or int8, and one float32 scale for each (page, kv_head) in k_scale, v_scale (pages, kv_heads).
+    Pages hold 16, 32, 64 or 128 tokens; dim is 64 or 128. ``KvCache.empty`` allocates one."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "page", "dim", "fmt", "args")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        if k.dtype is torch.float8_e4m3fn:
+            self.fmt = KV_E4M3
+        elif k.dtype is torch.int8:
+            self.fmt = KV_INT8
+        else:
+            raise TypeError(f"codes must be float8_e4m3fn or int8, got {k.dtype}")
+        if k.dim() != 4 or k.shape != v.shape or k.dtype is not v.dtype:
+            raise ValueError("k and v must share one (pages, kv_heads, page, dim) shape and one type")
+        self.pages, self.kv_heads, self.page, self.dim = k.shape
+        if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
+            raise TypeError("scales must be float32")
+        if k_scale.shape != (self.pages, self.kv_heads) or v_scale.shape != (self.pages, self.kv_heads):
+            raise ValueError(f"scales must have shape ({self.pages}, {self.kv_heads})")
+        for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            if not t.is_cuda:
+                raise TypeError(f"{name} must be a CUDA tensor")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.args = (k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.pages, self.kv_heads,
+                     self.page, self.dim, self.fmt)
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, page: int = 64, dim: int = 128, dtype=None, device="cuda"):
+        import torch
+        dtype = torch.float8_e4m3fn if dtype is None else dtype
+        k, v = (torch.zeros((pages, kv_heads, page, dim), dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
+        return cls(k, v, *(torch.zeros((pages, kv_heads), device=device) for _ in range(2)))
+
+
+def _batch(table, lens, cu, total):
+    """The C calls' batch arguments: table, its width, lens, cu, batch, total."""
+    if table.dim() != 2:
+        raise ValueError(f"table must have shape (batch, pages a sequence), got {tuple(table.shape)}")
+    B, width = table.shape
+    return (_ints(table, "table", (B, width)), width, _ints(lens, "lens", (B,)),
+            _ints(cu, "cu", (B + 1,)) if cu is not None else None, B, total)
+
+
+def kv_append(cache, K, V, table, lens, cu=None, max_new: int = 1, Q=None, inv_freq=None, amplitude: float = 1.0,
+              layout: int = ROPE_HALF, out=None, stream=None):
+    """Writes new keys and values K, V (total, kv_heads, dim), float16 or bfloat16, into ``cache``,
+    quantised on the way: sequence i's rows cu[i] .. cu[i + 1] - 1 (cu None: one row a sequence) go to
+    positions lens[i] .. of the pages in its row of ``table``. lens: int32 tokens held before the call;
+    max_new: no sequence has more rows. With ``inv_freq`` the keys are rotated first by their
+    positions (see ``rope``), and the queries Q (total, heads, dim), if given, too: returns them
+    (``out``, which may be Q), else None. The scales and roundings are in include/tg_gemm.h."""
+    import torch
+    k, kt, kh = _rows(K, "K")
+    v, vt, vh = _rows(V, "V", K.dtype)
+    dtype = _dtype_code(K.dtype, "K")
+    T = K.shape[0]
+    if K.shape != V.shape or K.shape[1] != cache.kv_heads or K.shape[2] != cache.dim:
+        raise ValueError(f"K and V must have shape (total, {cache.kv_heads}, {cache.dim}), got {tuple(K.shape)} "
+                         f"and {tuple(V.shape)}")
+    freq, rotary = _frequencies(inv_freq) if inv_freq is not None else (None, 0)
+    q = qo = (None, 0, 0)
+    heads = 0
+    if Q is not None:
+        if inv_freq is None:
+            raise ValueError("Q is only rotated: it needs inv_freq")
+        q, heads = _rows(Q, "Q", K.dtype), Q.shape[1]
+        if Q.shape[0] != T or Q.shape[2] != cache.dim:
+            raise ValueError(f"Q must have shape ({T}, heads, {cache.dim}), got {tuple(Q.shape)}")
+        if out is None:
+            with _on(stream):
+                out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+        elif out.shape != Q.shape:
+            raise ValueError("out has the wrong shape")
+        qo = _rows(out, "out", Q.dtype)
+    elif out is not None:
+        raise ValueError("out is for the rotated Q")
+    _check(_lib.tg_kv_append(*cache.args, k, kt, kh, v, vt, vh, *_batch(table, lens, cu, T), max_new, freq, rotary,
+                             amplitude, layout, *q, *qo, heads, dtype, _stream_handle(stream)))
+    return out
+
+
+def kv_read(cache, table, first, cu, total: int, dtype=None, out=None, stream=None):
+    """(K, V), each (total, kv_heads, dim), of positions first[i] .. first[i] + (cu[i + 1] - cu[i]) - 1 of
+    every sequence, packed at rows cu[i] .. (cu None: one row a sequence): code * scale, rounded once
+    to ``dtype`` (float16, the default, or bfloat16). ``out``: a pair of contiguous tensors."""
+    import torch
+    shape = (total, cache.kv_heads, cache.dim)
+    if out is None:
+        dtype = torch.float16 if dtype is None else dtype
+        with _on(stream):
+            K, V = (torch.empty(shape, dtype=dtype, device=cache.k.device) for _ in range(2))
+    else:
+        K, V = out
+        if tuple(K.shape) != shape or tuple(V.shape) != shape:
+            raise ValueError(f"out must be two tensors of shape {shape}")
+        if not (K.is_cuda and V.is_cuda and K.is_contiguous() and V.is_contiguous()):
+            raise ValueError("out must be contiguous CUDA tensors")
+        if K.dtype is not V.dtype or (dtype is not None and K.dtype is not dtype):
+            raise TypeError("out has the wrong type")
+    _check(_lib.tg_kv_read(*cache.args, *_batch(table, first, cu, total), K.data_ptr(), V.data_ptr(),
+                           _dtype_code(K.dtype, "dtype"), _stream_handle(stream)))
+    return K, V
+
+
+def attention_kv(Q, cache, table, lens, cu=None, max_new: int = 1, max_len: int | None = None, causal: bool = True,
+                 window: int = 0, scale: float | None = None, return_lse: bool = False, out=None, stream=None):
+    """Attention of the new tokens' queries Q (total, heads, dim), float16 or bfloat16, over ``cache``;
+    heads is a multiple of the cache's kv_heads. lens: int32 lengths with the new tokens, which are
+    each sequence's last. ``causal``: a token sees positions up to its own, with ``window`` only the
+    last so many. max_new and max_len bound the rows and the length of a sequence (max_len None: what
+    the table can hold). scale None: 1 / sqrt(dim). Rows that see nothing give zeros. Returns O (total,
+    heads, dim), with ``return_lse`` also the float32 log of each row's sum (total, heads)."""
+    import torch
+    q, qt, qh = _rows(Q, "Q")
+    dtype = _dtype_code(Q.dtype, "Q")
+    T, H, D = Q.shape
+    if D != cache.dim:
+        raise ValueError(f"Q must have shape (total, heads, {cache.dim}), got {tuple(Q.shape)}")
+    batch = _batch(table, lens, cu, T)
+    if max_len is None:
+        max_len = batch[1] * cache.page
+    handle = _stream_handle(stream)
+    need = _i64()
+    _check(_lib.tg_attention_kv_workspace(cache.kv_heads, cache.page, D, cache.fmt, H, batch[4], T, max_new, max_len,
+                                          window, dtype, ctypes.byref(need)))
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, H, D), dtype=Q.dtype, device=Q.device)
+        elif out.shape != Q.shape or out.dtype is not Q.dtype or not out.is_cuda or not out.is_contiguous():
+            raise ValueError("out must be a contiguous CUDA tensor of Q's shape and type")
+        lse = torch.empty((T, H), dtype=torch.float32, device=Q.device) if return_lse else None
+        work = torch.empty(need.value, dtype=torch.uint8, device=Q.device) if need.value else None
+    _check(_lib.tg_attention_kv(q, qt, qh, out.data_ptr(), lse.data_ptr() if return_lse else None, *cache.args, *batch,
+                                H, max_new, max_len, int(causal), window, scale if scale is not None else D ** -0.5,
+                                dtype, work.data_ptr() if work is not None else None, need.value, handle))
+    return (out, lse) if return_lse else out

@@ -935,6 +935,8 @@ tg_status tg_device_status(tg_stream_t stream_, int* where) {
     cudaDeviceSynchronize();
     if (where) *where = v;
     if (v == kSiteBounds) return fail(TG_ERR_BOUNDS, "a device-side bounds check failed (debug build)");
+    if (v == kSiteRange)
+        return fail(TG_ERR_BOUNDS, "a length, an offset or a page number of a cache call was out of range");
     return fail(TG_ERR_TIMEOUT, "a kernel wait expired (site %d)", v);
 }
 
@@ -1315,4 +1317,338 @@ extern "C" tg_status tg_softmax_rows(const void* X, void* Y, int64_t M, int64_t 
     cudaError_t e = launch_softmax(static_cast<const __half*>(X), static_cast<__half*>(Y), (int)M, (int)N, vec,
                                    g_dev[dev].sm_count, stream);
     return e == cudaSuccess ? TG_OK : cuda_fail(e, "softmax kernel launch");
+}
+
+// ---------------------------------------------------------------------------
+// Rotary positions and the paged 8-bit cache.
+
+namespace {
+
+constexpr int64_t kIntMax = 0x7FFFFFFFll;
+
+// Bytes from the first to past the last element of a strided (tokens, heads, dim) 16-bit tensor.
+int64_t span_bytes(int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride, int64_t head_stride) {
+    if (tokens <= 0 || heads <= 0 || dim <= 0) return 0;
+    return ((tokens - 1) * token_stride + (heads - 1) * head_stride + dim) * 2;
+}
+
+tg_status check_dtype(int dtype) {
+    if (dtype != TG_FP16 && dtype != TG_BF16)
+        return fail(TG_ERR_INVALID_ARG, "dtype must be TG_FP16 (0) or TG_BF16 (1), got %d", dtype);
+    return TG_OK;
+}
+
+// Strides of up to 2^30 elements keep every offset of 2^31 tokens inside 64 bits.
+tg_status check_strides(const char* name, int64_t token_stride, int64_t head_stride) {
+    const int64_t most = 1ll << 30;
+    if (token_stride < 0 || head_stride < 0 || token_stride > most || head_stride > most)
+        return fail(TG_ERR_INVALID_ARG, "strides of %s must be in [0, 2^30], got %lld and %lld", name,
+                    (long long)token_stride, (long long)head_stride);
+    return TG_OK;
+}
+
+// The rows of an output must not overlap each other: either tokens outside heads or heads outside tokens.
+bool rows_overlap(int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride, int64_t head_stride) {
+    const bool token_outer = (heads <= 1 || head_stride >= dim) && (tokens <= 1 || token_stride >= (heads - 1) * head_stride + dim);
+    const bool head_outer = (tokens <= 1 || token_stride >= dim) && (heads <= 1 || head_stride >= (tokens - 1) * token_stride + dim);
+    return !token_outer && !head_outer;
+}
+
+tg_status check_rope(const double* inv_freq, int64_t rotary, int64_t dim, int layout, double amplitude) {
+    if (layout != TG_ROPE_HALF && layout != TG_ROPE_INTERLEAVED)
+        return fail(TG_ERR_INVALID_ARG, "layout must be TG_ROPE_HALF (0) or TG_ROPE_INTERLEAVED (1), got %d", layout);
+    if (rotary < 0 || rotary % 2 != 0 || rotary > dim)
+        return fail(TG_ERR_INVALID_ARG, "rotary must be even and in [0, %lld], got %lld", (long long)dim,
+                    (long long)rotary);
+    if (rotary > 0 && inv_freq == nullptr) return fail(TG_ERR_INVALID_ARG, "inv_freq is NULL");
+    if (!aligned(inv_freq, 8)) return fail(TG_ERR_INVALID_ARG, "inv_freq must be 8-byte aligned");
+    if (!std::isfinite(static_cast<float>(amplitude)))
+        return fail(TG_ERR_INVALID_ARG, "amplitude must be finite in 32 bits");
+    return TG_OK;
+}
+
+tg_status check_cache(const void* k, const void* v, const float* ks, const float* vs, int64_t pages, int64_t kv_heads,
+                      int64_t page, int64_t dim, int format, KvCacheArgs* out) {
+    if (format != TG_KV_E4M3 && format != TG_KV_INT8)
+        return fail(TG_ERR_INVALID_ARG, "format must be TG_KV_E4M3 (0) or TG_KV_INT8 (1), got %d", format);
+    if (page != 16 && page != 32 && page != 64 && page != 128)
+        return fail(TG_ERR_INVALID_ARG, "page must be 16, 32, 64 or 128 tokens, got %lld", (long long)page);
+    if (dim != 64 && dim != 128)
+        return fail(TG_ERR_INVALID_ARG, "the cache supports head dimensions 64 and 128, got %lld", (long long)dim);
+    if (pages < 0 || pages > kIntMax || kv_heads < 1 || kv_heads > 1024)
+        return fail(TG_ERR_INVALID_ARG, "cache sizes out of range: pages=%lld kv_heads=%lld", (long long)pages,
+                    (long long)kv_heads);
+    if (pages > 0 && (!k || !v || !ks || !vs)) return fail(TG_ERR_INVALID_ARG, "a cache pointer is NULL");
+    if (!(aligned(k, 16) && aligned(v, 16) && aligned(ks, 4) && aligned(vs, 4)))
+        return fail(TG_ERR_INVALID_ARG, "cache codes must be 16-byte aligned and scales 4-byte aligned");
+    *out = KvCacheArgs{static_cast<uint8_t*>(const_cast<void*>(k)), static_cast<uint8_t*>(const_cast<void*>(v)),
+                       const_cast<float*>(ks), const_cast<float*>(vs), pages, (int)kv_heads, (int)page, (int)dim,
+                       format};
+    return TG_OK;
+}
+
+tg_status check_batch(const int32_t* table, int64_t table_width, const int32_t* lens, const int32_t* cu, int64_t batch,
+                      int64_t total, int64_t max_new, int64_t page, KvBatch* out) {
+    if (batch < 0 || batch > (1 << 20) || total < 0 || total > (1ll << 30) || max_new < 0 || max_new > kIntMax ||
+        table_width < 0 || table_width > kIntMax / page)
+        return fail(TG_ERR_INVALID_ARG, "sizes out of range: batch=%lld total=%lld max_new=%lld table_width=%lld",
+                    (long long)batch, (long long)total, (long long)max_new, (long long)table_width);
+    if (cu == nullptr && total != batch)
+        return fail(TG_ERR_INVALID_ARG, "without cu every sequence has one token: total %lld is not batch %lld",
+                    (long long)total, (long long)batch);
+    if (batch > 0 && total > 0) {
+        if (max_new < 1) return fail(TG_ERR_INVALID_ARG, "max_new must be at least 1, got %lld", (long long)max_new);
+        if (lens == nullptr || (table == nullptr && table_width > 0))
+            return fail(TG_ERR_INVALID_ARG, "table or lens is NULL");
+    }
+    if (!(aligned(table, 4) && aligned(lens, 4) && aligned(cu, 4)))
+        return fail(TG_ERR_INVALID_ARG, "table, lens and cu must be 4-byte aligned");
+    // a sequence has no more rows than there are, and where every sequence has one, one
+    const int64_t most = cu == nullptr ? 1 : (max_new < total ? max_new : total);
+    *out = KvBatch{table, table_width, lens, cu, (int)batch, (int)total, (int)most};
+    return TG_OK;
+}
+
+}  // namespace
+
+extern "C" tg_status tg_rope(const void* X, int64_t x_token_stride, int64_t x_head_stride, void* Y,
+                             int64_t y_token_stride, int64_t y_head_stride, const int32_t* positions, int64_t tokens,
+                             int64_t heads, int64_t dim, const double* inv_freq, int64_t rotary, double amplitude,
+                             int layout, int backward, int dtype, tg_stream_t stream_) {
+    t_last_error.clear();
+    const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    tg_status st = check_dtype(dtype);
+    if (st != TG_OK) return st;
+    if (backward != 0 && backward != 1) return fail(TG_ERR_INVALID_ARG, "backward must be 0 or 1, got %d", backward);
+    if (tokens < 0 || tokens > kIntMax || heads < 0 || heads > 0xFFFF || dim < 0 || dim > 1024)
+        return fail(TG_ERR_INVALID_ARG, "sizes out of range: tokens=%lld heads=%lld dim=%lld", (long long)tokens,
+                    (long long)heads, (long long)dim);
+    if ((st = check_strides("X", x_token_stride, x_head_stride)) != TG_OK) return st;
+    if ((st = check_strides("Y", y_token_stride, y_head_stride)) != TG_OK) return st;
+    if ((st = check_rope(inv_freq, rotary, dim, layout, amplitude)) != TG_OK) return st;
+    if (tokens == 0 || heads == 0 || dim == 0) return TG_OK;
+    if (!X || !Y || !positions) return fail(TG_ERR_INVALID_ARG, "X, Y or positions is NULL");
+    if (!(aligned(X, 2) && aligned(Y, 2) && aligned(positions, 4)))
+        return fail(TG_ERR_INVALID_ARG, "X and Y must be 2-byte aligned, positions 4-byte aligned");
+    if (rows_overlap(tokens, heads, dim, y_token_stride, y_head_stride))
+        return fail(TG_ERR_INVALID_ARG, "rows of Y overlap each other");
+    const bool in_place = X == Y && x_token_stride == y_token_stride && x_head_stride == y_head_stride;
+    if (!in_place && overlaps(Y, span_bytes(tokens, heads, dim, y_token_stride, y_head_stride), X,
+                              span_bytes(tokens, heads, dim, x_token_stride, x_head_stride)))
+        return fail(TG_ERR_INVALID_ARG, "Y overlaps X without being the same tensor");
+
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    if ((st = current_device(&dev)) != TG_OK) return st;
+    RopeCall c{};
+    c.x = Strided{const_cast<void*>(X), x_token_stride, x_head_stride};
+    c.y = Strided{Y, y_token_stride, y_head_stride};
+    c.positions = positions;
+    c.tokens = (int)tokens; c.heads = (int)heads; c.dim = (int)dim; c.dtype = dtype;
+    c.rope = RopeArgs{inv_freq, static_cast<float>(amplitude), (int)rotary, layout, backward ? -1.0f : 1.0f};
+    cudaError_t e = launch_rope(c, g_dev[dev].sm_count, stream);
+    return e == cudaSuccess ? TG_OK : cuda_fail(e, "rotary kernel launch");
+}
+
+extern "C" tg_status tg_kv_append(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int64_t pages,
+                                  int64_t kv_heads, int64_t page, int64_t dim, int format, const void* K,
+                                  int64_t k_token_stride, int64_t k_head_stride, const void* V, int64_t v_token_stride,
+                                  int64_t v_head_stride, const int32_t* table, int64_t table_width,
+                                  const int32_t* lens, const int32_t* cu, int64_t batch, int64_t total,
+                                  int64_t max_new, const double* inv_freq, int64_t rotary, double amplitude,
+                                  int layout, const void* Q, int64_t q_token_stride, int64_t q_head_stride,
+                                  void* Q_out, int64_t qo_token_stride, int64_t qo_head_stride, int64_t heads,
+                                  int dtype, tg_stream_t stream_) {
+    t_last_error.clear();
+    const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    KvAppendCall c{};
+    tg_status st = check_dtype(dtype);
+    if (st != TG_OK) return st;
+    if ((st = check_cache(k_cache, v_cache, k_scale, v_scale, pages, kv_heads, page, dim, format, &c.cache)) != TG_OK)
+        return st;
+    if ((st = check_batch(table, table_width, lens, cu, batch, total, max_new, page, &c.batch)) != TG_OK) return st;
+    if ((st = check_strides("K", k_token_stride, k_head_stride)) != TG_OK) return st;
+    if ((st = check_strides("V", v_token_stride, v_head_stride)) != TG_OK) return st;
+    if ((st = check_rope(inv_freq, rotary, dim, layout, amplitude)) != TG_OK) return st;
+    if (heads < 0 || heads > 0xFFFF) return fail(TG_ERR_INVALID_ARG, "heads out of range: %lld", (long long)heads);
+    if (heads > 0 && rotary == 0) return fail(TG_ERR_INVALID_ARG, "Q needs inv_freq: there is nothing to rotate it by");
+    if (batch == 0 || total == 0) return TG_OK;
+    if (!K || !V) return fail(TG_ERR_INVALID_ARG, "K or V is NULL");
+    if (!(aligned(K, 2) && aligned(V, 2))) return fail(TG_ERR_INVALID_ARG, "K and V must be 2-byte aligned");
+    const int64_t codes = pages * kv_heads * page * dim, scales = pages * kv_heads * 4;
+    const int64_t k_bytes = span_bytes(total, kv_heads, dim, k_token_stride, k_head_stride);
+    const int64_t v_bytes = span_bytes(total, kv_heads, dim, v_token_stride, v_head_stride);
+    const void* parts[4] = {k_cache, v_cache, k_scale, v_scale};
+    const int64_t part_bytes[4] = {codes, codes, scales, scales};
+    for (int i = 0; i < 4; ++i) {
+        if (overlaps(parts[i], part_bytes[i], K, k_bytes) || overlaps(parts[i], part_bytes[i], V, v_bytes))
+            return fail(TG_ERR_INVALID_ARG, "the cache overlaps K or V");
+        for (int j = 0; j < i; ++j)
+            if (overlaps(parts[i], part_bytes[i], parts[j], part_bytes[j]))
+                return fail(TG_ERR_INVALID_ARG, "the cache's tensors overlap each other");
+    }
+    if (heads > 0) {
+        if (!Q || !Q_out) return fail(TG_ERR_INVALID_ARG, "Q or Q_out is NULL");
+        if (!(aligned(Q, 2) && aligned(Q_out, 2)))
+            return fail(TG_ERR_INVALID_ARG, "Q and Q_out must be 2-byte aligned");
+        if ((st = check_strides("Q", q_token_stride, q_head_stride)) != TG_OK) return st;
+        if ((st = check_strides("Q_out", qo_token_stride, qo_head_stride)) != TG_OK) return st;
+        if (rows_overlap(total, heads, dim, qo_token_stride, qo_head_stride))
+            return fail(TG_ERR_INVALID_ARG, "rows of Q_out overlap each other");
+        // in place, Q may be interleaved with K and V (one packed projection); another output may not touch them
+        const bool in_place = Q == Q_out && q_token_stride == qo_token_stride && q_head_stride == qo_head_stride;
+        const int64_t q_bytes = span_bytes(total, heads, dim, q_token_stride, q_head_stride);
+        const int64_t o_bytes = span_bytes(total, heads, dim, qo_token_stride, qo_head_stride);
+        if (!in_place && (overlaps(Q_out, o_bytes, Q, q_bytes) || overlaps(Q_out, o_bytes, K, k_bytes) ||
+                          overlaps(Q_out, o_bytes, V, v_bytes)))
+            return fail(TG_ERR_INVALID_ARG, "Q_out overlaps an input without being Q itself");
+        for (int i = 0; i < 4; ++i)
+            if (overlaps(Q_out, o_bytes, parts[i], part_bytes[i]) || overlaps(Q, q_bytes, parts[i], part_bytes[i]))
+                return fail(TG_ERR_INVALID_ARG, "Q or Q_out overlaps the cache");
+    }
+
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    if ((st = current_device(&dev)) != TG_OK) return st;
+    c.k = Strided{const_cast<void*>(K), k_token_stride, k_head_stride};
+    c.v = Strided{const_cast<void*>(V), v_token_stride, v_head_stride};
+    c.q = Strided{const_cast<void*>(Q), q_token_stride, q_head_stride};
+    c.q_out = Strided{Q_out, qo_token_stride, qo_head_stride};
+    c.heads = (int)heads;
+    c.dtype = dtype;
+    c.rope = RopeArgs{rotary > 0 ? inv_freq : nullptr, static_cast<float>(amplitude), (int)rotary, layout, 1.0f};
+    c.wd = watchdog(g_dev[dev]);
+    cudaError_t e = launch_kv_append(c, g_dev[dev].sm_count, stream);
+    return e == cudaSuccess ? TG_OK : cuda_fail(e, "cache append kernel launch");
+}
+
+extern "C" tg_status tg_kv_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                                int64_t pages, int64_t kv_heads, int64_t page, int64_t dim, int format,
+                                const int32_t* table, int64_t table_width, const int32_t* first, const int32_t* cu,
+                                int64_t batch, int64_t total, void* K, void* V, int dtype, tg_stream_t stream_) {
+    t_last_error.clear();
+    const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    KvReadCall c{};
+    tg_status st = check_dtype(dtype);
+    if (st != TG_OK) return st;
+    if ((st = check_cache(k_cache, v_cache, k_scale, v_scale, pages, kv_heads, page, dim, format, &c.cache)) != TG_OK)
+        return st;
+    if ((st = check_batch(table, table_width, first, cu, batch, total, kIntMax, page, &c.batch)) != TG_OK) return st;
+    if (batch == 0 || total == 0) return TG_OK;
+    if (!K || !V) return fail(TG_ERR_INVALID_ARG, "K or V is NULL");
+    if (!(aligned(K, 16) && aligned(V, 16))) return fail(TG_ERR_INVALID_ARG, "K and V must be 16-byte aligned");
+    const int64_t codes = pages * kv_heads * page * dim, scales = pages * kv_heads * 4;
+    const int64_t bytes = total * kv_heads * dim * 2;
+    if (overlaps(K, bytes, V, bytes) || overlaps(K, bytes, k_cache, codes) || overlaps(K, bytes, v_cache, codes) ||
+        overlaps(V, bytes, k_cache, codes) || overlaps(V, bytes, v_cache, codes) ||
+        overlaps(K, bytes, k_scale, scales) || overlaps(K, bytes, v_scale, scales) ||
+        overlaps(V, bytes, k_scale, scales) || overlaps(V, bytes, v_scale, scales))
+        return fail(TG_ERR_INVALID_ARG, "K or V overlaps the cache or the other");
+
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    if ((st = current_device(&dev)) != TG_OK) return st;
+    c.k = K;
+    c.v = V;
+    c.dtype = dtype;
+    c.wd = watchdog(g_dev[dev]);
+    cudaError_t e = launch_kv_read(c, g_dev[dev].sm_count, stream);
+    return e == cudaSuccess ? TG_OK : cuda_fail(e, "cache read kernel launch");
+}
+
+namespace {
+
+// The checks that tg_attention_kv and its workspace query share.
+tg_status kv_attn_sizes(int64_t kv_heads, int64_t page, int64_t heads, int64_t total, int64_t max_len, int64_t window,
+                        int dtype, KvAttnCall* c) {
+    tg_status st = check_dtype(dtype);
+    if (st != TG_OK) return st;
+    if (heads < 1 || heads > 0xFFFF || kv_heads < 1 || heads % kv_heads != 0)
+        return fail(TG_ERR_INVALID_ARG, "heads must be a multiple of kv_heads, got %lld and %lld", (long long)heads,
+                    (long long)kv_heads);
+    if (max_len < 0 || max_len > kIntMax - page)
+        return fail(TG_ERR_INVALID_ARG, "max_len out of range: %lld", (long long)max_len);
+    if (window < 0 || window > kIntMax)
+        return fail(TG_ERR_INVALID_ARG, "window must be in [0, 2^31) (0: none), got %lld", (long long)window);
+    if (total * heads > (1ll << 33)) return fail(TG_ERR_INVALID_ARG, "too many rows");
+    c->heads = (int)heads;
+    c->dtype = dtype;
+    c->max_len = max_len;
+    c->window = window;
+    return TG_OK;
+}
+
+}  // namespace
+
+extern "C" tg_status tg_attention_kv_workspace(int64_t kv_heads, int64_t page, int64_t dim, int format, int64_t heads,
+                                               int64_t batch, int64_t total, int64_t max_new, int64_t max_len,
+                                               int64_t window, int dtype, int64_t* bytes) {
+    t_last_error.clear();
+    if (bytes == nullptr) return fail(TG_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = 0;
+    KvAttnCall c{};
+    static const int32_t some = 0;
+    tg_status st = check_cache(nullptr, nullptr, nullptr, nullptr, 0, kv_heads, page, dim, format, &c.cache);
+    if (st != TG_OK) return st;
+    if ((st = check_batch(&some, 0, &some, &some, batch, total, max_new, page, &c.batch)) != TG_OK) return st;
+    if ((st = kv_attn_sizes(kv_heads, page, heads, total, max_len, window, dtype, &c)) != TG_OK) return st;
+    if (batch == 0 || total == 0) return TG_OK;
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    if ((st = current_device(&dev)) != TG_OK) return st;
+    *bytes = kv_attn_workspace(c, g_dev[dev].sm_count);
+    return TG_OK;
+}
+
+extern "C" tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int64_t q_head_stride, void* O, float* lse,
+                                     const void* k_cache, const void* v_cache, const float* k_scale,
+                                     const float* v_scale, int64_t pages, int64_t kv_heads, int64_t page, int64_t dim,
+                                     int format, const int32_t* table, int64_t table_width, const int32_t* lens,
+                                     const int32_t* cu, int64_t batch, int64_t total, int64_t heads, int64_t max_new,
+                                     int64_t max_len, int causal, int64_t window, double scale, int dtype,
+                                     void* workspace, int64_t workspace_bytes, tg_stream_t stream_) {
+    t_last_error.clear();
+    const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    KvAttnCall c{};
+    tg_status st = check_cache(k_cache, v_cache, k_scale, v_scale, pages, kv_heads, page, dim, format, &c.cache);
+    if (st != TG_OK) return st;
+    if ((st = check_batch(table, table_width, lens, cu, batch, total, max_new, page, &c.batch)) != TG_OK) return st;
+    if ((st = kv_attn_sizes(kv_heads, page, heads, total, max_len, window, dtype, &c)) != TG_OK) return st;
+    if (causal != 0 && causal != 1) return fail(TG_ERR_INVALID_ARG, "causal must be 0 or 1, got %d", causal);
+    if (!causal && window > 0) return fail(TG_ERR_INVALID_ARG, "a window needs the causal mask");
+    if (!std::isfinite(static_cast<float>(scale)))
+        return fail(TG_ERR_INVALID_ARG, "scale must be finite in 32 bits");
+    if ((st = check_strides("Q", q_token_stride, q_head_stride)) != TG_OK) return st;
+    if (batch == 0 || total == 0) return TG_OK;
+    if (!Q || !O) return fail(TG_ERR_INVALID_ARG, "Q or O is NULL");
+    if (!(aligned(Q, 2) && aligned(O, 16) && aligned(lse, 4) && aligned(workspace, 16)))
+        return fail(TG_ERR_INVALID_ARG, "O and the workspace must be 16-byte aligned, Q 2-byte, lse 4-byte");
+    const int64_t codes = pages * kv_heads * page * dim, o_bytes = total * heads * dim * 2;
+    const int64_t l_bytes = lse ? total * heads * 4 : 0;
+    const int64_t q_bytes = span_bytes(total, heads, dim, q_token_stride, q_head_stride);
+    const void* in[5] = {Q, k_cache, v_cache, k_scale, v_scale};
+    const int64_t in_bytes[5] = {q_bytes, codes, codes, pages * kv_heads * 4, pages * kv_heads * 4};
+    for (int i = 0; i < 5; ++i)
+        if (overlaps(O, o_bytes, in[i], in_bytes[i]) || overlaps(lse, l_bytes, in[i], in_bytes[i]) ||
+            overlaps(workspace, workspace_bytes, in[i], in_bytes[i]))
+            return fail(TG_ERR_INVALID_ARG, "an output or the workspace overlaps an input");
+    if (overlaps(O, o_bytes, lse, l_bytes) || overlaps(workspace, workspace_bytes, O, o_bytes) ||
+        overlaps(workspace, workspace_bytes, lse, l_bytes))
+        return fail(TG_ERR_INVALID_ARG, "the outputs and the workspace overlap each other");
+
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    if ((st = current_device(&dev)) != TG_OK) return st;
+    c.q = Strided{const_cast<void*>(Q), q_token_stride, q_head_stride};
+    c.out = O;
+    c.lse = lse;
+    c.causal = causal;
+    c.scale = static_cast<float>(scale);
+    c.wd = watchdog(g_dev[dev]);
+    const int64_t need = kv_attn_workspace(c, g_dev[dev].sm_count);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+        return fail(TG_ERR_INVALID_ARG, "tg_attention_kv needs a workspace of %lld bytes, got %lld", (long long)need,
+                    (long long)(workspace ? workspace_bytes : 0));
+    cudaError_t e = launch_kv_attn(c, workspace, g_dev[dev].sm_count, stream);
+    return e == cudaSuccess ? TG_OK : cuda_fail(e, "cache attention kernel launch");
 }
