@@ -452,7 +452,9 @@ tg_status tg_kv_read(const void* k_cache, const void* v_cache, const float* k_sc
  * causal 0: all lens[i]. A row that sees nothing (lens[i] 0, say) gives zeros.
  * lse (NULL, or total x heads fp32) receives the natural log of the sum of
  * exp(scale * q . k_j), -inf for such a row. max_len bounds lens (longer
- * sequences are reported and give zeros).
+ * sequences are reported and give zeros). What lies in the cache past a
+ * sequence's length has no effect; a NaN value inside it makes NaN of the rows
+ * that see it, and may of the sequence's other rows in the same call.
  *
  * Scores, softmax and sums are fp32, codes enter the products exactly, O
  * (total x heads x dim, contiguous, 16-byte aligned) is rounded once. Results

@@ -185,18 +185,16 @@ def test_queries_of_every_size(tg, counts, lens):
 
 
 @pytest.mark.parametrize("most", [4, 30])
-def test_nan_in_the_cache_reaches_only_the_rows_that_see_it(tg, most):
-    counts, lens = [most, 1], [40, 33]
+def test_nan_in_the_cache_reaches_the_rows_that_see_it_and_no_other_sequence(tg, most):
+    counts, lens = [most, 1, most], [40, 33, 35]
     cache, host, table, q = _case(tg, counts, lens, 16, 1, 2, 64, 0, 0, seed=25, garbage=False)
     raw = cache.v.view(torch.uint8)
     raw[int(table[0, 2]), 0, 6, 7] = 0x7F  # sequence 0, position 38: its last two rows see it
-    cu = _ints([0, most, most + 1])
+    cu = _ints([0, most, most + 1, 2 * most + 1])
     out = tg.attention_kv(q.cuda(), cache, table.cuda(), _ints(lens), cu, max_new=most, max_len=40)
     nan = out.isnan()
-    assert nan[most - 2:most, :, 7].all() and not nan[most].any()
-    if most < 16:  # rows of one tile share its products, and a NaN times a weight of zero is one: a row of another tile does not see it
-        return
-    assert not nan[:8].any()
+    assert nan[most - 2:most, :, 7].all() and not nan[most:].any()
+    assert not nan[:, :, :7].any() and not nan[:, :, 8:].any()
 
 
 @pytest.mark.parametrize("most", [1, 40])

@@ -4,23 +4,61 @@
 //
 // over the keys that the token sees: positions up to its own (or all of the
 // sequence's when not causal), and with a window only the last `window` of
-// them. Query heads h * share .. (h + 1) * share - 1 read kv head h. A row that
+// them. Query heads g * share .. (g + 1) * share - 1 read kv head g. A row that
 // sees no key gives zeros, and -inf as its log of the sum.
+//
+// This file: few rows a kv head (single tokens, drafts). There the cache's
+// bytes bound the work, so each code is read once, by the copy engine, and the
+// products are arranged so that nothing has to be moved between lanes.
+//
+// Scales stay out of the products. With t_j = log2(e) scale k_scale (q . kcode_j)
+// + log2(v_scale), the weights w_j = 2^(t_j - m) carry the value scale of their
+// page, so o = sum w_j vcode_j / sum (w_j / v_scale): the codes enter both
+// products exactly (e4m3 and int8 are exact in fp16), and w_j <= 2^8 whatever
+// the scales. w is rounded to fp16 (2^-11 of itself) for its product, its sum is
+// kept in fp32 from the unrounded value.
+//
+// Splitting. The batch's work is a list of 64-token chunks, unit by unit (a unit
+// is a sequence, a kv head and a block of 8 * kTiles rows); every CTA takes the
+// same share of that list, so ragged lengths balance and few long sequences
+// spread over the GPU. A unit that lies inside one CTA's share is finished
+// there; parts of a unit that crosses shares go to the workspace and a second
+// kernel, launched early, joins them in order.
+//
+// Inside a CTA four warps take every fourth 16-token step of a chunk, each with
+// a ring of its own that TMA fills (16 tokens of one head are contiguous in a
+// page). Per step a warp computes, with m16n8k16:
+//   S^T (16 tokens x 8 rows) = K (16 x dim) Q^T, K the A operand,
+//   O^T (dim x 8 rows) += V^T (dim x 16) W^T, V the A operand,
+// so up to 8 rows cost one MMA column block, both operands are read from shared
+// memory as whole 16-byte pieces (which dim a lane's piece holds does not
+// matter as long as Q or O agrees), and W^T is S^T's registers through one
+// 8 x 8 transposition. The 128-byte swizzle and the order in which a step's
+// tokens are given to MMA rows (mma_token) keep those reads free of bank
+// conflicts.
+#include "tg_device.cuh"
 #include "tg_kv.cuh"
+
+#include <type_traits>
 
 namespace tg {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNoMax = -1e30f;        // running maximum before any visible key
+constexpr float kRescaleLog2 = 8.0f;    // the maximum moves only when a weight would pass 2^8
+
+// ---------------------------------------------------------------- rows by the dozen (any number of rows)
+
+constexpr int kRowWarps = 8;
 
 // One warp per (token, query head), one key at a time, the running maximum and sum in fp32.
 template <typename E, int kFmt, int kDim>
-__global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const KvAttnCall c) {
+__global__ void __launch_bounds__(kRowWarps * 32) attn_rows_kernel(const KvAttnCall c) {
     constexpr int kPer = kDim / 32;
     const KvBatch& b = c.batch;
     const int lane = threadIdx.x % 32;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + threadIdx.x / 32;
     if (row >= static_cast<int64_t>(b.total) * c.heads) return;
     const int token = static_cast<int>(row / c.heads), head = static_cast<int>(row % c.heads);
     int seq = token;
@@ -77,25 +115,728 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const KvAttnCall
     if (c.lse != nullptr && lane == 0) c.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * (1.0f / kLog2e);
 }
 
-template <typename E, int kFmt>
-cudaError_t launch(const KvAttnCall& c, cudaStream_t stream) {
+// ---------------------------------------------------------------- few rows
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStep = 16;                    // tokens per warp and step
+constexpr int kChunk = kWarps * kStep;       // tokens per unit of the work list
+constexpr int kStages = 4;                   // steps in flight per warp
+
+template <int kDim>
+struct Ring {
+    static constexpr int kHalf = kStep * kDim;       // bytes of one step's keys (or values)
+    static constexpr int kStage = 2 * kHalf;
+    static constexpr int kWarp = kStages * kStage;
+    static constexpr int kBytes = kWarps * kWarp;
+};
+
+// Where CTA k of `ctas` begins in a list of `total` chunks: equal shares, the first ones one longer.
+struct Shares {
+    int64_t each;
+    int rest;
+    int ctas;
+    __device__ Shares(int64_t total, int grid, int least) {
+        const int64_t most = (total + least - 1) / least;
+        ctas = static_cast<int>(min(static_cast<int64_t>(grid), most));
+        each = ctas > 0 ? total / ctas : 0;
+        rest = ctas > 0 ? static_cast<int>(total - each * ctas) : 0;
+    }
+    __device__ int64_t start(int k) const { return k * each + min(k, rest); }
+    __device__ int owner(int64_t chunk) const {
+        const int64_t longer = (each + 1) * rest;
+        return static_cast<int>(chunk < longer ? chunk / (each + 1) : rest + (chunk - longer) / each);
+    }
+};
+
+// What CTA k leaves for the joining kernel: the unit that its share begins inside of (chunks 0: none).
+struct Meta {
+    int64_t unit_start, total;
+    int chunks, seq, head, block;
+};
+
+struct FewArgs {
+    KvAttnCall c;
+    int share;          // query heads per kv head
+    int least;          // fewest chunks worth a CTA
+    int grid;
+    int q_vec;          // Q 8-byte aligned with strides of whole 8 bytes
+    Meta* meta;         // grid entries
+    float* parts;       // grid x 2 parts: rows x (dim + 2) floats each (values, then maxima, then sums)
+    int page_shift;
+};
+
+// A sequence's share of the list.
+struct SeqWork {
+    int first, count;      // its rows of the packed tensors
+    int len;
+    int chunk0, chunks;    // 64-token chunks that any of its rows sees (at least one, perhaps empty)
+    int blocks;            // row blocks per kv head
+    int64_t total;         // chunks over its units
+};
+
+template <int kTiles>
+__device__ __forceinline__ SeqWork seq_work(const FewArgs& a, int i) {
+    const KvAttnCall& c = a.c;
+    SeqWork w;
+    const SeqSpan span = seq_span(c.batch, i, c.wd);
+    w.first = span.first;
+    w.count = span.count;
+    w.len = __ldg(c.batch.lens + i);
+    if (w.len < 0 || w.len > c.max_len || w.len > c.batch.table_width << a.page_shift) {
+        report_range(c.wd);
+        w.len = 0;
+    }
+    const int64_t begin = c.window > 0 ? static_cast<int64_t>(w.len) - w.count - c.window + 1 : 0;
+    w.chunk0 = begin > 0 ? static_cast<int>(begin / kChunk) : 0;
+    w.chunks = max(1, (w.len + kChunk - 1) / kChunk - w.chunk0);
+    w.blocks = static_cast<int>((static_cast<int64_t>(w.count) * a.share + 8 * kTiles - 1) / (8 * kTiles));
+    w.total = static_cast<int64_t>(w.blocks) * c.cache.kv_heads * w.chunks;
+    return w;
+}
+
+// Token of a step that MMA row i stands for. A quarter-warp's 16-byte reads touch the rows 2 i and
+// 2 i + 1 (keys) or the even or odd ones of eight (values); with 128-byte lines swizzled by their
+// line number these orders send the eight reads to eight different 16-byte banks.
+template <int kDim>
+__device__ __forceinline__ int mma_token(int i) {
+    if constexpr (kDim == 128) {
+        const int r = i & 7;
+        return (i & 8) | ((r & 1) ? (r ^ 4) : r);  // 0 5 2 7 4 1 6 3
+    } else {
+        const int r = i & 7;                          // lines of two tokens: 0 1 4 5 8 9 12 13, then two further
+        return ((r >> 1) * 4 + (r & 1)) + ((i & 8) ? 2 : 0);
+    }
+}
+
+// Byte offset of piece `at` (bytes) of token t in a swizzled half stage.
+template <int kDim>
+__device__ __forceinline__ int ring_offset(int t, int at) {
+    const int line = kDim == 128 ? t : t >> 1;
+    const int in = kDim == 128 ? at : (t & 1) * 64 + at;
+    return line * 128 + (in ^ ((line & 7) << 4));
+}
+
+// Four codes to two fp16 pairs (codes 0 1, codes 2 3).
+template <int kFmt>
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if constexpr (kFmt == kKvE4M3) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    } else {
+        // code + 128 as the low byte of 1024 + (code + 128) in fp16, whose steps are 1 there
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 bias = __half2half2(__ushort_as_half(static_cast<unsigned short>(0x6480)));  // 1152
+        uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias), y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+        lo = *reinterpret_cast<const uint32_t*>(&x);
+        hi = *reinterpret_cast<const uint32_t*>(&y);
+    }
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four values of a query row from `d` on; bytes past a row's end are never read.
+template <typename E>
+__device__ __forceinline__ void load_q4(const E* row, int d, bool vec, float (&x)[4]) {
+    if (vec) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + d));
+        const E* e = reinterpret_cast<const E*>(&w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = to_float(e[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = to_float(row[d + i]);
+    }
+}
+
+// A row's result: unnormalised values o[0 .. n) at the running maximum's scale, its sum l.
+template <typename E>
+__device__ __forceinline__ float row_inverse(float l) {
+    return l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+}
+
+template <typename E, int kFmt, int kDim, int kTiles>
+__global__ void __launch_bounds__(kThreads, kTiles == 4 && kDim == 128 ? 2 : 3)
+    attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const FewArgs a) {
+    constexpr int kRows = 8 * kTiles;
+    constexpr int kK = kDim / 16;            // MMA steps along dim (scores) and m16 tiles along dim (values)
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ alignas(8) uint64_t bars[kWarps * kStages];
+    __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows];
+    __shared__ int64_t scan[kWarps], found_off;
+    __shared__ int found_seq;
+    __shared__ int abort_flag;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const KvAttnCall& c = a.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    const uint32_t ring = smem_u32(smem) + warp * Ring<kDim>::kWarp;
+    const uint32_t bar0 = smem_u32(bars + warp * kStages);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (lane == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init(bar0 + 8 * s, 1);
+        fence_barrier_init();
+    }
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        found_seq = -1;
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    const WaitCtx wc{&abort_flag, c.wd.status, c.wd.limit_ns};
+
+    // ---- this CTA's share of the list: the total, then the sequence in which the share begins
+    const int batch = c.batch.batch;
+    int64_t total = 0;
+    auto block_scan = [&](int64_t v, int64_t& before) {  // sum over the block; `before`: over lower threads
+        int64_t x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = x;
+        __syncthreads();
+        int64_t sum = 0, low = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) low += scan[w];
+            sum += scan[w];
+        }
+        before = low + x - v;
+        return sum;
+    };
+    int64_t mine = 0, before = 0;
+    for (int base = 0; base < batch; base += kThreads) {
+        const int i = base + threadIdx.x;
+        mine = i < batch ? seq_work<kTiles>(a, i).total : 0;
+        total += block_scan(mine, before);
+    }
+    const Shares shares(total, a.grid, a.least);
+    const int k = blockIdx.x;
+    if (k >= shares.ctas) {
+        if (threadIdx.x == 0) a.meta[k].chunks = 0;
+        return;
+    }
+    int64_t pos = shares.start(k);
+    const int64_t stop = shares.start(k + 1);
+    int64_t carry = 0;
+    for (int base = 0; base < batch; base += kThreads) {
+        if (batch > kThreads) {
+            const int i = base + threadIdx.x;
+            mine = i < batch ? seq_work<kTiles>(a, i).total : 0;
+            const int64_t sum = block_scan(mine, before);
+            before += carry;
+            carry += sum;
+        }
+        if (before <= pos && pos < before + mine) {
+            found_seq = base + threadIdx.x;
+            found_off = pos - before;
+        }
+    }
+    __syncthreads();
+    int seq = found_seq;
+    int64_t off = found_off;
+    SeqWork w = seq_work<kTiles>(a, seq);
+
+    int step_no = 0;  // steps issued to this warp's ring so far: stage and phase
+    bool first_segment = true;
+    bool ok = true;
+    while (pos < stop) {
+        if (off >= w.total) {  // the next sequence that has rows
+            do {
+                if (++seq >= batch) return;
+                w = seq_work<kTiles>(a, seq);
+            } while (w.total == 0);
+            off = 0;
+        }
+        const int unit = static_cast<int>(off / w.chunks);
+        const int c0 = static_cast<int>(off - static_cast<int64_t>(unit) * w.chunks);
+        const int c1 = static_cast<int>(min(static_cast<int64_t>(w.chunks), c0 + (stop - pos)));
+        const int head = unit / w.blocks, block = unit - head * w.blocks;
+        if (first_segment && threadIdx.x == 0) {
+            Meta m{pos - c0, total, c0 > 0 ? w.chunks : 0, seq, head, block};
+            a.meta[k] = m;
+        }
+        const int row0 = block * kRows, rows = min(kRows, w.count * a.share - row0);
+
+        // ---- the steps of this warp: chunks i0 .. i1 - 1, its 16 tokens of each
+        const int tok0 = (w.chunk0 + c0) * kChunk + warp * kStep;
+        const int64_t see0 = c.window > 0 ? static_cast<int64_t>(w.len) - w.count + row0 / a.share - c.window + 1 : 0;
+        int i0 = 0, i1 = c1 - c0;
+        if (tok0 >= w.len) i1 = 0;
+        else i1 = min(i1, (w.len - tok0 + kChunk - 1) / kChunk);
+        if (see0 > tok0) i0 = static_cast<int>(min(static_cast<int64_t>(i1), (see0 - tok0) / kChunk));
+        const int n_steps = i1 - i0;
+        const int32_t* table = c.batch.table + static_cast<int64_t>(seq) * c.batch.table_width;
+
+        // page and scales of 32 steps at a time, a step a lane; those of the next 32 in advance
+        auto page_of = [&](int s) {
+            if (s >= n_steps) return -1;
+            const int p = __ldg(table + ((tok0 + (i0 + s) * kChunk) >> a.page_shift));
+            if (p < 0 || p >= c.cache.pages) {
+                report_range(c.wd);
+                return -1;
+            }
+            return p;
+        };
+        auto scales_of = [&](int p, float& ks, float& lv, float& iv) {
+            const int64_t ph = static_cast<int64_t>(max(p, 0)) * c.cache.kv_heads + head;
+            ks = p >= 0 ? __ldg(c.cache.k_scale + ph) : 0.0f;
+            const float vs = p >= 0 ? max_nan(__ldg(c.cache.v_scale + ph), kScaleFloor) : 1.0f;
+            lv = lg2_approx(vs);
+            iv = rcp_approx(vs);
+        };
+        auto issue = [&](int s, int p, int slot) {  // lane 0: the copies of step s into stage slot
+            const uint32_t bar = bar0 + 8 * slot;
+            if (p >= 0) {
+                const int64_t place = (static_cast<int64_t>(p) * c.cache.kv_heads + head) * c.cache.page +
+                                      ((tok0 + (i0 + s) * kChunk) & (c.cache.page - 1));
+                const int line = static_cast<int>(kDim == 128 ? place : place >> 1);
+                mbar_arrive_expect_tx(bar, Ring<kDim>::kStage);
+                tma_load_2d(ring + slot * Ring<kDim>::kStage, &tmK, bar, 0, line);
+                tma_load_2d(ring + slot * Ring<kDim>::kStage + Ring<kDim>::kHalf, &tmV, bar, 0, line);
+            } else {
+                mbar_arrive(bar);
+            }
+        };
+        int pg = page_of(lane), pg_next = -1;
+        for (int s = 0; s < min(kStages, n_steps); ++s) {
+            const int p = __shfl_sync(0xFFFFFFFFu, pg, s);
+            if (lane == 0) issue(s, p, (step_no + s) % kStages);
+        }
+        float ks, lv, iv, ks_next = 0.0f, lv_next = 0.0f, iv_next = 0.0f;
+        scales_of(pg, ks, lv, iv);
+
+        // ---- the queries: lane (gid, tig) holds of row gid (of each tile) the values that meet its
+        // pieces of the keys. bf16 rows are moved by a power of two so that their largest value lies
+        // in [2^14, 2^15): fp16 then holds every value down to 2^-28 of it without loss.
+        uint32_t q[kTiles][kK][2];
+        float factor[kTiles][2];     // of rows 2 tig, 2 tig + 1: scale * log2(e) / that power
+        int see_from[kTiles][2], see_to[kTiles][2];
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+            const int r = row0 + min(8 * n + gid, rows - 1);
+            const int t = r / a.share;
+            const E* x = static_cast<const E*>(c.q.p) + (w.first + t) * c.q.token + (head * a.share + r - t * a.share) * c.q.head;
+            const bool real = 8 * n + gid < rows;
+            float most = 0.0f;
+            float f = c.scale * kLog2e;
+            float v[kK][4];
+#pragma unroll
+            for (int s = 0; s < kK; ++s) {
+                load_q4(x, (s >> 2) * 64 + tig * 16 + (s & 3) * 4, a.q_vec != 0, v[s]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (!real) v[s][e] = 0.0f;
+                    most = fmaxf(most, fabsf(v[s][e]));
+                }
+            }
+            if constexpr (!std::is_same<E, __half>::value) {
+                most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+                most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+                // the exponent of the largest value, kept where 2^(14 - e) is an ordinary number
+                const int e = most > 0.0f && most <= 3.3895314e38f ? max(-100, (__float_as_int(most) >> 23) - 127) : 14;
+                const float up = __int_as_float((14 - e + 127) << 23);
+                f *= __int_as_float((e - 14 + 127) << 23);
+#pragma unroll
+                for (int s = 0; s < kK; ++s)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[s][j] *= up;
+            }
+#pragma unroll
+            for (int s = 0; s < kK; ++s) {
+                q[n][s][0] = half2_bits(v[s][0], v[s][1]);
+                q[n][s][1] = half2_bits(v[s][2], v[s][3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                factor[n][e] = __shfl_sync(0xFFFFFFFFu, f, (2 * tig + e) * 4);
+                const int rr = row0 + min(8 * n + 2 * tig + e, rows - 1);
+                const int p = w.len - w.count + rr / a.share;
+                see_to[n][e] = c.causal ? min(w.len, p + 1) : w.len;
+                see_from[n][e] = c.window > 0 && p - c.window + 1 > 0 ? static_cast<int>(p - c.window + 1) : 0;
+            }
+        }
+        // keys that every row sees: no mask there
+        const int p_first = w.len - w.count + row0 / a.share, p_last = w.len - w.count + (row0 + rows - 1) / a.share;
+        const int all_to = c.causal ? min(w.len, p_first + 1) : w.len;
+        const int all_from = c.window > 0 && p_last - c.window + 1 > 0 ? static_cast<int>(p_last - c.window + 1) : 0;
+
+        float m[kTiles][2], l[kTiles][2], o[kTiles][kK][4];
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+            m[n][0] = m[n][1] = kNoMax;
+            l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kK; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.0f;
+        }
+
+        const int kt0 = mma_token<kDim>(gid), kt1 = mma_token<kDim>(gid + 8);
+        int s = 0;
+        for (; s < n_steps; ++s) {
+            const int in = s & 31;
+            if (s > 0 && in == 0) {
+                pg = pg_next;
+                ks = ks_next;
+                lv = lv_next;
+                iv = iv_next;
+            }
+            if (in == 0) pg_next = page_of(s + 32 + lane);
+            if (in == 8) scales_of(pg_next, ks_next, lv_next, iv_next);
+            const int slot = (step_no + s) % kStages;
+            const uint32_t phase = static_cast<uint32_t>((step_no + s) / kStages) & 1u;
+            if (!__all_sync(0xFFFFFFFFu, wait_phase(bar0 + 8 * slot, phase, wc, kSiteConvFull))) {
+                ok = false;
+                break;
+            }
+            const int p = __shfl_sync(0xFFFFFFFFu, pg, in);
+            if (p >= 0) {
+                const float ksc = __shfl_sync(0xFFFFFFFFu, ks, in), lvs = __shfl_sync(0xFFFFFFFFu, lv, in);
+                const float ivs = __shfl_sync(0xFFFFFFFFu, iv, in);
+                const uint32_t kbase = ring + slot * Ring<kDim>::kStage, vbase = kbase + Ring<kDim>::kHalf;
+                const int token = tok0 + (i0 + s) * kChunk;
+
+                // S^T = K Q^T
+                float sc[kTiles][4];
+#pragma unroll
+                for (int n = 0; n < kTiles; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < kDim / 64; ++j) {
+                    const uint4 x = lds_v4(kbase + ring_offset<kDim>(kt0, j * 64 + tig * 16));
+                    const uint4 y = lds_v4(kbase + ring_offset<kDim>(kt1, j * 64 + tig * 16));
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t a0, a1, a2, a3;
+                        codes_to_half<kFmt>(xs[e], a0, a2);
+                        codes_to_half<kFmt>(ys[e], a1, a3);
+#pragma unroll
+                        for (int n = 0; n < kTiles; ++n) mma16816(sc[n], a0, a1, a2, a3, q[n][j * 4 + e][0], q[n][j * 4 + e][1]);
+                    }
+                }
+                // t = scaled score + log2(value scale); masked keys -inf
+                bool above = false;
+#pragma unroll
+                for (int n = 0; n < kTiles; ++n) {
+                    const float f0 = factor[n][0] * ksc, f1 = factor[n][1] * ksc;
+                    sc[n][0] = fmaf(sc[n][0], f0, lvs);
+                    sc[n][1] = fmaf(sc[n][1], f1, lvs);
+                    sc[n][2] = fmaf(sc[n][2], f0, lvs);
+                    sc[n][3] = fmaf(sc[n][3], f1, lvs);
+                }
+                const bool edge = token < all_from || token + kStep > all_to;
+                if (edge) {
+#pragma unroll
+                    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int t0 = token + kt0, t1 = token + kt1;
+                            if (t0 < see_from[n][e] || t0 >= see_to[n][e]) sc[n][e] = -INFINITY;
+                            if (t1 < see_from[n][e] || t1 >= see_to[n][e]) sc[n][2 + e] = -INFINITY;
+                        }
+                }
+#pragma unroll
+                for (int n = 0; n < kTiles; ++n)
+                    above |= fmaxf(sc[n][0], sc[n][2]) > m[n][0] + kRescaleLog2 || fmaxf(sc[n][1], sc[n][3]) > m[n][1] + kRescaleLog2;
+                if (__any_sync(0xFFFFFFFFu, above)) {
+#pragma unroll
+                    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float t = fmaxf(sc[n][e], sc[n][2 + e]);
+                            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
+                            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
+                            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
+                            const float m_new = fmaxf(m[n][e], t);
+                            const float keep = ex2_approx(m[n][e] - m_new);
+                            m[n][e] = m_new;
+                            l[n][e] *= keep;
+#pragma unroll
+                            for (int j = 0; j < kK; ++j) {
+                                o[n][j][e] *= keep;
+                                o[n][j][2 + e] *= keep;
+                            }
+                        }
+                }
+                uint32_t wt[kTiles][2];
+#pragma unroll
+                for (int n = 0; n < kTiles; ++n) {
+                    const float w0 = ex2_approx(sc[n][0] - m[n][0]), w1 = ex2_approx(sc[n][1] - m[n][1]);
+                    const float w2 = ex2_approx(sc[n][2] - m[n][0]), w3 = ex2_approx(sc[n][3] - m[n][1]);
+                    l[n][0] = fmaf(w0 + w2, ivs, l[n][0]);
+                    l[n][1] = fmaf(w1 + w3, ivs, l[n][1]);
+                    wt[n][0] = transpose8x8(half2_bits(w0, w1));
+                    wt[n][1] = transpose8x8(half2_bits(w2, w3));
+                }
+                // O^T += V^T W^T
+                uint32_t v[4][kDim / 32];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = mma_token<kDim>(2 * tig + (e & 1) + (e >> 1) * 8);
+                    if constexpr (kDim == 128) {
+                        const uint4 x = lds_v4(vbase + ring_offset<kDim>(t, gid * 16));
+                        v[e][0] = x.x;
+                        v[e][1] = x.y;
+                        v[e][2] = x.z;
+                        v[e][3] = x.w;
+                    } else {
+                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                     : "=r"(v[e][0]), "=r"(v[e][1])
+                                     : "r"(vbase + ring_offset<kDim>(t, gid * 8))
+                                     : "memory");
+                    }
+                    // what lies past the sequence's end may be anything, and 0 times a NaN is one
+                    if (edge && token + t >= w.len) {
+#pragma unroll
+                        for (int j = 0; j < kDim / 32; ++j) v[e][j] = 0;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kDim / 32; ++j) {
+                    uint32_t a0, a1, a2, a3;
+                    codes_to_half<kFmt>(__byte_perm(v[0][j], v[1][j], 0x5140), a0, a1);
+                    codes_to_half<kFmt>(__byte_perm(v[2][j], v[3][j], 0x5140), a2, a3);
+#pragma unroll
+                    for (int n = 0; n < kTiles; ++n) mma16816(o[n][2 * j], a0, a1, a2, a3, wt[n][0], wt[n][1]);
+                    codes_to_half<kFmt>(__byte_perm(v[0][j], v[1][j], 0x7362), a0, a1);
+                    codes_to_half<kFmt>(__byte_perm(v[2][j], v[3][j], 0x7362), a2, a3);
+#pragma unroll
+                    for (int n = 0; n < kTiles; ++n) mma16816(o[n][2 * j + 1], a0, a1, a2, a3, wt[n][0], wt[n][1]);
+                }
+            }
+            __syncwarp();  // every lane has read the stage: it may be filled again
+            if (s + kStages < n_steps) {
+                const int ahead = (s + kStages) & 31;
+                const int p_ahead = __shfl_sync(0xFFFFFFFFu, ahead < in ? pg_next : pg, ahead);
+                if (lane == 0) issue(s + kStages, p_ahead, slot);
+            }
+        }
+        if (!ok) {  // let every copy in flight land, then stop with the others
+            for (const int issued = min(n_steps, s + kStages); s < issued; ++s)
+                wait_phase_drain(bar0 + 8 * ((step_no + s) % kStages), static_cast<uint32_t>((step_no + s) / kStages) & 1u, wc);
+        }
+        step_no += n_steps;
+
+        // ---- join the four warps: each brings its values to the common maximum, in its own ring
+        // (its copies have all been read), then all threads add them up
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 4);
+                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 8);
+                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 16);
+                if (gid == 0) {
+                    red_m[warp][8 * n + 2 * tig + e] = m[n][e];
+                    red_l[warp][8 * n + 2 * tig + e] = l[n][e];
+                }
+            }
+        if (__syncthreads_or(!ok)) break;
+        float* mine_o = reinterpret_cast<float*>(smem + warp * Ring<kDim>::kWarp);
+        static_assert(kRows * kDim * 4 <= Ring<kDim>::kWarp, "a warp's values fit its ring");
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * n + 2 * tig + e;
+                const float top = fmaxf(fmaxf(red_m[0][r], red_m[1][r]), fmaxf(red_m[2][r], red_m[3][r]));
+                const float keep = ex2_approx(m[n][e] - top);
+#pragma unroll
+                for (int j = 0; j < kK; ++j) {
+                    // (tile j, gid) holds value gid * dim / 8 + 2 j, (tile j, gid + 8) the next one
+                    float2 x = make_float2(o[n][j][e] * keep, o[n][j][2 + e] * keep);
+                    *reinterpret_cast<float2*>(mine_o + r * kDim + gid * (kDim / 8) + 2 * j) = x;
+                }
+            }
+        __syncthreads();
+        const bool whole = c0 == 0 && c1 == w.chunks;
+        float* part = a.parts + (static_cast<int64_t>(2 * k) + (first_segment ? 0 : 1)) * kRows * (kDim + 2);
+        for (int i = threadIdx.x; i < rows * (kDim / 4); i += kThreads) {
+            const int r = i / (kDim / 4), d = (i % (kDim / 4)) * 4;
+            float top = kNoMax, sum = 0.0f;
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) top = fmaxf(top, red_m[x][r]);
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) {
+                sum += red_l[x][r] * ex2_approx(red_m[x][r] - top);
+                const float4 y = *reinterpret_cast<const float4*>(smem + x * Ring<kDim>::kWarp + (r * kDim + d) * 4);
+                v.x += y.x;
+                v.y += y.y;
+                v.z += y.z;
+                v.w += y.w;
+            }
+            if (whole) {
+                const int t = (row0 + r) / a.share;
+                const int64_t to = static_cast<int64_t>(w.first + t) * c.heads + head * a.share + (row0 + r) - t * a.share;
+                const float inv = row_inverse<E>(sum);
+                E h[4] = {from_float<E>(v.x * inv), from_float<E>(v.y * inv), from_float<E>(v.z * inv), from_float<E>(v.w * inv)};
+                *reinterpret_cast<uint2*>(static_cast<E*>(c.out) + to * kDim + d) = *reinterpret_cast<const uint2*>(h);
+                if (d == 0 && c.lse != nullptr) c.lse[to] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * (1.0f / kLog2e);
+            } else {
+                *reinterpret_cast<float4*>(part + r * kDim + d) = v;
+                if (d == 0) {
+                    part[kRows * kDim + r] = top;
+                    part[kRows * (kDim + 1) + r] = sum;
+                }
+            }
+        }
+        fence_proxy_async_smem();  // these reads and writes come before the next copies into the rings
+        __syncthreads();
+        pos += c1 - c0;
+        off += c1 - c0;
+        first_segment = false;
+    }
+}
+
+// Joins the parts of the unit inside which share k begins, if k's is its first border: block
+// (k - 1, row). The order of the parts is that of their keys.
+template <typename E, int kDim, int kRows>
+__global__ void __launch_bounds__(kDim) attn_join_kernel(const FewArgs a) {
+    const KvAttnCall& c = a.c;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int k = blockIdx.x + 1, r = blockIdx.y, d = threadIdx.x;
+    const Meta m = a.meta[k];
+    if (m.chunks == 0) return;
+    const Shares shares(m.total, a.grid, a.least);
+    const int64_t before = shares.start(k - 1);
+    if (before > m.unit_start) return;  // an earlier border lies in the unit
+    const SeqSpan span = seq_span(c.batch, m.seq, c.wd);
+    const int row = m.block * kRows + r;
+    if (row >= span.count * a.share) return;
+    const int last = shares.owner(m.unit_start + m.chunks - 1);
+    auto part_of = [&](int x) {
+        const int slot = x == k - 1 && before < m.unit_start ? 1 : 0;
+        return a.parts + (static_cast<int64_t>(2 * x) + slot) * kRows * (kDim + 2);
+    };
+    float top = kNoMax;
+    for (int x = k - 1; x <= last; ++x) top = fmaxf(top, part_of(x)[kRows * kDim + r]);
+    float v = 0.0f, sum = 0.0f;
+#pragma unroll 4
+    for (int x = k - 1; x <= last; ++x) {
+        const float* p = part_of(x);
+        const float keep = ex2_approx(p[kRows * kDim + r] - top);
+        sum += p[kRows * (kDim + 1) + r] * keep;
+        v += p[r * kDim + d] * keep;
+    }
+    const int t = row / a.share;
+    const int64_t to = static_cast<int64_t>(span.first + t) * c.heads + m.head * a.share + row - t * a.share;
+    static_cast<E*>(c.out)[to * kDim + d] = from_float<E>(v * row_inverse<E>(sum));
+    if (d == 0 && c.lse != nullptr) c.lse[to] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * (1.0f / kLog2e);
+}
+
+// How the few-rows kernel runs a call: row tiles, CTAs, workspace.
+struct FewPlan {
+    int tiles, grid, rows;
+    bool split;            // a unit may cross shares
+    int64_t meta_bytes, bytes;
+};
+
+FewPlan few_plan(const KvAttnCall& c, int sm_count) {
+    FewPlan p{};
+    const int64_t most = static_cast<int64_t>(c.batch.max_new) * (c.heads / c.cache.kv_heads);
+    p.tiles = most <= 8 ? 1 : most <= 16 ? 2 : 4;
+    p.rows = 8 * p.tiles;
+    p.grid = sm_count * (p.tiles == 4 && c.cache.dim == 128 ? 2 : 3);
+    p.split = c.max_len > kChunk;
+    p.meta_bytes = (static_cast<int64_t>(p.grid) * sizeof(Meta) + 255) / 256 * 256;
+    p.bytes = p.meta_bytes + static_cast<int64_t>(p.grid) * 2 * p.rows * (c.cache.dim + 2) * 4;
+    return p;
+}
+
+// Rows of one kv head beyond which the few-rows kernel is not taken.
+bool few_rows(const KvAttnCall& c) { return static_cast<int64_t>(c.batch.max_new) * (c.heads / c.cache.kv_heads) <= 64; }
+
+template <typename E, int kFmt, int kDim, int kTiles>
+cudaError_t launch_few(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, const FewPlan& p,
+                       cudaStream_t stream) {
+    static int attr_gen[64] = {};
+    constexpr int smem = Ring<kDim>::kBytes + 1024;
+    auto* kernel = attn_few_kernel<E, kFmt, kDim, kTiles>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && attr_gen[dev] != g_generation) {
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+        attr_gen[dev] = g_generation;
+    }
+    FewArgs a{};
+    a.c = c;
+    a.share = c.heads / c.cache.kv_heads;
+    a.least = 1;
+    a.grid = p.grid;
+    a.q_vec = reinterpret_cast<uintptr_t>(c.q.p) % 8 == 0 && c.q.token % 4 == 0 && c.q.head % 4 == 0;
+    a.meta = static_cast<Meta*>(workspace);
+    a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.meta_bytes);
+    while (c.cache.page >> (a.page_shift + 1)) ++a.page_shift;
+    kernel<<<p.grid, kThreads, smem, stream>>>(tmK, tmV, a);
+    if ((e = cudaGetLastError()) != cudaSuccess || !p.split) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.grid - 1, 8 * kTiles);
+    cfg.blockDim = dim3(kDim);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<E, kDim, 8 * kTiles>, a);
+}
+
+template <typename E, int kFmt, int kDim>
+cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count,
+                   cudaStream_t stream) {
+    if (few_rows(c)) {
+        const FewPlan p = few_plan(c, sm_count);
+        if (p.tiles == 1) return launch_few<E, kFmt, kDim, 1>(c, tmK, tmV, workspace, p, stream);
+        if (p.tiles == 2) return launch_few<E, kFmt, kDim, 2>(c, tmK, tmV, workspace, p, stream);
+        return launch_few<E, kFmt, kDim, 4>(c, tmK, tmV, workspace, p, stream);
+    }
     const int64_t rows = static_cast<int64_t>(c.batch.total) * c.heads;
-    const unsigned grid = static_cast<unsigned>((rows + kWarps - 1) / kWarps);
-    if (c.cache.dim == 128) attn_rows_kernel<E, kFmt, 128><<<grid, kWarps * 32, 0, stream>>>(c);
-    else attn_rows_kernel<E, kFmt, 64><<<grid, kWarps * 32, 0, stream>>>(c);
+    attn_rows_kernel<E, kFmt, kDim><<<static_cast<unsigned>((rows + kRowWarps - 1) / kRowWarps), kRowWarps * 32, 0, stream>>>(c);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-int64_t kv_attn_workspace(const KvAttnCall&, int) { return 0; }
+int kv_attn_box_rows(const KvAttnCall& c) { return kStep * c.cache.dim / 128; }
 
-cudaError_t launch_kv_attn(const KvAttnCall& c, void*, int, cudaStream_t stream) {
-    const bool h = c.dtype == kFp16, e4 = c.cache.fmt == kKvE4M3;
-    if (h && e4) return launch<__half, kKvE4M3>(c, stream);
-    if (h) return launch<__half, kKvInt8>(c, stream);
-    if (e4) return launch<__nv_bfloat16, kKvE4M3>(c, stream);
-    return launch<__nv_bfloat16, kKvInt8>(c, stream);
+int64_t kv_attn_workspace(const KvAttnCall& c, int sm_count) { return few_rows(c) ? few_plan(c, sm_count).bytes : 0; }
+
+cudaError_t launch_kv_attn(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count,
+                           cudaStream_t stream) {
+    const bool h = c.dtype == kFp16, e4 = c.cache.fmt == kKvE4M3, d128 = c.cache.dim == 128;
+    auto go = [&](auto* f) { return f(c, tmK, tmV, workspace, sm_count, stream); };
+    if (h && e4) return d128 ? go(launch<__half, kKvE4M3, 128>) : go(launch<__half, kKvE4M3, 64>);
+    if (h) return d128 ? go(launch<__half, kKvInt8, 128>) : go(launch<__half, kKvInt8, 64>);
+    if (e4) return d128 ? go(launch<__nv_bfloat16, kKvE4M3, 128>) : go(launch<__nv_bfloat16, kKvE4M3, 64>);
+    return d128 ? go(launch<__nv_bfloat16, kKvInt8, 128>) : go(launch<__nv_bfloat16, kKvInt8, 64>);
 }
 
 }  // namespace tg

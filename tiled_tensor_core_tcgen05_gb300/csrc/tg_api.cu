@@ -1378,6 +1378,8 @@ tg_status check_cache(const void* k, const void* v, const float* ks, const float
     if (pages < 0 || pages > kIntMax || kv_heads < 1 || kv_heads > 1024)
         return fail(TG_ERR_INVALID_ARG, "cache sizes out of range: pages=%lld kv_heads=%lld", (long long)pages,
                     (long long)kv_heads);
+    if (pages * kv_heads * page > kIntMax * 128 / dim)  // lines of 128 bytes are numbered in 31 bits
+        return fail(TG_ERR_INVALID_ARG, "the cache is too large: %lld pages", (long long)pages);
     if (pages > 0 && (!k || !v || !ks || !vs)) return fail(TG_ERR_INVALID_ARG, "a cache pointer is NULL");
     if (!(aligned(k, 16) && aligned(v, 16) && aligned(ks, 4) && aligned(vs, 4)))
         return fail(TG_ERR_INVALID_ARG, "cache codes must be 16-byte aligned and scales 4-byte aligned");
@@ -1649,6 +1651,12 @@ extern "C" tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int6
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return fail(TG_ERR_INVALID_ARG, "tg_attention_kv needs a workspace of %lld bytes, got %lld", (long long)need,
                     (long long)(workspace ? workspace_bytes : 0));
-    cudaError_t e = launch_kv_attn(c, workspace, g_dev[dev].sm_count, stream);
+    // the codes as lines of 128 bytes (a cache without pages is never read: any address serves)
+    const uint64_t lines = pages > 0 ? static_cast<uint64_t>(codes) / 128 : 1;
+    CUtensorMap tmK, tmV;
+    const uint32_t box = static_cast<uint32_t>(kv_attn_box_rows(c));
+    if ((st = make_map_u8(&tmK, pages > 0 ? k_cache : O, 128, lines, 128, box)) != TG_OK) return st;
+    if ((st = make_map_u8(&tmV, pages > 0 ? v_cache : O, 128, lines, 128, box)) != TG_OK) return st;
+    cudaError_t e = launch_kv_attn(c, tmK, tmV, workspace, g_dev[dev].sm_count, stream);
     return e == cudaSuccess ? TG_OK : cuda_fail(e, "cache attention kernel launch");
 }
