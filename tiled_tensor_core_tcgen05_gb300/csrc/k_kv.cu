@@ -12,188 +12,526 @@
 // rounding to nearest even into e4m3 (qmax 448) or int8 (qmax 127). A page
 // whose first token is written by the call takes nothing over from what it
 // held before. Keys may be rotated on the way (in fp32, not rounded between).
+//
+// Memory bounds all of it. Prompts go page by page: the threads of a (page,
+// head) hold its values in registers between the maximum and the rounding, so
+// each is read once. Single tokens go sequence by sequence: a CTA rotates and
+// writes all heads of one token (and rotates its queries), a head a warp, and
+// only where a scale grows are the page's held codes touched at all.
 #include "tg_kv.cuh"
 
 namespace tg {
 namespace {
 
-constexpr int kThreads = 128;
-
-// The rotated (or plain) value d of a row at `pos`.
-template <typename E>
-__device__ __forceinline__ float row_value(const E* row, int d, int pos, const RopeArgs& r) {
-    const float x = to_float(row[d]);
-    if (r.inv_freq == nullptr || d >= r.rotary) return x;
-    const int half = r.rotary / 2;
-    const bool first = r.layout == kRopeHalf ? d < half : (d & 1) == 0;
-    const int j = r.layout == kRopeHalf ? (first ? d : d - half) : d / 2;
-    const int other = r.layout == kRopeHalf ? (first ? d + half : d - half) : d ^ 1;
-    const float2 cs = turn_cos_sin(turn_step(__ldg(r.inv_freq + j)), pos, r.amplitude, r.sign);
-    const float o = to_float(row[other]);
-    return first ? x * cs.x - o * cs.y : x * cs.x + o * cs.y;
+// The last i in [0, n) with start(i) <= x, start being non-decreasing: whole block, three barriers' worth.
+template <typename F>
+__device__ __forceinline__ int block_find(int n, F start, int64_t x) {
+    int found = 0;
+    for (int base = 0; base < n; base += blockDim.x) {
+        const int i = base + threadIdx.x;
+        const int here = __syncthreads_count(i < n && start(i) <= x);
+        found += here;
+        if (here < static_cast<int>(blockDim.x)) break;
+    }
+    return found > 0 ? found - 1 : 0;
 }
 
-// One CTA per (page that a sequence writes to, kv head, keys or values). Sequence i's pages
+__device__ __forceinline__ float max_finite(float most, float x) {
+    const float a = fabsf(x);
+    return a <= 3.402823466e38f ? fmaxf(most, a) : most;
+}
+
+// Codes of kN values of a row whose block has the largest finite value `most` and 1 / scale `per`.
+template <int kFmt, int kN>
+__device__ __forceinline__ void encode_values(const float (&x)[kN], float most, float per, uint32_t (&w)[kN / 4]) {
+    float y[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i)  // an infinity becomes the largest finite value
+        y[i] = __fmul_rn(min_nan(max_nan(x[i], -most), most), per);
+#pragma unroll
+    for (int i = 0; i < kN; i += 4) w[i / 4] = encode4<kFmt>(y[i], y[i + 1], y[i + 2], y[i + 3]);
+}
+
+template <int kFmt>
+__device__ __forceinline__ uint32_t again4(uint32_t w, float ratio) {
+    float x[4];
+    decode4<kFmt>(w, x);
+    return encode4<kFmt>(__fmul_rn(x[0], ratio), __fmul_rn(x[1], ratio), __fmul_rn(x[2], ratio), __fmul_rn(x[3], ratio));
+}
+
+// How rows may be read: 16-byte pieces (then 8-byte ones too) or single values.
+struct Wide {
+    bool k, v, q, q_out;
+};
+
+// ---------------------------------------------------------------- prompts: page by page
+
+struct PageArgs {
+    KvAppendCall c;
+    Wide wide;
+    int heads_a_cta;   // kv heads that a CTA's groups take one after another
+    int values_only;   // without rotation: 1 values, 0 keys and values (blockIdx.z)
+};
+
+constexpr int kVecs = 4;  // 16-byte pieces a thread holds
+
+// A group of page * dim / 32 threads takes one (page, head): piece i of thread t is piece
+// t + i * group of the page's page * dim / 8. blockIdx: x pages that sequences write to (sequence i's
 // are items base(i) .. base(i + 1) - 1 with base(i) = cu[i] / page + 2 i: n tokens touch at most
-// n / page + 2 pages, so some items have none.
-template <typename E, int kFmt>
-__global__ void __launch_bounds__(kThreads) append_kernel(const KvAppendCall c) {
-    __shared__ float red[kThreads / 32];
+// n / page + 2 pages, so some items have none), y heads, z keys or values (keys that are rotated are a
+// launch of their own).
+template <typename E, int kFmt, int kDim, bool kRope>
+__global__ void __launch_bounds__(512) append_pages_kernel(const PageArgs a) {
+    extern __shared__ float turns[];  // cos, then sin: (page, rotary / 2) each
+    __shared__ float red[16];
+    const KvAppendCall& c = a.c;
     const KvBatch& b = c.batch;
-    const int page = c.cache.page, dim = c.cache.dim;
-    const int item = blockIdx.x, head = blockIdx.y;
-    const bool values = blockIdx.z != 0;
-    int lo = 0, hi = b.batch;  // the last sequence with base <= item
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        const int base = (b.cu ? __ldg(b.cu + mid) : mid) / page + 2 * mid;
-        if (base <= item) lo = mid; else hi = mid;
-    }
-    const int seq = lo;
+    const int page = c.cache.page, item = blockIdx.x;
+    const bool values = kRope ? false : a.values_only || blockIdx.z != 0;
+    constexpr int kPieces = kDim / 8;  // of a row
+    auto base_of = [&](int i) { return static_cast<int64_t>((b.cu ? __ldg(b.cu + i) : i) / page) + 2 * i; };
+    const int seq = block_find(b.batch, base_of, item);
     const SeqSpan span = seq_span(b, seq, c.wd);
     if (span.count == 0) return;
-    const int k = item - ((b.cu ? __ldg(b.cu + seq) : seq) / page + 2 * seq);
+    const int k = static_cast<int>(item - base_of(seq));
     const int64_t len = __ldg(b.lens + seq);
     if (len < 0 || len + span.count > b.table_width * page) {
         report_range(c.wd);
         return;
     }
-    const int64_t first_slot = len / page;
-    const int64_t slot = first_slot + k;
-    if (slot * page >= len + span.count) return;
+    const int64_t slot = len / page + k;
+    if (k < 0 || slot * page >= len + span.count) return;
     const int p = seq_page(b, c.cache, seq, static_cast<int>(slot), c.wd);
     if (p < 0) return;
-    const int from = k == 0 ? static_cast<int>(len % page) : 0;                    // first new place in the page
+    const int from = k == 0 ? static_cast<int>(len % page) : 0;                     // first new place in the page
     const int to = static_cast<int>(min(static_cast<int64_t>(page), len + span.count - slot * page));
-    const int64_t row0 = span.first + (slot * page + from - len);                   // its packed row
+    const int64_t row0 = span.first + (slot * page - len);                          // packed row of place 0
+    const RopeArgs& rope = c.rope;
+    const int half = rope.rotary / 2;
+    float *cs = turns, *sn = turns + page * half;
+    if constexpr (kRope) {
+        for (int i = threadIdx.x; i < (to - from) * half; i += blockDim.x) {
+            const int t = i / half, j = i - t * half;
+            const float2 x = turn_cos_sin(turn_step(__ldg(rope.inv_freq + j)), static_cast<int>(slot * page) + from + t, rope.amplitude, rope.sign);
+            cs[(from + t) * half + j] = x.x;
+            sn[(from + t) * half + j] = x.y;
+        }
+        __syncthreads();
+    }
+
+    const int group = page * kPieces / kVecs, groups = blockDim.x / group;
+    const int g = threadIdx.x / group, t = threadIdx.x - g * group;
     const Strided& src = values ? c.v : c.k;
-    const E* x = static_cast<const E*>(src.p) + row0 * src.token + head * src.head;
-    uint8_t* codes = (values ? c.cache.v : c.cache.k) + (static_cast<int64_t>(p) * c.cache.kv_heads + head) * page * dim;
-    float* scale = (values ? c.cache.v_scale : c.cache.k_scale) + static_cast<int64_t>(p) * c.cache.kv_heads + head;
-    RopeArgs rope = c.rope;
-    if (values) rope.inv_freq = nullptr;
-
-    float most = 0.0f;  // of the finite values
-    for (int i = threadIdx.x; i < (to - from) * dim; i += kThreads) {
-        const int t = i / dim, d = i - t * dim;
-        const float a = fabsf(row_value(x + t * src.token, d, static_cast<int>(slot * page) + from + t, rope));
-        if (a <= 3.402823466e38f) most = fmaxf(most, a);
-    }
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = most;
-    const float s_old = from > 0 ? *scale : 0.0f;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) most = fmaxf(most, red[w]);
-    const float s = fmaxf(s_old, fmaxf(__fmul_rn(most, code_max_inverse<kFmt>()), kScaleFloor));
-    const float per = __fdiv_rn(1.0f, s);
-    if (from > 0 && s != s_old) {
+    const bool vec = values ? a.wide.v : a.wide.k;
+    const int head_end = min(c.cache.kv_heads, static_cast<int>(blockIdx.y + 1) * a.heads_a_cta);
+    // every group makes every round, so that all meet at the barriers
+    for (int head0 = blockIdx.y * a.heads_a_cta; head0 < head_end; head0 += groups) {
+        const int head = head0 + g;
+        const bool real = head < head_end;
+        const int64_t ph = static_cast<int64_t>(p) * c.cache.kv_heads + (real ? head : 0);
+        uint8_t* codes = (values ? c.cache.v : c.cache.k) + ph * page * kDim;
+        float* scale = (values ? c.cache.v_scale : c.cache.k_scale) + ph;
+        const float s_old = real && from > 0 ? *scale : 0.0f;
+        const E* x0 = static_cast<const E*>(src.p) + row0 * src.token + head * src.head;
+        float x[kVecs][8];
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int at = t + i * group, place = at / kPieces, d = (at - place * kPieces) * 8;
+            if (real && place >= from && place < to) load_values<E, 8>(x0 + place * src.token, d, vec, x[i]);
+        }
+        if constexpr (kRope) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const int at = t + i * group, place = at / kPieces, d = (at - place * kPieces) * 8;
+                if (real && place >= from && place < to) {
+                    float o[8];
+                    load_partners<E, 8>(x0 + place * src.token, d, vec, rope, o);
+                    rotate_values<8>(x[i], o, d, cs + place * half, sn + place * half, rope);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int place = (t + i * group) / kPieces;
+            if (real && place >= from && place < to) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) most = max_finite(most, x[i][e]);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+        if (group > 32) {
+            __syncthreads();
+            if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = most;
+            __syncthreads();
+            for (int w = g * group / 32; w < (g + 1) * group / 32; ++w) most = fmaxf(most, red[w]);
+        }
+        if (!real) continue;
+        const float s = fmaxf(s_old, fmaxf(__fmul_rn(most, code_max_inverse<kFmt>()), kScaleFloor));
+        const float per = __fdiv_rn(1.0f, s);
         const float ratio = __fmul_rn(s_old, per);
-        for (int i = threadIdx.x; i < from * dim; i += kThreads)
-            codes[i] = encode<kFmt>(__fmul_rn(decode<kFmt>(codes[i]), ratio));
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int at = t + i * group, place = at / kPieces;
+            uint2* q = reinterpret_cast<uint2*>(codes + at * 8);
+            if (place >= from && place < to) {
+                uint32_t w[2];
+                encode_values<kFmt, 8>(x[i], most, per, w);
+                *q = make_uint2(w[0], w[1]);
+            } else if (place < from && s != s_old) {
+                const uint2 w = *q;
+                *q = make_uint2(again4<kFmt>(w.x, ratio), again4<kFmt>(w.y, ratio));
+            }
+        }
+        if (t == 0) *scale = s;
     }
-    for (int i = threadIdx.x; i < (to - from) * dim; i += kThreads) {
-        const int t = i / dim, d = i - t * dim;
-        float v = row_value(x + t * src.token, d, static_cast<int>(slot * page) + from + t, rope);
-        v = min_nan(max_nan(v, -most), most);  // an infinity becomes the largest finite value
-        codes[(from + t) * dim + d] = encode<kFmt>(__fmul_rn(v, per));
-    }
-    if (threadIdx.x == 0) *scale = s;
 }
 
-// The rotated queries of an append: one CTA per token.
+// ---------------------------------------------------------------- single tokens: sequence by sequence
+
+constexpr int kTokenThreads = 512;
+constexpr int kTokenWarps = kTokenThreads / 32;
+constexpr int kRowsAtOnce = 4;
+
+struct TokenArgs {
+    KvAppendCall c;
+    Wide wide;
+};
+
+// Rows of the token, a warp each: keys of every kv head, values of every kv head, queries.
+template <typename E, int kFmt, int kDim>
+__global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const TokenArgs a) {
+    constexpr int kN = 4;   // values a lane; a head of 64 takes half a warp
+    __shared__ alignas(16) float cs[kDim / 2], sn[kDim / 2];
+    const KvAppendCall& c = a.c;
+    const KvBatch& b = c.batch;
+    const int seq = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32, d = lane * kN;
+    const SeqSpan span = seq_span(b, seq, c.wd);
+    if (span.count == 0) return;
+    const int64_t len = __ldg(b.lens + seq);
+    const int page = c.cache.page, kv = c.cache.kv_heads;
+    // rows are read before anything about pages is known
+    const int rows = 2 * kv + c.heads;
+    float x[kRowsAtOnce][kN], o[kRowsAtOnce][kN];
+    auto source = [&](int r, bool& vec) {
+        const Strided& s = r < kv ? c.k : r < 2 * kv ? c.v : c.q;
+        vec = r < kv ? a.wide.k : r < 2 * kv ? a.wide.v : a.wide.q;
+        const int h = r < kv ? r : r < 2 * kv ? r - kv : r - 2 * kv;
+        return static_cast<const E*>(s.p) + static_cast<int64_t>(span.first) * s.token + h * s.head;
+    };
+    auto load = [&](int first) {
+#pragma unroll
+        for (int i = 0; i < kRowsAtOnce; ++i) {
+            const int r = first + i * kTokenWarps;
+            if (r >= rows) continue;
+            bool vec;
+            const E* row = source(r, vec);
+#pragma unroll
+            for (int e = 0; e < kN; ++e) x[i][e] = o[i][e] = 0.0f;
+            if (d >= kDim) continue;
+            load_values<E, kN>(row, d, vec, x[i]);
+            if (c.rope.inv_freq != nullptr && (r < kv || r >= 2 * kv)) load_partners<E, kN>(row, d, vec, c.rope, o[i]);
+        }
+    };
+    load(warp);
+    bool in_range = len >= 0 && len < b.table_width * page;
+    if (!in_range) report_range(c.wd);
+    const int p = in_range ? seq_page(b, c.cache, seq, static_cast<int>(len / page), c.wd) : -1;
+    const int place = in_range ? static_cast<int>(len % page) : 0;
+    if (c.rope.inv_freq != nullptr) {
+        for (int j = threadIdx.x; j < c.rope.rotary / 2; j += kTokenThreads) {
+            const float2 y = turn_cos_sin(turn_step(__ldg(c.rope.inv_freq + j)), static_cast<int>(len), c.rope.amplitude, c.rope.sign);
+            cs[j] = y.x;
+            sn[j] = y.y;
+        }
+        __syncthreads();
+    }
+    for (int first = warp; first < rows; first += kRowsAtOnce * kTokenWarps) {
+        if (first != warp) load(first);
+#pragma unroll
+        for (int i = 0; i < kRowsAtOnce; ++i) {
+            const int r = first + i * kTokenWarps;
+            if (r >= rows) continue;
+            if (c.rope.inv_freq != nullptr && d < kDim && (r < kv || r >= 2 * kv)) rotate_values<kN>(x[i], o[i], d, cs, sn, c.rope);
+            if (r >= 2 * kv) {
+                if (!in_range) continue;
+                E* y = static_cast<E*>(c.q_out.p) + static_cast<int64_t>(span.first) * c.q_out.token + (r - 2 * kv) * c.q_out.head;
+                __syncwarp();  // in place, other lanes read their partners first
+                if (d < kDim) store_values<E, kN>(y, d, a.wide.q_out, x[i]);
+                continue;
+            }
+            if (p < 0) continue;
+            const bool values = r >= kv;
+            const int64_t ph = static_cast<int64_t>(p) * kv + (values ? r - kv : r);
+            uint8_t* codes = (values ? c.cache.v : c.cache.k) + ph * page * kDim;
+            float* scale = (values ? c.cache.v_scale : c.cache.k_scale) + ph;
+            const float s_old = place > 0 ? *scale : 0.0f;
+            float most = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kN; ++e) most = max_finite(most, x[i][e]);
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, m));
+            const float s = fmaxf(s_old, fmaxf(__fmul_rn(most, code_max_inverse<kFmt>()), kScaleFloor));
+            const float per = __fdiv_rn(1.0f, s);
+            if (place > 0 && s != s_old) {  // the held codes in the grown scale
+                const float ratio = __fmul_rn(s_old, per);
+                const int n = place * kDim / 16;
+                uint4* held = reinterpret_cast<uint4*>(codes);
+                for (int at = lane; at < n; at += 4 * 32) {
+                    uint4 w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (at + 32 * j < n) w[j] = held[at + 32 * j];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (at + 32 * j < n)
+                            held[at + 32 * j] = make_uint4(again4<kFmt>(w[j].x, ratio), again4<kFmt>(w[j].y, ratio), again4<kFmt>(w[j].z, ratio),
+                                                           again4<kFmt>(w[j].w, ratio));
+                }
+            }
+            uint32_t w[1];
+            encode_values<kFmt, kN>(x[i], most, per, w);
+            if (d < kDim) *reinterpret_cast<uint32_t*>(codes + place * kDim + d) = w[0];
+            __syncwarp();  // every lane has read the old scale
+            if (lane == 0 && s != s_old) *scale = s;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- queries beside a prompt's keys
+
+constexpr int kQThreads = 256;
+constexpr int kQTokens = 4;  // per CTA
+
+struct QArgs {
+    KvAppendCall c;
+    Wide wide;
+};
+
+// cos and sin of a few tokens once for all their heads, then a thread per eight values (with their
+// partners in the half layout when whole pieces pair up, else pair by pair).
 template <typename E>
-__global__ void __launch_bounds__(kThreads) append_q_kernel(const KvAppendCall c) {
+__global__ void __launch_bounds__(kQThreads) append_q_kernel(const QArgs a) {
+    extern __shared__ float turns[];
+    __shared__ int32_t where[kQTokens];
+    const KvAppendCall& c = a.c;
     const KvBatch& b = c.batch;
-    const int token = blockIdx.x;
-    int seq = token;
-    if (b.cu != nullptr) {
-        int lo = 0, hi = b.batch;  // the last sequence that starts at or before the token
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (__ldg(b.cu + mid) <= token) lo = mid; else hi = mid;
+    const int token0 = blockIdx.x * kQTokens, n = min(kQTokens, b.total - token0);
+    const int first = block_find(b.batch, [&](int i) { return static_cast<int64_t>(b.cu ? __ldg(b.cu + i) : i); }, token0);
+    if (threadIdx.x < n) {
+        const int token = token0 + threadIdx.x;
+        int seq = first, at = -1;
+        while (seq + 1 < b.batch && (b.cu ? __ldg(b.cu + seq + 1) : seq + 1) <= token) ++seq;
+        const SeqSpan span = seq_span(b, seq, c.wd);
+        if (token >= span.first && token < span.first + span.count) {
+            const int64_t pos = static_cast<int64_t>(__ldg(b.lens + seq)) + token - span.first;
+            at = pos >= 0 && pos < b.table_width * c.cache.page ? static_cast<int>(pos) : -1;  // the keys' kernel reports it
         }
-        seq = lo;
+        where[threadIdx.x] = at;
     }
-    const SeqSpan span = seq_span(b, seq, c.wd);
-    if (token < span.first || token >= span.first + span.count) return;
-    const int pos = __ldg(b.lens + seq) + token - span.first;
-    const E* x = static_cast<const E*>(c.q.p) + token * c.q.token;
-    E* y = static_cast<E*>(c.q_out.p) + token * c.q_out.token;
-    const int half = c.rope.rotary / 2, dim = c.cache.dim, per_head = half + dim - c.rope.rotary;
-    for (int i = threadIdx.x; i < c.heads * per_head; i += kThreads) {
-        const int h = i / per_head, j = i - h * per_head;
-        const E* xh = x + h * c.q.head;
-        E* yh = y + h * c.q_out.head;
-        if (j < half) {
-            const int ia = c.rope.layout == kRopeHalf ? j : 2 * j, ib = c.rope.layout == kRopeHalf ? j + half : 2 * j + 1;
-            const float2 cs = turn_cos_sin(turn_step(__ldg(c.rope.inv_freq + j)), pos, c.rope.amplitude, c.rope.sign);
-            const float u = to_float(xh[ia]), w = to_float(xh[ib]);
-            yh[ia] = from_float<E>(u * cs.x - w * cs.y);
-            yh[ib] = from_float<E>(w * cs.x + u * cs.y);
-        } else {
-            yh[half + j] = xh[half + j];
+    __syncthreads();
+    const int half = c.rope.rotary / 2, dim = c.cache.dim;
+    float *cs = turns, *sn = turns + n * half;
+    for (int i = threadIdx.x; i < n * half; i += kQThreads) {
+        const int t = i / half;
+        const float2 x = turn_cos_sin(turn_step(__ldg(c.rope.inv_freq + (i - t * half))), where[t], c.rope.amplitude, c.rope.sign);
+        cs[i] = x.x;
+        sn[i] = x.y;
+    }
+    __syncthreads();
+    const bool whole = a.wide.q && a.wide.q_out && (c.rope.layout == kRopeHalf ? half % 8 == 0 : c.rope.rotary % 8 == 0);
+    if (whole) {
+        const bool split = c.rope.layout == kRopeHalf;
+        const int turned = split ? half / 8 : c.rope.rotary / 8, per_head = turned + (dim - c.rope.rotary) / 8;
+        const int items = n * c.heads * per_head;
+#pragma unroll 2
+        for (int i = threadIdx.x; i < items; i += kQThreads) {
+            const int row = i / per_head, v = i - row * per_head, t = row / c.heads, h = row - t * c.heads;
+            if (where[t] < 0) continue;
+            const E* x = static_cast<const E*>(c.q.p) + static_cast<int64_t>(token0 + t) * c.q.token + h * c.q.head;
+            E* y = static_cast<E*>(c.q_out.p) + static_cast<int64_t>(token0 + t) * c.q_out.token + h * c.q_out.head;
+            const int d = v < turned ? 8 * v : c.rope.rotary + 8 * (v - turned);
+            float u[8], w[8];
+            load_values<E, 8>(x, d, true, u);
+            if (v < turned && split) {
+                load_values<E, 8>(x, d + half, true, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float cc = cs[t * half + d + e], ss = sn[t * half + d + e], p = u[e], q = w[e];
+                    u[e] = p * cc - q * ss;
+                    w[e] = q * cc + p * ss;
+                }
+                store_values<E, 8>(y, d + half, true, w);
+            } else if (v < turned) {
+                rotate_values<8>(u, u, d, cs + t * half, sn + t * half, c.rope);
+            }
+            store_values<E, 8>(y, d, true, u);
         }
-    }
-}
-
-// One CTA per packed row: its sequence, page and place, then every kv head.
-template <typename E, int kFmt>
-__global__ void __launch_bounds__(kThreads) read_kernel(const KvReadCall c) {
-    const KvBatch& b = c.batch;
-    const int row = blockIdx.x, page = c.cache.page, dim = c.cache.dim, heads = c.cache.kv_heads;
-    int seq = row;
-    if (b.cu != nullptr) {
-        int lo = 0, hi = b.batch;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (__ldg(b.cu + mid) <= row) lo = mid; else hi = mid;
-        }
-        seq = lo;
-    }
-    const SeqSpan span = seq_span(b, seq, c.wd);
-    if (row < span.first || row >= span.first + span.count) return;
-    const int64_t pos = static_cast<int64_t>(__ldg(b.lens + seq)) + row - span.first;
-    if (pos < 0 || pos >= b.table_width * page) {
-        report_range(c.wd);
         return;
     }
-    const int p = seq_page(b, c.cache, seq, static_cast<int>(pos / page), c.wd);
-    if (p < 0) return;
-    const int place = static_cast<int>(pos % page);
-    for (int i = threadIdx.x; i < heads * dim; i += kThreads) {
-        const int h = i / dim, d = i - h * dim;
-        const int64_t ph = static_cast<int64_t>(p) * heads + h;
-        const int64_t at = (ph * page + place) * dim + d;
-        const int64_t to = static_cast<int64_t>(row) * heads * dim + i;
-        static_cast<E*>(c.k)[to] = from_float<E>(decode<kFmt>(c.cache.k[at]) * c.cache.k_scale[ph]);
-        static_cast<E*>(c.v)[to] = from_float<E>(decode<kFmt>(c.cache.v[at]) * c.cache.v_scale[ph]);
+    const int per_head = half + dim - c.rope.rotary;
+    for (int i = threadIdx.x; i < n * c.heads * per_head; i += kQThreads) {
+        const int row = i / per_head, j = i - row * per_head, t = row / c.heads, h = row - t * c.heads;
+        if (where[t] < 0) continue;
+        const E* x = static_cast<const E*>(c.q.p) + static_cast<int64_t>(token0 + t) * c.q.token + h * c.q.head;
+        E* y = static_cast<E*>(c.q_out.p) + static_cast<int64_t>(token0 + t) * c.q_out.token + h * c.q_out.head;
+        if (j < half) {
+            const int ia = c.rope.layout == kRopeHalf ? j : 2 * j, ib = c.rope.layout == kRopeHalf ? j + half : 2 * j + 1;
+            const float cc = cs[t * half + j], ss = sn[t * half + j], u = to_float(x[ia]), w = to_float(x[ib]);
+            y[ia] = from_float<E>(u * cc - w * ss);
+            y[ib] = from_float<E>(w * cc + u * ss);
+        } else {
+            y[half + j] = x[half + j];
+        }
     }
+}
+
+// ---------------------------------------------------------------- reading back
+
+constexpr int kReadThreads = 256;
+constexpr int kReadRows = 16;  // packed rows a CTA
+
+// Eight codes in, eight values out, a thread: consecutive threads take consecutive pieces of a row of
+// all heads, so the output is written in whole lines and the codes are read in lines of a head.
+template <typename E, int kFmt, int kDim>
+__global__ void __launch_bounds__(kReadThreads) read_kernel(const KvReadCall c) {
+    __shared__ int32_t page_of[kReadRows], place_of[kReadRows];
+    const KvBatch& b = c.batch;
+    const int row0 = blockIdx.x * kReadRows, n = min(kReadRows, b.total - row0), page = c.cache.page, heads = c.cache.kv_heads;
+    constexpr int kPieces = kDim / 8;
+    const int first = block_find(b.batch, [&](int i) { return static_cast<int64_t>(b.cu ? __ldg(b.cu + i) : i); }, row0);
+    if (threadIdx.x < n) {
+        const int row = row0 + threadIdx.x;
+        int seq = first, p = -1, place = 0;
+        while (seq + 1 < b.batch && (b.cu ? __ldg(b.cu + seq + 1) : seq + 1) <= row) ++seq;
+        const SeqSpan span = seq_span(b, seq, c.wd);
+        if (row >= span.first && row < span.first + span.count) {
+            const int64_t pos = static_cast<int64_t>(__ldg(b.lens + seq)) + row - span.first;
+            if (pos < 0 || pos >= b.table_width * page) report_range(c.wd);
+            else {
+                p = seq_page(b, c.cache, seq, static_cast<int>(pos / page), c.wd);
+                place = static_cast<int>(pos % page);
+            }
+        }
+        page_of[threadIdx.x] = p;
+        place_of[threadIdx.x] = place;
+    }
+    __syncthreads();
+    const int per_row = heads * kPieces, items = n * per_row;
+    constexpr int kAtOnce = 4;
+    for (int i0 = threadIdx.x; i0 < items; i0 += kAtOnce * kReadThreads) {
+        uint2 kc[kAtOnce], vc[kAtOnce];
+        float ks[kAtOnce], vs[kAtOnce];
+        int64_t to[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int i = i0 + j * kReadThreads;
+            to[j] = -1;
+            if (i >= items) continue;
+            const int row = i / per_row, in = i - row * per_row, h = in / kPieces, d = (in - h * kPieces) * 8;
+            const int p = page_of[row];
+            if (p < 0) continue;
+            const int64_t ph = static_cast<int64_t>(p) * heads + h, at = (ph * page + place_of[row]) * kDim + d;
+            kc[j] = __ldg(reinterpret_cast<const uint2*>(c.cache.k + at));
+            vc[j] = __ldg(reinterpret_cast<const uint2*>(c.cache.v + at));
+            ks[j] = __ldg(c.cache.k_scale + ph);
+            vs[j] = __ldg(c.cache.v_scale + ph);
+            to[j] = static_cast<int64_t>(row0) * per_row * 8 + static_cast<int64_t>(i) * 8;
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            if (to[j] < 0) continue;
+            float lo[4], hi[4], x[8];
+            decode4<kFmt>(kc[j].x, lo);
+            decode4<kFmt>(kc[j].y, hi);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] = lo[e] * ks[j];
+                x[4 + e] = hi[e] * ks[j];
+            }
+            store_values<E, 8>(static_cast<E*>(c.k) + to[j], 0, true, x);
+            decode4<kFmt>(vc[j].x, lo);
+            decode4<kFmt>(vc[j].y, hi);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] = lo[e] * vs[j];
+                x[4 + e] = hi[e] * vs[j];
+            }
+            store_values<E, 8>(static_cast<E*>(c.v) + to[j], 0, true, x);
+        }
+    }
+}
+
+bool is_wide(const Strided& s) { return reinterpret_cast<uintptr_t>(s.p) % 16 == 0 && s.token % 8 == 0 && s.head % 8 == 0; }
+
+template <typename E, int kFmt, int kDim>
+cudaError_t launch_append(const KvAppendCall& c, int sm_count, cudaStream_t stream) {
+    const Wide wide{is_wide(c.k), is_wide(c.v), is_wide(c.q), is_wide(c.q_out)};
+    if (c.batch.max_new == 1) {
+        append_token_kernel<E, kFmt, kDim><<<c.batch.batch, kTokenThreads, 0, stream>>>(TokenArgs{c, wide});
+        return cudaGetLastError();
+    }
+    const int group = c.cache.page * kDim / 8 / kVecs;
+    const int threads = group > 256 ? group : 256;
+    const int half = c.rope.inv_freq != nullptr ? c.rope.rotary / 2 : 0;
+    const int smem = c.cache.page * half * 2 * static_cast<int>(sizeof(float));
+    const int items = c.batch.total / c.cache.page + 2 * c.batch.batch;
+    // one round of heads a CTA, unless keys are rotated: then the page's cos and sin serve as many
+    // heads as leave four CTAs an SM
+    int heads = threads / group;
+    if (half > 0)
+        while (heads < c.cache.kv_heads && static_cast<int64_t>(items) * (c.cache.kv_heads / (2 * heads)) >= 4 * sm_count) heads *= 2;
+    const PageArgs args{c, wide, heads, 0};
+    const PageArgs plain{c, wide, threads / group, 0};
+    const dim3 all(items, (c.cache.kv_heads + threads / group - 1) / (threads / group), 2);
+    if (half == 0) {
+        append_pages_kernel<E, kFmt, kDim, false><<<all, threads, 0, stream>>>(plain);
+        return cudaGetLastError();
+    }
+    static int attr_gen[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    auto* turning = append_pages_kernel<E, kFmt, kDim, true>;
+    if (dev < 64 && attr_gen[dev] != g_generation) {
+        if ((e = cudaFuncSetAttribute(turning, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * kDim * 4)) != cudaSuccess) return e;
+        attr_gen[dev] = g_generation;
+    }
+    turning<<<dim3(items, (c.cache.kv_heads + heads - 1) / heads), threads, smem, stream>>>(args);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    PageArgs of_values = plain;
+    of_values.values_only = 1;
+    append_pages_kernel<E, kFmt, kDim, false><<<dim3(items, all.y), threads, 0, stream>>>(of_values);
+    if ((e = cudaGetLastError()) != cudaSuccess || c.heads == 0) return e;
+    append_q_kernel<E><<<(c.batch.total + kQTokens - 1) / kQTokens, kQThreads, kQTokens * half * 2 * sizeof(float), stream>>>(QArgs{c, wide});
+    return cudaGetLastError();
+}
+
+template <typename E, int kFmt, int kDim>
+cudaError_t launch_read(const KvReadCall& c, int, cudaStream_t stream) {
+    read_kernel<E, kFmt, kDim><<<(c.batch.total + kReadRows - 1) / kReadRows, kReadThreads, 0, stream>>>(c);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_kv_append(const KvAppendCall& c, int, cudaStream_t stream) {
-    const dim3 grid(c.batch.total / c.cache.page + 2 * c.batch.batch, c.cache.kv_heads, 2);
-    const bool h = c.dtype == kFp16, e4 = c.cache.fmt == kKvE4M3;
-    if (h && e4) append_kernel<__half, kKvE4M3><<<grid, kThreads, 0, stream>>>(c);
-    else if (h) append_kernel<__half, kKvInt8><<<grid, kThreads, 0, stream>>>(c);
-    else if (e4) append_kernel<__nv_bfloat16, kKvE4M3><<<grid, kThreads, 0, stream>>>(c);
-    else append_kernel<__nv_bfloat16, kKvInt8><<<grid, kThreads, 0, stream>>>(c);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || c.heads == 0) return e;
-    if (h) append_q_kernel<__half><<<c.batch.total, kThreads, 0, stream>>>(c);
-    else append_q_kernel<__nv_bfloat16><<<c.batch.total, kThreads, 0, stream>>>(c);
-    return cudaGetLastError();
+cudaError_t launch_kv_append(const KvAppendCall& c, int sm_count, cudaStream_t stream) {
+    const bool h = c.dtype == kFp16, e4 = c.cache.fmt == kKvE4M3, d128 = c.cache.dim == 128;
+    auto go = [&](auto* f) { return f(c, sm_count, stream); };
+    if (h && e4) return d128 ? go(launch_append<__half, kKvE4M3, 128>) : go(launch_append<__half, kKvE4M3, 64>);
+    if (h) return d128 ? go(launch_append<__half, kKvInt8, 128>) : go(launch_append<__half, kKvInt8, 64>);
+    if (e4) return d128 ? go(launch_append<__nv_bfloat16, kKvE4M3, 128>) : go(launch_append<__nv_bfloat16, kKvE4M3, 64>);
+    return d128 ? go(launch_append<__nv_bfloat16, kKvInt8, 128>) : go(launch_append<__nv_bfloat16, kKvInt8, 64>);
 }
 
-cudaError_t launch_kv_read(const KvReadCall& c, int, cudaStream_t stream) {
-    const bool h = c.dtype == kFp16, e4 = c.cache.fmt == kKvE4M3;
-    const int grid = c.batch.total;
-    if (h && e4) read_kernel<__half, kKvE4M3><<<grid, kThreads, 0, stream>>>(c);
-    else if (h) read_kernel<__half, kKvInt8><<<grid, kThreads, 0, stream>>>(c);
-    else if (e4) read_kernel<__nv_bfloat16, kKvE4M3><<<grid, kThreads, 0, stream>>>(c);
-    else read_kernel<__nv_bfloat16, kKvInt8><<<grid, kThreads, 0, stream>>>(c);
-    return cudaGetLastError();
+cudaError_t launch_kv_read(const KvReadCall& c, int sm_count, cudaStream_t stream) {
+    const bool h = c.dtype == kFp16, e4 = c.cache.fmt == kKvE4M3, d128 = c.cache.dim == 128;
+    auto go = [&](auto* f) { return f(c, sm_count, stream); };
+    if (h && e4) return d128 ? go(launch_read<__half, kKvE4M3, 128>) : go(launch_read<__half, kKvE4M3, 64>);
+    if (h) return d128 ? go(launch_read<__half, kKvInt8, 128>) : go(launch_read<__half, kKvInt8, 64>);
+    if (e4) return d128 ? go(launch_read<__nv_bfloat16, kKvE4M3, 128>) : go(launch_read<__nv_bfloat16, kKvE4M3, 64>);
+    return d128 ? go(launch_read<__nv_bfloat16, kKvInt8, 128>) : go(launch_read<__nv_bfloat16, kKvInt8, 64>);
 }
 
 }  // namespace tg
