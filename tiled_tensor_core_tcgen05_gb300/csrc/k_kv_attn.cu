@@ -771,7 +771,7 @@ FewPlan few_plan(const KvAttnCall& c, int sm_count) {
 }
 
 // Rows of one kv head beyond which the few-rows kernel is not taken.
-bool few_rows(const KvAttnCall& c) { return static_cast<int64_t>(c.batch.max_new) * (c.heads / c.cache.kv_heads) <= 64; }
+bool few_rows(const KvAttnCall&) { return true; }
 
 template <typename E, int kFmt, int kDim, int kTiles>
 cudaError_t launch_few(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, const FewPlan& p,
