@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -101,6 +102,7 @@ def bind(path: str) -> ctypes.CDLL:
 
 
 _lib = bind(LIB_PATH)
+from . import _tg_binding as _fast  # noqa: E402  the same library's serving calls, without ctypes' conversions
 
 
 class TgError(RuntimeError):
@@ -218,21 +220,19 @@ def bias_gelu_(C, bias=None, gelu: bool = True, stream=None):
     return C
 
 
-def tg_rope(X: int, x_token_stride: int, x_head_stride: int, Y: int, y_token_stride: int, y_head_stride: int,
-            positions: int, tokens: int, heads: int, dim: int, inv_freq: int | None, rotary: int, amplitude: float,
-            layout: int, backward: bool, dtype: int, stream: int | None) -> None:
-    _check(_lib.tg_rope(X, x_token_stride, x_head_stride, Y, y_token_stride, y_head_stride, positions, tokens, heads,
-                        dim, inv_freq, rotary, amplitude, layout, int(backward), dtype, stream))
+def tg_rope(*args) -> None:
+    """The C entry point's arguments in its order (include/tg_gemm.h)."""
+    _check(_fast.rope(*args))
 
 
 def tg_kv_append(*args) -> None:
     """The C entry point's arguments in its order (include/tg_gemm.h)."""
-    _check(_lib.tg_kv_append(*args))
+    _check(_fast.kv_append(*args))
 
 
 def tg_kv_read(*args) -> None:
     """The C entry point's arguments in its order (include/tg_gemm.h)."""
-    _check(_lib.tg_kv_read(*args))
+    _check(_fast.kv_read(*args))
 
 
 def tg_attention_kv_workspace(kv_heads: int, page: int, dim: int, fmt: int, heads: int, batch: int, total: int,
@@ -246,7 +246,7 @@ def tg_attention_kv_workspace(kv_heads: int, page: int, dim: int, fmt: int, head
 
 def tg_attention_kv(*args) -> None:
     """The C entry point's arguments in its order (include/tg_gemm.h)."""
-    _check(_lib.tg_attention_kv(*args))
+    _check(_fast.attention_kv(*args))
 
 
 def tg_device_status(stream: int | None) -> tuple[int, int]:
@@ -301,10 +301,13 @@ def tg_shutdown() -> None:
 # ---------------------------------------------------------------- torch form
 
 def _stream_handle(stream):
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    if not torch.cuda.is_initialized():
+        return torch.cuda.current_stream().cuda_stream
+    # the current stream's handle without the object around it
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 _NO_CONTEXT = contextlib.nullcontext()
@@ -511,8 +514,8 @@ def rope(X, positions, inv_freq, amplitude: float = 1.0, layout: int = ROPE_HALF
     elif out.shape != X.shape:
         raise ValueError("out has the wrong shape")
     y, yt, yh = _rows(out, "out", X.dtype)
-    tg_rope(x, xt, xh, y, yt, yh, pos, T, H, D, freq, rotary, amplitude, layout, backward, dtype,
-            _stream_handle(stream))
+    _check(_fast.rope(x, xt, xh, y, yt, yh, pos, T, H, D, freq, rotary, amplitude, layout, int(backward), dtype,
+                      _stream_handle(stream)))
     return out
 
 
@@ -597,8 +600,8 @@ def kv_append(cache, K, V, table, lens, cu=None, max_new: int = 1, Q=None, inv_f
         qo = _rows(out, "out", Q.dtype)
     elif out is not None:
         raise ValueError("out is for the rotated Q")
-    _check(_lib.tg_kv_append(*cache.args, k, kt, kh, v, vt, vh, *_batch(table, lens, cu, T), max_new, freq, rotary,
-                             amplitude, layout, *q, *qo, heads, dtype, _stream_handle(stream)))
+    _check(_fast.kv_append(*cache.args, k, kt, kh, v, vt, vh, *_batch(table, lens, cu, T), max_new, freq, rotary,
+                           amplitude, layout, *q, *qo, heads, dtype, _stream_handle(stream)))
     return out
 
 
@@ -620,9 +623,14 @@ def kv_read(cache, table, first, cu, total: int, dtype=None, out=None, stream=No
             raise ValueError("out must be contiguous CUDA tensors")
         if K.dtype is not V.dtype or (dtype is not None and K.dtype is not dtype):
             raise TypeError("out has the wrong type")
-    _check(_lib.tg_kv_read(*cache.args, *_batch(table, first, cu, total), K.data_ptr(), V.data_ptr(),
-                           _dtype_code(K.dtype, "dtype"), _stream_handle(stream)))
+    _check(_fast.kv_read(*cache.args, *_batch(table, first, cu, total), K.data_ptr(), V.data_ptr(),
+                         _dtype_code(K.dtype, "dtype"), _stream_handle(stream)))
     return K, V
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv_workspace(*sizes) -> int:
+    return tg_attention_kv_workspace(*sizes)
 
 
 def attention_kv(Q, cache, table, lens, cu=None, max_new: int = 1, max_len: int | None = None, causal: bool = True,
@@ -643,17 +651,15 @@ def attention_kv(Q, cache, table, lens, cu=None, max_new: int = 1, max_len: int 
     if max_len is None:
         max_len = batch[1] * cache.page
     handle = _stream_handle(stream)
-    need = _i64()
-    _check(_lib.tg_attention_kv_workspace(cache.kv_heads, cache.page, D, cache.fmt, H, batch[4], T, max_new, max_len,
-                                          window, dtype, ctypes.byref(need)))
+    need = _kv_workspace(cache.kv_heads, cache.page, D, cache.fmt, H, batch[4], T, max_new, max_len, window, dtype)
     with _on(stream):
         if out is None:
             out = torch.empty((T, H, D), dtype=Q.dtype, device=Q.device)
         elif out.shape != Q.shape or out.dtype is not Q.dtype or not out.is_cuda or not out.is_contiguous():
             raise ValueError("out must be a contiguous CUDA tensor of Q's shape and type")
         lse = torch.empty((T, H), dtype=torch.float32, device=Q.device) if return_lse else None
-        work = torch.empty(need.value, dtype=torch.uint8, device=Q.device) if need.value else None
-    _check(_lib.tg_attention_kv(q, qt, qh, out.data_ptr(), lse.data_ptr() if return_lse else None, *cache.args, *batch,
-                                H, max_new, max_len, int(causal), window, scale if scale is not None else D ** -0.5,
-                                dtype, work.data_ptr() if work is not None else None, need.value, handle))
+        work = torch.empty(need, dtype=torch.uint8, device=Q.device) if need else None
+    _check(_fast.attention_kv(q, qt, qh, out.data_ptr(), lse.data_ptr() if return_lse else None, *cache.args, *batch, H,
+                              max_new, max_len, int(causal), window, D ** -0.5 if scale is None else scale, dtype,
+                              work.data_ptr() if need else None, need, handle))
     return (out, lse) if return_lse else out

@@ -3,7 +3,8 @@
 Each translation unit under csrc/ is compiled in parallel with nvcc
 (-gencode arch=compute_103a,code=sm_103a), then linked into one shared
 library next to this file. No torch extension machinery: the library exports
-a plain C ABI (include/tg_gemm.h).
+a plain C ABI (include/tg_gemm.h). Beside it a small CPython module,
+_tg_binding.so, calls the same library without ctypes (csrc/tg_binding.c).
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,10 +21,11 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtg_gemm.so")
+BINDING = os.path.join(PKG, "_tg_binding.so")
 # the debug build (device-side bounds checks, TG_DEBUG=1): same sources, its own objects
 OBJDIR_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libtg_gemm_debug.so")
-SOURCES = ["tg_api.cu", "k_tiled.cu", "k_tiled2.cu", "k_splitk.cu", "k_w4.cu", "k_w4r.cu", "k_attn.cu", "k_softmax.cu", "k_rope.cu", "k_kv.cu", "k_kv_attn.cu", "k_fill.cu", "k_epilogue.cu", "k_pad.cu"]
+SOURCES = ["tg_api.cu", "k_tiled.cu", "k_tiled2.cu", "k_splitk.cu", "k_w4.cu", "k_w4r.cu", "k_attn.cu", "k_softmax.cu", "k_rope.cu", "k_kv.cu", "k_kv_attn.cu", "k_kv_tile.cu", "k_fill.cu", "k_epilogue.cu", "k_pad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
           "--expt-relaxed-constexpr"]
@@ -47,10 +50,22 @@ def _inputs() -> list[str]:
 
 
 def up_to_date(lib: str = LIB) -> bool:
-    if not os.path.exists(lib):
+    made = [lib] if lib != LIB else [LIB, BINDING]
+    if not all(os.path.exists(f) for f in made):
         return False
-    t = os.path.getmtime(lib)
+    t = min(os.path.getmtime(f) for f in made)
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def build_binding() -> None:
+    """The CPython module, linked with the library next to it."""
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+           os.path.join(CSRC, "tg_binding.c"), "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for tg_binding.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None, debug: bool = False) -> str:
@@ -79,11 +94,13 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
     tmp = lib_path + f".tmp{os.getpid()}"
-    cmd = [cc, "-shared", "-o", tmp] + objs + ARCH + ["-lineinfo"]
+    cmd = [cc, "-shared", "-o", tmp, "-Xlinker", f"-soname={os.path.basename(lib_path)}"] + objs + ARCH + ["-lineinfo"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib_path)
+    if not debug:
+        build_binding()
     return lib_path
 
 

@@ -37,83 +37,12 @@
 // tokens are given to MMA rows (mma_token) keep those reads free of bank
 // conflicts.
 #include "tg_device.cuh"
-#include "tg_kv.cuh"
+#include "tg_kv_split.cuh"
 
 #include <type_traits>
 
 namespace tg {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNoMax = -1e30f;        // running maximum before any visible key
-constexpr float kRescaleLog2 = 8.0f;    // the maximum moves only when a weight would pass 2^8
-
-// ---------------------------------------------------------------- rows by the dozen (any number of rows)
-
-constexpr int kRowWarps = 8;
-
-// One warp per (token, query head), one key at a time, the running maximum and sum in fp32.
-template <typename E, int kFmt, int kDim>
-__global__ void __launch_bounds__(kRowWarps * 32) attn_rows_kernel(const KvAttnCall c) {
-    constexpr int kPer = kDim / 32;
-    const KvBatch& b = c.batch;
-    const int lane = threadIdx.x % 32;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + threadIdx.x / 32;
-    if (row >= static_cast<int64_t>(b.total) * c.heads) return;
-    const int token = static_cast<int>(row / c.heads), head = static_cast<int>(row % c.heads);
-    int seq = token;
-    if (b.cu != nullptr) {
-        int lo = 0, hi = b.batch;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (__ldg(b.cu + mid) <= token) lo = mid; else hi = mid;
-        }
-        seq = lo;
-    }
-    const SeqSpan span = seq_span(b, seq, c.wd);
-    int64_t len = __ldg(b.lens + seq);
-    const int page = c.cache.page;
-    if (len < 0 || len > b.table_width * page || len > c.max_len) {
-        report_range(c.wd);
-        len = 0;
-    }
-    const int64_t pos = len - span.count + token - span.first;
-    const bool mine = token >= span.first && token < span.first + span.count;
-    int64_t end = c.causal ? min(len, pos + 1) : len;
-    int64_t begin = c.window > 0 ? max(int64_t(0), pos - c.window + 1) : 0;
-    if (!mine) end = 0;
-    const int kvh = head / (c.heads / c.cache.kv_heads);
-    const E* q = static_cast<const E*>(c.q.p) + token * c.q.token + head * c.q.head;
-    float qr[kPer], acc[kPer] = {};
-    for (int i = 0; i < kPer; ++i) qr[i] = to_float(q[lane + 32 * i]) * (c.scale * kLog2e);
-    float m = -INFINITY, l = 0.0f;
-    for (int64_t j = begin; j < end;) {
-        const int p = seq_page(b, c.cache, seq, static_cast<int>(j / page), c.wd);
-        const int64_t stop = min(end, (j / page + 1) * page);
-        if (p < 0) {
-            j = stop;
-            continue;
-        }
-        const int64_t ph = static_cast<int64_t>(p) * c.cache.kv_heads + kvh;
-        const float ks = c.cache.k_scale[ph], vs = c.cache.v_scale[ph];
-        for (; j < stop; ++j) {
-            const int64_t at = (ph * page + j % page) * kDim + lane;
-            float s = 0.0f;
-            for (int i = 0; i < kPer; ++i) s = fmaf(qr[i], decode<kFmt>(c.cache.k[at + 32 * i]), s);
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-            s *= ks;
-            const float m_new = fmaxf(m, s);
-            const float keep = exp2f(m - m_new), e = exp2f(s - m_new);
-            m = m_new;
-            l = l * keep + e;
-            for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * keep + e * vs * decode<kFmt>(c.cache.v[at + 32 * i]);
-        }
-    }
-    E* out = static_cast<E*>(c.out) + row * kDim;
-    const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-    for (int i = 0; i < kPer; ++i) out[lane + 32 * i] = from_float<E>(acc[i] * inv);
-    if (c.lse != nullptr && lane == 0) c.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * (1.0f / kLog2e);
-}
 
 // ---------------------------------------------------------------- few rows
 
@@ -131,41 +60,6 @@ struct Ring {
     static constexpr int kBytes = kWarps * kWarp;
 };
 
-// Where CTA k of `ctas` begins in a list of `total` chunks: equal shares, the first ones one longer.
-struct Shares {
-    int64_t each;
-    int rest;
-    int ctas;
-    __device__ Shares(int64_t total, int grid, int least) {
-        const int64_t most = (total + least - 1) / least;
-        ctas = static_cast<int>(min(static_cast<int64_t>(grid), most));
-        each = ctas > 0 ? total / ctas : 0;
-        rest = ctas > 0 ? static_cast<int>(total - each * ctas) : 0;
-    }
-    __device__ int64_t start(int k) const { return k * each + min(k, rest); }
-    __device__ int owner(int64_t chunk) const {
-        const int64_t longer = (each + 1) * rest;
-        return static_cast<int>(chunk < longer ? chunk / (each + 1) : rest + (chunk - longer) / each);
-    }
-};
-
-// What CTA k leaves for the joining kernel: the unit that its share begins inside of (chunks 0: none).
-struct Meta {
-    int64_t unit_start, total;
-    int chunks, seq, head, block;
-};
-
-struct FewArgs {
-    KvAttnCall c;
-    int share;          // query heads per kv head
-    int least;          // fewest chunks worth a CTA
-    int grid;
-    int q_vec;          // Q 8-byte aligned with strides of whole 8 bytes
-    Meta* meta;         // grid entries
-    float* parts;       // grid x 2 parts: rows x (dim + 2) floats each (values, then maxima, then sums)
-    int page_shift;
-};
-
 // A sequence's share of the list.
 struct SeqWork {
     int first, count;      // its rows of the packed tensors
@@ -176,7 +70,7 @@ struct SeqWork {
 };
 
 template <int kTiles>
-__device__ __forceinline__ SeqWork seq_work(const FewArgs& a, int i) {
+__device__ __forceinline__ SeqWork seq_work(const SplitWork& a, int i) {
     const KvAttnCall& c = a.c;
     SeqWork w;
     const SeqSpan span = seq_span(c.batch, i, c.wd);
@@ -217,24 +111,6 @@ __device__ __forceinline__ int ring_offset(int t, int at) {
     return line * 128 + (in ^ ((line & 7) << 4));
 }
 
-// Four codes to two fp16 pairs (codes 0 1, codes 2 3).
-template <int kFmt>
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    if constexpr (kFmt == kKvE4M3) {
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-            : "=r"(lo), "=r"(hi)
-            : "r"(w));
-    } else {
-        // code + 128 as the low byte of 1024 + (code + 128) in fp16, whose steps are 1 there
-        const uint32_t u = w ^ 0x80808080u;
-        const __half2 bias = __half2half2(__ushort_as_half(static_cast<unsigned short>(0x6480)));  // 1152
-        uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-        const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias), y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
-        lo = *reinterpret_cast<const uint32_t*>(&x);
-        hi = *reinterpret_cast<const uint32_t*>(&y);
-    }
-}
-
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile(
@@ -246,17 +122,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ float lg2_approx(float x) {
-    float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -274,15 +139,9 @@ __device__ __forceinline__ void load_q4(const E* row, int d, bool vec, float (&x
     }
 }
 
-// A row's result: unnormalised values o[0 .. n) at the running maximum's scale, its sum l.
-template <typename E>
-__device__ __forceinline__ float row_inverse(float l) {
-    return l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-}
-
 template <typename E, int kFmt, int kDim, int kTiles>
 __global__ void __launch_bounds__(kThreads, kTiles == 4 && kDim == 128 ? 2 : 3)
-    attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const FewArgs a) {
+    attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const SplitWork a) {
     constexpr int kRows = 8 * kTiles;
     constexpr int kK = kDim / 16;            // MMA steps along dim (scores) and m16 tiles along dim (values)
     extern __shared__ uint8_t smem_raw[];
@@ -695,10 +554,10 @@ __global__ void __launch_bounds__(kThreads, kTiles == 4 && kDim == 128 ? 2 : 3)
             if (whole) {
                 const int t = (row0 + r) / a.share;
                 const int64_t to = static_cast<int64_t>(w.first + t) * c.heads + head * a.share + (row0 + r) - t * a.share;
-                const float inv = row_inverse<E>(sum);
+                const float inv = row_inverse(sum);
                 E h[4] = {from_float<E>(v.x * inv), from_float<E>(v.y * inv), from_float<E>(v.z * inv), from_float<E>(v.w * inv)};
                 *reinterpret_cast<uint2*>(static_cast<E*>(c.out) + to * kDim + d) = *reinterpret_cast<const uint2*>(h);
-                if (d == 0 && c.lse != nullptr) c.lse[to] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * (1.0f / kLog2e);
+                if (d == 0 && c.lse != nullptr) c.lse[to] = row_lse(top, sum);
             } else {
                 *reinterpret_cast<float4*>(part + r * kDim + d) = v;
                 if (d == 0) {
@@ -713,42 +572,6 @@ __global__ void __launch_bounds__(kThreads, kTiles == 4 && kDim == 128 ? 2 : 3)
         off += c1 - c0;
         first_segment = false;
     }
-}
-
-// Joins the parts of the unit inside which share k begins, if k's is its first border: block
-// (k - 1, row). The order of the parts is that of their keys.
-template <typename E, int kDim, int kRows>
-__global__ void __launch_bounds__(kDim) attn_join_kernel(const FewArgs a) {
-    const KvAttnCall& c = a.c;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int k = blockIdx.x + 1, r = blockIdx.y, d = threadIdx.x;
-    const Meta m = a.meta[k];
-    if (m.chunks == 0) return;
-    const Shares shares(m.total, a.grid, a.least);
-    const int64_t before = shares.start(k - 1);
-    if (before > m.unit_start) return;  // an earlier border lies in the unit
-    const SeqSpan span = seq_span(c.batch, m.seq, c.wd);
-    const int row = m.block * kRows + r;
-    if (row >= span.count * a.share) return;
-    const int last = shares.owner(m.unit_start + m.chunks - 1);
-    auto part_of = [&](int x) {
-        const int slot = x == k - 1 && before < m.unit_start ? 1 : 0;
-        return a.parts + (static_cast<int64_t>(2 * x) + slot) * kRows * (kDim + 2);
-    };
-    float top = kNoMax;
-    for (int x = k - 1; x <= last; ++x) top = fmaxf(top, part_of(x)[kRows * kDim + r]);
-    float v = 0.0f, sum = 0.0f;
-#pragma unroll 4
-    for (int x = k - 1; x <= last; ++x) {
-        const float* p = part_of(x);
-        const float keep = ex2_approx(p[kRows * kDim + r] - top);
-        sum += p[kRows * (kDim + 1) + r] * keep;
-        v += p[r * kDim + d] * keep;
-    }
-    const int t = row / a.share;
-    const int64_t to = static_cast<int64_t>(span.first + t) * c.heads + m.head * a.share + row - t * a.share;
-    static_cast<E*>(c.out)[to * kDim + d] = from_float<E>(v * row_inverse<E>(sum));
-    if (d == 0 && c.lse != nullptr) c.lse[to] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * (1.0f / kLog2e);
 }
 
 // How the few-rows kernel runs a call: row tiles, CTAs, workspace.
@@ -771,7 +594,7 @@ FewPlan few_plan(const KvAttnCall& c, int sm_count) {
 }
 
 // Rows of one kv head beyond which the few-rows kernel is not taken.
-bool few_rows(const KvAttnCall&) { return true; }
+bool few_rows(const KvAttnCall& c) { return static_cast<int64_t>(c.batch.max_new) * (c.heads / c.cache.kv_heads) <= 64; }
 
 template <typename E, int kFmt, int kDim, int kTiles>
 cudaError_t launch_few(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, const FewPlan& p,
@@ -786,7 +609,7 @@ cudaError_t launch_few(const KvAttnCall& c, const CUtensorMap& tmK, const CUtens
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
         attr_gen[dev] = g_generation;
     }
-    FewArgs a{};
+    SplitWork a{};
     a.c = c;
     a.share = c.heads / c.cache.kv_heads;
     a.least = 1;
@@ -797,40 +620,31 @@ cudaError_t launch_few(const KvAttnCall& c, const CUtensorMap& tmK, const CUtens
     while (c.cache.page >> (a.page_shift + 1)) ++a.page_shift;
     kernel<<<p.grid, kThreads, smem, stream>>>(tmK, tmV, a);
     if ((e = cudaGetLastError()) != cudaSuccess || !p.split) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.grid - 1, 8 * kTiles);
-    cfg.blockDim = dim3(kDim);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<E, kDim, 8 * kTiles>, a);
+    return launch_join<E, kDim, 8 * kTiles>(a, 8 * kTiles, stream);
 }
 
 template <typename E, int kFmt, int kDim>
 cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count,
                    cudaStream_t stream) {
-    if (few_rows(c)) {
+    {
         const FewPlan p = few_plan(c, sm_count);
         if (p.tiles == 1) return launch_few<E, kFmt, kDim, 1>(c, tmK, tmV, workspace, p, stream);
         if (p.tiles == 2) return launch_few<E, kFmt, kDim, 2>(c, tmK, tmV, workspace, p, stream);
         return launch_few<E, kFmt, kDim, 4>(c, tmK, tmV, workspace, p, stream);
     }
-    const int64_t rows = static_cast<int64_t>(c.batch.total) * c.heads;
-    attn_rows_kernel<E, kFmt, kDim><<<static_cast<unsigned>((rows + kRowWarps - 1) / kRowWarps), kRowWarps * 32, 0, stream>>>(c);
-    return cudaGetLastError();
 }
 
 }  // namespace
 
 int kv_attn_box_rows(const KvAttnCall& c) { return kStep * c.cache.dim / 128; }
 
-int64_t kv_attn_workspace(const KvAttnCall& c, int sm_count) { return few_rows(c) ? few_plan(c, sm_count).bytes : 0; }
+int64_t kv_attn_workspace(const KvAttnCall& c, int sm_count) {
+    return few_rows(c) ? few_plan(c, sm_count).bytes : kv_attn_tile_workspace(c, sm_count);
+}
 
 cudaError_t launch_kv_attn(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count,
                            cudaStream_t stream) {
+    if (!few_rows(c)) return launch_kv_attn_tile(c, workspace, sm_count, stream);
     const bool h = c.dtype == kFp16, e4 = c.cache.fmt == kKvE4M3, d128 = c.cache.dim == 128;
     auto go = [&](auto* f) { return f(c, tmK, tmV, workspace, sm_count, stream); };
     if (h && e4) return d128 ? go(launch<__half, kKvE4M3, 128>) : go(launch<__half, kKvE4M3, 64>);

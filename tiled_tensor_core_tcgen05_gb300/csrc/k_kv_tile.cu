@@ -1,0 +1,672 @@
+// Attention over the paged 8-bit cache, many rows a kv head (prompt chunks):
+// the operation, the way the scales are kept out of the products and the even
+// split of the work are those of k_kv_attn.cu. Here the products bound it, and
+// they run on tcgen05.
+//
+// A unit is a sequence, a kv head and a block of 256 rows (query heads of one
+// kv head, token by token); its list entries are tiles of 128 keys, from the
+// first that any row sees to the last. One CTA per SM walks its share:
+//   warps 0-3, 4-7  softmax of rows 0-127 and 128-255, a thread a row (its TMEM
+//                   lane), all 128 scores of a tile in registers. They also
+//                   bring the rows of Q to shared memory and write the result;
+//   warps 8-11      read the codes of 128 keys, then of their values, 16 bytes a
+//                   thread and a tile ahead, and leave them as fp16 (exact) in
+//                   128-byte-swizzled tiles, two of each; once for both halves
+//                   of the rows, which is what the 256 rows are for;
+//   warp 12         one thread issues the MMAs (warps 13-15 only complete its warpgroup).
+// TMEM: scores of either half 128 columns, outputs dim columns each. Weights (fp16,
+// 64 columns) overwrite the upper half of their scores, so that the lower half
+// of the next tile's scores can be issued at once behind the product that
+// still reads the weights, and only the upper half waits for it. The halves
+// alternate: while one's softmax runs, the other's products do.
+#include "tg_device.cuh"
+#include "tg_kv_split.cuh"
+
+#include <type_traits>
+
+namespace tg {
+namespace {
+
+constexpr int kHalfRows = 128;
+constexpr int kRows = 2 * kHalfRows;
+constexpr int kKeys = 128;               // keys a tile
+constexpr int kBlocks = kKeys / 16;      // blocks of 16 keys with one scale each (a page has at least 16)
+constexpr int kSoftmaxThreads = 256;
+constexpr int kConvThreads = 128;
+constexpr int kThreads = kSoftmaxThreads + kConvThreads + 128;   // the last four warps: one issues, three idle
+// Registers a thread: all start with kRegs; the softmax threads, which hold 128 scores, take what the
+// others give up. The sum (64512) stays within the launch's 512 x 128.
+constexpr int kRegs = 128, kRegsSoftmax = 168, kRegsConv = 104, kRegsIssue = 64;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsConv + 128 * kRegsIssue <= kThreads * kRegs, "register split");
+constexpr int kScaleSlots = 4;           // tiles whose scales are in shared memory
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0;            // + 128 half
+constexpr uint32_t kColP = 64;           // + 128 half
+constexpr uint32_t kColO = 256;          // + 128 half
+
+template <int kDim>
+struct Smem {
+    static constexpr int kBox = 128 * 128;                 // 128 rows of 64 fp16
+    static constexpr int kTile = kBox * (kDim / 64);
+    static constexpr int kQ = 0;                           // 2 halves
+    static constexpr int kK = 2 * kTile;                   // 2 stages
+    static constexpr int kV = 4 * kTile;                   // 2 stages
+    static constexpr int kScales = 6 * kTile;              // slots x blocks x {k scale, log2 v scale, 1 / v scale}
+    static constexpr int kBars = kScales + kScaleSlots * kBlocks * 3 * 4;
+    static constexpr int kNumBars = 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + kScaleSlots + 1;
+    static constexpr int kTmemSlot = kBars + 8 * kNumBars;
+    static constexpr int kAbort = kTmemSlot + 4;
+    static constexpr int kScan = (kAbort + 4 + 7) / 8 * 8;  // 16 int64, then found sequence and offset
+    static constexpr int kUsed = kScan + 16 * 8 + 16;
+    static_assert(kBars % 8 == 0 && kScales % 16 == 0 && kScan % 8 == 0, "alignment");
+    static_assert(kUsed + 1024 <= 227 * 1024, "shared memory of one CTA");
+    static constexpr int kAlloc = kUsed + 1024;
+};
+
+// A sequence and the tiles of its row blocks.
+struct TileWork {
+    int first, count, len;
+    int blocks;       // row blocks per kv head
+    int64_t total;    // tiles over all of them and all kv heads
+};
+
+// Tiles of row block `block`: first, and how many (at least one, perhaps of no key).
+__device__ __forceinline__ void tiles_of(const SplitWork& a, int count, int len, int block, int& tile0, int& tiles) {
+    const KvAttnCall& c = a.c;
+    const int rows = count * a.share, row0 = block * kRows, row1 = min(rows, row0 + kRows) - 1;
+    const int64_t p0 = static_cast<int64_t>(len) - count + row0 / a.share, p1 = static_cast<int64_t>(len) - count + row1 / a.share;
+    const int64_t from = c.window > 0 ? p0 - c.window + 1 : 0;
+    const int64_t to = c.causal ? min(static_cast<int64_t>(len), p1 + 1) : len;
+    tile0 = from > 0 ? static_cast<int>(from / kKeys) : 0;
+    tiles = max(1, (max(0, static_cast<int>(to)) + kKeys - 1) / kKeys - tile0);
+}
+
+__device__ __forceinline__ TileWork tile_work(const SplitWork& a, int i) {
+    const KvAttnCall& c = a.c;
+    TileWork w;
+    const SeqSpan span = seq_span(c.batch, i, c.wd);
+    w.first = span.first;
+    w.count = span.count;
+    w.len = __ldg(c.batch.lens + i);
+    if (w.len < 0 || w.len > c.max_len || w.len > c.batch.table_width << a.page_shift) {
+        report_range(c.wd);
+        w.len = 0;
+    }
+    w.blocks = (w.count * a.share + kRows - 1) / kRows;
+    int64_t per_head = 0;
+    for (int b = 0; b < w.blocks; ++b) {
+        int t0, n;
+        tiles_of(a, w.count, w.len, b, t0, n);
+        per_head += n;
+    }
+    w.total = per_head * c.cache.kv_heads;
+    return w;
+}
+
+// The segments of a CTA's share, one after another: every role walks them by itself.
+struct Segment {
+    int seq, head, block, first, count, len;
+    int tile0, tiles;   // of the unit
+    int t0, t1;         // the segment's among them
+};
+
+struct Walk {
+    const SplitWork& a;
+    int64_t left;
+    int seq, head, block, at;
+    TileWork w;
+    __device__ Walk(const SplitWork& args, int seq0, int64_t off, int64_t n) : a(args), left(n), seq(seq0), w(tile_work(args, seq0)) {
+        const int64_t per_head = w.total / a.c.cache.kv_heads;
+        head = static_cast<int>(off / per_head);
+        int64_t in = off - head * per_head;
+        block = 0;
+        int t0, k;
+        tiles_of(a, w.count, w.len, 0, t0, k);
+        while (in >= k && block + 1 < w.blocks) {
+            in -= k;
+            tiles_of(a, w.count, w.len, ++block, t0, k);
+        }
+        at = static_cast<int>(in);
+    }
+    __device__ bool next(Segment& s) {
+        if (left <= 0) return false;
+        while (block >= w.blocks) {  // the next kv head, or the next sequence that has rows
+            block = 0;
+            if (++head >= a.c.cache.kv_heads || w.blocks == 0) {
+                head = 0;
+                if (++seq >= a.c.batch.batch) return false;
+                w = tile_work(a, seq);
+            }
+        }
+        s.seq = seq;
+        s.head = head;
+        s.block = block;
+        s.first = w.first;
+        s.count = w.count;
+        s.len = w.len;
+        tiles_of(a, w.count, w.len, block, s.tile0, s.tiles);
+        s.t0 = at;
+        s.t1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), at + left));
+        left -= s.t1 - s.t0;
+        at = 0;
+        ++block;
+        return true;
+    }
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+template <typename E, int kFmt, int kDim>
+__global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork a) {
+    using L = Smem<kDim>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const KvAttnCall& c = a.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t bar = sbase + L::kBars;
+    auto bars = [&](int n) {
+        const uint32_t b = bar;
+        bar += 8 * n;
+        return b;
+    };
+    const uint32_t q_full = bars(2), k_full = bars(2), k_empty = bars(2), v_full = bars(2), v_empty = bars(2), s_full = bars(2);
+    const uint32_t p_full = bars(4), o_done = bars(2), scales_full = bars(kScaleSlots), drain = bars(1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+    int64_t* scan = reinterpret_cast<int64_t*>(smem + L::kScan);
+    int* found_seq = reinterpret_cast<int*>(smem + L::kScan + 16 * 8);
+    int64_t* found_off = reinterpret_cast<int64_t*>(smem + L::kScan + 16 * 8 + 8);
+    float* scales = reinterpret_cast<float*>(smem + L::kScales);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + 8 * i, 4);           // a warp's rows of one half each
+            mbar_init(k_full + 8 * i, kConvThreads / 32);
+            mbar_init(k_empty + 8 * i, 1);
+            mbar_init(v_full + 8 * i, kConvThreads / 32);
+            mbar_init(v_empty + 8 * i, 1);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(o_done + 8 * i, 1);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(p_full + 8 * i, 4);
+        for (int i = 0; i < kScaleSlots; ++i) mbar_init(scales_full + 8 * i, 1);
+        mbar_init(drain, 1);
+        fence_barrier_init();
+        *abort_flag = 0;
+    }
+
+    // ---- this CTA's share of the list
+    const int batch = c.batch.batch;
+    int64_t total = 0;
+    constexpr int kWarps = kThreads / 32;
+    auto block_scan = [&](int64_t v, int64_t& before) {
+        int64_t x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = x;
+        __syncthreads();
+        int64_t sum = 0, low = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) low += scan[w];
+            sum += scan[w];
+        }
+        before = low + x - v;
+        return sum;
+    };
+    int64_t mine = 0, before = 0;
+    for (int base = 0; base < batch; base += kThreads) {
+        const int i = base + threadIdx.x;
+        mine = i < batch ? tile_work(a, i).total : 0;
+        total += block_scan(mine, before);
+    }
+    const Shares shares(total, a.grid, a.least);
+    const int k = blockIdx.x;
+    if (k >= shares.ctas) {
+        if (threadIdx.x == 0) a.meta[k].chunks = 0;
+        return;
+    }
+    const int64_t start = shares.start(k), stop = shares.start(k + 1);
+    int64_t carry = 0;
+    for (int base = 0; base < batch; base += kThreads) {
+        if (batch > kThreads) {
+            const int i = base + threadIdx.x;
+            mine = i < batch ? tile_work(a, i).total : 0;
+            const int64_t sum = block_scan(mine, before);
+            before += carry;
+            carry += sum;
+        }
+        if (before <= start && start < before + mine) {
+            *found_seq = base + threadIdx.x;
+            *found_off = start - before;
+        }
+    }
+    if (warp == 12) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx wc{abort_flag, c.wd.status, c.wd.limit_ns};
+    Walk walk(a, *found_seq, *found_off, stop - start);
+    Segment sg;
+    uint32_t tile_no = 0;  // tiles so far: stages and phases
+
+    if (warp >= 12) {
+        // ------------------------------------------------------------ MMA issue
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+        if (warp == 12 && lane == 0) {
+            constexpr uint32_t idesc_s = idesc_f16_f32(128, 64, false, false);
+            constexpr uint32_t idesc_o = idesc_f16_f32(128, kDim, false, true);
+            // keys 64 part .. 64 part + 63 of the scores of half h
+            auto scores = [&](int h, int part, uint32_t stage) {
+#pragma unroll
+                for (int kk = 0; kk < kDim / 16; ++kk) {
+                    const uint32_t in = (kk >> 2) * L::kBox;
+                    const uint64_t off = static_cast<uint64_t>(((kk & 3) * 32) >> 4);
+                    const uint64_t qd = smem_desc_sw128(sbase + L::kQ + h * L::kTile + in, 16, 1024) + off;
+                    const uint64_t kd = smem_desc_sw128(sbase + L::kK + stage * L::kTile + in + part * 64 * 128, 16, 1024) + off;
+                    mma_f16(tmem + kColS + 128 * h + 64 * part, qd, kd, idesc_s, kk != 0);
+                }
+            };
+            auto outputs = [&](int h, int part, uint32_t stage, bool first) {
+#pragma unroll
+                for (int kk = 4 * part; kk < 4 * part + 4; ++kk) {
+                    const uint64_t vd = smem_desc_sw128(sbase + L::kV + stage * L::kTile, L::kBox, 1024) + static_cast<uint64_t>((kk * 2048) >> 4);
+                    mma_f16_tmem_a(tmem + kColO + 128 * h, tmem + kColP + 128 * h + kk * 8, vd, idesc_o, !first || kk != 0);
+                }
+            };
+            bool ok = true;
+            uint32_t seg = 0;
+            for (; ok && walk.next(sg); ++seg) {
+                const int n = sg.t1 - sg.t0;
+                for (int j = -1; ok && j < n; ++j) {  // j = -1: the first tile's scores
+                    const uint32_t g = tile_no + j, ph = g & 1u;                    // tile j
+                    const uint32_t g1 = g + 1, st1 = g1 & 1u, kph = (g1 >> 1) & 1u;  // tile j + 1
+                    const bool more = j + 1 < n;
+                    for (int h = 0; ok && h < 2; ++h) {
+                        if (j < 0) {
+                            ok = wait_phase(q_full + 8 * h, seg & 1u, wc, kSiteMmaFull);
+                        } else {
+                            ok = wait_phase(p_full + 16 * h, ph, wc, kSiteMmaFull) &&
+                                 wait_phase(v_full + 8 * (g & 1u), (g >> 1) & 1u, wc, kSiteMmaFull);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            outputs(h, 0, g & 1u, j == 0);
+                            ok = wait_phase(p_full + 16 * h + 8, ph, wc, kSiteMmaFull);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            outputs(h, 1, g & 1u, false);
+                            mma_commit(o_done + 8 * h);
+                            if (h == 1) mma_commit(v_empty + 8 * (g & 1u));
+                        }
+                        if (!ok || !more) continue;
+                        ok = wait_phase(k_full + 8 * st1, kph, wc, kSiteMmaFull);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        scores(h, 0, st1);
+                        if (j >= 0) {  // the upper half overwrites the weights of tile j
+                            ok = wait_phase(o_done + 8 * h, ph, wc, kSiteMmaAccEmpty);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                        }
+                        scores(h, 1, st1);
+                        mma_commit(s_full + 8 * h);
+                        if (h == 1) mma_commit(k_empty + 8 * st1);
+                    }
+                }
+                tile_no += n;
+            }
+            mma_commit(drain);
+            wait_phase_drain(drain, 0, wc);
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------ codes to fp16 tiles
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
+        const int tid = threadIdx.x - kSoftmaxThreads;
+        constexpr int kLanes = kDim / 16;            // threads a row of codes
+        constexpr int kPass = kConvThreads / kLanes; // rows a pass: 16 or 32
+        constexpr int kPasses = kKeys / kPass;
+        const int row_in = tid / kLanes, piece = tid % kLanes;
+        // a lane of each warp per block of 16 keys: its page
+        auto page_of = [&](const Segment& s, int tile) {
+            const int token = (s.tile0 + tile) * kKeys + lane * 16;
+            if (lane >= kBlocks || token >= s.len) return -1;
+            return seq_page(c.batch, c.cache, s.seq, token >> a.page_shift, c.wd);
+        };
+        auto load = [&](const uint8_t* codes, const Segment& s, int tile, int pg, uint4 (&x)[kPasses]) {
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int t = i * kPass + row_in, token = (s.tile0 + tile) * kKeys + t;
+                const int p = __shfl_sync(0xFFFFFFFFu, pg, t >> 4);
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (p >= 0 && token < s.len) {
+                    const int64_t row = (static_cast<int64_t>(p) * c.cache.kv_heads + s.head) * c.cache.page + (token & (c.cache.page - 1));
+                    x[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * kDim + piece * 16));
+                }
+            }
+        };
+        auto store = [&](uint32_t tile_base, const uint4 (&x)[kPasses]) {
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int t = i * kPass + row_in;
+                uint32_t h[8];
+                codes_to_half<kFmt>(x[i].x, h[0], h[1]);
+                codes_to_half<kFmt>(x[i].y, h[2], h[3]);
+                codes_to_half<kFmt>(x[i].z, h[4], h[5]);
+                codes_to_half<kFmt>(x[i].w, h[6], h[7]);
+                // 16 codes are two 16-byte pieces of a box's row; rows' upper lanes write the odd one first,
+                // so that a quarter-warp's eight go to eight banks
+                const uint32_t line = tile_base + (piece >> 2) * L::kBox + t * 128;
+                const int odd = piece >> 2, c0 = (piece & 3) * 2;
+                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                sts_v4(line + (((c0 + odd) ^ (t & 7)) << 4), odd ? hi : lo);
+                sts_v4(line + (((c0 + 1 - odd) ^ (t & 7)) << 4), odd ? lo : hi);
+            }
+        };
+        Segment nx;  // one tile ahead
+        bool have = walk.next(nx);
+        int tile = have ? nx.t0 : 0;
+        int pg = have ? page_of(nx, tile) : -1;
+        uint4 kx[kPasses], vx[kPasses];
+        if (have) load(c.cache.k, nx, tile, pg, kx);
+        while (have) {
+            const uint32_t st = tile_no & 1u, eph = ((tile_no >> 1) & 1u) ^ 1u;
+            const Segment cur = nx;
+            const int cur_tile = tile, cur_pg = pg;
+            load(c.cache.v, cur, cur_tile, cur_pg, vx);
+            if (++tile >= nx.t1) {
+                have = walk.next(nx);
+                tile = nx.t0;
+            }
+            if (have) pg = page_of(nx, tile);
+            // keys, and the scales of the tile's blocks
+            if (!__all_sync(0xFFFFFFFFu, wait_phase_sleep(k_empty + 8 * st, eph, wc, kSiteConvEmpty, 32))) break;
+            if (warp == 8) {
+                float* slot = scales + (tile_no % kScaleSlots) * kBlocks * 3;
+                if (lane < kBlocks) {
+                    const int64_t ph = static_cast<int64_t>(max(cur_pg, 0)) * c.cache.kv_heads + cur.head;
+                    float ks = 0.0f, lv = -INFINITY, iv = 1.0f;  // no page: no weight
+                    if (cur_pg >= 0) {
+                        ks = __ldg(c.cache.k_scale + ph);
+                        const float vs = max_nan(__ldg(c.cache.v_scale + ph), kScaleFloor);
+                        lv = log2f(vs);
+                        iv = 1.0f / vs;
+                    }
+                    slot[lane] = ks;
+                    slot[kBlocks + lane] = lv;
+                    slot[2 * kBlocks + lane] = iv;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(scales_full + 8 * (tile_no % kScaleSlots));
+            }
+            store(sbase + L::kK + st * L::kTile, kx);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(k_full + 8 * st);
+            if (have) load(c.cache.k, nx, tile, pg, kx);
+            // values
+            if (!__all_sync(0xFFFFFFFFu, wait_phase_sleep(v_empty + 8 * st, eph, wc, kSiteConvEmpty, 32))) break;
+            store(sbase + L::kV + st * L::kTile, vx);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_full + 8 * st);
+            ++tile_no;
+        }
+    } else {
+        // ------------------------------------------------------------ softmax, Q and the result
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        const int h = warp >> 2;
+        const int row = (warp & 3) * 32 + lane;                       // of the half: its TMEM lane
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t col_s = lanes + kColS + 128 * h, col_p = lanes + kColP + 128 * h, col_o = lanes + kColO + 128 * h;
+        bool ok = true;
+        bool first_segment = true;
+        int64_t pos = start;
+        while (ok && walk.next(sg)) {
+            if (first_segment && threadIdx.x == 0) a.meta[k] = Meta{pos - sg.t0, total, sg.t0 > 0 ? sg.tiles : 0, sg.seq, sg.head, sg.block};
+            const int r = sg.block * kRows + h * kHalfRows + row;      // row of the (sequence, kv head)
+            const bool real = r < sg.count * a.share;
+            const int t = r / a.share;
+            const int64_t out_row = static_cast<int64_t>(sg.first + t) * c.heads + sg.head * a.share + r - t * a.share;
+            // Q: fp16 as it is; bf16 moved by a power of two so that the row's largest value lies in
+            // [2^14, 2^15). A negative scale goes into Q, so that larger products mean larger weights.
+            float f = fabsf(c.scale) * kLog2e;
+            {
+                const E* x = static_cast<const E*>(c.q.p) + static_cast<int64_t>(sg.first + t) * c.q.token + (sg.head * a.share + r - t * a.share) * c.q.head;
+                float up = c.scale < 0.0f ? -1.0f : 1.0f;
+                if constexpr (!std::is_same<E, __half>::value) {
+                    float most = 0.0f;
+                    if (real) {
+                        for (int d = 0; d < kDim; d += 8) {
+                            float v[8];
+                            load_values<E, 8>(x, d, a.q_vec != 0, v);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
+                        }
+                    }
+                    const int e = most > 0.0f && most <= 3.3895314e38f ? max(-100, (__float_as_int(most) >> 23) - 127) : 14;
+                    up *= __int_as_float((14 - e + 127) << 23);
+                    f *= __int_as_float((e - 14 + 127) << 23);
+                }
+#pragma unroll 4
+                for (int d = 0; d < kDim; d += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+                    if (real) load_values<E, 8>(x, d, a.q_vec != 0, v);
+                    const uint4 w = make_uint4(half2_bits(v[0] * up, v[1] * up), half2_bits(v[2] * up, v[3] * up),
+                                               half2_bits(v[4] * up, v[5] * up), half2_bits(v[6] * up, v[7] * up));
+                    sts_v4(sbase + L::kQ + h * L::kTile + (d >> 6) * L::kBox + row * 128 + ((((d & 63) >> 3) ^ (row & 7)) << 4), w);
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full + 8 * h);
+            int to = sg.len, from = 0;
+            {
+                const int64_t p = static_cast<int64_t>(sg.len) - sg.count + min(t, sg.count - 1);
+                if (c.causal) to = static_cast<int>(min(static_cast<int64_t>(sg.len), p + 1));
+                if (c.window > 0 && p - c.window + 1 > 0) from = static_cast<int>(p - c.window + 1);
+            }
+            float m = kNoMax, l = 0.0f;
+            const int n = sg.t1 - sg.t0;
+            for (int j = 0; j < n; ++j) {
+                const uint32_t g = tile_no + j, ph = g & 1u;
+                ok = wait_phase(scales_full + 8 * (g % kScaleSlots), (g / kScaleSlots) & 1u, wc, kSiteEpilogueAccFull) &&
+                     wait_phase(s_full + 8 * h, ph, wc, kSiteEpilogueAccFull);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const float* sc = scales + (g % kScaleSlots) * kBlocks * 3;
+                uint32_t s[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(col_s + 32 * q, s[q]);
+                tmem_ld_wait();
+                auto raw = [&](int i) { return __uint_as_float(s[i >> 5][i & 31]); };
+                const int key0 = (sg.tile0 + sg.t0 + j) * kKeys;
+                if (key0 < from || key0 + kKeys > to) {
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i)
+                        if (key0 + i < from || key0 + i >= to) s[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+                }
+                __syncwarp();
+                // the tile's maximum, block by block
+                float top = kNoMax;
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    float x = max3(raw(16 * b), raw(16 * b + 1), raw(16 * b + 2)), y = max3(raw(16 * b + 3), raw(16 * b + 4), raw(16 * b + 5));
+                    x = max3(x, raw(16 * b + 6), raw(16 * b + 7));
+                    y = max3(y, raw(16 * b + 8), raw(16 * b + 9));
+                    x = max3(x, raw(16 * b + 10), raw(16 * b + 11));
+                    y = max3(y, raw(16 * b + 12), raw(16 * b + 13));
+                    x = max3(x, raw(16 * b + 14), raw(16 * b + 15));
+                    top = fmaxf(top, fmaf(fmaxf(x, y), fmaxf(f * sc[b], 1e-38f), sc[kBlocks + b]));
+                }
+                float keep = 1.0f;
+                bool grew = false;
+                if (top > m + kRescaleLog2) {
+                    keep = ex2_approx(m - top);
+                    m = top;
+                    grew = true;
+                }
+                float sum = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int b = 2 * q; b < 2 * q + 2; ++b) {
+                        const float cb = fmaxf(f * sc[b], 1e-38f), ob = sc[kBlocks + b] - m;
+                        const float2 c2 = make_float2(cb, cb), o2 = make_float2(ob, ob);
+                        float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 x = __ffma2_rn(make_float2(raw(16 * b + 2 * e), raw(16 * b + 2 * e + 1)), c2, o2);
+                            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                            part = __fadd2_rn(part, p);
+                            w[(b & 1) * 8 + e] = half2_bits(p.x, p.y);
+                        }
+                        sum = fmaf(part.x + part.y, sc[2 * kBlocks + b], sum);
+                    }
+                    tmem_st_x16(col_p + 16 * q, w);
+                    // the outputs so far come to the new maximum before the first weights are handed over: the
+                    // products of the tile before have completed (this tile's scores were issued after them)
+                    if (q == 1 && j > 0 && __any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll 1
+                        for (int d = 0; d < kDim; d += 32) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(col_o + d, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                            tmem_st_32x32b_x32(col_o + d, o);
+                        }
+                    }
+                    if (q & 1) {
+                        tmem_st_wait();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_full + 16 * h + 8 * (q >> 1));
+                    }
+                }
+                l = l * keep + sum;
+            }
+            if (!ok) break;
+            tile_no += n;
+            if (!__all_sync(0xFFFFFFFFu, wait_phase_sleep(o_done + 8 * h, (tile_no - 1) & 1u, wc, kSiteEpilogueAccFull, 32))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            const bool whole = sg.t0 == 0 && sg.t1 == sg.tiles;
+            const float inv = row_inverse(l);
+            float* part = a.parts + (static_cast<int64_t>(2 * k) + (first_segment ? 0 : 1)) * kRows * (kDim + 2);
+            const int pr = h * kHalfRows + row;
+#pragma unroll 1
+            for (int d = 0; d < kDim; d += 32) {
+                uint32_t o[32];
+                __syncwarp();
+                tmem_ld_32x32b_x32(col_o + d, o);
+                tmem_ld_wait();
+                if (real && whole) {
+                    E* y = static_cast<E*>(c.out) + out_row * kDim + d;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o[e + i]) * inv;
+                        store_values<E, 8>(y, e, true, v);
+                    }
+                } else if (real) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4*>(part + pr * kDim + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            }
+            if (real && whole && c.lse != nullptr) c.lse[out_row] = row_lse(m, l);
+            if (real && !whole) {
+                part[kRows * kDim + pr] = m;
+                part[kRows * (kDim + 1) + pr] = l;
+            }
+            pos += n;
+            first_segment = false;
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+int64_t meta_bytes(int grid) { return (static_cast<int64_t>(grid) * sizeof(Meta) + 255) / 256 * 256; }
+
+template <typename E, int kFmt, int kDim>
+cudaError_t launch(const KvAttnCall& c, void* workspace, int sm_count, cudaStream_t stream) {
+    static int attr_gen[64] = {};
+    auto* kernel = attn_tile_kernel<E, kFmt, kDim>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && attr_gen[dev] != g_generation) {
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kDim>::kAlloc)) != cudaSuccess) return e;
+        // the register split draws on what the launch reserves: never more than that
+        cudaFuncAttributes fa{};
+        if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+        if (fa.numRegs < kRegs) return cudaErrorInvalidConfiguration;
+        attr_gen[dev] = g_generation;
+    }
+    SplitWork a{};
+    a.c = c;
+    a.share = c.heads / c.cache.kv_heads;
+    a.least = 2;
+    a.grid = sm_count;
+    a.q_vec = reinterpret_cast<uintptr_t>(c.q.p) % 16 == 0 && c.q.token % 8 == 0 && c.q.head % 8 == 0;
+    a.meta = static_cast<Meta*>(workspace);
+    a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + meta_bytes(a.grid));
+    while (c.cache.page >> (a.page_shift + 1)) ++a.page_shift;
+    kernel<<<a.grid, kThreads, Smem<kDim>::kAlloc, stream>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess || c.max_len <= kKeys) return e;
+    return launch_join<E, kDim, kRows>(a, 32, stream);
+}
+
+}  // namespace
+
+int64_t kv_attn_tile_workspace(const KvAttnCall& c, int sm_count) {
+    return meta_bytes(sm_count) + static_cast<int64_t>(sm_count) * 2 * kRows * (c.cache.dim + 2) * 4;
+}
+
+cudaError_t launch_kv_attn_tile(const KvAttnCall& c, void* workspace, int sm_count, cudaStream_t stream) {
+    const bool h = c.dtype == kFp16, e4 = c.cache.fmt == kKvE4M3, d128 = c.cache.dim == 128;
+    auto go = [&](auto* f) { return f(c, workspace, sm_count, stream); };
+    if (h && e4) return d128 ? go(launch<__half, kKvE4M3, 128>) : go(launch<__half, kKvE4M3, 64>);
+    if (h) return d128 ? go(launch<__half, kKvInt8, 128>) : go(launch<__half, kKvInt8, 64>);
+    if (e4) return d128 ? go(launch<__nv_bfloat16, kKvE4M3, 128>) : go(launch<__nv_bfloat16, kKvE4M3, 64>);
+    return d128 ? go(launch<__nv_bfloat16, kKvInt8, 128>) : go(launch<__nv_bfloat16, kKvInt8, 64>);
+}
+
+}  // namespace tg

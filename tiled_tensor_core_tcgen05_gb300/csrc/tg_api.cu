@@ -1572,7 +1572,7 @@ tg_status kv_attn_sizes(int64_t kv_heads, int64_t page, int64_t heads, int64_t t
         return fail(TG_ERR_INVALID_ARG, "max_len out of range: %lld", (long long)max_len);
     if (window < 0 || window > kIntMax)
         return fail(TG_ERR_INVALID_ARG, "window must be in [0, 2^31) (0: none), got %lld", (long long)window);
-    if (total * heads > (1ll << 33)) return fail(TG_ERR_INVALID_ARG, "too many rows");
+    if (total * (heads / kv_heads) > (1ll << 30)) return fail(TG_ERR_INVALID_ARG, "too many rows");
     c->heads = (int)heads;
     c->dtype = dtype;
     c->max_len = max_len;
