@@ -13,12 +13,13 @@
 //                   thread and a tile ahead, and leave them as fp16 (exact) in
 //                   128-byte-swizzled tiles, two of each; once for both halves
 //                   of the rows, which is what the 256 rows are for;
-//   warp 12         one thread issues the MMAs (warps 13-15 only complete its warpgroup).
-// TMEM: scores of either half 128 columns, outputs dim columns each. Weights (fp16,
-// 64 columns) overwrite the upper half of their scores, so that the lower half
-// of the next tile's scores can be issued at once behind the product that
-// still reads the weights, and only the upper half waits for it. The halves
-// alternate: while one's softmax runs, the other's products do.
+//   warps 12, 13    one thread each issues the MMAs of a half;
+//   warp 14         walks the share and hands every role its segments (the part of a
+//                   unit that this CTA computes) through a ring in shared memory, which
+//                   keeps the walk's state out of their registers; warp 15 idles.
+// TMEM: scores of either half 128 columns, outputs dim columns each; the weights (fp16, 64
+// columns) overwrite the upper half of their scores. A half's chain is scores, softmax,
+// product, and only then the next scores; the other half's runs in its gaps.
 #include "tg_device.cuh"
 #include "tg_kv_split.cuh"
 
@@ -39,6 +40,8 @@ constexpr int kThreads = kSoftmaxThreads + kConvThreads + 128;   // the last fou
 constexpr int kRegs = 128, kRegsSoftmax = 168, kRegsConv = 104, kRegsIssue = 64;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsConv + 128 * kRegsIssue <= kThreads * kRegs, "register split");
 constexpr int kScaleSlots = 4;           // tiles whose scales are in shared memory
+constexpr int kSegSlots = 4;             // segments handed out ahead
+constexpr int kSegReaders = 8 + 4 + 2;   // warps that read a segment: softmax, converters, issuers
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;            // + 128 half
 constexpr uint32_t kColP = 64;           // + 128 half
@@ -53,11 +56,12 @@ struct Smem {
     static constexpr int kV = 4 * kTile;                   // 2 stages
     static constexpr int kScales = 6 * kTile;              // slots x blocks x {k scale, log2 v scale, 1 / v scale}
     static constexpr int kBars = kScales + kScaleSlots * kBlocks * 3 * 4;
-    static constexpr int kNumBars = 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + kScaleSlots + 1;
+    static constexpr int kNumBars = 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + kScaleSlots + 2 + 2 * kSegSlots;
     static constexpr int kTmemSlot = kBars + 8 * kNumBars;
     static constexpr int kAbort = kTmemSlot + 4;
     static constexpr int kScan = (kAbort + 4 + 7) / 8 * 8;  // 16 int64, then found sequence and offset
-    static constexpr int kUsed = kScan + 16 * 8 + 16;
+    static constexpr int kSegments = kScan + 16 * 8 + 16;
+    static constexpr int kUsed = kSegments + kSegSlots * 64;
     static_assert(kBars % 8 == 0 && kScales % 16 == 0 && kScan % 8 == 0, "alignment");
     static_assert(kUsed + 1024 <= 227 * 1024, "shared memory of one CTA");
     static constexpr int kAlloc = kUsed + 1024;
@@ -103,12 +107,15 @@ __device__ __forceinline__ TileWork tile_work(const SplitWork& a, int i) {
     return w;
 }
 
-// The segments of a CTA's share, one after another: every role walks them by itself.
+// One piece of a CTA's share: tiles t0 .. t1 - 1 of a unit (none: the share is done).
 struct Segment {
     int seq, head, block, first, count, len;
     int tile0, tiles;   // of the unit
     int t0, t1;         // the segment's among them
 };
+static_assert(sizeof(Segment) <= 64, "a slot of the ring");
+
+// The segments of a CTA's share, one after another.
 
 struct Walk {
     const SplitWork& a;
@@ -184,7 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
         return b;
     };
     const uint32_t q_full = bars(2), k_full = bars(2), k_empty = bars(2), v_full = bars(2), v_empty = bars(2), s_full = bars(2);
-    const uint32_t p_full = bars(4), o_done = bars(2), scales_full = bars(kScaleSlots), drain = bars(1);
+    const uint32_t p_full = bars(4), o_done = bars(2), scales_full = bars(kScaleSlots), drain = bars(2);
+    const uint32_t seg_full = bars(kSegSlots), seg_empty = bars(kSegSlots);
+
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
     int64_t* scan = reinterpret_cast<int64_t*>(smem + L::kScan);
@@ -196,15 +205,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + 8 * i, 4);           // a warp's rows of one half each
             mbar_init(k_full + 8 * i, kConvThreads / 32);
-            mbar_init(k_empty + 8 * i, 1);
+            mbar_init(k_empty + 8 * i, 2);          // either half's products
             mbar_init(v_full + 8 * i, kConvThreads / 32);
-            mbar_init(v_empty + 8 * i, 1);
+            mbar_init(v_empty + 8 * i, 2);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(o_done + 8 * i, 1);
         }
         for (int i = 0; i < 4; ++i) mbar_init(p_full + 8 * i, 4);
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(scales_full + 8 * i, 1);
-        mbar_init(drain, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(drain + 8 * i, 1);
+        for (int i = 0; i < kSegSlots; ++i) {
+            mbar_init(seg_full + 8 * i, 1);
+            mbar_init(seg_empty + 8 * i, kSegReaders);
+        }
         fence_barrier_init();
         *abort_flag = 0;
     }
@@ -267,79 +280,89 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const WaitCtx wc{abort_flag, c.wd.status, c.wd.limit_ns};
-    Walk walk(a, *found_seq, *found_off, stop - start);
+    // the next segment for this warp; false when there is none, or a wait gave up
+    uint32_t seg_no = 0;
+    auto next_segment = [&](Segment& s) {
+        const uint32_t slot = seg_no % kSegSlots;
+        if (!__all_sync(0xFFFFFFFFu, wait_phase(seg_full + 8 * slot, (seg_no / kSegSlots) & 1u, wc, kSiteMmaFull))) return false;
+        s = *reinterpret_cast<const Segment*>(smem + L::kSegments + slot * 64);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_empty + 8 * slot);
+        ++seg_no;
+        return s.t1 > s.t0;
+    };
     Segment sg;
     uint32_t tile_no = 0;  // tiles so far: stages and phases
 
     if (warp >= 12) {
-        // ------------------------------------------------------------ MMA issue
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        if (warp == 12 && lane == 0) {
-            constexpr uint32_t idesc_s = idesc_f16_f32(128, 64, false, false);
+        if (warp == 14) {
+            // -------------------------------------------------------- segments
+            if (lane == 0) {
+                Walk walk(a, *found_seq, *found_off, stop - start);
+                for (bool more = true; more; ++seg_no) {
+                    const uint32_t slot = seg_no % kSegSlots;
+                    if (!wait_phase_sleep(seg_empty + 8 * slot, ((seg_no / kSegSlots) & 1u) ^ 1u, wc, kSiteProducerEmpty, 64)) break;
+                    more = walk.next(sg);
+                    if (!more) sg.t0 = sg.t1 = 0;
+                    *reinterpret_cast<Segment*>(smem + L::kSegments + slot * 64) = sg;
+                    mbar_arrive(seg_full + 8 * slot);
+                }
+            }
+            __syncwarp();
+        } else if (warp < 14) {
+            // -------------------------------------------------------- MMA issue of half h
+            const int h = warp - 12;
+            constexpr uint32_t idesc_s = idesc_f16_f32(128, 128, false, false);
             constexpr uint32_t idesc_o = idesc_f16_f32(128, kDim, false, true);
-            // keys 64 part .. 64 part + 63 of the scores of half h
-            auto scores = [&](int h, int part, uint32_t stage) {
-#pragma unroll
-                for (int kk = 0; kk < kDim / 16; ++kk) {
-                    const uint32_t in = (kk >> 2) * L::kBox;
-                    const uint64_t off = static_cast<uint64_t>(((kk & 3) * 32) >> 4);
-                    const uint64_t qd = smem_desc_sw128(sbase + L::kQ + h * L::kTile + in, 16, 1024) + off;
-                    const uint64_t kd = smem_desc_sw128(sbase + L::kK + stage * L::kTile + in + part * 64 * 128, 16, 1024) + off;
-                    mma_f16(tmem + kColS + 128 * h + 64 * part, qd, kd, idesc_s, kk != 0);
-                }
-            };
-            auto outputs = [&](int h, int part, uint32_t stage, bool first) {
-#pragma unroll
-                for (int kk = 4 * part; kk < 4 * part + 4; ++kk) {
-                    const uint64_t vd = smem_desc_sw128(sbase + L::kV + stage * L::kTile, L::kBox, 1024) + static_cast<uint64_t>((kk * 2048) >> 4);
-                    mma_f16_tmem_a(tmem + kColO + 128 * h, tmem + kColP + 128 * h + kk * 8, vd, idesc_o, !first || kk != 0);
-                }
-            };
+            const uint64_t qd = smem_desc_sw128(sbase + L::kQ + h * L::kTile, 16, 1024);
+            const uint64_t kd = smem_desc_sw128(sbase + L::kK, 16, 1024);
+            const uint64_t vd = smem_desc_sw128(sbase + L::kV, L::kBox, 1024);
+            const uint32_t col_s = tmem + kColS + 128 * h, col_p = tmem + kColP + 128 * h, col_o = tmem + kColO + 128 * h;
             bool ok = true;
-            uint32_t seg = 0;
-            for (; ok && walk.next(sg); ++seg) {
-                const int n = sg.t1 - sg.t0;
-                for (int j = -1; ok && j < n; ++j) {  // j = -1: the first tile's scores
-                    const uint32_t g = tile_no + j, ph = g & 1u;                    // tile j
-                    const uint32_t g1 = g + 1, st1 = g1 & 1u, kph = (g1 >> 1) & 1u;  // tile j + 1
-                    const bool more = j + 1 < n;
-                    for (int h = 0; ok && h < 2; ++h) {
-                        if (j < 0) {
-                            ok = wait_phase(q_full + 8 * h, seg & 1u, wc, kSiteMmaFull);
-                        } else {
-                            ok = wait_phase(p_full + 16 * h, ph, wc, kSiteMmaFull) &&
-                                 wait_phase(v_full + 8 * (g & 1u), (g >> 1) & 1u, wc, kSiteMmaFull);
-                            if (!ok) break;
-                            tc_fence_after_sync();
-                            outputs(h, 0, g & 1u, j == 0);
-                            ok = wait_phase(p_full + 16 * h + 8, ph, wc, kSiteMmaFull);
-                            if (!ok) break;
-                            tc_fence_after_sync();
-                            outputs(h, 1, g & 1u, false);
-                            mma_commit(o_done + 8 * h);
-                            if (h == 1) mma_commit(v_empty + 8 * (g & 1u));
-                        }
-                        if (!ok || !more) continue;
-                        ok = wait_phase(k_full + 8 * st1, kph, wc, kSiteMmaFull);
+            while (ok && next_segment(sg)) {
+                if (lane == 0) {
+                    const int n = sg.t1 - sg.t0;
+                    ok = wait_phase(q_full + 8 * h, (seg_no - 1) & 1u, wc, kSiteMmaFull);
+                    for (int j = 0; ok && j < n; ++j) {
+                        const uint32_t g = tile_no + j, st = g & 1u, kph = (g >> 1) & 1u;
+                        // the scores overwrite the weights of tile j - 1
+                        ok = wait_phase(k_full + 8 * st, kph, wc, kSiteMmaFull) &&
+                             (j == 0 || wait_phase(o_done + 8 * h, (g - 1) & 1u, wc, kSiteMmaAccEmpty));
                         if (!ok) break;
                         tc_fence_after_sync();
-                        scores(h, 0, st1);
-                        if (j >= 0) {  // the upper half overwrites the weights of tile j
-                            ok = wait_phase(o_done + 8 * h, ph, wc, kSiteMmaAccEmpty);
-                            if (!ok) break;
-                            tc_fence_after_sync();
+#pragma unroll
+                        for (int kk = 0; kk < kDim / 16; ++kk) {
+                            const uint32_t in = ((kk >> 2) * L::kBox + (kk & 3) * 32) >> 4;
+                            mma_f16(col_s, qd + in, kd + st * (L::kTile >> 4) + in, idesc_s, kk != 0);
                         }
-                        scores(h, 1, st1);
                         mma_commit(s_full + 8 * h);
-                        if (h == 1) mma_commit(k_empty + 8 * st1);
+                        mma_commit(k_empty + 8 * st);
+                        ok = wait_phase(p_full + 16 * h, g & 1u, wc, kSiteMmaFull) && wait_phase(v_full + 8 * st, kph, wc, kSiteMmaFull);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16_tmem_a(col_o, col_p + kk * 8, vd + st * (L::kTile >> 4) + kk * (2048 >> 4), idesc_o, j != 0 || kk != 0);
+                        ok = wait_phase(p_full + 16 * h + 8, g & 1u, wc, kSiteMmaFull);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int kk = 4; kk < 8; ++kk)
+                            mma_f16_tmem_a(col_o, col_p + kk * 8, vd + st * (L::kTile >> 4) + kk * (2048 >> 4), idesc_o, 1);
+                        mma_commit(o_done + 8 * h);
+                        mma_commit(v_empty + 8 * st);
                     }
+                    tile_no += n;
                 }
-                tile_no += n;
+                ok = __all_sync(0xFFFFFFFFu, ok);
             }
-            mma_commit(drain);
-            wait_phase_drain(drain, 0, wc);
+            if (lane == 0) {
+                mma_commit(drain + 8 * h);
+                wait_phase_drain(drain + 8 * h, 0, wc);
+            }
+            __syncwarp();
         }
-        __syncwarp();
     } else if (warp >= 8) {
         // ------------------------------------------------------------ codes to fp16 tiles
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
@@ -385,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
             }
         };
         Segment nx;  // one tile ahead
-        bool have = walk.next(nx);
+        bool have = next_segment(nx);
         int tile = have ? nx.t0 : 0;
         int pg = have ? page_of(nx, tile) : -1;
         uint4 kx[kPasses], vx[kPasses];
@@ -396,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
             const int cur_tile = tile, cur_pg = pg;
             load(c.cache.v, cur, cur_tile, cur_pg, vx);
             if (++tile >= nx.t1) {
-                have = walk.next(nx);
+                have = next_segment(nx);
                 tile = nx.t0;
             }
             if (have) pg = page_of(nx, tile);
@@ -443,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
         bool ok = true;
         bool first_segment = true;
         int64_t pos = start;
-        while (ok && walk.next(sg)) {
+        while (ok && next_segment(sg)) {
             if (first_segment && threadIdx.x == 0) a.meta[k] = Meta{pos - sg.t0, total, sg.t0 > 0 ? sg.tiles : 0, sg.seq, sg.head, sg.block};
             const int r = sg.block * kRows + h * kHalfRows + row;      // row of the (sequence, kv head)
             const bool real = r < sg.count * a.share;
