@@ -48,7 +48,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStep = 16;                    // tokens per warp and step
 constexpr int kChunk = kWarps * kStep;       // tokens per unit of the work list
 constexpr int kStages = 4;                   // steps in flight per warp
 
@@ -101,14 +100,6 @@ __device__ __forceinline__ int mma_token(int i) {
         const int r = i & 7;                          // lines of two tokens: 0 1 4 5 8 9 12 13, then two further
         return ((r >> 1) * 4 + (r & 1)) + ((i & 8) ? 2 : 0);
     }
-}
-
-// Byte offset of piece `at` (bytes) of token t in a swizzled half stage.
-template <int kDim>
-__device__ __forceinline__ int ring_offset(int t, int at) {
-    const int line = kDim == 128 ? t : t >> 1;
-    const int in = kDim == 128 ? at : (t & 1) * 64 + at;
-    return line * 128 + (in ^ ((line & 7) << 4));
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -644,7 +635,7 @@ int64_t kv_attn_workspace(const KvAttnCall& c, int sm_count) {
 
 cudaError_t launch_kv_attn(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count,
                            cudaStream_t stream) {
-    if (!few_rows(c)) return launch_kv_attn_tile(c, workspace, sm_count, stream);
+    if (!few_rows(c)) return launch_kv_attn_tile(c, tmK, tmV, workspace, sm_count, stream);
     const bool h = c.dtype == kFp16, e4 = c.cache.fmt == kKvE4M3, d128 = c.cache.dim == 128;
     auto go = [&](auto* f) { return f(c, tmK, tmV, workspace, sm_count, stream); };
     if (h && e4) return d128 ? go(launch<__half, kKvE4M3, 128>) : go(launch<__half, kKvE4M3, 64>);

@@ -6,20 +6,20 @@
 // A unit is a sequence, a kv head and a block of 256 rows (query heads of one
 // kv head, token by token); its list entries are tiles of 128 keys, from the
 // first that any row sees to the last. One CTA per SM walks its share:
-//   warps 0-3, 4-7  softmax of rows 0-127 and 128-255, a thread a row (its TMEM
-//                   lane), all 128 scores of a tile in registers. They also
+//   warps 0-7, 8-15 softmax of rows 0-127 and 128-255, two threads a row (its TMEM
+//                   lane), 64 scores of a tile each, in registers. They also
 //                   bring the rows of Q to shared memory and write the result;
-//   warps 8-11      read the codes of 128 keys, then of their values, 16 bytes a
-//                   thread and a tile ahead, and leave them as fp16 (exact) in
-//                   128-byte-swizzled tiles, two of each; once for both halves
-//                   of the rows, which is what the 256 rows are for;
-//   warps 12, 13    one thread each issues the MMAs of a half;
-//   warp 14         walks the share and hands every role its segments (the part of a
-//                   unit that this CTA computes) through a ring in shared memory, which
-//                   keeps the walk's state out of their registers; warp 15 idles.
-// TMEM: scores of either half 128 columns, outputs dim columns each; the weights (fp16, 64
-// columns) overwrite the upper half of their scores. A half's chain is scores, softmax,
-// product, and only then the next scores; the other half's runs in its gaps.
+//   warps 16-19     turn codes, 64 tokens at a time, into fp16 (exact) tiles with the
+//                   128-byte swizzle, two of keys and two of values: once for both
+//                   halves of the rows, which is what the 256 rows are for;
+//   warps 20, 21    one thread each issues the MMAs of a half;
+//   warp 22         walks the share and hands the segments (the part of a unit that
+//                   this CTA computes) to the others through a ring in shared memory;
+//   warp 23         looks up pages and scales a tile ahead and has TMA bring the
+//                   codes into a ring of three 64-token slots.
+// TMEM: scores of either half 128 columns, outputs dim columns each; the weights (fp16)
+// overwrite the scores they come from. A half's chain is scores, softmax, product, and
+// only then the next scores; the other half's runs in its gaps.
 #include "tg_device.cuh"
 #include "tg_kv_split.cuh"
 
@@ -31,40 +31,54 @@ namespace {
 constexpr int kHalfRows = 128;
 constexpr int kRows = 2 * kHalfRows;
 constexpr int kKeys = 128;               // keys a tile
-constexpr int kBlocks = kKeys / 16;      // blocks of 16 keys with one scale each (a page has at least 16)
-constexpr int kSoftmaxThreads = 256;
+constexpr int kBlocks = kKeys / kStep;   // blocks of 16 keys with one scale each (a page has at least 16)
+constexpr int kSoftmaxThreads = 512;
 constexpr int kConvThreads = 128;
-constexpr int kThreads = kSoftmaxThreads + kConvThreads + 128;   // the last four warps: one issues, three idle
-// Registers a thread: all start with kRegs; the softmax threads, which hold 128 scores, take what the
-// others give up. The sum (64512) stays within the launch's 512 x 128.
-constexpr int kRegs = 128, kRegsSoftmax = 168, kRegsConv = 104, kRegsIssue = 64;
-static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsConv + 128 * kRegsIssue <= kThreads * kRegs, "register split");
-constexpr int kScaleSlots = 4;           // tiles whose scales are in shared memory
+constexpr int kThreads = kSoftmaxThreads + kConvThreads + 128;
+// Registers a thread: all start with kRegs; the softmax threads, which hold 64 scores, take what the
+// others give up, within the launch's kThreads x kRegs.
+constexpr int kRegs = 80, kRegsSoftmax = 96, kRegsConv = 56, kRegsIssue = 40;
+static_assert(kSoftmaxThreads * kRegsSoftmax + kConvThreads * kRegsConv + 128 * kRegsIssue <= kThreads * kRegs, "register split");
+static_assert(kRegsSoftmax >= kRegs && kRegsConv <= kRegs && kRegsIssue <= kRegs, "who takes and who gives");
+constexpr int kInfoSlots = 8;            // tiles whose scales are in shared memory (four can be in use)
 constexpr int kSegSlots = 4;             // segments handed out ahead
-constexpr int kSegReaders = 8 + 4 + 2;   // warps that read a segment: softmax, converters, issuers
+constexpr int kSegReaders = 16 + 2 + 1;  // warps that read a segment: softmax, issuers, loader
+constexpr int kRawSlots = 3;             // 64-token pieces of codes in flight
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0;            // + 128 half
-constexpr uint32_t kColP = 64;           // + 128 half
+constexpr uint32_t kColS = 0;            // + 128 half; the weights of keys 64 g .. are the first 32 of their 64 columns
 constexpr uint32_t kColO = 256;          // + 128 half
+
+// What the softmax and the converters know of a tile: per block of 16 keys the key scale, log2 and
+// inverse of the value scale, and how many tokens are there.
+struct TileInfo {
+    float ks[kBlocks], lv[kBlocks], iv[kBlocks];
+    int there[kBlocks];
+};
 
 template <int kDim>
 struct Smem {
     static constexpr int kBox = 128 * 128;                 // 128 rows of 64 fp16
     static constexpr int kTile = kBox * (kDim / 64);
+    static constexpr int kRaw = 64 * kDim;                 // bytes of a 64-token piece
     static constexpr int kQ = 0;                           // 2 halves
     static constexpr int kK = 2 * kTile;                   // 2 stages
     static constexpr int kV = 4 * kTile;                   // 2 stages
-    static constexpr int kScales = 6 * kTile;              // slots x blocks x {k scale, log2 v scale, 1 / v scale}
-    static constexpr int kBars = kScales + kScaleSlots * kBlocks * 3 * 4;
-    static constexpr int kNumBars = 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + kScaleSlots + 2 + 2 * kSegSlots;
-    static constexpr int kTmemSlot = kBars + 8 * kNumBars;
+    static constexpr int kRawAt = 6 * kTile;
+    static constexpr int kRed = kRawAt + kRawSlots * kRaw; // [parity][half][key half][row] floats
+    static constexpr int kInfo = kRed + 2 * 2 * 2 * kHalfRows * 4;
+    static constexpr int kSegments = kInfo + kInfoSlots * static_cast<int>(sizeof(TileInfo));
+    static constexpr int kBars = kSegments + kSegSlots * 64;
+    static constexpr int kNumBars = 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + kInfoSlots + 2 + 2 * kSegSlots + 2 * kRawSlots;
+    static constexpr int kScan = kBars + 8 * kNumBars;      // a sum a warp, then found offset and sequence
+    static constexpr int kFoundOff = kScan + kThreads / 32 * 8;
+    static constexpr int kFoundSeq = kFoundOff + 8;
+    static constexpr int kTmemSlot = kFoundSeq + 4;
     static constexpr int kAbort = kTmemSlot + 4;
-    static constexpr int kScan = (kAbort + 4 + 7) / 8 * 8;  // 16 int64, then found sequence and offset
-    static constexpr int kSegments = kScan + 16 * 8 + 16;
-    static constexpr int kUsed = kSegments + kSegSlots * 64;
-    static_assert(kBars % 8 == 0 && kScales % 16 == 0 && kScan % 8 == 0, "alignment");
-    static_assert(kUsed + 1024 <= 227 * 1024, "shared memory of one CTA");
+    static constexpr int kUsed = kAbort + 4;
     static constexpr int kAlloc = kUsed + 1024;
+    static_assert(kRed % 16 == 0 && kInfo % 16 == 0 && kSegments % 16 == 0 && kBars % 8 == 0 && kScan % 8 == 0 && kFoundOff % 8 == 0, "alignment");
+    static_assert(kRawAt % 1024 == 0 && kRaw % 1024 == 0, "swizzle atoms");
+    static_assert(kAlloc <= 227 * 1024, "shared memory of one CTA");
 };
 
 // A sequence and the tiles of its row blocks.
@@ -177,7 +191,8 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
 }
 
 template <typename E, int kFmt, int kDim>
-__global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const SplitWork a) {
     using L = Smem<kDim>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -191,35 +206,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
         return b;
     };
     const uint32_t q_full = bars(2), k_full = bars(2), k_empty = bars(2), v_full = bars(2), v_empty = bars(2), s_full = bars(2);
-    const uint32_t p_full = bars(4), o_done = bars(2), scales_full = bars(kScaleSlots), drain = bars(2);
-    const uint32_t seg_full = bars(kSegSlots), seg_empty = bars(kSegSlots);
-
+    const uint32_t p_full = bars(4), o_done = bars(2), info_full = bars(kInfoSlots), drain = bars(2);
+    const uint32_t seg_full = bars(kSegSlots), seg_empty = bars(kSegSlots), raw_full = bars(kRawSlots), raw_empty = bars(kRawSlots);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
     int64_t* scan = reinterpret_cast<int64_t*>(smem + L::kScan);
-    int* found_seq = reinterpret_cast<int*>(smem + L::kScan + 16 * 8);
-    int64_t* found_off = reinterpret_cast<int64_t*>(smem + L::kScan + 16 * 8 + 8);
-    float* scales = reinterpret_cast<float*>(smem + L::kScales);
+    int* found_seq = reinterpret_cast<int*>(smem + L::kFoundSeq);
+    int64_t* found_off = reinterpret_cast<int64_t*>(smem + L::kFoundOff);
+    TileInfo* infos = reinterpret_cast<TileInfo*>(smem + L::kInfo);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full + 8 * i, 4);           // a warp's rows of one half each
+            mbar_init(q_full + 8 * i, 8);           // a warp's share of one half's rows
             mbar_init(k_full + 8 * i, kConvThreads / 32);
             mbar_init(k_empty + 8 * i, 2);          // either half's products
             mbar_init(v_full + 8 * i, kConvThreads / 32);
             mbar_init(v_empty + 8 * i, 2);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(o_done + 8 * i, 1);
+            mbar_init(drain + 8 * i, 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(p_full + 8 * i, 4);
-        for (int i = 0; i < kScaleSlots; ++i) mbar_init(scales_full + 8 * i, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(drain + 8 * i, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(p_full + 8 * i, 8);
+        for (int i = 0; i < kInfoSlots; ++i) mbar_init(info_full + 8 * i, 1);
         for (int i = 0; i < kSegSlots; ++i) {
             mbar_init(seg_full + 8 * i, 1);
             mbar_init(seg_empty + 8 * i, kSegReaders);
         }
+        for (int i = 0; i < kRawSlots; ++i) {
+            mbar_init(raw_full + 8 * i, 1);
+            mbar_init(raw_empty + 8 * i, kConvThreads / 32);
+        }
         fence_barrier_init();
         *abort_flag = 0;
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
     }
 
     // ---- this CTA's share of the list
@@ -271,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
             *found_off = start - before;
         }
     }
-    if (warp == 12) {
+    if (warp == 20) {
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
@@ -294,9 +314,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
     Segment sg;
     uint32_t tile_no = 0;  // tiles so far: stages and phases
 
-    if (warp >= 12) {
+    if (warp >= 20) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        if (warp == 14) {
+        if (warp == 22) {
             // -------------------------------------------------------- segments
             if (lane == 0) {
                 Walk walk(a, *found_seq, *found_off, stop - start);
@@ -310,15 +330,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
                 }
             }
             __syncwarp();
-        } else if (warp < 14) {
+        } else if (warp < 22) {
             // -------------------------------------------------------- MMA issue of half h
-            const int h = warp - 12;
+            const int h = warp - 20;
             constexpr uint32_t idesc_s = idesc_f16_f32(128, 128, false, false);
             constexpr uint32_t idesc_o = idesc_f16_f32(128, kDim, false, true);
             const uint64_t qd = smem_desc_sw128(sbase + L::kQ + h * L::kTile, 16, 1024);
             const uint64_t kd = smem_desc_sw128(sbase + L::kK, 16, 1024);
             const uint64_t vd = smem_desc_sw128(sbase + L::kV, L::kBox, 1024);
-            const uint32_t col_s = tmem + kColS + 128 * h, col_p = tmem + kColP + 128 * h, col_o = tmem + kColO + 128 * h;
+            const uint32_t col_s = tmem + kColS + 128 * h, col_o = tmem + kColO + 128 * h;
+            // 16 keys of the product; their weights are 8 columns
+            auto product = [&](int kk, uint32_t st, bool add) {
+                mma_f16_tmem_a(col_o, col_s + (kk >> 2) * 64 + (kk & 3) * 8, vd + st * (L::kTile >> 4) + kk * (2048 >> 4), idesc_o, add);
+            };
             bool ok = true;
             while (ok && next_segment(sg)) {
                 if (lane == 0) {
@@ -341,15 +365,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
                         ok = wait_phase(p_full + 16 * h, g & 1u, wc, kSiteMmaFull) && wait_phase(v_full + 8 * st, kph, wc, kSiteMmaFull);
                         if (!ok) break;
                         tc_fence_after_sync();
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f16_tmem_a(col_o, col_p + kk * 8, vd + st * (L::kTile >> 4) + kk * (2048 >> 4), idesc_o, j != 0 || kk != 0);
+                        product(0, st, j != 0);  // keys 0-31 and 64-95 are handed over first
+                        product(1, st, true);
+                        product(4, st, true);
+                        product(5, st, true);
                         ok = wait_phase(p_full + 16 * h + 8, g & 1u, wc, kSiteMmaFull);
                         if (!ok) break;
                         tc_fence_after_sync();
-#pragma unroll
-                        for (int kk = 4; kk < 8; ++kk)
-                            mma_f16_tmem_a(col_o, col_p + kk * 8, vd + st * (L::kTile >> 4) + kk * (2048 >> 4), idesc_o, 1);
+                        product(2, st, true);
+                        product(3, st, true);
+                        product(6, st, true);
+                        product(7, st, true);
                         mma_commit(o_done + 8 * h);
                         mma_commit(v_empty + 8 * st);
                     }
@@ -362,116 +388,151 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
                 wait_phase_drain(drain + 8 * h, 0, wc);
             }
             __syncwarp();
+        } else {
+            // -------------------------------------------------------- pages, scales and the copies of the codes
+            // a lane per block of 16 keys
+            auto page_of = [&](const Segment& s, int tile) {
+                const int token = (s.tile0 + tile) * kKeys + lane * kStep;
+                if (lane >= kBlocks || token >= s.len) return -1;
+                return seq_page(c.batch, c.cache, s.seq, token >> a.page_shift, c.wd);
+            };
+            uint32_t piece = 0;  // 64-token pieces so far
+            bool have = next_segment(sg);
+            int tile = sg.t0;
+            int pg = have ? page_of(sg, tile) : -1;
+            while (have) {
+                const int head = sg.head, token = (sg.tile0 + tile) * kKeys + lane * kStep, len = sg.len, cur = pg;
+                const int64_t ph = static_cast<int64_t>(max(cur, 0)) * c.cache.kv_heads + head;
+                float ks = 0.0f, vs = 1.0f;
+                if (cur >= 0) {
+                    ks = __ldg(c.cache.k_scale + ph);
+                    vs = __ldg(c.cache.v_scale + ph);
+                }
+                if (++tile >= sg.t1) {
+                    have = next_segment(sg);
+                    tile = sg.t0;
+                }
+                if (have) pg = page_of(sg, tile);
+                const int64_t place = ph * c.cache.page + (token & (c.cache.page - 1));
+                const int line = static_cast<int>(kDim == 128 ? place : place >> 1);
+                bool ok = true;
+                for (int part = 0; part < 4; ++part, ++piece) {  // keys 0-63, 64-127, then values
+                    const uint32_t slot = piece % kRawSlots;
+                    ok = wait_phase_sleep(raw_empty + 8 * slot, ((piece / kRawSlots) & 1u) ^ 1u, wc, kSiteConvEmpty, 32);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    if (part == 0) {
+                        TileInfo& info = infos[tile_no % kInfoSlots];
+                        if (lane < kBlocks) {
+                            vs = max_nan(vs, kScaleFloor);
+                            info.ks[lane] = ks;
+                            info.lv[lane] = cur >= 0 ? log2f(vs) : -INFINITY;  // no page: no weight
+                            info.iv[lane] = 1.0f / vs;
+                            info.there[lane] = cur >= 0 ? min(kStep, len - token) : 0;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(info_full + 8 * (tile_no % kInfoSlots));
+                    }
+                    const bool mine = lane < kBlocks && (lane >> 2) == (part & 1) && cur >= 0;
+                    const uint32_t many = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+                    const uint32_t bar_at = raw_full + 8 * slot;
+                    if (lane == 0) {
+                        if (many > 0) mbar_arrive_expect_tx(bar_at, many * kStep * kDim);
+                        else mbar_arrive(bar_at);
+                    }
+                    __syncwarp();
+                    if (mine) tma_load_2d(sbase + L::kRawAt + slot * L::kRaw + (lane & 3) * kStep * kDim, part < 2 ? &tmK : &tmV, bar_at, 0, line);
+                }
+                if (!ok) break;
+                ++tile_no;
+            }
+            // the converters stop at a tile of which nothing is said but that it is the end
+            if (!have) {
+                TileInfo& info = infos[tile_no % kInfoSlots];
+                if (lane == 0 && wait_phase_sleep(raw_empty + 8 * (piece % kRawSlots), ((piece / kRawSlots) & 1u) ^ 1u, wc, kSiteConvEmpty, 32)) {
+                    info.there[0] = -1;
+                    mbar_arrive(info_full + 8 * (tile_no % kInfoSlots));
+                }
+            }
+            // let every copy in flight land before the CTA ends
+            for (uint32_t i = piece > kRawSlots ? piece - kRawSlots : 0; lane == 0 && i < piece; ++i)
+                wait_phase_drain(raw_full + 8 * (i % kRawSlots), (i / kRawSlots) & 1u, wc);
+            __syncwarp();
         }
-    } else if (warp >= 8) {
+    } else if (warp >= 16) {
         // ------------------------------------------------------------ codes to fp16 tiles
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
         const int tid = threadIdx.x - kSoftmaxThreads;
         constexpr int kLanes = kDim / 16;            // threads a row of codes
         constexpr int kPass = kConvThreads / kLanes; // rows a pass: 16 or 32
-        constexpr int kPasses = kKeys / kPass;
-        const int row_in = tid / kLanes, piece = tid % kLanes;
-        // a lane of each warp per block of 16 keys: its page
-        auto page_of = [&](const Segment& s, int tile) {
-            const int token = (s.tile0 + tile) * kKeys + lane * 16;
-            if (lane >= kBlocks || token >= s.len) return -1;
-            return seq_page(c.batch, c.cache, s.seq, token >> a.page_shift, c.wd);
-        };
-        auto load = [&](const uint8_t* codes, const Segment& s, int tile, int pg, uint4 (&x)[kPasses]) {
-#pragma unroll
-            for (int i = 0; i < kPasses; ++i) {
-                const int t = i * kPass + row_in, token = (s.tile0 + tile) * kKeys + t;
-                const int p = __shfl_sync(0xFFFFFFFFu, pg, t >> 4);
-                x[i] = make_uint4(0, 0, 0, 0);
-                if (p >= 0 && token < s.len) {
-                    const int64_t row = (static_cast<int64_t>(p) * c.cache.kv_heads + s.head) * c.cache.page + (token & (c.cache.page - 1));
-                    x[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * kDim + piece * 16));
-                }
-            }
-        };
-        auto store = [&](uint32_t tile_base, const uint4 (&x)[kPasses]) {
-#pragma unroll
-            for (int i = 0; i < kPasses; ++i) {
-                const int t = i * kPass + row_in;
-                uint32_t h[8];
-                codes_to_half<kFmt>(x[i].x, h[0], h[1]);
-                codes_to_half<kFmt>(x[i].y, h[2], h[3]);
-                codes_to_half<kFmt>(x[i].z, h[4], h[5]);
-                codes_to_half<kFmt>(x[i].w, h[6], h[7]);
-                // 16 codes are two 16-byte pieces of a box's row; rows' upper lanes write the odd one first,
-                // so that a quarter-warp's eight go to eight banks
-                const uint32_t line = tile_base + (piece >> 2) * L::kBox + t * 128;
-                const int odd = piece >> 2, c0 = (piece & 3) * 2;
-                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                sts_v4(line + (((c0 + odd) ^ (t & 7)) << 4), odd ? hi : lo);
-                sts_v4(line + (((c0 + 1 - odd) ^ (t & 7)) << 4), odd ? lo : hi);
-            }
-        };
-        Segment nx;  // one tile ahead
-        bool have = next_segment(nx);
-        int tile = have ? nx.t0 : 0;
-        int pg = have ? page_of(nx, tile) : -1;
-        uint4 kx[kPasses], vx[kPasses];
-        if (have) load(c.cache.k, nx, tile, pg, kx);
-        while (have) {
+        constexpr int kPasses = 64 / kPass;
+        const int row_in = tid / kLanes, at = tid % kLanes;
+        uint32_t piece = 0;
+        bool ok = true;
+        while (ok) {
             const uint32_t st = tile_no & 1u, eph = ((tile_no >> 1) & 1u) ^ 1u;
-            const Segment cur = nx;
-            const int cur_tile = tile, cur_pg = pg;
-            load(c.cache.v, cur, cur_tile, cur_pg, vx);
-            if (++tile >= nx.t1) {
-                have = next_segment(nx);
-                tile = nx.t0;
-            }
-            if (have) pg = page_of(nx, tile);
-            // keys, and the scales of the tile's blocks
-            if (!__all_sync(0xFFFFFFFFu, wait_phase_sleep(k_empty + 8 * st, eph, wc, kSiteConvEmpty, 32))) break;
-            if (warp == 8) {
-                float* slot = scales + (tile_no % kScaleSlots) * kBlocks * 3;
-                if (lane < kBlocks) {
-                    const int64_t ph = static_cast<int64_t>(max(cur_pg, 0)) * c.cache.kv_heads + cur.head;
-                    float ks = 0.0f, lv = -INFINITY, iv = 1.0f;  // no page: no weight
-                    if (cur_pg >= 0) {
-                        ks = __ldg(c.cache.k_scale + ph);
-                        const float vs = max_nan(__ldg(c.cache.v_scale + ph), kScaleFloor);
-                        lv = log2f(vs);
-                        iv = 1.0f / vs;
-                    }
-                    slot[lane] = ks;
-                    slot[kBlocks + lane] = lv;
-                    slot[2 * kBlocks + lane] = iv;
-                }
+            ok = __all_sync(0xFFFFFFFFu, wait_phase(info_full + 8 * (tile_no % kInfoSlots), (tile_no / kInfoSlots) & 1u, wc, kSiteConvFull));
+            if (!ok) break;
+            const TileInfo& info = infos[tile_no % kInfoSlots];
+            if (info.there[0] < 0) break;
+            for (int part = 0; part < 4; ++part, ++piece) {
+                const uint32_t slot = piece % kRawSlots, raw = sbase + L::kRawAt + slot * L::kRaw;
+                ok = __all_sync(0xFFFFFFFFu, wait_phase(raw_full + 8 * slot, (piece / kRawSlots) & 1u, wc, kSiteConvFull));
+                if (!ok) break;
+                uint4 x[kPasses];
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) x[i] = lds_v4(raw + ring_offset<kDim>(i * kPass + row_in, at * 16));
                 __syncwarp();
-                if (lane == 0) mbar_arrive(scales_full + 8 * (tile_no % kScaleSlots));
+                if (lane == 0) mbar_arrive(raw_empty + 8 * slot);
+                if ((part & 1) == 0) {
+                    ok = __all_sync(0xFFFFFFFFu, wait_phase((part == 0 ? k_empty : v_empty) + 8 * st, eph, wc, kSiteConvEmpty));
+                    if (!ok) break;
+                }
+                const uint32_t base = sbase + (part < 2 ? L::kK : L::kV) + st * L::kTile + (at >> 2) * L::kBox;
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    const int t = (part & 1) * 64 + i * kPass + row_in;
+                    if ((t & 15) >= info.there[t >> 4]) x[i] = make_uint4(0, 0, 0, 0);  // past the end, or no page
+                    uint32_t h[8];
+                    codes_to_half<kFmt>(x[i].x, h[0], h[1]);
+                    codes_to_half<kFmt>(x[i].y, h[2], h[3]);
+                    codes_to_half<kFmt>(x[i].z, h[4], h[5]);
+                    codes_to_half<kFmt>(x[i].w, h[6], h[7]);
+                    // 16 codes are two 16-byte pieces of a box's row; the threads of the second box write the odd
+                    // one first, so that a quarter-warp's eight go to eight banks
+                    const uint32_t line = base + t * 128;
+                    const int odd = at >> 2, c0 = (at & 3) * 2;
+                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                    sts_v4(line + (((c0 + odd) ^ (t & 7)) << 4), odd ? hi : lo);
+                    sts_v4(line + (((c0 + 1 - odd) ^ (t & 7)) << 4), odd ? lo : hi);
+                }
+                if (part & 1) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive((part == 1 ? k_full : v_full) + 8 * st);
+                }
             }
-            store(sbase + L::kK + st * L::kTile, kx);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(k_full + 8 * st);
-            if (have) load(c.cache.k, nx, tile, pg, kx);
-            // values
-            if (!__all_sync(0xFFFFFFFFu, wait_phase_sleep(v_empty + 8 * st, eph, wc, kSiteConvEmpty, 32))) break;
-            store(sbase + L::kV + st * L::kTile, vx);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(v_full + 8 * st);
             ++tile_no;
         }
     } else {
         // ------------------------------------------------------------ softmax, Q and the result
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        const int h = warp >> 2;
+        const int h = warp >> 3, kh = (warp >> 2) & 1;                // rows' half, keys' half
         const int row = (warp & 3) * 32 + lane;                       // of the half: its TMEM lane
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t col_s = lanes + kColS + 128 * h, col_p = lanes + kColP + 128 * h, col_o = lanes + kColO + 128 * h;
+        const uint32_t col_s = lanes + kColS + 128 * h + 64 * kh, col_o = lanes + kColO + 128 * h + kh * (kDim / 2);
+        float* red = reinterpret_cast<float*>(smem + L::kRed) + (h * 2) * kHalfRows + row;  // + parity 4 * 128, + key half 128
         bool ok = true;
         bool first_segment = true;
-        int64_t pos = start;
-        while (ok && next_segment(sg)) {
-            if (first_segment && threadIdx.x == 0) a.meta[k] = Meta{pos - sg.t0, total, sg.t0 > 0 ? sg.tiles : 0, sg.seq, sg.head, sg.block};
+        while (true) {
+            // all of the half go on, or none: no warp waits at a barrier for one that has left
+            if (named_barrier_or(1 + h, 256, !next_segment(sg))) break;
+            if (first_segment && threadIdx.x == 0) a.meta[k] = Meta{start - sg.t0, total, sg.t0 > 0 ? sg.tiles : 0, sg.seq, sg.head, sg.block};
             const int r = sg.block * kRows + h * kHalfRows + row;      // row of the (sequence, kv head)
             const bool real = r < sg.count * a.share;
             const int t = r / a.share;
-            const int64_t out_row = static_cast<int64_t>(sg.first + t) * c.heads + sg.head * a.share + r - t * a.share;
             // Q: fp16 as it is; bf16 moved by a power of two so that the row's largest value lies in
             // [2^14, 2^15). A negative scale goes into Q, so that larger products mean larger weights.
             float f = fabsf(c.scale) * kLog2e;
@@ -481,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
                 if constexpr (!std::is_same<E, __half>::value) {
                     float most = 0.0f;
                     if (real) {
+#pragma unroll 4
                         for (int d = 0; d < kDim; d += 8) {
                             float v[8];
                             load_values<E, 8>(x, d, a.q_vec != 0, v);
@@ -493,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
                     f *= __int_as_float((e - 14 + 127) << 23);
                 }
 #pragma unroll 4
-                for (int d = 0; d < kDim; d += 8) {
+                for (int i = 0; i < kDim / 2; i += 8) {
+                    const int d = kh * (kDim / 2) + i;
                     float v[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] = 0.0f;
@@ -517,38 +580,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
             const int n = sg.t1 - sg.t0;
             for (int j = 0; j < n; ++j) {
                 const uint32_t g = tile_no + j, ph = g & 1u;
-                ok = wait_phase(scales_full + 8 * (g % kScaleSlots), (g / kScaleSlots) & 1u, wc, kSiteEpilogueAccFull) &&
+                // a wait that gave up still reaches the barrier of the maxima, where all of the half learn of it
+                ok = wait_phase(info_full + 8 * (g % kInfoSlots), (g / kInfoSlots) & 1u, wc, kSiteEpilogueAccFull) &&
                      wait_phase(s_full + 8 * h, ph, wc, kSiteEpilogueAccFull);
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
-                    break;
-                }
+                __syncwarp();
                 tc_fence_after_sync();
-                const float* sc = scales + (g % kScaleSlots) * kBlocks * 3;
-                uint32_t s[4][32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(col_s + 32 * q, s[q]);
+                const TileInfo& info = infos[g % kInfoSlots];
+                uint32_t s[2][32];
+                tmem_ld_32x32b_x32(col_s, s[0]);
+                tmem_ld_32x32b_x32(col_s + 32, s[1]);
                 tmem_ld_wait();
                 auto raw = [&](int i) { return __uint_as_float(s[i >> 5][i & 31]); };
-                const int key0 = (sg.tile0 + sg.t0 + j) * kKeys;
-                if (key0 < from || key0 + kKeys > to) {
+                const int key0 = (sg.tile0 + sg.t0 + j) * kKeys + 64 * kh;
+                if (key0 < from || key0 + 64 > to) {
 #pragma unroll
-                    for (int i = 0; i < kKeys; ++i)
+                    for (int i = 0; i < 64; ++i)
                         if (key0 + i < from || key0 + i >= to) s[i >> 5][i & 31] = __float_as_uint(-INFINITY);
                 }
-                __syncwarp();
-                // the tile's maximum, block by block
+                // this half's maximum, block by block, then the row's
                 float top = kNoMax;
 #pragma unroll
-                for (int b = 0; b < kBlocks; ++b) {
+                for (int b = 0; b < 4; ++b) {
                     float x = max3(raw(16 * b), raw(16 * b + 1), raw(16 * b + 2)), y = max3(raw(16 * b + 3), raw(16 * b + 4), raw(16 * b + 5));
                     x = max3(x, raw(16 * b + 6), raw(16 * b + 7));
                     y = max3(y, raw(16 * b + 8), raw(16 * b + 9));
                     x = max3(x, raw(16 * b + 10), raw(16 * b + 11));
                     y = max3(y, raw(16 * b + 12), raw(16 * b + 13));
                     x = max3(x, raw(16 * b + 14), raw(16 * b + 15));
-                    top = fmaxf(top, fmaf(fmaxf(x, y), fmaxf(f * sc[b], 1e-38f), sc[kBlocks + b]));
+                    top = fmaxf(top, fmaf(fmaxf(x, y), fmaxf(f * info.ks[4 * kh + b], 1e-38f), info.lv[4 * kh + b]));
                 }
+                red[ph * 4 * kHalfRows + kh * kHalfRows] = top;
+                if (named_barrier_or(1 + h, 256, !ok)) {
+                    ok = false;
+                    break;
+                }
+                top = fmaxf(top, red[ph * 4 * kHalfRows + (kh ^ 1) * kHalfRows]);
                 float keep = 1.0f;
                 bool grew = false;
                 if (top > m + kRescaleLog2) {
@@ -558,11 +624,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
                 }
                 float sum = 0.0f;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 2; ++q) {
                     uint32_t w[16];
 #pragma unroll
                     for (int b = 2 * q; b < 2 * q + 2; ++b) {
-                        const float cb = fmaxf(f * sc[b], 1e-38f), ob = sc[kBlocks + b] - m;
+                        const float cb = fmaxf(f * info.ks[4 * kh + b], 1e-38f), ob = info.lv[4 * kh + b] - m;
                         const float2 c2 = make_float2(cb, cb), o2 = make_float2(ob, ob);
                         float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -572,14 +638,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
                             part = __fadd2_rn(part, p);
                             w[(b & 1) * 8 + e] = half2_bits(p.x, p.y);
                         }
-                        sum = fmaf(part.x + part.y, sc[2 * kBlocks + b], sum);
+                        sum = fmaf(part.x + part.y, info.iv[4 * kh + b], sum);
                     }
-                    tmem_st_x16(col_p + 16 * q, w);
+                    tmem_st_x16(col_s + 16 * q, w);
                     // the outputs so far come to the new maximum before the first weights are handed over: the
-                    // products of the tile before have completed (this tile's scores were issued after them)
-                    if (q == 1 && j > 0 && __any_sync(0xFFFFFFFFu, grew)) {
+                    // product of the tile before has completed (this tile's scores were issued after it)
+                    if (q == 0 && j > 0 && __any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll 1
-                        for (int d = 0; d < kDim; d += 32) {
+                        for (int d = 0; d < kDim / 2; d += 32) {
                             uint32_t o[32];
                             tmem_ld_32x32b_x32(col_o + d, o);
                             tmem_ld_wait();
@@ -588,31 +654,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
                             tmem_st_32x32b_x32(col_o + d, o);
                         }
                     }
-                    if (q & 1) {
-                        tmem_st_wait();
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(p_full + 16 * h + 8 * (q >> 1));
-                    }
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full + 16 * h + 8 * q);
                 }
                 l = l * keep + sum;
             }
             if (!ok) break;
             tile_no += n;
-            if (!__all_sync(0xFFFFFFFFu, wait_phase_sleep(o_done + 8 * h, (tile_no - 1) & 1u, wc, kSiteEpilogueAccFull, 32))) {
+            ok = wait_phase_sleep(o_done + 8 * h, (tile_no - 1) & 1u, wc, kSiteEpilogueAccFull, 32);
+            // both key halves' sums; the maxima of the last tile were in the other parity
+            red[(tile_no & 1u) * 4 * kHalfRows + kh * kHalfRows] = l;
+            if (named_barrier_or(1 + h, 256, !ok)) {
                 ok = false;
                 break;
             }
+            l += red[(tile_no & 1u) * 4 * kHalfRows + (kh ^ 1) * kHalfRows];
             tc_fence_after_sync();
             const bool whole = sg.t0 == 0 && sg.t1 == sg.tiles;
             const float inv = row_inverse(l);
+            const int64_t out_row = static_cast<int64_t>(sg.first + t) * c.heads + sg.head * a.share + r - t * a.share;
             float* part = a.parts + (static_cast<int64_t>(2 * k) + (first_segment ? 0 : 1)) * kRows * (kDim + 2);
             const int pr = h * kHalfRows + row;
 #pragma unroll 1
-            for (int d = 0; d < kDim; d += 32) {
+            for (int i = 0; i < kDim / 2; i += 32) {
+                const int d = kh * (kDim / 2) + i;
                 uint32_t o[32];
                 __syncwarp();
-                tmem_ld_32x32b_x32(col_o + d, o);
+                tmem_ld_32x32b_x32(col_o + i, o);
                 tmem_ld_wait();
                 if (real && whole) {
                     E* y = static_cast<E*>(c.out) + out_row * kDim + d;
@@ -620,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
                     for (int e = 0; e < 32; e += 8) {
                         float v[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o[e + i]) * inv;
+                        for (int x = 0; x < 8; ++x) v[x] = __uint_as_float(o[e + x]) * inv;
                         store_values<E, 8>(y, e, true, v);
                     }
                 } else if (real) {
@@ -629,18 +699,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
                         *reinterpret_cast<uint4*>(part + pr * kDim + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
             }
-            if (real && whole && c.lse != nullptr) c.lse[out_row] = row_lse(m, l);
-            if (real && !whole) {
+            if (real && whole && kh == 0 && c.lse != nullptr) c.lse[out_row] = row_lse(m, l);
+            if (real && !whole && kh == 0) {
                 part[kRows * kDim + pr] = m;
                 part[kRows * (kDim + 1) + pr] = l;
             }
-            pos += n;
             first_segment = false;
         }
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 20) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, kTmemCols);
     }
@@ -649,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const SplitWork 
 int64_t meta_bytes(int grid) { return (static_cast<int64_t>(grid) * sizeof(Meta) + 255) / 256 * 256; }
 
 template <typename E, int kFmt, int kDim>
-cudaError_t launch(const KvAttnCall& c, void* workspace, int sm_count, cudaStream_t stream) {
+cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count, cudaStream_t stream) {
     static int attr_gen[64] = {};
     auto* kernel = attn_tile_kernel<E, kFmt, kDim>;
     int dev = 0;
@@ -672,7 +741,7 @@ cudaError_t launch(const KvAttnCall& c, void* workspace, int sm_count, cudaStrea
     a.meta = static_cast<Meta*>(workspace);
     a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + meta_bytes(a.grid));
     while (c.cache.page >> (a.page_shift + 1)) ++a.page_shift;
-    kernel<<<a.grid, kThreads, Smem<kDim>::kAlloc, stream>>>(a);
+    kernel<<<a.grid, kThreads, Smem<kDim>::kAlloc, stream>>>(tmK, tmV, a);
     if ((e = cudaGetLastError()) != cudaSuccess || c.max_len <= kKeys) return e;
     return launch_join<E, kDim, kRows>(a, 32, stream);
 }
@@ -683,9 +752,10 @@ int64_t kv_attn_tile_workspace(const KvAttnCall& c, int sm_count) {
     return meta_bytes(sm_count) + static_cast<int64_t>(sm_count) * 2 * kRows * (c.cache.dim + 2) * 4;
 }
 
-cudaError_t launch_kv_attn_tile(const KvAttnCall& c, void* workspace, int sm_count, cudaStream_t stream) {
+cudaError_t launch_kv_attn_tile(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count,
+                                cudaStream_t stream) {
     const bool h = c.dtype == kFp16, e4 = c.cache.fmt == kKvE4M3, d128 = c.cache.dim == 128;
-    auto go = [&](auto* f) { return f(c, workspace, sm_count, stream); };
+    auto go = [&](auto* f) { return f(c, tmK, tmV, workspace, sm_count, stream); };
     if (h && e4) return d128 ? go(launch<__half, kKvE4M3, 128>) : go(launch<__half, kKvE4M3, 64>);
     if (h) return d128 ? go(launch<__half, kKvInt8, 128>) : go(launch<__half, kKvInt8, 64>);
     if (e4) return d128 ? go(launch<__nv_bfloat16, kKvE4M3, 128>) : go(launch<__nv_bfloat16, kKvE4M3, 64>);

@@ -259,7 +259,8 @@ cudaError_t launch_kv_append(const KvAppendCall& c, int sm_count, cudaStream_t s
 cudaError_t launch_kv_read(const KvReadCall& c, int sm_count, cudaStream_t stream);
 int64_t kv_attn_workspace(const KvAttnCall& c, int sm_count);
 int64_t kv_attn_tile_workspace(const KvAttnCall& c, int sm_count);
-cudaError_t launch_kv_attn_tile(const KvAttnCall& c, void* workspace, int sm_count, cudaStream_t stream);
+cudaError_t launch_kv_attn_tile(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace,
+                                int sm_count, cudaStream_t stream);
 // Maps of the cache's codes as lines of 128 bytes, swizzled, in boxes of kv_attn_box_rows lines.
 int kv_attn_box_rows(const KvAttnCall& c);
 cudaError_t launch_kv_attn(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace,

@@ -46,6 +46,14 @@ struct SplitWork {
     float* parts;       // grid x 2 parts: rows x (dim + 2) floats each (values, then maxima, then sums)
 };
 
+// Byte offset of piece `at` (bytes) of token t among tokens that TMA left as lines of 128 bytes, swizzled.
+template <int kDim>
+__device__ __forceinline__ int ring_offset(int t, int at) {
+    const int line = kDim == 128 ? t : t >> 1;
+    const int in = kDim == 128 ? at : (t & 1) * 64 + at;
+    return line * 128 + (in ^ ((line & 7) << 4));
+}
+
 // Four codes to two fp16 pairs (codes 0 1, codes 2 3).
 template <int kFmt>
 __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -74,6 +82,8 @@ __device__ __forceinline__ float lg2_approx(float x) {
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+constexpr int kStep = 16;  // tokens a box of the cache's tensor maps
 
 // 1 / a row's sum; 0 for a row that sees nothing.
 __device__ __forceinline__ float row_inverse(float l) { return l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l); }
