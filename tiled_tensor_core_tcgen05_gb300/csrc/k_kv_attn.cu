@@ -611,7 +611,7 @@ cudaError_t launch_few(const KvAttnCall& c, const CUtensorMap& tmK, const CUtens
     while (c.cache.page >> (a.page_shift + 1)) ++a.page_shift;
     kernel<<<p.grid, kThreads, smem, stream>>>(tmK, tmV, a);
     if ((e = cudaGetLastError()) != cudaSuccess || !p.split) return e;
-    return launch_join<E, kDim, 8 * kTiles>(a, 8 * kTiles, stream);
+    return launch_join<E, kDim, 8 * kTiles>(a, stream);
 }
 
 template <typename E, int kFmt, int kDim>

@@ -743,7 +743,7 @@ cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMa
     while (c.cache.page >> (a.page_shift + 1)) ++a.page_shift;
     kernel<<<a.grid, kThreads, Smem<kDim>::kAlloc, stream>>>(tmK, tmV, a);
     if ((e = cudaGetLastError()) != cudaSuccess || c.max_len <= kKeys) return e;
-    return launch_join<E, kDim, kRows>(a, 32, stream);
+    return launch_join<E, kDim, kRows>(a, stream);
 }
 
 }  // namespace

@@ -92,51 +92,81 @@ __device__ __forceinline__ float row_inverse(float l) { return l > 0.0f ? 1.0f /
 __device__ __forceinline__ float row_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * (1.0f / kLog2e); }
 
 // Joins the parts of the unit inside which share k begins, if k's is its first border: block
-// (k - 1, rows blockIdx.y, blockIdx.y + gridDim.y, ..), a thread a value. The order of the parts is
-// that of their keys.
+// (k - 1, rows 8 blockIdx.y ..), a warp a row, kDim / 32 values a lane. The order of the parts is that
+// of their keys. What a part counts for is computed once, a part a lane.
+constexpr int kJoinRows = 8;
+
 template <typename E, int kDim, int kRows>
-__global__ void __launch_bounds__(kDim) attn_join_kernel(const SplitWork a) {
+__global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const SplitWork a) {
+    constexpr int kN = kDim / 32;
     const KvAttnCall& c = a.c;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int k = blockIdx.x + 1, d = threadIdx.x;
+    const int k = blockIdx.x + 1, lane = threadIdx.x % 32, r = blockIdx.y * kJoinRows + threadIdx.x / 32;
     const Meta m = a.meta[k];
     if (m.chunks == 0) return;
     const Shares shares(m.total, a.grid, a.least);
     const int64_t before = shares.start(k - 1);
     if (before > m.unit_start) return;  // an earlier border lies in the unit
     const SeqSpan span = seq_span(c.batch, m.seq, c.wd);
+    const int row = m.block * kRows + r;
+    if (row >= span.count * a.share) return;
     const int last = shares.owner(m.unit_start + m.chunks - 1);
     auto part_of = [&](int x) {
         const int slot = x == k - 1 && before < m.unit_start ? 1 : 0;
         return a.parts + (static_cast<int64_t>(2 * x) + slot) * kRows * (kDim + 2);
     };
-    for (int r = blockIdx.y; r < kRows; r += gridDim.y) {
-        const int row = m.block * kRows + r;
-        if (row >= span.count * a.share) return;
-        float top = kNoMax;
-#pragma unroll 4
-        for (int x = k - 1; x <= last; ++x) top = fmaxf(top, part_of(x)[kRows * kDim + r]);
-        float v = 0.0f, sum = 0.0f;
-#pragma unroll 4
-        for (int x = k - 1; x <= last; ++x) {
-            const float* p = part_of(x);
-            const float keep = ex2_approx(p[kRows * kDim + r] - top);
-            sum += p[kRows * (kDim + 1) + r] * keep;
-            v += p[r * kDim + d] * keep;
-        }
-        const int t = row / a.share;
-        const int64_t to = static_cast<int64_t>(span.first + t) * c.heads + m.head * a.share + row - t * a.share;
-        static_cast<E*>(c.out)[to * kDim + d] = from_float<E>(v * row_inverse(sum));
-        if (d == 0 && c.lse != nullptr) c.lse[to] = row_lse(top, sum);
+    float top = kNoMax;
+    for (int x0 = k - 1; x0 <= last; x0 += 32) {
+        const int x = x0 + lane;
+        if (x <= last) top = fmaxf(top, part_of(x)[kRows * kDim + r]);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    float v[kN] = {}, sum = 0.0f;
+    for (int x0 = k - 1; x0 <= last; x0 += 32) {
+        const int x = x0 + lane;
+        float keep = 0.0f, l = 0.0f;
+        if (x <= last) {
+            keep = ex2_approx(part_of(x)[kRows * kDim + r] - top);
+            l = part_of(x)[kRows * (kDim + 1) + r] * keep;
+        }
+        const int many = min(32, last + 1 - x0);
+#pragma unroll 8
+        for (int i = 0; i < many; ++i) {
+            const float* p = part_of(x0 + i) + r * kDim + lane * kN;
+            const float w = __shfl_sync(0xFFFFFFFFu, keep, i);
+            sum += __shfl_sync(0xFFFFFFFFu, l, i);
+            if constexpr (kN == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(p);
+                v[0] = fmaf(y.x, w, v[0]);
+                v[1] = fmaf(y.y, w, v[1]);
+                v[2] = fmaf(y.z, w, v[2]);
+                v[3] = fmaf(y.w, w, v[3]);
+            } else {
+                const float2 y = *reinterpret_cast<const float2*>(p);
+                v[0] = fmaf(y.x, w, v[0]);
+                v[1] = fmaf(y.y, w, v[1]);
+            }
+        }
+    }
+    const int t = row / a.share;
+    const int64_t to = static_cast<int64_t>(span.first + t) * c.heads + m.head * a.share + row - t * a.share;
+    const float inv = row_inverse(sum);
+    E out[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) out[i] = from_float<E>(v[i] * inv);
+    E* y = static_cast<E*>(c.out) + to * kDim + lane * kN;
+    if constexpr (kN == 4) *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(out);
+    else *reinterpret_cast<uint32_t*>(y) = *reinterpret_cast<const uint32_t*>(out);
+    if (lane == 0 && c.lse != nullptr) c.lse[to] = row_lse(top, sum);
 }
 
-// Launches the join so that its blocks are in place when the parts are: `rows_y` of them a border.
+// Launches the join so that its blocks are in place when the parts are.
 template <typename E, int kDim, int kRows>
-cudaError_t launch_join(const SplitWork& a, int rows_y, cudaStream_t stream) {
+cudaError_t launch_join(const SplitWork& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(a.grid - 1, rows_y);
-    cfg.blockDim = dim3(kDim);
+    cfg.gridDim = dim3(a.grid - 1, kRows / kJoinRows);
+    cfg.blockDim = dim3(32 * kJoinRows);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
