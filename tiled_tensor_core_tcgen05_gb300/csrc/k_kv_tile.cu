@@ -19,7 +19,9 @@
 //                   codes into a ring of three 64-token slots.
 // TMEM: scores of either half 128 columns, outputs dim columns each; the weights (fp16)
 // overwrite the scores they come from. A half's chain is scores, softmax, product, and
-// only then the next scores; the other half's runs in its gaps.
+// only then the next scores. The second half's scores of a tile are issued when the first
+// half's weights begin to arrive, so that one half's MMAs lie beside the other's
+// exponentials.
 #include "tg_device.cuh"
 #include "tg_kv_split.cuh"
 
@@ -43,6 +45,7 @@ static_assert(kRegsSoftmax >= kRegs && kRegsConv <= kRegs && kRegsIssue <= kRegs
 constexpr int kInfoSlots = 8;            // tiles whose scales are in shared memory (four can be in use)
 constexpr int kSegSlots = 4;             // segments handed out ahead
 constexpr int kSegReaders = 16 + 2 + 1;  // warps that read a segment: softmax, issuers, loader
+constexpr int kTurns = 4;                // tiles whose turns are told apart (the halves are two apart at most)
 constexpr int kRawSlots = 3;             // 64-token pieces of codes in flight
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;            // + 128 half; the weights of keys 64 g .. are the first 32 of their 64 columns
@@ -53,6 +56,8 @@ constexpr uint32_t kColO = 256;          // + 128 half
 struct TileInfo {
     float ks[kBlocks], lv[kBlocks], iv[kBlocks];
     int there[kBlocks];
+    int state;   // 1: every token is there, 0: not every one, -1: no tile, the share is done
+    int pad[3];
 };
 
 template <int kDim>
@@ -68,7 +73,7 @@ struct Smem {
     static constexpr int kInfo = kRed + 2 * 2 * 2 * kHalfRows * 4;
     static constexpr int kSegments = kInfo + kInfoSlots * static_cast<int>(sizeof(TileInfo));
     static constexpr int kBars = kSegments + kSegSlots * 64;
-    static constexpr int kNumBars = 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + kInfoSlots + 2 + 2 * kSegSlots + 2 * kRawSlots;
+    static constexpr int kNumBars = 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + kInfoSlots + 2 + kTurns + 2 * kSegSlots + 2 * kRawSlots;
     static constexpr int kScan = kBars + 8 * kNumBars;      // a sum a warp, then found offset and sequence
     static constexpr int kFoundOff = kScan + kThreads / 32 * 8;
     static constexpr int kFoundSeq = kFoundOff + 8;
@@ -206,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return b;
     };
     const uint32_t q_full = bars(2), k_full = bars(2), k_empty = bars(2), v_full = bars(2), v_empty = bars(2), s_full = bars(2);
-    const uint32_t p_full = bars(4), o_done = bars(2), info_full = bars(kInfoSlots), drain = bars(2);
+    const uint32_t p_full = bars(4), o_done = bars(2), info_full = bars(kInfoSlots), drain = bars(2), turn = bars(kTurns);
     const uint32_t seg_full = bars(kSegSlots), seg_empty = bars(kSegSlots), raw_full = bars(kRawSlots), raw_empty = bars(kRawSlots);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
@@ -227,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(drain + 8 * i, 1);
         }
         for (int i = 0; i < 4; ++i) mbar_init(p_full + 8 * i, 8);
+        for (int i = 0; i < kTurns; ++i) mbar_init(turn + 8 * i, 1);
         for (int i = 0; i < kInfoSlots; ++i) mbar_init(info_full + 8 * i, 1);
         for (int i = 0; i < kSegSlots; ++i) {
             mbar_init(seg_full + 8 * i, 1);
@@ -304,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t seg_no = 0;
     auto next_segment = [&](Segment& s) {
         const uint32_t slot = seg_no % kSegSlots;
-        if (!__all_sync(0xFFFFFFFFu, wait_phase(seg_full + 8 * slot, (seg_no / kSegSlots) & 1u, wc, kSiteMmaFull))) return false;
+        if (!__all_sync(0xFFFFFFFFu, wait_suspended(seg_full + 8 * slot, (seg_no / kSegSlots) & 1u, wc, kSiteMmaFull))) return false;
         s = *reinterpret_cast<const Segment*>(smem + L::kSegments + slot * 64);
         __syncwarp();
         if (lane == 0) mbar_arrive(seg_empty + 8 * slot);
@@ -347,12 +353,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (ok && next_segment(sg)) {
                 if (lane == 0) {
                     const int n = sg.t1 - sg.t0;
-                    ok = wait_phase(q_full + 8 * h, (seg_no - 1) & 1u, wc, kSiteMmaFull);
+                    ok = wait_suspended(q_full + 8 * h, (seg_no - 1) & 1u, wc, kSiteMmaFull);
                     for (int j = 0; ok && j < n; ++j) {
                         const uint32_t g = tile_no + j, st = g & 1u, kph = (g >> 1) & 1u;
                         // the scores overwrite the weights of tile j - 1
-                        ok = wait_phase(k_full + 8 * st, kph, wc, kSiteMmaFull) &&
-                             (j == 0 || wait_phase(o_done + 8 * h, (g - 1) & 1u, wc, kSiteMmaAccEmpty));
+                        ok = wait_suspended(k_full + 8 * st, kph, wc, kSiteMmaFull) &&
+                             (j == 0 || wait_suspended(o_done + 8 * h, (g - 1) & 1u, wc, kSiteMmaAccEmpty)) &&
+                             (h == 0 || wait_suspended(turn + 8 * (g % kTurns), (g / kTurns) & 1u, wc, kSiteMmaFull));
                         if (!ok) break;
                         tc_fence_after_sync();
 #pragma unroll
@@ -362,14 +369,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         mma_commit(s_full + 8 * h);
                         mma_commit(k_empty + 8 * st);
-                        ok = wait_phase(p_full + 16 * h, g & 1u, wc, kSiteMmaFull) && wait_phase(v_full + 8 * st, kph, wc, kSiteMmaFull);
+                        ok = wait_suspended(v_full + 8 * st, kph, wc, kSiteMmaFull) && wait_suspended(p_full + 16 * h, g & 1u, wc, kSiteMmaFull);
                         if (!ok) break;
+                        if (h == 0) mbar_arrive(turn + 8 * (g % kTurns));
                         tc_fence_after_sync();
                         product(0, st, j != 0);  // keys 0-31 and 64-95 are handed over first
                         product(1, st, true);
                         product(4, st, true);
                         product(5, st, true);
-                        ok = wait_phase(p_full + 16 * h + 8, g & 1u, wc, kSiteMmaFull);
+                        ok = wait_suspended(p_full + 16 * h + 8, g & 1u, wc, kSiteMmaFull);
                         if (!ok) break;
                         tc_fence_after_sync();
                         product(2, st, true);
@@ -432,6 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             info.iv[lane] = 1.0f / vs;
                             info.there[lane] = cur >= 0 ? min(kStep, len - token) : 0;
                         }
+                        const bool full = __all_sync(0xFFFFFFFFu, lane >= kBlocks || (cur >= 0 && len - token >= kStep));
+                        if (lane == 0) info.state = full ? 1 : 0;
                         __syncwarp();
                         if (lane == 0) mbar_arrive(info_full + 8 * (tile_no % kInfoSlots));
                     }
@@ -452,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!have) {
                 TileInfo& info = infos[tile_no % kInfoSlots];
                 if (lane == 0 && wait_phase_sleep(raw_empty + 8 * (piece % kRawSlots), ((piece / kRawSlots) & 1u) ^ 1u, wc, kSiteConvEmpty, 32)) {
-                    info.there[0] = -1;
+                    info.state = -1;
                     mbar_arrive(info_full + 8 * (tile_no % kInfoSlots));
                 }
             }
@@ -464,49 +474,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 16) {
         // ------------------------------------------------------------ codes to fp16 tiles
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-        const int tid = threadIdx.x - kSoftmaxThreads;
-        constexpr int kLanes = kDim / 16;            // threads a row of codes
-        constexpr int kPass = kConvThreads / kLanes; // rows a pass: 16 or 32
-        constexpr int kPasses = 64 / kPass;
-        const int row_in = tid / kLanes, at = tid % kLanes;
+        // A thread takes 16 codes (two 16-byte pieces of fp16) of a token: 64 of a row's codes, one box of the fp16
+        // tile, are four lanes; a quarter-warp is two tokens whose numbers differ so that its reads of the
+        // swizzled codes and its writes of the swizzled fp16 both go to eight different 16-byte banks. A warp is
+        // 8 tokens of one box; the four warps take boxes and groups of 8 tokens in turn.
+        const int at = lane & 3, r = lane >> 3, b = lane >> 2 & 1;
+        const int t8 = kDim == 128 ? r ^ (b ? 5 : 0) : 2 * r + b;       // token of eight
+        constexpr int kRounds = 64 / 8 * (kDim / 64) / 4;               // of the four warps in a 64-token piece: 4 or 2
+        const int box = kDim == 128 ? warp & 1 : 0;
+        const int group0 = kDim == 128 ? (warp - 16) >> 1 : warp - 16;  // first group of 8 tokens, then every 2nd or 4th
+        constexpr int kGroupStep = kDim == 128 ? 2 : 4;
+        // groups of a warp are an even number apart, so a thread's place in the swizzle is the same in all
+        const uint32_t get = ring_offset<kDim>(group0 * 8 + t8, (kDim == 128 ? box * 64 : 0) + at * 16);
+        const uint32_t put = box * L::kBox + (group0 * 8 + t8) * 128, put0 = ((2 * at) ^ t8) << 4, put1 = ((2 * at + 1) ^ t8) << 4;
         uint32_t piece = 0;
         bool ok = true;
         while (ok) {
             const uint32_t st = tile_no & 1u, eph = ((tile_no >> 1) & 1u) ^ 1u;
-            ok = __all_sync(0xFFFFFFFFu, wait_phase(info_full + 8 * (tile_no % kInfoSlots), (tile_no / kInfoSlots) & 1u, wc, kSiteConvFull));
+            ok = __all_sync(0xFFFFFFFFu, wait_suspended(info_full + 8 * (tile_no % kInfoSlots), (tile_no / kInfoSlots) & 1u, wc, kSiteConvFull));
             if (!ok) break;
             const TileInfo& info = infos[tile_no % kInfoSlots];
-            if (info.there[0] < 0) break;
+            const int state = info.state;
+            if (state < 0) break;
             for (int part = 0; part < 4; ++part, ++piece) {
-                const uint32_t slot = piece % kRawSlots, raw = sbase + L::kRawAt + slot * L::kRaw;
-                ok = __all_sync(0xFFFFFFFFu, wait_phase(raw_full + 8 * slot, (piece / kRawSlots) & 1u, wc, kSiteConvFull));
+                const uint32_t slot = piece % kRawSlots, raw = sbase + L::kRawAt + slot * L::kRaw + get;
+                ok = __all_sync(0xFFFFFFFFu, wait_suspended(raw_full + 8 * slot, (piece / kRawSlots) & 1u, wc, kSiteConvFull));
                 if (!ok) break;
-                uint4 x[kPasses];
+                uint4 x[kRounds];
 #pragma unroll
-                for (int i = 0; i < kPasses; ++i) x[i] = lds_v4(raw + ring_offset<kDim>(i * kPass + row_in, at * 16));
+                for (int i = 0; i < kRounds; ++i) x[i] = lds_v4(raw + i * kGroupStep * 8 * kDim);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(raw_empty + 8 * slot);
+                if (state == 0) {  // tokens past the end, or without a page, are zeros
+#pragma unroll
+                    for (int i = 0; i < kRounds; ++i) {
+                        const int t = (part & 1) * 64 + (group0 + i * kGroupStep) * 8 + t8;
+                        if ((t & 15) >= info.there[t >> 4]) x[i] = make_uint4(0, 0, 0, 0);
+                    }
+                }
                 if ((part & 1) == 0) {
-                    ok = __all_sync(0xFFFFFFFFu, wait_phase((part == 0 ? k_empty : v_empty) + 8 * st, eph, wc, kSiteConvEmpty));
+                    ok = __all_sync(0xFFFFFFFFu, wait_suspended((part == 0 ? k_empty : v_empty) + 8 * st, eph, wc, kSiteConvEmpty));
                     if (!ok) break;
                 }
-                const uint32_t base = sbase + (part < 2 ? L::kK : L::kV) + st * L::kTile + (at >> 2) * L::kBox;
+                const uint32_t base = sbase + (part < 2 ? L::kK : L::kV) + st * L::kTile + (part & 1) * 64 * 128 + put;
 #pragma unroll
-                for (int i = 0; i < kPasses; ++i) {
-                    const int t = (part & 1) * 64 + i * kPass + row_in;
-                    if ((t & 15) >= info.there[t >> 4]) x[i] = make_uint4(0, 0, 0, 0);  // past the end, or no page
+                for (int i = 0; i < kRounds; ++i) {
                     uint32_t h[8];
                     codes_to_half<kFmt>(x[i].x, h[0], h[1]);
                     codes_to_half<kFmt>(x[i].y, h[2], h[3]);
                     codes_to_half<kFmt>(x[i].z, h[4], h[5]);
                     codes_to_half<kFmt>(x[i].w, h[6], h[7]);
-                    // 16 codes are two 16-byte pieces of a box's row; the threads of the second box write the odd
-                    // one first, so that a quarter-warp's eight go to eight banks
-                    const uint32_t line = base + t * 128;
-                    const int odd = at >> 2, c0 = (at & 3) * 2;
-                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                    sts_v4(line + (((c0 + odd) ^ (t & 7)) << 4), odd ? hi : lo);
-                    sts_v4(line + (((c0 + 1 - odd) ^ (t & 7)) << 4), odd ? lo : hi);
+                    sts_v4(base + put0 + i * kGroupStep * 8 * 128, make_uint4(h[0], h[1], h[2], h[3]));
+                    sts_v4(base + put1 + i * kGroupStep * 8 * 128, make_uint4(h[4], h[5], h[6], h[7]));
                 }
                 if (part & 1) {
                     fence_proxy_async_smem();
@@ -523,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = (warp & 3) * 32 + lane;                       // of the half: its TMEM lane
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t col_s = lanes + kColS + 128 * h + 64 * kh, col_o = lanes + kColO + 128 * h + kh * (kDim / 2);
+        const int pair = h * 4 + (warp & 3);                          // the two warps of the same 32 rows
         float* red = reinterpret_cast<float*>(smem + L::kRed) + (h * 2) * kHalfRows + row;  // + parity 4 * 128, + key half 128
         bool ok = true;
         bool first_segment = true;
@@ -580,37 +600,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = sg.t1 - sg.t0;
             for (int j = 0; j < n; ++j) {
                 const uint32_t g = tile_no + j, ph = g & 1u;
-                // a wait that gave up still reaches the barrier of the maxima, where all of the half learn of it
-                ok = wait_phase(info_full + 8 * (g % kInfoSlots), (g / kInfoSlots) & 1u, wc, kSiteEpilogueAccFull) &&
-                     wait_phase(s_full + 8 * h, ph, wc, kSiteEpilogueAccFull);
+                // a wait that gave up still reaches the barrier of the maxima, where both warps learn of it
+                ok = wait_suspended(info_full + 8 * (g % kInfoSlots), (g / kInfoSlots) & 1u, wc, kSiteEpilogueAccFull) &&
+                     wait_suspended(s_full + 8 * h, ph, wc, kSiteEpilogueAccFull);
                 __syncwarp();
                 tc_fence_after_sync();
                 const TileInfo& info = infos[g % kInfoSlots];
-                uint32_t s[2][32];
-                tmem_ld_32x32b_x32(col_s, s[0]);
-                tmem_ld_32x32b_x32(col_s + 32, s[1]);
-                tmem_ld_wait();
-                auto raw = [&](int i) { return __uint_as_float(s[i >> 5][i & 31]); };
-                const int key0 = (sg.tile0 + sg.t0 + j) * kKeys + 64 * kh;
-                if (key0 < from || key0 + 64 > to) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (key0 + i < from || key0 + i >= to) s[i >> 5][i & 31] = __float_as_uint(-INFINITY);
-                }
-                // this half's maximum, block by block, then the row's
+                // keys key0 .. key0 + 63; a tile that some row of the warp does not see whole is masked
+                const int key0 = (sg.tile0 + sg.t0 + j) * kKeys + 64 * kh, lo = from - key0, hi = to - key0;
+                const bool edge = __any_sync(0xFFFFFFFFu, lo > 0 || hi < 64);
+                // this half's maximum, block by block, then the row's. The scores are read twice, 32 at a
+                // time, in loops: the code stays small and the registers few
                 float top = kNoMax;
+                float xs[2][32];
+                tmem_ld_32x32b_x32(col_s, reinterpret_cast<uint32_t(&)[32]>(xs[0]));
+                tmem_ld_32x32b_x32(col_s + 32, reinterpret_cast<uint32_t(&)[32]>(xs[1]));
+                tmem_ld_wait();
+                if (edge) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    float x = max3(raw(16 * b), raw(16 * b + 1), raw(16 * b + 2)), y = max3(raw(16 * b + 3), raw(16 * b + 4), raw(16 * b + 5));
-                    x = max3(x, raw(16 * b + 6), raw(16 * b + 7));
-                    y = max3(y, raw(16 * b + 8), raw(16 * b + 9));
-                    x = max3(x, raw(16 * b + 10), raw(16 * b + 11));
-                    y = max3(y, raw(16 * b + 12), raw(16 * b + 13));
-                    x = max3(x, raw(16 * b + 14), raw(16 * b + 15));
-                    top = fmaxf(top, fmaf(fmaxf(x, y), fmaxf(f * info.ks[4 * kh + b], 1e-38f), info.lv[4 * kh + b]));
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < lo - 32 * q || i >= hi - 32 * q) xs[q][i] = -INFINITY;
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float (&x)[32] = xs[q];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const float* y = x + 16 * b;
+                        const float u = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]), max3(y[6], y[7], y[8]));
+                        const float v = max3(max3(y[9], y[10], y[11]), max3(y[12], y[13], y[14]), y[15]);
+                        top = fmaxf(top, fmaf(fmaxf(u, v), fmaxf(f * info.ks[4 * kh + 2 * q + b], 1e-38f), info.lv[4 * kh + 2 * q + b]));
+                    }
                 }
                 red[ph * 4 * kHalfRows + kh * kHalfRows] = top;
-                if (named_barrier_or(1 + h, 256, !ok)) {
+                if (named_barrier_or(3 + pair, 64, !ok)) {
                     ok = false;
                     break;
                 }
@@ -625,21 +650,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float sum = 0.0f;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
+                    float2 (&x)[16] = reinterpret_cast<float2(&)[16]>(xs[q]);
+                    // pair by pair, in place: while the exponential unit takes a pair, the next one is scaled
+                    // and the one before the last is summed and rounded
                     uint32_t w[16];
+                    float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    float2 cb[2], ob[2];
 #pragma unroll
-                    for (int b = 2 * q; b < 2 * q + 2; ++b) {
-                        const float cb = fmaxf(f * info.ks[4 * kh + b], 1e-38f), ob = info.lv[4 * kh + b] - m;
-                        const float2 c2 = make_float2(cb, cb), o2 = make_float2(ob, ob);
-                        float2 part = make_float2(0.0f, 0.0f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 x = __ffma2_rn(make_float2(raw(16 * b + 2 * e), raw(16 * b + 2 * e + 1)), c2, o2);
-                            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                            part = __fadd2_rn(part, p);
-                            w[(b & 1) * 8 + e] = half2_bits(p.x, p.y);
-                        }
-                        sum = fmaf(part.x + part.y, info.iv[4 * kh + b], sum);
+                    for (int b = 0; b < 2; ++b) {
+                        const float cc = fmaxf(f * info.ks[4 * kh + 2 * q + b], 1e-38f), oo = info.lv[4 * kh + 2 * q + b] - m;
+                        cb[b] = make_float2(cc, cc);
+                        ob[b] = make_float2(oo, oo);
                     }
+#pragma unroll
+                    for (int e = 0; e < 20; ++e) {
+                        if (e < 16) x[e] = __ffma2_rn(x[e], cb[e >> 3], ob[e >> 3]);
+                        if (e >= 2 && e < 18) {
+                            x[e - 2].x = ex2_approx(x[e - 2].x);
+                            x[e - 2].y = ex2_approx(x[e - 2].y);
+                        }
+                        if (e >= 4) {
+                            w[e - 4] = half2_bits(x[e - 4].x, x[e - 4].y);
+                            part[(e - 4) >> 3] = __fadd2_rn(part[(e - 4) >> 3], x[e - 4]);
+                        }
+                    }
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) sum = fmaf(part[b].x + part[b].y, info.iv[4 * kh + 2 * q + b], sum);
                     tmem_st_x16(col_s + 16 * q, w);
                     // the outputs so far come to the new maximum before the first weights are handed over: the
                     // product of the tile before has completed (this tile's scores were issued after it)
@@ -663,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             tile_no += n;
-            ok = wait_phase_sleep(o_done + 8 * h, (tile_no - 1) & 1u, wc, kSiteEpilogueAccFull, 32);
+            ok = wait_suspended(o_done + 8 * h, (tile_no - 1) & 1u, wc, kSiteEpilogueAccFull);
             // both key halves' sums; the maxima of the last tile were in the other parity
             red[(tile_no & 1u) * 4 * kHalfRows + kh * kHalfRows] = l;
             if (named_barrier_or(1 + h, 256, !ok)) {

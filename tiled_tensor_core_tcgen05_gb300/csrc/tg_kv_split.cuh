@@ -2,9 +2,37 @@
 // work and the joining of units that cross shares, and the codes' way to fp16.
 #pragma once
 
+#include "tg_device.cuh"
 #include "tg_kv.cuh"
 
 namespace tg {
+
+// wait_phase for warps that share their scheduler with others' arithmetic: the hardware suspends the
+// warp for up to 20 us a try, where shorter tries in a loop took half of the issue slots from the
+// exponentials beside them. Same bound and abort rules.
+__device__ __forceinline__ bool wait_suspended(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
+    uint64_t t0 = 0;
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        if (*w.abort) return false;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) {
+            t0 = now;
+        } else if (now - t0 > w.limit_ns) {
+            *w.abort = 1;
+            atomicCAS(w.status, 0, site);
+            return false;
+        }
+    }
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNoMax = -1e30f;        // running maximum before any visible key
