@@ -14,9 +14,7 @@ CPU path: if the library has not been built, importing this package raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
-import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -102,7 +100,6 @@ def bind(path: str) -> ctypes.CDLL:
 
 
 _lib = bind(LIB_PATH)
-from . import _tg_binding as _fast  # noqa: E402  the same library's serving calls, without ctypes' conversions
 
 
 class TgError(RuntimeError):
@@ -222,17 +219,17 @@ def bias_gelu_(C, bias=None, gelu: bool = True, stream=None):
 
 def tg_rope(*args) -> None:
     """The C entry point's arguments in its order (include/tg_gemm.h)."""
-    _check(_fast.rope(*args))
+    _check(_lib.tg_rope(*args))
 
 
 def tg_kv_append(*args) -> None:
     """The C entry point's arguments in its order (include/tg_gemm.h)."""
-    _check(_fast.kv_append(*args))
+    _check(_lib.tg_kv_append(*args))
 
 
 def tg_kv_read(*args) -> None:
     """The C entry point's arguments in its order (include/tg_gemm.h)."""
-    _check(_fast.kv_read(*args))
+    _check(_lib.tg_kv_read(*args))
 
 
 def tg_attention_kv_workspace(kv_heads: int, page: int, dim: int, fmt: int, heads: int, batch: int, total: int,
@@ -246,7 +243,7 @@ def tg_attention_kv_workspace(kv_heads: int, page: int, dim: int, fmt: int, head
 
 def tg_attention_kv(*args) -> None:
     """The C entry point's arguments in its order (include/tg_gemm.h)."""
-    _check(_fast.attention_kv(*args))
+    _check(_lib.tg_attention_kv(*args))
 
 
 def tg_device_status(stream: int | None) -> tuple[int, int]:
@@ -308,17 +305,6 @@ def _stream_handle(stream):
         return torch.cuda.current_stream().cuda_stream
     # the current stream's handle without the object around it
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-
-
-_NO_CONTEXT = contextlib.nullcontext()
-
-
-def _on(stream):
-    """The torch context in which tensors are allocated for work on ``stream``."""
-    if stream is None:
-        return _NO_CONTEXT
-    import torch
-    return torch.cuda.stream(stream)
 
 
 def _dev_fp16(t, name):
@@ -412,47 +398,24 @@ def ring_bytes(block_M: int, block_N: int, block_K: int, num_stages: int, elem_b
 
 # ---------------------------------------------------------------- rotary positions and the 8-bit cache
 
-def _dtype_code(dtype, name):
-    import torch
-    if dtype is torch.float16:
-        return FP16
-    if dtype is torch.bfloat16:
-        return BF16
-    raise TypeError(f"{name} must be float16 or bfloat16, got {dtype}")
+_fast = None
 
 
-def _rows(t, name, dtype=None):
-    """(pointer, token stride, head stride) of a (tokens, heads, dim) CUDA tensor with contiguous dim."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have shape (tokens, heads, dim), got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    token, head, unit = t.stride()
-    if unit != 1 and t.shape[2] > 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-    return t.data_ptr(), token, head
+def _binding():
+    """The module of the tensor forms below (csrc/tg_torch.cpp), loaded with torch on first use."""
+    global _fast
+    if _fast is None:
+        import torch  # noqa: F401  its libraries, which the module needs
+        from . import _tg_torch
+        _fast = _tg_torch
+    return _fast
 
 
-def _ints(t, name, shape):
-    import torch
-    if t.dtype is not torch.int32:
-        raise TypeError(f"{name} must be int32, got {t.dtype}")
-    if not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _frequencies(inv_freq):
-    import torch
-    if inv_freq.dtype is not torch.float64 or not inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise TypeError("inv_freq must be a contiguous CUDA float64 vector (radians per position of each pair)")
-    return inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+def _answer(result):
+    """A tensor form's result, or the library's refusal as an error."""
+    if type(result) is int:
+        _check(result)
+    return result
 
 
 def rope_frequencies(rotary: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -502,21 +465,7 @@ def rope(X, positions, inv_freq, amplitude: float = 1.0, layout: int = ROPE_HALF
     ``amplitude``, the others copied. ``positions`` int32, ``inv_freq`` float64 (see
     ``rope_frequencies``). ``backward``: the transposed map, which takes the output's gradient to
     the input's. ``out`` may be X. X and out may be slices (contiguous in dim)."""
-    import torch
-    x, xt, xh = _rows(X, "X")
-    dtype = _dtype_code(X.dtype, "X")
-    T, H, D = X.shape
-    freq, rotary = _frequencies(inv_freq)
-    pos = _ints(positions, "positions", (T,))
-    if out is None:
-        with _on(stream):
-            out = torch.empty((T, H, D), dtype=X.dtype, device=X.device)
-    elif out.shape != X.shape:
-        raise ValueError("out has the wrong shape")
-    y, yt, yh = _rows(out, "out", X.dtype)
-    _check(_fast.rope(x, xt, xh, y, yt, yh, pos, T, H, D, freq, rotary, amplitude, layout, int(backward), dtype,
-                      _stream_handle(stream)))
-    return out
+    return _answer((_fast or _binding()).rope(X, positions, inv_freq, amplitude, layout, backward, out, stream))
 
 
 class KvCache:
@@ -527,28 +476,9 @@ class KvCache:
     __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "page", "dim", "fmt", "args")
 
     def __init__(self, k, v, k_scale, v_scale):
-        import torch
-        if k.dtype is torch.float8_e4m3fn:
-            self.fmt = KV_E4M3
-        elif k.dtype is torch.int8:
-            self.fmt = KV_INT8
-        else:
-            raise TypeError(f"codes must be float8_e4m3fn or int8, got {k.dtype}")
-        if k.dim() != 4 or k.shape != v.shape or k.dtype is not v.dtype:
-            raise ValueError("k and v must share one (pages, kv_heads, page, dim) shape and one type")
-        self.pages, self.kv_heads, self.page, self.dim = k.shape
-        if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
-            raise TypeError("scales must be float32")
-        if k_scale.shape != (self.pages, self.kv_heads) or v_scale.shape != (self.pages, self.kv_heads):
-            raise ValueError(f"scales must have shape ({self.pages}, {self.kv_heads})")
-        for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
-            if not t.is_cuda:
-                raise TypeError(f"{name} must be a CUDA tensor")
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
+        self.args = a = (_fast or _binding()).cache_args(k, v, k_scale, v_scale)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.args = (k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.pages, self.kv_heads,
-                     self.page, self.dim, self.fmt)
+        _, _, _, _, self.pages, self.kv_heads, self.page, self.dim, self.fmt = a
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, page: int = 64, dim: int = 128, dtype=None, device="cuda"):
@@ -556,15 +486,6 @@ class KvCache:
         dtype = torch.float8_e4m3fn if dtype is None else dtype
         k, v = (torch.zeros((pages, kv_heads, page, dim), dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
         return cls(k, v, *(torch.zeros((pages, kv_heads), device=device) for _ in range(2)))
-
-
-def _batch(table, lens, cu, total):
-    """The C calls' batch arguments: table, its width, lens, cu, batch, total."""
-    if table.dim() != 2:
-        raise ValueError(f"table must have shape (batch, pages a sequence), got {tuple(table.shape)}")
-    B, width = table.shape
-    return (_ints(table, "table", (B, width)), width, _ints(lens, "lens", (B,)),
-            _ints(cu, "cu", (B + 1,)) if cu is not None else None, B, total)
 
 
 def kv_append(cache, K, V, table, lens, cu=None, max_new: int = 1, Q=None, inv_freq=None, amplitude: float = 1.0,
@@ -575,34 +496,8 @@ def kv_append(cache, K, V, table, lens, cu=None, max_new: int = 1, Q=None, inv_f
     max_new: no sequence has more rows. With ``inv_freq`` the keys are rotated first by their
     positions (see ``rope``), and the queries Q (total, heads, dim), if given, too: returns them
     (``out``, which may be Q), else None. The scales and roundings are in include/tg_gemm.h."""
-    import torch
-    k, kt, kh = _rows(K, "K")
-    v, vt, vh = _rows(V, "V", K.dtype)
-    dtype = _dtype_code(K.dtype, "K")
-    T = K.shape[0]
-    if K.shape != V.shape or K.shape[1] != cache.kv_heads or K.shape[2] != cache.dim:
-        raise ValueError(f"K and V must have shape (total, {cache.kv_heads}, {cache.dim}), got {tuple(K.shape)} "
-                         f"and {tuple(V.shape)}")
-    freq, rotary = _frequencies(inv_freq) if inv_freq is not None else (None, 0)
-    q = qo = (None, 0, 0)
-    heads = 0
-    if Q is not None:
-        if inv_freq is None:
-            raise ValueError("Q is only rotated: it needs inv_freq")
-        q, heads = _rows(Q, "Q", K.dtype), Q.shape[1]
-        if Q.shape[0] != T or Q.shape[2] != cache.dim:
-            raise ValueError(f"Q must have shape ({T}, heads, {cache.dim}), got {tuple(Q.shape)}")
-        if out is None:
-            with _on(stream):
-                out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
-        elif out.shape != Q.shape:
-            raise ValueError("out has the wrong shape")
-        qo = _rows(out, "out", Q.dtype)
-    elif out is not None:
-        raise ValueError("out is for the rotated Q")
-    _check(_fast.kv_append(*cache.args, k, kt, kh, v, vt, vh, *_batch(table, lens, cu, T), max_new, freq, rotary,
-                           amplitude, layout, *q, *qo, heads, dtype, _stream_handle(stream)))
-    return out
+    return _answer((_fast or _binding()).kv_append(cache.args, K, V, table, lens, cu, max_new, Q, inv_freq, amplitude,
+                                                   layout, out, stream))
 
 
 def kv_read(cache, table, first, cu, total: int, dtype=None, out=None, stream=None):
@@ -610,27 +505,13 @@ def kv_read(cache, table, first, cu, total: int, dtype=None, out=None, stream=No
     every sequence, packed at rows cu[i] .. (cu None: one row a sequence): code * scale, rounded once
     to ``dtype`` (float16, the default, or bfloat16). ``out``: a pair of contiguous tensors."""
     import torch
-    shape = (total, cache.kv_heads, cache.dim)
-    if out is None:
-        dtype = torch.float16 if dtype is None else dtype
-        with _on(stream):
-            K, V = (torch.empty(shape, dtype=dtype, device=cache.k.device) for _ in range(2))
-    else:
-        K, V = out
-        if tuple(K.shape) != shape or tuple(V.shape) != shape:
-            raise ValueError(f"out must be two tensors of shape {shape}")
-        if not (K.is_cuda and V.is_cuda and K.is_contiguous() and V.is_contiguous()):
-            raise ValueError("out must be contiguous CUDA tensors")
-        if K.dtype is not V.dtype or (dtype is not None and K.dtype is not dtype):
-            raise TypeError("out has the wrong type")
-    _check(_fast.kv_read(*cache.args, *_batch(table, first, cu, total), K.data_ptr(), V.data_ptr(),
-                         _dtype_code(K.dtype, "dtype"), _stream_handle(stream)))
-    return K, V
-
-
-@functools.lru_cache(maxsize=1024)
-def _kv_workspace(*sizes) -> int:
-    return tg_attention_kv_workspace(*sizes)
+    K, V = out if out is not None else (None, None)
+    if dtype is None:
+        dtype = K.dtype if K is not None else torch.float16
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise TypeError(f"dtype must be float16 or bfloat16, got {dtype}")
+    return _answer((_fast or _binding()).kv_read(cache.args, cache.k, table, first, cu, total,
+                                                 dtype is torch.bfloat16, K, V, stream))
 
 
 def attention_kv(Q, cache, table, lens, cu=None, max_new: int = 1, max_len: int | None = None, causal: bool = True,
@@ -641,25 +522,5 @@ def attention_kv(Q, cache, table, lens, cu=None, max_new: int = 1, max_len: int 
     last so many. max_new and max_len bound the rows and the length of a sequence (max_len None: what
     the table can hold). scale None: 1 / sqrt(dim). Rows that see nothing give zeros. Returns O (total,
     heads, dim), with ``return_lse`` also the float32 log of each row's sum (total, heads)."""
-    import torch
-    q, qt, qh = _rows(Q, "Q")
-    dtype = _dtype_code(Q.dtype, "Q")
-    T, H, D = Q.shape
-    if D != cache.dim:
-        raise ValueError(f"Q must have shape (total, heads, {cache.dim}), got {tuple(Q.shape)}")
-    batch = _batch(table, lens, cu, T)
-    if max_len is None:
-        max_len = batch[1] * cache.page
-    handle = _stream_handle(stream)
-    need = _kv_workspace(cache.kv_heads, cache.page, D, cache.fmt, H, batch[4], T, max_new, max_len, window, dtype)
-    with _on(stream):
-        if out is None:
-            out = torch.empty((T, H, D), dtype=Q.dtype, device=Q.device)
-        elif out.shape != Q.shape or out.dtype is not Q.dtype or not out.is_cuda or not out.is_contiguous():
-            raise ValueError("out must be a contiguous CUDA tensor of Q's shape and type")
-        lse = torch.empty((T, H), dtype=torch.float32, device=Q.device) if return_lse else None
-        work = torch.empty(need, dtype=torch.uint8, device=Q.device) if need else None
-    _check(_fast.attention_kv(q, qt, qh, out.data_ptr(), lse.data_ptr() if return_lse else None, *cache.args, *batch, H,
-                              max_new, max_len, int(causal), window, D ** -0.5 if scale is None else scale, dtype,
-                              work.data_ptr() if need else None, need, handle))
-    return (out, lse) if return_lse else out
+    return _answer((_fast or _binding()).attention_kv(Q, cache.args, table, lens, cu, max_new, max_len, causal, window,
+                                                      scale, return_lse, out, stream))

@@ -4,7 +4,8 @@ Each translation unit under csrc/ is compiled in parallel with nvcc
 (-gencode arch=compute_103a,code=sm_103a), then linked into one shared
 library next to this file. No torch extension machinery: the library exports
 a plain C ABI (include/tg_gemm.h). Beside it a small CPython module,
-_tg_binding.so, calls the same library without ctypes (csrc/tg_binding.c).
+_tg_torch.so, holds the tensor forms of a serving step's calls
+(csrc/tg_torch.cpp, against torch's headers).
 """
 from __future__ import annotations
 
@@ -21,7 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtg_gemm.so")
-BINDING = os.path.join(PKG, "_tg_binding.so")
+BINDING = os.path.join(PKG, "_tg_torch.so")
 # the debug build (device-side bounds checks, TG_DEBUG=1): same sources, its own objects
 OBJDIR_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libtg_gemm_debug.so")
@@ -57,14 +58,32 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
-def build_binding() -> None:
-    """The CPython module, linked with the library next to it."""
-    tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
-           os.path.join(CSRC, "tg_binding.c"), "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN"]
+def compile_binding(objdir: str) -> str:
+    """The CPython module's object file."""
+    import importlib.util
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    include = os.path.join(torch_dir, "include")
+    obj = os.path.join(objdir, "tg_torch.o")
+    home = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", os.path.join(CSRC, "tg_torch.cpp"), "-o", obj, "-I", INCLUDE,
+           "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-I", os.path.join(home, "include"), "-I", sysconfig.get_paths()["include"]]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed for tg_binding.c:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed for tg_torch.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def link_binding(obj: str) -> None:
+    """Links the module with the library next to it and with torch."""
+    import importlib.util
+    lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", obj, "-o", tmp, LIB, "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed for tg_torch.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
 
 
@@ -91,7 +110,8 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = None if debug else ex.submit(compile_binding, objdir)
         objs = list(ex.map(compile_one, SOURCES))
     tmp = lib_path + f".tmp{os.getpid()}"
     cmd = [cc, "-shared", "-o", tmp, "-Xlinker", f"-soname={os.path.basename(lib_path)}"] + objs + ARCH + ["-lineinfo"]
@@ -99,8 +119,8 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib_path)
-    if not debug:
-        build_binding()
+    if binding is not None:
+        link_binding(binding.result())
     return lib_path
 
 

@@ -20,6 +20,8 @@
 // only where a scale grows are the page's held codes touched at all.
 #include "tg_kv.cuh"
 
+#include <type_traits>
+
 namespace tg {
 namespace {
 
@@ -59,6 +61,40 @@ __device__ __forceinline__ uint32_t again4(uint32_t w, float ratio) {
     return encode4<kFmt>(__fmul_rn(x[0], ratio), __fmul_rn(x[1], ratio), __fmul_rn(x[2], ratio), __fmul_rn(x[3], ratio));
 }
 
+// Eight values as they are stored.
+template <typename E>
+__device__ __forceinline__ uint4 load_piece(const E* p, bool vec) {
+    if (vec) return *reinterpret_cast<const uint4*>(p);
+    uint4 u;
+    E* e = reinterpret_cast<E*>(&u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = p[i];
+    return u;
+}
+
+// The partners of values d .. d + 7 of a row in the half layout (zeros elsewhere).
+template <typename E>
+__device__ __forceinline__ uint4 load_partner_piece(const E* row, int d, bool vec, const RopeArgs& r) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (r.layout != kRopeHalf || d >= r.rotary) return u;
+    const int half = r.rotary / 2;
+    if (half % 8 == 0) return load_piece(row + (d < half ? d + half : d - half), vec);
+    E* e = reinterpret_cast<E*>(&u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int at = d + i;
+        if (at < r.rotary) e[i] = row[at < half ? at + half : at - half];
+    }
+    return u;
+}
+
+template <typename E>
+__device__ __forceinline__ void piece_values(const uint4& u, float (&x)[8]) {
+    const E* e = reinterpret_cast<const E*>(&u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_float(e[i]);
+}
+
 // How rows may be read: 16-byte pieces (then 8-byte ones too) or single values.
 struct Wide {
     bool k, v, q, q_out;
@@ -81,9 +117,9 @@ constexpr int kVecs = 4;  // 16-byte pieces a thread holds
 // n / page + 2 pages, so some items have none), y heads, z keys or values (keys that are rotated are a
 // launch of their own).
 template <typename E, int kFmt, int kDim, bool kRope>
-__global__ void __launch_bounds__(512) append_pages_kernel(const PageArgs a) {
+__global__ void __launch_bounds__(512, kRope ? 1 : 2) append_pages_kernel(const PageArgs a) {
     extern __shared__ float turns[];  // cos, then sin: (page, rotary / 2) each
-    __shared__ float red[16];
+    __shared__ float red[2][16];
     const KvAppendCall& c = a.c;
     const KvBatch& b = c.batch;
     const int page = c.cache.page, item = blockIdx.x;
@@ -124,67 +160,90 @@ __global__ void __launch_bounds__(512) append_pages_kernel(const PageArgs a) {
     const Strided& src = values ? c.v : c.k;
     const bool vec = values ? a.wide.v : a.wide.k;
     const int head_end = min(c.cache.kv_heads, static_cast<int>(blockIdx.y + 1) * a.heads_a_cta);
-    // every group makes every round, so that all meet at the barriers
-    for (int head0 = blockIdx.y * a.heads_a_cta; head0 < head_end; head0 += groups) {
-        const int head = head0 + g;
-        const bool real = head < head_end;
-        const int64_t ph = static_cast<int64_t>(p) * c.cache.kv_heads + (real ? head : 0);
-        uint8_t* codes = (values ? c.cache.v : c.cache.k) + ph * page * kDim;
-        float* scale = (values ? c.cache.v_scale : c.cache.k_scale) + ph;
-        const float s_old = real && from > 0 ? *scale : 0.0f;
-        const E* x0 = static_cast<const E*>(src.p) + row0 * src.token + head * src.head;
-        float x[kVecs][8];
-        float most = 0.0f;
+    const E* x0 = static_cast<const E*>(src.p) + row0 * src.token;
+    uint8_t* all_codes = values ? c.cache.v : c.cache.k;
+    float* all_scales = values ? c.cache.v_scale : c.cache.k_scale;
+    // one head's pieces (and, rotated, their partners) and old scale, fetched while the head before is worked on
+    uint4 own[kVecs], other[kVecs];
+    float s_old = 0.0f;
+    auto fetch = [&](int head) {
+        if (head >= head_end) return;
+        s_old = from > 0 ? all_scales[static_cast<int64_t>(p) * c.cache.kv_heads + head] : 0.0f;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             const int at = t + i * group, place = at / kPieces, d = (at - place * kPieces) * 8;
-            if (real && place >= from && place < to) load_values<E, 8>(x0 + place * src.token, d, vec, x[i]);
-        }
-        if constexpr (kRope) {
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const int at = t + i * group, place = at / kPieces, d = (at - place * kPieces) * 8;
-                if (real && place >= from && place < to) {
-                    float o[8];
-                    load_partners<E, 8>(x0 + place * src.token, d, vec, rope, o);
-                    rotate_values<8>(x[i], o, d, cs + place * half, sn + place * half, rope);
-                }
+            if (place >= from && place < to) {
+                const E* row = x0 + place * src.token + head * src.head;
+                own[i] = load_piece(row + d, vec);
+                if constexpr (kRope) other[i] = load_partner_piece(row, d, vec, rope);
             }
         }
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int place = (t + i * group) / kPieces;
-            if (real && place >= from && place < to) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) most = max_finite(most, x[i][e]);
-            }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-        if (group > 32) {
-            __syncthreads();
-            if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = most;
-            __syncthreads();
-            for (int w = g * group / 32; w < (g + 1) * group / 32; ++w) most = fmaxf(most, red[w]);
-        }
-        if (!real) continue;
-        const float s = fmaxf(s_old, fmaxf(__fmul_rn(most, code_max_inverse<kFmt>()), kScaleFloor));
-        const float per = __fdiv_rn(1.0f, s);
-        const float ratio = __fmul_rn(s_old, per);
+    };
+    fetch(blockIdx.y * a.heads_a_cta + g);
+    int round = 0;
+    // every group makes every round, so that all meet at the barriers
+    for (int head0 = blockIdx.y * a.heads_a_cta; head0 < head_end; head0 += groups, ++round) {
+        const int head = head0 + g;
+        const bool real = head < head_end;
+        const float s_held = s_old;
+        // rotated values are kept in fp32, others as they were read: they are half the registers
+        std::conditional_t<kRope, float[kVecs][8], uint4[kVecs]> x;
+        float most = 0.0f;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             const int at = t + i * group, place = at / kPieces;
-            uint2* q = reinterpret_cast<uint2*>(codes + at * 8);
-            if (place >= from && place < to) {
-                uint32_t w[2];
-                encode_values<kFmt, 8>(x[i], most, per, w);
-                *q = make_uint2(w[0], w[1]);
-            } else if (place < from && s != s_old) {
-                const uint2 w = *q;
-                *q = make_uint2(again4<kFmt>(w.x, ratio), again4<kFmt>(w.y, ratio));
+            if (real && place >= from && place < to) {
+                float v[8];
+                piece_values<E>(own[i], v);
+                if constexpr (kRope) {
+                    float o[8];
+                    piece_values<E>(other[i], o);
+                    rotate_values<8>(v, o, (at - place * kPieces) * 8, cs + place * half, sn + place * half, rope);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[i][e] = v[e];
+                } else {
+                    x[i] = own[i];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) most = max_finite(most, v[e]);
             }
         }
-        if (t == 0) *scale = s;
+        fetch(head + groups);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+        if (group > 32) {
+            float* r = red[round & 1];  // the other half is still being read
+            if (threadIdx.x % 32 == 0) r[threadIdx.x / 32] = most;
+            __syncthreads();
+            for (int w = g * group / 32; w < (g + 1) * group / 32; ++w) most = fmaxf(most, r[w]);
+        }
+        if (real) {
+            const int64_t ph = static_cast<int64_t>(p) * c.cache.kv_heads + head;
+            uint8_t* codes = all_codes + ph * page * kDim;
+            const float s = fmaxf(s_held, fmaxf(__fmul_rn(most, code_max_inverse<kFmt>()), kScaleFloor));
+            const float per = __fdiv_rn(1.0f, s);
+            const float ratio = __fmul_rn(s_held, per);
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const int at = t + i * group, place = at / kPieces;
+                uint2* q = reinterpret_cast<uint2*>(codes + at * 8);
+                if (place >= from && place < to) {
+                    uint32_t w[2];
+                    if constexpr (kRope) {
+                        encode_values<kFmt, 8>(x[i], most, per, w);
+                    } else {
+                        float v[8];
+                        piece_values<E>(x[i], v);
+                        encode_values<kFmt, 8>(v, most, per, w);
+                    }
+                    *q = make_uint2(w[0], w[1]);
+                } else if (place < from && s != s_held) {
+                    const uint2 w = *q;
+                    *q = make_uint2(again4<kFmt>(w.x, ratio), again4<kFmt>(w.y, ratio));
+                }
+            }
+            if (t == 0) all_scales[ph] = s;
+        }
     }
 }
 
@@ -473,20 +532,23 @@ cudaError_t launch_append(const KvAppendCall& c, int sm_count, cudaStream_t stre
         return cudaGetLastError();
     }
     const int group = c.cache.page * kDim / 8 / kVecs;
-    const int threads = group > 256 ? group : 256;
+    const int threads = group > 128 ? group : 128, groups = threads / group;
     const int half = c.rope.inv_freq != nullptr ? c.rope.rotary / 2 : 0;
     const int smem = c.cache.page * half * 2 * static_cast<int>(sizeof(float));
     const int items = c.batch.total / c.cache.page + 2 * c.batch.batch;
-    // one round of heads a CTA, unless keys are rotated: then the page's cos and sin serve as many
-    // heads as leave four CTAs an SM
-    int heads = threads / group;
-    if (half > 0)
-        while (heads < c.cache.kv_heads && static_cast<int64_t>(items) * (c.cache.kv_heads / (2 * heads)) >= 4 * sm_count) heads *= 2;
-    const PageArgs args{c, wide, heads, 0};
-    const PageArgs plain{c, wide, threads / group, 0};
-    const dim3 all(items, (c.cache.kv_heads + threads / group - 1) / (threads / group), 2);
+    // a CTA takes the heads of a page one after another, as many as leave eight CTAs an SM: what comes
+    // before the first head (five dependent reads, and for keys cos and sin of the page) is paid once,
+    // and the next head's values are on their way while one is written
+    auto heads_for = [&](int64_t ctas_a_round) {
+        int heads = groups;
+        while (heads < c.cache.kv_heads && ctas_a_round * ((c.cache.kv_heads + 2 * heads - 1) / (2 * heads)) >= 8 * sm_count) heads *= 2;
+        return heads;
+    };
+    const int heads = heads_for(half > 0 ? items : 2 * items);
+    const PageArgs plain{c, wide, heads, 0};
+    const unsigned rounds = (c.cache.kv_heads + heads - 1) / heads;
     if (half == 0) {
-        append_pages_kernel<E, kFmt, kDim, false><<<all, threads, 0, stream>>>(plain);
+        append_pages_kernel<E, kFmt, kDim, false><<<dim3(items, rounds, 2), threads, 0, stream>>>(plain);
         return cudaGetLastError();
     }
     static int attr_gen[64] = {};
@@ -498,11 +560,11 @@ cudaError_t launch_append(const KvAppendCall& c, int sm_count, cudaStream_t stre
         if ((e = cudaFuncSetAttribute(turning, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * kDim * 4)) != cudaSuccess) return e;
         attr_gen[dev] = g_generation;
     }
-    turning<<<dim3(items, (c.cache.kv_heads + heads - 1) / heads), threads, smem, stream>>>(args);
+    turning<<<dim3(items, rounds), threads, smem, stream>>>(plain);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     PageArgs of_values = plain;
     of_values.values_only = 1;
-    append_pages_kernel<E, kFmt, kDim, false><<<dim3(items, all.y), threads, 0, stream>>>(of_values);
+    append_pages_kernel<E, kFmt, kDim, false><<<dim3(items, rounds), threads, 0, stream>>>(of_values);
     if ((e = cudaGetLastError()) != cudaSuccess || c.heads == 0) return e;
     append_q_kernel<E><<<(c.batch.total + kQTokens - 1) / kQTokens, kQThreads, kQTokens * half * 2 * sizeof(float), stream>>>(QArgs{c, wide});
     return cudaGetLastError();
