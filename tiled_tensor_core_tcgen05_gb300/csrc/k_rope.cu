@@ -57,81 +57,49 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const RopeCall c) {
 
 // ---- rows on 16-byte boundaries, rotary / 2 (half layout) or rotary (interleaved) a multiple of 8
 //
-// An item is eight values of one head of one token, in the half layout with their eight partners.
-template <typename E>
-struct Item {
-    const E* x;
-    E* y;
-    int d;       // first value
-    int kind;    // 0 none, 1 passes, 2 rotated with partners at d + half, 3 rotated in itself
-    uint4 a, b;
-};
+// An item is eight values of one head of one token, in the half layout with their eight partners. A
+// thread keeps its place in the head (so what it does, and with which pairs, is settled once) and
+// steps through the (token, head) rows of the CTA, four rows' loads at a time.
+constexpr int kAtOnce = 4;
 
-template <typename E>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeCall c, int tokens_a_cta, int per_head) {
+template <typename E, bool kHalf>
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeCall c, int tokens_a_cta, int per_head, int rows_at_once) {
     extern __shared__ float smem[];
     __shared__ int32_t where[kMaxTokens];
     const int half = c.rope.rotary / 2;
     const int token0 = blockIdx.x * tokens_a_cta, n = min(tokens_a_cta, c.tokens - token0);
     float *cs = smem, *sn = smem + tokens_a_cta * half;
-    const int items = n * c.heads * per_head;
-    const int rotated = c.rope.layout == kRopeHalf ? half / 8 : c.rope.rotary / 8;  // items of a head that turn
-    auto load = [&](int i, Item<E>& t, int& slot) {
-        t.kind = 0;
-        if (i >= items) return;
-        const int row = i / per_head, v = i - row * per_head;
-        slot = row / c.heads;
-        const int h = row - slot * c.heads;
-        t.x = static_cast<const E*>(c.x.p) + (token0 + slot) * c.x.token + h * c.x.head;
-        t.y = static_cast<E*>(c.y.p) + (token0 + slot) * c.y.token + h * c.y.head;
-        if (v < rotated) {
-            t.kind = c.rope.layout == kRopeHalf ? 2 : 3;
-            t.d = 8 * v;
-        } else {
-            t.kind = 1;
-            t.d = c.rope.rotary + 8 * (v - rotated);
+    const int v = threadIdx.x % per_head;
+    const int turned = kHalf ? half / 8 : c.rope.rotary / 8;  // items of a head that turn
+    const bool turns = v < turned;
+    const int d = turns ? 8 * v : c.rope.rotary + 8 * (v - turned);
+    int tok = 0, h = threadIdx.x / per_head;  // this thread's next row
+    if (h >= rows_at_once) tok = n;           // beyond the whole rows of threads
+    auto settle = [&] {
+        while (h >= c.heads && tok < n) {
+            h -= c.heads;
+            ++tok;
         }
-        t.a = *reinterpret_cast<const uint4*>(t.x + t.d);
-        if (t.kind == 2) t.b = *reinterpret_cast<const uint4*>(t.x + t.d + half);
     };
-    auto finish = [&](Item<E>& t, int slot) {
-        if (t.kind == 0) return;
-        if (t.kind > 1) {
-            const float *cj = cs + slot * half, *sj = sn + slot * half;
-            E* a = reinterpret_cast<E*>(&t.a);
-            if (t.kind == 2) {
-                E* b = reinterpret_cast<E*>(&t.b);
-                float cv[8], sv[8];
+    settle();
+    uint4 a[kAtOnce], b[kAtOnce];
+    int at[kAtOnce];
+    E* to[kAtOnce];
+    auto load = [&] {
 #pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    *reinterpret_cast<float4*>(cv + i) = *reinterpret_cast<const float4*>(cj + t.d + i);
-                    *reinterpret_cast<float4*>(sv + i) = *reinterpret_cast<const float4*>(sj + t.d + i);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float u = to_float(a[i]), w = to_float(b[i]);
-                    a[i] = from_float<E>(u * cv[i] - w * sv[i]);
-                    b[i] = from_float<E>(w * cv[i] + u * sv[i]);
-                }
-            } else {
-                float cv[4], sv[4];
-                *reinterpret_cast<float4*>(cv) = *reinterpret_cast<const float4*>(cj + t.d / 2);
-                *reinterpret_cast<float4*>(sv) = *reinterpret_cast<const float4*>(sj + t.d / 2);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float u = to_float(a[2 * i]), w = to_float(a[2 * i + 1]);
-                    a[2 * i] = from_float<E>(u * cv[i] - w * sv[i]);
-                    a[2 * i + 1] = from_float<E>(w * cv[i] + u * sv[i]);
-                }
+        for (int i = 0; i < kAtOnce; ++i) {
+            at[i] = tok < n ? tok : -1;
+            if (tok < n) {
+                const E* x = static_cast<const E*>(c.x.p) + static_cast<int64_t>(token0 + tok) * c.x.token + h * c.x.head + d;
+                to[i] = static_cast<E*>(c.y.p) + static_cast<int64_t>(token0 + tok) * c.y.token + h * c.y.head + d;
+                a[i] = *reinterpret_cast<const uint4*>(x);
+                if (kHalf && turns) b[i] = *reinterpret_cast<const uint4*>(x + half);
+                h += rows_at_once;
+                settle();
             }
         }
-        *reinterpret_cast<uint4*>(t.y + t.d) = t.a;
-        if (t.kind == 2) *reinterpret_cast<uint4*>(t.y + t.d + half) = t.b;
     };
-    Item<E> t0, t1;
-    int s0 = 0, s1 = 0;
-    load(threadIdx.x, t0, s0);
-    load(threadIdx.x + kThreads, t1, s1);
+    load();
     if (threadIdx.x < n) where[threadIdx.x] = __ldg(c.positions + token0 + threadIdx.x);
     __syncthreads();
     for (int i = threadIdx.x; i < n * half; i += kThreads) {
@@ -141,28 +109,59 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeCall c, int to
         sn[i] = x.y;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < items; i += 2 * kThreads) {
-        finish(t0, s0);
-        finish(t1, s1);
-        load(i + 2 * kThreads, t0, s0);
-        load(i + 3 * kThreads, t1, s1);
+    constexpr int kPairs = kHalf ? 8 : 4;
+    while (at[0] >= 0) {
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            if (at[i] < 0) continue;
+            if (turns) {
+                float cv[kPairs], sv[kPairs];
+                const int j = at[i] * half + (kHalf ? d : d / 2);
+#pragma unroll
+                for (int e = 0; e < kPairs; e += 4) {
+                    *reinterpret_cast<float4*>(cv + e) = *reinterpret_cast<const float4*>(cs + j + e);
+                    *reinterpret_cast<float4*>(sv + e) = *reinterpret_cast<const float4*>(sn + j + e);
+                }
+                E* p = reinterpret_cast<E*>(&a[i]);
+                E* q = reinterpret_cast<E*>(&b[i]);
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) {
+                    E& first = kHalf ? p[e] : p[2 * e];
+                    E& second = kHalf ? q[e] : p[2 * e + 1];
+                    const float u = to_float(first), w = to_float(second);
+                    first = from_float<E>(u * cv[e] - w * sv[e]);
+                    second = from_float<E>(w * cv[e] + u * sv[e]);
+                }
+            }
+            *reinterpret_cast<uint4*>(to[i]) = a[i];
+            if (kHalf && turns) *reinterpret_cast<uint4*>(to[i] + half) = b[i];
+        }
+        load();
     }
 }
 
 template <typename E>
-cudaError_t launch(const RopeCall& c, cudaStream_t stream) {
+cudaError_t launch(const RopeCall& c, int sm_count, cudaStream_t stream) {
     const int half = c.rope.rotary / 2;
     auto wide = [](const Strided& s) {
         return reinterpret_cast<uintptr_t>(s.p) % 16 == 0 && s.token % 8 == 0 && s.head % 8 == 0;
     };
-    const bool whole = c.rope.layout == kRopeHalf ? half % 8 == 0 : c.rope.rotary % 8 == 0;
+    const bool split = c.rope.layout == kRopeHalf;
+    const bool whole = split ? half % 8 == 0 : c.rope.rotary % 8 == 0;
+    const int per_head = (split ? half : c.rope.rotary) / 8 + (c.dim - c.rope.rotary) / 8;
     if (wide(c.x) && wide(c.y) && c.dim % 8 == 0 && whole) {
-        const int per_head = (c.rope.layout == kRopeHalf ? half : c.rope.rotary) / 8 + (c.dim - c.rope.rotary) / 8;
-        // two items a thread in a CTA, or a few more where heads are few
-        int tokens = 2 * kThreads / (c.heads * per_head);
+        const int rows_at_once = kThreads / per_head;  // dim is at most 1024: per_head at most 128
+        // four rows a thread where there are tokens enough for eight CTAs an SM, and no more tokens than
+        // keep cos and sin of all of them in 32 KB
+        int tokens = kAtOnce * rows_at_once / c.heads;
+        const int many = c.tokens / (8 * sm_count), fit = half > 0 ? 4096 / half : kMaxTokens;
+        tokens = tokens < many ? tokens : many;
+        tokens = tokens < fit ? tokens : fit;
         tokens = tokens < 1 ? 1 : tokens > kMaxTokens ? kMaxTokens : tokens;
         const int smem = tokens * half * 2 * static_cast<int>(sizeof(float));
-        rope_kernel<E><<<(c.tokens + tokens - 1) / tokens, kThreads, smem, stream>>>(c, tokens, per_head);
+        const int grid = (c.tokens + tokens - 1) / tokens;
+        if (split) rope_kernel<E, true><<<grid, kThreads, smem, stream>>>(c, tokens, per_head, rows_at_once);
+        else rope_kernel<E, false><<<grid, kThreads, smem, stream>>>(c, tokens, per_head, rows_at_once);
     } else {
         rope_any_kernel<E><<<c.tokens, kThreads, c.rope.rotary * static_cast<int>(sizeof(float)), stream>>>(c);
     }
@@ -171,8 +170,8 @@ cudaError_t launch(const RopeCall& c, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeCall& c, int, cudaStream_t stream) {
-    return c.dtype == kFp16 ? launch<__half>(c, stream) : launch<__nv_bfloat16>(c, stream);
+cudaError_t launch_rope(const RopeCall& c, int sm_count, cudaStream_t stream) {
+    return c.dtype == kFp16 ? launch<__half>(c, sm_count, stream) : launch<__nv_bfloat16>(c, sm_count, stream);
 }
 
 }  // namespace tg
