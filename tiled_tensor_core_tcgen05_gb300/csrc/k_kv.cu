@@ -43,6 +43,18 @@ __device__ __forceinline__ float max_finite(float most, float x) {
     return a <= 3.402823466e38f ? fmaxf(most, a) : most;
 }
 
+// The largest |x| of eight values as they are stored; NaN where one of them is.
+__device__ __forceinline__ float piece_most(const uint4& u, __half) {
+    const __half2* x = reinterpret_cast<const __half2*>(&u);
+    const __half2 m = __hmax2_nan(__hmax2_nan(__habs2(x[0]), __habs2(x[1])), __hmax2_nan(__habs2(x[2]), __habs2(x[3])));
+    return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+}
+__device__ __forceinline__ float piece_most(const uint4& u, __nv_bfloat16) {
+    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&u);
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(__habs2(x[0]), __habs2(x[1])), __hmax2_nan(__habs2(x[2]), __habs2(x[3])));
+    return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
+}
+
 // Codes of kN values of a row whose block has the largest finite value `most` and 1 / scale `per`.
 template <int kFmt, int kN>
 __device__ __forceinline__ void encode_values(const float (&x)[kN], float most, float per, uint32_t (&w)[kN / 4]) {
@@ -188,24 +200,45 @@ __global__ void __launch_bounds__(512, kRope ? 1 : 2) append_pages_kernel(const 
         const float s_held = s_old;
         // rotated values are kept in fp32, others as they were read: they are half the registers
         std::conditional_t<kRope, float[kVecs][8], uint4[kVecs]> x;
-        float most = 0.0f;
+        float most = 0.0f;  // NaN or infinite where a value is
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             const int at = t + i * group, place = at / kPieces;
             if (real && place >= from && place < to) {
-                float v[8];
-                piece_values<E>(own[i], v);
                 if constexpr (kRope) {
-                    float o[8];
+                    float v[8], o[8];
+                    piece_values<E>(own[i], v);
                     piece_values<E>(other[i], o);
                     rotate_values<8>(v, o, (at - place * kPieces) * 8, cs + place * half, sn + place * half, rope);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[i][e] = v[e];
+                    for (int e = 0; e < 8; ++e) {
+                        x[i][e] = v[e];
+                        most = max_nan(most, fabsf(v[e]));
+                    }
                 } else {
                     x[i] = own[i];
+                    most = max_nan(most, piece_most(own[i], E()));
                 }
+            }
+        }
+        // where this thread's values are all finite, they need no second look
+        const bool plain = most <= 3.402823466e38f;
+        if (!plain) {
+            most = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) most = max_finite(most, v[e]);
+            for (int i = 0; i < kVecs; ++i) {
+                const int place = (t + i * group) / kPieces;
+                if (real && place >= from && place < to) {
+                    float v[8];
+                    if constexpr (kRope) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = x[i][e];
+                    } else {
+                        piece_values<E>(x[i], v);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) most = max_finite(most, v[e]);
+                }
             }
         }
         fetch(head + groups);
@@ -229,11 +262,19 @@ __global__ void __launch_bounds__(512, kRope ? 1 : 2) append_pages_kernel(const 
                 uint2* q = reinterpret_cast<uint2*>(codes + at * 8);
                 if (place >= from && place < to) {
                     uint32_t w[2];
+                    float v[8];
                     if constexpr (kRope) {
-                        encode_values<kFmt, 8>(x[i], most, per, w);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = x[i][e];
                     } else {
-                        float v[8];
                         piece_values<E>(x[i], v);
+                    }
+                    if (plain) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], per);
+                        w[0] = encode4_in_range<kFmt>(v[0], v[1], v[2], v[3]);
+                        w[1] = encode4_in_range<kFmt>(v[4], v[5], v[6], v[7]);
+                    } else {
                         encode_values<kFmt, 8>(v, most, per, w);
                     }
                     *q = make_uint2(w[0], w[1]);

@@ -230,6 +230,20 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
     }
 }
 
+// encode4 for values known to be finite and at most the largest code (and a rounding error): int8 codes
+// are the low bytes of x + 1.5 * 2^23, whose steps are 1 and whose rounding is to nearest even.
+template <int kFmt>
+__device__ __forceinline__ uint32_t encode4_in_range(float a, float b, float c, float d) {
+    if constexpr (kFmt == kKvE4M3) {
+        return encode4<kFmt>(a, b, c, d);
+    } else {
+        const float k = 12582912.0f;
+        const uint32_t lo = __byte_perm(__float_as_uint(__fadd_rn(a, k)), __float_as_uint(__fadd_rn(b, k)), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(__fadd_rn(c, k)), __float_as_uint(__fadd_rn(d, k)), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
+    }
+}
+
 template <int kFmt>
 __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
     if constexpr (kFmt == kKvE4M3) {
@@ -244,8 +258,12 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
         x[2] = b.x;
         x[3] = b.y;
     } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = static_cast<float>(static_cast<int8_t>(w >> (8 * i)));
+        // code + 128 as the low byte of 2^23 + (code + 128), whose steps are 1: no integer conversion
+        const uint32_t u = w ^ 0x80808080u;
+        x[0] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)) - 8388736.0f;
+        x[1] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441)) - 8388736.0f;
+        x[2] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)) - 8388736.0f;
+        x[3] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443)) - 8388736.0f;
     }
 }
 
