@@ -49,10 +49,13 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = kWarps * kStep;       // tokens per unit of the work list
-constexpr int kStages = 4;                   // steps in flight per warp
+
+// CTAs that fit an SM: registers for the queries and outputs of all tiles decide.
+constexpr int ctas_a_sm(int dim, int tiles) { return dim * tiles >= 320 ? 2 : 3; }
 
 template <int kDim>
 struct Ring {
+    static constexpr int kStages = kDim == 64 ? 6 : 4;   // steps in flight per warp
     static constexpr int kHalf = kStep * kDim;       // bytes of one step's keys (or values)
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kWarp = kStages * kStage;
@@ -84,7 +87,7 @@ __device__ __forceinline__ SeqWork seq_work(const SplitWork& a, int i) {
     w.chunk0 = begin > 0 ? static_cast<int>(begin / kChunk) : 0;
     w.chunks = max(1, (w.len + kChunk - 1) / kChunk - w.chunk0);
     w.blocks = static_cast<int>((static_cast<int64_t>(w.count) * a.share + 8 * kTiles - 1) / (8 * kTiles));
-    w.total = static_cast<int64_t>(w.blocks) * c.cache.kv_heads * w.chunks;
+    w.total = static_cast<int64_t>(w.blocks) * c.cache.kv_heads * (w.chunks + a.extra);
     return w;
 }
 
@@ -116,25 +119,23 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
-// Four values of a query row from `d` on; bytes past a row's end are never read.
+// Four values of a query row as they are stored.
 template <typename E>
-__device__ __forceinline__ void load_q4(const E* row, int d, bool vec, float (&x)[4]) {
-    if (vec) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + d));
-        const E* e = reinterpret_cast<const E*>(&w);
+__device__ __forceinline__ uint2 load_four(const E* p, bool vec) {
+    if (vec) return __ldg(reinterpret_cast<const uint2*>(p));
+    uint2 u;
+    E* e = reinterpret_cast<E*>(&u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = to_float(e[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = to_float(row[d + i]);
-    }
+    for (int i = 0; i < 4; ++i) e[i] = p[i];
+    return u;
 }
 
 template <typename E, int kFmt, int kDim, int kTiles>
-__global__ void __launch_bounds__(kThreads, kTiles == 4 && kDim == 128 ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, ctas_a_sm(kDim, kTiles))
     attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const SplitWork a) {
     constexpr int kRows = 8 * kTiles;
     constexpr int kK = kDim / 16;            // MMA steps along dim (scores) and m16 tiles along dim (values)
+    constexpr int kStages = Ring<kDim>::kStages;
     extern __shared__ uint8_t smem_raw[];
     __shared__ alignas(8) uint64_t bars[kWarps * kStages];
     __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows];
@@ -225,14 +226,19 @@ __global__ void __launch_bounds__(kThreads, kTiles == 4 && kDim == 128 ? 2 : 3)
             } while (w.total == 0);
             off = 0;
         }
-        const int unit = static_cast<int>(off / w.chunks);
-        const int c0 = static_cast<int>(off - static_cast<int64_t>(unit) * w.chunks);
-        const int c1 = static_cast<int>(min(static_cast<int64_t>(w.chunks), c0 + (stop - pos)));
+        const int entries = w.chunks + a.extra;
+        const int unit = static_cast<int>(off / entries);
+        const int e0 = static_cast<int>(off - static_cast<int64_t>(unit) * entries);
+        const int e1 = static_cast<int>(min(static_cast<int64_t>(entries), e0 + (stop - pos)));
+        const int c0 = max(0, e0 - a.extra), c1 = max(0, e1 - a.extra);
         const int head = unit / w.blocks, block = unit - head * w.blocks;
         if (first_segment && threadIdx.x == 0) {
-            Meta m{pos - c0, total, c0 > 0 ? w.chunks : 0, seq, head, block};
+            Meta m{pos - e0, total, c0 > 0 ? w.chunks : 0, seq, head, block};
             a.meta[k] = m;
         }
+        pos += e1 - e0;
+        off += e1 - e0;
+        if (c1 == 0) continue;  // the share ends before the unit's first chunk
         const int row0 = block * kRows, rows = min(kRows, w.count * a.share - row0);
 
         // ---- the steps of this warp: chunks i0 .. i1 - 1, its 16 tokens of each
@@ -290,24 +296,29 @@ __global__ void __launch_bounds__(kThreads, kTiles == 4 && kDim == 128 ? 2 : 3)
         float factor[kTiles][2];     // of rows 2 tig, 2 tig + 1: scale * log2(e) / that power
         int see_from[kTiles][2], see_to[kTiles][2];
 #pragma unroll
-        for (int n = 0; n < kTiles; ++n) {
-            const int r = row0 + min(8 * n + gid, rows - 1);
-            const int t = r / a.share;
-            const E* x = static_cast<const E*>(c.q.p) + (w.first + t) * c.q.token + (head * a.share + r - t * a.share) * c.q.head;
-            const bool real = 8 * n + gid < rows;
-            float most = 0.0f;
-            float f = c.scale * kLog2e;
-            float v[kK][4];
+        for (int n = 0; n < kTiles; ++n) {  // all tiles' reads first, so that they wait once
+            const int r = row0 + min(8 * n + gid, rows - 1), t = r / a.share;
+            const E* x = static_cast<const E*>(c.q.p) + static_cast<int64_t>(w.first + t) * c.q.token + (head * a.share + r - t * a.share) * c.q.head;
 #pragma unroll
             for (int s = 0; s < kK; ++s) {
-                load_q4(x, (s >> 2) * 64 + tig * 16 + (s & 3) * 4, a.q_vec != 0, v[s]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (!real) v[s][e] = 0.0f;
-                    most = fmaxf(most, fabsf(v[s][e]));
-                }
+                const uint2 u = load_four(x + (s >> 2) * 64 + tig * 16 + (s & 3) * 4, a.q_vec != 0);
+                q[n][s][0] = u.x;
+                q[n][s][1] = u.y;
             }
+        }
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+            const bool real = 8 * n + gid < rows;
+            float f = c.scale * kLog2e;
             if constexpr (!std::is_same<E, __half>::value) {
+                float most = 0.0f;
+#pragma unroll
+                for (int s = 0; s < kK; ++s)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const __nv_bfloat162 y = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&q[n][s][e]));
+                        most = fmaxf(most, fmaxf(__low2float(y), __high2float(y)));
+                    }
                 most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
                 most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
                 // the exponent of the largest value, kept where 2^(14 - e) is an ordinary number
@@ -317,12 +328,14 @@ __global__ void __launch_bounds__(kThreads, kTiles == 4 && kDim == 128 ? 2 : 3)
 #pragma unroll
                 for (int s = 0; s < kK; ++s)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[s][j] *= up;
+                    for (int j = 0; j < 2; ++j) {
+                        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q[n][s][j]));
+                        q[n][s][j] = half2_bits(y.x * up, y.y * up);
+                    }
             }
+            if (!real) {
 #pragma unroll
-            for (int s = 0; s < kK; ++s) {
-                q[n][s][0] = half2_bits(v[s][0], v[s][1]);
-                q[n][s][1] = half2_bits(v[s][2], v[s][3]);
+                for (int s = 0; s < kK; ++s) q[n][s][0] = q[n][s][1] = 0;
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -559,26 +572,41 @@ __global__ void __launch_bounds__(kThreads, kTiles == 4 && kDim == 128 ? 2 : 3)
         }
         fence_proxy_async_smem();  // these reads and writes come before the next copies into the rings
         __syncthreads();
-        pos += c1 - c0;
-        off += c1 - c0;
         first_segment = false;
     }
 }
+
+// Row tiles a block can have: what the registers of a thread hold.
+constexpr int kMaxTiles128 = 4, kMaxTiles64 = 6;
 
 // How the few-rows kernel runs a call: row tiles, CTAs, workspace.
 struct FewPlan {
     int tiles, grid, rows;
     bool split;            // a unit may cross shares
+    int least, extra;
     int64_t meta_bytes, bytes;
 };
 
 FewPlan few_plan(const KvAttnCall& c, int sm_count) {
     FewPlan p{};
     const int64_t most = static_cast<int64_t>(c.batch.max_new) * (c.heads / c.cache.kv_heads);
-    p.tiles = most <= 8 ? 1 : most <= 16 ? 2 : 4;
+    // the fewest row blocks (each reads the cache), then the fewest tiles that hold a block's rows
+    const int64_t widest = c.cache.dim == 128 ? kMaxTiles128 : kMaxTiles64;
+    const int64_t least_blocks = (most + 8 * widest - 1) / (8 * widest);
+    p.tiles = static_cast<int>((most + 8 * least_blocks - 1) / (8 * least_blocks));
     p.rows = 8 * p.tiles;
-    p.grid = sm_count * (p.tiles == 4 && c.cache.dim == 128 ? 2 : 3);
+    p.grid = sm_count * ctas_a_sm(c.cache.dim, p.tiles);
     p.split = c.max_len > kChunk;
+    // Every unit costs a share about as much as four chunks, whatever its length (its queries, an empty
+    // pipeline, the join of four warps), and a CTA is worth starting for eight. 64 ragged sequences, three of
+    // them idle: 130 us without that charge (one share held all the idle units), 110 with it, 110 with
+    // twice it; one sequence of 16000: 23.4 us with any CTA, 20.5 with eight. Where the whole list is less
+    // than two chunks a CTA, every chunk pair has a CTA to itself (one sequence of 1023: 9.6 us, not 11.2),
+    // and every unit of a single chunk.
+    const int64_t blocks = (most + p.rows - 1) / p.rows, chunks = (c.max_len + kChunk - 1) / kChunk;
+    const bool small = blocks * c.cache.kv_heads * c.batch.batch * chunks <= 2 * p.grid;
+    p.least = !small ? 8 : chunks >= 2 ? 2 : 1;
+    p.extra = small ? 0 : 4;
     p.meta_bytes = (static_cast<int64_t>(p.grid) * sizeof(Meta) + 255) / 256 * 256;
     p.bytes = p.meta_bytes + static_cast<int64_t>(p.grid) * 2 * p.rows * (c.cache.dim + 2) * 4;
     return p;
@@ -603,7 +631,8 @@ cudaError_t launch_few(const KvAttnCall& c, const CUtensorMap& tmK, const CUtens
     SplitWork a{};
     a.c = c;
     a.share = c.heads / c.cache.kv_heads;
-    a.least = 1;
+    a.least = p.least;
+    a.extra = p.extra;
     a.grid = p.grid;
     a.q_vec = reinterpret_cast<uintptr_t>(c.q.p) % 8 == 0 && c.q.token % 4 == 0 && c.q.head % 4 == 0;
     a.meta = static_cast<Meta*>(workspace);
@@ -617,12 +646,18 @@ cudaError_t launch_few(const KvAttnCall& c, const CUtensorMap& tmK, const CUtens
 template <typename E, int kFmt, int kDim>
 cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count,
                    cudaStream_t stream) {
-    {
-        const FewPlan p = few_plan(c, sm_count);
-        if (p.tiles == 1) return launch_few<E, kFmt, kDim, 1>(c, tmK, tmV, workspace, p, stream);
-        if (p.tiles == 2) return launch_few<E, kFmt, kDim, 2>(c, tmK, tmV, workspace, p, stream);
-        return launch_few<E, kFmt, kDim, 4>(c, tmK, tmV, workspace, p, stream);
+    const FewPlan p = few_plan(c, sm_count);
+    switch (p.tiles) {
+        case 1: return launch_few<E, kFmt, kDim, 1>(c, tmK, tmV, workspace, p, stream);
+        case 2: return launch_few<E, kFmt, kDim, 2>(c, tmK, tmV, workspace, p, stream);
+        case 3: return launch_few<E, kFmt, kDim, 3>(c, tmK, tmV, workspace, p, stream);
+        case 4: return launch_few<E, kFmt, kDim, 4>(c, tmK, tmV, workspace, p, stream);
     }
+    if constexpr (kDim == 64) {
+        if (p.tiles == 5) return launch_few<E, kFmt, kDim, 5>(c, tmK, tmV, workspace, p, stream);
+        if (p.tiles == 6) return launch_few<E, kFmt, kDim, 6>(c, tmK, tmV, workspace, p, stream);
+    }
+    return cudaErrorInvalidConfiguration;
 }
 
 }  // namespace

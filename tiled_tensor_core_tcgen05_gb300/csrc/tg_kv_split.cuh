@@ -56,7 +56,8 @@ struct Shares {
     }
 };
 
-// What CTA k leaves for the joining kernel: the unit that its share begins inside of (chunks 0: none).
+// What CTA k leaves for the joining kernel: the unit of which its share begins past the first chunk
+// (chunks 0: none), and where that unit's entries begin in the list.
 struct Meta {
     int64_t unit_start, total;
     int chunks, seq, head, block;
@@ -67,6 +68,7 @@ struct SplitWork {
     KvAttnCall c;
     int share;          // query heads per kv head
     int least;          // fewest list entries worth a CTA
+    int extra;          // entries before a unit's first chunk, for what every unit costs whatever its length
     int grid;
     int q_vec;          // Q aligned, and strides whole, for the kernel's wide loads
     int page_shift;
@@ -133,12 +135,12 @@ __global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const SplitWo
     const Meta m = a.meta[k];
     if (m.chunks == 0) return;
     const Shares shares(m.total, a.grid, a.least);
-    const int64_t before = shares.start(k - 1);
-    if (before > m.unit_start) return;  // an earlier border lies in the unit
+    const int64_t before = shares.start(k - 1), first_chunk = m.unit_start + a.extra;
+    if (before > first_chunk) return;  // an earlier border lies in the unit's chunks
     const SeqSpan span = seq_span(c.batch, m.seq, c.wd);
     const int row = m.block * kRows + r;
     if (row >= span.count * a.share) return;
-    const int last = shares.owner(m.unit_start + m.chunks - 1);
+    const int last = shares.owner(first_chunk + m.chunks - 1);
     auto part_of = [&](int x) {
         const int slot = x == k - 1 && before < m.unit_start ? 1 : 0;
         return a.parts + (static_cast<int64_t>(2 * x) + slot) * kRows * (kDim + 2);
