@@ -12,6 +12,7 @@
 
 #include "tg_gemm.h"
 #include "tg_internal.h"
+#include "tg_kv_internal.h"
 
 namespace tg {
 int g_generation = 1;

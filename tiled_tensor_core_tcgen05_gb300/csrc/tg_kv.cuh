@@ -6,7 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "tg_internal.h"
+#include "tg_kv_internal.h"
 #include "tg_ptx.cuh"
 
 namespace tg {
