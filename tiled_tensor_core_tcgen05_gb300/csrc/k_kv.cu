@@ -181,15 +181,19 @@ __global__ void __launch_bounds__(512, kRope ? 1 : 2) append_pages_kernel(const 
     auto fetch = [&](int head) {
         if (head >= head_end) return;
         s_old = from > 0 ? all_scales[static_cast<int64_t>(p) * c.cache.kv_heads + head] : 0.0f;
+        auto pieces = [&](bool wide) {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int at = t + i * group, place = at / kPieces, d = (at - place * kPieces) * 8;
-            if (place >= from && place < to) {
-                const E* row = x0 + place * src.token + head * src.head;
-                own[i] = load_piece(row + d, vec);
-                if constexpr (kRope) other[i] = load_partner_piece(row, d, vec, rope);
+            for (int i = 0; i < kVecs; ++i) {
+                const int at = t + i * group, place = at / kPieces, d = (at - place * kPieces) * 8;
+                if (place >= from && place < to) {
+                    const E* row = x0 + place * src.token + head * src.head;
+                    own[i] = load_piece(row + d, wide);
+                    if constexpr (kRope) other[i] = load_partner_piece(row, d, wide, rope);
+                }
             }
-        }
+        };
+        if (vec) pieces(true);
+        else pieces(false);
     };
     fetch(blockIdx.y * a.heads_a_cta + g);
     int round = 0;
@@ -221,8 +225,9 @@ __global__ void __launch_bounds__(512, kRope ? 1 : 2) append_pages_kernel(const 
                 }
             }
         }
-        // where this thread's values are all finite, they need no second look
-        const bool plain = most <= 3.402823466e38f;
+        // where the warp's values are all finite, they need no second look (a branch of the whole warp: taken
+        // thread by thread, the instructions of the other way were issued too)
+        const bool plain = __all_sync(0xFFFFFFFFu, most <= 3.402823466e38f);
         if (!plain) {
             most = 0.0f;
 #pragma unroll
