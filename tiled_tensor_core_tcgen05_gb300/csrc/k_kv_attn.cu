@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, ctas_a_sm(kDim, kTiles))
         const int c0 = max(0, e0 - a.extra), c1 = max(0, e1 - a.extra);
         const int head = unit / w.blocks, block = unit - head * w.blocks;
         if (first_segment && threadIdx.x == 0) {
-            Meta m{pos - e0, total, c0 > 0 ? w.chunks : 0, seq, head, block};
+            Meta m{pos - e0, total, c0 > 0 ? w.chunks : 0, head, block, w.first, w.count};
             a.meta[k] = m;
         }
         pos += e1 - e0;

@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (true) {
             // all of the half go on, or none: no warp waits at a barrier for one that has left
             if (named_barrier_or(1 + h, 256, !next_segment(sg))) break;
-            if (first_segment && threadIdx.x == 0) a.meta[k] = Meta{start - sg.t0, total, sg.t0 > 0 ? sg.tiles : 0, sg.seq, sg.head, sg.block};
+            if (first_segment && threadIdx.x == 0) a.meta[k] = Meta{start - sg.t0, total, sg.t0 > 0 ? sg.tiles : 0, sg.head, sg.block, sg.first, sg.count};
             const int r = sg.block * kRows + h * kHalfRows + row;      // row of the (sequence, kv head)
             const bool real = r < sg.count * a.share;
             const int t = r / a.share;

@@ -60,7 +60,8 @@ struct Shares {
 // (chunks 0: none), and where that unit's entries begin in the list.
 struct Meta {
     int64_t unit_start, total;
-    int chunks, seq, head, block;
+    int chunks, head, block;
+    int first, count;   // the sequence's rows of the packed tensors
 };
 
 // A split call: what both kernels and the join need.
@@ -137,50 +138,62 @@ __global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const SplitWo
     const Shares shares(m.total, a.grid, a.least);
     const int64_t before = shares.start(k - 1), first_chunk = m.unit_start + a.extra;
     if (before > first_chunk) return;  // an earlier border lies in the unit's chunks
-    const SeqSpan span = seq_span(c.batch, m.seq, c.wd);
     const int row = m.block * kRows + r;
-    if (row >= span.count * a.share) return;
+    if (row >= m.count * a.share) return;
     const int last = shares.owner(first_chunk + m.chunks - 1);
     auto part_of = [&](int x) {
         const int slot = x == k - 1 && before < m.unit_start ? 1 : 0;
         return a.parts + (static_cast<int64_t>(2 * x) + slot) * kRows * (kDim + 2);
     };
-    float top = kNoMax;
-    for (int x0 = k - 1; x0 <= last; x0 += 32) {
-        const int x = x0 + lane;
-        if (x <= last) top = fmaxf(top, part_of(x)[kRows * kDim + r]);
+    struct alignas(4 * kN) Values {
+        float v[kN];
+    };
+    auto values_of = [&](int x) { return *reinterpret_cast<const Values*>(part_of(x) + r * kDim + lane * kN); };
+    // the first parts' values are on their way while the maxima and sums are read and compared
+    constexpr int kAhead = 8;
+    Values ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (k - 1 + i <= last) ahead[i] = values_of(k - 1 + i);
+    float top = kNoMax, own_m = kNoMax, own_l = 0.0f;
+    for (int x = k - 1 + lane; x <= last; x += 32) {
+        const float y = part_of(x)[kRows * kDim + r];
+        if (x < k - 1 + 32) {
+            own_m = y;
+            own_l = part_of(x)[kRows * (kDim + 1) + r];
+        }
+        top = fmaxf(top, y);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     float v[kN] = {}, sum = 0.0f;
     for (int x0 = k - 1; x0 <= last; x0 += 32) {
-        const int x = x0 + lane;
-        float keep = 0.0f, l = 0.0f;
-        if (x <= last) {
-            keep = ex2_approx(part_of(x)[kRows * kDim + r] - top);
-            l = part_of(x)[kRows * (kDim + 1) + r] * keep;
+        if (x0 > k - 1) {
+            const int x = x0 + lane;
+            own_m = x <= last ? part_of(x)[kRows * kDim + r] : kNoMax;
+            own_l = x <= last ? part_of(x)[kRows * (kDim + 1) + r] : 0.0f;
         }
+        const float keep = ex2_approx(own_m - top), l = own_l * keep;
         const int many = min(32, last + 1 - x0);
-#pragma unroll 8
-        for (int i = 0; i < many; ++i) {
-            const float* p = part_of(x0 + i) + r * kDim + lane * kN;
+        auto add = [&](int i, const Values& y) {
             const float w = __shfl_sync(0xFFFFFFFFu, keep, i);
             sum += __shfl_sync(0xFFFFFFFFu, l, i);
-            if constexpr (kN == 4) {
-                const float4 y = *reinterpret_cast<const float4*>(p);
-                v[0] = fmaf(y.x, w, v[0]);
-                v[1] = fmaf(y.y, w, v[1]);
-                v[2] = fmaf(y.z, w, v[2]);
-                v[3] = fmaf(y.w, w, v[3]);
-            } else {
-                const float2 y = *reinterpret_cast<const float2*>(p);
-                v[0] = fmaf(y.x, w, v[0]);
-                v[1] = fmaf(y.y, w, v[1]);
+#pragma unroll
+            for (int e = 0; e < kN; ++e) v[e] = fmaf(y.v[e], w, v[e]);
+        };
+        for (int i = 0; i < many; i += kAhead) {  // a group's reads together
+            if (x0 > k - 1 || i > 0) {
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if (i + j < many) ahead[j] = values_of(x0 + i + j);
             }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (i + j < many) add(i + j, ahead[j]);
         }
     }
     const int t = row / a.share;
-    const int64_t to = static_cast<int64_t>(span.first + t) * c.heads + m.head * a.share + row - t * a.share;
+    const int64_t to = static_cast<int64_t>(m.first + t) * c.heads + m.head * a.share + row - t * a.share;
     const float inv = row_inverse(sum);
     E out[kN];
 #pragma unroll
