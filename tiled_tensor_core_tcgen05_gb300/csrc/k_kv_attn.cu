@@ -49,13 +49,11 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = kWarps * kStep;       // tokens per unit of the work list
-
-// CTAs that fit an SM: registers for the queries and outputs of all tiles decide.
-constexpr int ctas_a_sm(int dim, int tiles) { return dim * tiles >= 320 ? 2 : 3; }
+constexpr int kCtasPerSm = 3;
 
 template <int kDim>
 struct Ring {
-    static constexpr int kStages = kDim == 64 ? 6 : 4;   // steps in flight per warp
+    static constexpr int kStages = 4;                // steps in flight per warp
     static constexpr int kHalf = kStep * kDim;       // bytes of one step's keys (or values)
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kWarp = kStages * kStage;
@@ -131,7 +129,7 @@ __device__ __forceinline__ uint2 load_four(const E* p, bool vec) {
 }
 
 template <typename E, int kFmt, int kDim, int kTiles>
-__global__ void __launch_bounds__(kThreads, ctas_a_sm(kDim, kTiles))
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const SplitWork a) {
     constexpr int kRows = 8 * kTiles;
     constexpr int kK = kDim / 16;            // MMA steps along dim (scores) and m16 tiles along dim (values)
@@ -576,8 +574,11 @@ __global__ void __launch_bounds__(kThreads, ctas_a_sm(kDim, kTiles))
     }
 }
 
-// Row tiles a block can have: what the registers of a thread hold.
-constexpr int kMaxTiles128 = 4, kMaxTiles64 = 6;
+// Row tiles of a block. Wider blocks read the cache less often, but their queries and outputs take the
+// registers of a third CTA on the SM, and there are fewer of them: 33 sequences of 35 rows, dim 64, window 2048, run in
+// 32.5 us with blocks of 40 rows, 28.7 with 24, 25.8 with 16; 120 of them without a window, 368 MB of cache,
+// in 119, 107 and 106 us (a unit's blocks are neighbours in the list, so the later ones read L2).
+constexpr int kMaxTiles = 2;
 
 // How the few-rows kernel runs a call: row tiles, CTAs, workspace.
 struct FewPlan {
@@ -590,12 +591,11 @@ struct FewPlan {
 FewPlan few_plan(const KvAttnCall& c, int sm_count) {
     FewPlan p{};
     const int64_t most = static_cast<int64_t>(c.batch.max_new) * (c.heads / c.cache.kv_heads);
-    // the fewest row blocks (each reads the cache), then the fewest tiles that hold a block's rows
-    const int64_t widest = c.cache.dim == 128 ? kMaxTiles128 : kMaxTiles64;
-    const int64_t least_blocks = (most + 8 * widest - 1) / (8 * widest);
+    // the fewest row blocks, then the fewest tiles that hold a block's rows
+    const int64_t least_blocks = (most + 8 * kMaxTiles - 1) / (8 * kMaxTiles);
     p.tiles = static_cast<int>((most + 8 * least_blocks - 1) / (8 * least_blocks));
     p.rows = 8 * p.tiles;
-    p.grid = sm_count * ctas_a_sm(c.cache.dim, p.tiles);
+    p.grid = sm_count * kCtasPerSm;
     p.split = c.max_len > kChunk;
     // Every unit costs a share about as much as four chunks, whatever its length (its queries, an empty
     // pipeline, the join of four warps), and a CTA is worth starting for eight. 64 ragged sequences, three of
@@ -612,7 +612,10 @@ FewPlan few_plan(const KvAttnCall& c, int sm_count) {
     return p;
 }
 
-// Rows of one kv head beyond which the few-rows kernel is not taken.
+// Rows of one kv head up to which a call runs here; above, k_kv_tile.cu takes it. Measured in us, here and there,
+// with 32 heads over 8: 32 sequences of 2000, 36 rows 44 and 85, 64 rows 56 and 91, 96 rows 81 and 91, 128 rows 94
+// and 99, 192 rows 140 and 103; four of 30000, 64 rows 88 and 105, 96 rows 129 and 108. Only calls too small to
+// fill the GPU are still quicker here beyond it: two of 2000, 128 rows 21 and 27, 256 rows 27 and 34.
 bool few_rows(const KvAttnCall& c) { return static_cast<int64_t>(c.batch.max_new) * (c.heads / c.cache.kv_heads) <= 64; }
 
 template <typename E, int kFmt, int kDim, int kTiles>
@@ -647,17 +650,8 @@ template <typename E, int kFmt, int kDim>
 cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count,
                    cudaStream_t stream) {
     const FewPlan p = few_plan(c, sm_count);
-    switch (p.tiles) {
-        case 1: return launch_few<E, kFmt, kDim, 1>(c, tmK, tmV, workspace, p, stream);
-        case 2: return launch_few<E, kFmt, kDim, 2>(c, tmK, tmV, workspace, p, stream);
-        case 3: return launch_few<E, kFmt, kDim, 3>(c, tmK, tmV, workspace, p, stream);
-        case 4: return launch_few<E, kFmt, kDim, 4>(c, tmK, tmV, workspace, p, stream);
-    }
-    if constexpr (kDim == 64) {
-        if (p.tiles == 5) return launch_few<E, kFmt, kDim, 5>(c, tmK, tmV, workspace, p, stream);
-        if (p.tiles == 6) return launch_few<E, kFmt, kDim, 6>(c, tmK, tmV, workspace, p, stream);
-    }
-    return cudaErrorInvalidConfiguration;
+    if (p.tiles == 1) return launch_few<E, kFmt, kDim, 1>(c, tmK, tmV, workspace, p, stream);
+    return launch_few<E, kFmt, kDim, 2>(c, tmK, tmV, workspace, p, stream);
 }
 
 }  // namespace
