@@ -18,7 +18,7 @@
 // each is read once. Single tokens go sequence by sequence: a CTA rotates and
 // writes all heads of one token (and rotates its queries), a head a warp, and
 // only where a scale grows are the page's held codes touched at all.
-#include "tg_kv.cuh"
+#include "tg_rope.cuh"
 
 #include <type_traits>
 
@@ -157,16 +157,6 @@ __global__ void __launch_bounds__(512, kRope ? 1 : 2) append_pages_kernel(const 
     const RopeArgs& rope = c.rope;
     const int half = rope.rotary / 2;
     float *cs = turns, *sn = turns + page * half;
-    if constexpr (kRope) {
-        for (int i = threadIdx.x; i < (to - from) * half; i += blockDim.x) {
-            const int t = i / half, j = i - t * half;
-            const float2 x = turn_cos_sin(turn_step(__ldg(rope.inv_freq + j)), static_cast<int>(slot * page) + from + t, rope.amplitude, rope.sign);
-            cs[(from + t) * half + j] = x.x;
-            sn[(from + t) * half + j] = x.y;
-        }
-        __syncthreads();
-    }
-
     const int group = page * kPieces / kVecs, groups = blockDim.x / group;
     const int g = threadIdx.x / group, t = threadIdx.x - g * group;
     const Strided& src = values ? c.v : c.k;
@@ -196,6 +186,15 @@ __global__ void __launch_bounds__(512, kRope ? 1 : 2) append_pages_kernel(const 
         else pieces(false);
     };
     fetch(blockIdx.y * a.heads_a_cta + g);
+    if constexpr (kRope) {
+        for (int i = threadIdx.x; i < (to - from) * half; i += blockDim.x) {
+            const int t = i / half, j = i - t * half;
+            const float2 x = turn_cos_sin(turn_step(__ldg(rope.inv_freq + j)), static_cast<int>(slot * page) + from + t, rope.amplitude, rope.sign);
+            cs[(from + t) * half + j] = x.x;
+            sn[(from + t) * half + j] = x.y;
+        }
+        __syncthreads();
+    }
     int round = 0;
     // every group makes every round, so that all meet at the barriers
     for (int head0 = blockIdx.y * a.heads_a_cta; head0 < head_end; head0 += groups, ++round) {
@@ -406,23 +405,11 @@ __global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const Token
 
 // ---------------------------------------------------------------- queries beside a prompt's keys
 
-constexpr int kQThreads = 256;
-constexpr int kQTokens = 4;  // per CTA
+constexpr int kQTokens = 4;  // per CTA, where rows are not whole 16-byte pieces
 
-struct QArgs {
-    KvAppendCall c;
-    Wide wide;
-};
-
-// cos and sin of a few tokens once for all their heads, then a thread per eight values (with their
-// partners in the half layout when whole pieces pair up, else pair by pair).
-template <typename E>
-__global__ void __launch_bounds__(kQThreads) append_q_kernel(const QArgs a) {
-    extern __shared__ float turns[];
-    __shared__ int32_t where[kQTokens];
-    const KvAppendCall& c = a.c;
+// The positions of tokens token0 .. token0 + n - 1; -1 for one of no sequence or of no place.
+__device__ __forceinline__ void q_positions(const KvAppendCall& c, int32_t* where, int token0, int n) {
     const KvBatch& b = c.batch;
-    const int token0 = blockIdx.x * kQTokens, n = min(kQTokens, b.total - token0);
     const int first = block_find(b.batch, [&](int i) { return static_cast<int64_t>(b.cu ? __ldg(b.cu + i) : i); }, token0);
     if (threadIdx.x < n) {
         const int token = token0 + threadIdx.x;
@@ -435,48 +422,33 @@ __global__ void __launch_bounds__(kQThreads) append_q_kernel(const QArgs a) {
         }
         where[threadIdx.x] = at;
     }
+}
+
+template <typename E, bool kHalf>
+__global__ void __launch_bounds__(kRopeThreads, 4) append_q_kernel(const KvAppendCall c, const RopeRows r) {
+    extern __shared__ float smem[];
+    rope_rows<E, kHalf, true>(r, smem, [&](int32_t* where, int token0, int n) { q_positions(c, where, token0, n); });
+}
+
+// Any alignment and rotary width: pair by pair.
+template <typename E>
+__global__ void __launch_bounds__(kRopeThreads) append_q_any_kernel(const KvAppendCall c) {
+    extern __shared__ float turns[];
+    __shared__ int32_t where[kQTokens];
+    const int token0 = blockIdx.x * kQTokens, n = min(kQTokens, c.batch.total - token0);
+    q_positions(c, where, token0, n);
     __syncthreads();
     const int half = c.rope.rotary / 2, dim = c.cache.dim;
     float *cs = turns, *sn = turns + n * half;
-    for (int i = threadIdx.x; i < n * half; i += kQThreads) {
+    for (int i = threadIdx.x; i < n * half; i += kRopeThreads) {
         const int t = i / half;
         const float2 x = turn_cos_sin(turn_step(__ldg(c.rope.inv_freq + (i - t * half))), where[t], c.rope.amplitude, c.rope.sign);
         cs[i] = x.x;
         sn[i] = x.y;
     }
     __syncthreads();
-    const bool whole = a.wide.q && a.wide.q_out && (c.rope.layout == kRopeHalf ? half % 8 == 0 : c.rope.rotary % 8 == 0);
-    if (whole) {
-        const bool split = c.rope.layout == kRopeHalf;
-        const int turned = split ? half / 8 : c.rope.rotary / 8, per_head = turned + (dim - c.rope.rotary) / 8;
-        const int items = n * c.heads * per_head;
-#pragma unroll 2
-        for (int i = threadIdx.x; i < items; i += kQThreads) {
-            const int row = i / per_head, v = i - row * per_head, t = row / c.heads, h = row - t * c.heads;
-            if (where[t] < 0) continue;
-            const E* x = static_cast<const E*>(c.q.p) + static_cast<int64_t>(token0 + t) * c.q.token + h * c.q.head;
-            E* y = static_cast<E*>(c.q_out.p) + static_cast<int64_t>(token0 + t) * c.q_out.token + h * c.q_out.head;
-            const int d = v < turned ? 8 * v : c.rope.rotary + 8 * (v - turned);
-            float u[8], w[8];
-            load_values<E, 8>(x, d, true, u);
-            if (v < turned && split) {
-                load_values<E, 8>(x, d + half, true, w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float cc = cs[t * half + d + e], ss = sn[t * half + d + e], p = u[e], q = w[e];
-                    u[e] = p * cc - q * ss;
-                    w[e] = q * cc + p * ss;
-                }
-                store_values<E, 8>(y, d + half, true, w);
-            } else if (v < turned) {
-                rotate_values<8>(u, u, d, cs + t * half, sn + t * half, c.rope);
-            }
-            store_values<E, 8>(y, d, true, u);
-        }
-        return;
-    }
     const int per_head = half + dim - c.rope.rotary;
-    for (int i = threadIdx.x; i < n * c.heads * per_head; i += kQThreads) {
+    for (int i = threadIdx.x; i < n * c.heads * per_head; i += kRopeThreads) {
         const int row = i / per_head, j = i - row * per_head, t = row / c.heads, h = row - t * c.heads;
         if (where[t] < 0) continue;
         const E* x = static_cast<const E*>(c.q.p) + static_cast<int64_t>(token0 + t) * c.q.token + h * c.q.head;
@@ -582,19 +554,18 @@ cudaError_t launch_append(const KvAppendCall& c, int sm_count, cudaStream_t stre
     const int half = c.rope.inv_freq != nullptr ? c.rope.rotary / 2 : 0;
     const int smem = c.cache.page * half * 2 * static_cast<int>(sizeof(float));
     const int items = c.batch.total / c.cache.page + 2 * c.batch.batch;
-    // a CTA takes the heads of a page one after another, as many as leave eight CTAs an SM: what comes
+    // a CTA takes the heads of a page one after another, as many as leave a number of CTAs an SM: what comes
     // before the first head (five dependent reads, and for keys cos and sin of the page) is paid once,
     // and the next head's values are on their way while one is written
-    auto heads_for = [&](int64_t ctas_a_round) {
+    auto heads_for = [&](int64_t ctas_a_round, int ctas_a_sm) {
         int heads = groups;
-        while (heads < c.cache.kv_heads && ctas_a_round * ((c.cache.kv_heads + 2 * heads - 1) / (2 * heads)) >= 8 * sm_count) heads *= 2;
+        while (heads < c.cache.kv_heads && ctas_a_round * ((c.cache.kv_heads + 2 * heads - 1) / (2 * heads)) >= ctas_a_sm * sm_count) heads *= 2;
         return heads;
     };
-    const int heads = heads_for(half > 0 ? items : 2 * items);
-    const PageArgs plain{c, wide, heads, 0};
-    const unsigned rounds = (c.cache.kv_heads + heads - 1) / heads;
+    auto rounds_of = [&](const PageArgs& p) { return static_cast<unsigned>((c.cache.kv_heads + p.heads_a_cta - 1) / p.heads_a_cta); };
     if (half == 0) {
-        append_pages_kernel<E, kFmt, kDim, false><<<dim3(items, rounds, 2), threads, 0, stream>>>(plain);
+        const PageArgs both{c, wide, heads_for(2 * items, 8), 0};
+        append_pages_kernel<E, kFmt, kDim, false><<<dim3(items, rounds_of(both), 2), threads, 0, stream>>>(both);
         return cudaGetLastError();
     }
     static int attr_gen[64] = {};
@@ -606,13 +577,19 @@ cudaError_t launch_append(const KvAppendCall& c, int sm_count, cudaStream_t stre
         if ((e = cudaFuncSetAttribute(turning, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * kDim * 4)) != cudaSuccess) return e;
         attr_gen[dev] = g_generation;
     }
-    turning<<<dim3(items, rounds), threads, smem, stream>>>(plain);
+    // turned keys: no more CTAs than the registers of one wave, each with cos and sin of its page once
+    const PageArgs of_keys{c, wide, heads_for(items, 512 / threads), 0}, of_values{c, wide, heads_for(items, 8), 1};
+    turning<<<dim3(items, rounds_of(of_keys)), threads, smem, stream>>>(of_keys);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    PageArgs of_values = plain;
-    of_values.values_only = 1;
-    append_pages_kernel<E, kFmt, kDim, false><<<dim3(items, rounds), threads, 0, stream>>>(of_values);
+    append_pages_kernel<E, kFmt, kDim, false><<<dim3(items, rounds_of(of_values)), threads, 0, stream>>>(of_values);
     if ((e = cudaGetLastError()) != cudaSuccess || c.heads == 0) return e;
-    append_q_kernel<E><<<(c.batch.total + kQTokens - 1) / kQTokens, kQThreads, kQTokens * half * 2 * sizeof(float), stream>>>(QArgs{c, wide});
+    if (rope_whole(c.q, c.q_out, kDim, c.rope)) {
+        const RopeRows r = rope_rows_of(c.q, c.q_out, c.batch.total, c.heads, kDim, c.rope, sm_count);
+        auto* kernel = c.rope.layout == kRopeHalf ? append_q_kernel<E, true> : append_q_kernel<E, false>;
+        kernel<<<rope_grid(r), kRopeThreads, rope_smem(r), stream>>>(c, r);
+    } else {
+        append_q_any_kernel<E><<<(c.batch.total + kQTokens - 1) / kQTokens, kRopeThreads, kQTokens * half * 2 * sizeof(float), stream>>>(c);
+    }
     return cudaGetLastError();
 }
 
