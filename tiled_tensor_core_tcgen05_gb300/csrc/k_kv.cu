@@ -129,7 +129,7 @@ constexpr int kVecs = 4;  // 16-byte pieces a thread holds
 // n / page + 2 pages, so some items have none), y heads, z keys or values (keys that are rotated are a
 // launch of their own).
 template <typename E, int kFmt, int kDim, bool kRope>
-__global__ void __launch_bounds__(512, kRope ? 1 : 2) append_pages_kernel(const PageArgs a) {
+__device__ __forceinline__ void append_pages(const PageArgs& a) {
     extern __shared__ float turns[];  // cos, then sin: (page, rotary / 2) each
     __shared__ float red[2][16];
     const KvAppendCall& c = a.c;
@@ -292,6 +292,34 @@ __global__ void __launch_bounds__(512, kRope ? 1 : 2) append_pages_kernel(const 
     }
 }
 
+// With rotation, keys, values and queries are three launches that neither read nor write one another's rows:
+// each lets the next one start beside it, and ends after the one before it, so that the last one's end is
+// the end of all.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void end_after_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename E, int kFmt, int kDim, bool kRope>
+__global__ void __launch_bounds__(512, kRope ? 1 : 2) append_pages_kernel(const PageArgs a) {
+    let_next_start();
+    append_pages<E, kFmt, kDim, kRope>(a);
+    end_after_last();
+}
+
+template <typename... Args>
+cudaError_t launch_beside(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---------------------------------------------------------------- single tokens: sequence by sequence
 
 constexpr int kTokenThreads = 512;
@@ -428,6 +456,7 @@ template <typename E, bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads, 4) append_q_kernel(const KvAppendCall c, const RopeRows r) {
     extern __shared__ float smem[];
     rope_rows<E, kHalf, true>(r, smem, [&](int32_t* where, int token0, int n) { q_positions(c, where, token0, n); });
+    end_after_last();
 }
 
 // Any alignment and rotary width: pair by pair.
@@ -462,6 +491,7 @@ __global__ void __launch_bounds__(kRopeThreads) append_q_any_kernel(const KvAppe
             y[half + j] = x[half + j];
         }
     }
+    end_after_last();
 }
 
 // ---------------------------------------------------------------- reading back
@@ -577,20 +607,20 @@ cudaError_t launch_append(const KvAppendCall& c, int sm_count, cudaStream_t stre
         if ((e = cudaFuncSetAttribute(turning, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * kDim * 4)) != cudaSuccess) return e;
         attr_gen[dev] = g_generation;
     }
-    // turned keys: no more CTAs than the registers of one wave, each with cos and sin of its page once
+    // Turned keys: as few CTAs as still fill one wave, two of 256 threads or the like an SM by their registers, since
+    // each pays for cos and sin of its page. 17 410 tokens, the whole call with four or eight CTAs an SM
+    // instead: 113 and 134 us with pages of 64, not 102.
     const PageArgs of_keys{c, wide, heads_for(items, 512 / threads), 0}, of_values{c, wide, heads_for(items, 8), 1};
     turning<<<dim3(items, rounds_of(of_keys)), threads, smem, stream>>>(of_keys);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    append_pages_kernel<E, kFmt, kDim, false><<<dim3(items, rounds_of(of_values)), threads, 0, stream>>>(of_values);
-    if ((e = cudaGetLastError()) != cudaSuccess || c.heads == 0) return e;
-    if (rope_whole(c.q, c.q_out, kDim, c.rope)) {
-        const RopeRows r = rope_rows_of(c.q, c.q_out, c.batch.total, c.heads, kDim, c.rope, sm_count);
-        auto* kernel = c.rope.layout == kRopeHalf ? append_q_kernel<E, true> : append_q_kernel<E, false>;
-        kernel<<<rope_grid(r), kRopeThreads, rope_smem(r), stream>>>(c, r);
-    } else {
-        append_q_any_kernel<E><<<(c.batch.total + kQTokens - 1) / kQTokens, kRopeThreads, kQTokens * half * 2 * sizeof(float), stream>>>(c);
-    }
-    return cudaGetLastError();
+    e = launch_beside(append_pages_kernel<E, kFmt, kDim, false>, dim3(items, rounds_of(of_values)), threads, 0, stream, of_values);
+    if (e != cudaSuccess || c.heads == 0) return e;
+    if (!rope_whole(c.q, c.q_out, kDim, c.rope))
+        return launch_beside(append_q_any_kernel<E>, (c.batch.total + kQTokens - 1) / kQTokens, kRopeThreads,
+                             kQTokens * half * 2 * static_cast<int>(sizeof(float)), stream, c);
+    const RopeRows r = rope_rows_of(c.q, c.q_out, c.batch.total, c.heads, kDim, c.rope, sm_count);
+    auto* kernel = c.rope.layout == kRopeHalf ? append_q_kernel<E, true> : append_q_kernel<E, false>;
+    return launch_beside(kernel, rope_grid(r), kRopeThreads, rope_smem(r), stream, c, r);
 }
 
 template <typename E, int kFmt, int kDim>
