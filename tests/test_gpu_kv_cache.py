@@ -392,3 +392,49 @@ def test_other_stream_and_graph(tg):
     y = tg.rope(static, places, f, stream=side2)
     side2.synchronize()
     assert torch.equal(y, r)
+
+
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("graph", [False, True])
+def test_rotated_prompts_are_whole_before_what_follows(tg, graph, off):
+    """A rotated append of prompts is several launches side by side: whatever comes behind it on the stream, reading
+    or overwriting, meets all of them ended. Every round's results are those of a round with a wait after each call."""
+    counts, lens, page, heads, dim = [900, 37, 0, 1400], [10, 64, 5, 0], 64, 4, 128
+    T, f = sum(counts), ref.freqs(128).cuda()
+    total = [a + b for a, b in zip(counts, lens)]
+    pages = sum(-(-t // page) for t in total) + 2
+    cache, _ = _cache(tg, pages, heads, page, dim, torch.int8)
+    start = [x.clone() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    table, first, cu = _table(total, page, pages, 3).cuda(), _ints(lens), _ints([0, 900, 937, 937, 2337])
+    none, every = _ints([0] * 4), _ints([0] + torch.tensor(total).cumsum(0).tolist())
+    rounds = 12
+    x = torch.randn(rounds, T, 4 * heads + 1, dim, generator=torch.Generator().manual_seed(4)).half().cuda()
+
+    def round_of(i, wait):
+        for a, b in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), start):
+            a.copy_(b)
+        rows = x[i].clone()
+        flat = rows.view(T, -1)
+        q = torch.as_strided(rows, (T, 2 * heads, dim), (flat.shape[1], dim, 1), 2 * heads * dim + off)
+        k, v = rows[:, :heads], rows[:, heads:2 * heads]
+        wait()
+        out = tg.kv_append(cache, k, v, table, first, cu, max_new=max(counts), Q=q, inv_freq=f)
+        wait()
+        rows.zero_()  # overwrites what the call reads
+        got = (out.clone(), *tg.kv_read(cache, table, none, every, sum(total)))
+        wait()
+        return got
+
+    want = [round_of(i, torch.cuda.synchronize) for i in range(rounds)]
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = [round_of(i, lambda: None) for i in range(rounds)]
+        g.replay()
+    else:
+        got = [round_of(i, lambda: None) for i in range(rounds)]
+    torch.cuda.synchronize()
+    for i in range(rounds):
+        for a, b in zip(got[i], want[i]):
+            assert torch.equal(a, b), i
+    _status_ok(tg)

@@ -36,6 +36,11 @@
 // 8 x 8 transposition. The 128-byte swizzle and the order in which a step's
 // tokens are given to MMA rows (mma_token) keep those reads free of bank
 // conflicts.
+//
+// Measured (one GB300): 64 ragged sequences of up to 8192, 32 heads over 8 of 128, 630 MB of cache, 109 us,
+// 5.8 TB/s or 0.85 of the copy rate; four sequences of up to 131071, 105 us, 0.83. What is missing is the
+// start (lengths, shares, first pages: three dependent reads) and the join. One token over 1023: 8.5 us,
+// all of it latency of the two kernels.
 #include "tg_device.cuh"
 #include "tg_kv_split.cuh"
 

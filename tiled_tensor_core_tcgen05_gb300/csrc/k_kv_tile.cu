@@ -22,6 +22,10 @@
 // only then the next scores. The second half's scores of a tile are issued when the first
 // half's weights begin to arrive, so that one half's MMAs lie beside the other's
 // exponentials.
+//
+// Measured (one GB300): chunks of up to 4096 new tokens on 8192, 32 heads over 8 of 128, causal: 656 us, 775 TFLOP/s or
+// 0.42 of the dense rate. MMAs of M = 128, N = 128 and fp16 operands take 104 (scores) and 93 (product) cycles where
+// the dense rate has 64, and about 600 cycles of a half's chain are hand-overs that the other half does not fill.
 #include "tg_device.cuh"
 #include "tg_kv_split.cuh"
 
