@@ -165,10 +165,13 @@ __device__ __forceinline__ void append_pages(const PageArgs& a) {
     float *cs = turns, *sn = turns + page * half;
     const int group = page * kPieces / kVecs, groups = blockDim.x / group;
     const int g = threadIdx.x / group, t = threadIdx.x - g * group;
+    // a group is page / kVecs whole rows: a thread's pieces are at one place of a row, `rows` rows apart
+    const int place0 = t / kPieces, d = (t - place0 * kPieces) * 8, rows = page / kVecs;
     const Strided& src = values ? c.v : c.k;
     const bool vec = values ? a.wide.v : a.wide.k;
     const int head_end = min(c.cache.kv_heads, static_cast<int>(blockIdx.y + 1) * a.heads_a_cta);
-    const E* x0 = static_cast<const E*>(src.p) + row0 * src.token;
+    const E* x0 = static_cast<const E*>(src.p) + (row0 + place0) * src.token;
+    const int64_t apart = rows * src.token;
     uint8_t* all_codes = values ? c.cache.v : c.cache.k;
     float* all_scales = values ? c.cache.v_scale : c.cache.k_scale;
     // one head's pieces (and, rotated, their partners) and old scale, fetched while the head before is worked on
@@ -180,9 +183,9 @@ __device__ __forceinline__ void append_pages(const PageArgs& a) {
         auto pieces = [&](bool wide) {
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const int at = t + i * group, place = at / kPieces, d = (at - place * kPieces) * 8;
+                const int place = place0 + i * rows;
                 if (place >= from && place < to) {
-                    const E* row = x0 + place * src.token + head * src.head;
+                    const E* row = x0 + i * apart + head * src.head;
                     own[i] = load_piece(row + d, wide);
                     if constexpr (kRope) other[i] = load_partner_piece(row, d, wide, rope);
                 }
@@ -212,13 +215,13 @@ __device__ __forceinline__ void append_pages(const PageArgs& a) {
         float most = 0.0f;  // NaN or infinite where a value is
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            const int at = t + i * group, place = at / kPieces;
+            const int place = place0 + i * rows;
             if (real && place >= from && place < to) {
                 if constexpr (kRope) {
                     float v[8], o[8];
                     piece_values<E>(own[i], v);
                     piece_values<E>(other[i], o);
-                    rotate_values<8>(v, o, (at - place * kPieces) * 8, cs + place * half, sn + place * half, rope);
+                    rotate_values<8>(v, o, d, cs + place * half, sn + place * half, rope);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         x[i][e] = v[e];
@@ -237,7 +240,7 @@ __device__ __forceinline__ void append_pages(const PageArgs& a) {
             most = 0.0f;
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const int place = (t + i * group) / kPieces;
+                const int place = place0 + i * rows;
                 if (real && place >= from && place < to) {
                     float v[8];
                     if constexpr (kRope) {
@@ -262,14 +265,14 @@ __device__ __forceinline__ void append_pages(const PageArgs& a) {
         }
         if (real) {
             const int64_t ph = static_cast<int64_t>(p) * c.cache.kv_heads + head;
-            uint8_t* codes = all_codes + ph * page * kDim;
+            uint8_t* codes = all_codes + ph * page * kDim + t * 8;
             const float s = fmaxf(s_held, fmaxf(__fmul_rn(most, code_max_inverse<kFmt>()), kScaleFloor));
             const float per = __fdiv_rn(1.0f, s);
             const float ratio = __fmul_rn(s_held, per);
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const int at = t + i * group, place = at / kPieces;
-                uint2* q = reinterpret_cast<uint2*>(codes + at * 8);
+                const int place = place0 + i * rows;
+                uint2* q = reinterpret_cast<uint2*>(codes + i * group * 8);
                 if (place >= from && place < to) {
                     uint32_t w[2];
                     float v[8];
