@@ -140,10 +140,10 @@ __device__ __forceinline__ void append_pages(const PageArgs& a) {
     __shared__ float red[2][16];
     const KvAppendCall& c = a.c;
     const KvBatch& b = c.batch;
-    const int page = c.cache.page, item = blockIdx.x;
+    const int page = c.cache.page, shift = 31 - __clz(page), item = blockIdx.x;  // a power of two
     const bool values = kRope ? false : a.values_only || blockIdx.z != 0;
     constexpr int kPieces = kDim / 8;  // of a row
-    auto base_of = [&](int i) { return static_cast<int64_t>((b.cu ? __ldg(b.cu + i) : i) / page) + 2 * i; };
+    auto base_of = [&](int i) { return static_cast<int64_t>((b.cu ? __ldg(b.cu + i) : i) >> shift) + 2 * i; };
     const int seq = block_find(b.batch, base_of, item);
     const SeqSpan span = seq_span(b, seq, c.wd);
     if (span.count == 0) return;
@@ -153,11 +153,11 @@ __device__ __forceinline__ void append_pages(const PageArgs& a) {
         report_range(c.wd);
         return;
     }
-    const int64_t slot = len / page + k;
+    const int64_t slot = (len >> shift) + k;
     if (k < 0 || slot * page >= len + span.count) return;
     const int p = seq_page(b, c.cache, seq, static_cast<int>(slot), c.wd);
     if (p < 0) return;
-    const int from = k == 0 ? static_cast<int>(len % page) : 0;                     // first new place in the page
+    const int from = k == 0 ? static_cast<int>(len & (page - 1)) : 0;                     // first new place in the page
     const int to = static_cast<int>(min(static_cast<int64_t>(page), len + span.count - slot * page));
     const int64_t row0 = span.first + (slot * page - len);                          // packed row of place 0
     const RopeArgs& rope = c.rope;
@@ -196,11 +196,13 @@ __device__ __forceinline__ void append_pages(const PageArgs& a) {
     };
     fetch(blockIdx.y * a.heads_a_cta + g);
     if constexpr (kRope) {
-        for (int i = threadIdx.x; i < (to - from) * half; i += blockDim.x) {
-            const int t = i / half, j = i - t * half;
-            const float2 x = turn_cos_sin(turn_step(__ldg(rope.inv_freq + j)), static_cast<int>(slot * page) + from + t, rope.amplitude, rope.sign);
-            cs[(from + t) * half + j] = x.x;
-            sn[(from + t) * half + j] = x.y;
+        // a thread keeps to one pair, whose step is settled once; a block has twice a row's pairs or more
+        const int j = threadIdx.x % half, many = blockDim.x / half;
+        const auto step = turn_step(__ldg(rope.inv_freq + j));
+        for (int i = from + threadIdx.x / half; i < to && threadIdx.x < many * half; i += many) {
+            const float2 x = turn_cos_sin(step, static_cast<int>(slot << shift) + i, rope.amplitude, rope.sign);
+            cs[i * half + j] = x.x;
+            sn[i * half + j] = x.y;
         }
         __syncthreads();
     }
