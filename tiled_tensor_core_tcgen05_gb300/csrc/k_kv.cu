@@ -19,9 +19,10 @@
 // writes all heads of one token (and rotates its queries), a head a warp, and
 // only where a scale grows are the page's held codes touched at all.
 //
-// Measured: 17 410 tokens of 7 prompts, 8 heads of 128, to int8 in pages of 32: 27 us
-// where its bytes take 15.7: the conversions are 70 % of the issue slots. With
-// rotation, and 32 heads of queries, e4m3, pages of 64: 95 us where the bytes take 58.
+// Measured: 17 410 tokens of 7 prompts, 8 heads of 128, to int8 in pages of 32: 23.5 us
+// where its bytes take 15.7: conversion, rounding and addresses fill the issue slots.
+// With rotation, and 32 heads of queries, e4m3, pages of 64: 87 us where the bytes take
+// 58: keys 30, values 17 and queries 44 by themselves.
 // One token each of 256 sequences, rotated: 7.5 us, five dependent reads. Reading
 // back 890 MB: 134 us, 6.6 TB/s or 0.98 of the copy rate.
 #include "tg_rope.cuh"
@@ -620,7 +621,7 @@ cudaError_t launch_append(const KvAppendCall& c, int sm_count, cudaStream_t stre
     }
     // Turned keys: as few CTAs as still fill one wave, two of 256 threads or the like an SM by their registers, since
     // each pays for cos and sin of its page. 17 410 tokens, the whole call with four or eight CTAs an SM
-    // instead: 113 and 134 us with pages of 64, not 102.
+    // instead: 113 and 134 us with pages of 64, not 102 (before later steps took all of them down).
     const PageArgs of_keys{c, wide, heads_for(items, 512 / threads), 0}, of_values{c, wide, heads_for(items, 8), 1};
     turning<<<dim3(items, rounds_of(of_keys)), threads, smem, stream>>>(of_keys);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
