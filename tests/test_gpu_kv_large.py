@@ -1,0 +1,69 @@
+"""GPU checks of the cache operators at sizes where a CTA makes many rounds: the same bits from launch to launch."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tg():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import tiled_tensor_core_tcgen05_gb300 as m
+    torch.cuda.set_device(0)
+    return m
+
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _status_ok(tg):
+    st, where = tg.tg_device_status(None)
+    assert st == tg.OK, f"device status {st} at {where}"
+
+
+def _made_on_the_gpu(tg, counts, lens, page, kv, share, dim, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    need = [-(-n // page) for n in lens]
+    order = torch.randperm(sum(need), generator=g, device="cuda").int()
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for i, m in enumerate(need):
+        table[i, :m] = order[at:at + m]
+        at += m
+    k, v = (torch.randint(-100, 101, (at, kv, page, dim), generator=g, dtype=torch.int8, device="cuda") for _ in range(2))
+    if dtype is not torch.int8:
+        k, v = ((x.half() * 4).to(dtype) for x in (k, v))
+    ks, vs = (torch.rand(at, kv, generator=g, device="cuda").add(0.5) / (70 if dtype is torch.int8 else 280) for _ in range(2))
+    q = torch.randn(sum(counts), kv * share, dim, generator=g, device="cuda").half()
+    return tg.KvCache(k, v, ks, vs), table, q
+
+
+@pytest.mark.parametrize("batch,most,longest,page,share,dim,dtype", [
+    (64, 1, 8000, 64, 4, 128, torch.float8_e4m3fn),   # a decode step: every ring slot filled some twenty times
+    (33, 5, 6000, 16, 7, 64, torch.int8),             # drafts
+    (2, 2048, 6000, 64, 4, 128, torch.float8_e4m3fn),  # prompt chunks
+    (3, 600, 3000, 16, 3, 64, torch.int8),
+])
+def test_forty_launches_agree_bit_for_bit(tg, batch, most, longest, page, share, dim, dtype):
+    """A slot of codes is refilled by the copy engine after ordinary reads; a copy that overtook them would show as
+    other results from launch to launch."""
+    r = torch.Generator().manual_seed(batch)
+    lens = [longest - int(torch.randint(0, longest // 2, (), generator=r)) for _ in range(batch)]
+    counts = [most - int(torch.randint(0, most // 2 + 1, (), generator=r)) for _ in range(batch)]
+    counts[0] = most
+    cache, table, q = _made_on_the_gpu(tg, counts, lens, page, 8, share, dim, dtype, seed=batch)
+    cu = _ints([0] + torch.tensor(counts).cumsum(0).tolist())
+
+    def once():
+        return tg.attention_kv(q, cache, table, _ints(lens), cu, max_new=most, max_len=longest, return_lse=True)
+
+    out, lse = once()
+    assert out.isfinite().all() and lse.isfinite().all()
+    for i in range(39):
+        again, lagain = once()
+        assert torch.equal(out, again) and torch.equal(lse, lagain), f"launch {i + 2} differs"
+    _status_ok(tg)

@@ -496,7 +496,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     for (int n = 0; n < kTiles; ++n) mma16816(o[n][2 * j + 1], a0, a1, a2, a3, wt[n][0], wt[n][1]);
                 }
             }
-            __syncwarp();  // every lane has read the stage: it may be filled again
+            // every lane has read the stage: it may be filled again. The copy that fills it writes through another
+            // proxy than these reads, and without the fence could land before them
+            fence_proxy_async_smem();
+            __syncwarp();
             if (s + kStages < n_steps) {
                 const int ahead = (s + kStages) & 31;
                 const int p_ahead = __shfl_sync(0xFFFFFFFFu, ahead < in ? pg_next : pg, ahead);

@@ -507,6 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint4 x[kRounds];
 #pragma unroll
                 for (int i = 0; i < kRounds; ++i) x[i] = lds_v4(raw + i * kGroupStep * 8 * kDim);
+                // the next copy into this slot writes through another proxy than these reads: without the fence it
+                // could land before them
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(raw_empty + 8 * slot);
                 if (state == 0) {  // tokens past the end, or without a page, are zeros
