@@ -67,3 +67,38 @@ def test_forty_launches_agree_bit_for_bit(tg, batch, most, longest, page, share,
         again, lagain = once()
         assert torch.equal(out, again) and torch.equal(lse, lagain), f"launch {i + 2} differs"
     _status_ok(tg)
+
+
+# ---------------------------------------------------------------- waits that run out
+
+def _times_out_and_recovers(tg, counts, lens, share, dim, max_len):
+    """A call with one arrival a CTA withheld ends with a timeout; the next call is what it was before."""
+    cache, table, q = _made_on_the_gpu(tg, counts, lens, 16, 2, share, dim, torch.int8, seed=5)
+    cu = _ints([0] + torch.tensor(counts).cumsum(0).tolist())
+    args = (q, cache, table, _ints(lens), cu)
+    want = tg.attention_kv(*args, max_new=max(counts), max_len=max_len)
+    _status_ok(tg)
+    tg.tg_set_watchdog_ns(20_000_000)  # 20 ms
+    tg.tg_debug_skip_first_arrive(True)
+    try:
+        tg.attention_kv(*args, max_new=max(counts), max_len=max_len)
+        st, where = tg.tg_device_status(None)
+    finally:
+        tg.tg_debug_skip_first_arrive(False)
+        tg.tg_set_watchdog_ns(0)
+    assert st == tg.ERR_TIMEOUT
+    _status_ok(tg)
+    assert torch.equal(tg.attention_kv(*args, max_new=max(counts), max_len=max_len), want)
+    _status_ok(tg)
+    return where
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("counts,lens,share", [
+    ([100], [100], 1),                 # one tile a unit
+    ([300, 90, 200], [300, 4000, 2111], 4),  # units in parts, several segments a CTA
+    ([65] * 40, [700] * 40, 2),        # whole units, one after another
+])
+def test_withheld_arrivals_of_prompt_chunks_time_out(tg, counts, lens, share, dim):
+    where = _times_out_and_recovers(tg, counts, lens, share, dim, max(lens))
+    assert where in (1, 2, 3, 4, 6, 7), where  # whichever of the CTAs' waits gave up first

@@ -55,6 +55,10 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;            // + 128 half; the weights of keys 64 g .. are the first 32 of their 64 columns
 constexpr uint32_t kColO = 256;          // + 128 half
 
+// What a CTA holds back while the watchdog's test hook is on, one CTA after another: its first piece of codes, or word
+// of its first tile's products.
+constexpr int kNoCodes = 1, kNoProduct = 2;
+
 // What the softmax and the converters know of a tile: per block of 16 keys the key scale, log2 and
 // inverse of the value scale, and how many tokens are there.
 struct TileInfo {
@@ -310,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const WaitCtx wc{abort_flag, c.wd.status, c.wd.limit_ns};
+    const int withheld = c.wd.skip_first_arrive ? 1 + static_cast<int>(blockIdx.x & 1) : 0;
     // the next segment for this warp; false when there is none, or a wait gave up
     uint32_t seg_no = 0;
     auto next_segment = [&](Segment& s) {
@@ -388,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         product(3, st, true);
                         product(6, st, true);
                         product(7, st, true);
-                        mma_commit(o_done + 8 * h);
+                        if (withheld != kNoProduct || g != 0) mma_commit(o_done + 8 * h);
                         mma_commit(v_empty + 8 * st);
                     }
                     tile_no += n;
@@ -452,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool mine = lane < kBlocks && (lane >> 2) == (part & 1) && cur >= 0;
                     const uint32_t many = __popc(__ballot_sync(0xFFFFFFFFu, mine));
                     const uint32_t bar_at = raw_full + 8 * slot;
+                    if (withheld == kNoCodes && piece == 0) continue;
                     if (lane == 0) {
                         if (many > 0) mbar_arrive_expect_tx(bar_at, many * kStep * kDim);
                         else mbar_arrive(bar_at);
@@ -471,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // let every copy in flight land before the CTA ends
-            for (uint32_t i = piece > kRawSlots ? piece - kRawSlots : 0; lane == 0 && i < piece; ++i)
+            for (uint32_t i = piece > kRawSlots ? piece - kRawSlots : withheld == kNoCodes; lane == 0 && i < piece; ++i)
                 wait_phase_drain(raw_full + 8 * (i % kRawSlots), (i / kRawSlots) & 1u, wc);
             __syncwarp();
         }
@@ -551,7 +557,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t col_s = lanes + kColS + 128 * h + 64 * kh, col_o = lanes + kColO + 128 * h + kh * (kDim / 2);
         const int pair = h * 4 + (warp & 3);                          // the two warps of the same 32 rows
         float* red = reinterpret_cast<float*>(smem + L::kRed) + (h * 2) * kHalfRows + row;  // + parity 4 * 128, + key half 128
-        bool ok = true;
         bool first_segment = true;
         while (true) {
             // all of the half go on, or none: no warp waits at a barrier for one that has left
@@ -604,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c.window > 0 && p - c.window + 1 > 0) from = static_cast<int>(p - c.window + 1);
             }
             float m = kNoMax, l = 0.0f;
+            bool ok = true;
             const int n = sg.t1 - sg.t0;
             for (int j = 0; j < n; ++j) {
                 const uint32_t g = tile_no + j, ph = g & 1u;
@@ -704,15 +710,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 l = l * keep + sum;
             }
-            if (!ok) break;
+            // Every warp of the half comes to this barrier once a segment, whatever became of its waits, and all leave
+            // together: the others may have taken their last tile before this one saw the abort flag, and the
+            // barrier has no limit of its own.
             tile_no += n;
-            ok = wait_suspended(o_done + 8 * h, (tile_no - 1) & 1u, wc, kSiteEpilogueAccFull);
+            if (ok) ok = wait_suspended(o_done + 8 * h, (tile_no - 1) & 1u, wc, kSiteEpilogueAccFull);
             // both key halves' sums; the maxima of the last tile were in the other parity
             red[(tile_no & 1u) * 4 * kHalfRows + kh * kHalfRows] = l;
-            if (named_barrier_or(1 + h, 256, !ok)) {
-                ok = false;
-                break;
-            }
+            if (named_barrier_or(1 + h, 256, !ok)) break;
             l += red[(tile_no & 1u) * 4 * kHalfRows + (kh ^ 1) * kHalfRows];
             tc_fence_after_sync();
             const bool whole = sg.t0 == 0 && sg.t1 == sg.tiles;
