@@ -500,8 +500,8 @@ tg_status tg_set_watchdog_ns(uint64_t ns);
  * CTA (every CTA pair for the pair kernel), so the consumers' bounded waits
  * expire and the call ends with TG_ERR_TIMEOUT from tg_device_status. The
  * cache attention for many rows (more than 64 a kv head) withholds one arrival
- * a CTA, of its codes or of a finished product. Off by default; has no effect
- * on other kernels.
+ * a CTA, of its codes, of a finished product or of its first piece of work. Off
+ * by default; has no effect on other kernels.
  */
 tg_status tg_debug_skip_first_arrive(int on);
 

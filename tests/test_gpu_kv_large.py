@@ -72,16 +72,24 @@ def test_forty_launches_agree_bit_for_bit(tg, batch, most, longest, page, share,
 # ---------------------------------------------------------------- waits that run out
 
 def _times_out_and_recovers(tg, counts, lens, share, dim, max_len):
-    """A call with one arrival a CTA withheld ends with a timeout; the next call is what it was before."""
+    """A call with one arrival a CTA withheld ends with a timeout; the next call is what it was before. The
+    workspace holds all ones, so that an entry which no kernel wrote would read as sizes far out of range."""
     cache, table, q = _made_on_the_gpu(tg, counts, lens, 16, 2, share, dim, torch.int8, seed=5)
     cu = _ints([0] + torch.tensor(counts).cumsum(0).tolist())
     args = (q, cache, table, _ints(lens), cu)
     want = tg.attention_kv(*args, max_new=max(counts), max_len=max_len)
     _status_ok(tg)
+    T, H = q.shape[:2]
+    need = tg.tg_attention_kv_workspace(cache.kv_heads, cache.page, dim, cache.fmt, H, len(lens), T, max(counts), max_len, 0, tg.FP16)
+    work = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    out, lens_d = torch.empty_like(want), args[3]
+    sizes = (cache.pages, cache.kv_heads, cache.page, dim, cache.fmt)
     tg.tg_set_watchdog_ns(20_000_000)  # 20 ms
     tg.tg_debug_skip_first_arrive(True)
     try:
-        tg.attention_kv(*args, max_new=max(counts), max_len=max_len)
+        tg.tg_attention_kv(q.data_ptr(), *q.stride()[:2], out.data_ptr(), None, cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+                           cache.v_scale.data_ptr(), *sizes, table.data_ptr(), table.shape[1], lens_d.data_ptr(), cu.data_ptr(), len(lens), T, H,
+                           max(counts), max_len, 1, 0, dim ** -0.5, tg.FP16, work.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
         st, where = tg.tg_device_status(None)
     finally:
         tg.tg_debug_skip_first_arrive(False)

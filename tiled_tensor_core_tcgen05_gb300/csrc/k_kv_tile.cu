@@ -55,9 +55,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;            // + 128 half; the weights of keys 64 g .. are the first 32 of their 64 columns
 constexpr uint32_t kColO = 256;          // + 128 half
 
-// What a CTA holds back while the watchdog's test hook is on, one CTA after another: its first piece of codes, or word
-// of its first tile's products.
-constexpr int kNoCodes = 1, kNoProduct = 2;
+// What a CTA holds back while the watchdog's test hook is on, one CTA after another: its first piece of codes, word
+// of its first tile's products, or its first segment.
+constexpr int kNoCodes = 1, kNoProduct = 2, kNoSegment = 3;
 
 // What the softmax and the converters know of a tile: per block of 16 keys the key scale, log2 and
 // inverse of the value scale, and how many tokens are there.
@@ -286,10 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const Shares shares(total, a.grid, a.least);
     const int k = blockIdx.x;
-    if (k >= shares.ctas) {
-        if (threadIdx.x == 0) a.meta[k].chunks = 0;
-        return;
-    }
+    // the joining kernel runs whatever becomes of this one: until the first segment is known there is nothing to join
+    if (threadIdx.x == 0) a.meta[k].chunks = 0;
+    if (k >= shares.ctas) return;
     const int64_t start = shares.start(k), stop = shares.start(k + 1);
     int64_t carry = 0;
     for (int base = 0; base < batch; base += kThreads) {
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const WaitCtx wc{abort_flag, c.wd.status, c.wd.limit_ns};
-    const int withheld = c.wd.skip_first_arrive ? 1 + static_cast<int>(blockIdx.x & 1) : 0;
+    const int withheld = c.wd.skip_first_arrive ? 1 + static_cast<int>(blockIdx.x % 3) : 0;
     // the next segment for this warp; false when there is none, or a wait gave up
     uint32_t seg_no = 0;
     auto next_segment = [&](Segment& s) {
@@ -341,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     more = walk.next(sg);
                     if (!more) sg.t0 = sg.t1 = 0;
                     *reinterpret_cast<Segment*>(smem + L::kSegments + slot * 64) = sg;
-                    mbar_arrive(seg_full + 8 * slot);
+                    if (withheld != kNoSegment || seg_no != 0) mbar_arrive(seg_full + 8 * slot);
                 }
             }
             __syncwarp();
