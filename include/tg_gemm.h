@@ -498,10 +498,10 @@ tg_status tg_set_watchdog_ns(uint64_t ns);
  * tiled kernels (TG_KERNEL_TILED_TMA, TG_KERNEL_TILED_PAIR) and of the 4-bit
  * register kernel (TG_W4_KERNEL_REG) skip the first pipeline stage of every
  * CTA (every CTA pair for the pair kernel), so the consumers' bounded waits
- * expire and the call ends with TG_ERR_TIMEOUT from tg_device_status. The
- * cache attention for many rows (more than 64 a kv head) withholds one arrival
- * a CTA, of its codes, of a finished product or of its first piece of work. Off
- * by default; has no effect on other kernels.
+ * expire and the call ends with TG_ERR_TIMEOUT from tg_device_status. So does
+ * the cache attention for few rows; that for many rows (more than 64 a kv head)
+ * withholds one arrival a CTA, of its codes, of a finished product or of its
+ * first piece of work. Off by default; has no effect on other kernels.
  */
 tg_status tg_debug_skip_first_arrive(int on);
 

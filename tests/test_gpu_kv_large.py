@@ -110,3 +110,13 @@ def _times_out_and_recovers(tg, counts, lens, share, dim, max_len):
 def test_withheld_arrivals_of_prompt_chunks_time_out(tg, counts, lens, share, dim):
     where = _times_out_and_recovers(tg, counts, lens, share, dim, max(lens))
     assert where in (1, 2, 3, 4, 6, 7), where  # whichever of the CTAs' waits gave up first
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("counts,lens,share", [
+    ([1], [40], 4),                  # one step
+    ([1, 5, 3], [300, 9000, 2111], 4),  # units in parts
+    ([1] * 300, [200] * 300, 8),     # whole units, one after another
+])
+def test_withheld_arrivals_of_few_rows_time_out(tg, counts, lens, share, dim):
+    assert _times_out_and_recovers(tg, counts, lens, share, dim, max(lens)) == 6  # the wait for a step's codes

@@ -271,8 +271,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             lv = lg2_approx(vs);
             iv = rcp_approx(vs);
         };
+        // the watchdog's test hook: the first step of a CTA never arrives
+        auto withheld = [&](int s) { return c.wd.skip_first_arrive != 0 && warp == 0 && step_no + s == 0; };
         auto issue = [&](int s, int p, int slot) {  // lane 0: the copies of step s into stage slot
             const uint32_t bar = bar0 + 8 * slot;
+            if (withheld(s)) return;
             if (p >= 0) {
                 const int64_t place = (static_cast<int64_t>(p) * c.cache.kv_heads + head) * c.cache.page +
                                       ((tok0 + (i0 + s) * kChunk) & (c.cache.page - 1));
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         if (!ok) {  // let every copy in flight land, then stop with the others
             for (const int issued = min(n_steps, s + kStages); s < issued; ++s)
-                wait_phase_drain(bar0 + 8 * ((step_no + s) % kStages), static_cast<uint32_t>((step_no + s) / kStages) & 1u, wc);
+                if (!withheld(s)) wait_phase_drain(bar0 + 8 * ((step_no + s) % kStages), static_cast<uint32_t>((step_no + s) / kStages) & 1u, wc);
         }
         step_no += n_steps;
 
