@@ -1,6 +1,10 @@
-"""GPU checks of the cache operators at sizes where a CTA makes many rounds: the same bits from launch to launch."""
+"""GPU checks of the cache operators at sizes where a CTA makes many rounds: against the definitions in float64 of the
+small tests, the same bits from launch to launch, and waits that run out."""
 import pytest
 import torch
+
+from tests import test_gpu_attention_kv as attend
+from tests import test_gpu_kv_cache as cache_tests
 
 pytestmark = pytest.mark.gpu
 
@@ -66,6 +70,48 @@ def test_forty_launches_agree_bit_for_bit(tg, batch, most, longest, page, share,
     for i in range(39):
         again, lagain = once()
         assert torch.equal(out, again) and torch.equal(lse, lagain), f"launch {i + 2} differs"
+    _status_ok(tg)
+
+
+# ---------------------------------------------------------------- many rounds of a CTA
+
+@pytest.mark.parametrize("counts,lens,page,heads,dim,ct,dt", [
+    ([9000, 1, 6000, 5003], [5, 63, 0, 130], 64, 8, 64, 0, 0),   # a CTA takes four heads of a page one after another
+    ([7001, 5000], [17, 16], 16, 8, 64, 1, 1),                   # eight, four at a time
+    ([300, 8200], [77, 0], 32, 16, 128, 1, 0),
+])
+@pytest.mark.parametrize("rotate", [False, True])
+def test_append_of_many_heads_a_cta(tg, counts, lens, page, heads, dim, ct, dt, rotate):
+    cache_tests.test_append(tg, counts, lens, page, heads, dim, ct, dt, True, rotate)
+
+
+@pytest.mark.parametrize("counts,lens,page,kv,share,dim,ct,dt", [
+    ([1, 1, 1], [200000, 170001, 199999], 128, 4, 4, 64, 1, 0),  # over 64 steps a warp and unit: pages and scales are fetched three times
+    ([3, 2, 3], [200000, 199990, 190007], 16, 2, 4, 64, 0, 1),   # over 32, blocks of 16 rows
+    ([1] * 12, [60000] * 11 + [59000], 64, 2, 2, 128, 0, 0),
+])
+def test_attention_over_many_steps(tg, counts, lens, page, kv, share, dim, ct, dt):
+    cache, host, table, q = attend._case(tg, counts, lens, page, kv, share, dim, ct, dt, seed=31)
+    cu = [0] + torch.tensor(counts).cumsum(0).tolist()
+    out, lse = tg.attention_kv(q.cuda(), cache, table.cuda(), _ints(lens), _ints(cu), max_new=max(counts), max_len=max(lens), return_lse=True)
+    attend._check(out, lse, host, table, q, counts, lens, page, True, 0, dim ** -0.5)
+    _status_ok(tg)
+
+
+def test_prompt_chunks_of_more_sequences_than_threads(tg):
+    """Most of 900 sequences have one new token, some 70, a few are idle: the chunk kernel's list takes two passes."""
+    g = torch.Generator().manual_seed(32)
+    lens = [int(n) for n in torch.randint(1, 200, (900,), generator=g)]
+    counts = [1] * 900
+    for i in (0, 500, 767, 768, 899):
+        counts[i], lens[i] = 70, 100 + i % 60
+    for i in (3, 770, 771):
+        lens[i] = 0
+    counts[770] = 0
+    cache, host, table, q = attend._case(tg, counts, lens, 16, 2, 1, 64, 0, 0, seed=33)
+    cu = [0] + torch.tensor(counts).cumsum(0).tolist()
+    out, lse = tg.attention_kv(q.cuda(), cache, table.cuda(), _ints(lens), _ints(cu), max_new=70, max_len=200, return_lse=True)
+    attend._check(out, lse, host, table, q, counts, lens, 16, True, 0, 0.125)
     _status_ok(tg)
 
 
