@@ -456,9 +456,11 @@ tg_status tg_kv_read(const void* k_cache, const void* v_cache, const float* k_sc
  * sequence's length has no effect; a NaN value inside it makes NaN of the rows
  * that see it, and may of the sequence's other rows in the same call.
  *
- * Scores, softmax and sums are fp32, codes enter the products exactly, O
- * (total x heads x dim, contiguous, 16-byte aligned) is rounded once. Results
- * are bit-identical from run to run. The caller gives `workspace` (16-byte
+ * Scores, maxima, exponentials and sums are fp32, and codes enter the products
+ * exactly. For the product with the values a key's weight (with its page's
+ * value scale) is rounded to 16 bits: by 2^-11 of itself, or by 2^-34 of the
+ * row's largest. O (total x heads x dim, contiguous, 16-byte aligned) is rounded
+ * once. Results are bit-identical from run to run. The caller gives `workspace` (16-byte
  * aligned) of at least the bytes that tg_attention_kv_workspace answers for
  * the same sizes; its contents need not be kept between calls. Stream-ordered;
  * allocates nothing, so it can be captured into a graph.

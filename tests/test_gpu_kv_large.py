@@ -3,6 +3,7 @@ small tests, the same bits from launch to launch, and waits that run out."""
 import pytest
 import torch
 
+from tests import kv_reference as ref
 from tests import test_gpu_attention_kv as attend
 from tests import test_gpu_kv_cache as cache_tests
 
@@ -113,6 +114,48 @@ def test_prompt_chunks_of_more_sequences_than_threads(tg):
     out, lse = tg.attention_kv(q.cuda(), cache, table.cuda(), _ints(lens), _ints(cu), max_new=70, max_len=200, return_lse=True)
     attend._check(out, lse, host, table, q, counts, lens, 16, True, 0, 0.125)
     _status_ok(tg)
+
+
+# ---------------------------------------------------------------- many small weights under a few large ones
+
+@pytest.mark.parametrize("batch,most,ct", [(2000, 1, 1), (700, 3, 0), (200, 70, 1), (60, 260, 0)])
+def test_small_weights_under_large_ones_count(tg, batch, most, ct):
+    """Four keys of zero value (one for each warp of the kernel for few rows) take all but about 2^-14.6 of a row's
+    weight, so each of the 8188 others, whose values are all positive and make up the whole output, has some 2^-25.6
+    of the largest weight. All sequences have the same pages, so that a CTA walks a sequence whole.
+
+    A weight is rounded to 16 bits: by 2^-11 of itself, or by 2^-34 of the row's largest."""
+    L, dim, page, dtype = 8192, 64, 64, attend.CODES[ct]
+    g = torch.Generator().manual_seed(most)
+    sign = torch.randint(0, 2, (dim,), generator=g) * 2 - 1
+    k = torch.randint(-10, 11, (L, dim), generator=g)
+    v = torch.randint(50, 121, (L, dim), generator=g) // 8 * 8   # exact in e4m3
+    sinks = [5, 21, 37, 53]
+    k[sinks], v[sinks] = 120 * sign, 0
+    order = torch.randperm(L // page, generator=g)
+    codes = [torch.empty(L // page, 1, page, dim).index_copy_(0, order, x.float().view(L // page, 1, page, dim)).to(dtype) for x in (k, v)]
+    # a sink's score: 120 * 64 / 8 * scale = 17.76 = ln(2^25.6) above the others', which are about 0
+    scales = [torch.full((L // page, 1), 17.76 / 960), torch.ones(L // page, 1)]
+    rows = batch * most
+    q = (sign * (1 + torch.rand(rows, 1, 1, generator=g) / 64)).half()
+    cache = tg.KvCache(*(x.cuda() for x in codes + scales))
+    table = order.int().expand(batch, -1).contiguous().cuda()
+    cu = torch.arange(0, rows + 1, most, dtype=torch.int32).cuda()
+    out, lse = tg.attention_kv(q.cuda(), cache, table, _ints([L] * batch), cu, max_new=most, max_len=L, return_lse=True)
+    _status_ok(tg)
+    kd, vd = (x.double()[order].view(L, dim).cuda() for x in codes)
+    z = q[:, 0].double().cuda() @ (kd * scales[0][0, 0].double()).T / 8
+    z = z.masked_fill((torch.arange(L) > L - most + torch.arange(rows)[:, None] % most).cuda(), -torch.inf)
+    size = 1.05 * 17.76   # of the largest sum of |q k|, scaled
+    ds = 2 * dim * 2.0 ** -24 * size + 2.0 ** -21
+    l = torch.logsumexp(z, 1)
+    p = (z - l[:, None]).exp()
+    o = p @ vd
+    small = 2.0 ** -34 * p.amax(1, keepdim=True) * vd.sum(0)
+    tol = (2 * ds + 2.0 ** -11 + L * 2.0 ** -24) * o + small
+    assert (tol < o * 2.0 ** -7).all()
+    ref.near(out[:, 0], o.cpu(), (tol + o * 2.0 ** -11 + 2.0 ** -25).cpu())
+    ref.near(lse[:, 0], l.cpu(), (ds + L * 2.0 ** -24 + 2.0 ** -21 * (1 + l.abs())).cpu())
 
 
 # ---------------------------------------------------------------- waits that run out

@@ -14,8 +14,10 @@
 // Scales stay out of the products. With t_j = log2(e) scale k_scale (q . kcode_j)
 // + log2(v_scale), the weights w_j = 2^(t_j - m) carry the value scale of their
 // page, so o = sum w_j vcode_j / sum (w_j / v_scale): the codes enter both
-// products exactly (e4m3 and int8 are exact in fp16), and w_j <= 2^8 whatever
-// the scales. w is rounded to fp16 (2^-11 of itself) for its product, its sum is
+// products exactly (e4m3 and int8 are exact in fp16), and w_j < 2^16 whatever
+// the scales. w is rounded to fp16 for its product, so that it can meet the codes
+// in one tensor-core instruction: by 2^-11 of itself down to 2^-23 of the largest
+// w of the row, below that in steps of 2^-33 of it (tg_kv_split.cuh). Its sum is
 // kept in fp32 from the unrounded value.
 //
 // Splitting. The batch's work is a list of 64-token chunks, unit by unit (a unit
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
 #pragma unroll
                 for (int n = 0; n < kTiles; ++n)
-                    above |= fmaxf(sc[n][0], sc[n][2]) > m[n][0] + kRescaleLog2 || fmaxf(sc[n][1], sc[n][3]) > m[n][1] + kRescaleLog2;
+                    above |= fmaxf(sc[n][0], sc[n][2]) > m[n][0] + kMostLog2 || fmaxf(sc[n][1], sc[n][3]) > m[n][1] + kMostLog2;
                 if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
                     for (int n = 0; n < kTiles; ++n)
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
                             t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
                             t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
-                            const float m_new = fmaxf(m[n][e], t);
+                            const float m_new = fmaxf(m[n][e], t - kHeadroomLog2);
                             const float keep = ex2_approx(m[n][e] - m_new);
                             m[n][e] = m_new;
                             l[n][e] *= keep;

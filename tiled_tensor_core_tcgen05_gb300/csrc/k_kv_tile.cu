@@ -654,9 +654,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 top = fmaxf(top, red[ph * 4 * kHalfRows + (kh ^ 1) * kHalfRows]);
                 float keep = 1.0f;
                 bool grew = false;
-                if (top > m + kRescaleLog2) {
-                    keep = ex2_approx(m - top);
-                    m = top;
+                if (top > m + kMostLog2) {
+                    keep = ex2_approx(m - (top - kHeadroomLog2));
+                    m = top - kHeadroomLog2;
                     grew = true;
                 }
                 float sum = 0.0f;

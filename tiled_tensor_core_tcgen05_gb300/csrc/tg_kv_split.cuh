@@ -35,8 +35,17 @@ __device__ __forceinline__ bool wait_suspended(uint32_t bar, uint32_t parity, co
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNoMax = -1e30f;        // running maximum before any visible key
-constexpr float kRescaleLog2 = 8.0f;    // the maximum moves only when a weight would pass 2^8
+constexpr float kNoMax = -1e30f;        // a row's reference before any visible key
+
+// A row's weights are 2^(t - m) for a reference m that follows the row's maximum from kHeadroomLog2 below, and that
+// moves only when a weight would pass 2^kMostLog2, near fp16's largest value. The sums carry the same factor, so the
+// quotient and m + log2 of the sum do not know where m lies: it is chosen for fp16, in which the weights go into
+// their product. Its ordinary values end at 2^-14 and its last one is 2^-24, so a key keeps 11 bits down to
+// 2^-23 of the largest weight and counts for something down to 2^-34 of it, however many such keys there are under one
+// that dominates. More headroom means that m moves more often (the chunks of k_kv_tile.cu take 675 us with 7,
+// 676 with 9, 680 with 10).
+constexpr float kHeadroomLog2 = 9.0f;
+constexpr float kMostLog2 = 15.99f;
 
 // Where CTA k of `ctas` begins in a list of `total` chunks: equal shares, the first ones one longer.
 struct Shares {
@@ -119,7 +128,7 @@ constexpr int kStep = 16;  // tokens a box of the cache's tensor maps
 // 1 / a row's sum; 0 for a row that sees nothing.
 __device__ __forceinline__ float row_inverse(float l) { return l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l); }
 
-// The natural log of a row's sum l at the running maximum m (base 2).
+// The natural log of a row's sum l at the reference m (base 2).
 __device__ __forceinline__ float row_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * (1.0f / kLog2e); }
 
 // Joins the parts of the unit inside which share k begins, if k's is its first border: block
