@@ -56,7 +56,7 @@ constexpr uint32_t kColS = 0;            // + 128 half; the weights of keys 64 g
 constexpr uint32_t kColO = 256;          // + 128 half
 
 // What a CTA holds back while the watchdog's test hook is on, one CTA after another: its first piece of codes, word
-// of its first tile's products, or its first segment.
+// of its products, or its first segment.
 constexpr int kNoCodes = 1, kNoProduct = 2, kNoSegment = 3;
 
 // What the softmax and the converters know of a tile: per block of 16 keys the key scale, log2 and
@@ -81,7 +81,7 @@ struct Smem {
     static constexpr int kInfo = kRed + 2 * 2 * 2 * kHalfRows * 4;
     static constexpr int kSegments = kInfo + kInfoSlots * static_cast<int>(sizeof(TileInfo));
     static constexpr int kBars = kSegments + kSegSlots * 64;
-    static constexpr int kNumBars = 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + kInfoSlots + 2 + kTurns + 2 * kSegSlots + 2 * kRawSlots;
+    static constexpr int kNumBars = 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + kInfoSlots + 2 + kTurns + 2 * kSegSlots + 2 * kRawSlots + 1;
     static constexpr int kScan = kBars + 8 * kNumBars;      // a sum a warp, then found offset and sequence
     static constexpr int kFoundOff = kScan + kThreads / 32 * 8;
     static constexpr int kFoundSeq = kFoundOff + 8;
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const uint32_t q_full = bars(2), k_full = bars(2), k_empty = bars(2), v_full = bars(2), v_empty = bars(2), s_full = bars(2);
     const uint32_t p_full = bars(4), o_done = bars(2), info_full = bars(kInfoSlots), drain = bars(2), turn = bars(kTurns);
-    const uint32_t seg_full = bars(kSegSlots), seg_empty = bars(kSegSlots), raw_full = bars(kRawSlots), raw_empty = bars(kRawSlots);
+    const uint32_t seg_full = bars(kSegSlots), seg_empty = bars(kSegSlots), raw_full = bars(kRawSlots), raw_empty = bars(kRawSlots), nowhere = bars(1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
     int64_t* scan = reinterpret_cast<int64_t*>(smem + L::kScan);
@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(o_done + 8 * i, 1);
             mbar_init(drain + 8 * i, 1);
         }
+        mbar_init(nowhere, 2);  // that nothing waits for
         for (int i = 0; i < 4; ++i) mbar_init(p_full + 8 * i, 8);
         for (int i = 0; i < kTurns; ++i) mbar_init(turn + 8 * i, 1);
         for (int i = 0; i < kInfoSlots; ++i) mbar_init(info_full + 8 * i, 1);
@@ -353,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t kd = smem_desc_sw128(sbase + L::kK, 16, 1024);
             const uint64_t vd = smem_desc_sw128(sbase + L::kV, L::kBox, 1024);
             const uint32_t col_s = tmem + kColS + 128 * h, col_o = tmem + kColO + 128 * h;
+            const uint32_t product_done = withheld == kNoProduct ? nowhere : o_done + 8 * h;
             // 16 keys of the product; their weights are 8 columns
             auto product = [&](int kk, uint32_t st, bool add) {
                 mma_f16_tmem_a(col_o, col_s + (kk >> 2) * 64 + (kk & 3) * 8, vd + st * (L::kTile >> 4) + kk * (2048 >> 4), idesc_o, add);
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         product(3, st, true);
                         product(6, st, true);
                         product(7, st, true);
-                        if (withheld != kNoProduct || g != 0) mma_commit(o_done + 8 * h);
+                        mma_commit(product_done);
                         mma_commit(v_empty + 8 * st);
                     }
                     tile_no += n;
@@ -556,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t col_s = lanes + kColS + 128 * h + 64 * kh, col_o = lanes + kColO + 128 * h + kh * (kDim / 2);
         const int pair = h * 4 + (warp & 3);                          // the two warps of the same 32 rows
         float* red = reinterpret_cast<float*>(smem + L::kRed) + (h * 2) * kHalfRows + row;  // + parity 4 * 128, + key half 128
+        bool ok = true;
         bool first_segment = true;
         while (true) {
             // all of the half go on, or none: no warp waits at a barrier for one that has left
@@ -608,7 +611,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c.window > 0 && p - c.window + 1 > 0) from = static_cast<int>(p - c.window + 1);
             }
             float m = kNoMax, l = 0.0f;
-            bool ok = true;
             const int n = sg.t1 - sg.t0;
             for (int j = 0; j < n; ++j) {
                 const uint32_t g = tile_no + j, ph = g & 1u;
@@ -709,11 +711,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 l = l * keep + sum;
             }
-            // Every warp of the half comes to this barrier once a segment, whatever became of its waits, and all leave
-            // together: the others may have taken their last tile before this one saw the abort flag, and the
-            // barrier has no limit of its own.
+            // Every warp of the half comes to the barrier at the segment's end once, whatever became of its waits, and
+            // all leave together: the others may have taken their last tile before this one saw the abort flag,
+            // and the barrier has no limit of its own.
+            if (!ok) {
+                named_barrier_or(1 + h, 256, true);
+                break;
+            }
             tile_no += n;
-            if (ok) ok = wait_suspended(o_done + 8 * h, (tile_no - 1) & 1u, wc, kSiteEpilogueAccFull);
+            ok = wait_suspended(o_done + 8 * h, (tile_no - 1) & 1u, wc, kSiteEpilogueAccFull);
             // both key halves' sums; the maxima of the last tile were in the other parity
             red[(tile_no & 1u) * 4 * kHalfRows + kh * kHalfRows] = l;
             if (named_barrier_or(1 + h, 256, !ok)) break;
