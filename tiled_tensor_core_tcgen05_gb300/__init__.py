@@ -471,14 +471,30 @@ def rope(X, positions, inv_freq, amplitude: float = 1.0, layout: int = ROPE_HALF
 class KvCache:
     """A paged key/value cache held in 8 bits: codes k, v (pages, kv_heads, page, dim), float8_e4m3fn
     or int8, and one float32 scale for each (page, kv_head) in k_scale, v_scale (pages, kv_heads).
-    Pages hold 16, 32, 64 or 128 tokens; dim is 64 or 128. ``KvCache.empty`` allocates one."""
+    Pages hold 16, 32, 64 or 128 tokens; dim is 64 or 128. ``KvCache.empty`` allocates one. A cache keeps
+    its four tensors for good (for others, make another cache); what they hold, where and in which shape, is
+    looked at in every call."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "page", "dim", "fmt", "args")
+    __slots__ = ("args",)
 
     def __init__(self, k, v, k_scale, v_scale):
-        self.args = a = (_fast or _binding()).cache_args(k, v, k_scale, v_scale)
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        _, _, _, _, self.pages, self.kv_heads, self.page, self.dim, self.fmt = a
+        object.__setattr__(self, "args", (_fast or _binding()).cache_args(k, v, k_scale, v_scale))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a KvCache's {name} cannot be set: make another KvCache")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"a KvCache's {name} cannot be deleted")
+
+    k = property(lambda self: self.args[0])
+    v = property(lambda self: self.args[1])
+    k_scale = property(lambda self: self.args[2])
+    v_scale = property(lambda self: self.args[3])
+    pages = property(lambda self: self.k.shape[0])
+    kv_heads = property(lambda self: self.k.shape[1])
+    page = property(lambda self: self.k.shape[2])
+    dim = property(lambda self: self.k.shape[3])
+    fmt = property(lambda self: KV_INT8 if str(self.k.dtype) == "torch.int8" else KV_E4M3)
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, page: int = 64, dim: int = 128, dtype=None, device="cuda"):
@@ -510,7 +526,7 @@ def kv_read(cache, table, first, cu, total: int, dtype=None, out=None, stream=No
         dtype = K.dtype if K is not None else torch.float16
     if dtype is not torch.float16 and dtype is not torch.bfloat16:
         raise TypeError(f"dtype must be float16 or bfloat16, got {dtype}")
-    return _answer((_fast or _binding()).kv_read(cache.args, cache.k, table, first, cu, total,
+    return _answer((_fast or _binding()).kv_read(cache.args, table, first, cu, total,
                                                  dtype is torch.bfloat16, K, V, stream))
 
 

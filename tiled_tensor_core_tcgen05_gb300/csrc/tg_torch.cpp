@@ -131,12 +131,35 @@ struct Cache {
     int format;
 };
 
-// What KvCache keeps: the pointers and sizes below, in this order.
+// A cache's tensors k, v, k_scale, v_scale, looked at in every call: their storage may have been exchanged or resized
+// since the last one.
+Cache cache_of(PyObject* const* a) {
+    static const char* names[4] = {"k", "v", "k_scale", "v_scale"};
+    const at::Tensor* t[4];
+    for (int i = 0; i < 4; ++i) t[i] = &tensor(a[i], names[i]);
+    const auto type = t[0]->scalar_type();
+    if (type != at::kFloat8_e4m3fn && type != at::kChar)
+        type_error(std::string("codes must be float8_e4m3fn or int8, got ") + c10::toString(type));
+    if (t[0]->dim() != 4 || t[0]->sizes() != t[1]->sizes() || t[1]->scalar_type() != type)
+        value_error("k and v must share one (pages, kv_heads, page, dim) shape and one type");
+    for (int i = 2; i < 4; ++i) {
+        if (t[i]->scalar_type() != at::kFloat) type_error("scales must be float32");
+        if (t[i]->dim() != 2 || t[i]->size(0) != t[0]->size(0) || t[i]->size(1) != t[0]->size(1))
+            value_error("scales must have shape (" + std::to_string(t[0]->size(0)) + ", " + std::to_string(t[0]->size(1)) + ")");
+    }
+    for (int i = 0; i < 4; ++i) {
+        on_cuda(*t[i], names[i]);
+        if (!t[i]->is_contiguous()) value_error(std::string(names[i]) + " must be contiguous");
+    }
+    return Cache{t[0]->data_ptr(), t[1]->data_ptr(), static_cast<float*>(t[2]->data_ptr()), static_cast<float*>(t[3]->data_ptr()), t[0]->size(0),
+                 t[0]->size(1), t[0]->size(2), t[0]->size(3), type == at::kChar ? TG_KV_INT8 : TG_KV_E4M3};
+}
+
+// What KvCache keeps: its four tensors.
 Cache cache(PyObject* t) {
-    if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 9) type_error("cache must be a KvCache");
-    auto p = [&](int i) { return PyLong_AsVoidPtr(PyTuple_GET_ITEM(t, i)); };
-    auto n = [&](int i) { return integer(PyTuple_GET_ITEM(t, i)); };
-    return Cache{p(0), p(1), static_cast<float*>(p(2)), static_cast<float*>(p(3)), n(4), n(5), n(6), n(7), static_cast<int>(n(8))};
+    if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 4) type_error("cache must be a KvCache");
+    PyObject* const a[4] = {PyTuple_GET_ITEM(t, 0), PyTuple_GET_ITEM(t, 1), PyTuple_GET_ITEM(t, 2), PyTuple_GET_ITEM(t, 3)};
+    return cache_of(a);
 }
 
 struct Batch {
@@ -216,26 +239,8 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (k, v, k_scale, v_scale) -> what KvCache keeps
 PyObject* cache_args(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 4, [&]() -> PyObject* {
-        static const char* names[4] = {"k", "v", "k_scale", "v_scale"};
-        const at::Tensor *t[4];
-        for (int i = 0; i < 4; ++i) t[i] = &tensor(a[i], names[i]);
-        const auto type = t[0]->scalar_type();
-        if (type != at::kFloat8_e4m3fn && type != at::kChar)
-            type_error(std::string("codes must be float8_e4m3fn or int8, got ") + c10::toString(type));
-        if (t[0]->dim() != 4 || t[0]->sizes() != t[1]->sizes() || t[1]->scalar_type() != type)
-            value_error("k and v must share one (pages, kv_heads, page, dim) shape and one type");
-        for (int i = 2; i < 4; ++i) {
-            if (t[i]->scalar_type() != at::kFloat) type_error("scales must be float32");
-            if (t[i]->dim() != 2 || t[i]->size(0) != t[0]->size(0) || t[i]->size(1) != t[0]->size(1))
-                value_error("scales must have shape (" + std::to_string(t[0]->size(0)) + ", " + std::to_string(t[0]->size(1)) + ")");
-        }
-        for (int i = 0; i < 4; ++i) {
-            on_cuda(*t[i], names[i]);
-            if (!t[i]->is_contiguous()) value_error(std::string(names[i]) + " must be contiguous");
-        }
-        return Py_BuildValue("(KKKKLLLLi)", (unsigned long long)t[0]->data_ptr(), (unsigned long long)t[1]->data_ptr(), (unsigned long long)t[2]->data_ptr(),
-                             (unsigned long long)t[3]->data_ptr(), (long long)t[0]->size(0), (long long)t[0]->size(1), (long long)t[0]->size(2),
-                             (long long)t[0]->size(3), type == at::kChar ? TG_KV_INT8 : TG_KV_E4M3);
+        cache_of(a);
+        return PyTuple_Pack(4, a[0], a[1], a[2], a[3]);
     });
 }
 
@@ -286,24 +291,24 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// (cache, device tensor, table, first, cu, total, bf16, K or None, V or None, stream)
+// (cache, table, first, cu, total, bf16, K or None, V or None, stream)
 PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 10, [&]() -> PyObject* {
+    return guarded(n, 9, [&]() -> PyObject* {
         const Cache c = cache(a[0]);
-        const Batch b = batch(a[2], a[3], a[4]);
-        const int64_t total = integer(a[5]);
+        const Batch b = batch(a[1], a[2], a[3]);
+        const int64_t total = integer(a[4]);
         if (total < 0) value_error("total must not be negative");
-        const Where where(a[9]);
+        const Where where(a[8]);
         at::Tensor made[2];
-        int dtype = truth(a[6]) ? TG_BF16 : TG_FP16;
+        int dtype = truth(a[5]) ? TG_BF16 : TG_FP16;
         void* to[2];
         for (int i = 0; i < 2; ++i) {
-            if (a[7 + i] == Py_None) {
-                made[i] = at::empty({total, c.kv_heads, c.dim}, tensor(a[1], "k").options().dtype(dtype == TG_BF16 ? at::kBFloat16 : at::kHalf));
+            if (a[6 + i] == Py_None) {
+                made[i] = at::empty({total, c.kv_heads, c.dim}, tensor(PyTuple_GET_ITEM(a[0], 0), "k").options().dtype(dtype == TG_BF16 ? at::kBFloat16 : at::kHalf));
                 to[i] = made[i].data_ptr();
                 continue;
             }
-            const at::Tensor& t = tensor(a[7 + i], "out");
+            const at::Tensor& t = tensor(a[6 + i], "out");
             on_cuda(t, "out");
             if (t.dim() != 3 || t.size(0) != total || t.size(1) != c.kv_heads || t.size(2) != c.dim || !t.is_contiguous())
                 value_error("out must be two contiguous tensors of shape (" + std::to_string(total) + ", " + std::to_string(c.kv_heads) + ", " + std::to_string(c.dim) + ")");
@@ -315,7 +320,7 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
             [&]() -> PyObject* {
                 PyObject* pair = PyTuple_New(2);
                 for (int i = 0; pair != nullptr && i < 2; ++i)
-                    PyTuple_SET_ITEM(pair, i, made[i].defined() ? THPVariable_Wrap(std::move(made[i])) : same(a[7 + i]));
+                    PyTuple_SET_ITEM(pair, i, made[i].defined() ? THPVariable_Wrap(std::move(made[i])) : same(a[6 + i]));
                 return pair;
             });
     });
