@@ -367,12 +367,17 @@ tg_status tg_softmax_rows(const void* X, void* Y, int64_t M, int64_t N, tg_strea
  * order. Packed tensors hold the sequences' new tokens one after another,
  * sequence i's in rows cu[i] .. cu[i + 1] - 1 (batch + 1 int32 offsets; with
  * cu NULL every sequence has one row); no sequence has more than max_new.
+ * Rows that no sequence has (before cu[0], or from cu[batch] on: a batch padded
+ * to a fixed size) come back as those of a token that sees nothing from the
+ * attention, as zeros from reading and as they are from the rotation of queries.
  * No page is shared by sequences that are written in one call.
  *
  * These arrays live on the device, so the kernels check them: an offset,
  * length or page number out of range is not followed, the sequence (append),
  * the row (read) or the page's keys (attention) are left out, and the next
- * tg_device_status answers TG_ERR_BOUNDS. Table entries past a sequence's last
+ * tg_device_status answers TG_ERR_BOUNDS. The rows of a sequence whose span of cu
+ * is out of range or longer than max_new are treated as rows of no sequence, and
+ * queries of a sequence that is left out are not rotated. Table entries past a sequence's last
  * page are never read.
  * ------------------------------------------------------------------------- */
 

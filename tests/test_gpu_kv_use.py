@@ -57,3 +57,103 @@ def test_a_cache_whose_storage_was_exchanged(tg):
     with pytest.raises(ValueError, match="scales must have shape"):
         tg.kv_read(cache, *args)
     _status_ok(tg)
+
+
+# ---------------------------------------------------------------- rows that no sequence has
+
+NOTHING = [[0, 3, 5], [2, 5, 7], [3, 3, 3], [9, 9, 9], [0, 0, 0], [0]]   # of nine rows: padded behind, around, empty, no sequences
+
+
+@pytest.mark.parametrize("wide", [1, 40])  # the kernels for few rows, and for many
+@pytest.mark.parametrize("offsets", NOTHING)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_of_rows_that_no_sequence_has(tg, wide, offsets, dim):
+    cache = _filled(tg, pages=40, dim=dim)
+    batch, offsets = len(offsets) - 1, [wide * x for x in offsets]
+    T = 9 * wide
+    lens = _ints([5 * wide, 100 + wide][:batch])
+    table = torch.arange(40, dtype=torch.int32).view(2, 20)[:batch].cuda()
+    q = torch.randn(T, 4, dim, generator=torch.Generator().manual_seed(1)).half().cuda()
+    out = torch.full_like(q, torch.nan)
+    got, lse = tg.attention_kv(q, cache, table, lens, _ints(offsets), max_new=5 * wide, max_len=320, out=out, return_lse=True)
+    fresh = tg.attention_kv(q, cache, table, lens, _ints(offsets), max_new=5 * wide, max_len=320)
+    _status_ok(tg)
+    none = torch.ones(T, dtype=torch.bool, device="cuda")
+    none[offsets[0]:offsets[-1]] = False
+    assert (got[none] == 0).all() and (lse[none] == -torch.inf).all() and torch.equal(got, fresh)
+    assert got.isfinite().all() and lse[~none].isfinite().all() and (got[~none] != 0).any(-1).all()
+
+
+@pytest.mark.parametrize("most", [2, 70])
+@pytest.mark.parametrize("max_len", [64, 4000])
+def test_attention_of_spans_out_of_range(tg, most, max_len):
+    """Reported, and zeros in their rows whatever the output held; the other sequences are as they were."""
+    cache = _filled(tg, pages=16)
+    table, lens = torch.arange(16, dtype=torch.int32).view(4, 4).cuda(), _ints([60, 64, 50, 64])
+    cu = [i * most for i in range(5)]
+    q = torch.randn(4 * most, 8, 64, generator=torch.Generator().manual_seed(2)).half().cuda()
+
+    def run(offsets, bound):
+        out = torch.full_like(q, torch.nan)
+        return tg.attention_kv(q, cache, table, lens, _ints(offsets), max_new=bound, max_len=max_len, out=out, return_lse=True)
+
+    good, glse = run(cu, most)
+    _status_ok(tg)
+    for offsets, bound, zero, same in ((cu[:2] + [cu[2] + 1] + cu[3:], most, (most, 2 * most + 1), (0, most)),          # longer than max_new
+                                       (cu[:4] + [cu[4] + 1], most + 1, (3 * most, 4 * most), (0, 3 * most)),           # past the end
+                                       ([-1] + cu[1:], most + 2, (0, most), (most, 4 * most))):                         # before the start
+        out, lse = run(offsets, bound)
+        assert tg.tg_device_status(None)[0] == tg.ERR_BOUNDS, offsets
+        assert (out[slice(*zero)] == 0).all() and (lse[slice(*zero)] == -torch.inf).all(), offsets
+        near = dict(rtol=2.0 ** -9, atol=2.0 ** -12)   # the work may be split in another way
+        assert torch.allclose(out[slice(*same)], good[slice(*same)], **near) and torch.allclose(lse[slice(*same)], glse[slice(*same)], **near)
+        assert out.isfinite().all()
+    _status_ok(tg)
+
+
+@pytest.mark.parametrize("offsets", NOTHING)
+def test_reading_rows_that_no_sequence_has(tg, offsets):
+    cache = _filled(tg)
+    batch = len(offsets) - 1
+    table, first = _ints([[0, 1], [2, 3]])[:batch], _ints([1, 15])[:batch]
+    out = tuple(torch.full((9, 2, 64), torch.nan, dtype=torch.float16, device="cuda") for _ in range(2))
+    tg.kv_read(cache, table.contiguous(), first, _ints(offsets), 9, out=out)
+    _status_ok(tg)
+    none = torch.ones(9, dtype=torch.bool, device="cuda")
+    none[offsets[0]:offsets[-1]] = False
+    for x in out:
+        assert (x[none] == 0).all() and x.isfinite().all() and (x[~none] != 0).any(-1).all()
+
+
+@pytest.mark.parametrize("most", [1, 3])      # the kernels for single tokens, and for prompts
+@pytest.mark.parametrize("off", [0, 1])       # whole 16-byte pieces, and not
+@pytest.mark.parametrize("case", [([0, 1, 2], [0, 0], 0), ([2, 3, 4], [5, 31], 0), ([5, 5, 5], [0, 0], 0), ([0], [], 0),
+                                  ([1, 2, 3], [32, 3], 1), ([1, 2, 3], [-1, 3], 1), ([1, 9, 8], [0, 3], 1), ([1, 6, 7], [3, 3], 1)])
+def test_queries_that_are_not_rotated_are_copied(tg, most, off, case):
+    """Rows of no sequence, and of a sequence that is out of range (reported)."""
+    offsets, lens, bad = case
+    if most > 1:
+        offsets, lens = [most * x for x in offsets], [x if x != 31 else 29 for x in lens]
+    T, batch = 7 * most, len(lens)
+    cache = _filled(tg, pages=4)
+    table = _ints([[0, 1], [2, 3]])[:batch].contiguous()
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(T, 2, 64, generator=g).half().cuda() for _ in range(2))
+    q = torch.randn(T * 4 * 64 + 8, generator=g).half().cuda()[off:off + T * 256].view(T, 4, 64)
+    f, amplitude = tg.rope_frequencies(64)
+    out = torch.full((T, 4, 64), torch.nan, dtype=torch.float16, device="cuda")
+    tg.kv_append(cache, k, v, table, _ints(lens), _ints(offsets), max_new=most, Q=q, inv_freq=f, amplitude=2.0, out=out)
+    assert tg.tg_device_status(None)[0] == (tg.ERR_BOUNDS if bad else tg.OK)
+    want, row = q.clone(), 0
+    for i in range(batch):
+        lo, hi = offsets[i], offsets[i + 1]
+        if 0 <= lo < hi <= T and hi - lo <= most and lens[i] >= 0 and lens[i] + hi - lo <= 32:
+            want[lo:hi] = tg.rope(q[lo:hi], torch.arange(lens[i], lens[i] + hi - lo, dtype=torch.int32, device="cuda"), f, 2.0)
+    turned = (want != q).any(-1).any(-1)
+    assert torch.equal(out[~turned], q[~turned])
+    assert torch.allclose(out[turned].float(), want[turned].float(), rtol=2.0 ** -10, atol=2.0 ** -16)
+    inplace = q.clone()
+    tg.kv_append(cache, k, v, table, _ints(lens), _ints(offsets), max_new=most, Q=inplace, inv_freq=f, amplitude=2.0, out=inplace)
+    tg.tg_device_status(None)
+    assert torch.equal(inplace[~turned], q[~turned])
+    _status_ok(tg)

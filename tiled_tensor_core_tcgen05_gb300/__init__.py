@@ -509,17 +509,17 @@ def kv_append(cache, K, V, table, lens, cu=None, max_new: int = 1, Q=None, inv_f
     """Writes new keys and values K, V (total, kv_heads, dim), float16 or bfloat16, into ``cache``,
     quantised on the way: sequence i's rows cu[i] .. cu[i + 1] - 1 (cu None: one row a sequence) go to
     positions lens[i] .. of the pages in its row of ``table``. lens: int32 tokens held before the call;
-    max_new: no sequence has more rows. With ``inv_freq`` the keys are rotated first by their
+    max_new: no sequence has more rows (one that does is left out, and ``tg_device_status`` says so). With ``inv_freq`` the keys are rotated first by their
     positions (see ``rope``), and the queries Q (total, heads, dim), if given, too: returns them
-    (``out``, which may be Q), else None. The scales and roundings are in include/tg_gemm.h."""
+    (``out``, which may be Q; rows that no sequence has as they are), else None. The scales and roundings are in include/tg_gemm.h."""
     return _answer((_fast or _binding()).kv_append(cache.args, K, V, table, lens, cu, max_new, Q, inv_freq, amplitude,
                                                    layout, out, stream))
 
 
 def kv_read(cache, table, first, cu, total: int, dtype=None, out=None, stream=None):
     """(K, V), each (total, kv_heads, dim), of positions first[i] .. first[i] + (cu[i + 1] - cu[i]) - 1 of
-    every sequence, packed at rows cu[i] .. (cu None: one row a sequence): code * scale, rounded once
-    to ``dtype`` (float16, the default, or bfloat16). ``out``: a pair of contiguous tensors."""
+    every sequence, packed at rows cu[i] .. (cu None: one row a sequence; rows that no sequence has are
+    zeros): code * scale, rounded once to ``dtype`` (float16, the default, or bfloat16). ``out``: a pair of contiguous tensors."""
     import torch
     K, V = out if out is not None else (None, None)
     if dtype is None:
@@ -536,7 +536,8 @@ def attention_kv(Q, cache, table, lens, cu=None, max_new: int = 1, max_len: int 
     heads is a multiple of the cache's kv_heads. lens: int32 lengths with the new tokens, which are
     each sequence's last. ``causal``: a token sees positions up to its own, with ``window`` only the
     last so many. max_new and max_len bound the rows and the length of a sequence (max_len None: what
-    the table can hold). scale None: 1 / sqrt(dim). Rows that see nothing give zeros. Returns O (total,
+    the table can hold). scale None: 1 / sqrt(dim). Rows that see nothing, and rows that no sequence has,
+    give zeros; so do those of a sequence beyond either bound, and ``tg_device_status`` says so. Returns O (total,
     heads, dim), with ``return_lse`` also the float32 log of each row's sum (total, heads)."""
     return _answer((_fast or _binding()).attention_kv(Q, cache.args, table, lens, cu, max_new, max_len, causal, window,
                                                       scale, return_lse, out, stream))

@@ -343,6 +343,16 @@ struct TokenArgs {
     Wide wide;
 };
 
+// Queries first, first + step, .. before `last`, of no sequence or of no place, as they are: whole block.
+template <typename E, int kDim>
+__device__ __forceinline__ void copy_queries(const KvAppendCall& c, int first, int last, int step) {
+    for (int64_t r = first; r < last; r += step) {
+        const E* x = static_cast<const E*>(c.q.p) + r * c.q.token;
+        E* y = static_cast<E*>(c.q_out.p) + r * c.q_out.token;
+        for (int i = threadIdx.x; i < c.heads * kDim; i += blockDim.x) y[i / kDim * c.q_out.head + i % kDim] = x[i / kDim * c.q.head + i % kDim];
+    }
+}
+
 // Rows of the token, a warp each: keys of every kv head, values of every kv head, queries.
 template <typename E, int kFmt, int kDim>
 __global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const TokenArgs a) {
@@ -351,8 +361,17 @@ __global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const Token
     const KvAppendCall& c = a.c;
     const KvBatch& b = c.batch;
     const int seq = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32, d = lane * kN;
+    if (seq >= b.batch) {  // queries of no sequence
+        const Uncovered none = uncovered(b);
+        copy_queries<E, kDim>(c, seq - b.batch, none.before, gridDim.x - b.batch);
+        copy_queries<E, kDim>(c, none.after + seq - b.batch, b.total, gridDim.x - b.batch);
+        return;
+    }
     const SeqSpan span = seq_span(b, seq, c.wd);
-    if (span.count == 0) return;
+    if (span.count == 0) {
+        if (span.bad) copy_queries<E, kDim>(c, packed_row(b, seq), packed_row(b, seq + 1), 1);
+        return;
+    }
     const int64_t len = __ldg(b.lens + seq);
     const int page = c.cache.page, kv = c.cache.kv_heads;
     // rows are read before anything about pages is known
@@ -412,9 +431,8 @@ __global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const Token
         for (int i = 0; i < kRowsAtOnce; ++i) {
             const int r = first + i * kTokenWarps;
             if (r >= rows) continue;
-            if (c.rope.inv_freq != nullptr && d < kDim && (r < kv || r >= 2 * kv)) rotate_values<kN>(x[i], o[i], d, cs, sn, c.rope);
+            if (in_range && c.rope.inv_freq != nullptr && d < kDim && (r < kv || r >= 2 * kv)) rotate_values<kN>(x[i], o[i], d, cs, sn, c.rope);
             if (r >= 2 * kv) {
-                if (!in_range) continue;
                 E* y = static_cast<E*>(c.q_out.p) + static_cast<int64_t>(span.first) * c.q_out.token + (r - 2 * kv) * c.q_out.head;
                 __syncwarp();  // in place, other lanes read their partners first
                 if (d < kDim) store_values<E, kN>(y, d, a.wide.q_out, x[i]);
@@ -462,7 +480,7 @@ __global__ void __launch_bounds__(kTokenThreads) append_token_kernel(const Token
 
 constexpr int kQTokens = 4;  // per CTA, where rows are not whole 16-byte pieces
 
-// The positions of tokens token0 .. token0 + n - 1; -1 for one of no sequence or of no place.
+// The positions of tokens token0 .. token0 + n - 1; -1 for one of no sequence, or of one that does not fit.
 __device__ __forceinline__ void q_positions(const KvAppendCall& c, int32_t* where, int token0, int n) {
     const KvBatch& b = c.batch;
     const int first = block_find(b.batch, [&](int i) { return static_cast<int64_t>(b.cu ? __ldg(b.cu + i) : i); }, token0);
@@ -472,8 +490,8 @@ __device__ __forceinline__ void q_positions(const KvAppendCall& c, int32_t* wher
         while (seq + 1 < b.batch && (b.cu ? __ldg(b.cu + seq + 1) : seq + 1) <= token) ++seq;
         const SeqSpan span = seq_span(b, seq, c.wd);
         if (token >= span.first && token < span.first + span.count) {
-            const int64_t pos = static_cast<int64_t>(__ldg(b.lens + seq)) + token - span.first;
-            at = pos >= 0 && pos < b.table_width * c.cache.page ? static_cast<int>(pos) : -1;  // the keys' kernel reports it
+            const int64_t len = __ldg(b.lens + seq);
+            if (len >= 0 && len + span.count <= b.table_width * c.cache.page) at = static_cast<int>(len) + token - span.first;  // or the keys' kernel reports it
         }
         where[threadIdx.x] = at;
     }
@@ -506,14 +524,16 @@ __global__ void __launch_bounds__(kRopeThreads) append_q_any_kernel(const KvAppe
     const int per_head = half + dim - c.rope.rotary;
     for (int i = threadIdx.x; i < n * c.heads * per_head; i += kRopeThreads) {
         const int row = i / per_head, j = i - row * per_head, t = row / c.heads, h = row - t * c.heads;
-        if (where[t] < 0) continue;
+        const bool turns = where[t] >= 0;
         const E* x = static_cast<const E*>(c.q.p) + static_cast<int64_t>(token0 + t) * c.q.token + h * c.q.head;
         E* y = static_cast<E*>(c.q_out.p) + static_cast<int64_t>(token0 + t) * c.q_out.token + h * c.q_out.head;
         if (j < half) {
             const int ia = c.rope.layout == kRopeHalf ? j : 2 * j, ib = c.rope.layout == kRopeHalf ? j + half : 2 * j + 1;
-            const float cc = cs[t * half + j], ss = sn[t * half + j], u = to_float(x[ia]), w = to_float(x[ib]);
-            y[ia] = from_float<E>(u * cc - w * ss);
-            y[ib] = from_float<E>(w * cc + u * ss);
+            const float cc = cs[t * half + j], ss = sn[t * half + j];
+            const E xa = x[ia], xb = x[ib];
+            const float u = to_float(xa), w = to_float(xb);
+            y[ia] = turns ? from_float<E>(u * cc - w * ss) : xa;
+            y[ib] = turns ? from_float<E>(w * cc + u * ss) : xb;
         } else {
             y[half + j] = x[half + j];
         }
@@ -525,6 +545,7 @@ __global__ void __launch_bounds__(kRopeThreads) append_q_any_kernel(const KvAppe
 
 constexpr int kReadThreads = 256;
 constexpr int kReadRows = 16;  // packed rows a CTA
+constexpr int kNoSequence = -2;  // in the place of a row's page: the row comes back as zeros (-1: it is left as it is)
 
 // Eight codes in, eight values out, a thread: consecutive threads take consecutive pieces of a row of
 // all heads, so the output is written in whole lines and the codes are read in lines of a head.
@@ -537,11 +558,12 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const KvReadCall c) 
     const int first = block_find(b.batch, [&](int i) { return static_cast<int64_t>(b.cu ? __ldg(b.cu + i) : i); }, row0);
     if (threadIdx.x < n) {
         const int row = row0 + threadIdx.x;
-        int seq = first, p = -1, place = 0;
+        int seq = first, p = kNoSequence, place = 0;
         while (seq + 1 < b.batch && (b.cu ? __ldg(b.cu + seq + 1) : seq + 1) <= row) ++seq;
-        const SeqSpan span = seq_span(b, seq, c.wd);
+        const SeqSpan span = b.batch > 0 ? seq_span(b, seq, c.wd) : SeqSpan{0, 0, false};
         if (row >= span.first && row < span.first + span.count) {
             const int64_t pos = static_cast<int64_t>(__ldg(b.lens + seq)) + row - span.first;
+            p = -1;
             if (pos < 0 || pos >= b.table_width * page) report_range(c.wd);
             else {
                 p = seq_page(b, c.cache, seq, static_cast<int>(pos / page), c.wd);
@@ -565,13 +587,18 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const KvReadCall c) 
             if (i >= items) continue;
             const int row = i / per_row, in = i - row * per_row, h = in / kPieces, d = (in - h * kPieces) * 8;
             const int p = page_of[row];
-            if (p < 0) continue;
+            if (p == -1) continue;
+            to[j] = static_cast<int64_t>(row0) * per_row * 8 + static_cast<int64_t>(i) * 8;
+            if (p == kNoSequence) {
+                kc[j] = vc[j] = make_uint2(0, 0);
+                ks[j] = vs[j] = 0.0f;
+                continue;
+            }
             const int64_t ph = static_cast<int64_t>(p) * heads + h, at = (ph * page + place_of[row]) * kDim + d;
             kc[j] = __ldg(reinterpret_cast<const uint2*>(c.cache.k + at));
             vc[j] = __ldg(reinterpret_cast<const uint2*>(c.cache.v + at));
             ks[j] = __ldg(c.cache.k_scale + ph);
             vs[j] = __ldg(c.cache.v_scale + ph);
-            to[j] = static_cast<int64_t>(row0) * per_row * 8 + static_cast<int64_t>(i) * 8;
         }
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
@@ -602,8 +629,16 @@ bool is_wide(const Strided& s) { return reinterpret_cast<uintptr_t>(s.p) % 16 ==
 template <typename E, int kFmt, int kDim>
 cudaError_t launch_append(const KvAppendCall& c, int sm_count, cudaStream_t stream) {
     const Wide wide{is_wide(c.k), is_wide(c.v), is_wide(c.q), is_wide(c.q_out)};
-    if (c.batch.max_new == 1) {
-        append_token_kernel<E, kFmt, kDim><<<c.batch.batch, kTokenThreads, 0, stream>>>(TokenArgs{c, wide});
+    if (c.batch.max_new == 1 || c.batch.batch == 0) {
+        // queries of no sequence are copied by CTAs of their own, which look whether there are any (those of the sequences
+        // would wait for the offsets: 256 tokens in 10.5 us a call, not 10.0)
+        int copies = 0;
+        if (c.heads > 0 && c.batch.cu != nullptr && c.q.p != c.q_out.p) {
+            copies = c.batch.total - c.batch.batch;
+            copies = copies < 1 ? 1 : copies > sm_count ? sm_count : copies;
+        }
+        if (c.batch.batch + copies == 0) return cudaSuccess;
+        append_token_kernel<E, kFmt, kDim><<<c.batch.batch + copies, kTokenThreads, 0, stream>>>(TokenArgs{c, wide});
         return cudaGetLastError();
     }
     const int group = c.cache.page * kDim / 8 / kVecs;

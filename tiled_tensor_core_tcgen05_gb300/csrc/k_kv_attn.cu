@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         mine = i < batch ? seq_work<kTiles>(a, i).total : 0;
         total += block_scan(mine, before);
     }
+    if (!a.joined) clear_uncovered<E, kDim>(c);
     const Shares shares(total, a.grid, a.least);
     const int k = blockIdx.x;
     if (k >= shares.ctas) {
@@ -650,6 +651,7 @@ cudaError_t launch_few(const KvAttnCall& c, const CUtensorMap& tmK, const CUtens
     a.least = p.least;
     a.extra = p.extra;
     a.grid = p.grid;
+    a.joined = p.split;
     a.q_vec = reinterpret_cast<uintptr_t>(c.q.p) % 8 == 0 && c.q.token % 4 == 0 && c.q.head % 4 == 0;
     a.meta = static_cast<Meta*>(workspace);
     a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.meta_bytes);

@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mine = i < batch ? tile_work(a, i).total : 0;
         total += block_scan(mine, before);
     }
+    if (!a.joined) clear_uncovered<E, kDim>(c);
     const Shares shares(total, a.grid, a.least);
     const int k = blockIdx.x;
     // the joining kernel runs whatever becomes of this one: until the first segment is known there is nothing to join
@@ -790,12 +791,13 @@ cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMa
     a.share = c.heads / c.cache.kv_heads;
     a.least = 2;
     a.grid = sm_count;
+    a.joined = c.max_len > kKeys;
     a.q_vec = reinterpret_cast<uintptr_t>(c.q.p) % 16 == 0 && c.q.token % 8 == 0 && c.q.head % 8 == 0;
     a.meta = static_cast<Meta*>(workspace);
     a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + meta_bytes(a.grid));
     while (c.cache.page >> (a.page_shift + 1)) ++a.page_shift;
     kernel<<<a.grid, kThreads, Smem<kDim>::kAlloc, stream>>>(tmK, tmV, a);
-    if ((e = cudaGetLastError()) != cudaSuccess || c.max_len <= kKeys) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess || !a.joined) return e;
     return launch_join<E, kDim, kRows>(a, stream);
 }
 

@@ -1407,7 +1407,8 @@ tg_status check_batch(const int32_t* table, int64_t table_width, const int32_t* 
     if (!(aligned(table, 4) && aligned(lens, 4) && aligned(cu, 4)))
         return fail(TG_ERR_INVALID_ARG, "table, lens and cu must be 4-byte aligned");
     // a sequence has no more rows than there are, and where every sequence has one, one
-    const int64_t most = cu == nullptr ? 1 : (max_new < total ? max_new : total);
+    int64_t most = cu == nullptr ? 1 : (max_new < total ? max_new : total);
+    if (most < 1) most = 1;  // no sequences, or no rows
     *out = KvBatch{table, table_width, lens, cu, (int)batch, (int)total, (int)most};
     return TG_OK;
 }
@@ -1475,7 +1476,7 @@ extern "C" tg_status tg_kv_append(void* k_cache, void* v_cache, float* k_scale, 
     if ((st = check_rope(inv_freq, rotary, dim, layout, amplitude)) != TG_OK) return st;
     if (heads < 0 || heads > 0xFFFF) return fail(TG_ERR_INVALID_ARG, "heads out of range: %lld", (long long)heads);
     if (heads > 0 && rotary == 0) return fail(TG_ERR_INVALID_ARG, "Q needs inv_freq: there is nothing to rotate it by");
-    if (batch == 0 || total == 0) return TG_OK;
+    if (total == 0 || (batch == 0 && heads == 0)) return TG_OK;
     if (!K || !V) return fail(TG_ERR_INVALID_ARG, "K or V is NULL");
     if (!(aligned(K, 2) && aligned(V, 2))) return fail(TG_ERR_INVALID_ARG, "K and V must be 2-byte aligned");
     const int64_t codes = pages * kv_heads * page * dim, scales = pages * kv_heads * 4;
@@ -1537,7 +1538,7 @@ extern "C" tg_status tg_kv_read(const void* k_cache, const void* v_cache, const 
     if ((st = check_cache(k_cache, v_cache, k_scale, v_scale, pages, kv_heads, page, dim, format, &c.cache)) != TG_OK)
         return st;
     if ((st = check_batch(table, table_width, first, cu, batch, total, kIntMax, page, &c.batch)) != TG_OK) return st;
-    if (batch == 0 || total == 0) return TG_OK;
+    if (total == 0) return TG_OK;
     if (!K || !V) return fail(TG_ERR_INVALID_ARG, "K or V is NULL");
     if (!(aligned(K, 16) && aligned(V, 16))) return fail(TG_ERR_INVALID_ARG, "K and V must be 16-byte aligned");
     const int64_t codes = pages * kv_heads * page * dim, scales = pages * kv_heads * 4;
@@ -1595,7 +1596,7 @@ extern "C" tg_status tg_attention_kv_workspace(int64_t kv_heads, int64_t page, i
     if (st != TG_OK) return st;
     if ((st = check_batch(&some, 0, &some, &some, batch, total, max_new, page, &c.batch)) != TG_OK) return st;
     if ((st = kv_attn_sizes(kv_heads, page, heads, total, max_len, window, dtype, &c)) != TG_OK) return st;
-    if (batch == 0 || total == 0) return TG_OK;
+    if (total == 0) return TG_OK;
     std::lock_guard<std::mutex> lock(g_mu);
     int dev = 0;
     if ((st = current_device(&dev)) != TG_OK) return st;
@@ -1622,7 +1623,7 @@ extern "C" tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int6
     if (!std::isfinite(static_cast<float>(scale)))
         return fail(TG_ERR_INVALID_ARG, "scale must be finite in 32 bits");
     if ((st = check_strides("Q", q_token_stride, q_head_stride)) != TG_OK) return st;
-    if (batch == 0 || total == 0) return TG_OK;
+    if (total == 0) return TG_OK;
     if (!Q || !O) return fail(TG_ERR_INVALID_ARG, "Q or O is NULL");
     if (!(aligned(Q, 2) && aligned(O, 16) && aligned(lse, 4) && aligned(workspace, 16)))
         return fail(TG_ERR_INVALID_ARG, "O and the workspace must be 16-byte aligned, Q 2-byte, lse 4-byte");

@@ -286,12 +286,13 @@ __device__ __forceinline__ void report_range(const Watchdog& wd) { atomicCAS(wd.
 struct SeqSpan {
     int first;  // first packed row of the sequence's new tokens
     int count;  // how many
+    bool bad;   // out of range
 };
 
 // Sequence i's rows of the packed tensors: cu[i] .. cu[i + 1], or row i where cu is NULL.
 // A span outside [0, total] or longer than max_new is reported and comes back empty.
 __device__ __forceinline__ SeqSpan seq_span(const KvBatch& b, int i, const Watchdog& wd) {
-    SeqSpan s{i, 1};
+    SeqSpan s{i, 1, false};
     if (b.cu != nullptr) {
         const int lo = __ldg(b.cu + i), hi = __ldg(b.cu + i + 1);
         s.first = lo;
@@ -300,9 +301,21 @@ __device__ __forceinline__ SeqSpan seq_span(const KvBatch& b, int i, const Watch
             report_range(wd);
             s.first = 0;
             s.count = 0;
+            s.bad = true;
         }
     }
     return s;
+}
+
+// An offset as a row of the packed tensors, whatever it is.
+__device__ __forceinline__ int packed_row(const KvBatch& b, int i) { return min(max(__ldg(b.cu + i), 0), b.total); }
+
+// Rows that no sequence has: 0 .. before - 1 and after .. total - 1 (a batch padded to a fixed size, say).
+struct Uncovered {
+    int before, after;
+};
+__device__ __forceinline__ Uncovered uncovered(const KvBatch& b) {
+    return b.cu == nullptr ? Uncovered{0, b.total} : Uncovered{packed_row(b, 0), packed_row(b, b.batch)};
 }
 
 // Page `slot` of sequence i, or -1 (reported) where the table holds no page of the cache.

@@ -80,6 +80,7 @@ struct SplitWork {
     int least;          // fewest list entries worth a CTA
     int extra;          // entries before a unit's first chunk, for what every unit costs whatever its length
     int grid;
+    int joined;         // whether the joining kernel runs
     int q_vec;          // Q aligned, and strides whole, for the kernel's wide loads
     int page_shift;
     Meta* meta;         // grid entries
@@ -131,6 +132,27 @@ __device__ __forceinline__ float row_inverse(float l) { return l > 0.0f ? 1.0f /
 // The natural log of a row's sum l at the reference m (base 2).
 __device__ __forceinline__ float row_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * (1.0f / kLog2e); }
 
+// Row r of the outputs as that of a token that sees nothing: whole block.
+template <typename E, int kDim>
+__device__ __forceinline__ void clear_row(const KvAttnCall& c, int64_t r) {
+    uint4* y = reinterpret_cast<uint4*>(static_cast<E*>(c.out) + r * c.heads * kDim);
+    for (int x = threadIdx.x; x < c.heads * (kDim / 8); x += blockDim.x) y[x] = make_uint4(0, 0, 0, 0);
+    for (int h = threadIdx.x; c.lse != nullptr && h < c.heads; h += blockDim.x) c.lse[r * c.heads + h] = -INFINITY;
+}
+
+// Clears the rows that no sequence has, and those of spans out of range, the grid's CTAs together. The joining kernel
+// does it while the parts are being computed; where there is none, the kernel itself.
+template <typename E, int kDim>
+__device__ __forceinline__ void clear_uncovered(const KvAttnCall& c) {
+    if (c.batch.cu == nullptr) return;
+    const Uncovered none = uncovered(c.batch);
+    const int many = none.before + c.batch.total - none.after;
+    for (int i = blockIdx.x; i < many; i += gridDim.x) clear_row<E, kDim>(c, i < none.before ? i : none.after + i - none.before);
+    for (int i = blockIdx.x; i < c.batch.batch; i += gridDim.x)
+        if (seq_span(c.batch, i, c.wd).bad)
+            for (int r = packed_row(c.batch, i); r < packed_row(c.batch, i + 1); ++r) clear_row<E, kDim>(c, r);
+}
+
 // Joins the parts of the unit inside which share k begins, if k's is its first border: block
 // (k - 1, rows 8 blockIdx.y ..), a warp a row, kDim / 32 values a lane. The order of the parts is that
 // of their keys. What a part counts for is computed once, a part a lane.
@@ -140,6 +162,7 @@ template <typename E, int kDim, int kRows>
 __global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const SplitWork a) {
     constexpr int kN = kDim / 32;
     const KvAttnCall& c = a.c;
+    if (blockIdx.y == 0) clear_uncovered<E, kDim>(c);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int k = blockIdx.x + 1, lane = threadIdx.x % 32, r = blockIdx.y * kJoinRows + threadIdx.x / 32;
     const Meta m = a.meta[k];

@@ -16,7 +16,7 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeTokens = 16;  // most tokens a CTA
 constexpr int kAtOnce = 4;
 
-// `fill(where, token0, n)` gives each token's position; with kSkips a token at a negative one is left out.
+// `fill(where, token0, n)` gives each token's position; with kSkips a token at a negative one has none and is copied.
 struct RopeRows {
     Strided x, y;
     int tokens, heads, dim;
@@ -74,8 +74,8 @@ __device__ __forceinline__ void rope_rows(const RopeRows& c, float* smem, Fill f
     while (at[0] >= 0) {
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            if (at[i] < 0 || (kSkips && where[at[i]] < 0)) continue;
-            if (turns) {
+            if (at[i] < 0) continue;
+            if (turns && !(kSkips && where[at[i]] < 0)) {
                 float cv[kPairs], sv[kPairs];
                 const int j = at[i] * half + (kHalf ? d : d / 2);
 #pragma unroll
