@@ -372,13 +372,20 @@ tg_status tg_softmax_rows(const void* X, void* Y, int64_t M, int64_t N, tg_strea
  * attention, as zeros from reading and as they are from the rotation of queries.
  * No page is shared by sequences that are written in one call.
  *
- * These arrays live on the device, so the kernels check them: an offset,
- * length or page number out of range is not followed, the sequence (append),
- * the row (read) or the page's keys (attention) are left out, and the next
- * tg_device_status answers TG_ERR_BOUNDS. The rows of a sequence whose span of cu
- * is out of range or longer than max_new are treated as rows of no sequence, and
- * queries of a sequence that is left out are not rotated. Table entries past a sequence's last
- * page are never read.
+ * These arrays live on the device, so the kernels check them. What is out of
+ * range is not followed, and the next tg_device_status answers TG_ERR_BOUNDS:
+ *
+ *   a page number    its tokens are not written (append; the sequence's other
+ *                    pages are, and its queries are rotated), its rows are left
+ *                    as they were (read), its keys do not count (attention)
+ *   a length         the sequence is not written and its queries are copied
+ *                    (append), rows out of the table's reach are left as they
+ *                    were (read), the sequence's rows see nothing (attention)
+ *   an offset, or a  the sequence's rows count as rows of no sequence
+ *   span longer than
+ *   max_new
+ *
+ * Table entries past a sequence's last page are never read.
  * ------------------------------------------------------------------------- */
 
 typedef enum { TG_FP16 = 0, TG_BF16 = 1 } tg_dtype;

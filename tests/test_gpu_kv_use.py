@@ -157,3 +157,29 @@ def test_queries_that_are_not_rotated_are_copied(tg, most, off, case):
     tg.tg_device_status(None)
     assert torch.equal(inplace[~turned], q[~turned])
     _status_ok(tg)
+
+
+# ---------------------------------------------------------------- one page of several out of range
+
+@pytest.mark.parametrize("entry", [4, -1, 2 ** 31 - 1])
+@pytest.mark.parametrize("rotate", [False, True])
+def test_append_with_the_second_of_three_pages_out_of_range(tg, entry, rotate):
+    """That page's tokens are not written; the sequence's others are, as without the fault, and its queries are rotated."""
+    g = torch.Generator().manual_seed(4)
+    k, v = (torch.randn(45, 2, 64, generator=g).half().cuda() for _ in range(2))
+    q = torch.randn(45, 4, 64, generator=g).half().cuda()
+    f, _ = tg.rope_frequencies(64)
+    start = _filled(tg)
+    caches, outs = [], []
+    for second in (2, entry):
+        cache = tg.KvCache(*(x.clone() for x in start.args))
+        outs.append(tg.kv_append(cache, k, v, _ints([[3, second, 1]]), _ints([2]), _ints([0, 45]), max_new=45, Q=q if rotate else None,
+                                 inv_freq=f if rotate else None))
+        assert tg.tg_device_status(None)[0] == (tg.OK if second == 2 else tg.ERR_BOUNDS)
+        caches.append(cache)
+    for whole, part, before in zip(caches[0].args, caches[1].args, start.args):
+        assert torch.equal(part[[1, 3]], whole[[1, 3]]) and torch.equal(part[[0, 2]], before[[0, 2]])
+        assert not torch.equal(whole[2], before[2])
+    if rotate:
+        assert torch.equal(*outs)
+    _status_ok(tg)
