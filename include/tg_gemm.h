@@ -404,9 +404,9 @@ typedef enum {
  *
  * the others are copied. inv_freq: rotary / 2 float64 radians per position (a
  * scaling for long contexts is a choice of these and of amplitude). backward =
- * 1 applies the transposed map: with dY for X it gives dX. Angles are exact to
- * 2^-31 of a half turn for every int32 position; products are fp32, rounded once. Y
- * may be X itself (same strides) but must not otherwise overlap it.
+ * 1 applies the transposed map: with dY for X it gives dX. Angles are off by at
+ * most 1e-7 radians, whatever the int32 position; products are fp32, rounded once. Y may be X itself (same strides) but must not otherwise
+ * overlap it.
  * Stream-ordered; allocates nothing.
  */
 tg_status tg_rope(const void* X, int64_t x_token_stride, int64_t x_head_stride, void* Y, int64_t y_token_stride,

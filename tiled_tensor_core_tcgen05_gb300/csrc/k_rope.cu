@@ -6,8 +6,9 @@
 //
 // for the first `rotary` values of a head; the rest pass through. The gradient
 // is the transposed map, the same kernel with the sign of sin turned round.
-// Angles are exact fractions of a turn (tg_kv.cuh), products and sums are fp32,
-// and each value is rounded once to its 16-bit type.
+// Angles are computed as 64-bit fractions of a turn and off by at most 1e-7
+// radians (tg_kv.cuh), products and sums are fp32, and each value is rounded
+// once to its 16-bit type.
 //
 // Memory bounds it: every value is read and written once. A CTA takes a few
 // tokens, so that cos and sin, about forty instructions a pair, are computed

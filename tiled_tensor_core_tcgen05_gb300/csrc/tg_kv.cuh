@@ -63,7 +63,8 @@ __device__ __forceinline__ uint64_t turn_step(double radians_per_position) {
 // amplitude * (cos, sin) of the angle at `position`, sin negated for the backward rotation.
 __device__ __forceinline__ float2 turn_cos_sin(uint64_t step, int32_t position, float amplitude, float sign) {
     const uint64_t frac = step * static_cast<uint64_t>(static_cast<int64_t>(position));
-    // the top 32 bits, signed: [-1/2, 1/2) turn, to half turns for sincospi
+    // the top 32 bits, signed: [-1/2, 1/2) turn, to half turns for sincospi, in 24 bits: off by 2^-25 and
+    // the 2^-31 that the lower bits are worth, 1e-7 radians in all
     const float half_turns = static_cast<float>(static_cast<int32_t>(frac >> 32)) * 4.656612873077393e-10f;  // 2^-31
     float s, c;
     sincospif(half_turns, &s, &c);
