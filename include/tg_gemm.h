@@ -405,8 +405,8 @@ typedef enum {
  * the others are copied. inv_freq: rotary / 2 float64 radians per position (a
  * scaling for long contexts is a choice of these and of amplitude). backward =
  * 1 applies the transposed map: with dY for X it gives dX. Angles are off by at
- * most 1e-7 radians, whatever the int32 position; products are fp32, rounded once. Y may be X itself (same strides) but must not otherwise
- * overlap it.
+ * most 1e-7 radians, whatever the int32 position; products are fp32, rounded
+ * once. Y may be X itself (same strides) but must not otherwise overlap it.
  * Stream-ordered; allocates nothing.
  */
 tg_status tg_rope(const void* X, int64_t x_token_stride, int64_t x_head_stride, void* Y, int64_t y_token_stride,
@@ -429,7 +429,8 @@ tg_status tg_rope(const void* X, int64_t x_token_stride, int64_t x_head_stride, 
  * written takes over nothing of what it held. With rotary > 0 the keys are
  * rotated first, in fp32 and not rounded between, by their position (see
  * tg_rope), and with heads > 0 the queries Q too, into Q_out (Q itself, with
- * the same strides, is allowed). Results do not depend on timing.
+ * the same strides, is allowed, if it has no value in common with K and V, from
+ * which keys and values are read meanwhile). Results do not depend on timing.
  * Stream-ordered; allocates nothing.
  */
 tg_status tg_kv_append(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int64_t pages, int64_t kv_heads,

@@ -165,3 +165,28 @@ def test_reference_gradient_is_the_transpose():
             e[at] = 1e-4
             d = (ref.rope(x + e, pos, f, 1.3, inter)[0] - ref.rope(x - e, pos, f, 1.3, inter)[0]) / 2e-4
             assert abs((d * dy).sum() - dx[at]) < 1e-8
+
+
+# a scale tensor lies on the queries, so that every call is refused on the host, if not for the one reason then for the other
+PACKED = dict(q=Q, qo=Q, qt=48 * 128, qot=48 * 128, kt=48 * 128, vt=48 * 128, pages=1, vs=Q)
+
+
+@pytest.mark.parametrize("changes,meets", [
+    (dict(nk=Q + 32 * 256, nv=Q + 40 * 256), False),                                # queries, keys, values
+    (dict(nk=Q - 16 * 256, nv=Q - 8 * 256, vs=Q + 6 * 48 * 256), False),                                 # keys and values first
+    (dict(nk=Q + 31 * 256, nv=Q + 40 * 256), True),                                 # the last query head is the first key head
+    (dict(nk=Q + 32 * 256, nv=Q - 7 * 256, vs=Q + 290 * 256), True),
+    (dict(nk=Q + 32 * 256 + 2 * 48 * 256, nv=Q + 40 * 256), False),                 # keys of other tokens of the same tensor
+    (dict(nk=Q, kt=32 * 128, nv=NV, vs=Q + 236 * 256), True),                               # not slices of one tensor
+    (dict(heads=8, qh=384, qoh=384, qt=3200, qot=3200, kt=3200, vt=3200, kh=384, vh=384, nk=Q + 256, nv=Q + 512), False),  # head by head
+    (dict(heads=8, qh=384, qoh=384, qt=3200, qot=3200, kt=3200, vt=3200, kh=384, vh=384, nk=Q + 256, nv=Q + 254), True),
+    (dict(total=1, nk=Q + 32 * 256, nv=Q + 40 * 256), False),
+    (dict(total=1, nk=Q + 32 * 256 - 2, nv=Q + 40 * 256), True),
+])
+def test_queries_rotated_in_place_beside_keys(tg, changes, meets):
+    """The queries are written while keys and values are read: a value in common is refused."""
+    args = _args(APPEND, {**PACKED, **changes})
+    with pytest.raises(tg.TgError) as e:
+        tg.tg_kv_append(*args)
+    assert e.value.status == tg.ERR_INVALID_ARG
+    assert ("in common" if meets else "Q or Q_out overlaps the cache") in str(e.value)

@@ -1355,6 +1355,30 @@ bool rows_overlap(int64_t tokens, int64_t heads, int64_t dim, int64_t token_stri
     return !token_outer && !head_outer;
 }
 
+// Whether two strided tensors of the same tokens have an element in common. Slices of one packed projection have their
+// spans interleaved: there, one token's slices are compared.
+bool rows_meet(const void* a, int64_t a_heads, int64_t a_token, int64_t a_head, const void* b, int64_t b_heads, int64_t b_token, int64_t b_head,
+               int64_t tokens, int64_t dim) {
+    if (!overlaps(a, span_bytes(tokens, a_heads, dim, a_token, a_head), b, span_bytes(tokens, b_heads, dim, b_token, b_head))) return false;
+    const int64_t apart = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(b)) - static_cast<int64_t>(reinterpret_cast<uintptr_t>(a))) / 2;
+    const int64_t stride = tokens > 1 ? a_token : 0;
+    if (tokens > 1 && (a_token != b_token || stride == 0)) return true;  // not slices of one tensor
+    auto below = [&](int64_t x) { return (x % stride + stride) % stride; };
+    if (tokens > 1) {
+        const int64_t at = below(apart);
+        if (at >= (a_heads - 1) * a_head + dim && at + (b_heads - 1) * b_head + dim <= stride) return false;
+    }
+    for (int64_t i = 0; i < a_heads; ++i)
+        for (int64_t j = 0; j < b_heads; ++j) {
+            const int64_t d = apart + j * b_head - i * a_head;
+            if (d < dim && d > -dim) return true;
+            if (tokens == 1) continue;
+            const int64_t at = below(d);
+            if (at < dim || stride - at < dim) return true;
+        }
+    return false;
+}
+
 tg_status check_rope(const double* inv_freq, int64_t rotary, int64_t dim, int layout, double amplitude) {
     if (layout != TG_ROPE_HALF && layout != TG_ROPE_INTERLEAVED)
         return fail(TG_ERR_INVALID_ARG, "layout must be TG_ROPE_HALF (0) or TG_ROPE_INTERLEAVED (1), got %d", layout);
@@ -1506,6 +1530,9 @@ extern "C" tg_status tg_kv_append(void* k_cache, void* v_cache, float* k_scale, 
         if (!in_place && (overlaps(Q_out, o_bytes, Q, q_bytes) || overlaps(Q_out, o_bytes, K, k_bytes) ||
                           overlaps(Q_out, o_bytes, V, v_bytes)))
             return fail(TG_ERR_INVALID_ARG, "Q_out overlaps an input without being Q itself");
+        if (in_place && (rows_meet(Q, heads, q_token_stride, q_head_stride, K, kv_heads, k_token_stride, k_head_stride, total, dim) ||
+                         rows_meet(Q, heads, q_token_stride, q_head_stride, V, kv_heads, v_token_stride, v_head_stride, total, dim)))
+            return fail(TG_ERR_INVALID_ARG, "Q is rotated in place, but has values in common with K or V");
         for (int i = 0; i < 4; ++i)
             if (overlaps(Q_out, o_bytes, parts[i], part_bytes[i]) || overlaps(Q, q_bytes, parts[i], part_bytes[i]))
                 return fail(TG_ERR_INVALID_ARG, "Q or Q_out overlaps the cache");
