@@ -175,7 +175,7 @@ PACKED = dict(q=Q, qo=Q, qt=48 * 128, qot=48 * 128, kt=48 * 128, vt=48 * 128, pa
     (dict(nk=Q + 32 * 256, nv=Q + 40 * 256), False),                                # queries, keys, values
     (dict(nk=Q - 16 * 256, nv=Q - 8 * 256, vs=Q + 6 * 48 * 256), False),                                 # keys and values first
     (dict(nk=Q + 31 * 256, nv=Q + 40 * 256), True),                                 # the last query head is the first key head
-    (dict(nk=Q + 32 * 256, nv=Q - 7 * 256, vs=Q + 290 * 256), True),
+    (dict(nk=Q + 32 * 256, nv=Q - 7 * 256, vs=VS), True),
     (dict(nk=Q + 32 * 256 + 2 * 48 * 256, nv=Q + 40 * 256), False),                 # keys of other tokens of the same tensor
     (dict(nk=Q, kt=32 * 128, nv=NV, vs=Q + 236 * 256), True),                               # not slices of one tensor
     (dict(heads=8, qh=384, qoh=384, qt=3200, qot=3200, kt=3200, vt=3200, kh=384, vh=384, nk=Q + 256, nv=Q + 512), False),  # head by head
