@@ -406,7 +406,10 @@ def _binding():
     global _fast
     if _fast is None:
         import torch  # noqa: F401  its libraries, which the module needs
-        from . import _tg_torch
+        try:
+            from . import _tg_torch
+        except ImportError as e:
+            raise ImportError("the module of the tensor forms (_tg_torch.so) cannot be loaded: build again with this torch") from e
         _fast = _tg_torch
     return _fast
 

@@ -5,7 +5,8 @@ Each translation unit under csrc/ is compiled in parallel with nvcc
 library next to this file. No torch extension machinery: the library exports
 a plain C ABI (include/tg_gemm.h). Beside it a small CPython module,
 _tg_torch.so, holds the tensor forms of a serving step's calls
-(csrc/tg_torch.cpp, against torch's headers).
+(csrc/tg_torch.cpp, against torch's headers): it is left out where torch is not
+installed, which the library does not need, and built again for another torch.
 """
 from __future__ import annotations
 
@@ -23,6 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtg_gemm.so")
 BINDING = os.path.join(PKG, "_tg_torch.so")
+BINDING_FOR = os.path.join(OBJDIR, "tg_torch.for")
 # the debug build (device-side bounds checks, TG_DEBUG=1): same sources, its own objects
 OBJDIR_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libtg_gemm_debug.so")
@@ -50,18 +52,42 @@ def _inputs() -> list[str]:
     return files
 
 
+def _newest(made: str, inputs: list[str]) -> bool:
+    return os.path.exists(made) and all(os.path.getmtime(f) <= os.path.getmtime(made) for f in inputs)
+
+
 def up_to_date(lib: str = LIB) -> bool:
-    made = [lib] if lib != LIB else [LIB, BINDING]
-    if not all(os.path.exists(f) for f in made):
-        return False
-    t = min(os.path.getmtime(f) for f in made)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return _newest(lib, _inputs())
 
 
-def compile_binding(objdir: str) -> str:
-    """The CPython module's object file."""
+def torch_dir() -> str | None:
+    """Where torch (with CUDA) is installed."""
     import importlib.util
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    d = os.path.dirname(spec.origin)
+    return d if os.path.exists(os.path.join(d, "lib", "libc10_cuda.so")) else None
+
+
+def binding_for(torch_dir: str) -> str:
+    """What the module is built for: the interpreter and torch's place and version."""
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        return f"{sys.version}\n{torch_dir}\n{f.read()}"
+
+
+def binding_up_to_date(torch_dir: str) -> bool:
+    if not _newest(BINDING, [os.path.join(CSRC, "tg_torch.cpp"), os.path.join(INCLUDE, "tg_gemm.h"), os.path.abspath(__file__)]):
+        return False
+    try:
+        with open(BINDING_FOR) as f:
+            return f.read() == binding_for(torch_dir)
+    except FileNotFoundError:
+        return False
+
+
+def compile_binding(objdir: str, torch_dir: str) -> str:
+    """The CPython module's object file."""
     include = os.path.join(torch_dir, "include")
     obj = os.path.join(objdir, "tg_torch.o")
     home = os.path.dirname(os.path.dirname(nvcc()))
@@ -74,10 +100,9 @@ def compile_binding(objdir: str) -> str:
     return obj
 
 
-def link_binding(obj: str) -> None:
+def link_binding(obj: str, torch_dir: str) -> None:
     """Links the module with the library next to it and with torch."""
-    import importlib.util
-    lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+    lib = os.path.join(torch_dir, "lib")
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", obj, "-o", tmp, LIB, "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
            "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
@@ -85,6 +110,8 @@ def link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed for tg_torch.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(binding_for(torch_dir))
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None, debug: bool = False) -> str:
@@ -92,7 +119,10 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     device-side bounds checks); returns its path. Skips work when up to date."""
     lib_path = LIB_DEBUG if debug else LIB
     objdir = OBJDIR_DEBUG if debug else OBJDIR
-    if not force and not extra and up_to_date(lib_path):
+    torch = None if debug else torch_dir()
+    want_lib = force or bool(extra) or not up_to_date(lib_path)
+    want_binding = torch is not None and (force or not binding_up_to_date(torch))
+    if not want_lib and not want_binding:
         return lib_path
     os.makedirs(objdir, exist_ok=True)
     cc = nvcc()
@@ -111,16 +141,17 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = None if debug else ex.submit(compile_binding, objdir)
-        objs = list(ex.map(compile_one, SOURCES))
-    tmp = lib_path + f".tmp{os.getpid()}"
-    cmd = [cc, "-shared", "-o", tmp, "-Xlinker", f"-soname={os.path.basename(lib_path)}"] + objs + ARCH + ["-lineinfo"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, lib_path)
+        binding = ex.submit(compile_binding, objdir, torch) if want_binding else None
+        objs = list(ex.map(compile_one, SOURCES)) if want_lib else []
+    if want_lib:
+        tmp = lib_path + f".tmp{os.getpid()}"
+        cmd = [cc, "-shared", "-o", tmp, "-Xlinker", f"-soname={os.path.basename(lib_path)}"] + objs + ARCH + ["-lineinfo"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, lib_path)
     if binding is not None:
-        link_binding(binding.result())
+        link_binding(binding.result(), torch)
     return lib_path
 
 
