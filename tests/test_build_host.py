@@ -72,3 +72,11 @@ def test_another_torch_builds_the_module_again(made):
     install("two", "2.12")
     assert built() == ["tg_torch.o", "BINDING"]
     assert built() == []
+
+
+def test_the_package_keeps_to_public_torch():
+    package = os.path.join(ROOT, "tiled_tensor_core_tcgen05_gb300")
+    for name in os.listdir(package):
+        if name.endswith(".py"):
+            with open(os.path.join(package, name)) as f:
+                assert "torch._C" not in f.read(), name

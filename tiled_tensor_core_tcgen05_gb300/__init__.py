@@ -298,13 +298,10 @@ def tg_shutdown() -> None:
 # ---------------------------------------------------------------- torch form
 
 def _stream_handle(stream):
-    if stream is not None:
-        return stream.cuda_stream
     import torch
-    if not torch.cuda.is_initialized():
-        return torch.cuda.current_stream().cuda_stream
-    # the current stream's handle without the object around it
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream
 
 
 def _dev_fp16(t, name):
