@@ -190,3 +190,11 @@ def test_queries_rotated_in_place_beside_keys(tg, changes, meets):
         tg.tg_kv_append(*args)
     assert e.value.status == tg.ERR_INVALID_ARG
     assert ("in common" if meets else "Q or Q_out overlaps the cache") in str(e.value)
+
+
+def test_binding_refuses_tensors_of_another_device(tg):
+    """Every tensor of a call goes through this check with the current device."""
+    check = tg._binding().check_device
+    assert check(0, 0, "Q") is None and check(3, 3, "Q") is None
+    with pytest.raises(ValueError, match="Q is on cuda:1, but the current device is cuda:0"):
+        check(1, 0, "Q")

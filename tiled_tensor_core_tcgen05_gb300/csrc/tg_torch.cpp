@@ -45,8 +45,18 @@ const at::Tensor& tensor(PyObject* x, const char* name) {
     return THPVariable_Unpack(x);
 }
 
+// The kernels run on the current device, with its stream: tensors of another one are not reached from there.
+void check_device(int64_t has, int64_t current, const char* name) {
+    if (has != current)
+        value_error(std::string(name) + " is on cuda:" + std::to_string(has) + ", but the current device is cuda:" + std::to_string(current));
+}
+
+thread_local int t_device = -1;  // the current device, once a call has asked
+
 void on_cuda(const at::Tensor& t, const char* name) {
     if (!t.is_cuda()) type_error(std::string(name) + " must be a CUDA tensor");
+    if (t_device < 0) t_device = c10::cuda::current_device();
+    check_device(t.get_device(), t_device, name);
 }
 
 int64_t integer(PyObject* x) {
@@ -100,6 +110,7 @@ const double* frequencies(PyObject* x, int64_t* rotary) {
     const at::Tensor& t = tensor(x, "inv_freq");
     if (t.scalar_type() != at::kDouble || !t.is_cuda() || t.dim() != 1 || !t.is_contiguous())
         type_error("inv_freq must be a contiguous CUDA float64 vector (radians per position of each pair)");
+    on_cuda(t, "inv_freq");
     *rotary = 2 * t.size(0);
     return static_cast<const double*>(t.data_ptr());
 }
@@ -132,8 +143,8 @@ struct Cache {
 };
 
 // A cache's tensors k, v, k_scale, v_scale, looked at in every call: their storage may have been exchanged or resized
-// since the last one.
-Cache cache_of(PyObject* const* a) {
+// since the last one. A cache may be made while another device is the current one.
+Cache cache_of(PyObject* const* a, bool making) {
     static const char* names[4] = {"k", "v", "k_scale", "v_scale"};
     const at::Tensor* t[4];
     for (int i = 0; i < 4; ++i) t[i] = &tensor(a[i], names[i]);
@@ -148,7 +159,9 @@ Cache cache_of(PyObject* const* a) {
             value_error("scales must have shape (" + std::to_string(t[0]->size(0)) + ", " + std::to_string(t[0]->size(1)) + ")");
     }
     for (int i = 0; i < 4; ++i) {
-        on_cuda(*t[i], names[i]);
+        if (!making) on_cuda(*t[i], names[i]);
+        else if (!t[i]->is_cuda()) type_error(std::string(names[i]) + " must be a CUDA tensor");
+        else if (t[i]->get_device() != t[0]->get_device()) value_error("the cache's tensors must be on one device");
         if (!t[i]->is_contiguous()) value_error(std::string(names[i]) + " must be contiguous");
     }
     return Cache{t[0]->data_ptr(), t[1]->data_ptr(), static_cast<float*>(t[2]->data_ptr()), static_cast<float*>(t[3]->data_ptr()), t[0]->size(0),
@@ -159,7 +172,7 @@ Cache cache_of(PyObject* const* a) {
 Cache cache(PyObject* t) {
     if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 4) type_error("cache must be a KvCache");
     PyObject* const a[4] = {PyTuple_GET_ITEM(t, 0), PyTuple_GET_ITEM(t, 1), PyTuple_GET_ITEM(t, 2), PyTuple_GET_ITEM(t, 3)};
-    return cache_of(a);
+    return cache_of(a, false);
 }
 
 struct Batch {
@@ -184,6 +197,7 @@ Batch batch(PyObject* table, PyObject* lens, PyObject* cu) {
 template <typename F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F body) {
     HANDLE_TH_ERRORS
+    t_device = -1;
     if (n != want) {
         PyErr_Format(PyExc_TypeError, "%zd arguments wanted, got %zd", want, n);
         return nullptr;
@@ -239,7 +253,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (k, v, k_scale, v_scale) -> what KvCache keeps
 PyObject* cache_args(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 4, [&]() -> PyObject* {
-        cache_of(a);
+        cache_of(a, true);
         return PyTuple_Pack(4, a[0], a[1], a[2], a[3]);
     });
 }
@@ -349,6 +363,7 @@ PyObject* attention_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor& O = a[11] == Py_None ? made : tensor(a[11], "out");
         if (O.sizes() != Q.sizes() || O.scalar_type() != Q.scalar_type() || !O.is_cuda() || !O.is_contiguous())
             value_error("out must be a contiguous CUDA tensor of Q's shape and type");
+        on_cuda(O, "out");
         if (want_lse) lse = at::empty({T, H}, Q.options().dtype(at::kFloat));
         if (need > 0) work = at::empty({need}, Q.options().dtype(at::kByte));
         void *po = O.data_ptr(), *pw = need > 0 ? work.data_ptr() : nullptr;
@@ -370,7 +385,18 @@ PyObject* attention_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// (device that a tensor has, current device, name): the check above, for a machine with one
+PyObject* check_device_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 3, [&]() -> PyObject* {
+        const char* name = PyUnicode_AsUTF8(a[2]);
+        if (name == nullptr) return nullptr;
+        check_device(integer(a[0]), integer(a[1]), name);
+        Py_RETURN_NONE;
+    });
+}
+
 PyMethodDef methods[] = {
+    {"check_device", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(check_device_py)), METH_FASTCALL, nullptr},
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope)), METH_FASTCALL, nullptr},
     {"cache_args", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_args)), METH_FASTCALL, nullptr},
     {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_append)), METH_FASTCALL, nullptr},
