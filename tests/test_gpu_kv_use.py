@@ -183,3 +183,36 @@ def test_append_with_the_second_of_three_pages_out_of_range(tg, entry, rotate):
     if rotate:
         assert torch.equal(*outs)
     _status_ok(tg)
+
+
+# ---------------------------------------------------------------- what torch is told
+
+def test_tensors_that_are_overwritten_say_so(tg):
+    cache = _filled(tg)
+    k, q = torch.randn(1, 2, 64).half().cuda(), torch.randn(1, 4, 64).half().cuda()
+    f, _ = tg.rope_frequencies(64)
+    table, lens = _ints([[0, 1]]), _ints([3])
+
+    def bumped(call, changed, kept):
+        before = [x._version for x in (*changed, *kept)]
+        call()
+        after = [x._version for x in (*changed, *kept)]
+        assert [a > b for a, b in zip(after, before)] == [True] * len(changed) + [False] * len(kept)
+
+    pair = (torch.empty_like(k), torch.empty_like(k))
+    o = torch.empty_like(q)
+    bumped(lambda: tg.kv_append(cache, k, k, table, lens, Q=q, inv_freq=f, out=q), (*cache.args, q), (k, table, lens, f))
+    bumped(lambda: tg.kv_append(cache, k, k, table, lens, Q=q, inv_freq=f), cache.args, (k, q))
+    bumped(lambda: tg.rope(q, lens, f, out=q), (q,), (lens, f))
+    bumped(lambda: tg.rope(q, lens, f), (), (q, lens, f))
+    bumped(lambda: tg.kv_read(cache, table, lens, None, 1, out=pair), pair, cache.args)
+    bumped(lambda: tg.attention_kv(q, cache, table, lens, out=o), (o,), (q, *cache.args))
+    x = torch.randn(1, 4, 64, device="cuda", requires_grad=True)
+    y = x.half().exp()   # the gradient of exp reads its output
+    tg.rope(y.detach(), lens, f, out=y.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    with torch.inference_mode():
+        frozen = _filled(tg)
+    tg.kv_append(frozen, k, k, table, lens)  # tensors that torch keeps no account of
+    _status_ok(tg)

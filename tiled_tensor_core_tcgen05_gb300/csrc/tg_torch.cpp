@@ -220,6 +220,15 @@ PyObject* answer(F call, R result) {
     return status == TG_OK ? result() : PyLong_FromLong(status);
 }
 
+// What torch keeps account of when a tensor is overwritten: a backward pass that saved it says so instead of reading
+// other values.
+void written(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(PyObject* x) {
+    if (x != Py_None) written(tensor(x, "out"));
+}
+
 PyObject* same(PyObject* x) {
     Py_INCREF(x);
     return x;
@@ -246,7 +255,10 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Rows y = rows(Y, "out");
         return answer(
             [&] { return tg_rope(x.p, x.token, x.head, y.p, y.token, y.head, pos, T, H, D, freq, rotary, amplitude, layout, backward, dtype, where.handle); },
-            [&] { return made.defined() ? THPVariable_Wrap(std::move(made)) : same(a[6]); });
+            [&] {
+                written(a[6]);
+                return made.defined() ? THPVariable_Wrap(std::move(made)) : same(a[6]);
+            });
     });
 }
 
@@ -301,7 +313,11 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                     b.lens, b.cu, b.batch, T, max_new, freq, rotary, amplitude, layout, q.p, q.token, q.head, qo.p, qo.token, qo.head, heads, dtype,
                                     where.handle);
             },
-            [&] { return made.defined() ? THPVariable_Wrap(std::move(made)) : same(a[11]); });
+            [&] {
+                for (int i = 0; i < 4; ++i) written(PyTuple_GET_ITEM(a[0], i));
+                written(a[11]);
+                return made.defined() ? THPVariable_Wrap(std::move(made)) : same(a[11]);
+            });
     });
 }
 
@@ -332,6 +348,8 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
         return answer(
             [&] { return tg_kv_read(c.k, c.v, c.ks, c.vs, c.pages, c.kv_heads, c.page, c.dim, c.format, b.table, b.width, b.lens, b.cu, b.batch, total, to[0], to[1], dtype, where.handle); },
             [&]() -> PyObject* {
+                written(a[6]);
+                written(a[7]);
                 PyObject* pair = PyTuple_New(2);
                 for (int i = 0; pair != nullptr && i < 2; ++i)
                     PyTuple_SET_ITEM(pair, i, made[i].defined() ? THPVariable_Wrap(std::move(made[i])) : same(a[6 + i]));
@@ -374,6 +392,7 @@ PyObject* attention_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                        b.cu, b.batch, T, H, max_new, max_len, causal, window, scale, dtype, pw, need, where.handle);
             },
             [&]() -> PyObject* {
+                written(a[11]);
                 PyObject* o = made.defined() ? THPVariable_Wrap(std::move(made)) : same(a[11]);
                 if (!want_lse || o == nullptr) return o;
                 PyObject* pair = PyTuple_New(2);
