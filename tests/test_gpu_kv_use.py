@@ -216,3 +216,44 @@ def test_tensors_that_are_overwritten_say_so(tg):
         frozen = _filled(tg)
     tg.kv_append(frozen, k, k, table, lens)  # tensors that torch keeps no account of
     _status_ok(tg)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("backward", [False, True])
+def test_rope_has_a_gradient(tg, interleaved, backward):
+    """The gradient of a weighted sum is the transposed rotation of the weights, and so are those of slices, of a plain
+    sum (whose gradient is one value, spread) and on another stream."""
+    g = torch.Generator().manual_seed(6)
+    packed = torch.randn(5, 6, 64, generator=g).half().cuda().requires_grad_()
+    w = torch.randn(5, 4, 64, generator=g).half().cuda()
+    pos = _ints([3, 1, 4, 1, 5])
+    f, _ = tg.rope_frequencies(32)
+    how = dict(amplitude=1.25, layout=tg.ROPE_INTERLEAVED if interleaved else tg.ROPE_HALF)
+
+    def gradient(weight, stream=None):
+        y = tg.rope(packed[:, 1:5], pos, f, backward=backward, stream=stream, **how)
+        assert y.requires_grad and torch.equal(y, tg.rope(packed.detach()[:, 1:5], pos, f, backward=backward, **how))
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(stream)
+        (d,) = torch.autograd.grad((y * weight).sum() if weight is not None else y.sum(), packed)
+        assert (d[:, [0, 5]] == 0).all()
+        return d[:, 1:5]
+
+    want = tg.rope(w, pos, f, backward=not backward, **how)
+    assert torch.equal(gradient(w), want)
+    assert torch.equal(gradient(None), tg.rope(torch.ones_like(w), pos, f, backward=not backward, **how))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert torch.equal(gradient(w, side), want)
+    x = packed[:, 1:5]
+    with pytest.raises(RuntimeError, match="no gradient"):
+        tg.rope(x, pos, f, out=torch.empty_like(x))
+    with torch.no_grad():
+        assert not tg.rope(x, pos, f).requires_grad
+    # the gradient's own gradient: the map is linear, so that of <w, rope(x)> by w is rope(x)
+    w.requires_grad_()
+    y = tg.rope(packed[:, 1:5], pos, f, backward=backward, **how)
+    (d,) = torch.autograd.grad(y, packed, w, create_graph=True)
+    (dw,) = torch.autograd.grad(d, w, packed.detach())
+    assert torch.equal(dw, y)
+    _status_ok(tg)

@@ -458,13 +458,48 @@ def rope_frequencies(rotary: int, base: float = 10000.0, scaling: str = "none", 
     return freq.to(device), amplitude
 
 
+_rope_function = None
+
+
+def _rope_with_gradient(*args):
+    """rope as a step of torch's graph: its gradient is the transposed rotation, with the same positions."""
+    global _rope_function
+    import torch
+    if _rope_function is None:
+        class Rope(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, X, positions, inv_freq, amplitude, layout, backward):
+                ctx.save_for_backward(positions, inv_freq)
+                ctx.how = amplitude, layout, backward
+                return _answer((_fast or _binding()).rope(X, positions, inv_freq, amplitude, layout, backward, None, None))
+
+            @staticmethod
+            def backward(ctx, dY):
+                positions, inv_freq = ctx.saved_tensors
+                amplitude, layout, backward = ctx.how
+                # a gradient may be spread over its last dimension (that of a sum is one value)
+                dY = dY if dY.stride(-1) == 1 else dY.contiguous()
+                return rope(dY, positions, inv_freq, amplitude, layout, not backward), None, None, None, None, None
+        _rope_function = Rope
+    *args, out, stream = args
+    if out is not None:
+        raise RuntimeError("rope with out= has no gradient, but X requires one: leave out out=, or call it under torch.no_grad()")
+    with torch.cuda.stream(stream):  # None: the current one. The graph takes the gradient on the same stream
+        return _rope_function.apply(*args)
+
+
 def rope(X, positions, inv_freq, amplitude: float = 1.0, layout: int = ROPE_HALF, backward: bool = False, out=None,
          stream=None):
     """Rotary positions on X (tokens, heads, dim), float16 or bfloat16: the first 2 * len(inv_freq)
     values of each head turned in pairs by positions[token] * inv_freq[pair] and multiplied by
     ``amplitude``, the others copied. ``positions`` int32, ``inv_freq`` float64 (see
     ``rope_frequencies``). ``backward``: the transposed map, which takes the output's gradient to
-    the input's. ``out`` may be X. X and out may be slices (contiguous in dim)."""
+    the input's. ``out`` may be X. X and out may be slices (contiguous in dim). Where X requires a gradient it gets
+    one, by the transposed map (not with ``out``)."""
+    if getattr(X, "requires_grad", False):
+        import torch
+        if torch.is_grad_enabled():
+            return _rope_with_gradient(X, positions, inv_freq, amplitude, layout, backward, out, stream)
     return _answer((_fast or _binding()).rope(X, positions, inv_freq, amplitude, layout, backward, out, stream))
 
 
@@ -511,7 +546,7 @@ def kv_append(cache, K, V, table, lens, cu=None, max_new: int = 1, Q=None, inv_f
     positions lens[i] .. of the pages in its row of ``table``. lens: int32 tokens held before the call;
     max_new: no sequence has more rows (one that does is left out, and ``tg_device_status`` says so). With ``inv_freq`` the keys are rotated first by their
     positions (see ``rope``), and the queries Q (total, heads, dim), if given, too: returns them
-    (``out``, which may be Q; rows that no sequence has as they are), else None. The scales and roundings are in include/tg_gemm.h."""
+    (``out``, which may be Q; rows that no sequence has as they are), else None. No gradient is recorded. The scales and roundings are in include/tg_gemm.h."""
     return _answer((_fast or _binding()).kv_append(cache.args, K, V, table, lens, cu, max_new, Q, inv_freq, amplitude,
                                                    layout, out, stream))
 
@@ -538,6 +573,7 @@ def attention_kv(Q, cache, table, lens, cu=None, max_new: int = 1, max_len: int 
     last so many. max_new and max_len bound the rows and the length of a sequence (max_len None: what
     the table can hold). scale None: 1 / sqrt(dim). Rows that see nothing, and rows that no sequence has,
     give zeros; so do those of a sequence beyond either bound, and ``tg_device_status`` says so. Returns O (total,
-    heads, dim), with ``return_lse`` also the float32 log of each row's sum (total, heads)."""
+    heads, dim), with ``return_lse`` also the float32 log of each row's sum (total, heads). No gradient is
+    recorded."""
     return _answer((_fast or _binding()).attention_kv(Q, cache.args, table, lens, cu, max_new, max_len, causal, window,
                                                       scale, return_lse, out, stream))
