@@ -257,3 +257,16 @@ def test_rope_has_a_gradient(tg, interleaved, backward):
     (dw,) = torch.autograd.grad(d, w, packed.detach())
     assert torch.equal(dw, y)
     _status_ok(tg)
+
+
+def test_layouts_are_not_cut_to_32_bits(tg):
+    x, pos = torch.zeros(1, 1, 64).half().cuda(), _ints([0])
+    f, _ = tg.rope_frequencies(64)
+    for layout in (1 << 32, -(1 << 32) + 1):
+        with pytest.raises(ValueError, match="layout"):
+            tg.rope(x, pos, f, layout=layout)
+        with pytest.raises(ValueError, match="layout"):
+            tg.kv_append(_filled(tg, kv=1), x, x, _ints([[0]]), pos, inv_freq=f, layout=layout)
+    for layout in (2, -1):
+        with pytest.raises(tg.TgError, match="layout"):
+            tg.rope(x, pos, f, layout=layout)

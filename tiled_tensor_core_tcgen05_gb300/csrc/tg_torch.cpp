@@ -65,6 +65,13 @@ int64_t integer(PyObject* x) {
     return v;
 }
 
+// One of the C ABI's int arguments.
+int small(PyObject* x, const char* name) {
+    const int64_t v = integer(x);
+    if (v != static_cast<int>(v)) value_error(std::string(name) + " is out of range: " + std::to_string(v));
+    return static_cast<int>(v);
+}
+
 double real(PyObject* x) {
     const double v = PyFloat_AsDouble(x);
     if (v == -1.0 && PyErr_Occurred()) throw Refused{};
@@ -245,7 +252,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t T = X.size(0), H = X.size(1), D = X.size(2);
         const int32_t* pos = ints(a[1], "positions", T);
         const double amplitude = real(a[3]);
-        const int layout = static_cast<int>(integer(a[4])), backward = truth(a[5]);
+        const int layout = small(a[4], "layout"), backward = truth(a[5]);
         const Where where(a[7]);
         at::Tensor made;
         if (a[6] == Py_None) made = at::empty({T, H, D}, X.options());
@@ -286,7 +293,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int64_t rotary = 0;
         const double* freq = a[8] == Py_None ? nullptr : frequencies(a[8], &rotary);
         const double amplitude = real(a[9]);
-        const int layout = static_cast<int>(integer(a[10]));
+        const int layout = small(a[10], "layout");
         const Where where(a[12]);
         at::Tensor made;
         Rows q, qo;
