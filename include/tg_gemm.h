@@ -362,6 +362,9 @@ tg_status tg_softmax_rows(const void* X, void* Y, int64_t M, int64_t N, tg_strea
  *
  * A code q of page p, head h stands for value(q) * scale[p][h], value() being
  * e4m3 (TG_KV_E4M3, largest 448) or two's complement (TG_KV_INT8, -127..127).
+ * Scales that an append writes are at least 2^-60. Scales made elsewhere must not
+ * be negative; to the attention, a value scale below 2^-60 is one of 2^-60, and a
+ * NaN one makes values of NaN.
  *
  * The batch. Sequence i's pages are table[i * table_width + 0, 1, ..], in
  * order. Packed tensors hold the sequences' new tokens one after another,

@@ -2,6 +2,8 @@
 import pytest
 import torch
 
+from tests import test_gpu_attention_kv as attend
+
 pytestmark = pytest.mark.gpu
 
 
@@ -270,3 +272,15 @@ def test_layouts_are_not_cut_to_32_bits(tg):
     for layout in (2, -1):
         with pytest.raises(tg.TgError, match="layout"):
             tg.rope(x, pos, f, layout=layout)
+
+
+# ---------------------------------------------------------------- scales that no append writes
+
+@pytest.mark.parametrize("most", [1, 4, 70])
+@pytest.mark.parametrize("which", [2, 3])
+def test_a_scale_that_is_nan_reaches_the_rows_that_see_it(tg, most, which):
+    cache, host, table, q = attend._case(tg, [most, most], [most + 90, most + 90], 16, 2, 4, 64, 0, 0, seed=42, garbage=False)
+    cache.args[which][int(table[0, 3]), 1] = torch.nan
+    out = tg.attention_kv(q.cuda(), cache, table.cuda(), _ints([most + 90] * 2), _ints([0, most, 2 * most]), max_new=most, max_len=most + 90)
+    assert out[:most, 4:].isnan().all() and not out[:most, :4].isnan().any() and not out[most:].isnan().any()
+    _status_ok(tg)

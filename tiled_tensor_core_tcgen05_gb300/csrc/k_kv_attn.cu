@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const int64_t ph = static_cast<int64_t>(max(p, 0)) * c.cache.kv_heads + head;
             ks = p >= 0 ? __ldg(c.cache.k_scale + ph) : 0.0f;
             const float vs = p >= 0 ? max_nan(__ldg(c.cache.v_scale + ph), kScaleFloor) : 1.0f;
-            lv = lg2_approx(vs);
+            lv = lg2_approx(vs);  // both are off by 2^-22, far below the rounding of the weights
             iv = rcp_approx(vs);
         };
         // the watchdog's test hook: the first step of a CTA never arrives

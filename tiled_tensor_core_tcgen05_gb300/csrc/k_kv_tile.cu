@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float* y = x + 16 * b;
                         const float u = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]), max3(y[6], y[7], y[8]));
                         const float v = max3(max3(y[9], y[10], y[11]), max3(y[12], y[13], y[14]), y[15]);
-                        top = fmaxf(top, fmaf(fmaxf(u, v), fmaxf(f * info.ks[4 * kh + 2 * q + b], 1e-38f), info.lv[4 * kh + 2 * q + b]));
+                        top = fmaxf(top, fmaf(fmaxf(u, v), max_nan(f * info.ks[4 * kh + 2 * q + b], 1e-38f), info.lv[4 * kh + 2 * q + b]));
                     }
                 }
                 red[ph * 4 * kHalfRows + kh * kHalfRows] = top;
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float2 cb[2], ob[2];
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const float cc = fmaxf(f * info.ks[4 * kh + 2 * q + b], 1e-38f), oo = info.lv[4 * kh + 2 * q + b] - m;
+                        const float cc = max_nan(f * info.ks[4 * kh + 2 * q + b], 1e-38f), oo = info.lv[4 * kh + 2 * q + b] - m;
                         cb[b] = make_float2(cc, cc);
                         ob[b] = make_float2(oo, oo);
                     }
