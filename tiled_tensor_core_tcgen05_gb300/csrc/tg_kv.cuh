@@ -191,21 +191,8 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     return y;
 }
 
-// x (in units of the scale) to the nearest code, ties to even; beyond the
+// Four codes, the first in the low byte: x (in units of the scale) to the nearest code, ties to even; beyond the
 // largest code it saturates. A NaN stays one in e4m3 and becomes 0 in int8.
-template <int kFmt>
-__device__ __forceinline__ uint8_t encode(float x) {
-    if constexpr (kFmt == kKvE4M3) {
-        uint16_t two;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(x));
-        return static_cast<uint8_t>(two);
-    } else {
-        const float c = fminf(fmaxf(rintf(x), -127.0f), 127.0f);
-        return static_cast<uint8_t>(x == x ? static_cast<int>(c) : 0);
-    }
-}
-
-// Four codes, the first in the low byte.
 template <int kFmt>
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
     if constexpr (kFmt == kKvE4M3) {
@@ -265,17 +252,6 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
         x[1] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441)) - 8388736.0f;
         x[2] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)) - 8388736.0f;
         x[3] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443)) - 8388736.0f;
-    }
-}
-
-template <int kFmt>
-__device__ __forceinline__ float decode(uint8_t code) {
-    if constexpr (kFmt == kKvE4M3) {
-        uint32_t h2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(code)));
-        return __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xFFFFu)));
-    } else {
-        return static_cast<float>(static_cast<int8_t>(code));
     }
 }
 
