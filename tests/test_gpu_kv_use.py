@@ -1,4 +1,6 @@
 """GPU checks of how the cache operators' tensor forms treat what a program does around them."""
+import copy
+
 import pytest
 import torch
 
@@ -42,6 +44,15 @@ def test_a_cache_keeps_its_tensors(tg):
             delattr(cache, name)
     assert (cache.pages, cache.kv_heads, cache.page, cache.dim, cache.fmt) == (4, 2, 16, 64, tg.KV_INT8)
     assert tg.KvCache.empty(1, 1).fmt == tg.KV_E4M3
+
+
+def test_a_cache_can_be_copied(tg):
+    cache = _filled(tg)
+    same, other = copy.copy(cache), copy.deepcopy(cache)
+    assert all(a is b for a, b in zip(same.args, cache.args))
+    other.k.zero_()
+    assert (cache.k != 0).any() and torch.equal(other.v, cache.v) and other.v.data_ptr() != cache.v.data_ptr()
+    assert (tg.kv_read(other, _ints([[0]]), _ints([0]), _ints([0, 9]), 9)[0] == 0).all()
 
 
 def test_a_cache_whose_storage_was_exchanged(tg):

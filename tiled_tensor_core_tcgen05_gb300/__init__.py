@@ -521,6 +521,9 @@ class KvCache:
     def __delattr__(self, name):
         raise AttributeError(f"a KvCache's {name} cannot be deleted")
 
+    def __reduce__(self):  # copies are made from the tensors
+        return KvCache, self.args
+
     k = property(lambda self: self.args[0])
     v = property(lambda self: self.args[1])
     k_scale = property(lambda self: self.args[2])
