@@ -23,8 +23,10 @@
 // where its bytes take 15.7: conversion, rounding and addresses fill the issue slots.
 // With rotation, and 32 heads of queries, e4m3, pages of 64: 87 us where the bytes take
 // 58: keys 30, values 17 and queries 44 by themselves.
-// One token each of 256 sequences, rotated: 7.2 us, five dependent reads. Reading
-// back 890 MB: 134 us, 6.6 TB/s or 0.98 of the copy rate.
+// One token each of 256 sequences, rotated: 7.5 us where no page's scale grows, 11.9 where
+// every one does; 1024 sequences 23 and 47. A CTA's five dependent reads are paid for every
+// wave of CTAs, and 512 threads of 115 to 128 registers let one CTA on an SM. Reading back
+// 890 MB: 134 us, 6.6 TB/s or 0.98 of the copy rate.
 #include "tg_rope.cuh"
 
 #include <type_traits>

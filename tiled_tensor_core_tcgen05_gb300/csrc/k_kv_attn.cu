@@ -39,9 +39,9 @@
 // tokens are given to MMA rows (mma_token) keep those reads free of bank
 // conflicts.
 //
-// Measured (one GB300): 64 ragged sequences of up to 8192, 32 heads over 8 of 128, 630 MB of cache, 109 us,
-// 5.8 TB/s or 0.85 of the copy rate; four sequences of up to 131071, 105 us, 0.83. What is missing is the
-// start (lengths, shares, first pages: three dependent reads) and the join. One token over 1023: 8.5 us,
+// Measured (one GB300, in a graph): 64 ragged sequences of up to 8192, 32 heads over 8 of 128, 630 MB of cache, 110 us,
+// 5.7 TB/s or 0.84 of the copy rate; four sequences of up to 131071, 104 us, 0.84. What is missing is the
+// start (lengths, shares, first pages: three dependent reads) and the join. One token over 1023: 8.6 us,
 // all of it latency of the two kernels.
 #include "tg_device.cuh"
 #include "tg_kv_split.cuh"
@@ -628,8 +628,10 @@ FewPlan few_plan(const KvAttnCall& c, int sm_count) {
 
 // Rows of one kv head up to which a call runs here; above, k_kv_tile.cu takes it. Measured in us, here and there,
 // with 32 heads over 8: 32 sequences of 2000, 36 rows 44 and 85, 64 rows 56 and 91, 96 rows 81 and 91, 128 rows 94
-// and 99, 192 rows 140 and 103; four of 30000, 64 rows 88 and 105, 96 rows 129 and 108. Only calls too small to
-// fill the GPU are still quicker here beyond it: two of 2000, 128 rows 21 and 27, 256 rows 27 and 34.
+// and 99, 192 rows 140 and 103; four of 30000, 64 rows 88 and 105, 96 rows 129 and 108. Up to 64 rows this kernel is
+// the quicker one throughout. From there to 128 it depends on the lengths, by up to a fifth either way, and
+// calls too small to fill the GPU stay quicker here further on (two of 2000, 128 rows 21 and 27, 256 rows 27 and
+// 34): the rule does not look at either.
 bool few_rows(const KvAttnCall& c) { return static_cast<int64_t>(c.batch.max_new) * (c.heads / c.cache.kv_heads) <= 64; }
 
 template <typename E, int kFmt, int kDim, int kTiles>

@@ -23,9 +23,13 @@
 // half's weights begin to arrive, so that one half's MMAs lie beside the other's
 // exponentials.
 //
-// Measured (one GB300): chunks of up to 4096 new tokens on 8192, 32 heads over 8 of 128, causal: 656 us, 775 TFLOP/s or
-// 0.42 of the dense rate. MMAs of M = 128, N = 128 and fp16 operands take 104 (scores) and 93 (product) cycles where
-// the dense rate has 64, and about 600 cycles of a half's chain are hand-overs that the other half does not fill.
+// Measured (one GB300): chunks of up to 4096 new tokens on 8192, 32 heads over 8 of 128, causal: 669 us, 760 TFLOP/s or
+// 0.39 of the dense rate; the tensor pipe is active 36 % of the cycles. MMAs of M = 128, N = 128 and fp16 operands take
+// 104 (scores) and 93 (product) cycles where the dense rate has 64, which alone would leave 65 %: the attention
+// over 16-bit keys (k_attn.cu) has the same MMAs and reaches 1118 TFLOP/s. What is different here: every tile of
+// codes is turned into fp16 again for each block of 256 rows that sees it, by four warps and through a ring of its
+// own, which leaves shared memory for two stages of keys and values and 80 to 96 registers for the softmax (about
+// 100 bytes spilled); and some 600 cycles of a half's chain are hand-overs that the other half does not fill.
 #include "tg_device.cuh"
 #include "tg_kv_split.cuh"
 

@@ -15,8 +15,8 @@
 // once for all heads of a token (in shared memory, two arrays so that a
 // thread's eight of each are two 16-byte reads), and each thread's loads are
 // under way before it computes them. Measured: 8192 tokens of 40 heads of 128,
-// 28.7 us, 5.9 TB/s or 0.86 of the copy rate; 4099 of 32 heads, 64 of 128
-// values turned, interleaved, 12.5 us, 0.79; one token 2.3 us. A CTA a token
+// 28.3 us, 5.9 TB/s or 0.87 of the copy rate; 4099 of 32 heads, 64 of 128
+// values turned, interleaved, 14.2 us, 0.70; one token 2.3 us. A CTA a token
 // (cos and sin in waits of their own): 36 and 18.5 us.
 #include "tg_rope.cuh"
 
