@@ -158,6 +158,22 @@ def test_small_weights_under_large_ones_count(tg, batch, most, ct):
     ref.near(lse[:, 0], l.cpu(), (ds + L * 2.0 ** -24 + 2.0 ** -21 * (1 + l.abs())).cpu())
 
 
+@pytest.mark.parametrize("most", [1, 5, 70])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_log_of_the_sum_of_equal_weights(tg, most, dim):
+    """With a scale of 0 the log of a row's sum is that of the number of its keys, whatever the value scales that the weights
+    carry: within the reference's tolerance, of roundings of numbers below 16 and one unit of 2^-24 a key."""
+    lens = [most, most + 1, most + 29, most + 200, most + 3000]
+    for ct in (0, 1):
+        cache, host, table, q = attend._case(tg, [most] * 5, lens, 16, 2, 3, dim, ct, 1, seed=45, garbage=False)
+        cu = [most * i for i in range(6)]
+        out, lse = tg.attention_kv(q.cuda(), cache, table.cuda(), _ints(lens), _ints(cu), max_new=most, max_len=max(lens), scale=0.0, return_lse=True)
+        attend._check(out, lse, host, table, q, [most] * 5, lens, 16, True, 0, 0.0)
+        keys = torch.cat([torch.arange(n - most + 1, n + 1) for n in lens]).double()
+        ref.near(lse, keys.log()[:, None].expand(-1, 6), (2.0 ** -20 + keys * 2.0 ** -24 + 2.0 ** -21 * keys.log())[:, None])
+    _status_ok(tg)
+
+
 # ---------------------------------------------------------------- waits that run out
 
 def _times_out_and_recovers(tg, counts, lens, share, dim, max_len):

@@ -129,8 +129,14 @@ constexpr int kStep = 16;  // tokens a box of the cache's tensor maps
 // 1 / a row's sum; 0 for a row that sees nothing.
 __device__ __forceinline__ float row_inverse(float l) { return l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l); }
 
-// The natural log of a row's sum l at the reference m (base 2).
-__device__ __forceinline__ float row_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * (1.0f / kLog2e); }
+// The natural log of a row's sum l at the reference m (base 2). The sum's exponent goes to m first: the two are of
+// about the same size and opposite signs where scores are small, and log2f(l) would be rounded at that size.
+__device__ __forceinline__ float row_lse(float m, float l) {
+    if (l == 0.0f) return -INFINITY;
+    const int bits = __float_as_int(l), e = (bits >> 23) - 127;
+    if (e <= -127 || e >= 128) return (m + log2f(l)) * (1.0f / kLog2e);  // not an ordinary positive number
+    return (m + static_cast<float>(e) + log2f(__int_as_float((bits & 0x7FFFFF) | 0x3F800000))) * (1.0f / kLog2e);
+}
 
 // Row r of the outputs as that of a token that sees nothing: whole block.
 template <typename E, int kDim>
