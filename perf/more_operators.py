@@ -359,7 +359,7 @@ def _branch(s):
     wanted = (at >= start[:, None]) & (at < end[:, None])
     got = torch.where(wanted & (place < free.sum()), order[place.clamp(0, pages - 1).long()], -1)
     new = torch.where(wanted, got, new)
-    spare = (free.sum() - count.sum()).to(torch.int32)
+    spare = (free.sum() - count.sum()).to(torch.int32).view(1)
     target = new.gather(1, (length // page).clamp(max=width - 1)[:, None].long())[:, 0]
     some = (source >= 0) & (target >= 0)
     a, b = source[some].long(), target[some].long()
@@ -387,7 +387,7 @@ def _gather(s):
         _bytes(s[name])[b] = _bytes(s[name])[a]
     for name in ("ks", "vs"):
         s[name][b] = s[name][a]
-    return [new, torch.where(table >= 0, moved[table.clamp(min=0).long()], -1), moved, used.to(torch.int32), s["k"], s["v"], s["ks"], s["vs"]]
+    return [new, torch.where(table >= 0, moved[table.clamp(min=0).long()], -1), moved, used.to(torch.int32).view(1), s["k"], s["v"], s["ks"], s["vs"]]
 
 
 def _dense(codes, scales, at, kv, dim):
