@@ -492,6 +492,75 @@ tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int64_t q_head_
                           int64_t window, double scale, int dtype, void* workspace, int64_t workspace_bytes,
                           tg_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Pages of the cache. `refs` (pages int32) counts the table entries, of all
+ * tables there are, that hold each page; 0: it is free. A sequence holds the
+ * pages at the beginning of its table row, up to the first entry that is
+ * negative. Its pages lens / page and further are open (new tokens are written
+ * there) and are its own; those before are full and may be shared, since nothing
+ * writes to them. The calls below read refs, table and lens and leave new ones
+ * in other arrays, so that what a caller holds stays valid until it goes over to
+ * the new ones. Outputs, workspace, cache and inputs must not overlap. All is
+ * stream-ordered, decided on the device and the same every run; nothing is
+ * allocated, and the workspace's contents need not be kept.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Pages src[i] of one cache (codes and scales) to pages dst[i] of another of the
+ * same form, which may be the same one. The dst are distinct, and within one
+ * cache none is another pair's src; what a page that breaks this gets is
+ * unspecified. A pair with a page out of range is left out and reported
+ * (TG_ERR_BOUNDS). count int32 pairs on the device.
+ */
+tg_status tg_kv_copy(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, int64_t pages,
+                     void* to_k, void* to_v, float* to_k_scale, float* to_v_scale, int64_t to_pages, int64_t kv_heads,
+                     int64_t page, int64_t dim, int format, const int32_t* src, const int32_t* dst, int64_t count,
+                     tg_stream_t stream);
+
+/*
+ * The batch becomes `count` sequences, of which the i-th continues parents[i]
+ * (an old sequence, or negative: it begins empty; parents NULL: each continues
+ * itself, count is batch). Old sequences that no one continues are let go of.
+ * Every new sequence has pages for at least its length and `room` more tokens.
+ *
+ *   lens_out[i]     its parent's length (0 without one)
+ *   table_out[i]    count x table_width: the parent's full pages, shared; then
+ *                   the parent's open pages go to its first child, as far as
+ *                   refs says 1; then new pages up to the room; then -1
+ *   new pages       get the tokens that the parent's partly filled page holds,
+ *                   where they take its place (codes of those tokens, scales)
+ *   refs_out        entries of the old table taken off refs, new ones added
+ *   spare           one int32: free pages that are left. Negative: so many were
+ *                   lacking; the last of the new entries are then -1
+ *
+ * New pages are the lowest-numbered ones that nobody holds after the old
+ * sequences are gone (a page that tokens are copied from is not among them),
+ * given in the order of sequences and places. What is out of range is reported
+ * (TG_ERR_BOUNDS) and not followed: a page number ends its sequence's pages, a
+ * length beyond them is 0, a parent is none, and room stops at the table's width.
+ */
+tg_status tg_kv_fork_workspace(int64_t pages, int64_t page, int64_t batch, int64_t count, int64_t table_width,
+                               int64_t* bytes);
+tg_status tg_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int64_t pages, int64_t kv_heads,
+                     int64_t page, int64_t dim, int format, const int32_t* refs, const int32_t* table,
+                     int64_t table_width, const int32_t* lens, int64_t batch, const int32_t* parents, int64_t count,
+                     int64_t room, int32_t* refs_out, int32_t* table_out, int32_t* lens_out, int32_t* spare,
+                     void* workspace, int64_t workspace_bytes, tg_stream_t stream);
+
+/*
+ * Moves pages so that those in use are 0 .. used - 1: the m-th lowest page from
+ * `used` on that is in use goes to the m-th lowest free one before. moved
+ * (pages int32) says where each page is now, -1 for a free one, so that other
+ * tables than this one can follow; table_out is table with its pages replaced
+ * (-1 where it has none, or one that nobody holds). A page number beyond the
+ * cache becomes -1 and is reported (TG_ERR_BOUNDS).
+ */
+tg_status tg_kv_compact_workspace(int64_t pages, int64_t* bytes);
+tg_status tg_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int64_t pages, int64_t kv_heads,
+                        int64_t page, int64_t dim, int format, const int32_t* refs, const int32_t* table,
+                        int64_t table_width, int64_t batch, int32_t* refs_out, int32_t* table_out, int32_t* moved,
+                        int32_t* used, void* workspace, int64_t workspace_bytes, tg_stream_t stream);
+
 /*
  * Synchronises `stream`, then reports (and clears) the device-side status word
  * that kernels set when one of their bounded waits expires: TG_OK or

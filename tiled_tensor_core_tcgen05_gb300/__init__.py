@@ -35,6 +35,7 @@ EXPORTS = ("tg_gemm", "tg_gemm_ex", "tg_gemm_plan", "tg_gemm_staged", "tg_gemm_s
            "tg_gemm_w4_kernel", "tg_attention_fwd",
            "tg_softmax_rows", "tg_bias_gelu",
            "tg_rope", "tg_kv_append", "tg_kv_read", "tg_attention_kv_workspace", "tg_attention_kv",
+           "tg_kv_copy", "tg_kv_fork_workspace", "tg_kv_fork", "tg_kv_compact_workspace", "tg_kv_compact",
            "tg_device_status", "tg_debug_status",
            "tg_set_watchdog_ns",
            "tg_debug_skip_first_arrive", "tg_debug_bounds_limit", "tg_debug_build", "tg_status_string",
@@ -75,6 +76,11 @@ def bind(path: str) -> ctypes.CDLL:
     lib.tg_attention_kv_workspace.argtypes = [_i64, _i64, _i64, _int] + [_i64] * 6 + [_int, ctypes.POINTER(_i64)]
     lib.tg_attention_kv.argtypes = (strided + [_vp, _vp] + cache + batch + [_i64, _i64, _i64, _int, _i64, _dbl, _int,
                                                                             _vp, _i64, _vp])
+    lib.tg_kv_copy.argtypes = [_vp] * 4 + [_i64] + [_vp] * 4 + [_i64] * 4 + [_int, _vp, _vp, _i64, _vp]
+    lib.tg_kv_fork_workspace.argtypes = [_i64] * 5 + [ctypes.POINTER(_i64)]
+    lib.tg_kv_fork.argtypes = cache + [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64] + [_vp] * 5 + [_i64, _vp]
+    lib.tg_kv_compact_workspace.argtypes = [_i64, ctypes.POINTER(_i64)]
+    lib.tg_kv_compact.argtypes = cache + [_vp, _vp, _i64, _i64] + [_vp] * 5 + [_i64, _vp]
     lib.tg_device_status.argtypes = [_vp, ctypes.POINTER(_int)]
     lib.tg_debug_status.argtypes = [_vp]
     lib.tg_set_watchdog_ns.argtypes = [_u64]
@@ -92,7 +98,8 @@ def bind(path: str) -> ctypes.CDLL:
     lib.tg_shutdown.restype = None
     for name in ("tg_gemm", "tg_gemm_ex", "tg_gemm_plan", "tg_gemm_staged", "tg_gemm_splitk_noalloc", "tg_gemm_w4", "tg_gemm_w4_ex",
                  "tg_gemm_w4_kernel", "tg_attention_fwd", "tg_softmax_rows", "tg_bias_gelu", "tg_rope", "tg_kv_append", "tg_kv_read", "tg_attention_kv_workspace",
-                 "tg_attention_kv", "tg_device_status", "tg_debug_status",
+                 "tg_attention_kv", "tg_kv_copy", "tg_kv_fork_workspace", "tg_kv_fork", "tg_kv_compact_workspace", "tg_kv_compact",
+                 "tg_device_status", "tg_debug_status",
                  "tg_set_watchdog_ns", "tg_debug_skip_first_arrive", "tg_debug_bounds_limit", "tg_debug_build",
                  "tg_version"):
         getattr(lib, name).restype = _int
@@ -244,6 +251,35 @@ def tg_attention_kv_workspace(kv_heads: int, page: int, dim: int, fmt: int, head
 def tg_attention_kv(*args) -> None:
     """The C entry point's arguments in its order (include/tg_gemm.h)."""
     _check(_lib.tg_attention_kv(*args))
+
+
+def tg_kv_copy(*args) -> None:
+    """The C entry point's arguments in its order (include/tg_gemm.h)."""
+    _check(_lib.tg_kv_copy(*args))
+
+
+def tg_kv_fork_workspace(pages: int, page: int, batch: int, count: int, table_width: int) -> int:
+    """Bytes of workspace that tg_kv_fork needs for these sizes."""
+    n = _i64()
+    _check(_lib.tg_kv_fork_workspace(pages, page, batch, count, table_width, ctypes.byref(n)))
+    return n.value
+
+
+def tg_kv_fork(*args) -> None:
+    """The C entry point's arguments in its order (include/tg_gemm.h)."""
+    _check(_lib.tg_kv_fork(*args))
+
+
+def tg_kv_compact_workspace(pages: int) -> int:
+    """Bytes of workspace that tg_kv_compact needs for so many pages."""
+    n = _i64()
+    _check(_lib.tg_kv_compact_workspace(pages, ctypes.byref(n)))
+    return n.value
+
+
+def tg_kv_compact(*args) -> None:
+    """The C entry point's arguments in its order (include/tg_gemm.h)."""
+    _check(_lib.tg_kv_compact(*args))
 
 
 def tg_device_status(stream: int | None) -> tuple[int, int]:
@@ -580,3 +616,27 @@ def attention_kv(Q, cache, table, lens, cu=None, max_new: int = 1, max_len: int 
     recorded."""
     return _answer((_fast or _binding()).attention_kv(Q, cache.args, table, lens, cu, max_new, max_len, causal, window,
                                                       scale, return_lse, out, stream))
+
+
+def kv_copy(cache, src, dst, to=None, stream=None) -> None:
+    """Pages src[i] of ``cache``, codes and scales, to pages dst[i] (int32 vectors) of the KvCache ``to``, of the
+    same form, or of ``cache`` itself. The dst are distinct, and within one cache none is another pair's src."""
+    return _answer((_fast or _binding()).kv_copy(cache.args, src, dst, to if to is None else to.args, stream))
+
+
+def kv_fork(cache, refs, table, lens, parents=None, room: int = 0, out=None, stream=None):
+    """The sequences of ``table`` (batch, width) and ``lens`` go on as those that continue ``parents`` (int32, one a
+    new sequence: an old sequence, or negative for one that begins empty; None: each continues itself): reordered,
+    multiplied, let go of, and given pages for ``room`` tokens beyond their lengths. ``refs`` (int32, one a page of
+    ``cache``) counts the table entries that hold each page; 0 is a free page. Full pages are shared; a partly filled
+    one goes to the first child, and further children get copies of its tokens in new pages. Returns (refs, table, lens,
+    spare): new tensors, or ``out``, four that overlap none of the inputs. spare (1,): free pages that are left;
+    negative: so many were lacking, and the last new entries are -1. The rules are in include/tg_gemm.h."""
+    return _answer((_fast or _binding()).kv_fork(cache.args, refs, table, lens, parents, room, out, stream))
+
+
+def kv_compact(cache, refs, table, out=None, stream=None):
+    """Moves pages of ``cache`` so that those that ``refs`` says are in use are its first ones. Returns (refs, table,
+    moved, used): new tensors, or ``out``, four that overlap none of the inputs. moved (pages,): where each page is now
+    (-1: it is free), for other tables than ``table``; used (1,): how many are in use."""
+    return _answer((_fast or _binding()).kv_compact(cache.args, refs, table, out, stream))

@@ -1689,3 +1689,178 @@ extern "C" tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int6
     cudaError_t e = launch_kv_attn(c, tmK, tmV, workspace, g_dev[dev].sm_count, stream);
     return e == cudaSuccess ? TG_OK : cuda_fail(e, "cache attention kernel launch");
 }
+
+namespace {
+
+struct Piece {
+    const void* p;
+    int64_t bytes;
+};
+
+// Whether some output lies on an input or on another output. The first `outputs` pieces are the outputs.
+bool any_overlap(const Piece* x, int outputs, int all) {
+    for (int i = 0; i < outputs; ++i)
+        for (int j = i + 1; j < all; ++j)
+            if (overlaps(x[i].p, x[i].bytes, x[j].p, x[j].bytes)) return true;
+    return false;
+}
+
+int64_t cache_bytes(const KvCacheArgs& c) { return c.pages * c.kv_heads * c.page * c.dim; }
+int64_t scale_bytes(const KvCacheArgs& c) { return c.pages * c.kv_heads * 4; }
+
+tg_status check_tables(int64_t batch, int64_t width, int64_t page, const char* what) {
+    if (batch < 0 || batch > (1 << 20) || width < 0 || width > kIntMax / page)
+        return fail(TG_ERR_INVALID_ARG, "%s out of range: %lld rows of %lld pages", what, (long long)batch, (long long)width);
+    return TG_OK;
+}
+
+}  // namespace
+
+extern "C" tg_status tg_kv_copy(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, int64_t pages,
+                                void* to_k, void* to_v, float* to_k_scale, float* to_v_scale, int64_t to_pages, int64_t kv_heads,
+                                int64_t page, int64_t dim, int format, const int32_t* src, const int32_t* dst, int64_t count,
+                                tg_stream_t stream_) {
+    t_last_error.clear();
+    const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    PageCopyCall c{};
+    tg_status st = check_cache(k_cache, v_cache, k_scale, v_scale, pages, kv_heads, page, dim, format, &c.from);
+    if (st != TG_OK) return st;
+    if ((st = check_cache(to_k, to_v, to_k_scale, to_v_scale, to_pages, kv_heads, page, dim, format, &c.to)) != TG_OK) return st;
+    if (count < 0 || count > kIntMax) return fail(TG_ERR_INVALID_ARG, "count out of range: %lld", (long long)count);
+    if (count == 0) return TG_OK;
+    if (!src || !dst) return fail(TG_ERR_INVALID_ARG, "src or dst is NULL");
+    if (!(aligned(src, 4) && aligned(dst, 4))) return fail(TG_ERR_INVALID_ARG, "src and dst must be 4-byte aligned");
+    const bool same = k_cache == to_k && v_cache == to_v && k_scale == to_k_scale && v_scale == to_v_scale && pages == to_pages;
+    const int64_t list = count * 4;
+    const Piece outs[10] = {{to_k, cache_bytes(c.to)},  {to_v, cache_bytes(c.to)},  {to_k_scale, scale_bytes(c.to)}, {to_v_scale, scale_bytes(c.to)},
+                            {src, list},                {dst, list},                {k_cache, cache_bytes(c.from)},  {v_cache, cache_bytes(c.from)},
+                            {k_scale, scale_bytes(c.from)}, {v_scale, scale_bytes(c.from)}};
+    if (any_overlap(outs, 4, same ? 6 : 10))
+        return fail(TG_ERR_INVALID_ARG, "the caches overlap without being the same, or a list lies in one");
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    if ((st = current_device(&dev)) != TG_OK) return st;
+    c.src = src;
+    c.dst = dst;
+    c.count = (int)count;
+    c.wd = watchdog(g_dev[dev]);
+    cudaError_t e = launch_kv_copy(c, g_dev[dev].sm_count, stream);
+    return e == cudaSuccess ? TG_OK : cuda_fail(e, "page copy kernel launch");
+}
+
+extern "C" tg_status tg_kv_fork_workspace(int64_t pages, int64_t page, int64_t batch, int64_t count, int64_t table_width, int64_t* bytes) {
+    t_last_error.clear();
+    if (bytes == nullptr) return fail(TG_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = 0;
+    if (page != 16 && page != 32 && page != 64 && page != 128)
+        return fail(TG_ERR_INVALID_ARG, "page must be 16, 32, 64 or 128 tokens, got %lld", (long long)page);
+    if (pages < 0 || pages > kIntMax) return fail(TG_ERR_INVALID_ARG, "pages out of range: %lld", (long long)pages);
+    tg_status st = check_tables(batch, table_width, page, "the table");
+    if (st != TG_OK || (st = check_tables(count, table_width, page, "the new table")) != TG_OK) return st;
+    ForkWork w;
+    *bytes = kv_fork_workspace(pages, batch, count, table_width, &w, nullptr);
+    return TG_OK;
+}
+
+extern "C" tg_status tg_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int64_t pages, int64_t kv_heads,
+                                int64_t page, int64_t dim, int format, const int32_t* refs, const int32_t* table, int64_t table_width,
+                                const int32_t* lens, int64_t batch, const int32_t* parents, int64_t count, int64_t room,
+                                int32_t* refs_out, int32_t* table_out, int32_t* lens_out, int32_t* spare, void* workspace,
+                                int64_t workspace_bytes, tg_stream_t stream_) {
+    t_last_error.clear();
+    const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    KvForkCall c{};
+    tg_status st = check_cache(k_cache, v_cache, k_scale, v_scale, pages, kv_heads, page, dim, format, &c.cache);
+    if (st != TG_OK) return st;
+    if ((st = check_tables(batch, table_width, page, "the table")) != TG_OK) return st;
+    if ((st = check_tables(count, table_width, page, "the new table")) != TG_OK) return st;
+    if (parents == nullptr && count != batch)
+        return fail(TG_ERR_INVALID_ARG, "without parents every sequence continues itself: count %lld is not batch %lld", (long long)count,
+                    (long long)batch);
+    if (room < 0 || room > kIntMax) return fail(TG_ERR_INVALID_ARG, "room out of range: %lld", (long long)room);
+    if (!spare || (pages > 0 && (!refs || !refs_out)) || (batch > 0 && (!lens || (table_width > 0 && !table))) ||
+        (count > 0 && (!lens_out || (table_width > 0 && !table_out))))
+        return fail(TG_ERR_INVALID_ARG, "refs, table, lens or an output is NULL");
+    for (const void* p : {(const void*)refs, (const void*)table, (const void*)lens, (const void*)parents, (const void*)refs_out,
+                          (const void*)table_out, (const void*)lens_out, (const void*)spare})
+        if (!aligned(p, 4)) return fail(TG_ERR_INVALID_ARG, "refs, table, lens, parents and the outputs must be 4-byte aligned");
+    const int64_t need = kv_fork_workspace(pages, batch, count, table_width, &c.w, workspace);
+    if (workspace == nullptr || workspace_bytes < need)
+        return fail(TG_ERR_INVALID_ARG, "tg_kv_fork needs a workspace of %lld bytes, got %lld", (long long)need,
+                    (long long)(workspace ? workspace_bytes : 0));
+    if (!aligned(workspace, 16)) return fail(TG_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
+    const Piece all[13] = {{refs_out, pages * 4}, {table_out, count * table_width * 4}, {lens_out, count * 4}, {spare, 4}, {workspace, need},
+                           {k_cache, cache_bytes(c.cache)}, {v_cache, cache_bytes(c.cache)}, {k_scale, scale_bytes(c.cache)},
+                           {v_scale, scale_bytes(c.cache)}, {refs, pages * 4}, {table, batch * table_width * 4}, {lens, batch * 4},
+                           {parents, parents ? count * 4 : 0}};
+    if (any_overlap(all, 9, 13)) return fail(TG_ERR_INVALID_ARG, "an output, the workspace or the cache overlaps an input or another output");
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    if ((st = current_device(&dev)) != TG_OK) return st;
+    c.refs = refs;
+    c.table = table;
+    c.lens = lens;
+    c.parents = parents;
+    c.width = table_width;
+    c.room = room;
+    c.batch = (int)batch;
+    c.count = (int)count;
+    while (page >> (c.page_shift + 1)) ++c.page_shift;
+    c.refs_out = refs_out;
+    c.table_out = table_out;
+    c.lens_out = lens_out;
+    c.spare = spare;
+    c.wd = watchdog(g_dev[dev]);
+    cudaError_t e = launch_kv_fork(c, g_dev[dev].sm_count, stream);
+    return e == cudaSuccess ? TG_OK : cuda_fail(e, "fork kernel launch");
+}
+
+extern "C" tg_status tg_kv_compact_workspace(int64_t pages, int64_t* bytes) {
+    t_last_error.clear();
+    if (bytes == nullptr) return fail(TG_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = 0;
+    if (pages < 0 || pages > kIntMax) return fail(TG_ERR_INVALID_ARG, "pages out of range: %lld", (long long)pages);
+    PageWork w;
+    *bytes = kv_compact_workspace(pages, &w, nullptr);
+    return TG_OK;
+}
+
+extern "C" tg_status tg_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int64_t pages, int64_t kv_heads,
+                                   int64_t page, int64_t dim, int format, const int32_t* refs, const int32_t* table,
+                                   int64_t table_width, int64_t batch, int32_t* refs_out, int32_t* table_out, int32_t* moved,
+                                   int32_t* used, void* workspace, int64_t workspace_bytes, tg_stream_t stream_) {
+    t_last_error.clear();
+    const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    KvCompactCall c{};
+    tg_status st = check_cache(k_cache, v_cache, k_scale, v_scale, pages, kv_heads, page, dim, format, &c.cache);
+    if (st != TG_OK) return st;
+    if ((st = check_tables(batch, table_width, page, "the table")) != TG_OK) return st;
+    if (!used || (pages > 0 && (!refs || !refs_out || !moved)) || (batch > 0 && table_width > 0 && (!table || !table_out)))
+        return fail(TG_ERR_INVALID_ARG, "refs, table or an output is NULL");
+    for (const void* p : {(const void*)refs, (const void*)table, (const void*)refs_out, (const void*)table_out, (const void*)moved, (const void*)used})
+        if (!aligned(p, 4)) return fail(TG_ERR_INVALID_ARG, "refs, table and the outputs must be 4-byte aligned");
+    const int64_t need = kv_compact_workspace(pages, &c.w, workspace);
+    if (workspace == nullptr || workspace_bytes < need)
+        return fail(TG_ERR_INVALID_ARG, "tg_kv_compact needs a workspace of %lld bytes, got %lld", (long long)need,
+                    (long long)(workspace ? workspace_bytes : 0));
+    if (!aligned(workspace, 16)) return fail(TG_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
+    const int64_t entries = batch * table_width * 4;
+    const Piece all[11] = {{refs_out, pages * 4}, {table_out, entries}, {moved, pages * 4}, {used, 4}, {workspace, need},
+                           {k_cache, cache_bytes(c.cache)}, {v_cache, cache_bytes(c.cache)}, {k_scale, scale_bytes(c.cache)},
+                           {v_scale, scale_bytes(c.cache)}, {refs, pages * 4}, {table, entries}};
+    if (any_overlap(all, 9, 11)) return fail(TG_ERR_INVALID_ARG, "an output, the workspace or the cache overlaps an input or another output");
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    if ((st = current_device(&dev)) != TG_OK) return st;
+    c.refs = refs;
+    c.table = table;
+    c.width = table_width;
+    c.batch = (int)batch;
+    c.refs_out = refs_out;
+    c.table_out = table_out;
+    c.moved = moved;
+    c.used = used;
+    c.wd = watchdog(g_dev[dev]);
+    cudaError_t e = launch_kv_compact(c, g_dev[dev].sm_count, stream);
+    return e == cudaSuccess ? TG_OK : cuda_fail(e, "compact kernel launch");
+}

@@ -84,6 +84,63 @@ struct KvAttnCall {
     Watchdog wd;
 };
 
+// A page's first tokens on their way to another page.
+struct PageItem {
+    int from, to, tokens;
+};
+
+// What the bookkeeping of pages leaves for the copying: a list, and its length.
+struct PageWork {
+    int* items_count;
+    PageItem* items;
+};
+
+struct PageCopyCall {
+    KvCacheArgs from, to;
+    const int32_t* src;      // count pairs of pages, or
+    const int32_t* dst;
+    int count;
+    const PageItem* items;   // a list that another kernel leaves
+    const int* items_count;
+    Watchdog wd;
+};
+
+// Between the steps of a fork: per old sequence its children, the first of them, its pages, its length and the entries
+// that its first child takes over; per new one the pages it needs and their place in the list of those given.
+struct ForkWork : PageWork {
+    int *children, *first, *held, *lens, *kept, *need;
+    int64_t* place;
+    int* given;
+};
+
+struct KvForkCall {
+    KvCacheArgs cache;
+    const int32_t *refs, *table, *lens;
+    const int32_t* parents;  // null: every sequence continues itself
+    int64_t width, room;
+    int batch, count, page_shift;
+    int32_t *refs_out, *table_out, *lens_out, *spare;
+    ForkWork w;
+    Watchdog wd;
+};
+
+struct KvCompactCall {
+    KvCacheArgs cache;
+    const int32_t *refs, *table;
+    int64_t width;
+    int batch;
+    int32_t *refs_out, *table_out, *moved, *used;
+    PageWork w;
+    Watchdog wd;
+};
+
+// Bytes of a call's workspace; its parts, if it lies at `at`.
+int64_t kv_fork_workspace(int64_t pages, int64_t batch, int64_t count, int64_t width, ForkWork* w, void* at);
+int64_t kv_compact_workspace(int64_t pages, PageWork* w, void* at);
+cudaError_t launch_kv_copy(const PageCopyCall& c, int sm_count, cudaStream_t stream);
+cudaError_t launch_kv_fork(const KvForkCall& c, int sm_count, cudaStream_t stream);
+cudaError_t launch_kv_compact(const KvCompactCall& c, int sm_count, cudaStream_t stream);
+
 cudaError_t launch_rope(const RopeCall& c, int sm_count, cudaStream_t stream);
 cudaError_t launch_kv_append(const KvAppendCall& c, int sm_count, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvReadCall& c, int sm_count, cudaStream_t stream);

@@ -411,6 +411,129 @@ PyObject* attention_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// An output of `n` (x `m`) int32: made, or the given one.
+struct IntsOut {
+    at::Tensor made;
+    PyObject* given = Py_None;
+    int32_t* p = nullptr;
+    IntsOut(PyObject* out, int place, int of, const char* name, const at::Tensor& like, int64_t n, int64_t m = -1) {
+        if (out == Py_None) {
+            made = m < 0 ? at::empty({n}, like.options()) : at::empty({n, m}, like.options());
+            p = static_cast<int32_t*>(made.data_ptr());
+            return;
+        }
+        if (!PyTuple_Check(out) || PyTuple_GET_SIZE(out) != of) type_error("out must be a tuple of " + std::to_string(of) + " tensors");
+        given = PyTuple_GET_ITEM(out, place);
+        p = const_cast<int32_t*>(ints(given, name, n, m));
+    }
+    PyObject* answer() {
+        written(given);
+        return made.defined() ? THPVariable_Wrap(std::move(made)) : same(given);
+    }
+};
+
+PyObject* four(IntsOut& a, IntsOut& b, IntsOut& c, IntsOut& d) {
+    PyObject* t = PyTuple_New(4);
+    if (t == nullptr) return nullptr;
+    IntsOut* const x[4] = {&a, &b, &c, &d};
+    for (int i = 0; i < 4; ++i) PyTuple_SET_ITEM(t, i, x[i]->answer());
+    return t;
+}
+
+// A table of any number of rows.
+const int32_t* table_of(PyObject* x, int64_t* rows, int64_t* width) {
+    const at::Tensor& t = tensor(x, "table");
+    if (t.dim() != 2) value_error("table must have shape (sequences, pages a sequence), got " + shape_of(t));
+    *rows = t.size(0);
+    *width = t.size(1);
+    return ints(x, "table", *rows, *width);
+}
+
+// (cache, src, dst, other cache or None, stream)
+PyObject* kv_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 5, [&]() -> PyObject* {
+        const Cache c = cache(a[0]), d = a[3] == Py_None ? c : cache(a[3]);
+        if (d.kv_heads != c.kv_heads || d.page != c.page || d.dim != c.dim || d.format != c.format)
+            value_error("both caches must have the same heads, page, dim and type of codes");
+        const at::Tensor& s = tensor(a[1], "src");
+        if (s.dim() != 1) value_error("src must be a vector, got " + shape_of(s));
+        const int64_t count = s.size(0);
+        const int32_t *src = ints(a[1], "src", count), *dst = ints(a[2], "dst", count);
+        const Where where(a[4]);
+        return answer(
+            [&] { return tg_kv_copy(c.k, c.v, c.ks, c.vs, c.pages, d.k, d.v, d.ks, d.vs, d.pages, c.kv_heads, c.page, c.dim, c.format, src, dst, count, where.handle); },
+            [&]() -> PyObject* {
+                for (int i = 0; i < 4; ++i) written(PyTuple_GET_ITEM(a[3] == Py_None ? a[0] : a[3], i));
+                Py_RETURN_NONE;
+            });
+    });
+}
+
+// (cache, refs, table, lens, parents or None, room, out or None, stream)
+PyObject* kv_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 8, [&]() -> PyObject* {
+        const Cache c = cache(a[0]);
+        const int32_t* refs = ints(a[1], "refs", c.pages);
+        int64_t batch = 0, width = 0;
+        const int32_t* table = table_of(a[2], &batch, &width);
+        const int32_t* lens = ints(a[3], "lens", batch);
+        int64_t count = batch;
+        const int32_t* parents = nullptr;
+        if (a[4] != Py_None) {
+            const at::Tensor& p = tensor(a[4], "parents");
+            if (p.dim() != 1) value_error("parents must be a vector, got " + shape_of(p));
+            count = p.size(0);
+            parents = ints(a[4], "parents", count);
+        }
+        const int64_t room = integer(a[5]);
+        const Where where(a[7]);
+        const at::Tensor& like = tensor(a[1], "refs");
+        IntsOut o0(a[6], 0, 4, "refs of out", like, c.pages), o1(a[6], 1, 4, "table of out", like, count, width), o2(a[6], 2, 4, "lens of out", like, count),
+            o3(a[6], 3, 4, "spare of out", like, 1);
+        int64_t need = 0;
+        const int status = tg_kv_fork_workspace(c.pages, c.page, batch, count, width, &need);
+        if (status != TG_OK) return PyLong_FromLong(status);
+        const at::Tensor work = at::empty({need}, like.options().dtype(at::kByte));
+        void* w = work.data_ptr();
+        return answer(
+            [&] {
+                // an empty parents tensor has no address
+                static const int32_t none = 0;
+                return tg_kv_fork(c.k, c.v, c.ks, c.vs, c.pages, c.kv_heads, c.page, c.dim, c.format, refs, table, width, lens, batch,
+                                  a[4] != Py_None && parents == nullptr ? &none : parents, count, room, o0.p, o1.p, o2.p, o3.p, w, need, where.handle);
+            },
+            [&] {
+                for (int i = 0; i < 4; ++i) written(PyTuple_GET_ITEM(a[0], i));
+                return four(o0, o1, o2, o3);
+            });
+    });
+}
+
+// (cache, refs, table, out or None, stream)
+PyObject* kv_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 5, [&]() -> PyObject* {
+        const Cache c = cache(a[0]);
+        const int32_t* refs = ints(a[1], "refs", c.pages);
+        int64_t batch = 0, width = 0;
+        const int32_t* table = table_of(a[2], &batch, &width);
+        const Where where(a[4]);
+        const at::Tensor& like = tensor(a[1], "refs");
+        IntsOut o0(a[3], 0, 4, "refs of out", like, c.pages), o1(a[3], 1, 4, "table of out", like, batch, width), o2(a[3], 2, 4, "moved of out", like, c.pages),
+            o3(a[3], 3, 4, "used of out", like, 1);
+        int64_t need = 0;
+        const int status = tg_kv_compact_workspace(c.pages, &need);
+        if (status != TG_OK) return PyLong_FromLong(status);
+        const at::Tensor work = at::empty({need}, like.options().dtype(at::kByte));
+        void* w = work.data_ptr();
+        return answer(
+            [&] { return tg_kv_compact(c.k, c.v, c.ks, c.vs, c.pages, c.kv_heads, c.page, c.dim, c.format, refs, table, width, batch, o0.p, o1.p, o2.p, o3.p, w, need, where.handle); },
+            [&] {
+                for (int i = 0; i < 4; ++i) written(PyTuple_GET_ITEM(a[0], i));
+                return four(o0, o1, o2, o3);
+            });
+    });
+}
+
 // (device that a tensor has, current device, name): the check above, for a machine with one
 PyObject* check_device_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 3, [&]() -> PyObject* {
@@ -428,6 +551,9 @@ PyMethodDef methods[] = {
     {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_append)), METH_FASTCALL, nullptr},
     {"kv_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_read)), METH_FASTCALL, nullptr},
     {"attention_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention_kv)), METH_FASTCALL, nullptr},
+    {"kv_copy", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_copy)), METH_FASTCALL, nullptr},
+    {"kv_fork", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_fork)), METH_FASTCALL, nullptr},
+    {"kv_compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_compact)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
