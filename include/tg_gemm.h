@@ -561,6 +561,39 @@ tg_status tg_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v_s
                         int64_t table_width, int64_t batch, int32_t* refs_out, int32_t* table_out, int32_t* moved,
                         int32_t* used, void* workspace, int64_t workspace_bytes, tg_stream_t stream);
 
+/* Types of logits: tg_dtype's, or 32 bits. */
+#define TG_FP32 2
+
+/*
+ * Draws a token from each row of logits X (rows x vocab, contiguous along vocab,
+ * row_stride in elements; TG_FP16, TG_BF16 or TG_FP32). With T = temperature,
+ *
+ *     w_i = exp((x_i - max x) / T),
+ *
+ * tokens are kept that are among the top_k largest (of equal ones the lowest
+ * index first; 0 or less: all), that have w_i >= min_p (0: all), and, of those,
+ * in falling order (of equal ones the lowest index first) as long as the ones
+ * before them have less than top_p of the weight (at least 1: all; the first one
+ * is always kept). The row's token is the first of the kept, by index, up to
+ * which the sum of their weights exceeds u[row] times the whole. u is in [0, 1);
+ * values beyond are brought to it, and a NaN is 0.
+ *
+ * A row whose temperature is 0 or less (or a NaN) gives the largest logit's
+ * token, of equal ones the lowest. NaN logits are as if -inf; a row without any
+ * logit above -inf gives -1; where +inf is among them, only those count, alike.
+ *
+ * Each of the settings is one float32 (top_k: int32) a row on the device, or
+ * where the pointer is NULL the number beside it for all rows. Weights are 64-bit
+ * fixed point, of 2^-44 of the row's largest (w_i below half of that count as
+ * none), right to 2^-38 of themselves, and their sums are exact: the token does not depend on how
+ * the work is split, nor on the other rows. vocab is at most 2^18.
+ * Stream-ordered; allocates nothing.
+ */
+tg_status tg_sample(const void* X, int64_t row_stride, int64_t rows, int64_t vocab, int dtype, const float* u,
+                    const float* temperature, double temperature_all, const int32_t* top_k, int64_t top_k_all,
+                    const float* top_p, double top_p_all, const float* min_p, double min_p_all, int32_t* tokens,
+                    tg_stream_t stream);
+
 /*
  * Synchronises `stream`, then reports (and clears) the device-side status word
  * that kernels set when one of their bounded waits expires: TG_OK or

@@ -25,7 +25,7 @@ NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024  # TG_NOALLOC_SCRATCH_BYTES
 KERNEL_AUTO, KERNEL_TILED_TMA, KERNEL_TILED_LSU, KERNEL_SPLITK, KERNEL_TILED_PAIR = 0, 1, 2, 3, 4
 W4_INT4, W4_FP4_E2M1 = 0, 1
 W4_KERNEL_AUTO, W4_KERNEL_TMEM, W4_KERNEL_REG = 0, 1, 2
-FP16, BF16 = 0, 1
+FP16, BF16, FP32 = 0, 1, 2
 KV_E4M3, KV_INT8 = 0, 1
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED_DEVICE, ERR_CUDA, ERR_TIMEOUT, ERR_NO_MEMORY, ERR_BOUNDS = range(7)
@@ -35,7 +35,7 @@ EXPORTS = ("tg_gemm", "tg_gemm_ex", "tg_gemm_plan", "tg_gemm_staged", "tg_gemm_s
            "tg_gemm_w4_kernel", "tg_attention_fwd",
            "tg_softmax_rows", "tg_bias_gelu",
            "tg_rope", "tg_kv_append", "tg_kv_read", "tg_attention_kv_workspace", "tg_attention_kv",
-           "tg_kv_copy", "tg_kv_fork_workspace", "tg_kv_fork", "tg_kv_compact_workspace", "tg_kv_compact",
+           "tg_kv_copy", "tg_kv_fork_workspace", "tg_kv_fork", "tg_kv_compact_workspace", "tg_kv_compact", "tg_sample",
            "tg_device_status", "tg_debug_status",
            "tg_set_watchdog_ns",
            "tg_debug_skip_first_arrive", "tg_debug_bounds_limit", "tg_debug_build", "tg_status_string",
@@ -81,6 +81,7 @@ def bind(path: str) -> ctypes.CDLL:
     lib.tg_kv_fork.argtypes = cache + [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64] + [_vp] * 5 + [_i64, _vp]
     lib.tg_kv_compact_workspace.argtypes = [_i64, ctypes.POINTER(_i64)]
     lib.tg_kv_compact.argtypes = cache + [_vp, _vp, _i64, _i64] + [_vp] * 5 + [_i64, _vp]
+    lib.tg_sample.argtypes = [_vp, _i64, _i64, _i64, _int, _vp, _vp, _dbl, _vp, _i64, _vp, _dbl, _vp, _dbl, _vp, _vp]
     lib.tg_device_status.argtypes = [_vp, ctypes.POINTER(_int)]
     lib.tg_debug_status.argtypes = [_vp]
     lib.tg_set_watchdog_ns.argtypes = [_u64]
@@ -98,7 +99,7 @@ def bind(path: str) -> ctypes.CDLL:
     lib.tg_shutdown.restype = None
     for name in ("tg_gemm", "tg_gemm_ex", "tg_gemm_plan", "tg_gemm_staged", "tg_gemm_splitk_noalloc", "tg_gemm_w4", "tg_gemm_w4_ex",
                  "tg_gemm_w4_kernel", "tg_attention_fwd", "tg_softmax_rows", "tg_bias_gelu", "tg_rope", "tg_kv_append", "tg_kv_read", "tg_attention_kv_workspace",
-                 "tg_attention_kv", "tg_kv_copy", "tg_kv_fork_workspace", "tg_kv_fork", "tg_kv_compact_workspace", "tg_kv_compact",
+                 "tg_attention_kv", "tg_kv_copy", "tg_kv_fork_workspace", "tg_kv_fork", "tg_kv_compact_workspace", "tg_kv_compact", "tg_sample",
                  "tg_device_status", "tg_debug_status",
                  "tg_set_watchdog_ns", "tg_debug_skip_first_arrive", "tg_debug_bounds_limit", "tg_debug_build",
                  "tg_version"):
@@ -280,6 +281,11 @@ def tg_kv_compact_workspace(pages: int) -> int:
 def tg_kv_compact(*args) -> None:
     """The C entry point's arguments in its order (include/tg_gemm.h)."""
     _check(_lib.tg_kv_compact(*args))
+
+
+def tg_sample(*args) -> None:
+    """The C entry point's arguments in its order (include/tg_gemm.h)."""
+    _check(_lib.tg_sample(*args))
 
 
 def tg_device_status(stream: int | None) -> tuple[int, int]:
@@ -640,3 +646,14 @@ def kv_compact(cache, refs, table, out=None, stream=None):
     moved, used): new tensors, or ``out``, four that overlap none of the inputs. moved (pages,): where each page is now
     (-1: it is free), for other tables than ``table``; used (1,): how many are in use."""
     return _answer((_fast or _binding()).kv_compact(cache.args, refs, table, out, stream))
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None, stream=None):
+    """A token from each row of ``logits`` (rows, vocab), float16, bfloat16 or float32, by the given random numbers
+    ``u`` (rows,), float32 in [0, 1): from the softmax at ``temperature`` (None: 1; 0: the largest logit), of the
+    ``top_k`` largest (None or 0: all), of those at least ``min_p`` as likely as the likeliest (None: all), of the likeliest
+    that together have ``top_p`` of what is left (None: all). A setting is a number, or a tensor with one a row
+    (float32, top_k int32). The token is the first, by index, up to which the kept ones' weight exceeds u of the
+    whole; sums are exact, so it depends on nothing but its row. int32 (rows,), ``out`` if given; -1 for a row of nothing
+    but -inf or NaN. No gradient is recorded. The rules are in include/tg_gemm.h."""
+    return _answer((_fast or _binding()).sample(logits, u, temperature, top_k, top_p, min_p, out, stream))

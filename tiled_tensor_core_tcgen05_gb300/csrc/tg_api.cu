@@ -1864,3 +1864,36 @@ extern "C" tg_status tg_kv_compact(void* k_cache, void* v_cache, float* k_scale,
     cudaError_t e = launch_kv_compact(c, g_dev[dev].sm_count, stream);
     return e == cudaSuccess ? TG_OK : cuda_fail(e, "compact kernel launch");
 }
+
+extern "C" tg_status tg_sample(const void* X, int64_t row_stride, int64_t rows, int64_t vocab, int dtype, const float* u,
+                               const float* temperature, double temperature_all, const int32_t* top_k, int64_t top_k_all,
+                               const float* top_p, double top_p_all, const float* min_p, double min_p_all, int32_t* tokens,
+                               tg_stream_t stream_) {
+    t_last_error.clear();
+    const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (dtype != TG_FP16 && dtype != TG_BF16 && dtype != TG_FP32)
+        return fail(TG_ERR_INVALID_ARG, "dtype must be TG_FP16 (0), TG_BF16 (1) or TG_FP32 (2), got %d", dtype);
+    if (rows < 0 || rows > (1 << 24) || vocab < 0 || vocab > (1 << 18))
+        return fail(TG_ERR_INVALID_ARG, "sizes out of range: rows=%lld vocab=%lld (at most 2^18)", (long long)rows, (long long)vocab);
+    if (row_stride < 0 || row_stride > kIntMax) return fail(TG_ERR_INVALID_ARG, "row_stride out of range: %lld", (long long)row_stride);
+    if (std::isnan(temperature_all) || std::isnan(top_p_all) || std::isnan(min_p_all))
+        return fail(TG_ERR_INVALID_ARG, "temperature, top_p and min_p must be numbers");
+    if (rows == 0) return TG_OK;
+    if (vocab == 0) return fail(TG_ERR_INVALID_ARG, "there is nothing to draw from: vocab is 0");
+    if (!X || !u || !tokens) return fail(TG_ERR_INVALID_ARG, "X, u or tokens is NULL");
+    const int64_t size = dtype == TG_FP32 ? 4 : 2, x_bytes = ((rows - 1) * row_stride + vocab) * size;
+    if (!aligned(X, size)) return fail(TG_ERR_INVALID_ARG, "X must be aligned to its type");
+    for (const void* p : {(const void*)u, (const void*)temperature, (const void*)top_k, (const void*)top_p, (const void*)min_p, (const void*)tokens})
+        if (!aligned(p, 4)) return fail(TG_ERR_INVALID_ARG, "u, the settings and tokens must be 4-byte aligned");
+    const Piece all[7] = {{tokens, rows * 4}, {X, x_bytes}, {u, rows * 4}, {temperature, rows * 4}, {top_k, rows * 4}, {top_p, rows * 4}, {min_p, rows * 4}};
+    if (any_overlap(all, 1, 7)) return fail(TG_ERR_INVALID_ARG, "tokens overlaps an input");
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    tg_status st = current_device(&dev);
+    if (st != TG_OK) return st;
+    auto brought = [](int64_t v) { return (int)(v < 0 ? 0 : v > kIntMax ? kIntMax : v); };
+    SampleCall c{X, row_stride, rows, (int)vocab, dtype, u, temperature, top_p, min_p, top_k, (float)temperature_all, (float)top_p_all,
+                 (float)min_p_all, brought(top_k_all), tokens};
+    cudaError_t e = launch_sample(c, g_dev[dev].sm_count, stream);
+    return e == cudaSuccess ? TG_OK : cuda_fail(e, "sampling kernel launch");
+}

@@ -134,6 +134,21 @@ struct KvCompactCall {
     Watchdog wd;
 };
 
+struct SampleCall {
+    const void* x;       // (rows, vocab), vocab contiguous
+    int64_t row_stride, rows;
+    int vocab, dtype;    // tg_dtype, or kFp32
+    const float* u;
+    // a setting a row, or where null one for all
+    const float *temperature, *top_p, *min_p;
+    const int32_t* top_k;
+    float temperature_all, top_p_all, min_p_all;
+    int top_k_all;
+    int32_t* tokens;
+};
+constexpr int kFp32 = 2;
+cudaError_t launch_sample(const SampleCall& c, int sm_count, cudaStream_t stream);
+
 // Bytes of a call's workspace; its parts, if it lies at `at`.
 int64_t kv_fork_workspace(int64_t pages, int64_t batch, int64_t count, int64_t width, ForkWork* w, void* at);
 int64_t kv_compact_workspace(int64_t pages, PageWork* w, void* at);

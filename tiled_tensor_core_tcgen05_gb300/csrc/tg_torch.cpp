@@ -534,6 +534,63 @@ PyObject* kv_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// One number a row, or one for all rows, or None.
+struct Setting {
+    const void* p = nullptr;
+    double all;
+    Setting(PyObject* x, const char* name, int64_t rows, at::ScalarType type, double none) : all(none) {
+        if (x == Py_None) return;
+        if (!THPVariable_Check(x)) {
+            all = type == at::kInt ? static_cast<double>(integer(x)) : real(x);
+            return;
+        }
+        p = vector(x, name, rows, type);
+    }
+    static const void* vector(PyObject* x, const char* name, int64_t rows, at::ScalarType type) {
+        const at::Tensor& t = tensor(x, name);
+        if (t.scalar_type() != type) type_error(std::string(name) + (type == at::kInt ? " must be int32, got " : " must be float32, got ") + c10::toString(t.scalar_type()));
+        on_cuda(t, name);
+        if (t.dim() != 1 || t.size(0) != rows) value_error(std::string(name) + " must have shape (" + std::to_string(rows) + ",), got " + shape_of(t));
+        if (!t.is_contiguous()) value_error(std::string(name) + " must be contiguous");
+        return t.data_ptr();
+    }
+};
+
+// (logits, u, temperature, top_k, top_p, min_p, out or None, stream)
+PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 8, [&]() -> PyObject* {
+        const at::Tensor& X = tensor(a[0], "logits");
+        if (X.dim() != 2) value_error("logits must have shape (rows, vocab), got " + shape_of(X));
+        const int dtype = X.scalar_type() == at::kFloat ? TG_FP32 : X.scalar_type() == at::kHalf ? TG_FP16 : X.scalar_type() == at::kBFloat16 ? TG_BF16 : -1;
+        if (dtype < 0) type_error(std::string("logits must be float16, bfloat16 or float32, got ") + c10::toString(X.scalar_type()));
+        on_cuda(X, "logits");
+        const int64_t rows = X.size(0), vocab = X.size(1);
+        if (vocab > 1 && X.stride(1) != 1) value_error("logits must be contiguous along their last dimension");
+        const float* u = static_cast<const float*>(Setting::vector(a[1], "u", rows, at::kFloat));
+        const Setting t(a[2], "temperature", rows, at::kFloat, 1.0), k(a[3], "top_k", rows, at::kInt, 0.0), p(a[4], "top_p", rows, at::kFloat, 1.0), m(a[5], "min_p", rows, at::kFloat, 0.0);
+        const Where where(a[7]);
+        at::Tensor made;
+        int32_t* out;
+        if (a[6] == Py_None) {
+            made = at::empty({rows}, X.options().dtype(at::kInt));
+            out = static_cast<int32_t*>(made.data_ptr());
+        } else {
+            out = const_cast<int32_t*>(ints(a[6], "out", rows));
+        }
+        const void* x = X.data_ptr();
+        const int64_t stride = X.stride(0);
+        return answer(
+            [&] {
+                return tg_sample(x, stride, rows, vocab, dtype, u, static_cast<const float*>(t.p), t.all, static_cast<const int32_t*>(k.p), static_cast<int64_t>(k.all),
+                                 static_cast<const float*>(p.p), p.all, static_cast<const float*>(m.p), m.all, out, where.handle);
+            },
+            [&] {
+                written(a[6]);
+                return made.defined() ? THPVariable_Wrap(std::move(made)) : same(a[6]);
+            });
+    });
+}
+
 // (device that a tensor has, current device, name): the check above, for a machine with one
 PyObject* check_device_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 3, [&]() -> PyObject* {
@@ -554,6 +611,7 @@ PyMethodDef methods[] = {
     {"kv_copy", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_copy)), METH_FASTCALL, nullptr},
     {"kv_fork", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_fork)), METH_FASTCALL, nullptr},
     {"kv_compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_compact)), METH_FASTCALL, nullptr},
+    {"sample", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(sample)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
