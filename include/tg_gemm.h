@@ -492,6 +492,36 @@ tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int64_t q_head_
                           int64_t window, double scale, int dtype, void* workspace, int64_t workspace_bytes,
                           tg_stream_t stream);
 
+/*
+ * tg_attention_kv for sequences that begin with the same tokens: the keys and
+ * values of what a group shares are read once for the whole group instead of
+ * once a sequence. Group g is the sequences groups[g] .. groups[g + 1] - 1
+ * (group_count + 1 int32 offsets; sequences before the first or behind the last
+ * are in none). The first shared[g] tokens of all of them lie in the same pages:
+ * their table rows begin alike, and the kernels read the first sequence's.
+ * (Where they do not, results are those of the first sequence's pages.) A
+ * sequence whose tokens before its new ones are fewer than shared[g] (an idle
+ * slot, say) is attended by itself. No group has more than max_rows new tokens.
+ * Results are tg_attention_kv's within its own bounds; there is no window. The
+ * workspace query takes the same sizes.
+ *
+ * A shared[g] that is negative or beyond max_len or the table, and a group with
+ * more than max_rows rows, are reported (TG_ERR_BOUNDS) and make the group's
+ * sequences ones of no group. So do, for all groups, offsets that fall or are
+ * out of range.
+ */
+tg_status tg_attention_kv_shared_workspace(int64_t kv_heads, int64_t page, int64_t dim, int format, int64_t heads,
+                                           int64_t batch, int64_t total, int64_t group_count, int64_t max_new,
+                                           int64_t max_rows, int64_t max_len, int dtype, int64_t* bytes);
+tg_status tg_attention_kv_shared(const void* Q, int64_t q_token_stride, int64_t q_head_stride, void* O, float* lse,
+                                 const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                                 int64_t pages, int64_t kv_heads, int64_t page, int64_t dim, int format,
+                                 const int32_t* table, int64_t table_width, const int32_t* lens, const int32_t* cu,
+                                 int64_t batch, int64_t total, int64_t heads, int64_t max_new, int64_t max_len,
+                                 int causal, const int32_t* groups, const int32_t* shared, int64_t group_count,
+                                 int64_t max_rows, double scale, int dtype, void* workspace, int64_t workspace_bytes,
+                                 tg_stream_t stream);
+
 /* ---------------------------------------------------------------------------
  * Pages of the cache. `refs` (pages int32) counts the table entries, of all
  * tables there are, that hold each page; 0: it is free. A sequence holds the

@@ -35,6 +35,7 @@ EXPORTS = ("tg_gemm", "tg_gemm_ex", "tg_gemm_plan", "tg_gemm_staged", "tg_gemm_s
            "tg_gemm_w4_kernel", "tg_attention_fwd",
            "tg_softmax_rows", "tg_bias_gelu",
            "tg_rope", "tg_kv_append", "tg_kv_read", "tg_attention_kv_workspace", "tg_attention_kv",
+           "tg_attention_kv_shared_workspace", "tg_attention_kv_shared",
            "tg_kv_copy", "tg_kv_fork_workspace", "tg_kv_fork", "tg_kv_compact_workspace", "tg_kv_compact", "tg_sample",
            "tg_device_status", "tg_debug_status",
            "tg_set_watchdog_ns",
@@ -76,6 +77,9 @@ def bind(path: str) -> ctypes.CDLL:
     lib.tg_attention_kv_workspace.argtypes = [_i64, _i64, _i64, _int] + [_i64] * 6 + [_int, ctypes.POINTER(_i64)]
     lib.tg_attention_kv.argtypes = (strided + [_vp, _vp] + cache + batch + [_i64, _i64, _i64, _int, _i64, _dbl, _int,
                                                                             _vp, _i64, _vp])
+    lib.tg_attention_kv_shared_workspace.argtypes = [_i64, _i64, _i64, _int] + [_i64] * 7 + [_int, ctypes.POINTER(_i64)]
+    lib.tg_attention_kv_shared.argtypes = (strided + [_vp, _vp] + cache + batch + [_i64, _i64, _i64, _int, _vp, _vp, _i64, _i64, _dbl,
+                                                                                   _int, _vp, _i64, _vp])
     lib.tg_kv_copy.argtypes = [_vp] * 4 + [_i64] + [_vp] * 4 + [_i64] * 4 + [_int, _vp, _vp, _i64, _vp]
     lib.tg_kv_fork_workspace.argtypes = [_i64] * 5 + [ctypes.POINTER(_i64)]
     lib.tg_kv_fork.argtypes = cache + [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64] + [_vp] * 5 + [_i64, _vp]
@@ -99,7 +103,7 @@ def bind(path: str) -> ctypes.CDLL:
     lib.tg_shutdown.restype = None
     for name in ("tg_gemm", "tg_gemm_ex", "tg_gemm_plan", "tg_gemm_staged", "tg_gemm_splitk_noalloc", "tg_gemm_w4", "tg_gemm_w4_ex",
                  "tg_gemm_w4_kernel", "tg_attention_fwd", "tg_softmax_rows", "tg_bias_gelu", "tg_rope", "tg_kv_append", "tg_kv_read", "tg_attention_kv_workspace",
-                 "tg_attention_kv", "tg_kv_copy", "tg_kv_fork_workspace", "tg_kv_fork", "tg_kv_compact_workspace", "tg_kv_compact", "tg_sample",
+                 "tg_attention_kv", "tg_attention_kv_shared_workspace", "tg_attention_kv_shared", "tg_kv_copy", "tg_kv_fork_workspace", "tg_kv_fork", "tg_kv_compact_workspace", "tg_kv_compact", "tg_sample",
                  "tg_device_status", "tg_debug_status",
                  "tg_set_watchdog_ns", "tg_debug_skip_first_arrive", "tg_debug_bounds_limit", "tg_debug_build",
                  "tg_version"):
@@ -252,6 +256,20 @@ def tg_attention_kv_workspace(kv_heads: int, page: int, dim: int, fmt: int, head
 def tg_attention_kv(*args) -> None:
     """The C entry point's arguments in its order (include/tg_gemm.h)."""
     _check(_lib.tg_attention_kv(*args))
+
+
+def tg_attention_kv_shared_workspace(kv_heads: int, page: int, dim: int, fmt: int, heads: int, batch: int, total: int,
+                                     group_count: int, max_new: int, max_rows: int, max_len: int, dtype: int) -> int:
+    """Bytes of workspace that tg_attention_kv_shared needs for these sizes."""
+    n = _i64()
+    _check(_lib.tg_attention_kv_shared_workspace(kv_heads, page, dim, fmt, heads, batch, total, group_count, max_new,
+                                                 max_rows, max_len, dtype, ctypes.byref(n)))
+    return n.value
+
+
+def tg_attention_kv_shared(*args) -> None:
+    """The C entry point's arguments in its order (include/tg_gemm.h)."""
+    _check(_lib.tg_attention_kv_shared(*args))
 
 
 def tg_kv_copy(*args) -> None:
@@ -622,6 +640,18 @@ def attention_kv(Q, cache, table, lens, cu=None, max_new: int = 1, max_len: int 
     recorded."""
     return _answer((_fast or _binding()).attention_kv(Q, cache.args, table, lens, cu, max_new, max_len, causal, window,
                                                       scale, return_lse, out, stream))
+
+
+def attention_kv_shared(Q, cache, table, lens, groups, shared, cu=None, max_new: int = 1, max_rows: int | None = None,
+                        max_len: int | None = None, causal: bool = True, scale: float | None = None,
+                        return_lse: bool = False, out=None, stream=None):
+    """``attention_kv`` where sequences begin with the same tokens, which are then read once for all of them: group g is
+    the sequences groups[g] .. groups[g + 1] - 1 (int32), and the first shared[g] tokens (int32) of each lie in the
+    same pages, so their rows of ``table`` begin alike. max_rows: no group has more new tokens (None: their
+    total). Sequences in no group, and those that have fewer tokens before their new ones than their group shares, are
+    attended by themselves. The rest is as in ``attention_kv``, without a window."""
+    return _answer((_fast or _binding()).attention_kv_shared(Q, cache.args, table, lens, groups, shared, cu, max_new, max_rows,
+                                                             max_len, causal, scale, return_lse, out, stream))
 
 
 def kv_copy(cache, src, dst, to=None, stream=None) -> None:

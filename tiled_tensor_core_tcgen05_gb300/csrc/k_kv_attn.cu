@@ -74,6 +74,7 @@ struct SeqWork {
     int chunk0, chunks;    // 64-token chunks that any of its rows sees (at least one, perhaps empty)
     int blocks;            // row blocks per kv head
     int64_t total;         // chunks over its units
+    int begin;             // keys before it are another call's
 };
 
 template <int kTiles>
@@ -88,7 +89,8 @@ __device__ __forceinline__ SeqWork seq_work(const SplitWork& a, int i) {
         report_range(c.wd);
         w.len = 0;
     }
-    const int64_t begin = c.window > 0 ? static_cast<int64_t>(w.len) - w.count - c.window + 1 : 0;
+    w.begin = c.begin != nullptr ? __ldg(c.begin + i) : 0;
+    const int64_t begin = c.window > 0 ? static_cast<int64_t>(w.len) - w.count - c.window + 1 : w.begin;
     w.chunk0 = begin > 0 ? static_cast<int>(begin / kChunk) : 0;
     w.chunks = max(1, (w.len + kChunk - 1) / kChunk - w.chunk0);
     w.blocks = static_cast<int>((static_cast<int64_t>(w.count) * a.share + 8 * kTiles - 1) / (8 * kTiles));
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int c0 = max(0, e0 - a.extra), c1 = max(0, e1 - a.extra);
         const int head = unit / w.blocks, block = unit - head * w.blocks;
         if (first_segment && threadIdx.x == 0) {
-            Meta m{pos - e0, total, c0 > 0 ? w.chunks : 0, head, block, w.first, w.count};
+            Meta m{pos - e0, total, c0 > 0 ? w.chunks : 0, head, block, w.first, w.count, w.begin > 0};
             a.meta[k] = m;
         }
         pos += e1 - e0;
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         else i1 = min(i1, (w.len - tok0 + kChunk - 1) / kChunk);
         if (see0 > tok0) i0 = static_cast<int>(min(static_cast<int64_t>(i1), (see0 - tok0) / kChunk));
         const int n_steps = i1 - i0;
-        const int32_t* table = c.batch.table + static_cast<int64_t>(seq) * c.batch.table_width;
+        const int32_t* table = table_row(c.batch, seq);
 
         // page and scales of 32 steps at a time, a step a lane; those of the next 32 in advance
         auto page_of = [&](int s) {
@@ -570,10 +572,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             if (whole) {
                 const int t = (row0 + r) / a.share;
                 const int64_t to = static_cast<int64_t>(w.first + t) * c.heads + head * a.share + (row0 + r) - t * a.share;
-                const float inv = row_inverse(sum);
-                E h[4] = {from_float<E>(v.x * inv), from_float<E>(v.y * inv), from_float<E>(v.z * inv), from_float<E>(v.w * inv)};
-                *reinterpret_cast<uint2*>(static_cast<E*>(c.out) + to * kDim + d) = *reinterpret_cast<const uint2*>(h);
-                if (d == 0 && c.lse != nullptr) c.lse[to] = row_lse(top, sum);
+                float x[4] = {v.x, v.y, v.z, v.w};
+                finish_row<E, kDim, 4>(c, to, d, x, top, sum, w.begin > 0);
             } else {
                 *reinterpret_cast<float4*>(part + r * kDim + d) = v;
                 if (d == 0) {
@@ -632,7 +632,9 @@ FewPlan few_plan(const KvAttnCall& c, int sm_count) {
 // the quicker one throughout. From there to 128 it depends on the lengths, by up to a fifth either way, and
 // calls too small to fill the GPU stay quicker here further on (two of 2000, 128 rows 21 and 27, 256 rows 27 and
 // 34): the rule does not look at either.
-bool few_rows(const KvAttnCall& c) { return static_cast<int64_t>(c.batch.max_new) * (c.heads / c.cache.kv_heads) <= 64; }
+bool few_rows(const KvAttnCall& c) {
+    return static_cast<int64_t>(c.batch.max_new) * (c.heads / c.cache.kv_heads) <= 64;
+}
 
 template <typename E, int kFmt, int kDim, int kTiles>
 cudaError_t launch_few(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, const FewPlan& p,
@@ -672,6 +674,8 @@ cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMa
 }
 
 }  // namespace
+
+bool kv_attn_few_rows(const KvAttnCall& c) { return few_rows(c); }
 
 int kv_attn_box_rows(const KvAttnCall& c) { return kStep * c.cache.dim / 128; }
 

@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (true) {
             // all of the half go on, or none: no warp waits at a barrier for one that has left
             if (named_barrier_or(1 + h, 256, !next_segment(sg))) break;
-            if (first_segment && threadIdx.x == 0) a.meta[k] = Meta{start - sg.t0, total, sg.t0 > 0 ? sg.tiles : 0, sg.head, sg.block, sg.first, sg.count};
+            if (first_segment && threadIdx.x == 0) a.meta[k] = Meta{start - sg.t0, total, sg.t0 > 0 ? sg.tiles : 0, sg.head, sg.block, sg.first, sg.count, 0};
             const int r = sg.block * kRows + h * kHalfRows + row;      // row of the (sequence, kv head)
             const bool real = r < sg.count * a.share;
             const int t = r / a.share;
@@ -742,7 +742,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 tmem_ld_32x32b_x32(col_o + i, o);
                 tmem_ld_wait();
-                if (real && whole) {
+                if (real && whole && c.found != nullptr) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4*>(c.found + out_row * kDim + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                } else if (real && whole) {
                     E* y = static_cast<E*>(c.out) + out_row * kDim + d;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
@@ -757,7 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4*>(part + pr * kDim + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
             }
-            if (real && whole && kh == 0 && c.lse != nullptr) c.lse[out_row] = row_lse(m, l);
+            if (real && whole && kh == 0 && c.found != nullptr) c.found_weight[out_row] = make_float2(m, l);
+            else if (real && whole && kh == 0 && c.lse != nullptr) c.lse[out_row] = row_lse(m, l);
             if (real && !whole && kh == 0) {
                 part[kRows * kDim + pr] = m;
                 part[kRows * (kDim + 1) + pr] = l;

@@ -1631,6 +1631,52 @@ extern "C" tg_status tg_attention_kv_workspace(int64_t kv_heads, int64_t page, i
     return TG_OK;
 }
 
+namespace {
+
+// The checks of an attention call, beyond its sizes.
+tg_status check_attention(const void* Q, int64_t q_token_stride, int64_t q_head_stride, void* O, float* lse, int64_t total, int causal, int64_t window,
+                          double scale, void* workspace, int64_t workspace_bytes, KvAttnCall* c) {
+    if (causal != 0 && causal != 1) return fail(TG_ERR_INVALID_ARG, "causal must be 0 or 1, got %d", causal);
+    if (!causal && window > 0) return fail(TG_ERR_INVALID_ARG, "a window needs the causal mask");
+    if (!std::isfinite(static_cast<float>(scale)))
+        return fail(TG_ERR_INVALID_ARG, "scale must be finite in 32 bits");
+    tg_status st = check_strides("Q", q_token_stride, q_head_stride);
+    if (st != TG_OK || total == 0) return st;
+    if (!Q || !O) return fail(TG_ERR_INVALID_ARG, "Q or O is NULL");
+    if (!(aligned(Q, 2) && aligned(O, 16) && aligned(lse, 4) && aligned(workspace, 16)))
+        return fail(TG_ERR_INVALID_ARG, "O and the workspace must be 16-byte aligned, Q 2-byte, lse 4-byte");
+    const KvCacheArgs& k = c->cache;
+    const int64_t codes = k.pages * k.kv_heads * k.page * k.dim, o_bytes = total * c->heads * k.dim * 2;
+    const int64_t l_bytes = lse ? total * c->heads * 4 : 0;
+    const int64_t q_bytes = span_bytes(total, c->heads, k.dim, q_token_stride, q_head_stride);
+    const void* in[5] = {Q, k.k, k.v, k.k_scale, k.v_scale};
+    const int64_t in_bytes[5] = {q_bytes, codes, codes, k.pages * k.kv_heads * 4, k.pages * k.kv_heads * 4};
+    for (int i = 0; i < 5; ++i)
+        if (overlaps(O, o_bytes, in[i], in_bytes[i]) || overlaps(lse, l_bytes, in[i], in_bytes[i]) ||
+            overlaps(workspace, workspace_bytes, in[i], in_bytes[i]))
+            return fail(TG_ERR_INVALID_ARG, "an output or the workspace overlaps an input");
+    if (overlaps(O, o_bytes, lse, l_bytes) || overlaps(workspace, workspace_bytes, O, o_bytes) ||
+        overlaps(workspace, workspace_bytes, lse, l_bytes))
+        return fail(TG_ERR_INVALID_ARG, "the outputs and the workspace overlap each other");
+    c->q = Strided{const_cast<void*>(Q), q_token_stride, q_head_stride};
+    c->out = O;
+    c->lse = lse;
+    c->causal = causal;
+    c->scale = static_cast<float>(scale);
+    return TG_OK;
+}
+
+// The codes as lines of 128 bytes (a cache without pages is never read: any address serves).
+tg_status attention_maps(const KvAttnCall& c, CUtensorMap* tmK, CUtensorMap* tmV) {
+    const KvCacheArgs& k = c.cache;
+    const uint64_t lines = k.pages > 0 ? static_cast<uint64_t>(k.pages * k.kv_heads * k.page * k.dim) / 128 : 1;
+    const uint32_t box = static_cast<uint32_t>(kv_attn_box_rows(c));
+    tg_status st = make_map_u8(tmK, k.pages > 0 ? k.k : c.out, 128, lines, 128, box);
+    return st != TG_OK ? st : make_map_u8(tmV, k.pages > 0 ? k.v : c.out, 128, lines, 128, box);
+}
+
+}  // namespace
+
 extern "C" tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int64_t q_head_stride, void* O, float* lse,
                                      const void* k_cache, const void* v_cache, const float* k_scale,
                                      const float* v_scale, int64_t pages, int64_t kv_heads, int64_t page, int64_t dim,
@@ -1645,49 +1691,96 @@ extern "C" tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int6
     if (st != TG_OK) return st;
     if ((st = check_batch(table, table_width, lens, cu, batch, total, max_new, page, &c.batch)) != TG_OK) return st;
     if ((st = kv_attn_sizes(kv_heads, page, heads, total, max_len, window, dtype, &c)) != TG_OK) return st;
-    if (causal != 0 && causal != 1) return fail(TG_ERR_INVALID_ARG, "causal must be 0 or 1, got %d", causal);
-    if (!causal && window > 0) return fail(TG_ERR_INVALID_ARG, "a window needs the causal mask");
-    if (!std::isfinite(static_cast<float>(scale)))
-        return fail(TG_ERR_INVALID_ARG, "scale must be finite in 32 bits");
-    if ((st = check_strides("Q", q_token_stride, q_head_stride)) != TG_OK) return st;
+    if ((st = check_attention(Q, q_token_stride, q_head_stride, O, lse, total, causal, window, scale, workspace, workspace_bytes, &c)) != TG_OK) return st;
     if (total == 0) return TG_OK;
-    if (!Q || !O) return fail(TG_ERR_INVALID_ARG, "Q or O is NULL");
-    if (!(aligned(Q, 2) && aligned(O, 16) && aligned(lse, 4) && aligned(workspace, 16)))
-        return fail(TG_ERR_INVALID_ARG, "O and the workspace must be 16-byte aligned, Q 2-byte, lse 4-byte");
-    const int64_t codes = pages * kv_heads * page * dim, o_bytes = total * heads * dim * 2;
-    const int64_t l_bytes = lse ? total * heads * 4 : 0;
-    const int64_t q_bytes = span_bytes(total, heads, dim, q_token_stride, q_head_stride);
-    const void* in[5] = {Q, k_cache, v_cache, k_scale, v_scale};
-    const int64_t in_bytes[5] = {q_bytes, codes, codes, pages * kv_heads * 4, pages * kv_heads * 4};
-    for (int i = 0; i < 5; ++i)
-        if (overlaps(O, o_bytes, in[i], in_bytes[i]) || overlaps(lse, l_bytes, in[i], in_bytes[i]) ||
-            overlaps(workspace, workspace_bytes, in[i], in_bytes[i]))
-            return fail(TG_ERR_INVALID_ARG, "an output or the workspace overlaps an input");
-    if (overlaps(O, o_bytes, lse, l_bytes) || overlaps(workspace, workspace_bytes, O, o_bytes) ||
-        overlaps(workspace, workspace_bytes, lse, l_bytes))
-        return fail(TG_ERR_INVALID_ARG, "the outputs and the workspace overlap each other");
-
     std::lock_guard<std::mutex> lock(g_mu);
     int dev = 0;
     if ((st = current_device(&dev)) != TG_OK) return st;
-    c.q = Strided{const_cast<void*>(Q), q_token_stride, q_head_stride};
-    c.out = O;
-    c.lse = lse;
-    c.causal = causal;
-    c.scale = static_cast<float>(scale);
     c.wd = watchdog(g_dev[dev]);
     const int64_t need = kv_attn_workspace(c, g_dev[dev].sm_count);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return fail(TG_ERR_INVALID_ARG, "tg_attention_kv needs a workspace of %lld bytes, got %lld", (long long)need,
                     (long long)(workspace ? workspace_bytes : 0));
-    // the codes as lines of 128 bytes (a cache without pages is never read: any address serves)
-    const uint64_t lines = pages > 0 ? static_cast<uint64_t>(codes) / 128 : 1;
     CUtensorMap tmK, tmV;
-    const uint32_t box = static_cast<uint32_t>(kv_attn_box_rows(c));
-    if ((st = make_map_u8(&tmK, pages > 0 ? k_cache : O, 128, lines, 128, box)) != TG_OK) return st;
-    if ((st = make_map_u8(&tmV, pages > 0 ? v_cache : O, 128, lines, 128, box)) != TG_OK) return st;
+    if ((st = attention_maps(c, &tmK, &tmV)) != TG_OK) return st;
     cudaError_t e = launch_kv_attn(c, tmK, tmV, workspace, g_dev[dev].sm_count, stream);
     return e == cudaSuccess ? TG_OK : cuda_fail(e, "cache attention kernel launch");
+}
+
+namespace {
+
+tg_status check_groups(int64_t total, int64_t group_count, int64_t max_rows, const KvAttnCall& c, KvSharedCall* s) {
+    if (group_count < 0 || group_count > c.batch.batch)
+        return fail(TG_ERR_INVALID_ARG, "there are at most as many groups as sequences, got %lld of %d", (long long)group_count, c.batch.batch);
+    if (max_rows < 0 || (max_rows < 1 && total > 0 && group_count > 0))
+        return fail(TG_ERR_INVALID_ARG, "max_rows must be at least 1, got %lld", (long long)max_rows);
+    s->c = c;
+    s->group_count = (int)group_count;
+    s->max_rows = (int)(max_rows < total ? max_rows : total);
+    return TG_OK;
+}
+
+}  // namespace
+
+extern "C" tg_status tg_attention_kv_shared_workspace(int64_t kv_heads, int64_t page, int64_t dim, int format,
+                                                      int64_t heads, int64_t batch, int64_t total, int64_t group_count,
+                                                      int64_t max_new, int64_t max_rows, int64_t max_len, int dtype,
+                                                      int64_t* bytes) {
+    t_last_error.clear();
+    if (bytes == nullptr) return fail(TG_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = 0;
+    KvAttnCall c{};
+    KvSharedCall s{};
+    static const int32_t some = 0;
+    tg_status st = check_cache(nullptr, nullptr, nullptr, nullptr, 0, kv_heads, page, dim, format, &c.cache);
+    if (st != TG_OK) return st;
+    if ((st = check_batch(&some, 0, &some, &some, batch, total, max_new, page, &c.batch)) != TG_OK) return st;
+    if ((st = kv_attn_sizes(kv_heads, page, heads, total, max_len, 0, dtype, &c)) != TG_OK) return st;
+    if ((st = check_groups(total, group_count, max_rows, c, &s)) != TG_OK) return st;
+    if (total == 0) return TG_OK;
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    if ((st = current_device(&dev)) != TG_OK) return st;
+    *bytes = kv_attn_shared_workspace(s, g_dev[dev].sm_count);
+    return TG_OK;
+}
+
+extern "C" tg_status tg_attention_kv_shared(const void* Q, int64_t q_token_stride, int64_t q_head_stride, void* O, float* lse,
+                                            const void* k_cache, const void* v_cache, const float* k_scale,
+                                            const float* v_scale, int64_t pages, int64_t kv_heads, int64_t page,
+                                            int64_t dim, int format, const int32_t* table, int64_t table_width,
+                                            const int32_t* lens, const int32_t* cu, int64_t batch, int64_t total,
+                                            int64_t heads, int64_t max_new, int64_t max_len, int causal,
+                                            const int32_t* groups, const int32_t* shared, int64_t group_count,
+                                            int64_t max_rows, double scale, int dtype, void* workspace,
+                                            int64_t workspace_bytes, tg_stream_t stream_) {
+    t_last_error.clear();
+    const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    KvAttnCall c{};
+    KvSharedCall s{};
+    tg_status st = check_cache(k_cache, v_cache, k_scale, v_scale, pages, kv_heads, page, dim, format, &c.cache);
+    if (st != TG_OK) return st;
+    if ((st = check_batch(table, table_width, lens, cu, batch, total, max_new, page, &c.batch)) != TG_OK) return st;
+    if ((st = kv_attn_sizes(kv_heads, page, heads, total, max_len, 0, dtype, &c)) != TG_OK) return st;
+    if ((st = check_attention(Q, q_token_stride, q_head_stride, O, lse, total, causal, 0, scale, workspace, workspace_bytes, &c)) != TG_OK) return st;
+    if ((st = check_groups(total, group_count, max_rows, c, &s)) != TG_OK) return st;
+    if (total == 0) return TG_OK;
+    if (group_count > 0 && (!groups || !shared)) return fail(TG_ERR_INVALID_ARG, "groups or shared is NULL");
+    if (!(aligned(groups, 4) && aligned(shared, 4))) return fail(TG_ERR_INVALID_ARG, "groups and shared must be 4-byte aligned");
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    if ((st = current_device(&dev)) != TG_OK) return st;
+    s.c.wd = watchdog(g_dev[dev]);
+    s.groups = groups;
+    s.shared = shared;
+    const int64_t need = kv_attn_shared_workspace(s, g_dev[dev].sm_count);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+        return fail(TG_ERR_INVALID_ARG, "tg_attention_kv_shared needs a workspace of %lld bytes, got %lld", (long long)need,
+                    (long long)(workspace ? workspace_bytes : 0));
+    CUtensorMap tmK, tmV;
+    if ((st = attention_maps(s.c, &tmK, &tmV)) != TG_OK) return st;
+    cudaError_t e = launch_kv_attn_shared(s, tmK, tmV, workspace, g_dev[dev].sm_count, stream);
+    return e == cudaSuccess ? TG_OK : cuda_fail(e, "shared cache attention kernel launch");
 }
 
 namespace {

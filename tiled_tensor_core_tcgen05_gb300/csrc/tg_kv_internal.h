@@ -43,6 +43,7 @@ struct KvBatch {
     const int32_t* lens;   // batch lengths (append: before the call; attention: with the new tokens)
     const int32_t* cu;     // batch + 1 offsets into the packed rows, or null: one row a sequence
     int batch, total, max_new;
+    const int32_t* rows;   // row of `table` of each sequence, or null: its own number
 };
 
 struct RopeCall {
@@ -82,6 +83,22 @@ struct KvAttnCall {
     int64_t window;      // 0: none
     float scale;
     Watchdog wd;
+    // Rows in parts. Keys before begin[i] (a multiple of 64; null: 0) of sequence i are left out, and what another call
+    // found there is added: `seed`. A call with `found` leaves that instead of out and lse: for each row and head
+    // the values times their weights, and the weights' reference (base 2) and sum.
+    const int32_t* begin;
+    const float* seed;          // (total, heads, dim)
+    const float2* seed_weight;  // (total, heads)
+    float* found;
+    float2* found_weight;
+};
+
+// Attention of sequences that begin with the same tokens: groups of sequences, and how many tokens each group shares.
+struct KvSharedCall {
+    KvAttnCall c;
+    const int32_t* groups;
+    const int32_t* shared;
+    int group_count, max_rows;
 };
 
 // A page's first tokens on their way to another page.
@@ -160,6 +177,10 @@ cudaError_t launch_rope(const RopeCall& c, int sm_count, cudaStream_t stream);
 cudaError_t launch_kv_append(const KvAppendCall& c, int sm_count, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvReadCall& c, int sm_count, cudaStream_t stream);
 int64_t kv_attn_workspace(const KvAttnCall& c, int sm_count);
+int64_t kv_attn_shared_workspace(const KvSharedCall& s, int sm_count);
+cudaError_t launch_kv_attn_shared(const KvSharedCall& s, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace,
+                                  int sm_count, cudaStream_t stream);
+bool kv_attn_few_rows(const KvAttnCall& c);  // whether a call runs in the kernel for few rows
 int64_t kv_attn_tile_workspace(const KvAttnCall& c, int sm_count);
 cudaError_t launch_kv_attn_tile(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace,
                                 int sm_count, cudaStream_t stream);

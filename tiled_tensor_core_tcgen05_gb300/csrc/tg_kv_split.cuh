@@ -71,6 +71,7 @@ struct Meta {
     int64_t unit_start, total;
     int chunks, head, block;
     int first, count;   // the sequence's rows of the packed tensors
+    int seeded;         // whether another call's part is to be added
 };
 
 // A split call: what both kernels and the join need.
@@ -150,13 +151,45 @@ __device__ __forceinline__ void clear_row(const KvAttnCall& c, int64_t r) {
 // does it while the parts are being computed; where there is none, the kernel itself.
 template <typename E, int kDim>
 __device__ __forceinline__ void clear_uncovered(const KvAttnCall& c) {
-    if (c.batch.cu == nullptr) return;
+    if (c.batch.cu == nullptr || c.found != nullptr) return;
     const Uncovered none = uncovered(c.batch);
     const int many = none.before + c.batch.total - none.after;
     for (int i = blockIdx.x; i < many; i += gridDim.x) clear_row<E, kDim>(c, i < none.before ? i : none.after + i - none.before);
     for (int i = blockIdx.x; i < c.batch.batch; i += gridDim.x)
         if (seq_span(c.batch, i, c.wd).bad)
             for (int r = packed_row(c.batch, i); r < packed_row(c.batch, i + 1); ++r) clear_row<E, kDim>(c, r);
+}
+
+// kN values from d on of row and head `to`, all of whose parts are joined: their sum v of values times weights, the
+// weights' reference and sum. Adds another call's part if the sequence has one, and writes what the call leaves.
+template <typename E, int kDim, int kN>
+__device__ __forceinline__ void finish_row(const KvAttnCall& c, int64_t to, int d, float (&v)[kN], float top, float sum, bool seeded) {
+    if (c.found != nullptr) {
+#pragma unroll
+        for (int i = 0; i < kN; i += 2) *reinterpret_cast<float2*>(c.found + to * kDim + d + i) = make_float2(v[i], v[i + 1]);
+        if (d == 0) c.found_weight[to] = make_float2(top, sum);
+        return;
+    }
+    if (seeded) {
+        const float2 w = c.seed_weight[to];
+        const float all = fmaxf(top, w.x), a = ex2_approx(top - all), b = ex2_approx(w.x - all);
+        top = all;
+        sum = fmaf(sum, a, w.y * b);
+#pragma unroll
+        for (int i = 0; i < kN; i += 2) {
+            const float2 x = *reinterpret_cast<const float2*>(c.seed + to * kDim + d + i);
+            v[i] = fmaf(v[i], a, x.x * b);
+            v[i + 1] = fmaf(v[i + 1], a, x.y * b);
+        }
+    }
+    const float inv = row_inverse(sum);
+    E out[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) out[i] = from_float<E>(v[i] * inv);
+    E* y = static_cast<E*>(c.out) + to * kDim + d;
+    if constexpr (kN == 4) *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(out);
+    else *reinterpret_cast<uint32_t*>(y) = *reinterpret_cast<const uint32_t*>(out);
+    if (d == 0 && c.lse != nullptr) c.lse[to] = row_lse(top, sum);
 }
 
 // Joins the parts of the unit inside which share k begins, if k's is its first border: block
@@ -232,14 +265,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const SplitWo
     }
     const int t = row / a.share;
     const int64_t to = static_cast<int64_t>(m.first + t) * c.heads + m.head * a.share + row - t * a.share;
-    const float inv = row_inverse(sum);
-    E out[kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i) out[i] = from_float<E>(v[i] * inv);
-    E* y = static_cast<E*>(c.out) + to * kDim + lane * kN;
-    if constexpr (kN == 4) *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(out);
-    else *reinterpret_cast<uint32_t*>(y) = *reinterpret_cast<const uint32_t*>(out);
-    if (lane == 0 && c.lse != nullptr) c.lse[to] = row_lse(top, sum);
+    finish_row<E, kDim, kN>(c, to, lane * kN, v, top, sum, m.seeded != 0);
 }
 
 // Launches the join so that its blocks are in place when the parts are.

@@ -365,6 +365,34 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// What an attention call leaves: O, and the log of the sums if wanted.
+struct Attended {
+    at::Tensor made, lse;
+    PyObject* out;
+    void* po;
+    float* pl;
+    Attended(PyObject* given, const at::Tensor& Q, bool want_lse) : out(given) {
+        if (out == Py_None) made = at::empty({Q.size(0), Q.size(1), Q.size(2)}, Q.options());
+        const at::Tensor& O = out == Py_None ? made : tensor(out, "out");
+        if (O.sizes() != Q.sizes() || O.scalar_type() != Q.scalar_type() || !O.is_cuda() || !O.is_contiguous())
+            value_error("out must be a contiguous CUDA tensor of Q's shape and type");
+        on_cuda(O, "out");
+        if (want_lse) lse = at::empty({Q.size(0), Q.size(1)}, Q.options().dtype(at::kFloat));
+        po = O.data_ptr();
+        pl = want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr;
+    }
+    PyObject* answer() {
+        written(out);
+        PyObject* o = made.defined() ? THPVariable_Wrap(std::move(made)) : same(out);
+        if (pl == nullptr && !lse.defined()) return o;
+        PyObject* pair = o == nullptr ? nullptr : PyTuple_New(2);
+        if (pair == nullptr) return nullptr;
+        PyTuple_SET_ITEM(pair, 0, o);
+        PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(std::move(lse)));
+        return pair;
+    }
+};
+
 // (Q, cache, table, lens, cu, max_new, max_len, causal, window, scale, return_lse, out, stream)
 PyObject* attention_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 13, [&]() -> PyObject* {
@@ -383,31 +411,52 @@ PyObject* attention_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int64_t need = 0;
         const int status = tg_attention_kv_workspace(c.kv_heads, c.page, D, c.format, H, b.batch, T, max_new, max_len, window, dtype, &need);
         if (status != TG_OK) return PyLong_FromLong(status);
-        at::Tensor made, lse, work;
-        if (a[11] == Py_None) made = at::empty({T, H, D}, Q.options());
-        const at::Tensor& O = a[11] == Py_None ? made : tensor(a[11], "out");
-        if (O.sizes() != Q.sizes() || O.scalar_type() != Q.scalar_type() || !O.is_cuda() || !O.is_contiguous())
-            value_error("out must be a contiguous CUDA tensor of Q's shape and type");
-        on_cuda(O, "out");
-        if (want_lse) lse = at::empty({T, H}, Q.options().dtype(at::kFloat));
+        Attended o(a[11], Q, want_lse);
+        at::Tensor work;
         if (need > 0) work = at::empty({need}, Q.options().dtype(at::kByte));
-        void *po = O.data_ptr(), *pw = need > 0 ? work.data_ptr() : nullptr;
-        float* pl = want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr;
+        void* pw = need > 0 ? work.data_ptr() : nullptr;
         return answer(
             [&] {
-                return tg_attention_kv(q.p, q.token, q.head, po, pl, c.k, c.v, c.ks, c.vs, c.pages, c.kv_heads, c.page, c.dim, c.format, b.table, b.width, b.lens,
+                return tg_attention_kv(q.p, q.token, q.head, o.po, o.pl, c.k, c.v, c.ks, c.vs, c.pages, c.kv_heads, c.page, c.dim, c.format, b.table, b.width, b.lens,
                                        b.cu, b.batch, T, H, max_new, max_len, causal, window, scale, dtype, pw, need, where.handle);
             },
-            [&]() -> PyObject* {
-                written(a[11]);
-                PyObject* o = made.defined() ? THPVariable_Wrap(std::move(made)) : same(a[11]);
-                if (!want_lse || o == nullptr) return o;
-                PyObject* pair = PyTuple_New(2);
-                if (pair == nullptr) return nullptr;
-                PyTuple_SET_ITEM(pair, 0, o);
-                PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(std::move(lse)));
-                return pair;
-            });
+            [&] { return o.answer(); });
+    });
+}
+
+// (Q, cache, table, lens, groups, shared, cu, max_new, max_rows, max_len, causal, scale, return_lse, out, stream)
+PyObject* attention_kv_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 15, [&]() -> PyObject* {
+        const at::Tensor& Q = tensor(a[0], "Q");
+        const Rows q = rows(Q, "Q");
+        const int dtype = dtype_code(Q, "Q");
+        const Cache c = cache(a[1]);
+        const int64_t T = Q.size(0), H = Q.size(1), D = Q.size(2);
+        if (D != c.dim) value_error("Q must have shape (total, heads, " + std::to_string(c.dim) + "), got " + shape_of(Q));
+        const Batch b = batch(a[2], a[3], a[6]);
+        const at::Tensor& s = tensor(a[5], "shared");
+        if (s.dim() != 1) value_error("shared must be a vector, got " + shape_of(s));
+        const int64_t G = s.size(0);
+        const int32_t *shared = ints(a[5], "shared", G), *groups = ints(a[4], "groups", G + 1);
+        const int64_t max_new = integer(a[7]), max_rows = a[8] == Py_None ? T : integer(a[8]), max_len = a[9] == Py_None ? b.width * c.page : integer(a[9]);
+        const int causal = truth(a[10]);
+        const double scale = a[11] == Py_None ? 1.0 / std::sqrt(static_cast<double>(D)) : real(a[11]);
+        const bool want_lse = truth(a[12]);
+        const Where where(a[14]);
+        int64_t need = 0;
+        const int status = tg_attention_kv_shared_workspace(c.kv_heads, c.page, D, c.format, H, b.batch, T, G, max_new, max_rows, max_len, dtype, &need);
+        if (status != TG_OK) return PyLong_FromLong(status);
+        Attended o(a[13], Q, want_lse);
+        at::Tensor work;
+        if (need > 0) work = at::empty({need}, Q.options().dtype(at::kByte));
+        void* pw = need > 0 ? work.data_ptr() : nullptr;
+        return answer(
+            [&] {
+                return tg_attention_kv_shared(q.p, q.token, q.head, o.po, o.pl, c.k, c.v, c.ks, c.vs, c.pages, c.kv_heads, c.page, c.dim, c.format, b.table, b.width,
+                                              b.lens, b.cu, b.batch, T, H, max_new, max_len, causal, groups, shared, G, max_rows, scale, dtype, pw, need,
+                                              where.handle);
+            },
+            [&] { return o.answer(); });
     });
 }
 
@@ -608,6 +657,7 @@ PyMethodDef methods[] = {
     {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_append)), METH_FASTCALL, nullptr},
     {"kv_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_read)), METH_FASTCALL, nullptr},
     {"attention_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention_kv)), METH_FASTCALL, nullptr},
+    {"attention_kv_shared", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention_kv_shared)), METH_FASTCALL, nullptr},
     {"kv_copy", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_copy)), METH_FASTCALL, nullptr},
     {"kv_fork", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_fork)), METH_FASTCALL, nullptr},
     {"kv_compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_compact)), METH_FASTCALL, nullptr},
