@@ -39,7 +39,7 @@ def draw(x, u, t, k, p, m):
     if m > 0:
         keep &= y >= math.log(min(m, 1.0))
     w = y.exp() * keep
-    w = torch.where(w < 2.0 ** -45, 0.0, w)
+    w = torch.where(w < 2.0 ** -43, 0.0, w)  # less than half a unit of the weights is none
     whole = bool((w == w.round()).all())
     sure = True
     if p < 1:
