@@ -1,5 +1,5 @@
 """GPU checks of drawing tokens, against the definition in 64 bits on the CPU: whole numbers, equal or wrong. The sums of
-a row in 64 bits are good to 2^-35 of themselves (2^18 additions of 2^-53 each), the kernel's weights to 2^-38 of
+a row in 64 bits are good to 2^-35 of themselves (2^18 additions of 2^-53 each), the kernel's weights to 2^-37 of
 themselves: where a border (of the mass, or of u) lies nearer than 2^-34 of the sum to a token's edge either token may
 be right, and a test's inputs have none such. Weights that are whole are exact on both sides."""
 import math

@@ -7,7 +7,7 @@
 // two tokens of a vocabulary of 10^5, whose shares are about 10^-5 of the sum or
 // less: sums in 32 bits, off by 10^-7 and by how the row was split, would give
 // another token in one row of some hundreds. So weights are integers, of 2^-42 of the
-// row's largest, from a 2^t good to 2^-40 (weigh), and sums of them are exact
+// row's largest, good to 2^-37 (weigh), and sums of them are exact
 // in 64 bits: the same whatever the order, the split and the rest of the batch.
 //
 // Order: a token's rank is that of its 64-bit `place`: the logit's bits as an
@@ -17,15 +17,16 @@
 // A cluster of CTAs takes a row, each CTA a stretch of it, which the first pass leaves in
 // shared memory: the logits are read from HBM once. The passes, of which a row makes
 // those its settings ask for:
-//   1  the largest logit (a greedy row ends here);
-//   2  a count in each of kBins bins of t, 1/32 wide, and where top_p needs it the exact
-//      mass: the bin with the k-th, and a guess at the bin in which the mass reaches top_p;
-//   3  the tokens down to that bin, brought together where they are at most kList: the first
-//      CTA sorts them, cuts, and draws.
-// Otherwise:
-//   4  the exact mass above, and in each bin near the guess; the border's bin, its
-//      tokens brought together and sorted: the cut;
-//   5  the mass of what is kept, group by group of 32 lanes' pieces; the group,
+//   1  the largest logit (a greedy row ends here), and the largest of each thread's;
+//   2  where top_p needs it, the exact weight of all;
+//   3  a threshold from the threads' largest: as many of them are above it as top_k wants, or as much
+//      weight as top_p does, so what the row keeps is above it, and not much else;
+//   4  the tokens above it, brought together in order where they are at most kList: the first
+//      CTA cuts and draws. Few rows go on:
+//   5  a count in each of kBins bins of t, 1/32 wide: the bin with the k-th, and a guess at the bin in which
+//      the weight reaches top_p; the exact weight above, and in each bin near the guess;
+//   6  the tokens of the border's bin, brought together and sorted: the cut;
+//   7  the weight of what is kept, group by group of 32 lanes' pieces; the group,
 //      lane and token in which u of it is passed.
 #include "tg_device.cuh"
 #include "tg_kv.cuh"
@@ -44,9 +45,10 @@ constexpr int kUnit = 42;                    // weights are multiples of 2^-42
 constexpr int kSteps = 256;                  // of the table of powers: 2^(j / 256)
 constexpr int kBinSteps = 8;                 // of a bin
 constexpr int kBins = (kUnit + 3) * kSteps / kBinSteps;
-constexpr int kWindow = 16;                  // bins whose mass is taken exactly at a time
 constexpr int kList = 2048;                  // tokens that are sorted at a time
 constexpr int kSub = 1024;                   // parts of a bin that holds more
+constexpr int kSome = kThreads;              // tokens of a bin that are ranked by comparing each with each
+constexpr int kGuess = 1280;                 // threads' largest above a threshold that the list can be expected to hold
 constexpr int kMostGroups = (1 << 18) / 128 / kMaxCtas + 2;  // of a CTA
 constexpr float kNone = -INFINITY;
 using u64 = unsigned long long;
@@ -72,7 +74,7 @@ constexpr Powers make_powers() {
     for (int j = 0; j < kSteps; ++j) {
         const uint64_t hi = (x + (1ull << 38)) >> 39 << 39;  // 24 bits
         p.v[j].x = static_cast<float>(hi >> 39) / static_cast<float>(1 << 23);
-        p.v[j].y = static_cast<float>(static_cast<int64_t>(x - hi)) / static_cast<float>(1ull << 62);
+        p.v[j].y = j > 0 ? static_cast<float>(static_cast<int64_t>(x - hi)) / static_cast<float>(1ull << 62) : 0x1p-60f;  // not 0: its exponent is moved
         x = product_2_62(x, step);
     }
     return p;
@@ -82,69 +84,64 @@ __device__ const Powers kPowers = make_powers();
 // What a row's logits are weighed with.
 struct Scale {
     float top;       // the largest logit
-    float hi, lo;    // 2 * 256 log2(e) / T
+    float hi, lo;    // 2 / T
+    float none;      // a logit whose weight is none, and so are those below it
     bool flat;       // the largest is infinite: what is kept weighs the same
 };
 
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 minus(float2 a, float2 b) { return __ffma2_rn(b, both(-1.0f), a); }
+constexpr double kLn = 0.693147180559945309417 / kSteps;
+constexpr float kLnHi = static_cast<float>(kLn), kLnLo = static_cast<float>(kLn - static_cast<double>(kLnHi));
+constexpr float kPerLn = static_cast<float>(1.0 / kLn);
+constexpr float kRound = 12582912.0f;                    // 1.5 * 2^23: a sum with it is a whole number
+constexpr int kRoundBits = 0x4B400000;
+constexpr float kHigh = 12.0f, kLow = 1.5f / 524288.0f;  // sums with them are multiples of 2^-20 and 2^-42
+constexpr int kHighBits = 0x41400000, kLowBits = 0x36400000;
 
-// Weights of two logits as multiples of 2^-20 and 2^-42: w = hi + lo, each such that eight of them add up exactly in a float.
-// bits: 256 t to the nearest integer, above 0x4B400000. The logits are at most c.top and not so far below it that 2^t is no ordinary
-// float; t off by 2^-8 of 2^-40, and so the weight, before its rounding to 2^-42, by 2^-40 of itself: with the difference of halves of
-// the logits (which stays finite) as d + e exactly and the factor as hi + lo, 256 t = p + q; n = round(p); 2^(n / 256) is a power of two
-// times a table's entry th + tl; with f = p - n + q, at most 1/2 and a little, 2^(f / 256) = 1 + y + y^2 / 2 + y^3 / 6, y = f ln(2) / 256 <= 2^-9.5:
-// y^4 / 24 is 2^-42.6. All pairs of operations, two logits an instruction.
-__device__ __forceinline__ void weigh(float2 x, const Scale& c, const float2* powers, float2& hi, float2& lo, int& bits0, int& bits1) {
-    constexpr double kLn = 0.693147180559945309417 / kSteps;
-    constexpr float kLnHi = static_cast<float>(kLn), kLnLo = static_cast<float>(kLn - static_cast<double>(kLnHi));
-    constexpr float kRound = 12582912.0f;                    // 1.5 * 2^23: a sum with it is a whole number
-    constexpr float kHigh = 12.0f, kLow = 1.5f / 524288.0f;  // sums with them are multiples of 2^-20 and 2^-42
-    const float2 a = __fmul2_rn(x, both(0.5f)), b = both(-0.5f * c.top);
-    const float2 d = __fadd2_rn(a, b), bb = minus(d, a), e = __fadd2_rn(minus(a, minus(d, bb)), minus(b, bb));
-    const float2 p = __fmul2_rn(d, both(c.hi));
-    const float2 m = __fadd2_rn(p, both(kRound));
-    bits0 = __float_as_int(m.x);
-    bits1 = __float_as_int(m.y);
-    const float2 t0 = powers[bits0 & (kSteps - 1)], t1 = powers[bits1 & (kSteps - 1)];
-    const float2 th = make_float2(t0.x, t1.x), tl = make_float2(t0.y, t1.y);
-    const float2 q = __ffma2_rn(d, both(c.lo), __ffma2_rn(e, both(c.hi), __ffma2_rn(d, both(c.hi), __fmul2_rn(p, both(-1.0f)))));
-    const float2 f = minus(p, __fadd2_rn(m, both(-kRound)));
-    // y as u + v, with its square and cube in v
-    const float2 u = __fmul2_rn(f, both(kLnHi));
-    float2 v = __ffma2_rn(f, both(kLnHi), __fmul2_rn(u, both(-1.0f)));
-    v = __ffma2_rn(f, both(kLnLo), v);
-    v = __ffma2_rn(q, both(kLnHi), v);
-    v = __ffma2_rn(__fmul2_rn(u, u), __ffma2_rn(u, both(1.0f / 6.0f), both(0.5f)), v);
-    // (th + tl) (1 + u + v) = s + r
-    float2 s = __ffma2_rn(th, u, th);
-    float2 r = __ffma2_rn(th, u, minus(th, s));
-    r = __fadd2_rn(r, __ffma2_rn(th, v, __ffma2_rn(tl, u, tl)));
-    const float2 by = make_float2(__int_as_float((bits0 >> 8 << 23) + 0x3F800000), __int_as_float((bits1 >> 8 << 23) + 0x3F800000));
-    s = __fmul2_rn(s, by);
-    r = __fmul2_rn(r, by);
-    hi = __fadd2_rn(__fadd2_rn(s, both(kHigh)), both(-kHigh));
-    lo = __fadd2_rn(__fadd2_rn(__fadd2_rn(minus(s, hi), r), both(kLow)), both(-kLow));
+// ln w of a logit as P (of d, half its difference from the largest), and 256 log2 w to the nearest integer, above kRoundBits.
+__device__ __forceinline__ int step_bits(float p) { return __float_as_int(__fmaf_rn(p, kPerLn, kRound)); }
+
+// The weight of a logit, in two parts added to `high` and `low` (units(), below): w = (high part) 2^-20 + (low part) 2^-42. Its step comes back. The
+// logit is at most c.top and not so far below it that w is no ordinary float. w is right to 2^-37 of itself, and most to 2^-42, before its rounding to 2^-42:
+// with the difference of halves of the logits (which stays finite) as d + e exactly and 2 / T as hi + lo, ln w = p + q; n = round(256 log2 w);
+// what is left after n ln(2) / 256 is u (exactly: it has 22 bits) and some more, f, and with u at most 2^-9.5
+//     w = 2^(n / 256) (1 + u + (u^2 / 2 + u^3 / 6 + f + u f)),
+// u^4 / 24 being 2^-42.6 and f at most 2^-19; 2^(n / 256) is a table's entry th + tl, whose exponents are moved. The operations bound the passes that
+// weigh all logits: 30 of them on the floating point pipe (two at a time, in packed form, they take as long).
+__device__ __forceinline__ int weigh(float x, const Scale& c, const float2* powers, int& high, int& low) {
+    const float a = 0.5f * x, b = -0.5f * c.top, d = __fadd_rn(a, b);
+    const float bb = __fsub_rn(d, a), e = __fadd_rn(__fsub_rn(a, __fsub_rn(d, bb)), __fsub_rn(b, bb));
+    const float p = __fmul_rn(d, c.hi);
+    const float q = __fmaf_rn(d, c.lo, __fmaf_rn(e, c.hi, __fmaf_rn(d, c.hi, -p)));
+    const int bits = step_bits(p);
+    const float n = __fsub_rn(__int_as_float(bits), kRound);
+    const float2 t = powers[bits & (kSteps - 1)];
+    const int by = (bits & ~(kSteps - 1)) << 15;
+    const float th = __int_as_float(__float_as_int(t.x) + by), tl = __int_as_float(__float_as_int(t.y) + by);
+    const float u = __fmaf_rn(n, -kLnHi, p), f = __fmaf_rn(n, -kLnLo, q);
+    const float v = __fmaf_rn(__fmul_rn(u, u), __fmaf_rn(u, 1.0f / 6.0f, 0.5f), __fmaf_rn(u, f, f));
+    const float s = __fmaf_rn(th, u, th);
+    const float r = __fadd_rn(__fmaf_rn(th, u, __fsub_rn(th, s)), __fmaf_rn(th, v, __fmaf_rn(tl, u, tl)));
+    const float h = __fadd_rn(s, kHigh);
+    const float l = __fadd_rn(__fadd_rn(__fsub_rn(s, __fsub_rn(h, kHigh)), r), kLow);
+    high += __float_as_int(h) - kHighBits;
+    low += __float_as_int(l) - kLowBits;
+    return bits;
 }
 
-// Sums of at most eight hi and lo, in units of 2^-42.
-__device__ __forceinline__ u64 units(float hi, float lo) {
-    return static_cast<u64>((static_cast<int64_t>(__float2int_rn(hi * 1048576.0f)) << 22) + __float2int_rn(lo * 4398046511104.0f));
-}
+// Sums of weights' parts, in units of 2^-42.
+__device__ __forceinline__ u64 units(int high, int low) { return static_cast<u64>((static_cast<int64_t>(high) << 22) + low); }
 
 __device__ __forceinline__ u64 weight_of(float x, const Scale& c, const float2* powers) {
     if (c.flat) return 1ull << kUnit;
-    float2 hi, lo;
-    int n0, n1;
-    weigh(make_float2(x, c.top), c, powers, hi, lo, n0, n1);
-    return units(hi.x, lo.x);
+    int high = 0, low = 0;
+    weigh(x, c, powers, high, low);
+    return units(high, low);
 }
 
-// 256 t of a logit as weigh() has it, as a bin's number: falls as the logit does, so bins are in order.
-__device__ __forceinline__ int bin_of_bits(int bits) { return min((0x4B400000 - bits) / kBinSteps, kBins - 1); }
+// A step's bin, and a logit's: it falls as the logit does, so bins are in order.
+__device__ __forceinline__ int bin_of_bits(int bits) { return min((kRoundBits - bits) / kBinSteps, kBins - 1); }
 __device__ __forceinline__ int bin_of(float x, const Scale& c) {
-    const float d = __fadd_rn(0.5f * x, -0.5f * c.top);
-    return c.flat ? 0 : bin_of_bits(__float_as_int(__fadd_rn(__fmul_rn(d, c.hi), 12582912.0f)));
+    return c.flat ? 0 : bin_of_bits(step_bits(__fmul_rn(__fadd_rn(0.5f * x, -0.5f * c.top), c.hi)));
 }
 
 // A logit's rank among all: larger ones higher, of equal ones the lower index (-0 and 0 are equal).
@@ -235,15 +232,20 @@ struct Row {
 struct Shared {
     float2 powers[kSteps];
     u64 list[kList];           // of the first CTA; parts' masses
-    u64 groups[kMostGroups];
-    uint32_t bins[kBins], all[kBins];
-    u64 window[kWindow];
-    uint32_t window_count[kWindow];
+    u64 groups[kMostGroups];   // weights
+    int2 places[kMostGroups];  // how many go to the list, and where
+    union {
+        struct {
+            uint32_t bins[kBins], all[kBins];
+        };
+        u64 masses[kBins];     // of a list's bins
+    };
+    u64 some[kSome], some_weight[kSome];
     u64 box[2][2][kMaxCtas];   // what the CTAs tell each other
     u64 sums[kWarps];
     u64 answer;
-    int found[2];
-    uint32_t listed[2];
+    int found[2], window[2];
+    uint32_t listed;
     double log_min_p;
 };
 constexpr int kHeld = (sizeof(Shared) + 15) / 16 * 16;  // where the row's stretch begins
@@ -286,6 +288,9 @@ __device__ __forceinline__ u64 part_of(u64 whole, float fraction, bool up) {
     return __umul64hi(whole, f) + (up && whole * f != 0 ? 1 : 0);
 }
 
+// The weight that what comes before a token must not reach.
+__device__ __forceinline__ u64 target_of(u64 total, float top_p) { return max(part_of(total, fmaxf(top_p, 0.0f), true), 1ull); }
+
 template <typename E>
 struct Sampler {
     static constexpr int kV = Row<E>::kV;
@@ -298,6 +303,8 @@ struct Sampler {
     u64 cut = 0;       // least place kept: that of logit cut_x at index cut_i
     float cut_x;
     uint32_t cut_i;
+    float best = kNone;  // the thread's largest
+    bool easy = false;   // all that has a weight is kept
 
     __device__ Sampler(const SampleCall& call, Shared& shared, const E* x, uint4* held, uint32_t r, uint32_t n)
         : c(call), s(shared), row(x, held, call.vocab, r, n), rank(r), ctas(n) {}
@@ -311,7 +318,7 @@ struct Sampler {
     __device__ __forceinline__ bool kept(float x, int i) const { return x > cut_x || (x == cut_x && static_cast<uint32_t>(i) <= cut_i); }
     // A logit that no one of bin b or before is below.
     __device__ __forceinline__ float lowest_of(int b) const {
-        return scale.flat ? scale.top : scale.top - (2.0f * (b + 2) * kBinSteps / scale.hi) * 1.0001f - 1e-5f * fabsf(scale.top);
+        return scale.flat ? scale.top : scale.top - (2.0f * (b + 2) * kBinSteps * kLnHi / scale.hi) * 1.0001f - 1e-5f * fabsf(scale.top);
     }
 
     // Two numbers of this CTA's to every CTA; afterwards all of them are in the box that comes back. Threads of the CTA
@@ -346,7 +353,6 @@ struct Sampler {
 
     // The place of the largest logit; 0: there is none above -inf. `ready`: run once every CTA of the cluster runs.
     __device__ u64 largest() {
-        float best = kNone;
         int at = INT_MAX;
         row.load([&](int i, const float (&v)[kV]) {
 #pragma unroll
@@ -370,40 +376,46 @@ struct Sampler {
         return p;
     }
 
-    // Weights of a piece's kept logits, added up. f(e, bits): each kept one's step, as weigh() has it.
-    template <typename F>
-    __device__ __forceinline__ u64 weigh_piece(int i, const float (&v)[kV], F f) {
-        if (scale.flat) {
-            u64 n = 0;
+    // Weights of a piece's kept logits, added up; with kPart, of those in bins before `first`.
+    template <bool kPart>
+    __device__ __forceinline__ u64 weigh_piece(int i, const float (&v)[kV], int first = 0) {
+        float x[kV];
+        if (easy) {  // below the cut there is no weight
 #pragma unroll
-            for (int e = 0; e < kV; ++e)
-                if (kept(v[e], i + e)) {
-                    ++n;
-                    f(e, 0x4B400000);
-                }
-            return n << kUnit;
-        }
-        float2 hi = both(0.0f), lo = both(0.0f);
+            for (int e = 0; e < kV; ++e) x[e] = fmaxf(v[e], scale.none);
+        } else if (scale.none > kNone && !scale.flat) {
 #pragma unroll
-        for (int e = 0; e < kV; e += 2) {
-            const bool k0 = kept(v[e], i + e), k1 = kept(v[e + 1], i + e + 1);
-            float2 h, l;
-            int n0, n1;
-            weigh(make_float2(k0 ? v[e] : scale.top, k1 ? v[e + 1] : scale.top), scale, s.powers, h, l, n0, n1);
-            hi = __fadd2_rn(hi, make_float2(k0 ? h.x : 0.0f, k1 ? h.y : 0.0f));
-            lo = __fadd2_rn(lo, make_float2(k0 ? l.x : 0.0f, k1 ? l.y : 0.0f));
-            if (k0) f(e, n0);
-            if (k1) f(e + 1, n1);
+            for (int e = 0; e < kV; ++e) x[e] = kept(v[e], i + e) ? v[e] : scale.none;
+        } else {
+            u64 sum = 0;
+#pragma unroll 1
+            for (int e = 0; e < kV; ++e) {
+                float y = v[0];
+#pragma unroll
+                for (int k = 1; k < kV; ++k) y = k == e ? v[k] : y;
+                if (kept(y, i + e) && (!kPart || bin_of(y, scale) < first)) sum += weight_of(y, scale, s.powers);
+            }
+            return sum;
         }
-        return units(hi.x + hi.y, lo.x + lo.y);
+        int high = 0, low = 0;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) {
+            if (kPart) {
+                int h = 0, l = 0;
+                const bool in = weigh(x[e], scale, s.powers, h, l) > kRoundBits - first * kBinSteps;
+                high += in ? h : 0;
+                low += in ? l : 0;
+            } else {
+                weigh(x[e], scale, s.powers, high, low);
+            }
+        }
+        return units(high, low);
     }
 
-    // Counts of what is kept a bin, of all CTAs, in s.all; with kMass also its weight.
-    template <bool kMass>
-    __device__ u64 count() {
-        for (int b = threadIdx.x; b < kBins; b += kThreads) s.bins[b] = 0;
-        __syncthreads();
-        u64 mass = 0;
+    // Counts of what is kept a bin, of all CTAs, in the first CTA's s.all.
+    __device__ void count() {
+        for (int b = threadIdx.x; b < kBins; b += kThreads) s.bins[b] = s.all[b] = 0;
+        cluster_sync();
         row.each(cut_x, [&](int, int i, const float (&v)[kV]) {
             // many equal logits: one addition a warp
             bool same = true;
@@ -412,144 +424,221 @@ struct Sampler {
             const float first = __shfl_sync(0xFFFFFFFFu, v[0], 0);
             if (__all_sync(0xFFFFFFFFu, same && v[0] == first && v[0] > cut_x)) {
                 if ((threadIdx.x & 31) == 0) atomicAdd(&s.bins[bin_of(first, scale)], 32u * kV);
-                if (kMass) mass += weight_of(first, scale, s.powers) * kV;
                 return;
             }
-            auto add = [&](int, int bits) { atomicAdd(&s.bins[bin_of_bits(bits)], 1u); };
-            if constexpr (kMass) {
-                mass += weigh_piece(i, v, add);
-            } else {
 #pragma unroll
-                for (int e = 0; e < kV; ++e)
-                    if (kept(v[e], i + e)) atomicAdd(&s.bins[bin_of(v[e], scale)], 1u);
-            }
+            for (int e = 0; e < kV; ++e)
+                if (kept(v[e], i + e)) atomicAdd(&s.bins[bin_of(v[e], scale)], 1u);
         });
-        const u64 total = kMass ? sum_cluster(mass) : (cluster_sync(), 0);
-        for (int b = threadIdx.x; b < kBins; b += kThreads) {
-            uint32_t n = 0;
-            for (uint32_t r = 0; r < ctas; ++r) {
-                uint32_t x;
-                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(mapa_shared(smem_u32(&s.bins[b]), r)));
-                n += x;
-            }
-            s.all[b] = n;
-        }
         __syncthreads();
-        return total;
+        const uint32_t to = mapa_shared(smem_u32(s.all), 0);
+#pragma unroll
+        for (int b = threadIdx.x; b < kBins; b += kThreads)
+            if (s.bins[b] != 0) asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(to + 4 * b), "r"(s.bins[b]) : "memory");
+        cluster_sync();
     }
-
-    // The weight of what is kept.
-    __device__ u64 mass() {
-        u64 sum = 0;
-        row.each(cut_x, [&](int, int i, const float (&v)[kV]) { sum += weigh_piece(i, v, [](int, int) {}); });
-        return sum_cluster(sum);
+    // Counts of the threads' largest a bin, of all CTAs, in the first CTA's s.all, which is clear.
+    __device__ void count_best() {
+        if (best >= cut_x)
+            asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&s.all[bin_of(best, scale)]), 0)), "r"(1u) : "memory");
+        cluster_sync();
     }
-
-    // Among counts v(b): the first bin up to which they reach `want`, and the sum before it; kBins where they do not.
+    // Among numbers v(b): the first bin up to which they reach `want`, and the sum before it; kBins and the sum of all where they do not.
     template <typename V, typename F>
     __device__ void reach(F v, V want, V* sums, int& bin, V& before) {
         constexpr int kEach = (kBins + kThreads - 1) / kThreads;
-        V mine = 0, total;
+        V x[kEach], mine = 0, total;
         const int b0 = threadIdx.x * kEach;
-        for (int b = b0; b < min(kBins, b0 + kEach); ++b) mine += v(b);
-        V at = scan_block(mine, sums, total);
-        if (threadIdx.x == 0) s.found[0] = kBins;
-        __syncthreads();
-        V past = at;
-        for (int b = b0; b < min(kBins, b0 + kEach); ++b) {
-            const V next = past + v(b);
-            if (past < want && next >= want) {
-                s.found[0] = b;
-                s.answer = 0;
-                memcpy(&s.answer, &past, sizeof(V));
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            x[i] = b0 + i < kBins ? v(b0 + i) : 0;
+            mine += x[i];
+        }
+        V past = scan_block(mine, sums, total);
+        if (past < want && past + mine >= want) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                if (past < want && past + x[i] >= want) {
+                    s.found[0] = b0 + i;
+                    s.answer = past;
+                }
+                past += x[i];
             }
-            past = next;
         }
         __syncthreads();
-        bin = s.found[0];
-        before = total;
-        if (bin < kBins) memcpy(&before, &s.answer, sizeof(V));
-        __syncthreads();
+        const bool reached = total >= want;
+        bin = reached ? s.found[0] : kBins;
+        before = reached ? static_cast<V>(s.answer) : total;
     }
 
-    // Brings the kept places of logits of at least `least` for which f holds together in the first CTA's list, at most kList. The cluster
-    // meets afterwards.
+    // Brings the kept places of logits of at least `least` for which f holds together in the first CTA's list, in the order of the row, if they are
+    // at most kList. Afterwards the cluster has met. Returns how many they are.
     template <typename F>
-    __device__ void gather(int which, float least, F f) {
-        const uint32_t counter = mapa_shared(smem_u32(&s.listed[which]), 0), list = mapa_shared(smem_u32(s.list), 0);
+    __device__ int gather(float least, F f) {
+        const float from = fmaxf(least, cut_x);
         const int lane = threadIdx.x & 31;
-        row.each(fmaxf(least, cut_x), [&](int, int i, const float (&v)[kV]) {
-            uint32_t mine = 0;
+        for (int g = threadIdx.x / 32 + lane * kWarps; g < row.groups; g += kThreads) s.places[g] = make_int2(0, 0);
+        __syncwarp();
+        row.each(from, [&](int g, int i, const float (&v)[kV]) {
+            int mine = 0;
+#pragma unroll
+            for (int e = 0; e < kV; ++e) mine += kept(v[e], i + e) && f(v[e], i + e);
+            mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+            if (lane == 0) s.places[g].x = mine;
+        });
+        __syncthreads();
+        static_assert(kMostGroups <= kThreads, "a group a thread");
+        const int mine = threadIdx.x < row.groups ? s.places[threadIdx.x].x : 0;
+        int all, before = scan_block(mine, reinterpret_cast<int*>(s.sums), all), total = 0;
+        u64 (*box)[kMaxCtas] = tell(all, 0);
+        for (uint32_t r = 0; r < ctas; ++r) {
+            if (r < rank) before += static_cast<int>(box[0][r]);
+            total += static_cast<int>(box[0][r]);
+        }
+        if (total > kList) return total;
+        if (threadIdx.x < row.groups) s.places[threadIdx.x].y = before;
+        __syncthreads();
+        const uint32_t list = mapa_shared(smem_u32(s.list), 0);
+        for (int g = threadIdx.x / 32; g < row.groups; g += kWarps) {
+            if (s.places[g].x == 0) continue;
+            float v[kV];
+            Row<E>::open(row.held[g * 32 + lane], v);
+            const int i = row.index(g);
+            uint32_t in = 0;
 #pragma unroll
             for (int e = 0; e < kV; ++e)
-                if (kept(v[e], i + e) && f(v[e], i + e)) mine |= 1u << e;
-            int x = __popc(mine);
+                if (kept(v[e], i + e) && f(v[e], i + e)) in |= 1u << e;
+            int x = __popc(in);
             const int own = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
                 if (lane >= o) x += y;
             }
-            uint32_t at = 0;
-            if (lane == 31 && x > 0) asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(at) : "r"(counter), "r"(x) : "memory");
-            at = __shfl_sync(0xFFFFFFFFu, at, 31) + x - own;
+            int at = s.places[g].y + x - own;
 #pragma unroll
             for (int e = 0; e < kV; ++e)
-                if (mine >> e & 1) {
-                    if (at < kList) asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(list + 8 * at), "l"(place_of(v[e], i + e)) : "memory");
+                if (in >> e & 1) {
+                    asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(list + 8 * at), "l"(place_of(v[e], i + e)) : "memory");
                     ++at;
                 }
-        });
+        }
         cluster_sync();
+        return total;
     }
 
-    // Sorts n numbers of the list, the largest first (first CTA).
-    __device__ void sort(int n) {
-        int size = 1;
+    // Sorts n numbers of the list, the largest first (first CTA): in registers, kEach a lane, one after another, and through shared memory
+    // only between warps.
+    template <int kEach>
+    __device__ void sort_by(int n) {
+        int size = 32 * kEach;
         while (size < n) size *= 2;
-        for (int i = n + threadIdx.x; i < size; i += kThreads) s.list[i] = 0;
+        const int i0 = threadIdx.x * kEach;
+        u64 x[kEach];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) x[e] = i0 + e < n ? s.list[i0 + e] : 0;
+        const bool some = threadIdx.x / 32 * 32 * kEach < size;  // the warp takes part
         for (int k = 2; k <= size; k *= 2)
             for (int j = k / 2; j > 0; j /= 2) {
-                __syncthreads();
-                for (int t = threadIdx.x; t < size / 2; t += kThreads) {
-                    const int lo = 2 * t - (t & (j - 1)), hi = lo + j;
-                    const u64 a = s.list[lo], b = s.list[hi];
-                    if ((a < b) == ((lo & k) == 0)) {
-                        s.list[lo] = b;
-                        s.list[hi] = a;
+                if (j >= 32 * kEach) {
+                    __syncthreads();
+                    if (some) {
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e) s.list[i0 + e] = x[e];
                     }
+                    __syncthreads();
+                    if (some) {
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e) {
+                            const u64 y = s.list[(i0 + e) ^ j];
+                            const bool larger = ((i0 & j) == 0) == ((i0 & k) == 0);  // the larger one stays here
+                            x[e] = larger == (x[e] > y) ? x[e] : y;
+                        }
+                    }
+                } else if (j >= kEach) {
+                    if (some) {
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e) {
+                            const u64 y = __shfl_xor_sync(0xFFFFFFFFu, x[e], j / kEach);
+                            const bool larger = ((i0 & j) == 0) == ((i0 & k) == 0);
+                            x[e] = larger == (x[e] > y) ? x[e] : y;
+                        }
+                    }
+                } else if (some) {
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e)
+#pragma unroll
+                        for (int d = 1; d < kEach; d *= 2)
+                            if (d == j && (e & d) == 0) {
+                                const bool down = ((i0 + e) & k) == 0;
+                                const u64 a = x[e], b = x[e + d];
+                                if (down == (a < b)) {
+                                    x[e] = b;
+                                    x[e + d] = a;
+                                }
+                            }
                 }
             }
         __syncthreads();
+        if (some) {
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) s.list[i0 + e] = x[e];
+        }
+        __syncthreads();
+    }
+    __device__ void sort(int n) {
+        if (n <= 32) sort_by<1>(n);
+        else if (n <= 64) sort_by<2>(n);
+        else sort_by<4>(n);
     }
 
-    // In the first CTA's sorted list of n places: how many come first that have less than `target` of weight before them (at least one).
-    // total: the weight of all n.
-    __device__ int within(int n, u64 target, u64& total) {
+    // The weights of n places of the first CTA's list, one thread's after another's: f(i, weight, weight before) for each. Returns the weight of
+    // all n.
+    template <typename G, typename F>
+    __device__ __forceinline__ u64 weigh_list(int n, G logit, F f) {
         constexpr int kEach = kList / kThreads;
-        const int i0 = threadIdx.x * kEach;
-        u64 w[kEach], mine = 0;
+        const int each = (n + kThreads - 1) / kThreads, i0 = threadIdx.x * each;
+        u64 w[kEach], mine = 0, total;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            w[i] = i0 + i < n ? weight_of(logit_of(s.list[i0 + i]), scale, s.powers) : 0;
+            w[i] = i < each && i0 + i < n ? weight_of(logit(s.list[i0 + i]), scale, s.powers) : 0;
             mine += w[i];
         }
         u64 before = scan_block(mine, s.sums, total);
-        if (threadIdx.x == 0) s.found[1] = 1;
-        __syncthreads();
+        f(total);  // whole block
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            if (i0 + i < n && before < target) atomicMax(&s.found[1], i0 + i + 1);
+            if (i < each && i0 + i < n) f(i0 + i, w[i], before);
             before += w[i];
         }
+        return total;
+    }
+    // Of the first CTA's sorted list of n places: how many come first that have less than target(weight of all) before them, at
+    // least one; 0 where all have less than that.
+    template <typename T>
+    __device__ int within(int n, T target) {
+        struct Find {
+            Shared& s;
+            T target;
+            u64 want;
+            __device__ void operator()(u64 total) {
+                want = target(total);
+                if (threadIdx.x == 0) s.found[1] = 1;
+                __syncthreads();
+            }
+            __device__ void operator()(int i, u64, u64 before) {
+                if (before < want) atomicMax(&s.found[1], i + 1);
+            }
+        } find{s, target, 0};
+        const u64 total = weigh_list(n, [](u64 p) { return logit_of(p); }, [&](auto... x) { find(x...); });
         __syncthreads();
-        return s.found[1];
+        return total < find.want ? 0 : s.found[1];
     }
 
     // The cut inside bin b, which holds n places >= cut: the target-th of them, or with kMass the last one that has less than
     // `target` of the bin's weight before it.
     template <bool kMass>
-    __device__ u64 inside(int which, int b, uint32_t n, u64 target) {
+    __device__ u64 inside(int b, uint32_t n, u64 target) {
         u64 low = 0, high = ~0ull;
         const float from = fmaxf(lowest_of(b), cut_x);
         if (n > kList) {  // first the bin's own range
@@ -568,16 +657,16 @@ struct Sampler {
                 most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
             }
             if (threadIdx.x == 0) {
-                s.groups[0] = ~0ull;
-                s.groups[1] = 0;
+                s.some[0] = ~0ull;
+                s.some[1] = 0;
             }
             __syncthreads();
             if ((threadIdx.x & 31) == 0) {
-                atomicMin(&s.groups[0], least);
-                atomicMax(&s.groups[1], most);
+                atomicMin(&s.some[0], least);
+                atomicMax(&s.some[1], most);
             }
             __syncthreads();
-            u64 (*box)[kMaxCtas] = tell(s.groups[0], s.groups[1]);
+            u64 (*box)[kMaxCtas] = tell(s.some[0], s.some[1]);
             low = ~0ull;
             high = 0;
             for (uint32_t r = 0; r < ctas; ++r) {
@@ -638,15 +727,8 @@ struct Sampler {
             high = top;
             __syncthreads();
         }
-        gather(which, from, [&](float x, int i) { return bin_of(x, scale) == b && place_of(x, i) >= low && place_of(x, i) <= high; });
-        u64 found = 0;
-        if (rank == 0) {
-            sort(static_cast<int>(n));
-            u64 all;
-            const int i = kMass ? within(static_cast<int>(n), target, all) - 1 : static_cast<int>(target) - 1;
-            found = s.list[i];
-            __syncthreads();
-        }
+        gather(from, [&](float x, int i) { return bin_of(x, scale) == b && place_of(x, i) >= low && place_of(x, i) <= high; });
+        const u64 found = rank == 0 ? cut_of<kMass>(static_cast<int>(n), target) : 0;
         return tell(found, 0)[0][0];
     }
 
@@ -657,49 +739,259 @@ struct Sampler {
             const u64 p = s.list[i];
             s.list[i] = p << 32 | p >> 32;
         }
+        __syncthreads();
         sort(n);
-        constexpr int kEach = kList / kThreads;
-        const int i0 = threadIdx.x * kEach;
-        u64 w[kEach], mine = 0, total;
+        struct Find {
+            Shared& s;
+            float u;
+            int32_t* token;
+            u64 want;
+            __device__ void operator()(u64 total) { want = part_of(total, u, false); }
+            __device__ void operator()(int i, u64 w, u64 before) {
+                if (before <= want && want < before + w) *token = index_of(s.list[i] >> 32);
+            }
+        } find{s, u, token, 0};
+        weigh_list(n, [](u64 p) { return logit_of(p << 32); }, [&](auto... x) { find(x...); });
+    }
+
+    // The cut of the first CTA's list: the target-th largest place, or with kMass the last one that has less than `target` of weight before it.
+    // p, w: this thread's places and weights, 0 for those that do not count. By their part of the range of all, then each with each
+    // in the border's part. 0: more than kSome are there; 1: there is less than the target.
+    template <bool kMass, int kEach>
+    __device__ u64 cut_list(const u64 (&p)[kEach], const u64 (&w)[kEach], u64 target) {
+        u64 least = ~0ull, most = 0;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            w[i] = i0 + i < n ? weight_of(logit_of(s.list[i0 + i] << 32), scale, s.powers) : 0;
-            mine += w[i];
+        for (int i = 0; i < kEach; ++i)
+            if (w[i] != 0) {
+                least = min(least, p[i]);
+                most = max(most, p[i]);
+            }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
         }
-        u64 before = scan_block(mine, s.sums, total);
+        for (int b = threadIdx.x; b < kSub; b += kThreads) s.masses[b] = 0;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) {
+            s.sums[threadIdx.x >> 5] = least;
+            s.some[threadIdx.x >> 5] = most;
+        }
+        if (threadIdx.x == 0) s.listed = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            least = min(least, s.sums[i]);
+            most = max(most, s.some[i]);
+        }
+        if (least > most) return 1;
+        const int shift = max(0, 64 - __clzll(most - least) - 10);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (w[i] != 0) {
+                const int part = static_cast<int>((most - p[i]) >> shift);
+                if (kMass) atomicAdd(&s.masses[part], w[i]);
+                else atomicAdd(reinterpret_cast<uint32_t*>(&s.masses[part]), 1u);
+            }
+        __syncthreads();
+        int part;
+        u64 before;
+        reach<u64>([&](int b) { return b < kSub ? s.masses[b] : 0; }, target, s.sums, part, before);
+        if (part == kBins) return 1;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (w[i] != 0 && static_cast<int>((most - p[i]) >> shift) == part) {
+                const uint32_t at = atomicAdd(&s.listed, 1u);
+                if (at < kSome) {
+                    s.some[at] = p[i];
+                    s.some_weight[at] = kMass ? w[i] : 1;
+                }
+            }
+        __syncthreads();
+        const int n = static_cast<int>(s.listed);
+        if (n > kSome) return 0;
+        if (threadIdx.x < n) {
+            const u64 own = s.some[threadIdx.x];
+            u64 above = before;
+            for (int j = 0; j < n; ++j)
+                if (s.some[j] > own) above += s.some_weight[j];
+            if (above < target && above + s.some_weight[threadIdx.x] >= target) s.answer = own;
+        }
+        __syncthreads();
+        const u64 found = s.answer;
+        __syncthreads();
+        return found;
+    }
+    // The first CTA's list of n: a thread's places and weights, one thread's after another's.
+    static constexpr int kOwn = kList / kThreads;
+    __device__ __forceinline__ void read_list(int n, u64 (&p)[kOwn], u64 (&w)[kOwn]) {
+        const int each = (n + kThreads - 1) / kThreads, i0 = threadIdx.x * each;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const bool some = i < each && i0 + i < n;
+            p[i] = some ? s.list[i0 + i] : 0;
+            w[i] = some ? weight_of(logit_of(p[i]), scale, s.powers) : 0;
+        }
+    }
+    // The cut of the first CTA's list of n, as cut_list says; the list is sorted afterwards where it has to be.
+    template <bool kMass>
+    __device__ u64 cut_of(int n, u64 target) {
+        u64 p[kOwn], w[kOwn];
+        read_list(n, p, w);
+        if (!kMass) {
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) w[i] = p[i] != 0;
+        }
+        u64 found = cut_list<kMass>(p, w, target);
+        if (found == 0) {
+            sort(n);
+            found = s.list[kMass ? within(n, [&](u64) { return target; }) - 1 : static_cast<int>(target) - 1];
+            __syncthreads();
+        }
+        return found;
+    }
+
+    // draw_from of at most 128, by the first warp alone.
+    __device__ void draw_from_warp(int n, int top_k, float top_p, u64 target, float u, int32_t* token) {
+        constexpr int kEach = 4;
+        const int lane = threadIdx.x, i0 = lane * kEach;
+        auto before_lane = [&](u64 v, u64& total) {
+            u64 x = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                if (lane >= o) x += y;
+            }
+            total = __shfl_sync(0xFFFFFFFFu, x, 31);
+            return x - v;
+        };
+        u64 p[kEach], least = 1, total;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) p[e] = i0 + e < n ? s.list[i0 + e] : 0;
+        if (n > top_k || top_p < 1.0f) {
+            u64 q[kEach];
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) q[e] = p[e];
+            int size = kEach;
+            while (size < n) size *= 2;
+#pragma unroll 1
+            for (int k = 2; k <= size; k *= 2) {
+#pragma unroll 1
+                for (int j = k / 2; j >= kEach; j /= 2)
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) {
+                        const u64 y = __shfl_xor_sync(0xFFFFFFFFu, q[e], j / kEach);
+                        const bool larger = ((i0 & j) == 0) == ((i0 & k) == 0);
+                        q[e] = larger == (q[e] > y) ? q[e] : y;
+                    }
+#pragma unroll
+                for (int j = kEach / 2; j > 0; j /= 2)
+                    if (j < k)
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e)
+                            if ((e & j) == 0) {
+                                const u64 a = q[e], b = q[e + j];
+                                const bool swap = (((i0 + e) & k) == 0) == (a < b);
+                                q[e] = swap ? b : a;
+                                q[e + j] = swap ? a : b;
+                            }
+            }
+            u64 w[kEach], mine = 0;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                w[e] = i0 + e < min(n, top_k) ? weight_of(logit_of(q[e]), scale, s.powers) : 0;
+                mine += w[e];
+            }
+            u64 before = before_lane(mine, total);
+            const u64 want = top_p >= 1.0f ? ~0ull : target != 0 ? target : target_of(total, top_p);
+            u64 lowest = ~0ull;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                if (i0 + e < min(n, top_k) && before < want) lowest = q[e];
+                before += w[e];
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) lowest = min(lowest, __shfl_xor_sync(0xFFFFFFFFu, lowest, o));
+            least = lowest;
+        }
+        u64 w[kEach], mine = 0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            w[e] = p[e] >= least ? weight_of(logit_of(p[e]), scale, s.powers) : 0;
+            mine += w[e];
+        }
+        u64 before = before_lane(mine, total);
         const u64 want = part_of(total, u, false);
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            if (before <= want && want < before + w[i]) *token = index_of(s.list[i0 + i] >> 32);
+        for (int e = 0; e < kEach; ++e) {
+            if (before <= want && want < before + w[e]) *token = index_of(p[e]);
+            before += w[e];
+        }
+    }
+
+    // The token from the first CTA's list of n places, in the order of the row: of the top_k of it, and of the likeliest that reach `target` of
+    // weight (0: top_p of the weight of what is kept), which the list does.
+    __device__ void draw_from(int n, int top_k, float top_p, u64 target, float u, int32_t* token) {
+        if (n <= 128) {
+            if (threadIdx.x < 32) draw_from_warp(n, top_k, top_p, target, u, token);
+            return;
+        }
+        u64 p[kOwn], w[kOwn], mine = 0, total;
+        read_list(n, p, w);
+        auto keep = [&](u64 least) {
+            mine = 0;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                w[i] = p[i] >= least ? w[i] : 0;
+                mine += w[i];
+            }
+        };
+        u64 least = n > top_k ? cut_list<false>(p, w, top_k) : 1;
+        keep(least);
+        u64 before = scan_block(mine, s.sums, total);
+        if (least != 0 && top_p < 1.0f) {
+            least = cut_list<true>(p, w, target != 0 ? target : target_of(total, top_p));
+            keep(least);
+            before = scan_block(mine, s.sums, total);
+        }
+        if (least == 0) {  // many alike at a border
+            sort(n);
+            n = min(n, top_k);
+            if (top_p < 1.0f) n = within(n, [&](u64 all) { return target != 0 ? target : target_of(all, top_p); });
+            draw_list(n, u, token);
+            return;
+        }
+        const u64 want = part_of(total, u, false);
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            if (before <= want && want < before + w[i]) *token = index_of(p[i]);
             before += w[i];
         }
     }
 
-    // The token in which u of the weight of what is kept is passed.
-    __device__ void draw(float u, int32_t* token) {
-        u64 mine = 0;
+    // Weights of what is kept of the CTA's stretch, a group.
+    __device__ void weigh_groups() {
         for (int g = threadIdx.x / 32 + (threadIdx.x & 31) * kWarps; g < row.groups; g += kThreads) s.groups[g] = 0;
         __syncwarp();
         row.each(cut_x, [&](int g, int i, const float (&v)[kV]) {
-            const u64 sum = add_across(weigh_piece(i, v, [](int, int) {}));
-            if ((threadIdx.x & 31) == 0) {
-                s.groups[g] = sum;
-                mine += sum;
-            }
+            const u64 sum = add_across(weigh_piece<false>(i, v));
+            if ((threadIdx.x & 31) == 0) s.groups[g] = sum;
         });
-        const u64 all = sum_block(mine);
+        __syncthreads();
+    }
+
+    // The token in which u of the weight of what is kept is passed, given its weight a group.
+    __device__ void draw(float u, int32_t* token) {
+        static_assert(kMostGroups <= kThreads, "a group a thread");
+        const u64 sum = threadIdx.x < row.groups ? s.groups[threadIdx.x] : 0;
+        u64 all, at = scan_block(sum, s.sums, all), total = 0;
         u64 (*box)[kMaxCtas] = tell(all, 0);
-        u64 total = 0, before = 0;
         for (uint32_t r = 0; r < ctas; ++r) {
-            if (r < rank) before += box[0][r];
+            if (r < rank) at += box[0][r];
             total += box[0][r];
         }
         const u64 want = part_of(total, u, false);
-        if (want < before || want >= before + all) return;  // another CTA's
-        static_assert(kMostGroups <= kThreads, "a group a thread");
-        const u64 sum = threadIdx.x < row.groups ? s.groups[threadIdx.x] : 0;
-        u64 whole;
-        const u64 at = before + scan_block(sum, s.sums, whole);
+        if (!__syncthreads_or(at <= want && want < at + sum)) return;  // another CTA's
         if (at <= want && want < at + sum) {
             s.found[0] = threadIdx.x;
             s.answer = at;
@@ -729,99 +1021,173 @@ struct Sampler {
         }
     }
 
-    // About the weight in bin b, from its count.
+    // About the weight in bin b, from its count: 2^t in the bin's middle, 8 b + 3.5 steps down; with kLow no more than it is.
+    template <bool kLow>
     __device__ __forceinline__ u64 guess(int b) const {
-        const int n = -(b * kBinSteps + kBinSteps / 2 - 1);
-        const float w = s.powers[n & (kSteps - 1)].x * __int_as_float(((kUnit + (n >> 8)) + 127) << 23);
-        return s.all[b] * max(static_cast<u64>(w), 1ull);
+        const int n = -(b * kBinSteps + (kLow ? kBinSteps : kBinSteps / 2));
+        const float w = s.powers[n & (kSteps - 1)].x * (kLow ? 1.0f : 1.0013547f) * __int_as_float(((kUnit + (n >> 8)) + 127) << 23);
+        return s.all[b] * max(static_cast<u64>(w), kLow ? 0ull : 1ull);
     }
 
-    // Whether what reaches `target` of the weight, by the counts a bin, fits the list, and then the token, drawn from it.
-    __device__ bool draw_nucleus(u64 target, float u, int32_t* token) {
+    // Whether the token could be drawn from a list of few tokens: the top_k of the row among them, or (target not 0) the likeliest that have
+    // `target` of weight.
+    __device__ bool draw_few(int top_k, float top_p, u64 target, float u, int32_t* token) {
+        count_best();
+        int bin = 0;
+        if (rank == 0) {
+            u64 before;
+            if (target == 0) reach<u64>([&](int b) { return s.all[b]; }, static_cast<u64>(top_k), s.sums, bin, before);
+            else reach<u64>([&](int b) { return guess<true>(b); }, target, s.sums, bin, before);
+        }
+        bin = static_cast<int>(tell(bin, 0)[0][0]);
+        if (bin == kBins) {  // fewer threads than top_k, or less weight: everything, if it is little
+            if (c.vocab > kList) return false;
+            bin = kBins - 1;
+        }
+        const int n = gather(lowest_of(bin), [&](float x, int) { return bin_of(x, scale) <= bin; });
+        if (n > kList) return false;
+        if (rank == 0) draw_from(n, target == 0 ? top_k : INT_MAX, top_p, target, u, token);
+        return true;
+    }
+
+    // The first CTA, given the counts a bin: the bin in which a guessed weight of `want` is reached, and bins around it, of least .. most - 1, that
+    // the list can be expected to hold. In s.found.
+    __device__ void window(u64 want, int least, int most, int& first, int& last, uint32_t& many) {
         int bin;
         u64 before;
-        reach<u64>([&](int b) { return guess(b); }, target, s.sums, bin, before);
-        bin = min(bin + 1, kBins - 1);  // the guess may be a little high
-        u64 n = 0;
-        for (int b = threadIdx.x; b <= bin; b += kThreads) n += s.all[b];
-        n = sum_block(n);
-        if (n > kList) return false;
-        gather(0, lowest_of(bin), [&](float x, int) { return bin_of(x, scale) <= bin; });
-        u64 enough = 0;
-        if (rank == 0) {
-            sort(static_cast<int>(n));
-            const int k = within(static_cast<int>(n), target, enough);
-            enough = enough >= target;
-            if (enough) draw_list(k, u, token);
+        reach<u64>([&](int b) { return guess<false>(b); }, want, s.sums, bin, before);
+        bin = max(least, min(bin, most - 1));
+        constexpr int kEach = (kBins + kThreads - 1) / kThreads;
+        const int b0 = threadIdx.x * kEach;
+        int mine = 0, all;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) mine += b0 + i < kBins ? static_cast<int>(s.all[b0 + i]) : 0;
+        int up = scan_block(mine, reinterpret_cast<int*>(s.sums), all);  // counts before a bin
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (b0 + i < kBins) {
+                if (b0 + i == bin) {
+                    s.found[0] = up;
+                    s.found[1] = up + static_cast<int>(s.all[bin]);
+                }
+                s.bins[b0 + i] = up;
+                up += static_cast<int>(s.all[b0 + i]);
+            }
         }
-        return tell(enough, 0)[0][0] != 0;
+        __syncthreads();
+        const int from = s.found[0], to = s.found[1];
+        if (threadIdx.x == 0) s.window[0] = s.window[1] = bin;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kEach && to - from <= kList - kGuess; ++i) {  // a bin with more stays alone
+            const int b = b0 + i;
+            if (b < kBins && b >= least && b < bin && from - static_cast<int>(s.bins[b]) <= kGuess / 2) atomicMin(&s.window[0], b);
+            if (b < most && b > bin && static_cast<int>(s.bins[b] + s.all[b]) - to <= kGuess / 2) atomicMax(&s.window[1], b);
+        }
+        __syncthreads();
+        first = s.window[0];
+        last = s.window[1];
+        many = s.bins[last] + s.all[last] - s.bins[first];
     }
 
-    // The last place that has less than `target` of the weight of what is kept before it, given the counts a bin. Guesses where the
-    // border is from the counts, and takes the exact weight above, and in the kWindow bins there; where the guess missed,
-    // the next one starts from what is known exactly, on the border's side of the window: the search ends.
-    __device__ u64 nucleus(u64 target) {
-        int64_t known = 0;           // exact less guessed weight before a window
-        int least = 0, most = kBins; // the border's bin is one of least .. most - 1
-        while (true) {
-            int bin;
-            u64 skipped;
-            reach<u64>([&](int b) { return guess(b); }, static_cast<u64>(max(static_cast<int64_t>(target) - known, static_cast<int64_t>(1))), s.sums, bin, skipped);
-            const int from = max(least, min(bin - kWindow / 2, most - kWindow));
-            for (int i = threadIdx.x; i < kWindow; i += kThreads) {
-                s.window[i] = 0;
-                s.window_count[i] = 0;
-            }
-            __syncthreads();
-            u64 above = 0;
-            row.each(fmaxf(cut_x, lowest_of(from + kWindow - 1)), [&](int, int i, const float (&v)[kV]) {
-#pragma unroll
-                for (int e = 0; e < kV; ++e) {
-                    if (!kept(v[e], i + e)) continue;
-                    const int b = bin_of(v[e], scale);
-                    if (b >= from + kWindow) continue;
-                    const u64 w = weight_of(v[e], scale, s.powers);
-                    if (b < from) {
-                        above += w;
-                    } else {
-                        atomicAdd(&s.window[b - from], w);
-                        atomicAdd(&s.window_count[b - from], 1u);
-                    }
-                }
-            });
-            above = sum_cluster(above);
-            u64 in = 0;
-            uint32_t many = 0;
-            if (threadIdx.x < kWindow)
-                for (uint32_t r = 0; r < ctas; ++r) {
-                    u64 x;
-                    uint32_t y;
-                    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(mapa_shared(smem_u32(&s.window[threadIdx.x]), r)));
-                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(y) : "r"(mapa_shared(smem_u32(&s.window_count[threadIdx.x]), r)));
-                    in += x;
-                    many += y;
-                }
-            u64 inside_all;
-            const u64 before = above + scan_block(in, s.sums, inside_all);
-            if (threadIdx.x < kWindow && before < target && before + in >= target) {
-                s.found[0] = from + threadIdx.x;
-                s.found[1] = static_cast<int>(many);
-                s.answer = before;
-            }
-            cluster_sync();  // nobody reads the others' windows any more
-            if (above < target && target <= above + inside_all) {
-                const int b = s.found[0], n = s.found[1];
-                const u64 left = target - s.answer;
-                __syncthreads();
-                return inside<true>(1, b, static_cast<uint32_t>(n), left);
-            }
-            if (target <= above) most = from;
-            else least = from + kWindow;
+    // Cuts what is kept at the likeliest that have `target` of its weight. true: the token was drawn; false: the weight of each group is left.
+    // A guess from the counts gives a few bins around the border; one pass takes the exact weight of what is above them, and they are brought
+    // together. Where the guess missed, the next one starts from what is known exactly, on the border's side of the window: the search ends.
+    __device__ bool nucleus(u64 total, u64 target, float u, int32_t* token) {
+        count();
+        int64_t known = 0;            // exact less guessed weight before a window
+        if (rank == 0) {              // at first that of all: it is the few largest that a bin's middle misses most
             u64 part = 0, guessed;
-            for (int b = threadIdx.x; b < from; b += kThreads) part += guess(b);
+            for (int b = threadIdx.x; b < kBins; b += kThreads) part += guess<false>(b);
             scan_block(part, s.sums, guessed);
-            known = static_cast<int64_t>(above - guessed);
+            known = static_cast<int64_t>(total - guessed);
         }
+        int least = 0, most = kBins;  // the border's bin is one of least .. most - 1: fewer each time, so the search ends
+        while (least < most) {
+            int first = 0, last = 0;
+            uint32_t n = 0;
+            if (rank == 0) window(static_cast<u64>(max(static_cast<int64_t>(target) - known, static_cast<int64_t>(1))), least, most, first, last, n);
+            u64 (*box)[kMaxCtas] = tell(static_cast<u64>(first) << 32 | last, n);
+            first = static_cast<int>(box[0][0] >> 32);
+            last = static_cast<int>(static_cast<uint32_t>(box[0][0]));
+            n = static_cast<uint32_t>(box[1][0]);
+            u64 above = 0;
+            if (first > 0) {
+                for (int g = threadIdx.x / 32 + (threadIdx.x & 31) * kWarps; g < row.groups; g += kThreads) s.groups[g] = 0;
+                __syncwarp();
+                row.each(fmaxf(cut_x, lowest_of(first - 1)), [&](int g, int i, const float (&v)[kV]) {
+                    const u64 part = add_across(weigh_piece<true>(i, v, first));
+                    if ((threadIdx.x & 31) == 0) {
+                        s.groups[g] = part;
+                        above += part;
+                    }
+                });
+                above = sum_cluster(above);
+            }
+            // 2: the border is after the window; 0: before
+            u64 found = 0;
+            if (n > kList) {  // one bin, with many
+                u64 sum = 0;
+                row.each(fmaxf(cut_x, lowest_of(first)), [&](int, int i, const float (&v)[kV]) {
+#pragma unroll
+                    for (int e = 0; e < kV; ++e)
+                        if (kept(v[e], i + e) && bin_of(v[e], scale) == first) sum += weight_of(v[e], scale, s.powers);
+                });
+                sum = sum_cluster(sum);
+                found = target <= above ? 0 : target > above + sum ? 2 : inside<true>(first, n, target - above);
+            } else {
+                n = gather(lowest_of(last), [&](float x, int) {
+                    const int b = bin_of(x, scale);
+                    return b >= first && b <= last;
+                });
+                if (rank == 0 && above < target) {
+                    u64 p[kOwn], w[kOwn], sum = 0;
+                    read_list(n, p, w);
+#pragma unroll
+                    for (int i = 0; i < kOwn; ++i) sum += w[i];
+                    found = above + sum_block(sum) < target ? 2 : first == 0 ? 3 : cut_of<true>(n, target - above);
+                    if (found == 3) draw_from(n, INT_MAX, 0.5f, target, u, token);  // all that is kept is in the list
+                }
+                found = tell(found, 0)[0][0];
+                if (found == 3) return true;
+            }
+            if (found > 2) {  // the window's kept tokens come to their groups
+                if (first == 0) {
+                    for (int g = threadIdx.x / 32 + (threadIdx.x & 31) * kWarps; g < row.groups; g += kThreads) s.groups[g] = 0;
+                    __syncwarp();
+                }
+                keep_from(found);
+                row.each(cut_x, [&](int g, int i, const float (&v)[kV]) {
+                    u64 sum = 0;
+#pragma unroll
+                    for (int e = 0; e < kV; ++e)
+                        if (kept(v[e], i + e) && bin_of(v[e], scale) >= first) sum += weight_of(v[e], scale, s.powers);
+                    if (__any_sync(0xFFFFFFFFu, sum != 0)) {
+                        sum = add_across(sum);
+                        if ((threadIdx.x & 31) == 0) s.groups[g] += sum;
+                    }
+                });
+                __syncthreads();
+                return false;
+            }
+            if (found == 0) most = first;
+            else least = last + 1;
+            if (rank == 0) {
+                u64 part = 0, guessed;
+                for (int b = threadIdx.x; b < first; b += kThreads) part += guess<false>(b);
+                scan_block(part, s.sums, guessed);
+                known = static_cast<int64_t>(above - guessed);
+            }
+        }
+        weigh_groups();  // not reached: what is kept weighs at least the target
+        return false;
+    }
+
+    // The weight of what is kept.
+    __device__ u64 mass() {
+        u64 sum = 0;
+        row.each(cut_x, [&](int, int i, const float (&v)[kV]) { sum += weigh_piece<false>(i, v); });
+        return sum_cluster(sum);
     }
 };
 
@@ -843,7 +1209,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
     const float u = u_given > 0.0f ? fminf(u_given, 0.99999994f) : 0.0f;
     const bool greedy = !(temperature > 0.0f);
     for (int i = threadIdx.x; i < kSteps; i += kThreads) s.powers[i] = kPowers.v[i];
-    if (threadIdx.x == 0) s.listed[0] = s.listed[1] = 0;
+    for (int b = threadIdx.x; b < kBins; b += kThreads) s.all[b] = 0;
     if (threadIdx.x == kThreads - 32 && !greedy && min_p > 0.0f && min_p < 1.0f)  // in 64 bits, once, while the others read
         s.log_min_p = static_cast<double>(temperature) * log(static_cast<double>(min_p));
     const u64 top = w.largest();
@@ -856,16 +1222,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
         return;
     }
     {
-        // 512 log2(e) / T as hi + lo: 1 / T = y + y (1 - y T), good to 2^-46
-        constexpr double kFactor = 512.0 * 1.4426950408889634074;
-        constexpr float kHi = static_cast<float>(kFactor), kLo = static_cast<float>(kFactor - static_cast<double>(kHi));
-        const float y = 1.0f / temperature, yl = y * fmaf(-y, temperature, 1.0f), hi = fminf(y * kHi, 3e38f);
-        const float lo = fmaf(y, kHi, -hi) + fmaf(y, kLo, yl * kHi), x = logit_of(top);
-        w.scale = Scale{x, hi, fabsf(lo) <= 1e-6f * hi ? lo : 0.0f, isinf(x)};  // 0 where T or 1 / T is infinite
+        // 2 / T as hi + lo: 1 / T = y + y (1 - y T), good to 2^-46
+        const float y = 1.0f / temperature, hi = fminf(2.0f * y, 3e38f), lo = 2.0f * y * fmaf(-y, temperature, 1.0f), x = logit_of(top);
         // what is kept at all: above -inf, and not so small that a weight is nothing (2^-45 and below)
         const float none = x - 45.0f * 0.6931472f * temperature;
+        w.scale = Scale{x, hi, fabsf(lo) <= 1e-6f * hi ? lo : 0.0f, none > kNone ? none : kNone, isinf(x)};  // lo: 0 where T or 1 / T is infinite
         const u64 finite = static_cast<u64>(key_of(kNone) + 1) << 32;
         u64 cut = w.scale.flat ? top >> 32 << 32 : none > kNone ? max(finite, static_cast<u64>(key_of(none)) << 32) : finite;
+        w.easy = !w.scale.flat && none > kNone && !(min_p > 0.0f);
         if (min_p >= 1.0f) {
             cut = top >> 32 << 32;
         } else if (min_p > 0.0f) {
@@ -877,42 +1241,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
         w.keep_from(cut);
     }
     const bool by_count = top_k > 0 && top_k < c.vocab, by_mass = top_p < 1.0f;
-    auto target_of = [&](u64 total) { return max(part_of(total, fmaxf(top_p, 0.0f), true), 1ull); };
     if (by_count) {
-        w.template count<false>();
-        int bin;
-        uint32_t before;
-        w.template reach<uint32_t>([&](int b) { return s.all[b]; }, static_cast<uint32_t>(top_k), reinterpret_cast<uint32_t*>(s.sums), bin, before);
-        const uint32_t to = bin < kBins ? before + s.all[bin] : before;  // places to the end of that bin
-        if (to <= kList) {
-            const int last = min(bin, kBins - 1);
-            w.gather(0, w.lowest_of(last), [&](float x, int) { return bin_of(x, w.scale) <= last; });
-            if (rank == 0) {
-                w.sort(static_cast<int>(to));
-                int n = min(static_cast<int>(to), top_k);
-                if (by_mass) {
-                    u64 total;
-                    w.within(n, 1, total);
-                    n = w.within(n, target_of(total), total);
-                }
-                w.draw_list(n, u, c.tokens + r);
-            }
-            return;
+        if (top_k <= kList && w.draw_few(top_k, top_p, 0, u, c.tokens + r)) return;
+        w.count();
+        int bin = 0;
+        uint32_t before = 0, many = 0;
+        if (rank == 0) {
+            w.template reach<uint32_t>([&](int b) { return s.all[b]; }, static_cast<uint32_t>(top_k), reinterpret_cast<uint32_t*>(s.sums), bin, before);
+            many = bin < kBins ? s.all[bin] : 0;
         }
+        u64 (*box)[kMaxCtas] = w.tell(static_cast<u64>(bin) << 32 | many, before);
+        bin = static_cast<int>(box[0][0] >> 32);
+        many = static_cast<uint32_t>(box[0][0]);
+        before = static_cast<uint32_t>(box[1][0]);
         if (bin < kBins) {
-            const uint32_t n = s.all[bin];
-            w.keep_from(w.template inside<false>(0, bin, n, top_k - before));
-            if (by_mass) {  // the counts without what has been cut off
-                __syncthreads();
-                for (int b = bin + threadIdx.x; b < kBins; b += kThreads) s.all[b] = b == bin ? top_k - before : 0;
-                __syncthreads();
-            }
+            w.keep_from(w.template inside<false>(bin, many, top_k - before));
+            w.easy = false;
         }
-        if (by_mass) w.keep_from(w.nucleus(target_of(w.mass())));
-    } else if (by_mass) {
-        const u64 target = target_of(w.template count<true>());
-        if (w.draw_nucleus(target, u, c.tokens + r)) return;
-        w.keep_from(w.nucleus(target));
+    }
+    if (by_mass) {
+        const u64 total = w.mass(), target = target_of(total, top_p);
+        if (!by_count && w.draw_few(0, top_p, target, u, c.tokens + r)) return;
+        if (w.nucleus(total, target, u, c.tokens + r)) return;
+    } else {
+        w.weigh_groups();
     }
     w.draw(u, c.tokens + r);
 }
@@ -932,7 +1284,7 @@ cudaError_t launch(const SampleCall& c, int sm_count, cudaStream_t stream) {
     // fit an SM's shared memory
     const int64_t pieces = (c.vocab + Row<E>::kV - 1) / Row<E>::kV + 1, groups = (pieces + 31) / 32;
     int ctas = 1;
-    while (ctas < kMaxCtas && ((c.rows * ctas * 2 <= 2 * sm_count && c.vocab > 2048 * ctas) || groups > kMostGroups / 2 * ctas)) ctas *= 2;
+    while (ctas < kMaxCtas && ((c.rows * ctas * 2 <= 4 * sm_count && c.vocab > 2048 * ctas) || groups > kMostGroups / 2 * ctas)) ctas *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(c.rows * ctas));
     cfg.blockDim = dim3(kThreads);
