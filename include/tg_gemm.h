@@ -503,16 +503,18 @@ tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int64_t q_head_
  * sequence whose tokens before its new ones are fewer than shared[g] (an idle
  * slot, say) is attended by itself. No group has more than max_rows new tokens.
  * Results are tg_attention_kv's within its own bounds; there is no window. The
- * workspace query takes the same sizes.
+ * workspace query takes the same sizes. Where sharing cannot save 256 MB of reading
+ * by the bounds given (max_len, groups and sequences), or a sequence's own rows are
+ * many, the call is tg_attention_kv's.
  *
  * A shared[g] that is negative or beyond max_len or the table, and a group with
  * more than max_rows rows, are reported (TG_ERR_BOUNDS) and make the group's
  * sequences ones of no group. So do, for all groups, offsets that fall or are
  * out of range.
  */
-tg_status tg_attention_kv_shared_workspace(int64_t kv_heads, int64_t page, int64_t dim, int format, int64_t heads,
-                                           int64_t batch, int64_t total, int64_t group_count, int64_t max_new,
-                                           int64_t max_rows, int64_t max_len, int dtype, int64_t* bytes);
+tg_status tg_attention_kv_shared_workspace(int64_t kv_heads, int64_t page, int64_t dim, int format, int64_t table_width,
+                                           int64_t heads, int64_t batch, int64_t total, int64_t group_count,
+                                           int64_t max_new, int64_t max_rows, int64_t max_len, int dtype, int64_t* bytes);
 tg_status tg_attention_kv_shared(const void* Q, int64_t q_token_stride, int64_t q_head_stride, void* O, float* lse,
                                  const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
                                  int64_t pages, int64_t kv_heads, int64_t page, int64_t dim, int format,
@@ -654,6 +656,13 @@ tg_status tg_set_watchdog_ns(uint64_t ns);
  * first piece of work. Off by default; has no effect on other kernels.
  */
 tg_status tg_debug_skip_first_arrive(int on);
+
+/*
+ * Test hook: while `on` is non-zero, tg_attention_kv_shared (and its workspace
+ * query) reads what a group shares in a pass of its own however little that saves.
+ * Off by default.
+ */
+tg_status tg_debug_share_always(int on);
 
 /*
  * 1 if this library was compiled with TG_DEBUG=1, else 0. Debug builds check,

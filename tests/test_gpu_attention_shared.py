@@ -22,6 +22,14 @@ def tg():
     return m
 
 
+@pytest.fixture(autouse=True)
+def always(tg):
+    """The sizes here would not pay a pass of their own."""
+    tg.tg_debug_share_always(True)
+    yield
+    tg.tg_debug_share_always(False)
+
+
 def _share(table, groups, shared, lens, page):
     """Makes the sequences of each group begin with the pages of the group's longest."""
     for g, n in enumerate(shared):
@@ -132,6 +140,17 @@ def test_what_a_nan_in_the_prefix_reaches(tg):
     cache.v.view(torch.uint8)[table[0, 1], 0, 3] = 0x7F
     out = tg.attention_kv_shared(q.cuda(), cache, table.cuda(), _ints(lens), _ints([0, 3]), _ints([128]))
     assert out[:3, :4].isnan().all() and out[3:].isfinite().all() and out[:3, 4:].isfinite().all()
+    _status_ok(tg)
+
+
+@pytest.mark.parametrize("n,length", [(3, 700), (70, 8200)])  # too little to share, and enough
+def test_what_the_call_chooses(tg, n, length):
+    tg.tg_debug_share_always(False)
+    counts, lens, page = [1] * n, [length - 3 * (i % 5) for i in range(n)], 64
+    cache, host, table, q = attend._case(tg, counts, lens, page, 2, 8, 128, 0, 0)
+    _share(table, [0, n], [640], lens, page)
+    out, lse = tg.attention_kv_shared(q.cuda(), cache, table.cuda(), _ints(lens), _ints([0, n]), _ints([640]), max_len=length, return_lse=True)
+    _check(out, lse, host, table, q, counts, lens, page, True, 128 ** -0.5)
     _status_ok(tg)
 
 

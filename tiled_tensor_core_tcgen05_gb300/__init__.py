@@ -39,7 +39,7 @@ EXPORTS = ("tg_gemm", "tg_gemm_ex", "tg_gemm_plan", "tg_gemm_staged", "tg_gemm_s
            "tg_kv_copy", "tg_kv_fork_workspace", "tg_kv_fork", "tg_kv_compact_workspace", "tg_kv_compact", "tg_sample",
            "tg_device_status", "tg_debug_status",
            "tg_set_watchdog_ns",
-           "tg_debug_skip_first_arrive", "tg_debug_bounds_limit", "tg_debug_build", "tg_status_string",
+           "tg_debug_skip_first_arrive", "tg_debug_share_always", "tg_debug_bounds_limit", "tg_debug_build", "tg_status_string",
            "tg_last_error", "tg_version",
            "tg_ring_bytes", "tg_shutdown")
 
@@ -77,7 +77,7 @@ def bind(path: str) -> ctypes.CDLL:
     lib.tg_attention_kv_workspace.argtypes = [_i64, _i64, _i64, _int] + [_i64] * 6 + [_int, ctypes.POINTER(_i64)]
     lib.tg_attention_kv.argtypes = (strided + [_vp, _vp] + cache + batch + [_i64, _i64, _i64, _int, _i64, _dbl, _int,
                                                                             _vp, _i64, _vp])
-    lib.tg_attention_kv_shared_workspace.argtypes = [_i64, _i64, _i64, _int] + [_i64] * 7 + [_int, ctypes.POINTER(_i64)]
+    lib.tg_attention_kv_shared_workspace.argtypes = [_i64, _i64, _i64, _int] + [_i64] * 8 + [_int, ctypes.POINTER(_i64)]
     lib.tg_attention_kv_shared.argtypes = (strided + [_vp, _vp] + cache + batch + [_i64, _i64, _i64, _int, _vp, _vp, _i64, _i64, _dbl,
                                                                                    _int, _vp, _i64, _vp])
     lib.tg_kv_copy.argtypes = [_vp] * 4 + [_i64] + [_vp] * 4 + [_i64] * 4 + [_int, _vp, _vp, _i64, _vp]
@@ -90,6 +90,7 @@ def bind(path: str) -> ctypes.CDLL:
     lib.tg_debug_status.argtypes = [_vp]
     lib.tg_set_watchdog_ns.argtypes = [_u64]
     lib.tg_debug_skip_first_arrive.argtypes = [_int]
+    lib.tg_debug_share_always.argtypes = [_int]
     lib.tg_debug_bounds_limit.argtypes = [_i64]
     lib.tg_debug_build.argtypes = []
     lib.tg_status_string.argtypes = [_int]
@@ -105,7 +106,7 @@ def bind(path: str) -> ctypes.CDLL:
                  "tg_gemm_w4_kernel", "tg_attention_fwd", "tg_softmax_rows", "tg_bias_gelu", "tg_rope", "tg_kv_append", "tg_kv_read", "tg_attention_kv_workspace",
                  "tg_attention_kv", "tg_attention_kv_shared_workspace", "tg_attention_kv_shared", "tg_kv_copy", "tg_kv_fork_workspace", "tg_kv_fork", "tg_kv_compact_workspace", "tg_kv_compact", "tg_sample",
                  "tg_device_status", "tg_debug_status",
-                 "tg_set_watchdog_ns", "tg_debug_skip_first_arrive", "tg_debug_bounds_limit", "tg_debug_build",
+                 "tg_set_watchdog_ns", "tg_debug_skip_first_arrive", "tg_debug_share_always", "tg_debug_bounds_limit", "tg_debug_build",
                  "tg_version"):
         getattr(lib, name).restype = _int
     return lib
@@ -258,12 +259,12 @@ def tg_attention_kv(*args) -> None:
     _check(_lib.tg_attention_kv(*args))
 
 
-def tg_attention_kv_shared_workspace(kv_heads: int, page: int, dim: int, fmt: int, heads: int, batch: int, total: int,
-                                     group_count: int, max_new: int, max_rows: int, max_len: int, dtype: int) -> int:
+def tg_attention_kv_shared_workspace(kv_heads: int, page: int, dim: int, fmt: int, table_width: int, heads: int,
+                                     batch: int, total: int, group_count: int, max_new: int, max_rows: int, max_len: int, dtype: int) -> int:
     """Bytes of workspace that tg_attention_kv_shared needs for these sizes."""
     n = _i64()
-    _check(_lib.tg_attention_kv_shared_workspace(kv_heads, page, dim, fmt, heads, batch, total, group_count, max_new,
-                                                 max_rows, max_len, dtype, ctypes.byref(n)))
+    _check(_lib.tg_attention_kv_shared_workspace(kv_heads, page, dim, fmt, table_width, heads, batch, total, group_count,
+                                                 max_new, max_rows, max_len, dtype, ctypes.byref(n)))
     return n.value
 
 
@@ -323,6 +324,10 @@ def tg_set_watchdog_ns(ns: int) -> None:
 
 def tg_debug_skip_first_arrive(on: bool) -> None:
     _check(_lib.tg_debug_skip_first_arrive(1 if on else 0))
+
+
+def tg_debug_share_always(on: bool) -> None:
+    _check(_lib.tg_debug_share_always(1 if on else 0))
 
 
 def tg_debug_bounds_limit(floats: int) -> None:

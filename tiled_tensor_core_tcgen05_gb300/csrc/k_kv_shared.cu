@@ -12,7 +12,9 @@
 //
 // Where the rows of one sequence are many by themselves (more than few_rows allows)
 // a cache is read once for 256 of them in any case, and products bound the
-// call: then it is attended as without groups.
+// call; and where there is little to save, two passes cost more than they save
+// (pays()): then it is attended as without groups.
+#include <algorithm>
 #include <climits>
 
 #include "tg_device.cuh"
@@ -152,15 +154,28 @@ SharedWork layout(const KvSharedCall& s, int sm_count, void* at) {
     return w;
 }
 
+// Whether groups are worth their pass. What sharing can save at most is the reading of all sequences but one a group, as long as they may
+// be; the further pass, the kernel before it and the join take 20 to 50 us. Measured on a GB300, in us with groups and without,
+// 32 heads over 8 of 128: 8 sequences of 4000 (58 MB to save) 32 and 18, of 16000 (230 MB) 39 and 42; 64 of 1000 (133 MB) 47 and 29, of 4000 (520 MB)
+// 62 and 76, of 16000 76 and 258; four groups of 16 of 1000 (117 MB) 39 and 28, of 4000 (418 MB) 49 and 66. The bounds that the caller gives
+// are all that is known here: loose ones are taken for long sequences.
+bool pays(const KvSharedCall& s) {
+    const KvAttnCall& c = s.c;
+    const int64_t each = std::min(c.max_len, c.batch.table_width * c.cache.page) * c.cache.kv_heads * c.cache.dim * 2;
+    return s.always || each * (c.batch.batch - s.group_count) >= (256ll << 20);
+}
+
+bool in_groups(const KvSharedCall& s) { return s.group_count > 0 && kv_attn_few_rows(s.c) && pays(s); }
+
 }  // namespace
 
 int64_t kv_attn_shared_workspace(const KvSharedCall& s, int sm_count) {
-    return s.group_count > 0 && kv_attn_few_rows(s.c) ? layout(s, sm_count, nullptr).bytes : kv_attn_workspace(s.c, sm_count);
+    return in_groups(s) ? layout(s, sm_count, nullptr).bytes : kv_attn_workspace(s.c, sm_count);
 }
 
 cudaError_t launch_kv_attn_shared(const KvSharedCall& s, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count,
                                   cudaStream_t stream) {
-    if (s.group_count == 0 || !kv_attn_few_rows(s.c)) return launch_kv_attn(s.c, tmK, tmV, workspace, sm_count, stream);
+    if (!in_groups(s)) return launch_kv_attn(s.c, tmK, tmV, workspace, sm_count, stream);
     const SharedWork w = layout(s, sm_count, workspace);
     group_kernel<<<s.group_count + (s.c.batch.batch + kThreads - 1) / kThreads, kThreads, 0, stream>>>(s, w);
     cudaError_t e = cudaGetLastError();

@@ -593,6 +593,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     up *= __int_as_float((14 - e + 127) << 23);
                     f *= __int_as_float((e - 14 + 127) << 23);
                 }
+                const uint32_t to_row = sbase + L::kQ + h * L::kTile + row * 128;
+                if (std::is_same<E, __half>::value && c.scale >= 0.0f && a.q_vec != 0) {  // no arithmetic: all reads at once
+                    uint4 w[kDim / 16];
+#pragma unroll
+                    for (int i = 0; i < kDim / 16; ++i) w[i] = real ? __ldg(reinterpret_cast<const uint4*>(x + kh * (kDim / 2)) + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < kDim / 16; ++i) {
+                        const int d = kh * (kDim / 2) + i * 8;
+                        sts_v4(to_row + (d >> 6) * L::kBox + ((((d & 63) >> 3) ^ (row & 7)) << 4), w[i]);
+                    }
+                } else
 #pragma unroll 4
                 for (int i = 0; i < kDim / 2; i += 8) {
                     const int d = kh * (kDim / 2) + i;

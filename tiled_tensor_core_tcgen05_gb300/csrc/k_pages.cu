@@ -20,11 +20,17 @@
 namespace tg {
 namespace {
 
-constexpr int kCtas = 8;          // of the cluster (the portable most)
+constexpr int kMostCtas = 8;      // of the cluster (the portable most)
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAll = kCtas * kThreads;
 constexpr int kSeg = 256;         // entries of a table's row that a warp takes at a time
+
+// All threads of the cluster: a block's barrier where it is a single CTA.
+template <int kCtas>
+__device__ __forceinline__ void meet() {
+    if constexpr (kCtas == 1) __syncthreads();
+    else cluster_sync();
+}
 
 // What other CTAs of the cluster have written: past the first-level cache.
 __device__ __forceinline__ int fresh(const int* p) { return __ldcg(p); }
@@ -36,6 +42,7 @@ struct Order {
 
 // All threads. Every CTA writes its sum into the others' `box` (a call's own; every CTA must be known to run); the
 // cluster's barrier is inside.
+template <int kCtas>
 __device__ __forceinline__ Order cluster_order(int mine, int64_t* box, int* warps, uint32_t rank) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = mine;
@@ -56,7 +63,7 @@ __device__ __forceinline__ Order cluster_order(int mine, int64_t* box, int* warp
         const uint32_t to = mapa_shared(smem_u32(box + rank), threadIdx.x);
         asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(to), "l"(static_cast<int64_t>(sum)) : "memory");
     }
-    cluster_sync();
+    meet<kCtas>();
     Order o{low + x - mine, 0};
     for (uint32_t r = 0; r < kCtas; ++r) {
         if (r < rank) o.before += box[r];
@@ -68,15 +75,15 @@ __device__ __forceinline__ Order cluster_order(int mine, int64_t* box, int* warp
 // A thread's `pages` are places first .. last - 1: contiguous, thread after thread in the order of Order.
 struct Range {
     int first, last;
-    __device__ Range(int64_t n, int t) {
-        const int64_t each = (n + kAll - 1) / kAll;
+    __device__ Range(int64_t n, int t, int all) {
+        const int64_t each = (n + all - 1) / all;
         first = static_cast<int>(min(n, each * t));
         last = static_cast<int>(min(n, each * (t + 1)));
     }
 };
 
 // Entries of a table's rows, a warp at a time kSeg of one row: f(row, place).
-template <typename F>
+template <int kAll, typename F>
 __device__ __forceinline__ void for_entries(int rows, int64_t width, int t, F f) {
     const int64_t segs = (width + kSeg - 1) / kSeg;
     for (int64_t s = t / 32; s < rows * segs; s += kAll / 32) {
@@ -123,7 +130,9 @@ __device__ __forceinline__ Child child_of(const KvForkCall& c, int i, bool tell)
     return x;
 }
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) fork_kernel(const KvForkCall c) {
+template <int kCtas>
+__global__ void __launch_bounds__(kThreads, 1) fork_kernel(const KvForkCall c) {
+    constexpr int kAll = kCtas * kThreads;
     __shared__ int64_t box[2][kCtas];
     __shared__ int warps[kWarps];
     __shared__ int64_t carry;
@@ -140,7 +149,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
         w.first[j] = INT_MAX;
         w.held[j] = static_cast<int>(c.width);
     }
-    cluster_sync();
+    meet<kCtas>();
     // children of each sequence, and the first of them; its pages are the entries before the first that is none
     for (int i = t; i < c.count; i += kAll) {
         const int p = parent_of(c, i);
@@ -148,13 +157,13 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
         atomicAdd(w.children + p, 1);
         atomicMin(w.first + p, i);
     }
-    for_entries(c.batch, c.width, t, [&](int j, int at) {
+    for_entries<kAll>(c.batch, c.width, t, [&](int j, int at) {
         const int p = __ldg(c.table + j * c.width + at);
         if (p >= 0 && p < pages) return;
         if (p >= 0) report_range(c.wd);
         atomicMin(w.held + j, at);
     });
-    cluster_sync();
+    meet<kCtas>();
     // the entries that the first child takes over: the full pages, and open ones that no other sequence holds
     for (int j = t; j < c.batch; j += kAll) {
         const int held = fresh(w.held + j);
@@ -168,17 +177,17 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
         w.lens[j] = len;
         w.kept[j] = kept;
     }
-    cluster_sync();
+    meet<kCtas>();
     // entries that come and go; a page that tokens are copied from is let go of after the free ones have been
     // counted, so that it is not given away in the same call
-    for_entries(c.batch, c.width, t, [&](int j, int at) {
+    for_entries<kAll>(c.batch, c.width, t, [&](int j, int at) {
         if (at >= fresh(w.held + j)) return;
         const int children = fresh(w.children + j), len = fresh(w.lens + j), full = len >> c.page_shift, kept = fresh(w.kept + j);
         const int d = at < full ? children - 1 : at < kept && children > 0 ? 0 : -1;
         if (d == 0 || (at == full && at >= kept && children > 0 && (len & (page - 1)))) return;
         atomicAdd(c.refs_out + __ldg(c.table + j * c.width + at), d);
     });
-    for_entries(c.count, c.width, t, [&](int i, int at) {
+    for_entries<kAll>(c.count, c.width, t, [&](int i, int at) {
         const Child x = child_of(c, i, false);
         c.table_out[i * c.width + at] = at < x.start ? __ldg(c.table + x.parent * c.width + at) : -1;
     });
@@ -187,7 +196,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
         c.lens_out[i] = x.len;
         w.need[i] = x.end - x.start;
     }
-    cluster_sync();
+    meet<kCtas>();
     // where each child's new pages begin in the list of all of them: every CTA by itself
     if (threadIdx.x == 0) carry = 0;
     for (int base = 0; base < c.count; base += kThreads) {
@@ -214,10 +223,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
     __syncthreads();
     const int64_t wanted = carry;
     // the free pages, in rising order
-    const Range r(pages, t);
+    const Range r(pages, t, kAll);
     int mine = 0;
     for (int p = r.first; p < r.last; ++p) mine += fresh(c.refs_out + p) == 0;
-    const Order o = cluster_order(mine, box[0], warps, rank);
+    const Order o = cluster_order<kCtas>(mine, box[0], warps, rank);
     int64_t k = o.before;
     for (int p = r.first; p < r.last && k < wanted; ++p)
         if (fresh(c.refs_out + p) == 0) {
@@ -225,7 +234,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
             c.refs_out[p] = 1;
         }
     if (t == 0) *c.spare = static_cast<int>(max(o.total - wanted, static_cast<int64_t>(INT_MIN)));
-    cluster_sync();
+    meet<kCtas>();
     for (int i = t / 32; i < c.count; i += kAll / 32) {
         const Child x = child_of(c, i, false);
         const int64_t place = __ldcg(w.place + i);
@@ -247,26 +256,28 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
 
 // ---------------------------------------------------------------- compacting
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) compact_kernel(const KvCompactCall c) {
+template <int kCtas>
+__global__ void __launch_bounds__(kThreads, 1) compact_kernel(const KvCompactCall c) {
+    constexpr int kAll = kCtas * kThreads;
     __shared__ int64_t box[3][kCtas];
     __shared__ int warps[kWarps];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t rank = cluster_ctarank();
     const int t = rank * kThreads + threadIdx.x;
     const int64_t pages = c.cache.pages;
-    const Range r(pages, t);
+    const Range r(pages, t, kAll);
     int mine = 0;
     for (int p = r.first; p < r.last; ++p) mine += __ldg(c.refs + p) > 0;
-    cluster_sync();  // every CTA runs: its shared memory may be written
-    const int64_t used = cluster_order(mine, box[0], warps, rank).total;
+    meet<kCtas>();  // every CTA runs: its shared memory may be written
+    const int64_t used = cluster_order<kCtas>(mine, box[0], warps, rank).total;
     int holes = 0, movers = 0;
     for (int p = r.first; p < r.last; ++p) {
         const bool held = __ldg(c.refs + p) > 0;
         holes += !held && p < used;
         movers += held && p >= used;
     }
-    const Order hole = cluster_order(holes, box[1], warps, rank);
-    const Order mover = cluster_order(movers, box[2], warps, rank);
+    const Order hole = cluster_order<kCtas>(holes, box[1], warps, rank);
+    const Order mover = cluster_order<kCtas>(movers, box[2], warps, rank);
     int64_t h = hole.before, m = mover.before;
     for (int p = r.first; p < r.last; ++p) {
         const int n = __ldg(c.refs + p);
@@ -275,7 +286,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) com
         if (n <= 0 && p < used) c.w.items[h++].to = p;
         if (n > 0 && p >= used) c.w.items[m++].from = p;
     }
-    cluster_sync();
+    meet<kCtas>();
     for (int64_t i = t; i < mover.total; i += kAll) {
         PageItem* x = c.w.items + i;
         const int from = fresh(&x->from), to = fresh(&x->to);
@@ -287,8 +298,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) com
         *c.used = static_cast<int>(used);
         *c.w.items_count = static_cast<int>(mover.total);
     }
-    cluster_sync();
-    for_entries(c.batch, c.width, t, [&](int j, int at) {
+    meet<kCtas>();
+    for_entries<kAll>(c.batch, c.width, t, [&](int j, int at) {
         int p = __ldg(c.table + j * c.width + at);
         if (p >= pages) report_range(c.wd);
         c.table_out[j * c.width + at] = p >= 0 && p < pages ? fresh(c.moved + p) : -1;
@@ -364,6 +375,23 @@ cudaError_t launch_listed(const KvCacheArgs& cache, const PageWork& w, int64_t m
     return cudaLaunchKernelEx(&cfg, copy_pages_kernel<true>, c);
 }
 
+// Pages and entries up to which one CTA keeps the books: its barrier takes a fraction of the cluster's.
+constexpr int64_t kLittle = 16384;
+
+template <typename C>
+cudaError_t launch_books(void (*kernel)(const C), const C& c, int ctas, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {static_cast<unsigned>(ctas), 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, c);
+}
+
 int64_t up(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 }  // namespace
@@ -400,14 +428,12 @@ cudaError_t launch_kv_copy(const PageCopyCall& c, int sm_count, cudaStream_t str
 }
 
 cudaError_t launch_kv_fork(const KvForkCall& c, int sm_count, cudaStream_t stream) {
-    fork_kernel<<<kCtas, kThreads, 0, stream>>>(c);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = c.cache.pages + (c.batch + c.count) * c.width <= kLittle ? launch_books(fork_kernel<1>, c, 1, stream) : launch_books(fork_kernel<kMostCtas>, c, kMostCtas, stream);
     return e != cudaSuccess || c.count == 0 || c.cache.pages == 0 ? e : launch_listed(c.cache, c.w, c.count, sm_count, stream);
 }
 
 cudaError_t launch_kv_compact(const KvCompactCall& c, int sm_count, cudaStream_t stream) {
-    compact_kernel<<<kCtas, kThreads, 0, stream>>>(c);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = c.cache.pages + c.batch * c.width <= kLittle ? launch_books(compact_kernel<1>, c, 1, stream) : launch_books(compact_kernel<kMostCtas>, c, kMostCtas, stream);
     return e != cudaSuccess || c.cache.pages < 2 ? e : launch_listed(c.cache, c.w, c.cache.pages / 2, sm_count, stream);
 }
 

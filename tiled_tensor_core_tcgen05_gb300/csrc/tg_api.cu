@@ -1709,6 +1709,8 @@ extern "C" tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int6
 
 namespace {
 
+bool g_share_always = false;  // tg_debug_share_always
+
 tg_status check_groups(int64_t total, int64_t group_count, int64_t max_rows, const KvAttnCall& c, KvSharedCall* s) {
     if (group_count < 0 || group_count > c.batch.batch)
         return fail(TG_ERR_INVALID_ARG, "there are at most as many groups as sequences, got %lld of %d", (long long)group_count, c.batch.batch);
@@ -1717,15 +1719,22 @@ tg_status check_groups(int64_t total, int64_t group_count, int64_t max_rows, con
     s->c = c;
     s->group_count = (int)group_count;
     s->max_rows = (int)(max_rows < total ? max_rows : total);
+    s->always = g_share_always;
     return TG_OK;
 }
 
 }  // namespace
 
+extern "C" tg_status tg_debug_share_always(int on) {
+    t_last_error.clear();
+    g_share_always = on != 0;
+    return TG_OK;
+}
+
 extern "C" tg_status tg_attention_kv_shared_workspace(int64_t kv_heads, int64_t page, int64_t dim, int format,
-                                                      int64_t heads, int64_t batch, int64_t total, int64_t group_count,
-                                                      int64_t max_new, int64_t max_rows, int64_t max_len, int dtype,
-                                                      int64_t* bytes) {
+                                                      int64_t table_width, int64_t heads, int64_t batch, int64_t total,
+                                                      int64_t group_count, int64_t max_new, int64_t max_rows,
+                                                      int64_t max_len, int dtype, int64_t* bytes) {
     t_last_error.clear();
     if (bytes == nullptr) return fail(TG_ERR_INVALID_ARG, "bytes is NULL");
     *bytes = 0;
@@ -1734,7 +1743,7 @@ extern "C" tg_status tg_attention_kv_shared_workspace(int64_t kv_heads, int64_t 
     static const int32_t some = 0;
     tg_status st = check_cache(nullptr, nullptr, nullptr, nullptr, 0, kv_heads, page, dim, format, &c.cache);
     if (st != TG_OK) return st;
-    if ((st = check_batch(&some, 0, &some, &some, batch, total, max_new, page, &c.batch)) != TG_OK) return st;
+    if ((st = check_batch(&some, table_width, &some, &some, batch, total, max_new, page, &c.batch)) != TG_OK) return st;
     if ((st = kv_attn_sizes(kv_heads, page, heads, total, max_len, 0, dtype, &c)) != TG_OK) return st;
     if ((st = check_groups(total, group_count, max_rows, c, &s)) != TG_OK) return st;
     if (total == 0) return TG_OK;

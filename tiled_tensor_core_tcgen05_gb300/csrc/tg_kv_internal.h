@@ -99,6 +99,7 @@ struct KvSharedCall {
     const int32_t* groups;
     const int32_t* shared;
     int group_count, max_rows;
+    bool always;       // whatever it pays: tests
 };
 
 // A page's first tokens on their way to another page.

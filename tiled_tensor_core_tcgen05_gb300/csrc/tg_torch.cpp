@@ -444,7 +444,7 @@ PyObject* attention_kv_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const bool want_lse = truth(a[12]);
         const Where where(a[14]);
         int64_t need = 0;
-        const int status = tg_attention_kv_shared_workspace(c.kv_heads, c.page, D, c.format, H, b.batch, T, G, max_new, max_rows, max_len, dtype, &need);
+        const int status = tg_attention_kv_shared_workspace(c.kv_heads, c.page, D, c.format, b.width, H, b.batch, T, G, max_new, max_rows, max_len, dtype, &need);
         if (status != TG_OK) return PyLong_FromLong(status);
         Attended o(a[13], Q, want_lse);
         at::Tensor work;
