@@ -82,17 +82,18 @@ struct Range {
     }
 };
 
-// Entries of a table's rows, a warp at a time kSeg of one row: f(row, place).
-template <int kAll, typename F>
-__device__ __forceinline__ void for_entries(int rows, int64_t width, int t, F f) {
+// Entries of a table's rows, a warp at a time kSeg of one row: f(row, place, what `of` says of the row).
+template <int kAll, typename G, typename F>
+__device__ __forceinline__ void for_entries(int rows, int64_t width, int t, G of, F f) {
     const int64_t segs = (width + kSeg - 1) / kSeg;
     for (int64_t s = t / 32; s < rows * segs; s += kAll / 32) {
         const int row = static_cast<int>(s / segs);
         const int64_t base = (s - row * segs) * kSeg;
+        const auto x = of(row);
 #pragma unroll
         for (int i = 0; i < kSeg / 32; ++i) {
             const int64_t at = base + i * 32 + (t & 31);
-            if (at < width) f(row, static_cast<int>(at));
+            if (at < width) f(row, static_cast<int>(at), x);
         }
     }
 }
@@ -110,18 +111,26 @@ __device__ __forceinline__ int parent_of(const KvForkCall& c, int i) {
     return p;
 }
 
+// What the steps of a fork leave for one another: in the workspace, or for a single CTA in its shared memory.
+template <int kCtas>
+__device__ __forceinline__ int left(const int* p) {
+    if constexpr (kCtas == 1) return *p;
+    else return fresh(p);
+}
+
 // A child's pages: entries below `start` come from its parent, those up to `end` are new.
 struct Child {
     int parent, len, start, end;
     int source;  // page whose tokens go to the first new one, or -1
 };
 
-__device__ __forceinline__ Child child_of(const KvForkCall& c, int i, bool tell) {
+template <int kCtas>
+__device__ __forceinline__ Child child_of(const KvForkCall& c, const ForkWork& w, int i, bool tell) {
     Child x{parent_of(c, i), 0, 0, 0, -1};
     if (x.parent >= 0) {
-        x.len = fresh(c.w.lens + x.parent);
+        x.len = left<kCtas>(w.lens + x.parent);
         const int full = x.len >> c.page_shift;
-        x.start = fresh(c.w.first + x.parent) == i ? fresh(c.w.kept + x.parent) : full;
+        x.start = left<kCtas>(w.first + x.parent) == i ? left<kCtas>(w.kept + x.parent) : full;
         if ((x.len & (c.cache.page - 1)) && x.start == full) x.source = __ldg(c.table + x.parent * c.width + full);
     }
     const int64_t want = (x.len + c.room + c.cache.page - 1) >> c.page_shift;
@@ -141,9 +150,22 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const KvForkCall c) {
     const int t = rank * kThreads + threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int page = c.cache.page;
     const int64_t pages = c.cache.pages;
-    const ForkWork& w = c.w;
+    ForkWork w = c.w;
+    int32_t* refs = c.refs_out;
+    if constexpr (kCtas == 1) {
+        extern __shared__ int64_t held_here[];
+        w.place = held_here;
+        w.children = reinterpret_cast<int*>(held_here + c.count);
+        w.first = w.children + c.batch;
+        w.held = w.first + c.batch;
+        w.lens = w.held + c.batch;
+        w.kept = w.lens + c.batch;
+        w.need = w.kept + c.batch;
+        refs = w.need + c.count;
+        w.given = refs + pages;
+    }
 
-    for (int64_t p = t; p < pages; p += kAll) c.refs_out[p] = __ldg(c.refs + p);
+    for (int64_t p = t; p < pages; p += kAll) refs[p] = __ldg(c.refs + p);
     for (int j = t; j < c.batch; j += kAll) {
         w.children[j] = 0;
         w.first[j] = INT_MAX;
@@ -157,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const KvForkCall c) {
         atomicAdd(w.children + p, 1);
         atomicMin(w.first + p, i);
     }
-    for_entries<kAll>(c.batch, c.width, t, [&](int j, int at) {
+    for_entries<kAll>(c.batch, c.width, t, [](int) { return 0; }, [&](int j, int at, int) {
         const int p = __ldg(c.table + j * c.width + at);
         if (p >= 0 && p < pages) return;
         if (p >= 0) report_range(c.wd);
@@ -166,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const KvForkCall c) {
     meet<kCtas>();
     // the entries that the first child takes over: the full pages, and open ones that no other sequence holds
     for (int j = t; j < c.batch; j += kAll) {
-        const int held = fresh(w.held + j);
+        const int held = left<kCtas>(w.held + j);
         int len = __ldg(c.lens + j);
         if (len < 0 || len > static_cast<int64_t>(held) * page) {
             report_range(c.wd);
@@ -180,19 +202,22 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const KvForkCall c) {
     meet<kCtas>();
     // entries that come and go; a page that tokens are copied from is let go of after the free ones have been
     // counted, so that it is not given away in the same call
-    for_entries<kAll>(c.batch, c.width, t, [&](int j, int at) {
-        if (at >= fresh(w.held + j)) return;
-        const int children = fresh(w.children + j), len = fresh(w.lens + j), full = len >> c.page_shift, kept = fresh(w.kept + j);
-        const int d = at < full ? children - 1 : at < kept && children > 0 ? 0 : -1;
-        if (d == 0 || (at == full && at >= kept && children > 0 && (len & (page - 1)))) return;
-        atomicAdd(c.refs_out + __ldg(c.table + j * c.width + at), d);
-    });
-    for_entries<kAll>(c.count, c.width, t, [&](int i, int at) {
-        const Child x = child_of(c, i, false);
+    struct Old {
+        int held, children, len, kept;
+    };
+    for_entries<kAll>(
+        c.batch, c.width, t, [&](int j) { return Old{left<kCtas>(w.held + j), left<kCtas>(w.children + j), left<kCtas>(w.lens + j), left<kCtas>(w.kept + j)}; },
+        [&](int j, int at, const Old& x) {
+            if (at >= x.held) return;
+            const int full = x.len >> c.page_shift, d = at < full ? x.children - 1 : at < x.kept && x.children > 0 ? 0 : -1;
+            if (d == 0 || (at == full && at >= x.kept && x.children > 0 && (x.len & (page - 1)))) return;
+            atomicAdd(refs + __ldg(c.table + j * c.width + at), d);
+        });
+    for_entries<kAll>(c.count, c.width, t, [&](int i) { return child_of<kCtas>(c, w, i, false); }, [&](int i, int at, const Child& x) {
         c.table_out[i * c.width + at] = at < x.start ? __ldg(c.table + x.parent * c.width + at) : -1;
     });
     for (int i = t; i < c.count; i += kAll) {
-        const Child x = child_of(c, i, true);
+        const Child x = child_of<kCtas>(c, w, i, true);
         c.lens_out[i] = x.len;
         w.need[i] = x.end - x.start;
     }
@@ -200,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const KvForkCall c) {
     // where each child's new pages begin in the list of all of them: every CTA by itself
     if (threadIdx.x == 0) carry = 0;
     for (int base = 0; base < c.count; base += kThreads) {
-        const int i = base + threadIdx.x, n = i < c.count ? fresh(w.need + i) : 0;
+        const int i = base + threadIdx.x, n = i < c.count ? left<kCtas>(w.need + i) : 0;
         int x = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -225,33 +250,42 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const KvForkCall c) {
     // the free pages, in rising order
     const Range r(pages, t, kAll);
     int mine = 0;
-    for (int p = r.first; p < r.last; ++p) mine += fresh(c.refs_out + p) == 0;
+    for (int p = r.first; p < r.last; ++p) mine += left<kCtas>(refs + p) == 0;
     const Order o = cluster_order<kCtas>(mine, box[0], warps, rank);
     int64_t k = o.before;
     for (int p = r.first; p < r.last && k < wanted; ++p)
-        if (fresh(c.refs_out + p) == 0) {
+        if (left<kCtas>(refs + p) == 0) {
             w.given[k++] = p;
-            c.refs_out[p] = 1;
+            refs[p] = 1;
         }
     if (t == 0) *c.spare = static_cast<int>(max(o.total - wanted, static_cast<int64_t>(INT_MIN)));
     meet<kCtas>();
     for (int i = t / 32; i < c.count; i += kAll / 32) {
-        const Child x = child_of(c, i, false);
-        const int64_t place = __ldcg(w.place + i);
+        const Child x = child_of<kCtas>(c, w, i, false);
+        const int64_t place = kCtas == 1 ? w.place[i] : __ldcg(w.place + i);
         for (int at = x.start + lane; at < x.end; at += 32) {
             const int64_t g = place + at - x.start;
-            c.table_out[i * c.width + at] = g < o.total ? fresh(w.given + g) : -1;
+            c.table_out[i * c.width + at] = g < o.total ? left<kCtas>(w.given + g) : -1;
         }
         if (lane == 0) {
             const bool copied = x.source >= 0 && x.end > x.start && place < o.total;
-            w.items[i] = PageItem{x.source, copied ? fresh(w.given + place) : 0, copied ? x.len & (page - 1) : 0};
+            w.items[i] = PageItem{x.source, copied ? left<kCtas>(w.given + place) : 0, copied ? x.len & (page - 1) : 0};
         }
     }
     for (int j = t; j < c.batch; j += kAll) {
-        const int len = fresh(w.lens + j), full = len >> c.page_shift;
-        if ((len & (page - 1)) && fresh(w.kept + j) == full && fresh(w.children + j) > 0) atomicAdd(c.refs_out + __ldg(c.table + j * c.width + full), -1);
+        const int len = left<kCtas>(w.lens + j), full = len >> c.page_shift;
+        if ((len & (page - 1)) && left<kCtas>(w.kept + j) == full && left<kCtas>(w.children + j) > 0) atomicAdd(refs + __ldg(c.table + j * c.width + full), -1);
     }
     if (t == 0) *w.items_count = c.count;
+    if constexpr (kCtas == 1) {
+        __syncthreads();
+        for (int64_t p = t; p < pages; p += kAll) c.refs_out[p] = refs[p];
+    }
+}
+
+// Shared memory that a single CTA's fork needs.
+int64_t fork_smem(const KvForkCall& c) {
+    return c.count * 8 + (c.batch * 5ll + c.count + c.cache.pages + std::min(c.cache.pages, c.count * c.width)) * 4;
 }
 
 // ---------------------------------------------------------------- compacting
@@ -299,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const KvCompactCal
         *c.w.items_count = static_cast<int>(mover.total);
     }
     meet<kCtas>();
-    for_entries<kAll>(c.batch, c.width, t, [&](int j, int at) {
+    for_entries<kAll>(c.batch, c.width, t, [](int) { return 0; }, [&](int j, int at, int) {
         int p = __ldg(c.table + j * c.width + at);
         if (p >= pages) report_range(c.wd);
         c.table_out[j * c.width + at] = p >= 0 && p < pages ? fresh(c.moved + p) : -1;
@@ -375,14 +409,17 @@ cudaError_t launch_listed(const KvCacheArgs& cache, const PageWork& w, int64_t m
     return cudaLaunchKernelEx(&cfg, copy_pages_kernel<true>, c);
 }
 
-// Pages and entries up to which one CTA keeps the books: its barrier takes a fraction of the cluster's.
+// Pages and entries up to which one CTA keeps the books: its barrier takes a fraction of the cluster's, and what the steps of a fork leave
+// for one another stays in its shared memory.
 constexpr int64_t kLittle = 16384;
+constexpr int kMostSmem = 128 * 1024;
 
 template <typename C>
-cudaError_t launch_books(void (*kernel)(const C), const C& c, int ctas, cudaStream_t stream) {
+cudaError_t launch_books(void (*kernel)(const C), const C& c, int ctas, int64_t smem, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -428,12 +465,25 @@ cudaError_t launch_kv_copy(const PageCopyCall& c, int sm_count, cudaStream_t str
 }
 
 cudaError_t launch_kv_fork(const KvForkCall& c, int sm_count, cudaStream_t stream) {
-    const cudaError_t e = c.cache.pages + (c.batch + c.count) * c.width <= kLittle ? launch_books(fork_kernel<1>, c, 1, stream) : launch_books(fork_kernel<kMostCtas>, c, kMostCtas, stream);
+    const int64_t smem = fork_smem(c);
+    cudaError_t e;
+    if (c.cache.pages + (c.batch + c.count) * c.width <= kLittle && smem <= kMostSmem) {
+        static int attr_gen[64] = {};
+        int dev = 0;
+        if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+        if (dev < 64 && attr_gen[dev] != g_generation) {
+            if ((e = cudaFuncSetAttribute(fork_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem)) != cudaSuccess) return e;
+            attr_gen[dev] = g_generation;
+        }
+        e = launch_books(fork_kernel<1>, c, 1, smem, stream);
+    } else {
+        e = launch_books(fork_kernel<kMostCtas>, c, kMostCtas, 0, stream);
+    }
     return e != cudaSuccess || c.count == 0 || c.cache.pages == 0 ? e : launch_listed(c.cache, c.w, c.count, sm_count, stream);
 }
 
 cudaError_t launch_kv_compact(const KvCompactCall& c, int sm_count, cudaStream_t stream) {
-    const cudaError_t e = c.cache.pages + c.batch * c.width <= kLittle ? launch_books(compact_kernel<1>, c, 1, stream) : launch_books(compact_kernel<kMostCtas>, c, kMostCtas, stream);
+    const cudaError_t e = c.cache.pages + c.batch * c.width <= kLittle ? launch_books(compact_kernel<1>, c, 1, 0, stream) : launch_books(compact_kernel<kMostCtas>, c, kMostCtas, 0, stream);
     return e != cudaSuccess || c.cache.pages < 2 ? e : launch_listed(c.cache, c.w, c.cache.pages / 2, sm_count, stream);
 }
 
