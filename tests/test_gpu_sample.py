@@ -59,7 +59,8 @@ def _check(tg, x, u, t=None, k=None, p=None, m=None, **how):
     """x, u on the CPU; settings numbers, or lists of one a row."""
     rows = x.shape[0]
     on = lambda v, d: torch.tensor(v, dtype=d, device="cuda") if isinstance(v, list) else v  # noqa: E731
-    got = tg.sample(how.get("device_x", x.cuda()), u.cuda(), on(t, torch.float32), on(k, torch.int32), on(p, torch.float32), on(m, torch.float32))
+    out = torch.full((rows,), -7, dtype=torch.int32, device="cuda")  # that every row writes
+    got = tg.sample(how.get("device_x", x.cuda()), u.cuda(), on(t, torch.float32), on(k, torch.int32), on(p, torch.float32), on(m, torch.float32), out=out)
     assert got.dtype is torch.int32 and tuple(got.shape) == (rows,)
 
     def of(v, i, none):  # in 32 bits, as the call has it
@@ -158,6 +159,18 @@ def test_large_logits_far_apart(tg):
     x[3, ::2] = -3e38
     _check(tg, x, u, 5e36)
     _check(tg, x, u, 5e36, 40, 0.9)
+
+
+@pytest.mark.parametrize("p", [None, 0.9])
+@pytest.mark.parametrize("t", [1e-45, 1e-38, 1e-8, 0.002, 0.03, 0.06, 0.1, 0.5])
+def test_logits_as_coarse_as_the_temperature(tg, t, p):
+    """Neighbours of the largest logit (steps of 2^-7 in bfloat16 there, 2^-10 in float16, 2^-23 and 2^4 in float32) from all alike to none beside it."""
+    g = torch.Generator().manual_seed(13)
+    for top, dtype in ((1.0, torch.bfloat16), (-1.9, torch.float16), (1.5, torch.float32), (1e8, torch.float32), (-1e8, torch.float32)):
+        steps = torch.randint(0, 5, (3, 3000), generator=g)
+        bits = torch.int32 if dtype is torch.float32 else torch.int16
+        x = (torch.full((3, 3000), top, dtype=dtype).view(bits) + (steps if top < 0 else -steps).to(bits)).view(dtype)  # so many values lower
+        _check(tg, x, torch.tensor([0.1, 0.5, 0.9999]), t * 100 if dtype is torch.float32 and abs(top) == 1e8 else t, None, p, None)
 
 
 @pytest.mark.parametrize("dtype", TYPES)

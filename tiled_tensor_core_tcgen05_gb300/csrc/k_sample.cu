@@ -74,7 +74,7 @@ constexpr Powers make_powers() {
     for (int j = 0; j < kSteps; ++j) {
         const uint64_t hi = (x + (1ull << 38)) >> 39 << 39;  // 24 bits
         p.v[j].x = static_cast<float>(hi >> 39) / static_cast<float>(1 << 23);
-        p.v[j].y = j > 0 ? static_cast<float>(static_cast<int64_t>(x - hi)) / static_cast<float>(1ull << 62) : 0x1p-60f;  // not 0: its exponent is moved
+        p.v[j].y = j > 0 ? static_cast<float>(static_cast<int64_t>(x - hi)) / static_cast<float>(1ull << 62) : 0x1p-45f;  // not 0: its exponent is moved
         x = product_2_62(x, step);
     }
     return p;
@@ -133,6 +133,7 @@ __device__ __forceinline__ u64 units(int high, int low) { return static_cast<u64
 
 __device__ __forceinline__ u64 weight_of(float x, const Scale& c, const float2* powers) {
     if (c.flat) return 1ull << kUnit;
+    if (!(__fmul_rn(__fadd_rn(0.5f * x, -0.5f * c.top), c.hi) > -32.0f)) return 0;  // and where c.none says nothing
     int high = 0, low = 0;
     weigh(x, c, powers, high, low);
     return units(high, low);
@@ -1225,11 +1226,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
         // 2 / T as hi + lo: 1 / T = y + y (1 - y T), good to 2^-46
         const float y = 1.0f / temperature, hi = fminf(2.0f * y, 3e38f), lo = 2.0f * y * fmaf(-y, temperature, 1.0f), x = logit_of(top);
         // what is kept at all: above -inf, and not so small that a weight is nothing (2^-45 and below)
-        const float none = x - 45.0f * 0.6931472f * temperature;
-        w.scale = Scale{x, hi, fabsf(lo) <= 1e-6f * hi ? lo : 0.0f, none > kNone ? none : kNone, isinf(x)};  // lo: 0 where T or 1 / T is infinite
+        const float none = x - 45.0f * 0.6931472f * temperature, far = (0.5f * x - 0.5f * none) * y;
         const u64 finite = static_cast<u64>(key_of(kNone) + 1) << 32;
-        u64 cut = w.scale.flat ? top >> 32 << 32 : none > kNone ? max(finite, static_cast<u64>(key_of(none)) << 32) : finite;
-        w.easy = !w.scale.flat && none > kNone && !(min_p > 0.0f);
+        u64 cut = isinf(x) ? top >> 32 << 32 : none > kNone ? max(finite, static_cast<u64>(key_of(none)) << 32) : finite;
+        // lo: 0 where T or 1 / T is infinite. none: where logits are as coarse as T it may have a weight, or be too far off for weigh()
+        w.scale = Scale{x, hi, fabsf(lo) <= 1e-6f * hi ? lo : 0.0f, none > kNone && far > 15.2f && far < 25.0f ? none : kNone, isinf(x)};
+        w.easy = w.scale.none > kNone && !(min_p > 0.0f);
         if (min_p >= 1.0f) {
             cut = top >> 32 << 32;
         } else if (min_p > 0.0f) {
