@@ -77,7 +77,7 @@ struct SeqWork {
     int begin;             // keys before it are another call's
 };
 
-template <int kTiles>
+template <int kTiles, bool kParts>
 __device__ __forceinline__ SeqWork seq_work(const SplitWork& a, int i) {
     const KvAttnCall& c = a.c;
     SeqWork w;
@@ -89,7 +89,7 @@ __device__ __forceinline__ SeqWork seq_work(const SplitWork& a, int i) {
         report_range(c.wd);
         w.len = 0;
     }
-    w.begin = c.begin != nullptr ? __ldg(c.begin + i) : 0;
+    w.begin = kParts && c.begin != nullptr ? __ldg(c.begin + i) : 0;
     const int64_t begin = c.window > 0 ? static_cast<int64_t>(w.len) - w.count - c.window + 1 : w.begin;
     w.chunk0 = begin > 0 ? static_cast<int>(begin / kChunk) : 0;
     w.chunks = max(1, (w.len + kChunk - 1) / kChunk - w.chunk0);
@@ -137,7 +137,7 @@ __device__ __forceinline__ uint2 load_four(const E* p, bool vec) {
     return u;
 }
 
-template <typename E, int kFmt, int kDim, int kTiles>
+template <typename E, int kFmt, int kDim, int kTiles, bool kParts>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const SplitWork a) {
     constexpr int kRows = 8 * kTiles;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     int64_t mine = 0, before = 0;
     for (int base = 0; base < batch; base += kThreads) {
         const int i = base + threadIdx.x;
-        mine = i < batch ? seq_work<kTiles>(a, i).total : 0;
+        mine = i < batch ? seq_work<kTiles, kParts>(a, i).total : 0;
         total += block_scan(mine, before);
     }
     if (!a.joined) clear_uncovered<E, kDim>(c);
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     for (int base = 0; base < batch; base += kThreads) {
         if (batch > kThreads) {
             const int i = base + threadIdx.x;
-            mine = i < batch ? seq_work<kTiles>(a, i).total : 0;
+            mine = i < batch ? seq_work<kTiles, kParts>(a, i).total : 0;
             const int64_t sum = block_scan(mine, before);
             before += carry;
             carry += sum;
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     __syncthreads();
     int seq = found_seq;
     int64_t off = found_off;
-    SeqWork w = seq_work<kTiles>(a, seq);
+    SeqWork w = seq_work<kTiles, kParts>(a, seq);
 
     int step_no = 0;  // steps issued to this warp's ring so far: stage and phase
     bool first_segment = true;
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (off >= w.total) {  // the next sequence that has rows
             do {
                 if (++seq >= batch) return;
-                w = seq_work<kTiles>(a, seq);
+                w = seq_work<kTiles, kParts>(a, seq);
             } while (w.total == 0);
             off = 0;
         }
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         else i1 = min(i1, (w.len - tok0 + kChunk - 1) / kChunk);
         if (see0 > tok0) i0 = static_cast<int>(min(static_cast<int64_t>(i1), (see0 - tok0) / kChunk));
         const int n_steps = i1 - i0;
-        const int32_t* table = table_row(c.batch, seq);
+        const int32_t* table = table_row<kParts>(c.batch, seq);
 
         // page and scales of 32 steps at a time, a step a lane; those of the next 32 in advance
         auto page_of = [&](int s) {
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 const int t = (row0 + r) / a.share;
                 const int64_t to = static_cast<int64_t>(w.first + t) * c.heads + head * a.share + (row0 + r) - t * a.share;
                 float x[4] = {v.x, v.y, v.z, v.w};
-                finish_row<E, kDim, 4>(c, to, d, x, top, sum, w.begin > 0);
+                finish_row<E, kDim, 4, kParts>(c, to, d, x, top, sum, w.begin > 0);
             } else {
                 *reinterpret_cast<float4*>(part + r * kDim + d) = v;
                 if (d == 0) {
@@ -636,12 +636,12 @@ bool few_rows(const KvAttnCall& c) {
     return static_cast<int64_t>(c.batch.max_new) * (c.heads / c.cache.kv_heads) <= 64;
 }
 
-template <typename E, int kFmt, int kDim, int kTiles>
+template <typename E, int kFmt, int kDim, int kTiles, bool kParts>
 cudaError_t launch_few(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, const FewPlan& p,
                        cudaStream_t stream) {
     static int attr_gen[64] = {};
     constexpr int smem = Ring<kDim>::kBytes + 1024;
-    auto* kernel = attn_few_kernel<E, kFmt, kDim, kTiles>;
+    auto* kernel = attn_few_kernel<E, kFmt, kDim, kTiles, kParts>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -662,15 +662,20 @@ cudaError_t launch_few(const KvAttnCall& c, const CUtensorMap& tmK, const CUtens
     while (c.cache.page >> (a.page_shift + 1)) ++a.page_shift;
     kernel<<<p.grid, kThreads, smem, stream>>>(tmK, tmV, a);
     if ((e = cudaGetLastError()) != cudaSuccess || !p.split) return e;
-    return launch_join<E, kDim, 8 * kTiles>(a, stream);
+    return launch_join<E, kDim, 8 * kTiles, kParts>(a, stream);
 }
 
 template <typename E, int kFmt, int kDim>
 cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count,
                    cudaStream_t stream) {
     const FewPlan p = few_plan(c, sm_count);
-    if (p.tiles == 1) return launch_few<E, kFmt, kDim, 1>(c, tmK, tmV, workspace, p, stream);
-    return launch_few<E, kFmt, kDim, 2>(c, tmK, tmV, workspace, p, stream);
+    // the parts' code costs the other calls registers and a few percent
+    if (c.found != nullptr || c.begin != nullptr) {
+        if (p.tiles == 1) return launch_few<E, kFmt, kDim, 1, true>(c, tmK, tmV, workspace, p, stream);
+        return launch_few<E, kFmt, kDim, 2, true>(c, tmK, tmV, workspace, p, stream);
+    }
+    if (p.tiles == 1) return launch_few<E, kFmt, kDim, 1, false>(c, tmK, tmV, workspace, p, stream);
+    return launch_few<E, kFmt, kDim, 2, false>(c, tmK, tmV, workspace, p, stream);
 }
 
 }  // namespace

@@ -207,7 +207,7 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
         : "memory");
 }
 
-template <typename E, int kFmt, int kDim>
+template <typename E, int kFmt, int kDim, bool kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const SplitWork a) {
     using L = Smem<kDim>;
@@ -284,10 +284,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         return sum;
     };
     int64_t mine = 0, before = 0;
-    for (int base = 0; base < batch; base += kThreads) {
-        const int i = base + threadIdx.x;
-        mine = i < batch ? tile_work(a, i).total : 0;
-        total += block_scan(mine, before);
+    const bool by_warp = kParts && batch <= 32;  // every warp by itself, without a barrier: 2 us sooner
+    if (by_warp) {
+        mine = lane < batch ? tile_work(a, lane).total : 0;
+        int64_t x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        before = x - mine;
+        total = __shfl_sync(0xFFFFFFFFu, x, 31);
+    } else {
+        for (int base = 0; base < batch; base += kThreads) {
+            const int i = base + threadIdx.x;
+            mine = i < batch ? tile_work(a, i).total : 0;
+            total += block_scan(mine, before);
+        }
     }
     if (!a.joined) clear_uncovered<E, kDim>(c);
     const Shares shares(total, a.grid, a.least);
@@ -305,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             before += carry;
             carry += sum;
         }
-        if (before <= start && start < before + mine) {
+        if ((!by_warp || warp == 0) && before <= start && start < before + mine) {
             *found_seq = base + threadIdx.x;
             *found_off = start - before;
         }
@@ -417,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto page_of = [&](const Segment& s, int tile) {
                 const int token = (s.tile0 + tile) * kKeys + lane * kStep;
                 if (lane >= kBlocks || token >= s.len) return -1;
-                return seq_page(c.batch, c.cache, s.seq, token >> a.page_shift, c.wd);
+                return seq_page<kParts>(c.batch, c.cache, s.seq, token >> a.page_shift, c.wd);
             };
             uint32_t piece = 0;  // 64-token pieces so far
             bool have = next_segment(sg);
@@ -593,15 +606,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     up *= __int_as_float((14 - e + 127) << 23);
                     f *= __int_as_float((e - 14 + 127) << 23);
                 }
-                const uint32_t to_row = sbase + L::kQ + h * L::kTile + row * 128;
-                if (std::is_same<E, __half>::value && c.scale >= 0.0f && a.q_vec != 0) {  // no arithmetic: all reads at once
-                    uint4 w[kDim / 16];
+                if (kParts && std::is_same<E, __half>::value && c.scale >= 0.0f && a.q_vec != 0) {
+                    // no arithmetic: the warp's 32 half rows, several lanes a row, all reads at once (a row a lane takes half of each
+                    // sector at a time, and twice as long)
+                    constexpr int kPieces = kDim / 16, kRowsAtOnce = 32 / kPieces;
+                    const int piece = lane % kPieces, row0 = (warp & 3) * 32 + lane / kPieces;
+                    uint4 w[kPieces];
 #pragma unroll
-                    for (int i = 0; i < kDim / 16; ++i) w[i] = real ? __ldg(reinterpret_cast<const uint4*>(x + kh * (kDim / 2)) + i) : make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int rr = sg.block * kRows + h * kHalfRows + row0 + i * kRowsAtOnce, tt = rr / a.share;
+                        w[i] = make_uint4(0, 0, 0, 0);
+                        if (rr < sg.count * a.share)
+                            w[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const E*>(c.q.p) + static_cast<int64_t>(sg.first + tt) * c.q.token +
+                                                                       (sg.head * a.share + rr - tt * a.share) * c.q.head + kh * (kDim / 2)) + piece);
+                    }
 #pragma unroll
-                    for (int i = 0; i < kDim / 16; ++i) {
-                        const int d = kh * (kDim / 2) + i * 8;
-                        sts_v4(to_row + (d >> 6) * L::kBox + ((((d & 63) >> 3) ^ (row & 7)) << 4), w[i]);
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int d = kh * (kDim / 2) + piece * 8, to = row0 + i * kRowsAtOnce;
+                        sts_v4(sbase + L::kQ + h * L::kTile + to * 128 + (d >> 6) * L::kBox + ((((d & 63) >> 3) ^ (to & 7)) << 4), w[i]);
                     }
                 } else
 #pragma unroll 4
@@ -753,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 tmem_ld_32x32b_x32(col_o + i, o);
                 tmem_ld_wait();
-                if (real && whole && c.found != nullptr) {
+                if (kParts && real && whole) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
                         *reinterpret_cast<uint4*>(c.found + out_row * kDim + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
@@ -772,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4*>(part + pr * kDim + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
             }
-            if (real && whole && kh == 0 && c.found != nullptr) c.found_weight[out_row] = make_float2(m, l);
+            if (kParts && real && whole && kh == 0) c.found_weight[out_row] = make_float2(m, l);
             else if (real && whole && kh == 0 && c.lse != nullptr) c.lse[out_row] = row_lse(m, l);
             if (real && !whole && kh == 0) {
                 part[kRows * kDim + pr] = m;
@@ -791,10 +813,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int64_t meta_bytes(int grid) { return (static_cast<int64_t>(grid) * sizeof(Meta) + 255) / 256 * 256; }
 
-template <typename E, int kFmt, int kDim>
+// kParts: the first of two calls, which leaves what it has found (c.found).
+template <typename E, int kFmt, int kDim, bool kParts>
 cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count, cudaStream_t stream) {
     static int attr_gen[64] = {};
-    auto* kernel = attn_tile_kernel<E, kFmt, kDim>;
+    auto* kernel = attn_tile_kernel<E, kFmt, kDim, kParts>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -818,7 +841,7 @@ cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMa
     while (c.cache.page >> (a.page_shift + 1)) ++a.page_shift;
     kernel<<<a.grid, kThreads, Smem<kDim>::kAlloc, stream>>>(tmK, tmV, a);
     if ((e = cudaGetLastError()) != cudaSuccess || !a.joined) return e;
-    return launch_join<E, kDim, kRows>(a, stream);
+    return launch_join<E, kDim, kRows, kParts>(a, stream);
 }
 
 }  // namespace
@@ -831,10 +854,14 @@ cudaError_t launch_kv_attn_tile(const KvAttnCall& c, const CUtensorMap& tmK, con
                                 cudaStream_t stream) {
     const bool h = c.dtype == kFp16, e4 = c.cache.fmt == kKvE4M3, d128 = c.cache.dim == 128;
     auto go = [&](auto* f) { return f(c, tmK, tmV, workspace, sm_count, stream); };
-    if (h && e4) return d128 ? go(launch<__half, kKvE4M3, 128>) : go(launch<__half, kKvE4M3, 64>);
-    if (h) return d128 ? go(launch<__half, kKvInt8, 128>) : go(launch<__half, kKvInt8, 64>);
-    if (e4) return d128 ? go(launch<__nv_bfloat16, kKvE4M3, 128>) : go(launch<__nv_bfloat16, kKvE4M3, 64>);
-    return d128 ? go(launch<__nv_bfloat16, kKvInt8, 128>) : go(launch<__nv_bfloat16, kKvInt8, 64>);
+    auto one = [&](auto parts) {
+        constexpr bool kParts = decltype(parts)::value;
+        if (h && e4) return d128 ? go(launch<__half, kKvE4M3, 128, kParts>) : go(launch<__half, kKvE4M3, 64, kParts>);
+        if (h) return d128 ? go(launch<__half, kKvInt8, 128, kParts>) : go(launch<__half, kKvInt8, 64, kParts>);
+        if (e4) return d128 ? go(launch<__nv_bfloat16, kKvE4M3, 128, kParts>) : go(launch<__nv_bfloat16, kKvE4M3, 64, kParts>);
+        return d128 ? go(launch<__nv_bfloat16, kKvInt8, 128, kParts>) : go(launch<__nv_bfloat16, kKvInt8, 64, kParts>);
+    };
+    return c.found != nullptr ? one(std::true_type{}) : one(std::false_type{});
 }
 
 }  // namespace tg

@@ -295,14 +295,19 @@ __device__ __forceinline__ Uncovered uncovered(const KvBatch& b) {
     return b.cu == nullptr ? Uncovered{0, b.total} : Uncovered{packed_row(b, 0), packed_row(b, b.batch)};
 }
 
-// Sequence i's pages.
+// Sequence i's pages; kRows: from the row of the table that b.rows gives it.
+template <bool kRows>
 __device__ __forceinline__ const int32_t* table_row(const KvBatch& b, int i) {
-    return b.table + static_cast<int64_t>(b.rows != nullptr ? __ldg(b.rows + i) : i) * b.table_width;
+    if constexpr (kRows) {
+        if (b.rows != nullptr) i = __ldg(b.rows + i);
+    }
+    return b.table + static_cast<int64_t>(i) * b.table_width;
 }
 
 // Page `slot` of sequence i, or -1 (reported) where the table holds no page of the cache.
+template <bool kRows = false>
 __device__ __forceinline__ int seq_page(const KvBatch& b, const KvCacheArgs& c, int i, int slot, const Watchdog& wd) {
-    const int p = __ldg(table_row(b, i) + slot);
+    const int p = __ldg(table_row<kRows>(b, i) + slot);
     if (p < 0 || p >= c.pages) {
         report_range(wd);
         return -1;

@@ -151,7 +151,7 @@ __device__ __forceinline__ void clear_row(const KvAttnCall& c, int64_t r) {
 // does it while the parts are being computed; where there is none, the kernel itself.
 template <typename E, int kDim>
 __device__ __forceinline__ void clear_uncovered(const KvAttnCall& c) {
-    if (c.batch.cu == nullptr || c.found != nullptr) return;
+    if (c.batch.cu == nullptr || c.out == nullptr) return;  // the first of two calls leaves no rows
     const Uncovered none = uncovered(c.batch);
     const int many = none.before + c.batch.total - none.after;
     for (int i = blockIdx.x; i < many; i += gridDim.x) clear_row<E, kDim>(c, i < none.before ? i : none.after + i - none.before);
@@ -162,15 +162,16 @@ __device__ __forceinline__ void clear_uncovered(const KvAttnCall& c) {
 
 // kN values from d on of row and head `to`, all of whose parts are joined: their sum v of values times weights, the
 // weights' reference and sum. Adds another call's part if the sequence has one, and writes what the call leaves.
-template <typename E, int kDim, int kN>
+// kParts: whether the call may be one of two.
+template <typename E, int kDim, int kN, bool kParts>
 __device__ __forceinline__ void finish_row(const KvAttnCall& c, int64_t to, int d, float (&v)[kN], float top, float sum, bool seeded) {
-    if (c.found != nullptr) {
+    if (kParts && c.found != nullptr) {
 #pragma unroll
         for (int i = 0; i < kN; i += 2) *reinterpret_cast<float2*>(c.found + to * kDim + d + i) = make_float2(v[i], v[i + 1]);
         if (d == 0) c.found_weight[to] = make_float2(top, sum);
         return;
     }
-    if (seeded) {
+    if (kParts && seeded) {
         const float2 w = c.seed_weight[to];
         const float all = fmaxf(top, w.x), a = ex2_approx(top - all), b = ex2_approx(w.x - all);
         top = all;
@@ -197,7 +198,7 @@ __device__ __forceinline__ void finish_row(const KvAttnCall& c, int64_t to, int 
 // of their keys. What a part counts for is computed once, a part a lane.
 constexpr int kJoinRows = 8;
 
-template <typename E, int kDim, int kRows>
+template <typename E, int kDim, int kRows, bool kParts>
 __global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const SplitWork a) {
     constexpr int kN = kDim / 32;
     const KvAttnCall& c = a.c;
@@ -265,11 +266,11 @@ __global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const SplitWo
     }
     const int t = row / a.share;
     const int64_t to = static_cast<int64_t>(m.first + t) * c.heads + m.head * a.share + row - t * a.share;
-    finish_row<E, kDim, kN>(c, to, lane * kN, v, top, sum, m.seeded != 0);
+    finish_row<E, kDim, kN, kParts>(c, to, lane * kN, v, top, sum, m.seeded != 0);
 }
 
 // Launches the join so that its blocks are in place when the parts are.
-template <typename E, int kDim, int kRows>
+template <typename E, int kDim, int kRows, bool kParts>
 cudaError_t launch_join(const SplitWork& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.grid - 1, kRows / kJoinRows);
@@ -280,7 +281,7 @@ cudaError_t launch_join(const SplitWork& a, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<E, kDim, kRows>, a);
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<E, kDim, kRows, kParts>, a);
 }
 
 }  // namespace tg
