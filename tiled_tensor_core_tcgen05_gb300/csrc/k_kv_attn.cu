@@ -74,7 +74,7 @@ struct SeqWork {
     int chunk0, chunks;    // 64-token chunks that any of its rows sees (at least one, perhaps empty)
     int blocks;            // row blocks per kv head
     int64_t total;         // chunks over its units
-    int begin;             // keys before it are another call's
+    int begin;             // keys before it are left to another call
 };
 
 template <int kTiles, bool kParts>
@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int k = blockIdx.x;
     if (k >= shares.ctas) {
         if (threadIdx.x == 0) a.meta[k].chunks = 0;
+        if constexpr (kParts) wait_for_first();
         return;
     }
     int64_t pos = shares.start(k);
@@ -229,7 +230,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     while (pos < stop) {
         if (off >= w.total) {  // the next sequence that has rows
             do {
-                if (++seq >= batch) return;
+                if (++seq >= batch) {
+                    if constexpr (kParts) wait_for_first();
+                    return;
+                }
                 w = seq_work<kTiles, kParts>(a, seq);
             } while (w.total == 0);
             off = 0;
@@ -535,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
             }
         if (__syncthreads_or(!ok)) break;
+        if constexpr (kParts) wait_for_first();
         float* mine_o = reinterpret_cast<float*>(smem + warp * Ring<kDim>::kWarp);
         static_assert(kRows * kDim * 4 <= Ring<kDim>::kWarp, "a warp's values fit its ring");
 #pragma unroll
@@ -586,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         __syncthreads();
         first_segment = false;
     }
+    if constexpr (kParts) wait_for_first();
 }
 
 // Row tiles of a block. Wider blocks read the cache less often, but their queries and outputs take the
@@ -660,8 +666,7 @@ cudaError_t launch_few(const KvAttnCall& c, const CUtensorMap& tmK, const CUtens
     a.meta = static_cast<Meta*>(workspace);
     a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.meta_bytes);
     while (c.cache.page >> (a.page_shift + 1)) ++a.page_shift;
-    kernel<<<p.grid, kThreads, smem, stream>>>(tmK, tmV, a);
-    if ((e = cudaGetLastError()) != cudaSuccess || !p.split) return e;
+    if ((e = launch_attn(kernel, a, tmK, tmV, p.grid, kThreads, smem, stream)) != cudaSuccess || !p.split) return e;
     return launch_join<E, kDim, 8 * kTiles, kParts>(a, stream);
 }
 
@@ -670,7 +675,7 @@ cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMa
                    cudaStream_t stream) {
     const FewPlan p = few_plan(c, sm_count);
     // the parts' code costs the other calls registers and a few percent
-    if (c.found != nullptr || c.begin != nullptr) {
+    if (c.found != nullptr || c.seed != nullptr) {
         if (p.tiles == 1) return launch_few<E, kFmt, kDim, 1, true>(c, tmK, tmV, workspace, p, stream);
         return launch_few<E, kFmt, kDim, 2, true>(c, tmK, tmV, workspace, p, stream);
     }

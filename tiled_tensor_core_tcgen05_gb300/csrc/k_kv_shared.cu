@@ -1,13 +1,15 @@
 // Attention of sequences that begin with the same tokens. The shared keys are
 // attended by all rows of a group at once, as one sequence's that every row sees
-// whole (the tokens come before all new ones), and read once for the group; each
-// sequence's own keys follow in a second pass, which adds what the first has found:
+// whole (the tokens come before all new ones), and read once for the group. Each
+// sequence's own keys come before, in a first pass, whose findings this one adds:
 //
 //     o = (v1 2^(m1 - m) + v2 2^(m2 - m)) / (l1 2^(m1 - m) + l2 2^(m2 - m)),  m = max(m1, m2),
 //
 // v the values times their weights, m the weights' reference and l their sum, in
 // fp32 between the passes. Both passes are the cache attention's own kernels; the
-// first one takes many rows on tcgen05 (k_kv_tile.cu) where a group has many. This
+// second one takes many rows on tcgen05 (k_kv_tile.cu) where a group has many, and it is the second because
+// it takes long to begin (shares, queries, an empty pipeline: 11 us) and needs the other's findings only at its end: it is
+// launched early, and CTAs of it begin as SMs have done with the first. This
 // file holds what comes before: which sequences take part, and each group's rows.
 //
 // Where the rows of one sequence are many by themselves (more than few_rows allows)
@@ -118,8 +120,8 @@ __global__ void __launch_bounds__(kThreads) group_kernel(const KvSharedCall s, c
     w.rows[g] = lowest < INT_MAX ? lowest : 0;
 }
 
-// The first pass: groups as sequences.
-KvAttnCall first_call(const KvSharedCall& s, const SharedWork& w) {
+// The second pass: groups as sequences.
+KvAttnCall group_call(const KvSharedCall& s, const SharedWork& w) {
     KvAttnCall c = s.c;
     c.batch.lens = w.lens;
     c.batch.cu = w.cu;
@@ -127,10 +129,8 @@ KvAttnCall first_call(const KvSharedCall& s, const SharedWork& w) {
     c.batch.batch = s.group_count;
     c.batch.max_new = s.max_rows;
     c.causal = 0;
-    c.out = nullptr;
-    c.lse = nullptr;
-    c.found = w.found;
-    c.found_weight = w.found_weight;
+    c.seed = w.found;
+    c.seed_weight = w.found_weight;
     return c;
 }
 
@@ -149,16 +149,16 @@ SharedWork layout(const KvSharedCall& s, int sm_count, void* at) {
     w.begin = static_cast<int32_t*>(take(s.c.batch.batch * 4ll));
     w.found = static_cast<float*>(take(rows * s.c.cache.dim * 4));
     w.found_weight = static_cast<float2*>(take(rows * 8));
-    w.first = take(kv_attn_workspace(first_call(s, w), sm_count));
-    w.second = take(kv_attn_workspace(s.c, sm_count));
+    w.first = take(kv_attn_workspace(s.c, sm_count));
+    w.second = take(kv_attn_workspace(group_call(s, w), sm_count));
     return w;
 }
 
 // Whether groups are worth their pass. What sharing can save at most is the reading of all sequences but one a group, as long as they may
-// be; the further pass, the kernel before it and the join take 20 to 50 us. Measured on a GB300, in us with groups and without,
-// 32 heads over 8 of 128: 8 sequences of 4000 (58 MB to save) 32 and 18, of 16000 (230 MB) 39 and 42; 64 of 1000 (133 MB) 47 and 29, of 4000 (520 MB)
-// 62 and 76, of 16000 76 and 258; four groups of 16 of 1000 (117 MB) 39 and 28, of 4000 (418 MB) 49 and 66. The bounds that the caller gives
-// are all that is known here: loose ones are taken for long sequences.
+// be; the further pass, the kernel before both and the join take 20 to 45 us. Measured on a GB300, in us with groups and without,
+// 32 heads over 8 of 128: 8 sequences of 4000 (58 MB to save) 32 and 18, of 16000 (230 MB) 39 and 41; 32 of 4000 (256 MB) 50 and 43; 64 of 1000
+// (133 MB) 47 and 29, of 4000 (520 MB) 57 and 75, of 16000 71 and 255; four groups of 16 of 1000 (117 MB) 39 and 27, of 4000 (418 MB) 50
+// and 65. The bounds that the caller gives are all that is known here: loose ones are taken for long sequences.
 bool pays(const KvSharedCall& s) {
     const KvAttnCall& c = s.c;
     const int64_t each = std::min(c.max_len, c.batch.table_width * c.cache.page) * c.cache.kv_heads * c.cache.dim * 2;
@@ -180,12 +180,12 @@ cudaError_t launch_kv_attn_shared(const KvSharedCall& s, const CUtensorMap& tmK,
     group_kernel<<<s.group_count + (s.c.batch.batch + kThreads - 1) / kThreads, kThreads, 0, stream>>>(s, w);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if ((e = launch_kv_attn(first_call(s, w), tmK, tmV, w.first, sm_count, stream)) != cudaSuccess) return e;
     KvAttnCall c = s.c;
     c.begin = w.begin;
-    c.seed = w.found;
-    c.seed_weight = w.found_weight;
-    return launch_kv_attn(c, tmK, tmV, w.second, sm_count, stream);
+    c.found = w.found;
+    c.found_weight = w.found_weight;
+    if ((e = launch_kv_attn(c, tmK, tmV, w.first, sm_count, stream)) != cudaSuccess) return e;
+    return launch_kv_attn(group_call(s, w), tmK, tmV, w.second, sm_count, stream);
 }
 
 }  // namespace tg

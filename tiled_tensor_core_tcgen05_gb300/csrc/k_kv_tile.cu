@@ -307,7 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int k = blockIdx.x;
     // the joining kernel runs whatever becomes of this one: until the first segment is known there is nothing to join
     if (threadIdx.x == 0) a.meta[k].chunks = 0;
-    if (k >= shares.ctas) return;
+    if (k >= shares.ctas) {
+        if constexpr (kParts) wait_for_first();
+        return;
+    }
     const int64_t start = shares.start(k), stop = shares.start(k + 1);
     int64_t carry = 0;
     for (int base = 0; base < batch; base += kThreads) {
@@ -764,10 +767,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             l += red[(tile_no & 1u) * 4 * kHalfRows + (kh ^ 1) * kHalfRows];
             tc_fence_after_sync();
             const bool whole = sg.t0 == 0 && sg.t1 == sg.tiles;
-            const float inv = row_inverse(l);
             const int64_t out_row = static_cast<int64_t>(sg.first + t) * c.heads + sg.head * a.share + r - t * a.share;
             float* part = a.parts + (static_cast<int64_t>(2 * k) + (first_segment ? 0 : 1)) * kRows * (kDim + 2);
             const int pr = h * kHalfRows + row;
+            // the first call's share of the row: what it counts for, and this one's
+            float keep = 1.0f, more = 0.0f;
+            bool write = real;
+            if (kParts && whole) {
+                wait_for_first();
+                if (real) {
+                    const float2 w = c.seed_weight[out_row];
+                    const float top = fmaxf(m, w.x);
+                    write = !(w.y < 0.0f);
+                    keep = ex2_approx(m - top);
+                    more = ex2_approx(w.x - top);
+                    l = fmaf(l, keep, w.y * more);
+                    m = top;
+                }
+            }
+            const float inv = row_inverse(l);
 #pragma unroll 1
             for (int i = 0; i < kDim / 2; i += 32) {
                 const int d = kh * (kDim / 2) + i;
@@ -775,27 +793,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 tmem_ld_32x32b_x32(col_o + i, o);
                 tmem_ld_wait();
-                if (kParts && real && whole) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4*>(c.found + out_row * kDim + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                } else if (real && whole) {
+                if (write && whole) {
                     E* y = static_cast<E*>(c.out) + out_row * kDim + d;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         float v[8];
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) v[x] = __uint_as_float(o[e + x]) * inv;
+                        for (int x = 0; x < 8; ++x) {
+                            v[x] = __uint_as_float(o[e + x]);
+                            if constexpr (kParts) v[x] = fmaf(v[x], keep, c.seed[out_row * kDim + d + e + x] * more);
+                            v[x] *= inv;
+                        }
                         store_values<E, 8>(y, e, true, v);
                     }
-                } else if (real) {
+                } else if (real && !whole) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
                         *reinterpret_cast<uint4*>(part + pr * kDim + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
             }
-            if (kParts && real && whole && kh == 0) c.found_weight[out_row] = make_float2(m, l);
-            else if (real && whole && kh == 0 && c.lse != nullptr) c.lse[out_row] = row_lse(m, l);
+            if (write && whole && kh == 0 && c.lse != nullptr) c.lse[out_row] = row_lse(m, l);
             if (real && !whole && kh == 0) {
                 part[kRows * kDim + pr] = m;
                 part[kRows * (kDim + 1) + pr] = l;
@@ -803,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             first_segment = false;
         }
     }
+    if constexpr (kParts) wait_for_first();
     tc_fence_before_sync();
     __syncthreads();
     if (warp == 20) {
@@ -813,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int64_t meta_bytes(int grid) { return (static_cast<int64_t>(grid) * sizeof(Meta) + 255) / 256 * 256; }
 
-// kParts: the first of two calls, which leaves what it has found (c.found).
+// kParts: the second of two calls.
 template <typename E, int kFmt, int kDim, bool kParts>
 cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count, cudaStream_t stream) {
     static int attr_gen[64] = {};
@@ -839,8 +857,7 @@ cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMa
     a.meta = static_cast<Meta*>(workspace);
     a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + meta_bytes(a.grid));
     while (c.cache.page >> (a.page_shift + 1)) ++a.page_shift;
-    kernel<<<a.grid, kThreads, Smem<kDim>::kAlloc, stream>>>(tmK, tmV, a);
-    if ((e = cudaGetLastError()) != cudaSuccess || !a.joined) return e;
+    if ((e = launch_attn(kernel, a, tmK, tmV, a.grid, kThreads, Smem<kDim>::kAlloc, stream)) != cudaSuccess || !a.joined) return e;
     return launch_join<E, kDim, kRows, kParts>(a, stream);
 }
 
@@ -861,7 +878,7 @@ cudaError_t launch_kv_attn_tile(const KvAttnCall& c, const CUtensorMap& tmK, con
         if (e4) return d128 ? go(launch<__nv_bfloat16, kKvE4M3, 128, kParts>) : go(launch<__nv_bfloat16, kKvE4M3, 64, kParts>);
         return d128 ? go(launch<__nv_bfloat16, kKvInt8, 128, kParts>) : go(launch<__nv_bfloat16, kKvInt8, 64, kParts>);
     };
-    return c.found != nullptr ? one(std::true_type{}) : one(std::false_type{});
+    return c.seed != nullptr ? one(std::true_type{}) : one(std::false_type{});
 }
 
 }  // namespace tg

@@ -83,14 +83,15 @@ struct KvAttnCall {
     int64_t window;      // 0: none
     float scale;
     Watchdog wd;
-    // Rows in parts. Keys before begin[i] (a multiple of 64; null: 0) of sequence i are left out, and what another call
-    // found there is added: `seed`. A call with `found` leaves that instead of out and lse: for each row and head
-    // the values times their weights, and the weights' reference (base 2) and sum.
+    // Rows in two parts. The first call leaves out keys before begin[i] (a multiple of 64; 0: none) of sequence i, and
+    // where there are some leaves in `found`, for each row and head, the values times their weights, and the weights'
+    // reference (base 2) and sum, instead of out and lse; of other rows it says that they are done (a sum of -1).
+    // The second call adds what it finds there to its own, `seed`, and finishes the rows that are not done.
     const int32_t* begin;
-    const float* seed;          // (total, heads, dim)
-    const float2* seed_weight;  // (total, heads)
-    float* found;
-    float2* found_weight;
+    float* found;               // (total, heads, dim)
+    float2* found_weight;       // (total, heads)
+    const float* seed;
+    const float2* seed_weight;
 };
 
 // Attention of sequences that begin with the same tokens: groups of sequences, and how many tokens each group shares.

@@ -71,7 +71,7 @@ struct Meta {
     int64_t unit_start, total;
     int chunks, head, block;
     int first, count;   // the sequence's rows of the packed tensors
-    int seeded;         // whether another call's part is to be added
+    int part;           // whether keys of the sequence are left to another call
 };
 
 // A split call: what both kernels and the join need.
@@ -139,19 +139,26 @@ __device__ __forceinline__ float row_lse(float m, float l) {
     return (m + static_cast<float>(e) + log2f(__int_as_float((bits & 0x7FFFFF) | 0x3F800000))) * (1.0f / kLog2e);
 }
 
+// What the first of two calls says of a row that it has finished.
+constexpr float2 kDone{0.0f, -1.0f};
+
+// In the second of two calls: waits for the first, whose last kernel lets this one begin early.
+__device__ __forceinline__ void wait_for_first() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Row r of the outputs as that of a token that sees nothing: whole block.
 template <typename E, int kDim>
 __device__ __forceinline__ void clear_row(const KvAttnCall& c, int64_t r) {
     uint4* y = reinterpret_cast<uint4*>(static_cast<E*>(c.out) + r * c.heads * kDim);
     for (int x = threadIdx.x; x < c.heads * (kDim / 8); x += blockDim.x) y[x] = make_uint4(0, 0, 0, 0);
     for (int h = threadIdx.x; c.lse != nullptr && h < c.heads; h += blockDim.x) c.lse[r * c.heads + h] = -INFINITY;
+    for (int h = threadIdx.x; c.found != nullptr && h < c.heads; h += blockDim.x) c.found_weight[r * c.heads + h] = kDone;
 }
 
 // Clears the rows that no sequence has, and those of spans out of range, the grid's CTAs together. The joining kernel
 // does it while the parts are being computed; where there is none, the kernel itself.
 template <typename E, int kDim>
 __device__ __forceinline__ void clear_uncovered(const KvAttnCall& c) {
-    if (c.batch.cu == nullptr || c.out == nullptr) return;  // the first of two calls leaves no rows
+    if (c.batch.cu == nullptr || c.seed != nullptr) return;  // the first of two calls has done it
     const Uncovered none = uncovered(c.batch);
     const int many = none.before + c.batch.total - none.after;
     for (int i = blockIdx.x; i < many; i += gridDim.x) clear_row<E, kDim>(c, i < none.before ? i : none.after + i - none.before);
@@ -160,19 +167,22 @@ __device__ __forceinline__ void clear_uncovered(const KvAttnCall& c) {
             for (int r = packed_row(c.batch, i); r < packed_row(c.batch, i + 1); ++r) clear_row<E, kDim>(c, r);
 }
 
-// kN values from d on of row and head `to`, all of whose parts are joined: their sum v of values times weights, the
-// weights' reference and sum. Adds another call's part if the sequence has one, and writes what the call leaves.
-// kParts: whether the call may be one of two.
+// kN values from d on of row and head `to`, all of whose units are joined: their sum v of values times weights, the
+// weights' reference and sum. Writes what the call leaves. kParts: it is one of two; `part`: keys of the sequence are left to the
+// second.
 template <typename E, int kDim, int kN, bool kParts>
-__device__ __forceinline__ void finish_row(const KvAttnCall& c, int64_t to, int d, float (&v)[kN], float top, float sum, bool seeded) {
+__device__ __forceinline__ void finish_row(const KvAttnCall& c, int64_t to, int d, float (&v)[kN], float top, float sum, bool part) {
     if (kParts && c.found != nullptr) {
+        if (d == 0) c.found_weight[to] = part ? make_float2(top, sum) : kDone;
+        if (part) {
 #pragma unroll
-        for (int i = 0; i < kN; i += 2) *reinterpret_cast<float2*>(c.found + to * kDim + d + i) = make_float2(v[i], v[i + 1]);
-        if (d == 0) c.found_weight[to] = make_float2(top, sum);
-        return;
+            for (int i = 0; i < kN; i += 2) *reinterpret_cast<float2*>(c.found + to * kDim + d + i) = make_float2(v[i], v[i + 1]);
+            return;
+        }
     }
-    if (kParts && seeded) {
+    if (kParts && c.seed != nullptr) {
         const float2 w = c.seed_weight[to];
+        if (w.y < 0.0f) return;
         const float all = fmaxf(top, w.x), a = ex2_approx(top - all), b = ex2_approx(w.x - all);
         top = all;
         sum = fmaf(sum, a, w.y * b);
@@ -202,6 +212,7 @@ template <typename E, int kDim, int kRows, bool kParts>
 __global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const SplitWork a) {
     constexpr int kN = kDim / 32;
     const KvAttnCall& c = a.c;
+    if constexpr (kParts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.y == 0) clear_uncovered<E, kDim>(c);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int k = blockIdx.x + 1, lane = threadIdx.x % 32, r = blockIdx.y * kJoinRows + threadIdx.x / 32;
@@ -266,7 +277,23 @@ __global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const SplitWo
     }
     const int t = row / a.share;
     const int64_t to = static_cast<int64_t>(m.first + t) * c.heads + m.head * a.share + row - t * a.share;
-    finish_row<E, kDim, kN, kParts>(c, to, lane * kN, v, top, sum, m.seeded != 0);
+    finish_row<E, kDim, kN, kParts>(c, to, lane * kN, v, top, sum, m.part != 0);
+}
+
+// Launches a call's first kernel; that of the second of two calls so that it begins while the first one's last does.
+template <typename K>
+cudaError_t launch_attn(K* kernel, const SplitWork& a, const CUtensorMap& tmK, const CUtensorMap& tmV, int grid, int threads, int smem, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = a.c.seed != nullptr ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, tmK, tmV, a);
 }
 
 // Launches the join so that its blocks are in place when the parts are.
