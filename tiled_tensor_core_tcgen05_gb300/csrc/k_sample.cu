@@ -45,7 +45,7 @@ constexpr int kUnit = 42;                    // weights are multiples of 2^-42
 constexpr int kSteps = 256;                  // of the table of powers: 2^(j / 256)
 constexpr int kBinSteps = 8;                 // of a bin
 constexpr int kBins = (kUnit + 3) * kSteps / kBinSteps;
-constexpr int kList = 2048;                  // tokens that are sorted at a time
+constexpr int kList = 2047;                  // tokens in a list, at most: that many weights' upper halves add up in 32 bits
 constexpr int kSub = 1024;                   // parts of a bin that holds more
 constexpr int kSome = kThreads;              // tokens of a bin that are ranked by comparing each with each
 constexpr int kGuess = 1280;                 // threads' largest above a threshold that the list can be expected to hold
@@ -166,11 +166,13 @@ struct Row {
     uint4* held;          // shared memory
     int vocab, shift;     // index of piece q's first logit: q * kV - shift
     int group0, groups;   // of this CTA
+    int each_cta;         // of a CTA
     __device__ Row(const E* row, uint4* smem, int n, uint32_t rank, uint32_t ctas) : x(row), held(smem), vocab(n) {
         shift = static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(E));
-        const int all = ((n + shift + kV - 1) / kV + 31) / 32, each = (all + ctas - 1) / ctas;
-        group0 = min(all, static_cast<int>(rank) * each);
-        groups = min(all, group0 + each) - group0;
+        const int all = ((n + shift + kV - 1) / kV + 31) / 32;
+        each_cta = (all + ctas - 1) / ctas;
+        group0 = min(all, static_cast<int>(rank) * each_cta);
+        groups = min(all, group0 + each_cta) - group0;
     }
     __device__ int index(int group) const { return ((group0 + group) * 32 + (threadIdx.x & 31)) * kV - shift; }
     __device__ uint4 read(int group) const {
@@ -232,14 +234,16 @@ struct Row {
 
 struct Shared {
     float2 powers[kSteps];
-    u64 list[kList];           // of the first CTA; parts' masses
+    u64 list[kList + 1];           // of the first CTA; parts' masses
     u64 groups[kMostGroups];   // weights
     int2 places[kMostGroups];  // how many go to the list, and where
     union {
         struct {
             uint32_t bins[kBins], all[kBins];
         };
-        u64 masses[kBins];     // of a list's bins
+        struct {
+            uint32_t low[kSub], high[kSub];  // weights of a list's parts
+        };
     };
     u64 some[kSome], some_weight[kSome];
     u64 box[2][2][kMaxCtas];   // what the CTAs tell each other
@@ -320,6 +324,12 @@ struct Sampler {
     // A logit that no one of bin b or before is below.
     __device__ __forceinline__ float lowest_of(int b) const {
         return scale.flat ? scale.top : scale.top - (2.0f * (b + 2) * kBinSteps * kLnHi / scale.hi) * 1.0001f - 1e-5f * fabsf(scale.top);
+    }
+
+    // A logit above which there is none of bin b.
+    __device__ __forceinline__ float highest_of(int b) const {
+        const float half = (b - 1) * kBinSteps * kLnHi / scale.hi * 0.9999f;  // by halves: the whole way may pass what a float holds
+        return scale.flat ? scale.top : scale.top - half - half + 1e-5f * fabsf(scale.top);
     }
 
     // Two numbers of this CTA's to every CTA; afterwards all of them are in the box that comes back. Threads of the CTA
@@ -597,7 +607,7 @@ struct Sampler {
     // all n.
     template <typename G, typename F>
     __device__ __forceinline__ u64 weigh_list(int n, G logit, F f) {
-        constexpr int kEach = kList / kThreads;
+        constexpr int kEach = (kList + 1) / kThreads;
         const int each = (n + kThreads - 1) / kThreads, i0 = threadIdx.x * each;
         u64 w[kEach], mine = 0, total;
 #pragma unroll
@@ -729,7 +739,16 @@ struct Sampler {
             __syncthreads();
         }
         gather(from, [&](float x, int i) { return bin_of(x, scale) == b && place_of(x, i) >= low && place_of(x, i) <= high; });
-        const u64 found = rank == 0 ? cut_of<kMass>(static_cast<int>(n), target) : 0;
+        u64 found = 0;
+        if (rank == 0) {
+            u64 p[kOwn], w[kOwn];
+            read_list(static_cast<int>(n), p, w);
+            if (!kMass) {
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i) w[i] = p[i] != 0;
+            }
+            found = cut_of<kMass>(static_cast<int>(n), p, w, target);
+        }
         return tell(found, 0)[0][0];
     }
 
@@ -772,7 +791,7 @@ struct Sampler {
             least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
             most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
         }
-        for (int b = threadIdx.x; b < kSub; b += kThreads) s.masses[b] = 0;
+        for (int b = threadIdx.x; b < kSub; b += kThreads) s.low[b] = s.high[b] = 0;
         __syncthreads();
         if ((threadIdx.x & 31) == 0) {
             s.sums[threadIdx.x >> 5] = least;
@@ -791,13 +810,17 @@ struct Sampler {
         for (int i = 0; i < kEach; ++i)
             if (w[i] != 0) {
                 const int part = static_cast<int>((most - p[i]) >> shift);
-                if (kMass) atomicAdd(&s.masses[part], w[i]);
-                else atomicAdd(reinterpret_cast<uint32_t*>(&s.masses[part]), 1u);
+                if (kMass) {  // in two parts, whose sums fit 32 bits: additions in 64 bits are loops, which equal logits meet in
+                    atomicAdd(&s.low[part], static_cast<uint32_t>(w[i]) & 0x1FFFFFu);
+                    atomicAdd(&s.high[part], static_cast<uint32_t>(w[i] >> 21));
+                } else {
+                    atomicAdd(&s.low[part], 1u);
+                }
             }
         __syncthreads();
         int part;
         u64 before;
-        reach<u64>([&](int b) { return b < kSub ? s.masses[b] : 0; }, target, s.sums, part, before);
+        reach<u64>([&](int b) { return b < kSub ? (static_cast<u64>(s.high[b]) << 21) + s.low[b] : 0; }, target, s.sums, part, before);
         if (part == kBins) return 1;
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
@@ -824,7 +847,7 @@ struct Sampler {
         return found;
     }
     // The first CTA's list of n: a thread's places and weights, one thread's after another's.
-    static constexpr int kOwn = kList / kThreads;
+    static constexpr int kOwn = (kList + 1) / kThreads;
     __device__ __forceinline__ void read_list(int n, u64 (&p)[kOwn], u64 (&w)[kOwn]) {
         const int each = (n + kThreads - 1) / kThreads, i0 = threadIdx.x * each;
 #pragma unroll
@@ -834,15 +857,9 @@ struct Sampler {
             w[i] = some ? weight_of(logit_of(p[i]), scale, s.powers) : 0;
         }
     }
-    // The cut of the first CTA's list of n, as cut_list says; the list is sorted afterwards where it has to be.
+    // The cut of the first CTA's list of n, read as p and w, as cut_list says; the list is sorted where it has to be.
     template <bool kMass>
-    __device__ u64 cut_of(int n, u64 target) {
-        u64 p[kOwn], w[kOwn];
-        read_list(n, p, w);
-        if (!kMass) {
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i) w[i] = p[i] != 0;
-        }
+    __device__ u64 cut_of(int n, const u64 (&p)[kOwn], const u64 (&w)[kOwn], u64 target) {
         u64 found = cut_list<kMass>(p, w, target);
         if (found == 0) {
             sort(n);
@@ -1137,7 +1154,9 @@ struct Sampler {
                 sum = sum_cluster(sum);
                 found = target <= above ? 0 : target > above + sum ? 2 : inside<true>(first, n, target - above);
             } else {
-                n = gather(lowest_of(last), [&](float x, int) {
+                const float low = lowest_of(last), high = highest_of(first);
+                n = gather(low, [&](float x, int) {
+                    if (x < low || x > high) return false;  // nearly all
                     const int b = bin_of(x, scale);
                     return b >= first && b <= last;
                 });
@@ -1146,13 +1165,25 @@ struct Sampler {
                     read_list(n, p, w);
 #pragma unroll
                     for (int i = 0; i < kOwn; ++i) sum += w[i];
-                    found = above + sum_block(sum) < target ? 2 : first == 0 ? 3 : cut_of<true>(n, target - above);
+                    found = above + sum_block(sum) < target ? 2 : first == 0 ? 3 : cut_of<true>(n, p, w, target - above);
                     if (found == 3) draw_from(n, INT_MAX, 0.5f, target, u, token);  // all that is kept is in the list
+                    if (found > 3) {  // the window's kept tokens come to their groups
+#pragma unroll
+                        for (int i = 0; i < kOwn; ++i)
+                            if (w[i] != 0 && p[i] >= found) {
+                                const int g = (index_of(p[i]) + row.shift) / kV / 32, owner = g / row.each_cta;
+                                asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(&s.groups[g - owner * row.each_cta]), owner)), "l"(w[i]) : "memory");
+                            }
+                    }
                 }
                 found = tell(found, 0)[0][0];
                 if (found == 3) return true;
+                if (found > 3) {
+                    keep_from(found);
+                    return false;
+                }
             }
-            if (found > 2) {  // the window's kept tokens come to their groups
+            if (found > 2) {  // the bin's kept tokens come to their groups
                 if (first == 0) {
                     for (int g = threadIdx.x / 32 + (threadIdx.x & 31) * kWarps; g < row.groups; g += kThreads) s.groups[g] = 0;
                     __syncwarp();
@@ -1184,11 +1215,18 @@ struct Sampler {
         return false;
     }
 
-    // The weight of what is kept.
-    __device__ u64 mass() {
+    // The weight of what is kept, and of the threads' largest of it.
+    __device__ u64 mass(u64& largest) {
         u64 sum = 0;
         row.each(cut_x, [&](int, int i, const float (&v)[kV]) { sum += weigh_piece<false>(i, v); });
-        return sum_cluster(sum);
+        sum = sum_block(sum);
+        u64 (*box)[kMaxCtas] = tell(sum, sum_block(best >= cut_x ? weight_of(best, scale, s.powers) : 0));
+        sum = largest = 0;
+        for (uint32_t r = 0; r < ctas; ++r) {
+            sum += box[0][r];
+            largest += box[1][r];
+        }
+        return sum;
     }
 };
 
@@ -1262,8 +1300,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
         }
     }
     if (by_mass) {
-        const u64 total = w.mass(), target = target_of(total, top_p);
-        if (!by_count && w.draw_few(0, top_p, target, u, c.tokens + r)) return;
+        u64 largest;
+        const u64 total = w.mass(largest), target = target_of(total, top_p);
+        if (!by_count && (largest >= target || c.vocab <= kList) && w.draw_few(0, top_p, target, u, c.tokens + r)) return;
         if (w.nucleus(total, target, u, c.tokens + r)) return;
     } else {
         w.weigh_groups();
