@@ -173,6 +173,16 @@ def test_logits_as_coarse_as_the_temperature(tg, t, p):
         _check(tg, x, torch.tensor([0.1, 0.5, 0.9999]), t * 100 if dtype is torch.float32 and abs(top) == 1e8 else t, None, p, None)
 
 
+@pytest.mark.parametrize("t", [5e36, 1.5e37, 4e37, 3e38])
+@pytest.mark.parametrize("p", [None, 0.2, 0.97])
+def test_logits_over_the_whole_range_of_the_type(tg, t, p):
+    """Differences that pass the largest float, at temperatures at which they still count."""
+    g = torch.Generator().manual_seed(17)
+    x = (torch.rand(4, 60007, generator=g, dtype=torch.float64) * 6.8e38 - 3.4e38).float()
+    _check(tg, x, torch.tensor([0.0, 0.4, 0.9, 0.9999]), t, None, p, None)
+    _check(tg, x, torch.tensor([0.0, 0.4, 0.9, 0.9999]), t, 4000, p, None)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("offset", [0, 1, 2, 3, 5, 7])
 def test_strides_and_alignment(tg, dtype, offset):

@@ -2,14 +2,18 @@
 // same one (forked), given and freed, and moved together (compacted).
 //
 // The bookkeeping (which entries a page is held by, which pages are free, the
-// tables) is a few hundred kilobytes of integers in several steps that each
-// need the whole of the one before. One cluster of kCtas CTAs does all of them,
-// with the cluster's barrier between the steps: no launch and no host in
-// between, and no CTA waits for one that might not run. Then a grid that fills
-// the GPU copies the pages that the cluster listed; it is launched early and
+// tables) is up to a few hundred kilobytes of integers in several steps that each
+// need the whole of the one before. One CTA, or a cluster of kMostCtas where there is
+// much (kLittleFork), does all of them, with its barrier between the steps: no launch and
+// no host in between, and no CTA waits for one that might not run. Then a grid that
+// fills the GPU copies the pages that were listed; it is launched early and
 // waits for the list. Free pages are taken in rising order and given in the
 // order of sequences and places, by prefix sums, so results do not depend on
 // timing.
+//
+// Measured on a GB300, kernels alone: four beams of one prompt forked 10.9 us and 256 of 32 prompts of up to 8192 tokens 25.4
+// (steps that wait for one another: table rows, counts, prefix sums; the bytes take 3); compacting a pool of 301 pages 7.4, one of
+// 16384 pages of 128 KB that is 55 % full 177 (157 at the rate of a plain copy); copying 5003 such pages 200 (193).
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -410,8 +414,9 @@ cudaError_t launch_listed(const KvCacheArgs& cache, const PageWork& w, int64_t m
 }
 
 // Pages and entries up to which one CTA keeps the books: its barrier takes a fraction of the cluster's, and what the steps of a fork leave
-// for one another stays in its shared memory.
-constexpr int64_t kLittle = 16384;
+// for one another stays in its shared memory. Measured on a GB300, in us with one CTA and with eight: forks with 200 pages and entries 11.0 and 15.6,
+// 10400 15.3 and 18.0, 40000 26.9 and 22.7, 125000 51.9 and 22.0; compacting 500 7.4 and 11.7, 6200 12.3 and 14.0, 12400 23.1 and 15.9, 25000 48.7 and 18.2.
+constexpr int64_t kLittleFork = 16384, kLittleCompact = 8192;
 constexpr int kMostSmem = 128 * 1024;
 
 template <typename C>
@@ -467,7 +472,7 @@ cudaError_t launch_kv_copy(const PageCopyCall& c, int sm_count, cudaStream_t str
 cudaError_t launch_kv_fork(const KvForkCall& c, int sm_count, cudaStream_t stream) {
     const int64_t smem = fork_smem(c);
     cudaError_t e;
-    if (c.cache.pages + (c.batch + c.count) * c.width <= kLittle && smem <= kMostSmem) {
+    if (c.cache.pages + (c.batch + c.count) * c.width <= kLittleFork && smem <= kMostSmem) {
         static int attr_gen[64] = {};
         int dev = 0;
         if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -483,7 +488,7 @@ cudaError_t launch_kv_fork(const KvForkCall& c, int sm_count, cudaStream_t strea
 }
 
 cudaError_t launch_kv_compact(const KvCompactCall& c, int sm_count, cudaStream_t stream) {
-    const cudaError_t e = c.cache.pages + c.batch * c.width <= kLittle ? launch_books(compact_kernel<1>, c, 1, 0, stream) : launch_books(compact_kernel<kMostCtas>, c, kMostCtas, 0, stream);
+    const cudaError_t e = c.cache.pages + c.batch * c.width <= kLittleCompact ? launch_books(compact_kernel<1>, c, 1, 0, stream) : launch_books(compact_kernel<kMostCtas>, c, kMostCtas, 0, stream);
     return e != cudaSuccess || c.cache.pages < 2 ? e : launch_listed(c.cache, c.w, c.cache.pages / 2, sm_count, stream);
 }
 

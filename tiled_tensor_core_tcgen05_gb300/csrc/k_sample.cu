@@ -24,10 +24,14 @@
 //   4  the tokens above it, brought together in order where they are at most kList: the first
 //      CTA cuts and draws. Few rows go on:
 //   5  a count in each of kBins bins of t, 1/32 wide: the bin with the k-th, and a guess at the bin in which
-//      the weight reaches top_p; the exact weight above, and in each bin near the guess;
-//   6  the tokens of the border's bin, brought together and sorted: the cut;
-//   7  the weight of what is kept, group by group of 32 lanes' pieces; the group,
-//      lane and token in which u of it is passed.
+//      the weight reaches top_p; the exact weight above a window of bins around the guess, group by group of
+//      32 lanes' pieces;
+//   6  the tokens of the border's bins, brought together: the cut, and their kept weight to their groups;
+//   7  the group, lane and token in which u of the kept weight is passed.
+//
+// What bounds it is the chain of these steps, between which the CTAs meet, and the 30 operations that a weight takes,
+// not the bytes. Measured on a GB300, in a graph: one row of 32000 fp16 logits, top_p 0.9: 13.5 us; 64 rows of 131071 bf16: greedy 9.6,
+// no cut 33, top_k 50 35, top_p 0.9 100, settings mixed 52; 256 rows of 131072 fp32, top_p 0.9: 243 (the bytes take 20).
 #include "tg_device.cuh"
 #include "tg_kv.cuh"
 
@@ -362,7 +366,7 @@ struct Sampler {
         return t;
     }
 
-    // The place of the largest logit; 0: there is none above -inf. `ready`: run once every CTA of the cluster runs.
+    // The place of the largest logit; 0: there is none above -inf.
     __device__ u64 largest() {
         int at = INT_MAX;
         row.load([&](int i, const float (&v)[kV]) {
