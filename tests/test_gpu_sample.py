@@ -198,6 +198,17 @@ def test_strides_and_alignment(tg, dtype, offset):
     _check(tg, x[2:3].expand(7, 3001), u, None, 2500, 0.7, device_x=one)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_the_largest_vocabulary(tg, dtype):
+    """2^18 logits a row, one row of them off every boundary; a top_k as large as integers go."""
+    x, u = _logits(3, 2 ** 18, dtype)
+    wide = torch.zeros(3, 2 ** 18 + 1, dtype=dtype, device="cuda")
+    view = wide[:, 1:]
+    view.copy_(x)
+    for k, p in ((None, None), (2 ** 63 - 1, None), (None, 0.99), (40000, None), (30, 0.5)):
+        _check(tg, x, u, 1.5, k, p, None, device_x=view)
+
+
 def test_a_row_does_not_depend_on_the_batch(tg):
     """The split over CTAs follows the number of rows; the tokens do not."""
     x, u = _logits(700, 20011, torch.bfloat16)

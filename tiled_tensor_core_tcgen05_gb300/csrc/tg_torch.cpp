@@ -6,6 +6,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <optional>
@@ -590,7 +591,7 @@ struct Setting {
     Setting(PyObject* x, const char* name, int64_t rows, at::ScalarType type, double none) : all(none) {
         if (x == Py_None) return;
         if (!THPVariable_Check(x)) {
-            all = type == at::kInt ? static_cast<double>(integer(x)) : real(x);
+            all = type == at::kInt ? static_cast<double>(std::min<int64_t>(std::max<int64_t>(integer(x), 0), INT32_MAX)) : real(x);
             return;
         }
         p = vector(x, name, rows, type);
