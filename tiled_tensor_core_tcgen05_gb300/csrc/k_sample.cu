@@ -87,10 +87,14 @@ __device__ const Powers kPowers = make_powers();
 
 // What a row's logits are weighed with.
 struct Scale {
-    float top;       // the largest logit
-    float hi, lo;    // 2 / T
-    float none;      // a logit whose weight is none, and so are those below it
-    bool flat;       // the largest is infinite: what is kept weighs the same
+    float top;          // the largest logit
+    float half, minus;  // where not near: a half (with T so large that 2 / T is no good float, less), and as much of -top
+    float hi, lo;       // 1 / T; where not near 1 / (half T)
+    float round;        // kRound; near: less the steps of the largest, so that no logit is above kRound
+    float none;         // a logit whose weight is none, and so are those below it; kNone: not known
+    float wide;         // half of a bin's width in logits
+    bool near;          // logits are at most some hundred T: they are weighed without the largest's being taken off first
+    bool flat;          // the largest is infinite: what is kept weighs the same
 };
 
 constexpr double kLn = 0.693147180559945309417 / kSteps;
@@ -101,28 +105,39 @@ constexpr int kRoundBits = 0x4B400000;
 constexpr float kHigh = 12.0f, kLow = 1.5f / 524288.0f;  // sums with them are multiples of 2^-20 and 2^-42
 constexpr int kHighBits = 0x41400000, kLowBits = 0x36400000;
 
-// ln w of a logit as P (of d, half its difference from the largest), and 256 log2 w to the nearest integer, above kRoundBits.
-__device__ __forceinline__ int step_bits(float p) { return __float_as_int(__fmaf_rn(p, kPerLn, kRound)); }
+// ln w of a logit, or what is taken off it in the end, as p + q and some, and 256 log2 w to the nearest integer, above kRoundBits.
+__device__ __forceinline__ float differ(float x, const Scale& c) { return __fmaf_rn(c.half, x, c.minus); }
+__device__ __forceinline__ int step_bits(float p, const Scale& c) { return __float_as_int(__fmaf_rn(p, kPerLn, c.round)); }
 
 // The weight of a logit, in two parts added to `high` and `low` (units(), below): w = (high part) 2^-20 + (low part) 2^-42. Its step comes back. The
-// logit is at most c.top and not so far below it that w is no ordinary float. w is right to 2^-37 of itself, and most to 2^-42, before its rounding to 2^-42:
-// with the difference of halves of the logits (which stays finite) as d + e exactly and 2 / T as hi + lo, ln w = p + q; n = round(256 log2 w);
-// what is left after n ln(2) / 256 is u (exactly: it has 22 bits) and some more, f, and with u at most 2^-9.5
-//     w = 2^(n / 256) (1 + u + (u^2 / 2 + u^3 / 6 + f + u f)),
-// u^4 / 24 being 2^-42.6 and f at most 2^-19; 2^(n / 256) is a table's entry th + tl, whose exponents are moved. The operations bound the passes that
-// weigh all logits: 30 of them on the floating point pipe (two at a time, in packed form, they take as long).
+// logit is at most c.top and not so far below it that w is no ordinary float. w is right to 2^-37 of itself, before its rounding to 2^-42. x / T = p + q
+// with 1 / T as hi + lo, good to 2^-46 (an error that grows as x does is the same power of every weight: of their ratios, 2^-46 of the difference's);
+// m = round(256 / ln(2) p); what is left after m ln(2) / 256 is u (exactly: it has 24 bits) and some more, f, at most 2^-15; and with U = u + f,
+// at most 2^-9.4,
+//     exp(x / T) = 2^(m / 256) (1 + u + (f + U^2 / 2 + U^3 / 6)),
+// U^4 / 24 being 2^-42; 2^(m / 256) is a table's entry th + tl, whose exponents are moved: by m less the largest's, rounded up, so weights are
+// relative to something up to 2^(1 / 256) larger than the largest's, for all alike. That takes 22 operations on the floating point pipe, which bound
+// the passes that weigh all logits (two at a time, in packed form, they take as long; with the largest taken off first 30, which they took before:
+// 256 rows of 131072 fp32 120 us). Where logits are far from zero by T (`near` is not set) it is taken off: the difference of their halves, which stays finite,
+// as d + e exactly.
+template <bool kNear>
 __device__ __forceinline__ int weigh(float x, const Scale& c, const float2* powers, int& high, int& low) {
-    const float a = 0.5f * x, b = -0.5f * c.top, d = __fadd_rn(a, b);
-    const float bb = __fsub_rn(d, a), e = __fadd_rn(__fsub_rn(a, __fsub_rn(d, bb)), __fsub_rn(b, bb));
+    float d = x, e = 0.0f;
+    if (!kNear && !c.near) {
+        d = differ(x, c);
+        const float a = c.half * x, bb = __fsub_rn(d, a);
+        e = __fadd_rn(__fsub_rn(a, __fsub_rn(d, bb)), __fsub_rn(c.minus, bb));
+    }
     const float p = __fmul_rn(d, c.hi);
-    const float q = __fmaf_rn(d, c.lo, __fmaf_rn(e, c.hi, __fmaf_rn(d, c.hi, -p)));
-    const int bits = step_bits(p);
-    const float n = __fsub_rn(__int_as_float(bits), kRound);
+    float q = __fmaf_rn(d, c.lo, __fmaf_rn(d, c.hi, -p));
+    if (!kNear) q = __fmaf_rn(e, c.hi, q);
+    const int bits = step_bits(p, c);
+    const float m = __fsub_rn(__int_as_float(bits), c.round);
     const float2 t = powers[bits & (kSteps - 1)];
     const int by = (bits & ~(kSteps - 1)) << 15;
     const float th = __int_as_float(__float_as_int(t.x) + by), tl = __int_as_float(__float_as_int(t.y) + by);
-    const float u = __fmaf_rn(n, -kLnHi, p), f = __fmaf_rn(n, -kLnLo, q);
-    const float v = __fmaf_rn(__fmul_rn(u, u), __fmaf_rn(u, 1.0f / 6.0f, 0.5f), __fmaf_rn(u, f, f));
+    const float u = __fmaf_rn(m, -kLnHi, p), f = __fmaf_rn(m, -kLnLo, q), g = __fadd_rn(u, f);
+    const float v = __fmaf_rn(__fmul_rn(g, g), __fmaf_rn(g, 1.0f / 6.0f, 0.5f), f);
     const float s = __fmaf_rn(th, u, th);
     const float r = __fadd_rn(__fmaf_rn(th, u, __fsub_rn(th, s)), __fmaf_rn(th, v, __fmaf_rn(tl, u, tl)));
     const float h = __fadd_rn(s, kHigh);
@@ -137,16 +152,17 @@ __device__ __forceinline__ u64 units(int high, int low) { return static_cast<u64
 
 __device__ __forceinline__ u64 weight_of(float x, const Scale& c, const float2* powers) {
     if (c.flat) return 1ull << kUnit;
-    if (!(__fmul_rn(__fadd_rn(0.5f * x, -0.5f * c.top), c.hi) > -32.0f)) return 0;  // and where c.none says nothing
+    if (c.near) x = fmaxf(x, c.none);
+    else if (!(__fmul_rn(differ(x, c), c.hi) > -32.0f)) return 0;  // and where c.none says nothing
     int high = 0, low = 0;
-    weigh(x, c, powers, high, low);
+    weigh<false>(x, c, powers, high, low);
     return units(high, low);
 }
 
 // A step's bin, and a logit's: it falls as the logit does, so bins are in order.
 __device__ __forceinline__ int bin_of_bits(int bits) { return min((kRoundBits - bits) / kBinSteps, kBins - 1); }
 __device__ __forceinline__ int bin_of(float x, const Scale& c) {
-    return c.flat ? 0 : bin_of_bits(step_bits(__fmul_rn(__fadd_rn(0.5f * x, -0.5f * c.top), c.hi)));
+    return c.flat ? 0 : bin_of_bits(step_bits(__fmul_rn(differ(x, c), c.hi), c));
 }
 
 // A logit's rank among all: larger ones higher, of equal ones the lower index (-0 and 0 are equal).
@@ -201,7 +217,19 @@ struct Row {
             else v[i] = to_float(e[i]);
         }
     }
-    // The first pass: reads, keeps, f(index of the first, the kV logits).
+    // The largest of a piece.
+    __device__ __forceinline__ static float most(const uint4& u) {
+        if constexpr (std::is_same<E, float>::value) {
+            return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+        } else {
+            using E2 = std::conditional_t<std::is_same<E, __half>::value, __half2, __nv_bfloat162>;
+            E2 p[4];
+            memcpy(p, &u, 16);
+            const E2 x = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+            return to_float(__hmax(x.x, x.y));
+        }
+    }
+    // The first pass: reads, keeps, f(the piece).
     template <typename F>
     __device__ __forceinline__ void load(F f) {
         constexpr int kAhead = 4;
@@ -214,9 +242,7 @@ struct Row {
             for (int a = 0; a < kAhead; ++a) {
                 if (g + a * kWarps >= groups) break;
                 held[(g + a * kWarps) * 32 + (threadIdx.x & 31)] = u[a];
-                float v[kV];
-                open(u[a], v);
-                f(index(g + a * kWarps), v);
+                f(u[a]);
             }
         }
     }
@@ -225,12 +251,9 @@ struct Row {
     __device__ __forceinline__ void each(float least, F f) const {
         for (int g = threadIdx.x / 32; g < groups; g += kWarps) {
             const uint4 u = held[g * 32 + (threadIdx.x & 31)];
+            if (!__any_sync(0xFFFFFFFFu, !(most(u) < least))) continue;
             float v[kV];
             open(u, v);
-            float most = v[0];
-#pragma unroll
-            for (int e = 1; e < kV; ++e) most = fmaxf(most, v[e]);
-            if (!__any_sync(0xFFFFFFFFu, !(most < least))) continue;
             f(g, index(g), v);
         }
     }
@@ -327,12 +350,12 @@ struct Sampler {
     __device__ __forceinline__ bool kept(float x, int i) const { return x > cut_x || (x == cut_x && static_cast<uint32_t>(i) <= cut_i); }
     // A logit that no one of bin b or before is below.
     __device__ __forceinline__ float lowest_of(int b) const {
-        return scale.flat ? scale.top : scale.top - (2.0f * (b + 2) * kBinSteps * kLnHi / scale.hi) * 1.0001f - 1e-5f * fabsf(scale.top);
+        return scale.flat ? scale.top : scale.top - 2.0f * (b + 2) * scale.wide * 1.0001f - 1e-5f * fabsf(scale.top);
     }
 
     // A logit above which there is none of bin b.
     __device__ __forceinline__ float highest_of(int b) const {
-        const float half = (b - 1) * kBinSteps * kLnHi / scale.hi * 0.9999f;  // by halves: the whole way may pass what a float holds
+        const float half = (b - 1) * scale.wide * 0.9999f;  // by halves: the whole way may pass what a float holds
         return scale.flat ? scale.top : scale.top - half - half + 1e-5f * fabsf(scale.top);
     }
 
@@ -366,42 +389,44 @@ struct Sampler {
         return t;
     }
 
-    // The place of the largest logit; 0: there is none above -inf.
-    __device__ u64 largest() {
-        int at = INT_MAX;
-        row.load([&](int i, const float (&v)[kV]) {
-#pragma unroll
-            for (int e = 0; e < kV; ++e)
-                if (v[e] > best) {
-                    best = v[e];
-                    at = i + e;
-                }
-        });
-        u64 p = best > kNone ? place_of(best, at) : 0;
+    // The largest logit; -inf where there is none above.
+    __device__ float largest() {
+        row.load([&](const uint4& u) { best = fmaxf(best, Row<E>::most(u)); });
+        uint32_t p = key_of(best);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) p = max(p, __shfl_xor_sync(0xFFFFFFFFu, p, o));
         if ((threadIdx.x & 31) == 0) s.sums[threadIdx.x >> 5] = p;
         __syncthreads();
         p = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) p = max(p, s.sums[w]);
+        for (int w = 0; w < kWarps; ++w) p = max(p, static_cast<uint32_t>(s.sums[w]));
         asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // the arrival is at the kernel's start: every CTA runs
         u64 (*box)[kMaxCtas] = tell(p, 0);
-        for (uint32_t r = 0; r < ctas; ++r) p = max(p, box[0][r]);
-        return p;
+        for (uint32_t r = 0; r < ctas; ++r) p = max(p, static_cast<uint32_t>(box[0][r]));
+        return logit_of(static_cast<u64>(p) << 32);
+    }
+    // Writes the index of the first logit that is x.
+    __device__ void first_of(float x, int32_t* token) {
+        if (threadIdx.x == 0) s.found[0] = INT_MAX;
+        __syncthreads();
+        int at = INT_MAX;
+        row.each(x, [&](int, int i, const float (&v)[kV]) {
+#pragma unroll
+            for (int e = kV - 1; e >= 0; --e)
+                if (v[e] == x) at = min(at, i + e);
+        });
+        if (at < INT_MAX) atomicMin(&s.found[0], at);
+        __syncthreads();
+        u64 (*box)[kMaxCtas] = tell(static_cast<u64>(s.found[0]), 0);
+        u64 first = INT_MAX;
+        for (uint32_t r = 0; r < ctas; ++r) first = min(first, box[0][r]);
+        if (rank == 0 && threadIdx.x == 0) *token = static_cast<int32_t>(first);
     }
 
     // Weights of a piece's kept logits, added up; with kPart, of those in bins before `first`.
     template <bool kPart>
     __device__ __forceinline__ u64 weigh_piece(int i, const float (&v)[kV], int first = 0) {
-        float x[kV];
-        if (easy) {  // below the cut there is no weight
-#pragma unroll
-            for (int e = 0; e < kV; ++e) x[e] = fmaxf(v[e], scale.none);
-        } else if (scale.none > kNone && !scale.flat) {
-#pragma unroll
-            for (int e = 0; e < kV; ++e) x[e] = kept(v[e], i + e) ? v[e] : scale.none;
-        } else {
+        if (!scale.near) {
             u64 sum = 0;
 #pragma unroll 1
             for (int e = 0; e < kV; ++e) {
@@ -412,16 +437,24 @@ struct Sampler {
             }
             return sum;
         }
+        float x[kV];
+        if (easy) {  // below the cut there is no weight
+#pragma unroll
+            for (int e = 0; e < kV; ++e) x[e] = fmaxf(v[e], scale.none);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kV; ++e) x[e] = kept(v[e], i + e) ? v[e] : scale.none;
+        }
         int high = 0, low = 0;
 #pragma unroll
         for (int e = 0; e < kV; ++e) {
             if (kPart) {
                 int h = 0, l = 0;
-                const bool in = weigh(x[e], scale, s.powers, h, l) > kRoundBits - first * kBinSteps;
+                const bool in = weigh<true>(x[e], scale, s.powers, h, l) > kRoundBits - first * kBinSteps;
                 high += in ? h : 0;
                 low += in ? l : 0;
             } else {
-                weigh(x[e], scale, s.powers, high, low);
+                weigh<true>(x[e], scale, s.powers, high, low);
             }
         }
         return units(high, low);
@@ -1255,27 +1288,39 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
     for (int b = threadIdx.x; b < kBins; b += kThreads) s.all[b] = 0;
     if (threadIdx.x == kThreads - 32 && !greedy && min_p > 0.0f && min_p < 1.0f)  // in 64 bits, once, while the others read
         s.log_min_p = static_cast<double>(temperature) * log(static_cast<double>(min_p));
-    const u64 top = w.largest();
-    if (top == 0) {
+    const float x = w.largest();
+    if (!(x > kNone)) {
         if (rank == 0 && threadIdx.x == 0) c.tokens[r] = -1;
         return;
     }
     if (greedy) {
-        if (rank == 0 && threadIdx.x == 0) c.tokens[r] = index_of(top);
+        w.first_of(x, c.tokens + r);
         return;
     }
     {
-        // 2 / T as hi + lo: 1 / T = y + y (1 - y T), good to 2^-46
-        const float y = 1.0f / temperature, hi = fminf(2.0f * y, 3e38f), lo = 2.0f * y * fmaf(-y, temperature, 1.0f), x = logit_of(top);
+        const float y = 1.0f / temperature;
+        const u64 top = static_cast<u64>(key_of(x)) << 32;
         // what is kept at all: above -inf, and not so small that a weight is nothing (2^-45 and below)
         const float none = x - 45.0f * 0.6931472f * temperature, far = (0.5f * x - 0.5f * none) * y;
         const u64 finite = static_cast<u64>(key_of(kNone) + 1) << 32;
-        u64 cut = isinf(x) ? top >> 32 << 32 : none > kNone ? max(finite, static_cast<u64>(key_of(none)) << 32) : finite;
-        // lo: 0 where T or 1 / T is infinite. none: where logits are as coarse as T it may have a weight, or be too far off for weigh()
-        w.scale = Scale{x, hi, fabsf(lo) <= 1e-6f * hi ? lo : 0.0f, none > kNone && far > 15.2f && far < 25.0f ? none : kNone, isinf(x)};
-        w.easy = w.scale.none > kNone && !(min_p > 0.0f);
+        u64 cut = isinf(x) ? top : none > kNone ? max(finite, static_cast<u64>(key_of(none)) << 32) : finite;
+        Scale& a = w.scale;
+        a.top = x;
+        a.flat = isinf(x);
+        a.none = none > kNone && far > 15.2f && far < 25.0f ? none : kNone;  // where logits are as coarse as T it may have a weight, or be too far off
+        a.wide = 0.5f * kBinSteps * kLnHi * temperature;
+        a.near = a.none > kNone && fabsf(x) * y <= 200.0f && temperature < 1e18f && temperature > 1e-18f;
+        // 1 / T, times 2 or (T large) more, as hi + lo: 1 / t = z + z (1 - z t), good to 2^-46; lo is 0 where T or 1 / T is infinite
+        const float t = a.near || temperature < 1e18f ? temperature : temperature * 0x1p-100f, z = 1.0f / t, times = a.near ? 1.0f : 2.0f;
+        a.half = a.near ? 1.0f : t == temperature ? 0.5f : 0x1p-101f;
+        a.minus = a.near ? 0.0f : -a.half * x;
+        a.hi = fminf(times * z, 3e38f);
+        const float lo = times * z * fmaf(-z, t, 1.0f);
+        a.lo = fabsf(lo) <= 1e-6f * a.hi ? lo : 0.0f;
+        a.round = a.near ? kRound - ceilf(__fmul_rn(__fmul_rn(x, a.hi), kPerLn)) : kRound;
+        w.easy = a.near && !(min_p > 0.0f);
         if (min_p >= 1.0f) {
-            cut = top >> 32 << 32;
+            cut = top;
         } else if (min_p > 0.0f) {
             const double least = static_cast<double>(x) + s.log_min_p;
             float z = static_cast<float>(least);
