@@ -109,8 +109,8 @@ constexpr int kHighBits = 0x41400000, kLowBits = 0x36400000;
 __device__ __forceinline__ float differ(float x, const Scale& c) { return __fmaf_rn(c.half, x, c.minus); }
 __device__ __forceinline__ int step_bits(float p, const Scale& c) { return __float_as_int(__fmaf_rn(p, kPerLn, c.round)); }
 
-// The weight of a logit, in two parts added to `high` and `low` (units(), below): w = (high part) 2^-20 + (low part) 2^-42. Its step comes back. The
-// logit is at most c.top and not so far below it that w is no ordinary float. w is right to 2^-37 of itself, before its rounding to 2^-42. x / T = p + q
+// The weight of a logit, in two parts added to `high` and `low` (units(), below): w = (high part) 2^-20 + (low part) 2^-42. A logit whose step is below
+// `least` has none. The logit is at most c.top and not so far below it that w is no ordinary float. w is right to 2^-37 of itself, before its rounding to 2^-42. x / T = p + q
 // with 1 / T as hi + lo, good to 2^-46 (an error that grows as x does is the same power of every weight: of their ratios, 2^-46 of the difference's);
 // m = round(256 / ln(2) p); what is left after m ln(2) / 256 is u (exactly: it has 24 bits) and some more, f, at most 2^-15; and with U = u + f,
 // at most 2^-9.4,
@@ -121,7 +121,7 @@ __device__ __forceinline__ int step_bits(float p, const Scale& c) { return __flo
 // 256 rows of 131072 fp32 120 us). Where logits are far from zero by T (`near` is not set) it is taken off: the difference of their halves, which stays finite,
 // as d + e exactly.
 template <bool kNear>
-__device__ __forceinline__ int weigh(float x, const Scale& c, const float2* powers, int& high, int& low) {
+__device__ __forceinline__ void weigh(float x, const Scale& c, const float2* powers, int& high, int& low, int least = INT_MIN) {
     float d = x, e = 0.0f;
     if (!kNear && !c.near) {
         d = differ(x, c);
@@ -133,8 +133,9 @@ __device__ __forceinline__ int weigh(float x, const Scale& c, const float2* powe
     if (!kNear) q = __fmaf_rn(e, c.hi, q);
     const int bits = step_bits(p, c);
     const float m = __fsub_rn(__int_as_float(bits), c.round);
-    const float2 t = powers[bits & (kSteps - 1)];
-    const int by = (bits & ~(kSteps - 1)) << 15;
+    const int moved = bits >= least ? bits : kRoundBits - 60 * kSteps;  // 2^-60
+    const float2 t = powers[moved & (kSteps - 1)];
+    const int by = (moved & ~(kSteps - 1)) << 15;
     const float th = __int_as_float(__float_as_int(t.x) + by), tl = __int_as_float(__float_as_int(t.y) + by);
     const float u = __fmaf_rn(m, -kLnHi, p), f = __fmaf_rn(m, -kLnLo, q), g = __fadd_rn(u, f);
     const float v = __fmaf_rn(__fmul_rn(g, g), __fmaf_rn(g, 1.0f / 6.0f, 0.5f), f);
@@ -144,7 +145,6 @@ __device__ __forceinline__ int weigh(float x, const Scale& c, const float2* powe
     const float l = __fadd_rn(__fadd_rn(__fsub_rn(s, __fsub_rn(h, kHigh)), r), kLow);
     high += __float_as_int(h) - kHighBits;
     low += __float_as_int(l) - kLowBits;
-    return bits;
 }
 
 // Sums of weights' parts, in units of 2^-42.
@@ -160,7 +160,7 @@ __device__ __forceinline__ u64 weight_of(float x, const Scale& c, const float2* 
 }
 
 // A step's bin, and a logit's: it falls as the logit does, so bins are in order.
-__device__ __forceinline__ int bin_of_bits(int bits) { return min((kRoundBits - bits) / kBinSteps, kBins - 1); }
+__device__ __forceinline__ int bin_of_bits(int bits) { return min(static_cast<int>(static_cast<uint32_t>(kRoundBits - bits) / kBinSteps), kBins - 1); }
 __device__ __forceinline__ int bin_of(float x, const Scale& c) {
     return c.flat ? 0 : bin_of_bits(step_bits(__fmul_rn(differ(x, c), c.hi), c));
 }
@@ -195,20 +195,6 @@ struct Row {
         groups = min(all, group0 + each_cta) - group0;
     }
     __device__ int index(int group) const { return ((group0 + group) * 32 + (threadIdx.x & 31)) * kV - shift; }
-    __device__ uint4 read(int group) const {
-        const int i = index(group);
-        uint4 u;
-        if (i >= 0 && i + kV <= vocab) return __ldg(reinterpret_cast<const uint4*>(x + i));
-        E v[kV];
-#pragma unroll
-        for (int e = 0; e < kV; ++e) {
-            if (i + e >= 0 && i + e < vocab) v[e] = x[i + e];
-            else if constexpr (std::is_same<E, float>::value) v[e] = kNone;
-            else v[e] = from_float<E>(kNone);
-        }
-        memcpy(&u, v, 16);
-        return u;
-    }
     __device__ __forceinline__ static void open(const uint4& u, float (&v)[kV]) {
         const E* e = reinterpret_cast<const E*>(&u);
 #pragma unroll
@@ -233,11 +219,15 @@ struct Row {
     template <typename F>
     __device__ __forceinline__ void load(F f) {
         constexpr int kAhead = 4;
+        constexpr uint32_t kNones = std::is_same<E, float>::value ? 0xFF800000u : std::is_same<E, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
         for (int g = threadIdx.x / 32; g < groups; g += kWarps * kAhead) {
             uint4 u[kAhead];
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a)
-                if (g + a * kWarps < groups) u[a] = read(g + a * kWarps);
+            for (int a = 0; a < kAhead; ++a) {
+                const int i = index(g + a * kWarps);
+                u[a] = make_uint4(kNones, kNones, kNones, kNones);
+                if (g + a * kWarps < groups && i >= 0 && i + kV <= vocab) u[a] = __ldg(reinterpret_cast<const uint4*>(x + i));
+            }
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
                 if (g + a * kWarps >= groups) break;
@@ -245,6 +235,23 @@ struct Row {
                 f(u[a]);
             }
         }
+        edge(0, f);
+        edge((vocab - 1 + shift) / kV, f);
+    }
+    // Piece q, where it reaches beyond the row.
+    template <typename F>
+    __device__ __forceinline__ void edge(int q, F f) {
+        const int g = q / 32 - group0, i = q * kV - shift;
+        if (g < 0 || g >= groups || static_cast<int>(threadIdx.x) != g % kWarps * 32 + q % 32 || (i >= 0 && i + kV <= vocab)) return;
+        E v[kV];
+        uint4 u = held[g * 32 + (threadIdx.x & 31)];
+        memcpy(v, &u, 16);
+#pragma unroll
+        for (int e = 0; e < kV; ++e)
+            if (i + e >= 0 && i + e < vocab) v[e] = x[i + e];
+        memcpy(&u, v, 16);
+        held[g * 32 + (threadIdx.x & 31)] = u;
+        f(u);
     }
     // Further passes, over groups in which some logit is at least `least`: f(group, index of the first, the kV logits), whole warps.
     template <typename F>
@@ -389,38 +396,30 @@ struct Sampler {
         return t;
     }
 
-    // The largest logit; -inf where there is none above.
-    __device__ float largest() {
+    // The place of the largest logit, -inf's where there is none above: of the first one if `first`, else of any index.
+    __device__ u64 largest(bool first) {
         row.load([&](const uint4& u) { best = fmaxf(best, Row<E>::most(u)); });
-        uint32_t p = key_of(best);
+        const uint32_t own = key_of(best);
+        uint32_t k = __reduce_max_sync(0xFFFFFFFFu, own);
+        u64 p = static_cast<u64>(k) << 32;
+        if (first) {
+            int at = INT_MAX;
+            row.each(logit_of(p), [&](int, int i, const float (&v)[kV]) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) p = max(p, __shfl_xor_sync(0xFFFFFFFFu, p, o));
+                for (int e = kV - 1; e >= 0; --e)
+                    if (v[e] == logit_of(p)) at = min(at, i + e);
+            });
+            p |= static_cast<uint32_t>(~__reduce_min_sync(0xFFFFFFFFu, at));
+        }
         if ((threadIdx.x & 31) == 0) s.sums[threadIdx.x >> 5] = p;
         __syncthreads();
         p = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) p = max(p, static_cast<uint32_t>(s.sums[w]));
+        for (int w = 0; w < kWarps; ++w) p = max(p, s.sums[w]);
         asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // the arrival is at the kernel's start: every CTA runs
         u64 (*box)[kMaxCtas] = tell(p, 0);
-        for (uint32_t r = 0; r < ctas; ++r) p = max(p, static_cast<uint32_t>(box[0][r]));
-        return logit_of(static_cast<u64>(p) << 32);
-    }
-    // Writes the index of the first logit that is x.
-    __device__ void first_of(float x, int32_t* token) {
-        if (threadIdx.x == 0) s.found[0] = INT_MAX;
-        __syncthreads();
-        int at = INT_MAX;
-        row.each(x, [&](int, int i, const float (&v)[kV]) {
-#pragma unroll
-            for (int e = kV - 1; e >= 0; --e)
-                if (v[e] == x) at = min(at, i + e);
-        });
-        if (at < INT_MAX) atomicMin(&s.found[0], at);
-        __syncthreads();
-        u64 (*box)[kMaxCtas] = tell(static_cast<u64>(s.found[0]), 0);
-        u64 first = INT_MAX;
-        for (uint32_t r = 0; r < ctas; ++r) first = min(first, box[0][r]);
-        if (rank == 0 && threadIdx.x == 0) *token = static_cast<int32_t>(first);
+        for (uint32_t r = 0; r < ctas; ++r) p = max(p, box[0][r]);
+        return p;
     }
 
     // Weights of a piece's kept logits, added up; with kPart, of those in bins before `first`.
@@ -448,14 +447,7 @@ struct Sampler {
         int high = 0, low = 0;
 #pragma unroll
         for (int e = 0; e < kV; ++e) {
-            if (kPart) {
-                int h = 0, l = 0;
-                const bool in = weigh<true>(x[e], scale, s.powers, h, l) > kRoundBits - first * kBinSteps;
-                high += in ? h : 0;
-                low += in ? l : 0;
-            } else {
-                weigh<true>(x[e], scale, s.powers, high, low);
-            }
+            weigh<true>(x[e], scale, s.powers, high, low, kPart ? kRoundBits - first * kBinSteps + 1 : INT_MIN);
         }
         return units(high, low);
     }
@@ -466,12 +458,20 @@ struct Sampler {
         cluster_sync();
         row.each(cut_x, [&](int, int i, const float (&v)[kV]) {
             // many equal logits: one addition a warp
-            bool same = true;
-#pragma unroll
-            for (int e = 1; e < kV; ++e) same &= v[e] == v[0];
             const float first = __shfl_sync(0xFFFFFFFFu, v[0], 0);
-            if (__all_sync(0xFFFFFFFFu, same && v[0] == first && v[0] > cut_x)) {
-                if ((threadIdx.x & 31) == 0) atomicAdd(&s.bins[bin_of(first, scale)], 32u * kV);
+            if (__all_sync(0xFFFFFFFFu, v[0] == first && v[0] > cut_x)) {
+                bool same = true;
+#pragma unroll
+                for (int e = 1; e < kV; ++e) same &= v[e] == first;
+                if (__all_sync(0xFFFFFFFFu, same)) {
+                    if ((threadIdx.x & 31) == 0) atomicAdd(&s.bins[bin_of(first, scale)], 32u * kV);
+                    return;
+                }
+            }
+            if (cut_i == ~0u) {  // of logits as large as the cut's all are kept
+#pragma unroll
+                for (int e = 0; e < kV; ++e)
+                    if (v[e] >= cut_x) atomicAdd(&s.bins[bin_of(v[e], scale)], 1u);
                 return;
             }
 #pragma unroll
@@ -530,7 +530,7 @@ struct Sampler {
         row.each(from, [&](int g, int i, const float (&v)[kV]) {
             int mine = 0;
 #pragma unroll
-            for (int e = 0; e < kV; ++e) mine += kept(v[e], i + e) && f(v[e], i + e);
+            for (int e = 0; e < kV; ++e) mine += f(v[e], i + e) && kept(v[e], i + e);
             mine = __reduce_add_sync(0xFFFFFFFFu, mine);
             if (lane == 0) s.places[g].x = mine;
         });
@@ -555,7 +555,7 @@ struct Sampler {
             uint32_t in = 0;
 #pragma unroll
             for (int e = 0; e < kV; ++e)
-                if (kept(v[e], i + e) && f(v[e], i + e)) in |= 1u << e;
+                if (f(v[e], i + e) && kept(v[e], i + e)) in |= 1u << e;
             int x = __popc(in);
             const int own = x;
 #pragma unroll
@@ -1284,17 +1284,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
     const int top_k = c.top_k != nullptr ? __ldg(c.top_k + r) : c.top_k_all;
     const float u = u_given > 0.0f ? fminf(u_given, 0.99999994f) : 0.0f;
     const bool greedy = !(temperature > 0.0f);
-    for (int i = threadIdx.x; i < kSteps; i += kThreads) s.powers[i] = kPowers.v[i];
-    for (int b = threadIdx.x; b < kBins; b += kThreads) s.all[b] = 0;
+    if (!greedy) {
+        for (int i = threadIdx.x; i < kSteps; i += kThreads) s.powers[i] = kPowers.v[i];
+        for (int b = threadIdx.x; b < kBins; b += kThreads) s.all[b] = 0;
+    }
     if (threadIdx.x == kThreads - 32 && !greedy && min_p > 0.0f && min_p < 1.0f)  // in 64 bits, once, while the others read
         s.log_min_p = static_cast<double>(temperature) * log(static_cast<double>(min_p));
-    const float x = w.largest();
+    const u64 largest = w.largest(greedy);
+    const float x = logit_of(largest);
     if (!(x > kNone)) {
         if (rank == 0 && threadIdx.x == 0) c.tokens[r] = -1;
         return;
     }
     if (greedy) {
-        w.first_of(x, c.tokens + r);
+        if (rank == 0 && threadIdx.x == 0) c.tokens[r] = index_of(largest);
         return;
     }
     {
@@ -1349,9 +1352,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
         }
     }
     if (by_mass) {
-        u64 largest;
-        const u64 total = w.mass(largest), target = target_of(total, top_p);
-        if (!by_count && (largest >= target || c.vocab <= kList) && w.draw_few(0, top_p, target, u, c.tokens + r)) return;
+        u64 of_best;
+        const u64 total = w.mass(of_best), target = target_of(total, top_p);
+        if (!by_count && (of_best >= target || c.vocab <= kList) && w.draw_few(0, top_p, target, u, c.tokens + r)) return;
         if (w.nucleus(total, target, u, c.tokens + r)) return;
     } else {
         w.weigh_groups();
