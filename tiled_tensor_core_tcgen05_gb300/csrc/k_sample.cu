@@ -422,8 +422,8 @@ struct Sampler {
         return p;
     }
 
-    // Weights of a piece's kept logits, added up; with kPart, of those in bins before `first`.
-    template <bool kPart>
+    // Weights of a piece's kept logits, added up (with kGroup over the warp); with kPart, of those in bins before `first`.
+    template <bool kPart, bool kGroup>
     __device__ __forceinline__ u64 weigh_piece(int i, const float (&v)[kV], int first = 0) {
         if (!scale.near) {
             u64 sum = 0;
@@ -434,7 +434,7 @@ struct Sampler {
                 for (int k = 1; k < kV; ++k) y = k == e ? v[k] : y;
                 if (kept(y, i + e) && (!kPart || bin_of(y, scale) < first)) sum += weight_of(y, scale, s.powers);
             }
-            return sum;
+            return kGroup ? add_across(sum) : sum;
         }
         float x[kV];
         if (easy) {  // below the cut there is no weight
@@ -448,6 +448,10 @@ struct Sampler {
 #pragma unroll
         for (int e = 0; e < kV; ++e) {
             weigh<true>(x[e], scale, s.powers, high, low, kPart ? kRoundBits - first * kBinSteps + 1 : INT_MIN);
+        }
+        if (kGroup) {  // a group's parts fit 32 bits: at most 2^8 of 2^20
+            high = __reduce_add_sync(0xFFFFFFFFu, high);
+            low = __reduce_add_sync(0xFFFFFFFFu, low);
         }
         return units(high, low);
     }
@@ -1029,7 +1033,7 @@ struct Sampler {
         for (int g = threadIdx.x / 32 + (threadIdx.x & 31) * kWarps; g < row.groups; g += kThreads) s.groups[g] = 0;
         __syncwarp();
         row.each(cut_x, [&](int g, int i, const float (&v)[kV]) {
-            const u64 sum = add_across(weigh_piece<false>(i, v));
+            const u64 sum = weigh_piece<false, true>(i, v);
             if ((threadIdx.x & 31) == 0) s.groups[g] = sum;
         });
         __syncthreads();
@@ -1171,7 +1175,7 @@ struct Sampler {
                 for (int g = threadIdx.x / 32 + (threadIdx.x & 31) * kWarps; g < row.groups; g += kThreads) s.groups[g] = 0;
                 __syncwarp();
                 row.each(fmaxf(cut_x, lowest_of(first - 1)), [&](int g, int i, const float (&v)[kV]) {
-                    const u64 part = add_across(weigh_piece<true>(i, v, first));
+                    const u64 part = weigh_piece<true, true>(i, v, first);
                     if ((threadIdx.x & 31) == 0) {
                         s.groups[g] = part;
                         above += part;
@@ -1255,7 +1259,7 @@ struct Sampler {
     // The weight of what is kept, and of the threads' largest of it.
     __device__ u64 mass(u64& largest) {
         u64 sum = 0;
-        row.each(cut_x, [&](int, int i, const float (&v)[kV]) { sum += weigh_piece<false>(i, v); });
+        row.each(cut_x, [&](int, int i, const float (&v)[kV]) { sum += weigh_piece<false, false>(i, v); });
         sum = sum_block(sum);
         u64 (*box)[kMaxCtas] = tell(sum, sum_block(best >= cut_x ? weight_of(best, scale, s.powers) : 0));
         sum = largest = 0;
