@@ -181,6 +181,17 @@ def test_logits_over_the_whole_range_of_the_type(tg, t, p):
     x = (torch.rand(4, 60007, generator=g, dtype=torch.float64) * 6.8e38 - 3.4e38).float()
     _check(tg, x, torch.tensor([0.0, 0.4, 0.9, 0.9999]), t, None, p, None)
     _check(tg, x, torch.tensor([0.0, 0.4, 0.9, 0.9999]), t, 4000, p, None)
+    _check(tg, x, torch.tensor([0.0, 0.4, 0.9, 0.9999]), t, None, p, 0.3)
+
+
+@pytest.mark.parametrize("t", [1e-45, 1e-30, 0.3, 1.0, 1e3, 1e20, 3e38])
+@pytest.mark.parametrize("m", [1e-45, 1e-20, 0.05, 0.7, 0.99999994, 1.0])
+def test_least_weights(tg, t, m):
+    """At any temperature, of rows all over the type, a little, or around a number far from zero."""
+    g = torch.Generator().manual_seed(23)
+    y = torch.randn(3, 5000, generator=g)
+    for x in (y, y * t, y * 1e30, y + 1e4, y.bfloat16()):
+        _check(tg, x, torch.tensor([0.2, 0.55, 0.9999]), t, None, None, m)  # (at 0.5 some rows of weights nearly alike are beyond saying)
 
 
 @pytest.mark.parametrize("dtype", TYPES)

@@ -55,6 +55,7 @@ constexpr int kSome = kThreads;              // tokens of a bin that are ranked 
 constexpr int kGuess = 1280;                 // threads' largest above a threshold that the list can be expected to hold
 constexpr int kMostGroups = (1 << 18) / 128 / kMaxCtas + 2;  // of a CTA
 constexpr float kNone = -INFINITY;
+constexpr float kTiny = 0x1p-147f;            // a few of the least floats
 using u64 = unsigned long long;
 
 // 2^(j / 256) as the sum of two floats, by repeated square roots and products in integers.
@@ -88,11 +89,11 @@ __device__ const Powers kPowers = make_powers();
 // What a row's logits are weighed with.
 struct Scale {
     float top;          // the largest logit
-    float half, minus;  // where not near: a half (with T so large that 2 / T is no good float, less), and as much of -top
+    float half, minus;  // where not near: a half, times a power of two where 2 / T is no good float, and as much of -top
     float hi, lo;       // 1 / T; where not near 1 / (half T)
     float round;        // kRound; near: less the steps of the largest, so that no logit is above kRound
     float none;         // a logit whose weight is none, and so are those below it; kNone: not known
-    float wide;         // half of a bin's width in logits
+    float t;            // T
     bool near;          // logits are at most some hundred T: they are weighed without the largest's being taken off first
     bool flat;          // the largest is infinite: what is kept weighs the same
 };
@@ -285,7 +286,7 @@ struct Shared {
     u64 answer;
     int found[2], window[2];
     uint32_t listed;
-    double log_min_p;
+    float2 log_min_p;          // T ln(min_p), where T is large half of it, in two parts
 };
 constexpr int kHeld = (sizeof(Shared) + 15) / 16 * 16;  // where the row's stretch begins
 static_assert(kSub <= kBins && kSub <= kList && kSub == 2 * kThreads, "parts' counts and masses");
@@ -357,13 +358,12 @@ struct Sampler {
     __device__ __forceinline__ bool kept(float x, int i) const { return x > cut_x || (x == cut_x && static_cast<uint32_t>(i) <= cut_i); }
     // A logit that no one of bin b or before is below.
     __device__ __forceinline__ float lowest_of(int b) const {
-        return scale.flat ? scale.top : scale.top - 2.0f * (b + 2) * scale.wide * 1.0001f - 1e-5f * fabsf(scale.top);
+        return scale.flat ? scale.top : scale.top - (b + 2) * (kBinSteps * kLnHi * 1.0001f) * scale.t - 1e-5f * fabsf(scale.top) - kTiny;
     }
-
     // A logit above which there is none of bin b.
     __device__ __forceinline__ float highest_of(int b) const {
-        const float half = (b - 1) * scale.wide * 0.9999f;  // by halves: the whole way may pass what a float holds
-        return scale.flat ? scale.top : scale.top - half - half + 1e-5f * fabsf(scale.top);
+        const float half = (b - 1) * (0.5f * kBinSteps * kLnHi * 0.9999f) * scale.t;  // by halves: the whole way may pass what a float holds
+        return scale.flat ? scale.top : scale.top - half - half + 1e-5f * fabsf(scale.top) + kTiny;
     }
 
     // Two numbers of this CTA's to every CTA; afterwards all of them are in the box that comes back. Threads of the CTA
@@ -1292,8 +1292,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
         for (int i = threadIdx.x; i < kSteps; i += kThreads) s.powers[i] = kPowers.v[i];
         for (int b = threadIdx.x; b < kBins; b += kThreads) s.all[b] = 0;
     }
-    if (threadIdx.x == kThreads - 32 && !greedy && min_p > 0.0f && min_p < 1.0f)  // in 64 bits, once, while the others read
-        s.log_min_p = static_cast<double>(temperature) * log(static_cast<double>(min_p));
+    if (threadIdx.x == kThreads - 32 && !greedy && min_p > 0.0f && min_p < 1.0f) {  // in 64 bits, once, while the others read
+        const double below = (temperature < 1e30f ? 1.0 : 0.5) * static_cast<double>(temperature) * log(static_cast<double>(min_p));
+        s.log_min_p.x = static_cast<float>(below);
+        s.log_min_p.y = isinf(s.log_min_p.x) ? 0.0f : __double2float_ru(below - static_cast<double>(s.log_min_p.x));
+    }
     const u64 largest = w.largest(greedy);
     const float x = logit_of(largest);
     if (!(x > kNone)) {
@@ -1315,11 +1318,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
         a.top = x;
         a.flat = isinf(x);
         a.none = none > kNone && far > 15.2f && far < 25.0f ? none : kNone;  // where logits are as coarse as T it may have a weight, or be too far off
-        a.wide = 0.5f * kBinSteps * kLnHi * temperature;
+        a.t = temperature;
         a.near = a.none > kNone && fabsf(x) * y <= 200.0f && temperature < 1e18f && temperature > 1e-18f;
-        // 1 / T, times 2 or (T large) more, as hi + lo: 1 / t = z + z (1 - z t), good to 2^-46; lo is 0 where T or 1 / T is infinite
-        const float t = a.near || temperature < 1e18f ? temperature : temperature * 0x1p-100f, z = 1.0f / t, times = a.near ? 1.0f : 2.0f;
-        a.half = a.near ? 1.0f : t == temperature ? 0.5f : 0x1p-101f;
+        // 1 / t, with t = T, or as much of it as of the logits: 1 / t = z + z (1 - z t), good to 2^-46; lo is 0 where T or 1 / T is infinite. With T small and
+        // |x| not, nothing beside x has a weight
+        const float by = a.near || (temperature >= 1e-18f && temperature < 1e18f) ? 1.0f : temperature >= 1e18f ? 0x1p-100f : fabsf(x) < 0x1p20f ? 0x1p100f : 1.0f;
+        const float t = temperature * by, z = 1.0f / t, times = a.near ? 1.0f : 2.0f;
+        a.half = a.near ? 1.0f : 0.5f * by;
         a.minus = a.near ? 0.0f : -a.half * x;
         a.hi = fminf(times * z, 3e38f);
         const float lo = times * z * fmaf(-z, t, 1.0f);
@@ -1329,10 +1334,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleCall c)
         if (min_p >= 1.0f) {
             cut = top;
         } else if (min_p > 0.0f) {
-            const double least = static_cast<double>(x) + s.log_min_p;
-            float z = static_cast<float>(least);
-            if (static_cast<double>(z) < least) z = nextafterf(z, INFINITY);  // the least float that is not below
-            cut = max(cut, static_cast<u64>(key_of(z)) << 32);
+            // the least float that is not below x + T ln(min_p), or half of it, as s0 + t0 and less (64-bit arithmetic would take all threads 1000 cycles)
+            const float part = temperature < 1e30f ? 1.0f : 0.5f, h = part * x, b = s.log_min_p.x, s0 = __fadd_rn(h, b), bb = __fsub_rn(s0, h);
+            if (fabsf(s0) < INFINITY) {
+                const float t0 = __fadd_rn(__fadd_rn(__fsub_rn(h, __fsub_rn(s0, bb)), __fsub_rn(b, bb)), s.log_min_p.y);
+                float z = __fadd_rn(s0, t0);
+                if (__fsub_rn(t0, __fsub_rn(z, s0)) > 0.0f) z = nextafterf(z, INFINITY);
+                cut = max(cut, static_cast<u64>(key_of(z / part)) << 32);
+            }
         }
         w.keep_from(cut);
     }
