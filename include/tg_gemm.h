@@ -616,8 +616,8 @@ tg_status tg_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v_s
  *
  * Each of the settings is one float32 (top_k: int32) a row on the device, or
  * where the pointer is NULL the number beside it for all rows. Weights are 64-bit
- * fixed point, of 2^-42 of the row's largest (w_i below half of that count as
- * none), right to 2^-37 of themselves and half a unit, and their sums are exact:
+ * fixed point, of 2^-42 of about the row's largest (w_i below half of that count
+ * as none), right to 2^-37 of themselves and half a unit, and their sums are exact:
  * the token does not depend on how the work is split, nor on the other rows.
  * vocab is at most 2^18. Stream-ordered; allocates nothing.
  */

@@ -17,7 +17,7 @@
 // A cluster of CTAs takes a row, each CTA a stretch of it, which the first pass leaves in
 // shared memory: the logits are read from HBM once. The passes, of which a row makes
 // those its settings ask for:
-//   1  the largest logit (a greedy row ends here), and the largest of each thread's;
+//   1  the largest logit (a greedy row ends here), and each thread's largest;
 //   2  where top_p needs it, the exact weight of all;
 //   3  a threshold from the threads' largest: as many of them are above it as top_k wants, or as much
 //      weight as top_p does, so what the row keeps is above it, and not much else;
@@ -29,9 +29,10 @@
 //   6  the tokens of the border's bins, brought together: the cut, and their kept weight to their groups;
 //   7  the group, lane and token in which u of the kept weight is passed.
 //
-// What bounds it is the chain of these steps, between which the CTAs meet, and the 30 operations that a weight takes,
-// not the bytes. Measured on a GB300, in a graph: one row of 32000 fp16 logits, top_p 0.9: 13.5 us; 64 rows of 131071 bf16: greedy 9.6,
-// no cut 33, top_k 50 35, top_p 0.9 100, settings mixed 52; 256 rows of 131072 fp32, top_p 0.9: 243 (the bytes take 20).
+// What bounds it is the chain of these steps, between which the CTAs meet, and the 22 operations that a weight takes,
+// not the bytes: of 256 rows, warps issue in half of the cycles. Measured on a GB300, in a graph: one row of 32000 fp16 logits, top_p 0.9:
+// 12.9 us; 64 rows of 131071 bf16: greedy 6.2, no cut 21, top_k 50 17, top_p 0.9 76, settings mixed 42; 256 rows of 131072 fp32,
+// top_p 0.9: 216 (the bytes take 20).
 #include "tg_device.cuh"
 #include "tg_kv.cuh"
 
@@ -118,8 +119,8 @@ __device__ __forceinline__ int step_bits(float p, const Scale& c) { return __flo
 //     exp(x / T) = 2^(m / 256) (1 + u + (f + U^2 / 2 + U^3 / 6)),
 // U^4 / 24 being 2^-42; 2^(m / 256) is a table's entry th + tl, whose exponents are moved: by m less the largest's, rounded up, so weights are
 // relative to something up to 2^(1 / 256) larger than the largest's, for all alike. That takes 22 operations on the floating point pipe, which bound
-// the passes that weigh all logits (two at a time, in packed form, they take as long; with the largest taken off first 30, which they took before:
-// 256 rows of 131072 fp32 120 us). Where logits are far from zero by T (`near` is not set) it is taken off: the difference of their halves, which stays finite,
+// the passes that weigh all logits (two at a time, in packed form, they take as long). With the largest taken off first it is 30: 256 rows of 131072
+// fp32, no cut, 105 and 120 us. Where logits are far from zero by T (`near` is not set) it is taken off: the difference of their halves, which stays finite,
 // as d + e exactly.
 template <bool kNear>
 __device__ __forceinline__ void weigh(float x, const Scale& c, const float2* powers, int& high, int& low, int least = INT_MIN) {
@@ -1388,8 +1389,8 @@ cudaError_t launch(const SampleCall& c, int sm_count, cudaStream_t stream) {
     }
     // CTAs of a row: at least so many that two stretches fit an SM's shared memory; more where rows are few, with at least 2048 logits each: as
     // long as all run at once, two an SM, or, where rows have settings of their own, twice as many: the few that take several times as long as
-    // the others end sooner. Measured, us, 64 rows of 131071 bf16 with four and eight each: top_k 50 21.6 and 35.3, top_p 0.9 at T = 2
-    // 92 and 122, settings mixed 70.6 and 52.4.
+    // the others end sooner. Measured, us, 64 rows of 131071 bf16 with four and eight each: top_k 50 17.2 and 31.1, top_p 0.9 at T = 2
+    // 77 and 99, settings mixed 58.2 and 41.6.
     const int64_t pieces = (c.vocab + Row<E>::kV - 1) / Row<E>::kV + 1, groups = (pieces + 31) / 32;
     const int64_t most = (c.temperature != nullptr || c.top_k != nullptr || c.top_p != nullptr ? 4ll : 2ll) * sm_count;
     int ctas = 1;
