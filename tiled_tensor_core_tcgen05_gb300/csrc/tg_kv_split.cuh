@@ -203,19 +203,18 @@ __device__ __forceinline__ void finish_row(const KvAttnCall& c, int64_t to, int 
     if (d == 0 && c.lse != nullptr) c.lse[to] = row_lse(top, sum);
 }
 
-// Joins the parts of the unit inside which share k begins, if k's is its first border: block
-// (k - 1, rows 8 blockIdx.y ..), a warp a row, kDim / 32 values a lane. The order of the parts is that
-// of their keys. What a part counts for is computed once, a part a lane.
-constexpr int kJoinRows = 8;
+// Whether share k begins inside a unit whose first border that is.
+__device__ __forceinline__ bool first_border(const SplitWork& a, const Meta& m, int k) {
+    return m.chunks != 0 && Shares(m.total, a.grid, a.least).start(k - 1) <= m.unit_start + a.extra;
+}
 
+// Joins the parts of row r of the unit inside which share k begins, if k's is its first border: a warp, kDim / 32 values a lane.
+// The order of the parts is that of their keys. What a part counts for is computed once, a part a lane.
 template <typename E, int kDim, int kRows, bool kParts>
-__global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const SplitWork a) {
+__device__ __forceinline__ void join_row(const SplitWork& a, int k, int r) {
     constexpr int kN = kDim / 32;
     const KvAttnCall& c = a.c;
-    if constexpr (kParts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (blockIdx.y == 0) clear_uncovered<E, kDim>(c);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int k = blockIdx.x + 1, lane = threadIdx.x % 32, r = blockIdx.y * kJoinRows + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
     const Meta m = a.meta[k];
     if (m.chunks == 0) return;
     const Shares shares(m.total, a.grid, a.least);
@@ -280,6 +279,40 @@ __global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const SplitWo
     finish_row<E, kDim, kN, kParts>(c, to, lane * kN, v, top, sum, m.part != 0);
 }
 
+// A warp a row: block (k - 1, rows 8 blockIdx.y ..). Where groups of many rows share keys, units are few, and so are the borders that are a unit's
+// first: a grid of about what the GPU holds looks for them (a thread a border) and shares their rows out (64 sequences on 8192 shared tokens 89 -> 83 us;
+// prompt chunks, where nearly every border is one, take 677 us that way and 667 with a block a border and eight rows).
+constexpr int kJoinRows = 8;
+constexpr int kMostBorders = 1024;
+
+template <typename E, int kDim, int kRows, bool kParts>
+__global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const SplitWork a) {
+    if constexpr (kParts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.y == 0) clear_uncovered<E, kDim>(a.c);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if constexpr (!kParts || kRows <= 64) {
+        join_row<E, kDim, kRows, kParts>(a, blockIdx.x + 1, blockIdx.y * kJoinRows + warp);
+    } else {
+        __shared__ int borders[kMostBorders], found[kJoinRows];
+        int n = 0;
+        for (int base = 1; base < a.grid; base += 32 * kJoinRows) {
+            const int k = base + threadIdx.x;
+            const bool yes = k < a.grid && first_border(a, a.meta[k], k);
+            const uint32_t all = __ballot_sync(0xFFFFFFFFu, yes);
+            if (lane == 0) found[warp] = __popc(all);
+            __syncthreads();
+            for (int w = 0; w < kJoinRows; ++w) {
+                if (w == warp && yes) borders[n + __popc(all & ((1u << lane) - 1))] = k;
+                n += found[w];
+            }
+            __syncthreads();
+        }
+        constexpr int kPieces = kRows / kJoinRows;
+        for (int i = blockIdx.x; i < n * kPieces; i += gridDim.x) join_row<E, kDim, kRows, kParts>(a, borders[i / kPieces], i % kPieces * kJoinRows + warp);
+    }
+}
+
 // Launches a call's first kernel; that of the second of two calls so that it begins while the first one's last does.
 template <typename K>
 cudaError_t launch_attn(K* kernel, const SplitWork& a, const CUtensorMap& tmK, const CUtensorMap& tmV, int grid, int threads, int smem, cudaStream_t stream) {
@@ -300,7 +333,7 @@ cudaError_t launch_attn(K* kernel, const SplitWork& a, const CUtensorMap& tmK, c
 template <typename E, int kDim, int kRows, bool kParts>
 cudaError_t launch_join(const SplitWork& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(a.grid - 1, kRows / kJoinRows);
+    cfg.gridDim = !kParts || kRows <= 64 ? dim3(a.grid - 1, kRows / kJoinRows) : dim3(8 * a.grid);
     cfg.blockDim = dim3(32 * kJoinRows);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
