@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (real && !whole) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4*>(part + pr * kDim + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        *reinterpret_cast<uint4*>(part + part_offset<kDim>(pr, d + e)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
             }
             if (write && whole && kh == 0 && c.lse != nullptr) c.lse[out_row] = row_lse(m, l);

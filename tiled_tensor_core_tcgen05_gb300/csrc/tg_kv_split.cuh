@@ -85,7 +85,7 @@ struct SplitWork {
     int q_vec;          // Q aligned, and strides whole, for the kernel's wide loads
     int page_shift;
     Meta* meta;         // grid entries
-    float* parts;       // grid x 2 parts: rows x (dim + 2) floats each (values, then maxima, then sums)
+    float* parts;       // grid x 2 parts: rows x (dim + 2) floats each (values, then references, then sums)
 };
 
 // Byte offset of piece `at` (bytes) of token t among tokens that TMA left as lines of 128 bytes, swizzled.
@@ -279,37 +279,112 @@ __device__ __forceinline__ void join_row(const SplitWork& a, int k, int r) {
     finish_row<E, kDim, kN, kParts>(c, to, lane * kN, v, top, sum, m.part != 0);
 }
 
-// A warp a row: block (k - 1, rows 8 blockIdx.y ..). Where groups of many rows share keys, units are few, and so are the borders that are a unit's
-// first: a grid of about what the GPU holds looks for them (a thread a border) and shares their rows out (64 sequences on 8192 shared tokens 89 -> 83 us;
-// prompt chunks, where nearly every border is one, take 677 us that way and 667 with a block a border and eight rows).
-constexpr int kJoinRows = 8;
-constexpr int kMostBorders = 1024;
+// The same for units of many rows, whose parts hold their values in pieces of four, of eight rows one behind another (part_offset): a lane of the kernel
+// that writes them has a row, so a warp's store is whole lines (rows one behind another: 32 quarters of lines, and 3 us more at a share's end). Here a
+// warp reads 16 values of eight rows, whole lines too.
+template <int kDim>
+__device__ __forceinline__ int part_offset(int r, int d) { return ((r / 8 * (kDim / 4) + d / 4) * 8 + r % 8) * 4; }
 
 template <typename E, int kDim, int kRows, bool kParts>
-__global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(const SplitWork a) {
+__device__ __forceinline__ void join_eight(const SplitWork& a, int k, int eight, int d) {
+    const KvAttnCall& c = a.c;
+    const Meta m = a.meta[k];
+    if (m.chunks == 0) return;
+    const Shares shares(m.total, a.grid, a.least);
+    const int64_t before = shares.start(k - 1), first_chunk = m.unit_start + a.extra;
+    if (before > first_chunk) return;  // an earlier border lies in the unit's chunks
+    const int r = eight * 8 + threadIdx.x % 8, row = m.block * kRows + r;
+    if (row >= m.count * a.share) return;
+    const int last = shares.owner(first_chunk + m.chunks - 1);
+    auto part_of = [&](int x) {
+        const int slot = x == k - 1 && before < m.unit_start ? 1 : 0;
+        return a.parts + (static_cast<int64_t>(2 * x) + slot) * kRows * (kDim + 2);
+    };
+    constexpr int kAhead = 8;  // parts whose reads are together; those of the first are on their way while the references are compared
+    float4 y[kAhead];
+    float ref[kAhead], l[kAhead];
+    auto read = [&](int x0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (x0 + i <= last) y[i] = *reinterpret_cast<const float4*>(part_of(x0 + i) + part_offset<kDim>(r, d));
+    };
+    auto read_rest = [&](int x0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            ref[i] = x0 + i <= last ? part_of(x0 + i)[kRows * kDim + r] : kNoMax;
+            l[i] = x0 + i <= last ? part_of(x0 + i)[kRows * (kDim + 1) + r] : 0.0f;
+        }
+    };
+    read(k - 1);
+    read_rest(k - 1);
+    float top = kNoMax, sum = 0.0f, v[4] = {};
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) top = fmaxf(top, ref[i]);
+    for (int x0 = k - 1 + kAhead; x0 <= last; x0 += kAhead)
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) top = fmaxf(top, x0 + i <= last ? part_of(x0 + i)[kRows * kDim + r] : kNoMax);
+    for (int x0 = k - 1; x0 <= last; x0 += kAhead) {
+        if (x0 > k - 1) {
+            read(x0);
+            read_rest(x0);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (x0 + i <= last) {
+                const float w = ex2_approx(ref[i] - top);
+                sum = fmaf(l[i], w, sum);
+                v[0] = fmaf(y[i].x, w, v[0]);
+                v[1] = fmaf(y[i].y, w, v[1]);
+                v[2] = fmaf(y[i].z, w, v[2]);
+                v[3] = fmaf(y[i].w, w, v[3]);
+            }
+    }
+    const int t = row / a.share;
+    const int64_t to = static_cast<int64_t>(m.first + t) * c.heads + m.head * a.share + row - t * a.share;
+    finish_row<E, kDim, 4, kParts>(c, to, d, v, top, sum, m.part != 0);
+}
+
+// Block (k - 1, a piece of the rows). Where groups of many rows share keys, units are few, and so are the borders that are a unit's
+// first: a grid of about what the GPU holds looks for them (a thread a border) and shares their rows out (64 sequences on 8192 shared tokens 89 -> 84 us;
+// prompt chunks, where nearly every border is one, take 677 us that way and 667 with a block a border and piece).
+constexpr int kJoinWarps = 8;
+constexpr int kMostBorders = 1024;
+template <int kDim, int kRows>
+constexpr int kJoinPieces = kRows <= 64 ? kRows / kJoinWarps : kRows * kDim / (kJoinWarps * 128);  // a warp has a row, or 128 values of eight
+
+template <typename E, int kDim, int kRows, bool kParts>
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const SplitWork a) {
     if constexpr (kParts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.y == 0) clear_uncovered<E, kDim>(a.c);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    constexpr int kPieces = kJoinPieces<kDim, kRows>;
+    auto join = [&](int k, int piece) {
+        if constexpr (kRows <= 64) {
+            join_row<E, kDim, kRows, kParts>(a, k, piece * kJoinWarps + warp);
+        } else {
+            const int at = piece * kJoinWarps + warp;  // of all 16 values of eight rows
+            join_eight<E, kDim, kRows, kParts>(a, k, at / (kDim / 16), at % (kDim / 16) * 16 + lane / 8 * 4);
+        }
+    };
     if constexpr (!kParts || kRows <= 64) {
-        join_row<E, kDim, kRows, kParts>(a, blockIdx.x + 1, blockIdx.y * kJoinRows + warp);
+        join(blockIdx.x + 1, blockIdx.y);
     } else {
-        __shared__ int borders[kMostBorders], found[kJoinRows];
+        __shared__ int borders[kMostBorders], found[kJoinWarps];
         int n = 0;
-        for (int base = 1; base < a.grid; base += 32 * kJoinRows) {
+        for (int base = 1; base < a.grid; base += 32 * kJoinWarps) {
             const int k = base + threadIdx.x;
             const bool yes = k < a.grid && first_border(a, a.meta[k], k);
             const uint32_t all = __ballot_sync(0xFFFFFFFFu, yes);
             if (lane == 0) found[warp] = __popc(all);
             __syncthreads();
-            for (int w = 0; w < kJoinRows; ++w) {
+            for (int w = 0; w < kJoinWarps; ++w) {
                 if (w == warp && yes) borders[n + __popc(all & ((1u << lane) - 1))] = k;
                 n += found[w];
             }
             __syncthreads();
         }
-        constexpr int kPieces = kRows / kJoinRows;
-        for (int i = blockIdx.x; i < n * kPieces; i += gridDim.x) join_row<E, kDim, kRows, kParts>(a, borders[i / kPieces], i % kPieces * kJoinRows + warp);
+        for (int i = blockIdx.x; i < n * kPieces; i += gridDim.x) join(borders[i / kPieces], i % kPieces);
     }
 }
 
@@ -333,8 +408,8 @@ cudaError_t launch_attn(K* kernel, const SplitWork& a, const CUtensorMap& tmK, c
 template <typename E, int kDim, int kRows, bool kParts>
 cudaError_t launch_join(const SplitWork& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = !kParts || kRows <= 64 ? dim3(a.grid - 1, kRows / kJoinRows) : dim3(8 * a.grid);
-    cfg.blockDim = dim3(32 * kJoinRows);
+    cfg.gridDim = !kParts || kRows <= 64 ? dim3(a.grid - 1, kJoinPieces<kDim, kRows>) : dim3(8 * a.grid);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
