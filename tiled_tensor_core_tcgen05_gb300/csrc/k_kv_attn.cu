@@ -687,7 +687,7 @@ cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMa
 
 bool kv_attn_few_rows(const KvAttnCall& c) { return few_rows(c); }
 
-int kv_attn_box_rows(const KvAttnCall& c) { return kStep * c.cache.dim / 128; }
+int kv_attn_box_rows(const KvAttnCall& c) { return (few_rows(c) ? kStep : kv_attn_tile_box(c)) * c.cache.dim / 128; }
 
 int64_t kv_attn_workspace(const KvAttnCall& c, int sm_count) {
     return few_rows(c) ? few_plan(c, sm_count).bytes : kv_attn_tile_workspace(c, sm_count);

@@ -173,8 +173,10 @@ int64_t kv_attn_shared_workspace(const KvSharedCall& s, int sm_count) {
     return in_groups(s) ? layout(s, sm_count, nullptr).bytes : kv_attn_workspace(s.c, sm_count);
 }
 
-cudaError_t launch_kv_attn_shared(const KvSharedCall& s, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace, int sm_count,
-                                  cudaStream_t stream) {
+int kv_attn_groups_box_rows(const KvSharedCall& s) { return kv_attn_box_rows(group_call(s, SharedWork{})); }
+
+cudaError_t launch_kv_attn_shared(const KvSharedCall& s, const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmK2, const CUtensorMap& tmV2,
+                                  void* workspace, int sm_count, cudaStream_t stream) {
     if (!in_groups(s)) return launch_kv_attn(s.c, tmK, tmV, workspace, sm_count, stream);
     const SharedWork w = layout(s, sm_count, workspace);
     group_kernel<<<s.group_count + (s.c.batch.batch + kThreads - 1) / kThreads, kThreads, 0, stream>>>(s, w);
@@ -185,7 +187,7 @@ cudaError_t launch_kv_attn_shared(const KvSharedCall& s, const CUtensorMap& tmK,
     c.found = w.found;
     c.found_weight = w.found_weight;
     if ((e = launch_kv_attn(c, tmK, tmV, w.first, sm_count, stream)) != cudaSuccess) return e;
-    return launch_kv_attn(group_call(s, w), tmK, tmV, w.second, sm_count, stream);
+    return launch_kv_attn(group_call(s, w), tmK2, tmV2, w.second, sm_count, stream);
 }
 
 }  // namespace tg

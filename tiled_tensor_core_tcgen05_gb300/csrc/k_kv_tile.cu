@@ -9,22 +9,23 @@
 //   warps 0-7, 8-15 softmax of rows 0-127 and 128-255, two threads a row (its TMEM
 //                   lane), 64 scores of a tile each, in registers. They also
 //                   bring the rows of Q to shared memory and write the result;
-//   warps 16-19     turn codes, 64 tokens at a time, into fp16 (exact) tiles with the
+//   warps 16-19     turn codes, 8 KB at a time, into fp16 (exact) tiles with the
 //                   128-byte swizzle, two of keys and two of values: once for both
 //                   halves of the rows, which is what the 256 rows are for;
 //   warps 20, 21    one thread each issues the MMAs of a half;
 //   warp 22         walks the share and hands the segments (the part of a unit that
 //                   this CTA computes) to the others through a ring in shared memory;
-//   warp 23         looks up pages and scales a tile ahead and has TMA bring the
-//                   codes into a ring of three 64-token slots.
+//   warp 23         looks up pages and scales of four tiles at a time, the next four's while it has
+//                   TMA bring these' codes into a ring of three slots of 8 KB.
 // TMEM: scores of either half 128 columns, outputs dim columns each; the weights (fp16)
-// overwrite the scores they come from. A half's chain is scores, softmax, product, and
-// only then the next scores. The second half's scores of a tile are issued when the first
+// overwrite the scores they come from at dim 128, where a half's chain is scores, softmax,
+// product, and only then the next scores. The second half's scores of a tile are issued when the first
 // half's weights begin to arrive, so that one half's MMAs lie beside the other's
-// exponentials.
+// exponentials. At dim 64 the weights have columns of their own, and a half's next scores are computed
+// as soon as its softmax has read these.
 //
-// Measured (one GB300): chunks of up to 4096 new tokens on 8192, 32 heads over 8 of 128, causal: 669 us, 760 TFLOP/s or
-// 0.39 of the dense rate; the tensor pipe is active 36 % of the cycles. MMAs of M = 128, N = 128 and fp16 operands take
+// Measured (one GB300): chunks of up to 4096 new tokens on 8192, 32 heads over 8 of 128, causal: 661 us, 770 TFLOP/s or
+// 0.40 of the dense rate; the tensor pipe is active 36 % of the cycles. MMAs of M = 128, N = 128 and fp16 operands take
 // 104 (scores) and 93 (product) cycles where the dense rate has 64, which alone would leave 65 %: the attention
 // over 16-bit keys (k_attn.cu) has the same MMAs and reaches 1118 TFLOP/s. What is different here: every tile of
 // codes is turned into fp16 again for each block of 256 rows that sees it, by four warps and through a ring of its
@@ -33,6 +34,7 @@
 #include "tg_device.cuh"
 #include "tg_kv_split.cuh"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace tg {
@@ -50,14 +52,25 @@ constexpr int kThreads = kSoftmaxThreads + kConvThreads + 128;
 constexpr int kRegs = 80, kRegsSoftmax = 96, kRegsConv = 56, kRegsIssue = 40;
 static_assert(kSoftmaxThreads * kRegsSoftmax + kConvThreads * kRegsConv + 128 * kRegsIssue <= kThreads * kRegs, "register split");
 static_assert(kRegsSoftmax >= kRegs && kRegsConv <= kRegs && kRegsIssue <= kRegs, "who takes and who gives");
-constexpr int kInfoSlots = 8;            // tiles whose scales are in shared memory (four can be in use)
+constexpr int kInfoSlots = 16;           // tiles whose scales are in shared memory (ten can be in use)
 constexpr int kSegSlots = 4;             // segments handed out ahead
 constexpr int kSegReaders = 16 + 2 + 1;  // warps that read a segment: softmax, issuers, loader
 constexpr int kTurns = 4;                // tiles whose turns are told apart (the halves are two apart at most)
-constexpr int kRawSlots = 3;             // 64-token pieces of codes in flight
+// Codes come in pieces of 8 KB: a tile is two of keys and two of values, or one each.
+// (At dim 64 pieces of 4 KB take the warps that bring and convert them too long: four groups of 2 to 17 sequences on 30011 shared
+// tokens 108 us, with these 94; and 105 where a half's scores wait for its product.)
+template <int kDim>
+constexpr int kPiece = 8192 / kDim;                 // tokens
+template <int kDim>
+constexpr int kPieces = kKeys / kPiece<kDim>;       // of a tile's keys
+constexpr int kRawSlots = 3;                        // pieces in flight
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;            // + 128 half; the weights of keys 64 g .. are the first 32 of their 64 columns
-constexpr uint32_t kColO = 256;          // + 128 half
+constexpr uint32_t kColO = 256;          // + dim half
+constexpr uint32_t kColP = 384;          // + 64 half: the weights of all keys, at dim 64
+// Whether the weights have columns of their own, so that a half's next scores are computed while it weighs these.
+template <int kDim>
+constexpr bool kScoresAhead = kDim == 64;
 
 // What a CTA holds back while the watchdog's test hook is on, one CTA after another: its first piece of codes, word
 // of its products, or its first segment.
@@ -76,7 +89,7 @@ template <int kDim>
 struct Smem {
     static constexpr int kBox = 128 * 128;                 // 128 rows of 64 fp16
     static constexpr int kTile = kBox * (kDim / 64);
-    static constexpr int kRaw = 64 * kDim;                 // bytes of a 64-token piece
+    static constexpr int kRaw = kPiece<kDim> * kDim;       // bytes of a piece
     static constexpr int kQ = 0;                           // 2 halves
     static constexpr int kK = 2 * kTile;                   // 2 stages
     static constexpr int kV = 4 * kTile;                   // 2 stages
@@ -85,7 +98,7 @@ struct Smem {
     static constexpr int kInfo = kRed + 2 * 2 * 2 * kHalfRows * 4;
     static constexpr int kSegments = kInfo + kInfoSlots * static_cast<int>(sizeof(TileInfo));
     static constexpr int kBars = kSegments + kSegSlots * 64;
-    static constexpr int kNumBars = 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + kInfoSlots + 2 + kTurns + 2 * kSegSlots + 2 * kRawSlots + 1;
+    static constexpr int kNumBars = 2 + 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + kInfoSlots + 2 + kTurns + 2 * kSegSlots + 2 * kRawSlots + 1;
     static constexpr int kScan = kBars + 8 * kNumBars;      // a sum a warp, then found offset and sequence
     static constexpr int kFoundOff = kScan + kThreads / 32 * 8;
     static constexpr int kFoundSeq = kFoundOff + 8;
@@ -222,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar += 8 * n;
         return b;
     };
-    const uint32_t q_full = bars(2), k_full = bars(2), k_empty = bars(2), v_full = bars(2), v_empty = bars(2), s_full = bars(2);
+    const uint32_t q_full = bars(2), k_full = bars(2), k_empty = bars(2), v_full = bars(2), v_empty = bars(2), s_full = bars(2), s_read = bars(2);
     const uint32_t p_full = bars(4), o_done = bars(2), info_full = bars(kInfoSlots), drain = bars(2), turn = bars(kTurns);
     const uint32_t seg_full = bars(kSegSlots), seg_empty = bars(kSegSlots), raw_full = bars(kRawSlots), raw_empty = bars(kRawSlots), nowhere = bars(1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
@@ -240,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(v_full + 8 * i, kConvThreads / 32);
             mbar_init(v_empty + 8 * i, 2);
             mbar_init(s_full + 8 * i, 1);
+            mbar_init(s_read + 8 * i, 8);           // the warps of the half (with kScoresAhead)
             mbar_init(o_done + 8 * i, 1);
             mbar_init(drain + 8 * i, 1);
         }
@@ -374,11 +388,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t qd = smem_desc_sw128(sbase + L::kQ + h * L::kTile, 16, 1024);
             const uint64_t kd = smem_desc_sw128(sbase + L::kK, 16, 1024);
             const uint64_t vd = smem_desc_sw128(sbase + L::kV, L::kBox, 1024);
-            const uint32_t col_s = tmem + kColS + 128 * h, col_o = tmem + kColO + 128 * h;
+            const uint32_t col_s = tmem + kColS + 128 * h, col_o = tmem + kColO + kDim * h, col_p = kScoresAhead<kDim> ? tmem + kColP + 64 * h : col_s;
             const uint32_t product_done = withheld == kNoProduct ? nowhere : o_done + 8 * h;
             // 16 keys of the product; their weights are 8 columns
             auto product = [&](int kk, uint32_t st, bool add) {
-                mma_f16_tmem_a(col_o, col_s + (kk >> 2) * 64 + (kk & 3) * 8, vd + st * (L::kTile >> 4) + kk * (2048 >> 4), idesc_o, add);
+                mma_f16_tmem_a(col_o, col_p + (kk >> 2) * (kScoresAhead<kDim> ? 32 : 64) + (kk & 3) * 8, vd + st * (L::kTile >> 4) + kk * (2048 >> 4), idesc_o, add);
+            };
+            auto scores = [&](uint32_t st) {
+                tc_fence_after_sync();
+#pragma unroll
+                for (int kk = 0; kk < kDim / 16; ++kk) {
+                    const uint32_t in = ((kk >> 2) * L::kBox + (kk & 3) * 32) >> 4;
+                    mma_f16(col_s, qd + in, kd + st * (L::kTile >> 4) + in, idesc_s, kk != 0);
+                }
+                mma_commit(s_full + 8 * h);
+                mma_commit(k_empty + 8 * st);
             };
             bool ok = true;
             while (ok && next_segment(sg)) {
@@ -387,19 +411,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = wait_suspended(q_full + 8 * h, (seg_no - 1) & 1u, wc, kSiteMmaFull);
                     for (int j = 0; ok && j < n; ++j) {
                         const uint32_t g = tile_no + j, st = g & 1u, kph = (g >> 1) & 1u;
-                        // the scores overwrite the weights of tile j - 1
-                        ok = wait_suspended(k_full + 8 * st, kph, wc, kSiteMmaFull) &&
-                             (j == 0 || wait_suspended(o_done + 8 * h, (g - 1) & 1u, wc, kSiteMmaAccEmpty)) &&
-                             (h == 0 || wait_suspended(turn + 8 * (g % kTurns), (g / kTurns) & 1u, wc, kSiteMmaFull));
-                        if (!ok) break;
-                        tc_fence_after_sync();
-#pragma unroll
-                        for (int kk = 0; kk < kDim / 16; ++kk) {
-                            const uint32_t in = ((kk >> 2) * L::kBox + (kk & 3) * 32) >> 4;
-                            mma_f16(col_s, qd + in, kd + st * (L::kTile >> 4) + in, idesc_s, kk != 0);
+                        if (!kScoresAhead<kDim> || j == 0) {
+                            // the scores overwrite the weights of tile j - 1
+                            ok = wait_suspended(k_full + 8 * st, kph, wc, kSiteMmaFull) &&
+                                 (j == 0 || wait_suspended(o_done + 8 * h, (g - 1) & 1u, wc, kSiteMmaAccEmpty)) &&
+                                 (h == 0 || wait_suspended(turn + 8 * (g % kTurns), (g / kTurns) & 1u, wc, kSiteMmaFull));
+                            if (!ok) break;
+                            scores(st);
                         }
-                        mma_commit(s_full + 8 * h);
-                        mma_commit(k_empty + 8 * st);
+                        if (kScoresAhead<kDim> && j + 1 < n) {  // once these are read
+                            ok = wait_suspended(k_full + 8 * (st ^ 1u), ((g + 1) >> 1) & 1u, wc, kSiteMmaFull) &&
+                                 wait_suspended(s_read + 8 * h, g & 1u, wc, kSiteMmaAccEmpty);
+                            if (!ok) break;
+                            scores(st ^ 1u);
+                        }
                         ok = wait_suspended(v_full + 8 * st, kph, wc, kSiteMmaFull) && wait_suspended(p_full + 16 * h, g & 1u, wc, kSiteMmaFull);
                         if (!ok) break;
                         if (h == 0) mbar_arrive(turn + 8 * (g % kTurns));
@@ -429,74 +454,94 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else {
             // -------------------------------------------------------- pages, scales and the copies of the codes
-            // a lane per block of 16 keys
-            auto page_of = [&](const Segment& s, int tile) {
-                const int token = (s.tile0 + tile) * kKeys + lane * kStep;
-                if (lane >= kBlocks || token >= s.len) return -1;
-                return seq_page<kParts>(c.batch, c.cache, s.seq, token >> a.page_shift, c.wd);
+            // A lane per block of 16 keys, and four tiles at a time, their pages read while the four before are brought: what a
+            // tile's lookups wait for (the page, then its scales) takes longer than its products.
+            constexpr int kBatch = 32 / kBlocks;
+            uint32_t piece = 0, slot = 0, turned = 1;  // pieces so far, the next one's slot, and what its emptiness is waited for by
+            const int nth = lane / kBlocks, block = lane % kBlocks;
+            const int step = a.box / kStep;            // blocks a copy
+            constexpr int kInPiece = kPiece<kDim> / kStep;
+            const int32_t* row = nullptr;
+            int tile = 0, entry = 0;
+            bool have, asked = false;
+            auto look_up = [&] {  // the batch that begins at sg's `tile`
+                const int token = (sg.tile0 + tile + nth) * kKeys + block * kStep;
+                asked = tile + nth < sg.t1 && token < sg.len;
+                entry = asked ? __ldg(row + (token >> a.page_shift)) : -1;
             };
-            uint32_t piece = 0;  // 64-token pieces so far
-            bool have = next_segment(sg);
-            int tile = sg.t0;
-            int pg = have ? page_of(sg, tile) : -1;
+            auto next = [&] {
+                have = next_segment(sg);
+                tile = sg.t0;
+                if (have) row = table_row<kParts>(c.batch, sg.seq);
+            };
+            auto free_slot = [&] { return __all_sync(0xFFFFFFFFu, wait_suspended(raw_empty + 8 * slot, turned, wc, kSiteConvEmpty)); };
+            next();
+            if (have) look_up();
+            bool ok = true;
             while (have) {
-                const int head = sg.head, token = (sg.tile0 + tile) * kKeys + lane * kStep, len = sg.len, cur = pg;
-                const int64_t ph = static_cast<int64_t>(max(cur, 0)) * c.cache.kv_heads + head;
+                const int token = (sg.tile0 + tile + nth) * kKeys + block * kStep, tiles = min(kBatch, sg.t1 - tile);
+                int cur = entry;
+                if (asked && (cur < 0 || cur >= c.cache.pages)) {
+                    report_range(c.wd);
+                    cur = -1;
+                }
+                const int there = cur >= 0 ? min(kStep, sg.len - token) : 0;
+                const int64_t ph = static_cast<int64_t>(max(cur, 0)) * c.cache.kv_heads + sg.head;
                 float ks = 0.0f, vs = 1.0f;
                 if (cur >= 0) {
                     ks = __ldg(c.cache.k_scale + ph);
                     vs = __ldg(c.cache.v_scale + ph);
                 }
-                if (++tile >= sg.t1) {
-                    have = next_segment(sg);
-                    tile = sg.t0;
-                }
-                if (have) pg = page_of(sg, tile);
                 const int64_t place = ph * c.cache.page + (token & (c.cache.page - 1));
                 const int line = static_cast<int>(kDim == 128 ? place : place >> 1);
-                bool ok = true;
-                for (int part = 0; part < 4; ++part, ++piece) {  // keys 0-63, 64-127, then values
-                    const uint32_t slot = piece % kRawSlots;
-                    ok = wait_phase_sleep(raw_empty + 8 * slot, ((piece / kRawSlots) & 1u) ^ 1u, wc, kSiteConvEmpty, 32);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    if (part == 0) {
-                        TileInfo& info = infos[tile_no % kInfoSlots];
-                        if (lane < kBlocks) {
-                            vs = max_nan(vs, kScaleFloor);
-                            info.ks[lane] = ks;
-                            info.lv[lane] = cur >= 0 ? log2f(vs) : -INFINITY;  // no page: no weight
-                            info.iv[lane] = 1.0f / vs;
-                            info.there[lane] = cur >= 0 ? min(kStep, len - token) : 0;
+                const bool first = cur >= 0 && block % step == 0;  // a copy begins here
+                tile += tiles;
+                if (tile >= sg.t1) next();
+                if (have) look_up();
+                for (int i = 0; i < tiles; ++i) {
+#pragma unroll 1
+                    for (int part = 0; part < 2 * kPieces<kDim>; ++part) {  // keys, then values
+                        if (!(ok = free_slot())) break;
+                        const bool mine = first && lane / kInPiece == kPieces<kDim> * i + part % kPieces<kDim>;
+                        const uint32_t many = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * step;
+                        const uint32_t bar_at = raw_full + 8 * slot;
+                        if (withheld != kNoCodes || piece != 0) {
+                            if (lane == 0) {
+                                if (many > 0) mbar_arrive_expect_tx(bar_at, many * kStep * kDim);
+                                else mbar_arrive(bar_at);
+                            }
+                            __syncwarp();
+                            if (mine) tma_load_2d(sbase + L::kRawAt + slot * L::kRaw + lane % kInPiece * kStep * kDim, part < kPieces<kDim> ? &tmK : &tmV, bar_at, 0, line);
                         }
-                        const bool full = __all_sync(0xFFFFFFFFu, lane >= kBlocks || (cur >= 0 && len - token >= kStep));
-                        if (lane == 0) info.state = full ? 1 : 0;
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(info_full + 8 * (tile_no % kInfoSlots));
+                        ++piece;
+                        if (++slot == kRawSlots) {
+                            slot = 0;
+                            turned ^= 1;
+                        }
+                        if (i == 0 && part == 0) {  // what is said of the four tiles
+                            const uint32_t whole = __ballot_sync(0xFFFFFFFFu, there == kStep);
+                            TileInfo& info = infos[(tile_no + nth) % kInfoSlots];
+                            if (nth < tiles) {
+                                const float v = max_nan(vs, kScaleFloor);
+                                info.ks[block] = ks;
+                                info.lv[block] = cur >= 0 ? log2f(v) : -INFINITY;  // no page: no weight
+                                info.iv[block] = 1.0f / v;
+                                info.there[block] = there;
+                                if (block == 0) info.state = (whole >> (nth * kBlocks) & ((1u << kBlocks) - 1)) == (1u << kBlocks) - 1;
+                            }
+                            __syncwarp();
+                            if (nth < tiles && block == 0) mbar_arrive(info_full + 8 * ((tile_no + nth) % kInfoSlots));
+                        }
                     }
-                    const bool mine = lane < kBlocks && (lane >> 2) == (part & 1) && cur >= 0;
-                    const uint32_t many = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-                    const uint32_t bar_at = raw_full + 8 * slot;
-                    if (withheld == kNoCodes && piece == 0) continue;
-                    if (lane == 0) {
-                        if (many > 0) mbar_arrive_expect_tx(bar_at, many * kStep * kDim);
-                        else mbar_arrive(bar_at);
-                    }
-                    __syncwarp();
-                    if (mine) tma_load_2d(sbase + L::kRawAt + slot * L::kRaw + (lane & 3) * kStep * kDim, part < 2 ? &tmK : &tmV, bar_at, 0, line);
+                    if (!ok) break;
+                    ++tile_no;
                 }
                 if (!ok) break;
-                ++tile_no;
             }
             // the converters stop at a tile of which nothing is said but that it is the end
-            if (!have) {
-                TileInfo& info = infos[tile_no % kInfoSlots];
-                if (lane == 0 && wait_phase_sleep(raw_empty + 8 * (piece % kRawSlots), ((piece / kRawSlots) & 1u) ^ 1u, wc, kSiteConvEmpty, 32)) {
-                    info.state = -1;
-                    mbar_arrive(info_full + 8 * (tile_no % kInfoSlots));
-                }
+            if (ok && free_slot() && lane == 0) {
+                infos[tile_no % kInfoSlots].state = -1;
+                mbar_arrive(info_full + 8 * (tile_no % kInfoSlots));
             }
             // let every copy in flight land before the CTA ends
             for (uint32_t i = piece > kRawSlots ? piece - kRawSlots : withheld == kNoCodes; lane == 0 && i < piece; ++i)
@@ -512,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 8 tokens of one box; the four warps take boxes and groups of 8 tokens in turn.
         const int at = lane & 3, r = lane >> 3, b = lane >> 2 & 1;
         const int t8 = kDim == 128 ? r ^ (b ? 5 : 0) : 2 * r + b;       // token of eight
-        constexpr int kRounds = 64 / 8 * (kDim / 64) / 4;               // of the four warps in a 64-token piece: 4 or 2
+        constexpr int kRounds = kPiece<kDim> / 8 * (kDim / 64) / 4;     // of the four warps in a piece
         const int box = kDim == 128 ? warp & 1 : 0;
         const int group0 = kDim == 128 ? (warp - 16) >> 1 : warp - 16;  // first group of 8 tokens, then every 2nd or 4th
         constexpr int kGroupStep = kDim == 128 ? 2 : 4;
@@ -528,7 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const TileInfo& info = infos[tile_no % kInfoSlots];
             const int state = info.state;
             if (state < 0) break;
-            for (int part = 0; part < 4; ++part, ++piece) {
+            for (int part = 0; part < 2 * kPieces<kDim>; ++part, ++piece) {
+                const int nth = part % kPieces<kDim>;
                 const uint32_t slot = piece % kRawSlots, raw = sbase + L::kRawAt + slot * L::kRaw + get;
                 ok = __all_sync(0xFFFFFFFFu, wait_suspended(raw_full + 8 * slot, (piece / kRawSlots) & 1u, wc, kSiteConvFull));
                 if (!ok) break;
@@ -543,15 +589,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (state == 0) {  // tokens past the end, or without a page, are zeros
 #pragma unroll
                     for (int i = 0; i < kRounds; ++i) {
-                        const int t = (part & 1) * 64 + (group0 + i * kGroupStep) * 8 + t8;
+                        const int t = nth * kPiece<kDim> + (group0 + i * kGroupStep) * 8 + t8;
                         if ((t & 15) >= info.there[t >> 4]) x[i] = make_uint4(0, 0, 0, 0);
                     }
                 }
-                if ((part & 1) == 0) {
+                if (nth == 0) {
                     ok = __all_sync(0xFFFFFFFFu, wait_suspended((part == 0 ? k_empty : v_empty) + 8 * st, eph, wc, kSiteConvEmpty));
                     if (!ok) break;
                 }
-                const uint32_t base = sbase + (part < 2 ? L::kK : L::kV) + st * L::kTile + (part & 1) * 64 * 128 + put;
+                const uint32_t base = sbase + (part < kPieces<kDim> ? L::kK : L::kV) + st * L::kTile + nth * kPiece<kDim> * 128 + put;
 #pragma unroll
                 for (int i = 0; i < kRounds; ++i) {
                     uint32_t h[8];
@@ -562,10 +608,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sts_v4(base + put0 + i * kGroupStep * 8 * 128, make_uint4(h[0], h[1], h[2], h[3]));
                     sts_v4(base + put1 + i * kGroupStep * 8 * 128, make_uint4(h[4], h[5], h[6], h[7]));
                 }
-                if (part & 1) {
+                if (nth == kPieces<kDim> - 1) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive((part == 1 ? k_full : v_full) + 8 * st);
+                    if (lane == 0) mbar_arrive((part < kPieces<kDim> ? k_full : v_full) + 8 * st);
                 }
             }
             ++tile_no;
@@ -576,7 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int h = warp >> 3, kh = (warp >> 2) & 1;                // rows' half, keys' half
         const int row = (warp & 3) * 32 + lane;                       // of the half: its TMEM lane
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t col_s = lanes + kColS + 128 * h + 64 * kh, col_o = lanes + kColO + 128 * h + kh * (kDim / 2);
+        const uint32_t col_s = lanes + kColS + 128 * h + 64 * kh, col_o = lanes + kColO + kDim * h + kh * (kDim / 2);
+        const uint32_t col_p = kScoresAhead<kDim> ? lanes + kColP + 64 * h + 32 * kh : col_s;
         const int pair = h * 4 + (warp & 3);                          // the two warps of the same 32 rows
         float* red = reinterpret_cast<float*>(smem + L::kRed) + (h * 2) * kHalfRows + row;  // + parity 4 * 128, + key half 128
         bool ok = true;
@@ -671,6 +718,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_32x32b_x32(col_s, reinterpret_cast<uint32_t(&)[32]>(xs[0]));
                 tmem_ld_32x32b_x32(col_s + 32, reinterpret_cast<uint32_t(&)[32]>(xs[1]));
                 tmem_ld_wait();
+                if constexpr (kScoresAhead<kDim>) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_read + 8 * h);
+                }
                 if (edge) {
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
@@ -731,9 +783,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int b = 0; b < 2; ++b) sum = fmaf(part[b].x + part[b].y, info.iv[4 * kh + 2 * q + b], sum);
-                    tmem_st_x16(col_s + 16 * q, w);
-                    // the outputs so far come to the new maximum before the first weights are handed over: the
-                    // product of the tile before has completed (this tile's scores were issued after it)
+                    // the product of the tile before has completed (its weights lie here, and its outputs are there) where this tile's
+                    // scores were issued after it; where they were computed ahead it is waited for (a wait that gives up is
+                    // told by the next one, at the latest at the segment's end)
+                    if (kScoresAhead<kDim> && q == 0 && j > 0) {
+                        wait_suspended(o_done + 8 * h, (g - 1) & 1u, wc, kSiteEpilogueAccFull);
+                        __syncwarp();
+                        tc_fence_after_sync();
+                    }
+                    tmem_st_x16(col_p + 16 * q, w);
+                    // the outputs so far come to the new maximum before the first weights are handed over
                     if (q == 0 && j > 0 && __any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll 1
                         for (int d = 0; d < kDim / 2; d += 32) {
@@ -853,6 +912,7 @@ cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMa
     a.least = 2;
     a.grid = sm_count;
     a.joined = c.max_len > kKeys;
+    a.box = kv_attn_tile_box(c);
     a.q_vec = reinterpret_cast<uintptr_t>(c.q.p) % 16 == 0 && c.q.token % 8 == 0 && c.q.head % 8 == 0;
     a.meta = static_cast<Meta*>(workspace);
     a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + meta_bytes(a.grid));
@@ -862,6 +922,9 @@ cudaError_t launch(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMa
 }
 
 }  // namespace
+
+// As many as lie together, up to a piece: a warp issues a copy in 130 cycles, and 16 of them a tile take longer than its products.
+int kv_attn_tile_box(const KvAttnCall& c) { return std::min<int>(c.cache.page, 8192 / c.cache.dim); }
 
 int64_t kv_attn_tile_workspace(const KvAttnCall& c, int sm_count) {
     return meta_bytes(sm_count) + static_cast<int64_t>(sm_count) * 2 * kRows * (c.cache.dim + 2) * 4;

@@ -1667,10 +1667,10 @@ tg_status check_attention(const void* Q, int64_t q_token_stride, int64_t q_head_
 }
 
 // The codes as lines of 128 bytes (a cache without pages is never read: any address serves).
-tg_status attention_maps(const KvAttnCall& c, CUtensorMap* tmK, CUtensorMap* tmV) {
+tg_status attention_maps(const KvAttnCall& c, int box_rows, CUtensorMap* tmK, CUtensorMap* tmV) {
     const KvCacheArgs& k = c.cache;
     const uint64_t lines = k.pages > 0 ? static_cast<uint64_t>(k.pages * k.kv_heads * k.page * k.dim) / 128 : 1;
-    const uint32_t box = static_cast<uint32_t>(kv_attn_box_rows(c));
+    const uint32_t box = static_cast<uint32_t>(box_rows);
     tg_status st = make_map_u8(tmK, k.pages > 0 ? k.k : c.out, 128, lines, 128, box);
     return st != TG_OK ? st : make_map_u8(tmV, k.pages > 0 ? k.v : c.out, 128, lines, 128, box);
 }
@@ -1702,7 +1702,7 @@ extern "C" tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int6
         return fail(TG_ERR_INVALID_ARG, "tg_attention_kv needs a workspace of %lld bytes, got %lld", (long long)need,
                     (long long)(workspace ? workspace_bytes : 0));
     CUtensorMap tmK, tmV;
-    if ((st = attention_maps(c, &tmK, &tmV)) != TG_OK) return st;
+    if ((st = attention_maps(c, kv_attn_box_rows(c), &tmK, &tmV)) != TG_OK) return st;
     cudaError_t e = launch_kv_attn(c, tmK, tmV, workspace, g_dev[dev].sm_count, stream);
     return e == cudaSuccess ? TG_OK : cuda_fail(e, "cache attention kernel launch");
 }
@@ -1786,9 +1786,10 @@ extern "C" tg_status tg_attention_kv_shared(const void* Q, int64_t q_token_strid
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return fail(TG_ERR_INVALID_ARG, "tg_attention_kv_shared needs a workspace of %lld bytes, got %lld", (long long)need,
                     (long long)(workspace ? workspace_bytes : 0));
-    CUtensorMap tmK, tmV;
-    if ((st = attention_maps(s.c, &tmK, &tmV)) != TG_OK) return st;
-    cudaError_t e = launch_kv_attn_shared(s, tmK, tmV, workspace, g_dev[dev].sm_count, stream);
+    CUtensorMap tmK, tmV, tmK2, tmV2;
+    if ((st = attention_maps(s.c, kv_attn_box_rows(s.c), &tmK, &tmV)) != TG_OK) return st;
+    if ((st = attention_maps(s.c, kv_attn_groups_box_rows(s), &tmK2, &tmV2)) != TG_OK) return st;
+    cudaError_t e = launch_kv_attn_shared(s, tmK, tmV, tmK2, tmV2, workspace, g_dev[dev].sm_count, stream);
     return e == cudaSuccess ? TG_OK : cuda_fail(e, "shared cache attention kernel launch");
 }
 

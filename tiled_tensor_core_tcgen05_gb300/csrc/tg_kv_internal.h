@@ -180,10 +180,13 @@ cudaError_t launch_kv_append(const KvAppendCall& c, int sm_count, cudaStream_t s
 cudaError_t launch_kv_read(const KvReadCall& c, int sm_count, cudaStream_t stream);
 int64_t kv_attn_workspace(const KvAttnCall& c, int sm_count);
 int64_t kv_attn_shared_workspace(const KvSharedCall& s, int sm_count);
-cudaError_t launch_kv_attn_shared(const KvSharedCall& s, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace,
-                                  int sm_count, cudaStream_t stream);
+// tmK2, tmV2: of the groups' pass (boxes of kv_attn_groups_box_rows lines).
+cudaError_t launch_kv_attn_shared(const KvSharedCall& s, const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmK2, const CUtensorMap& tmV2,
+                                  void* workspace, int sm_count, cudaStream_t stream);
+int kv_attn_groups_box_rows(const KvSharedCall& s);
 bool kv_attn_few_rows(const KvAttnCall& c);  // whether a call runs in the kernel for few rows
 int64_t kv_attn_tile_workspace(const KvAttnCall& c, int sm_count);
+int kv_attn_tile_box(const KvAttnCall& c);   // tokens a box of its maps
 cudaError_t launch_kv_attn_tile(const KvAttnCall& c, const CUtensorMap& tmK, const CUtensorMap& tmV, void* workspace,
                                 int sm_count, cudaStream_t stream);
 // Maps of the cache's codes as lines of 128 bytes, swizzled, in boxes of kv_attn_box_rows lines.

@@ -82,6 +82,7 @@ struct SplitWork {
     int extra;          // entries before a unit's first chunk, for what every unit costs whatever its length
     int grid;
     int joined;         // whether the joining kernel runs
+    int box;            // tokens a copy of codes, in the kernel for many rows
     int q_vec;          // Q aligned, and strides whole, for the kernel's wide loads
     int page_shift;
     Meta* meta;         // grid entries
