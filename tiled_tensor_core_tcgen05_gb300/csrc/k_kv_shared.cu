@@ -155,9 +155,9 @@ SharedWork layout(const KvSharedCall& s, int sm_count, void* at) {
 }
 
 // Whether groups are worth their pass. What sharing can save at most is the reading of all sequences but one a group, as long as they may
-// be; the further pass, the kernel before both and the join take 20 to 45 us. Measured on a GB300, in us with groups and without,
-// 32 heads over 8 of 128: 8 sequences of 4000 (58 MB to save) 32 and 18, of 16000 (230 MB) 39 and 41; 32 of 4000 (256 MB) 50 and 43; 64 of 1000
-// (133 MB) 47 and 29, of 4000 (520 MB) 57 and 75, of 16000 71 and 255; four groups of 16 of 1000 (117 MB) 39 and 27, of 4000 (418 MB) 50
+// be; the further pass, the kernel before both and the join take some 20 us. Measured on a GB300, in us with groups and without,
+// 32 heads over 8 of 128: 8 sequences of 4000 (58 MB to save) 34 and 18, of 16000 (230 MB) 38 and 41; 32 of 4000 (256 MB) 42 and 43; 64 of 1000
+// (133 MB) 39 and 29, of 4000 (520 MB) 45 and 75, of 16000 60 and 255; four groups of 16 of 1000 (117 MB) 36 and 28, of 4000 (418 MB) 48
 // and 65. The bounds that the caller gives are all that is known here: loose ones are taken for long sequences.
 bool pays(const KvSharedCall& s) {
     const KvAttnCall& c = s.c;
