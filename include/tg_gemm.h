@@ -531,8 +531,9 @@ tg_status tg_attention_kv_shared(const void* Q, int64_t q_token_stride, int64_t 
  * negative. Its pages lens / page and further are open (new tokens are written
  * there) and are its own; those before are full and may be shared, since nothing
  * writes to them. The calls below read refs, table and lens and leave new ones
- * in other arrays, so that what a caller holds stays valid until it goes over to
- * the new ones. Outputs, workspace, cache and inputs must not overlap. All is
+ * in other arrays. The pages themselves change in place: those of sequences that a
+ * call lets go of may have been given away and written to by it, and the old arrays
+ * then say nothing of those. Outputs, workspace, cache and inputs must not overlap. All is
  * stream-ordered, decided on the device and the same every run; nothing is
  * allocated, and the workspace's contents need not be kept.
  * ------------------------------------------------------------------------- */
@@ -563,7 +564,8 @@ tg_status tg_kv_copy(const void* k_cache, const void* v_cache, const float* k_sc
  *                   where they take its place (codes of those tokens, scales)
  *   refs_out        entries of the old table taken off refs, new ones added
  *   spare           one int32: free pages that are left. Negative: so many were
- *                   lacking; the last of the new entries are then -1
+ *                   lacking; the last of the new entries are then -1, and a
+ *                   sequence whose table ends before its length has lost tokens
  *
  * New pages are the lowest-numbered ones that nobody holds after the old
  * sequences are gone (a page that tokens are copied from is not among them),
