@@ -29,8 +29,8 @@
 //   6  the tokens of the border's bins, brought together: the cut, and their kept weight to their groups;
 //   7  the group, lane and token in which u of the kept weight is passed.
 //
-// What bounds it is the chain of these steps, between which the CTAs meet, and the 22 operations that a weight takes,
-// not the bytes: of 256 rows, warps issue in half of the cycles. Measured on a GB300, in a graph: one row of 32000 fp16 logits, top_p 0.9:
+// What bounds it is the chain of these steps, between which the CTAs meet, and in rows without a cut the 22 operations that a
+// weight takes, not the bytes: of 256 rows, warps issue in half of the cycles. Measured on a GB300, in a graph: one row of 32000 fp16 logits, top_p 0.9:
 // 12.9 us; 64 rows of 131071 bf16: greedy 6.2, no cut 21, top_k 50 17, top_p 0.9 76, settings mixed 42; 256 rows of 131072 fp32,
 // top_p 0.9: 216 (the bytes take 20).
 #include "tg_device.cuh"
