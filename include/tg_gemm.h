@@ -564,8 +564,9 @@ tg_status tg_kv_copy(const void* k_cache, const void* v_cache, const float* k_sc
  *                   where they take its place (codes of those tokens, scales)
  *   refs_out        entries of the old table taken off refs, new ones added
  *   spare           one int32: free pages that are left. Negative: so many were
- *                   lacking; the last of the new entries are then -1, and a
- *                   sequence whose table ends before its length has lost tokens
+ *                   lacking (-2^31: at least so many); the last of the new
+ *                   entries are then -1, and a sequence whose table ends
+ *                   before its length has lost tokens
  *
  * New pages are the lowest-numbered ones that nobody holds after the old
  * sequences are gone (a page that tokens are copied from is not among them),

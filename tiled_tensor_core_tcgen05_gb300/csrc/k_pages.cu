@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const KvForkCall c) {
     constexpr int kAll = kCtas * kThreads;
     __shared__ int64_t box[2][kCtas];
     __shared__ int warps[kWarps];
-    __shared__ int64_t carry;
+    __shared__ int64_t carry, needs[kWarps];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t rank = cluster_ctarank();
     const int t = rank * kThreads + threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -226,24 +226,25 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const KvForkCall c) {
         w.need[i] = x.end - x.start;
     }
     meet<kCtas>();
-    // where each child's new pages begin in the list of all of them: every CTA by itself
+    // where each child's new pages begin in the list of all of them: every CTA by itself. In 64 bits: a child may ask for 2^27 pages,
+    // whatever there are
     if (threadIdx.x == 0) carry = 0;
     for (int base = 0; base < c.count; base += kThreads) {
-        const int i = base + threadIdx.x, n = i < c.count ? left<kCtas>(w.need + i) : 0;
-        int x = n;
+        const int i = base + threadIdx.x;
+        const int64_t n = i < c.count ? left<kCtas>(w.need + i) : 0;
+        int64_t x = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
             if (lane >= o) x += y;
         }
         __syncthreads();
-        if (lane == 31) warps[warp] = x;
+        if (lane == 31) needs[warp] = x;
         __syncthreads();
-        int64_t before = carry;
-        int sum = 0;
+        int64_t before = carry, sum = 0;
         for (int k = 0; k < kWarps; ++k) {
-            if (k < warp) before += warps[k];
-            sum += warps[k];
+            if (k < warp) before += needs[k];
+            sum += needs[k];
         }
         if (rank == 0 && i < c.count) w.place[i] = before + x - n;
         __syncthreads();
