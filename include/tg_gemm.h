@@ -504,8 +504,9 @@ tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int64_t q_head_
  * slot, say) is attended by itself. No group has more than max_rows new tokens.
  * Results are tg_attention_kv's within its own bounds; there is no window. The
  * workspace query takes the same sizes. Where sharing cannot save 256 MB of reading
- * by the bounds given (max_len, groups and sequences), or a sequence's own rows are
- * many, the call is tg_attention_kv's.
+ * by the bounds given (max_len for each sequence that is not its group's first;
+ * those are no more than max_rows - 1 a group), or a sequence's own rows are many,
+ * the call is tg_attention_kv's.
  *
  * A shared[g] that is negative or beyond max_len or the table, and a group with
  * more than max_rows rows, are reported (TG_ERR_BOUNDS) and make the group's

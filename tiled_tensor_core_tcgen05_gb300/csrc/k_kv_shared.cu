@@ -155,14 +155,17 @@ SharedWork layout(const KvSharedCall& s, int sm_count, void* at) {
 }
 
 // Whether groups are worth their pass. What sharing can save at most is the reading of all sequences but one a group, as long as they may
-// be; the further pass, the kernel before both and the join take some 20 us. Measured on a GB300, in us with groups and without,
+// be; a member has a row at least, so a group's are no more than max_rows, and sequences in no group save nothing. The further pass, the kernel
+// before both and the join take some 20 us. Measured on a GB300, in us with groups and without,
 // 32 heads over 8 of 128: 8 sequences of 4000 (58 MB to save) 34 and 18, of 16000 (230 MB) 38 and 41; 32 of 4000 (256 MB) 42 and 43; 64 of 1000
 // (133 MB) 39 and 29, of 4000 (520 MB) 45 and 75, of 16000 60 and 255; four groups of 16 of 1000 (117 MB) 36 and 28, of 4000 (418 MB) 48
-// and 65. The bounds that the caller gives are all that is known here: loose ones are taken for long sequences.
+// and 65; a group of two among 64 of 16000 (31 MB) 334 and 321, of 16 (469 MB) 295 and 305, 32 groups of two of 8000 (500 MB) 107 and 160. The
+// bounds that the caller gives are all that is known here: loose ones are taken for long sequences.
 bool pays(const KvSharedCall& s) {
     const KvAttnCall& c = s.c;
     const int64_t each = std::min(c.max_len, c.batch.table_width * c.cache.page) * c.cache.kv_heads * c.cache.dim * 2;
-    return s.always || each * (c.batch.batch - s.group_count) >= (256ll << 20);
+    const int64_t spared = std::min<int64_t>(c.batch.batch - s.group_count, static_cast<int64_t>(s.group_count) * std::max(s.max_rows - 1, 0));
+    return s.always || each * spared >= (256ll << 20);
 }
 
 bool in_groups(const KvSharedCall& s) { return s.group_count > 0 && kv_attn_few_rows(s.c) && pays(s); }
