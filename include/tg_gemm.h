@@ -498,8 +498,8 @@ tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int64_t q_head_
  * once a sequence. Group g is the sequences groups[g] .. groups[g + 1] - 1
  * (group_count + 1 int32 offsets; sequences before the first or behind the last
  * are in none). The first shared[g] tokens of all of them lie in the same pages:
- * their table rows begin alike, and the kernels read the first sequence's.
- * (Where they do not, results are those of the first sequence's pages.) A
+ * the table rows of all of them must begin alike. Which one's entries are read for
+ * these tokens is not specified: one's for all, each its own, or some of both. A
  * sequence whose tokens before its new ones are fewer than shared[g] (an idle
  * slot, say) is attended by itself. No group has more than max_rows new tokens.
  * Results are tg_attention_kv's within its own bounds; there is no window. The
@@ -511,7 +511,7 @@ tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int64_t q_head_
  * A shared[g] that is negative or beyond max_len or the table, and a group with
  * more than max_rows rows, are reported (TG_ERR_BOUNDS) and make the group's
  * sequences ones of no group. So do, for all groups, offsets that fall or are
- * out of range.
+ * out of range. (Where the call is tg_attention_kv's, groups are not looked at.)
  */
 tg_status tg_attention_kv_shared_workspace(int64_t kv_heads, int64_t page, int64_t dim, int format, int64_t table_width,
                                            int64_t heads, int64_t batch, int64_t total, int64_t group_count,
