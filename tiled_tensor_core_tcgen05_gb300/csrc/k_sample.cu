@@ -29,7 +29,7 @@
 //   6  the tokens of the border's bins, brought together: the cut, and their kept weight to their groups;
 //   7  the group, lane and token in which u of the kept weight is passed.
 //
-// What bounds it is the chain of these steps, between which the CTAs meet, and in rows without a cut the 22 operations that a
+// What bounds it is the chain of these steps, between which the CTAs meet, and in rows without a cut the 23 operations that a
 // weight takes, not the bytes: of 256 rows, warps issue in half of the cycles. Measured on a GB300, in a graph: one row of 32000 fp16 logits, top_p 0.9:
 // 12.9 us; 64 rows of 131071 bf16: greedy 6.2, no cut 21, top_k 50 17, top_p 0.9 76, settings mixed 42; 256 rows of 131072 fp32,
 // top_p 0.9: 216 (the bytes take 20).
@@ -53,7 +53,7 @@ constexpr int kBins = (kUnit + 3) * kSteps / kBinSteps;
 constexpr int kList = 2047;                  // tokens in a list, at most: that many weights' upper halves add up in 32 bits
 constexpr int kSub = 1024;                   // parts of a bin that holds more
 constexpr int kSome = kThreads;              // tokens of a bin that are ranked by comparing each with each
-constexpr int kGuess = 1280;                 // threads' largest above a threshold that the list can be expected to hold
+constexpr int kGuess = 1280;                 // tokens around a guessed bin that are brought together with its own, half on either side
 constexpr int kMostGroups = (1 << 18) / 128 / kMaxCtas + 2;  // of a CTA
 constexpr float kNone = -INFINITY;
 constexpr float kTiny = 0x1p-147f;            // a few of the least floats
@@ -104,7 +104,7 @@ constexpr float kLnHi = static_cast<float>(kLn), kLnLo = static_cast<float>(kLn 
 constexpr float kPerLn = static_cast<float>(1.0 / kLn);
 constexpr float kRound = 12582912.0f;                    // 1.5 * 2^23: a sum with it is a whole number
 constexpr int kRoundBits = 0x4B400000;
-constexpr float kHigh = 12.0f, kLow = 1.5f / 524288.0f;  // sums with them are multiples of 2^-20 and 2^-42
+constexpr float kHigh = 12.0f, kLow = 1.5f / 524288.0f;  // sums with them are multiples of 2^-20 and 2^-42; with kLow of what is below 2^-20
 constexpr int kHighBits = 0x41400000, kLowBits = 0x36400000;
 
 // ln w of a logit, or what is taken off it in the end, as p + q and some, and 256 log2 w to the nearest integer, above kRoundBits.
@@ -118,9 +118,10 @@ __device__ __forceinline__ int step_bits(float p, const Scale& c) { return __flo
 // at most 2^-9.4,
 //     exp(x / T) = 2^(m / 256) (1 + u + (f + U^2 / 2 + U^3 / 6)),
 // U^4 / 24 being 2^-42; 2^(m / 256) is a table's entry th + tl, whose exponents are moved: by m less the largest's, rounded up, so weights are
-// relative to something up to 2^(1 / 256) larger than the largest's, for all alike. That takes 22 operations on the floating point pipe, which bound
-// the passes that weigh all logits (two at a time, in packed form, they take as long). With the largest taken off first it is 30: 256 rows of 131072
-// fp32, no cut, 105 and 120 us. Where logits are far from zero by T (`near` is not set) it is taken off: the difference of their halves, which stays finite,
+// relative to something up to 2^(1 / 256) larger than the largest's, for all alike. The weight is s + r, r up to 2^-15 of s: the high part is taken of their sum, so
+// that the low one is within 2^-20. That takes 23 operations on the floating point pipe, which bound
+// the passes that weigh all logits (two at a time, in packed form, they take as long). With the largest taken off first it is 31: 256 rows of 131072
+// fp32, no cut, 106 and some 121 us. Where logits are far from zero by T (`near` is not set) it is taken off: the difference of their halves, which stays finite,
 // as d + e exactly.
 template <bool kNear>
 __device__ __forceinline__ void weigh(float x, const Scale& c, const float2* powers, int& high, int& low, int least = INT_MIN) {
@@ -143,7 +144,7 @@ __device__ __forceinline__ void weigh(float x, const Scale& c, const float2* pow
     const float v = __fmaf_rn(__fmul_rn(g, g), __fmaf_rn(g, 1.0f / 6.0f, 0.5f), f);
     const float s = __fmaf_rn(th, u, th);
     const float r = __fadd_rn(__fmaf_rn(th, u, __fsub_rn(th, s)), __fmaf_rn(th, v, __fmaf_rn(tl, u, tl)));
-    const float h = __fadd_rn(s, kHigh);
+    const float h = __fadd_rn(__fadd_rn(s, r), kHigh);
     const float l = __fadd_rn(__fadd_rn(__fsub_rn(s, __fsub_rn(h, kHigh)), r), kLow);
     high += __float_as_int(h) - kHighBits;
     low += __float_as_int(l) - kLowBits;
