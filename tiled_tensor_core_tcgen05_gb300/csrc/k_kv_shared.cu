@@ -66,8 +66,9 @@ __device__ __forceinline__ int tokens_of(const KvSharedCall& s, int g) {
     return tokens / kChunk * kChunk;
 }
 
-// Whether sequence i's tokens before its new ones are at least so many.
-__device__ __forceinline__ bool takes_part(const KvSharedCall& s, int i, int tokens) {
+// Whether sequence i of group g, whose shared tokens in whole chunks are so many, holds all that is shared, the rest behind the chunks too:
+// the pages of one that does not are its own from the first token on.
+__device__ __forceinline__ bool takes_part(const KvSharedCall& s, int i, int g, int tokens) {
     const KvBatch& b = s.c.batch;
     int n = 1;
     if (b.cu != nullptr) {
@@ -76,7 +77,7 @@ __device__ __forceinline__ bool takes_part(const KvSharedCall& s, int i, int tok
         if (lo < 0 || hi < lo || hi > b.total || n > b.max_new) return false;
     }
     const int len = __ldg(b.lens + i);
-    return tokens > 0 && len <= s.c.max_len && len <= b.table_width * s.c.cache.page && len - n >= tokens;
+    return tokens > 0 && len <= s.c.max_len && len <= b.table_width * s.c.cache.page && len - n >= __ldg(s.shared + g);
 }
 
 // Block g < group_count: that group. The blocks behind: the sequences.
@@ -87,9 +88,9 @@ __global__ void __launch_bounds__(kThreads) group_kernel(const KvSharedCall s, c
     if (g >= s.group_count) {
         const int i = (g - s.group_count) * kThreads + threadIdx.x;
         if (i >= s.c.batch.batch) return;
-        int tokens = 0;
+        int tokens = 0, lo = 0;
         if (good) {
-            int lo = 0, hi = s.group_count;  // the last group that begins at i or before
+            int hi = s.group_count;  // the last group that begins at i or before
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
                 if (__ldg(s.groups + mid) <= i) lo = mid;
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kThreads) group_kernel(const KvSharedCall s, c
             }
             if (i >= __ldg(s.groups + lo) && i < __ldg(s.groups + lo + 1)) tokens = tokens_of(s, lo);
         }
-        w.begin[i] = takes_part(s, i, tokens) ? tokens : 0;
+        w.begin[i] = takes_part(s, i, lo, tokens) ? tokens : 0;
         return;
     }
     const int tokens = good ? tokens_of(s, g) : -1;
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) group_kernel(const KvSharedCall s, c
     __syncthreads();
     const int first = good ? __ldg(s.groups + g) : 0, last = good ? __ldg(s.groups + g + 1) : 0;
     for (int i = first + threadIdx.x; i < last; i += kThreads)
-        if (takes_part(s, i, tokens)) {
+        if (takes_part(s, i, g, tokens)) {
             atomicMin(&lowest, i);
             break;
         }
