@@ -75,3 +75,34 @@ def test_rows_far_from_zero(tg, far, dtype):  # noqa: F811
                     for i in range(6):
                         want, sure = sample_tests.draw(y[i], float(u[i]), t, k or 0, 1.0 if p is None else float(torch.tensor(p)), 0.0 if m is None else float(torch.tensor(m)))
                         assert not sure or got[i] == want, (i, vocab, t, sign, k, p, m)
+
+
+@pytest.mark.parametrize("dtype", sample_tests.TYPES)
+@pytest.mark.parametrize("vocab", [50, 3001, 30000, 131072])
+def test_numbers_next_to_the_borders_of_longer_rows(tg, dtype, vocab):  # noqa: F811
+    """top_p is the float at, or next to, a token's edge in falling order; u the one at an edge of what that keeps, by index."""
+    g = torch.Generator().manual_seed(vocab)
+    for t, spread, around, k, m in ((1.0, 2.5, 0.0, 0, 0.0), (0.75, 1.0, 20.0, 0, 0.0), (2.0, 0.5, -150.0, 0, 1e-4), (1.0, 2.5, 90.0, 2500, 0.0), (1.0, 6.0, 0.0, 40, 0.05)):
+        rows = 6
+        x = ((torch.randn(rows, vocab, generator=g) * spread + around) * t).to(dtype)
+        u, p = torch.empty(rows), torch.ones(rows)
+        for i in range(rows):
+            y, at = ((x[i].double() - float(x[i].max())) / t).sort(descending=True, stable=True)
+            w = y.exp() * (y > -43 * math.log(2))
+            if k:
+                w[k:] = 0
+            if m:
+                w *= y >= math.log(float(torch.tensor(m)))
+            some = torch.rand(2, generator=g).tolist()
+            toward = torch.tensor([2.0, -1.0])[i % 2]
+            if i % 3:
+                edge = (w.cumsum(0) / w.sum())[int((w.cumsum(0) > some[0] * w.sum()).nonzero()[0])].float()
+                p[i] = min(edge if i % 3 == 1 else torch.nextafter(edge, toward), torch.tensor(1.0))
+                w = w * (w.cumsum(0) - w < float(p[i]) * w.sum())
+            c = torch.zeros_like(w).scatter_(0, at, w).cumsum(0)
+            edge = (c[int((c > some[1] * c[-1]).nonzero()[0])] / c[-1]).float()
+            u[i] = edge if i == 0 else torch.nextafter(edge, toward)
+        got = tg.sample(x.cuda(), u.cuda(), t, k, p.cuda(), m).tolist()
+        for i in range(rows):
+            want, sure = sample_tests.draw(x[i], float(u[i]), t, k, float(p[i]), float(torch.tensor(m)))
+            assert not sure or got[i] == want, (i, t, around, k, m, float(p[i]), float(u[i]))
