@@ -501,7 +501,8 @@ tg_status tg_attention_kv(const void* Q, int64_t q_token_stride, int64_t q_head_
  * the table rows of all of them must begin alike. Which one's entries are read for
  * these tokens is not specified: one's for all, each its own, or some of both. A
  * sequence whose tokens before its new ones are fewer than shared[g] (an idle
- * slot, say) is attended by itself. No group has more than max_rows new tokens.
+ * slot, say) is attended by itself. No group has more than max_rows new tokens,
+ * and there are no more groups, with or without sequences, than sequences.
  * Results are tg_attention_kv's within its own bounds; there is no window. The
  * workspace query takes the same sizes. Where sharing cannot save 256 MB of reading
  * by the bounds given (max_len for each sequence that is not its group's first;
@@ -621,7 +622,7 @@ tg_status tg_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v_s
  * Each of the settings is one float32 (top_k: int32) a row on the device, or
  * where the pointer is NULL the number beside it for all rows. Weights are 64-bit
  * fixed point, of 2^-42 of about the row's largest (w_i below half of that count
- * as none), right to 2^-37 of themselves and half a unit, and their sums are exact:
+ * as none), right to 2^-37 of themselves and 5/8 of a unit, and their sums are exact:
  * the token does not depend on how the work is split, nor on the other rows.
  * vocab is at most 2^18. Stream-ordered; allocates nothing.
  */

@@ -25,12 +25,12 @@
 // as soon as its softmax has read these.
 //
 // Measured (one GB300): chunks of up to 4096 new tokens on 8192, 32 heads over 8 of 128, causal: 661 us, 770 TFLOP/s or
-// 0.40 of the dense rate; the tensor pipe is active 36 % of the cycles. MMAs of M = 128, N = 128 and fp16 operands take
+// 0.40 of the dense rate (with heads of 64: 465 us, 547 TFLOP/s); the tensor pipe is active 36 % of the cycles. MMAs of M = 128, N = 128 and fp16 operands take
 // 104 (scores) and 93 (product) cycles where the dense rate has 64, which alone would leave 65 %: the attention
 // over 16-bit keys (k_attn.cu) has the same MMAs and reaches 1118 TFLOP/s. What is different here: every tile of
 // codes is turned into fp16 again for each block of 256 rows that sees it, by four warps and through a ring of its
-// own, which leaves shared memory for two stages of keys and values and 80 to 96 registers for the softmax (about
-// 100 bytes spilled); and some 600 cycles of a half's chain are hand-overs that the other half does not fill.
+// own, which leaves shared memory for two stages of keys and values and 80 to 96 registers for the softmax (160 to 176
+// bytes spilled, the two-part form 138 to 176; with 88 to 104, before the look-ahead, heads of 128 took the same time); and some 600 cycles of a half's chain are hand-overs that the other half does not fill.
 #include "tg_device.cuh"
 #include "tg_kv_split.cuh"
 

@@ -11,9 +11,9 @@
 // order of sequences and places, by prefix sums, so results do not depend on
 // timing.
 //
-// Measured on a GB300, kernels alone: four beams of one prompt forked 10.9 us and 256 of 32 prompts of up to 8192 tokens 25.4
-// (steps that wait for one another: table rows, counts, prefix sums; the bytes take 3); compacting a pool of 301 pages 7.4, one of
-// 16384 pages of 128 KB that is 55 % full 177 (157 at the rate of a plain copy); copying 5003 such pages 200 (193).
+// Measured on a GB300, kernels alone: four beams of one prompt forked 11.2 us and 256 of 32 prompts of up to 8192 tokens 24.9
+// (steps that wait for one another: table rows, counts, prefix sums; the bytes take 3); compacting a pool of 301 pages 7.3, one of
+// 16384 pages of 128 KB that is 55 % full 177 (157 at the rate of a plain copy); copying 5003 such pages 202 (193).
 #include <algorithm>
 #include <climits>
 #include <type_traits>

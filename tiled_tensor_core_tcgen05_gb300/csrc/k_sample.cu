@@ -31,8 +31,8 @@
 //
 // What bounds it is the chain of these steps, between which the CTAs meet, and in rows without a cut the 23 operations that a
 // weight takes, not the bytes: of 256 rows, warps issue in half of the cycles. Measured on a GB300, in a graph: one row of 32000 fp16 logits, top_p 0.9:
-// 12.9 us; 64 rows of 131071 bf16: greedy 6.2, no cut 21, top_k 50 17, top_p 0.9 76, settings mixed 42; 256 rows of 131072 fp32,
-// top_p 0.9: 216 (the bytes take 20).
+// 12.8 us; 64 rows of 131071 bf16: greedy 6.3, no cut 21, top_k 50 17, top_p 0.9 78, settings mixed 42; 256 rows of 131072 fp32,
+// top_p 0.9: 220 (the bytes take 20).
 #include "tg_device.cuh"
 #include "tg_kv.cuh"
 
@@ -120,8 +120,8 @@ __device__ __forceinline__ int step_bits(float p, const Scale& c) { return __flo
 // U^4 / 24 being 2^-42; 2^(m / 256) is a table's entry th + tl, whose exponents are moved: by m less the largest's, rounded up, so weights are
 // relative to something up to 2^(1 / 256) larger than the largest's, for all alike. The weight is s + r, r up to 2^-15 of s: the high part is taken of their sum, so
 // that the low one is within 2^-20. That takes 23 operations on the floating point pipe, which bound
-// the passes that weigh all logits (two at a time, in packed form, they take as long). With the largest taken off first it is 31: 256 rows of 131072
-// fp32, no cut, 106 and some 121 us. Where logits are far from zero by T (`near` is not set) it is taken off: the difference of their halves, which stays finite,
+// the passes that weigh all logits (two at a time, in packed form, they take as long): 256 rows of 131072 fp32, no cut, 106 us. With the largest taken
+// off first it is 31 (with one operation less each: 105 and 120 us). Where logits are far from zero by T (`near` is not set) it is taken off: the difference of their halves, which stays finite,
 // as d + e exactly.
 template <bool kNear>
 __device__ __forceinline__ void weigh(float x, const Scale& c, const float2* powers, int& high, int& low, int least = INT_MIN) {
